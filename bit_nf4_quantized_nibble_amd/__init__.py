@@ -17,7 +17,10 @@ Public API (names follow the pages' problem statement):
                dropout_mask=None, dropout_p=0.0)
     merge(q, lora_a, lora_b, alpha, rslora=False, out=None) -> Tensor [rows, cols]
     mse_loss_grad(y, target) -> (loss [1] fp32, dy) ; adamw_step(param, grad, m, v, step, ...)
+    distill_loss_grad(logits, top_values, top_index, temperature=1.0, weight=None, need_grad=True, dlogits=None,
+                      row_kl=None) -> (loss [1] fp32, dlogits or None)
     StackLayer.create(q, a32, b32, dtype) ; stack_train_step(layers, x, target, alpha, step, ...)
+    quantize_int8(w) -> Int8Weight ; linear_int8(w, x, bias=None) ; linear_int8_experts(w, x, offsets, bias=None)
     workspace_bytes(op, m, rows, cols, r, dtype, flags=0) ; levels()
 
 path: "fused" decodes W inside the GEMM kernels; "dequant" writes W~ (or W~^T for
@@ -27,18 +30,21 @@ workspace).  Calls with at most 16 tokens take the decode GEMV either way.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass
 from typing import Optional, Tuple
 
 from . import _lib
-from ._lib import QloraError, QloraNf4  # noqa: F401
+from ._lib import QloraError, QloraInt8, QloraNf4  # noqa: F401
 
 __all__ = ["NF4Weight", "quantize", "dequantize", "linear_fwd", "linear_bwd", "merge", "workspace_bytes",
            "linear_fwd_noalloc", "linear_fwd_cached",
            "levels", "QloraError", "dtype_code", "profile_enable", "profile_read", "mse_loss_grad",
            "adamw_step", "StackLayer", "stack_train_step", "stack_workspace_bytes",
-           "linear_fwd_group", "linear_bwd_group", "group_workspace_bytes"]
+           "linear_fwd_group", "linear_bwd_group", "group_workspace_bytes",
+           "Int8Weight", "quantize_int8", "linear_int8", "linear_int8_experts", "int8_workspace_bytes",
+           "distill_loss_grad"]
 
 
 def _torch():
@@ -486,6 +492,193 @@ def mse_loss_grad(y, target, dy=None):
     _lib.check(_lib.lib().qlora_mse_loss_grad(_ptr(y), _ptr(target), y.numel(), dtype_code(dt), _ptr(loss),
                                               _ptr(dy), _ptr(ws), ws.numel(), _stream_ptr(y.device)))
     return loss, dy
+
+
+def _on_device(device):
+    """Context in which the library's launches go to ``device`` (a no-op on the current one)."""
+    torch = _torch()
+    if device.index is None or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+
+
+def _strided_rows(x, cols):
+    """x as rows of ``cols`` contiguous elements and the stride between them (a view where
+    the layout allows, else a copy), with the leading dims."""
+    x2, lead = _flatten(x, cols)
+    if x2.shape[0] <= 1:
+        return (x2 if cols <= 1 or x2.stride(1) == 1 else x2.contiguous()), cols, lead
+    if (cols > 1 and x2.stride(1) != 1) or x2.stride(0) < cols:
+        x2 = x2.contiguous()
+    return x2, max(x2.stride(0), cols), lead
+
+
+@dataclass
+class Int8Weight:
+    """A weight [rows, cols] (or one for each expert, [experts, rows, cols]) in 8 bits with a
+    scale per output channel, held in device memory."""
+    rows: int
+    cols: int
+    codes: "object"        # int8 [experts, rows, ld], ld = cols rounded up to 128, zeros past cols
+    scale: "object"        # float32 [experts, rows]
+
+    @property
+    def experts(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def size_bytes(self) -> int:
+        return self.codes.numel() + 4 * self.scale.numel()
+
+    def descriptor(self) -> QloraInt8:
+        return QloraInt8(self.rows, self.cols, self.experts, 0, _ptr(self.codes), _ptr(self.scale))
+
+
+def quantize_int8(w) -> Int8Weight:
+    """8-bit codes and one scale per row of a [rows, cols] weight (fp32, bf16 or f16; for
+    instance the dense result of ``merge``), or of one weight per expert
+    [experts, rows, cols].  Rows may be strided."""
+    torch = _torch()
+    if not w.is_cuda:
+        raise ValueError("w must be a GPU tensor")
+    if w.dim() not in (2, 3) or (w.dim() == 3 and w.shape[0] < 1):
+        raise ValueError("w must be [rows, cols] or [experts, rows, cols] with at least one expert")
+    experts = w.shape[0] if w.dim() == 3 else 1
+    rows, cols = w.shape[-2], w.shape[-1]
+    if cols > _lib.QLORA_INT8_MAX_COLS:  # before anything is allocated
+        raise QloraError(-4, "int8_quantize: %d cols (at most %d)" % (cols, _lib.QLORA_INT8_MAX_COLS))
+    ld = (cols + 127) // 128 * 128
+    q = Int8Weight(rows, cols, torch.empty(experts, rows, ld, dtype=torch.int8, device=w.device),
+                   torch.empty(experts, rows, dtype=torch.float32, device=w.device))
+    if rows == 0 or cols == 0:
+        return q
+    w2, ldw, _ = _strided_rows(w, cols)
+    d = q.descriptor()
+    with _on_device(w.device):
+        _lib.check(_lib.lib().qlora_int8_quantize(_ptr(w2), ldw, dtype_code(w.dtype), ctypes.byref(d),
+                                                  _stream_ptr(w.device)))
+    return q
+
+
+def int8_workspace_bytes(w: Int8Weight, m: int, grouped: bool = False) -> int:
+    """Workspace bytes of linear_int8 (or, grouped, of linear_int8_experts) on m tokens."""
+    d = w.descriptor()
+    return int(_lib.lib().qlora_int8_workspace_bytes(ctypes.byref(d), m, int(grouped)))
+
+
+def _int8_call(w, x, offsets, bias, out, workspace):
+    torch = _torch()
+    dt = x.dtype
+    code = dtype_code(dt)
+    if not x.is_cuda:
+        raise ValueError("x must be a GPU tensor")
+    x2, ldx, lead = _strided_rows(x, w.cols)
+    m = x2.shape[0]
+    y = out if out is not None else torch.empty(m, w.rows, dtype=dt, device=x.device)
+    _need_cuda("out", y, dt)
+    if y.numel() != m * w.rows:
+        raise ValueError("out must hold %d x %d elements" % (m, w.rows))
+    _need_cuda("bias", bias, dt)
+    if bias is not None and bias.numel() != w.rows * (1 if offsets is None else w.experts):
+        raise ValueError("bias must hold one element per output channel (of each expert)")
+    _same_device(x.device, w=w.codes, offsets=offsets, bias=bias, out=out, workspace=workspace)
+    grouped = offsets is not None
+    d = w.descriptor()
+    lib = _lib.lib()
+    ws = _workspace(int(lib.qlora_int8_workspace_bytes(ctypes.byref(d), m, int(grouped))), x.device, workspace)
+    ws_bytes = ws.numel() * ws.element_size()
+    with _on_device(x.device):
+        if grouped:
+            _lib.check(lib.qlora_int8_linear_experts(ctypes.byref(d), _ptr(x2), m, ldx, _ptr(offsets), _ptr(bias),
+                                                     code, _ptr(y), _ptr(ws), ws_bytes, _stream_ptr(x.device)))
+        else:
+            _lib.check(lib.qlora_int8_linear(ctypes.byref(d), _ptr(x2), m, ldx, _ptr(bias), code, _ptr(y), _ptr(ws),
+                                             ws_bytes, _stream_ptr(x.device)))
+    return y.reshape(*lead, w.rows)
+
+
+def linear_int8(w: Int8Weight, x, bias=None, out=None, workspace=None):
+    """y = x . W^T (+ bias) in 8-bit integers: each row of x gets a scale of its own and is
+    brought to 8 bits within the call, the sums are exact, y has x's dtype.  Leading dims of
+    x are flattened to tokens; rows of x may be strided.  ``out`` may supply a preallocated
+    output."""
+    if w.experts != 1:
+        raise ValueError("w holds %d experts: linear_int8_experts takes those" % w.experts)
+    return _int8_call(w, x, None, bias, out, workspace)
+
+
+def linear_int8_experts(w: Int8Weight, x, offsets, bias=None, out=None, workspace=None):
+    """The same for rows sorted by expert: rows offsets[e] .. offsets[e + 1] - 1 of x take
+    expert e's weight (and bias[e]).  ``offsets``: int32 GPU tensor [experts + 1], read on the
+    device.  Rows that no expert has are left as they were in ``out`` (and are unspecified
+    without ``out``)."""
+    torch = _torch()
+    _need_cuda("offsets", offsets, torch.int32)
+    if offsets is None or offsets.numel() != w.experts + 1:
+        raise ValueError("offsets must hold experts + 1 = %d values" % (w.experts + 1))
+    return _int8_call(w, x, offsets, bias, out, workspace)
+
+
+def distill_loss_grad(logits, top_values, top_index, temperature: float = 1.0, weight=None, need_grad: bool = True,
+                      dlogits=None, row_kl=None):
+    """loss = sum_i w_i T^2 KL(softmax(top_values_i / T) || softmax(logits_i / T)) (a 1-element
+    fp32 GPU tensor) and its gradient with respect to the logits in their dtype (None without
+    ``need_grad``).  logits [..., vocab] (rows may be strided); the teacher's logits top_values
+    [..., k] (fp32, bf16 or f16) at the vocabulary entries top_index [..., k] (int32 or int64;
+    -1, or a value of -inf, marks an absent slot).  ``weight`` [...] fp32 (default 1 / rows;
+    0 leaves a row out); ``dlogits`` may be preallocated, ``logits`` itself included;
+    ``row_kl`` (fp32, one per row) receives the rows' T^2 KL."""
+    torch = _torch()
+    dt = logits.dtype
+    code = dtype_code(dt)
+    vocab = logits.shape[-1]
+    if not logits.is_cuda:
+        raise ValueError("logits must be a GPU tensor")
+    z, ldz, lead = _strided_rows(logits, vocab)
+    n = z.shape[0]
+    k = top_values.shape[-1]
+    if top_index.dtype not in (torch.int32, torch.int64):
+        raise TypeError("top_index must be int32 or int64, got %s" % (top_index.dtype,))
+    u, ix = top_values.reshape(-1, k).contiguous(), top_index.reshape(-1, top_index.shape[-1]).contiguous()
+    if tuple(u.shape) != (n, k) or tuple(ix.shape) != (n, k):
+        raise ValueError("top_values and top_index must be [%d rows, k]" % n)
+    _need_cuda("top_values", u)
+    _need_cuda("top_index", ix)
+    for name, t in (("weight", weight), ("row_kl", row_kl)):
+        _need_cuda(name, t, torch.float32)
+        if t is not None and t.numel() != n:
+            raise ValueError("%s must hold one value per row (%d)" % (name, n))
+    ldd = vocab
+    if dlogits is not None:
+        if not need_grad:
+            raise ValueError("dlogits given without need_grad")
+        if not dlogits.is_cuda or dlogits.dtype != dt or dlogits.shape != logits.shape:
+            raise ValueError("dlogits must be a GPU tensor like logits")
+        d2, ldd, _ = _strided_rows(dlogits, vocab)
+        if n and d2.data_ptr() != dlogits.data_ptr():
+            raise ValueError("dlogits must have rows of contiguous elements, evenly spaced")
+        g = dlogits
+    else:
+        g = torch.empty(*lead, vocab, dtype=dt, device=logits.device) if need_grad else None
+    _same_device(logits.device, top_values=u, top_index=ix, weight=weight, dlogits=dlogits, row_kl=row_kl)
+    loss = torch.empty(1, dtype=torch.float32, device=logits.device)
+    lib = _lib.lib()
+    ws = _workspace(int(lib.qlora_distill_workspace_bytes(n)), logits.device)
+    with _on_device(logits.device):
+        _lib.check(lib.qlora_distill_loss_grad(
+            _ptr(z), n, vocab, ldz, code, _ptr(u), dtype_code(u.dtype), _ptr(ix), 8 * ix.element_size(), k,
+            float(temperature), _ptr(weight), _ptr(loss), _ptr(row_kl), _ptr(g), ldd, _ptr(ws), ws.numel(),
+            _stream_ptr(logits.device)))
+    return loss, g
 
 
 def _adamw(lr, beta1, beta2, eps, weight_decay):

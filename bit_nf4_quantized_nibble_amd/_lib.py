@@ -30,11 +30,16 @@ EXPORTED = (
     "qlora_linear_fwd_dropout", "qlora_linear_bwd_dropout", "qlora_linear_fwd_cached",
     "qlora_linear_fwd_noalloc", "qlora_noalloc_scratch_bytes",
     "qlora_linear_fwd_group", "qlora_linear_bwd_group", "qlora_group_workspace_bytes",
+    "qlora_int8_quantize", "qlora_int8_linear", "qlora_int8_linear_experts", "qlora_int8_workspace_bytes",
+    "qlora_distill_loss_grad", "qlora_distill_workspace_bytes",
 )
 QLORA_GROUP_MAX = 8
 QLORA_MSE_WORKSPACE_BYTES = 4096
+QLORA_INT8_MAX_COLS = 131072
+QLORA_DISTILL_MAX_K = 1024
 KERNEL_KINDS = ("quantize", "dequantize", "lora_down", "reduce", "fwd_gemm", "gemv",
-                "bwd_dt", "bwd_dx", "bwd_da", "bwd_db", "merge", "loss", "optim")
+                "bwd_dt", "bwd_dx", "bwd_da", "bwd_db", "merge", "loss", "optim",
+                "int8_rows", "int8_gemm")
 
 
 class QloraNf4(ctypes.Structure):
@@ -51,6 +56,12 @@ class QloraNf4(ctypes.Structure):
         ("absmax_q", ctypes.c_void_p),
         ("absmax_scale2", ctypes.c_void_p),
     ]
+
+
+class QloraInt8(ctypes.Structure):
+    """Mirror of qlora_int8_t."""
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("experts", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
 
 
 class QloraAdamW(ctypes.Structure):
@@ -114,7 +125,18 @@ def _declare(lib):
     lib.qlora_linear_bwd_group.argtypes = [i32, vp, vp, vp, i64, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp, sz, vp]
     lib.qlora_group_workspace_bytes.argtypes = [i32, i32, vp, i64, vp, i32]
     lib.qlora_group_workspace_bytes.restype = sz
-    for name in ("qlora_nf4_quantize", "qlora_nf4_dequantize", "qlora_linear_fwd",
+    PI = ctypes.POINTER(QloraInt8)
+    lib.qlora_int8_quantize.argtypes = [vp, i64, i32, PI, vp]
+    lib.qlora_int8_linear.argtypes = [PI, vp, i64, i64, vp, i32, vp, vp, sz, vp]
+    lib.qlora_int8_linear_experts.argtypes = [PI, vp, i64, i64, vp, vp, i32, vp, vp, sz, vp]
+    lib.qlora_int8_workspace_bytes.argtypes = [PI, i64, i32]
+    lib.qlora_int8_workspace_bytes.restype = sz
+    lib.qlora_distill_loss_grad.argtypes = [vp, i64, i64, i64, i32, vp, i32, vp, i32, i32, f32, vp, vp, vp, vp, i64,
+                                            vp, sz, vp]
+    lib.qlora_distill_workspace_bytes.argtypes = [i64]
+    lib.qlora_distill_workspace_bytes.restype = sz
+    for name in ("qlora_int8_quantize", "qlora_int8_linear", "qlora_int8_linear_experts", "qlora_distill_loss_grad",
+                 "qlora_nf4_quantize", "qlora_nf4_dequantize", "qlora_linear_fwd",
                  "qlora_linear_bwd", "qlora_nf4_levels", "qlora_abi_version",
                  "qlora_profile_enable", "qlora_profile_read", "qlora_merge", "qlora_mse_loss_grad",
                  "qlora_adamw_step", "qlora_stack_train_step", "qlora_linear_fwd_dropout",

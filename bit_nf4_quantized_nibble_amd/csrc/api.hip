@@ -9,6 +9,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 #include <initializer_list>
 #include <mutex>
@@ -228,7 +229,7 @@ int64_t g_prof_n[QLORA_K_COUNT];
 
 const char* kKernelNames[QLORA_K_COUNT] = {
     "quantize", "dequantize", "lora_down", "reduce", "fwd_gemm", "gemv",
-    "bwd_dt",   "bwd_dx",     "bwd_da",    "bwd_db", "merge", "loss", "optim"};
+    "bwd_dt",   "bwd_dx",     "bwd_da",    "bwd_db", "merge", "loss", "optim", "int8_rows", "int8_gemm"};
 
 // Wait for every recorded pair and fold it into the totals (lock held).
 int prof_drain() {
@@ -689,6 +690,121 @@ int qlora_merge(const qlora_nf4_t* w, const void* lora_a, const void* lora_b, in
   if (w->rows > 4194240) return set_error(QLORA_ERR_UNSUPPORTED, "merge: %lld rows (at most 4194240)", (long long)w->rows);
   if ((rc = check_tables("merge"))) return rc;
   return launch_merge(make_w(w), lora_a, lora_b, r, lora_scale(alpha, r, flags), cd, out, (hipStream_t)stream);
+}
+
+namespace {
+bool aligned_to(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
+
+int validate_int8(const qlora_int8_t* q, bool need_data, const char* who) {
+  if (!q) return set_error(QLORA_ERR_INVALID_ARG, "%s: null descriptor", who);
+  if (q->reserved != 0) return set_error(QLORA_ERR_INVALID_ARG, "%s: reserved field must be 0", who);
+  if (q->experts < 1) return set_error(QLORA_ERR_INVALID_ARG, "%s: experts must be >= 1 (got %d)", who, q->experts);
+  if (q->rows < 0 || q->cols < 0) return set_error(QLORA_ERR_SHAPE, "%s: negative shape", who);
+  if (q->cols > QLORA_INT8_MAX_COLS)
+    return set_error(QLORA_ERR_UNSUPPORTED, "%s: %lld cols (at most %d)", who, (long long)q->cols, QLORA_INT8_MAX_COLS);
+  if (q->rows >= (1LL << 31) / q->experts)
+    return set_error(QLORA_ERR_UNSUPPORTED, "%s: %d x %lld rows (fewer than 2^31 in all)", who, q->experts,
+                     (long long)q->rows);
+  if (!need_data || q->rows == 0 || q->cols == 0) return QLORA_OK;
+  if (!q->codes || !q->scale) return set_error(QLORA_ERR_INVALID_ARG, "%s: null codes / scale", who);
+  if (!aligned16(q->codes) || !aligned_to(q->scale, 4))
+    return set_error(QLORA_ERR_INVALID_ARG, "%s: codes must be 16-byte aligned, scale 4-byte aligned", who);
+  return QLORA_OK;
+}
+
+int int8_impl(const qlora_int8_t* w, const void* x, int64_t m, int64_t ldx, const int32_t* offsets, const void* bias,
+              int32_t cd, void* y, void* ws, size_t ws_bytes, void* stream, const char* who) {
+  int rc = validate_int8(w, true, who);
+  if (rc) return rc;
+  if (!valid_cd(cd)) return set_error(QLORA_ERR_DTYPE, "%s: bad compute dtype %d", who, cd);
+  if (w->rows < 1 || w->cols < 1) return set_error(QLORA_ERR_SHAPE, "%s: empty weight", who);
+  if (m < 0) return set_error(QLORA_ERR_SHAPE, "%s: negative m", who);
+  if (m >= (1LL << 31)) return set_error(QLORA_ERR_UNSUPPORTED, "%s: %lld tokens (fewer than 2^31)", who, (long long)m);
+  if (ldx < w->cols)
+    return set_error(QLORA_ERR_SHAPE, "%s: row stride %lld of x below its %lld columns", who, (long long)ldx,
+                     (long long)w->cols);
+  if (m == 0) return QLORA_OK;
+  if (!x || !y) return set_error(QLORA_ERR_INVALID_ARG, "%s: null x / y", who);
+  const int es = cd_bytes(cd);
+  if (!aligned_to(x, es) || !aligned_to(y, es) || !aligned_to(bias, es))
+    return set_error(QLORA_ERR_INVALID_ARG, "%s: x, y and bias must be element-aligned", who);
+  if ((rc = check_ws(ws, ws_bytes, int8_workspace_bytes(w, m, offsets != nullptr), who))) return rc;
+  return launch_int8_linear(w, x, m, ldx, offsets, bias, cd, y, ws, (hipStream_t)stream);
+}
+}  // namespace
+
+int qlora_int8_quantize(const void* w, int64_t ldw, int32_t wd, qlora_int8_t* q, void* stream) {
+  g_err[0] = 0;
+  const char* who = "int8_quantize";
+  int rc = validate_int8(q, true, who);
+  if (rc) return rc;
+  if (!valid_cd(wd)) return set_error(QLORA_ERR_DTYPE, "%s: bad dtype %d", who, wd);
+  if (ldw < q->cols)
+    return set_error(QLORA_ERR_SHAPE, "%s: row stride %lld below the %lld columns", who, (long long)ldw,
+                     (long long)q->cols);
+  if (q->rows == 0 || q->cols == 0) return QLORA_OK;
+  if (!w) return set_error(QLORA_ERR_INVALID_ARG, "%s: null weight", who);
+  if (!aligned_to(w, cd_bytes(wd))) return set_error(QLORA_ERR_INVALID_ARG, "%s: weight must be element-aligned", who);
+  return launch_int8_quantize(w, ldw, wd, q, (hipStream_t)stream);
+}
+
+int qlora_int8_linear(const qlora_int8_t* w, const void* x, int64_t m, int64_t ldx, const void* bias, int32_t cd,
+                      void* y, void* ws, size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  const char* who = "int8_linear";
+  if (w && w->experts > 1)
+    return set_error(QLORA_ERR_INVALID_ARG, "%s: %d experts (qlora_int8_linear_experts takes those)", who, w->experts);
+  return int8_impl(w, x, m, ldx, nullptr, bias, cd, y, ws, ws_bytes, stream, who);
+}
+
+int qlora_int8_linear_experts(const qlora_int8_t* w, const void* x, int64_t m, int64_t ldx, const int32_t* offsets,
+                              const void* bias, int32_t cd, void* y, void* ws, size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  const char* who = "int8_linear_experts";
+  if (!offsets || !aligned_to(offsets, 4))
+    return set_error(QLORA_ERR_INVALID_ARG, "%s: offsets must be non-null and 4-byte aligned", who);
+  if (w && w->experts > 65535)
+    return set_error(QLORA_ERR_UNSUPPORTED, "%s: %d experts (at most 65535)", who, w->experts);
+  return int8_impl(w, x, m, ldx, offsets, bias, cd, y, ws, ws_bytes, stream, who);
+}
+
+size_t qlora_int8_workspace_bytes(const qlora_int8_t* w, int64_t m, int32_t grouped) {
+  if (m < 0 || m >= (1LL << 31) || validate_int8(w, false, "int8_workspace")) return 0;
+  if (grouped ? w->experts > 65535 : w->experts != 1) return 0;
+  return int8_workspace_bytes(w, m, grouped != 0);
+}
+
+size_t qlora_distill_workspace_bytes(int64_t n) { return n < 0 ? 0 : (size_t)round_up(std::max<int64_t>(n, 1) * 4, 256); }
+
+int qlora_distill_loss_grad(const void* logits, int64_t n, int64_t vocab, int64_t ld, int32_t cd,
+                            const void* top_values, int32_t td, const void* top_index, int32_t index_bits, int32_t k,
+                            float temperature, const float* weight, float* loss, float* row_kl, void* dlogits,
+                            int64_t ldd, void* ws, size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  const char* who = "distill";
+  if (!valid_cd(cd) || !valid_cd(td)) return set_error(QLORA_ERR_DTYPE, "%s: bad dtype %d / %d", who, cd, td);
+  if (n < 0 || vocab < 1 || k < 1) return set_error(QLORA_ERR_SHAPE, "%s: n < 0, vocab < 1 or k < 1", who);
+  if (ld < vocab || (dlogits && ldd < vocab))
+    return set_error(QLORA_ERR_SHAPE, "%s: row stride below the %lld vocabulary entries", who, (long long)vocab);
+  if (k > QLORA_DISTILL_MAX_K)
+    return set_error(QLORA_ERR_UNSUPPORTED, "%s: k = %d (at most %d)", who, k, QLORA_DISTILL_MAX_K);
+  if (n >= (1LL << 31) || vocab >= (1LL << 31))
+    return set_error(QLORA_ERR_UNSUPPORTED, "%s: 2^31 rows or vocabulary entries, or more", who);
+  if (!(temperature > 0.f) || !isfinite(temperature))
+    return set_error(QLORA_ERR_INVALID_ARG, "%s: temperature %g must be positive and finite", who, temperature);
+  if (index_bits != 32 && index_bits != 64)
+    return set_error(QLORA_ERR_INVALID_ARG, "%s: index_bits %d (32 or 64)", who, index_bits);
+  if (!loss || !aligned_to(loss, 4)) return set_error(QLORA_ERR_INVALID_ARG, "%s: null or unaligned loss", who);
+  if (n > 0 && (!logits || !top_values || !top_index))
+    return set_error(QLORA_ERR_INVALID_ARG, "%s: null logits / top_values / top_index", who);
+  if (!aligned_to(logits, cd_bytes(cd)) || !aligned_to(dlogits, cd_bytes(cd)) ||
+      !aligned_to(top_values, cd_bytes(td)) || !aligned_to(top_index, index_bits / 8) || !aligned_to(weight, 4) ||
+      !aligned_to(row_kl, 4))
+    return set_error(QLORA_ERR_INVALID_ARG, "%s: arrays must be element-aligned", who);
+  int rc = check_ws(ws, ws_bytes, qlora_distill_workspace_bytes(n), who);
+  if (rc) return rc;
+  return launch_distill(logits, n, vocab, ld, cd, top_values, td, top_index, index_bits == 64, k, temperature, weight,
+                        loss, row_kl ? row_kl : (float*)ws, dlogits, ldd, (hipStream_t)stream);
 }
 
 namespace {

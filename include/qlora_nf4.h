@@ -25,8 +25,10 @@
  *     output, and every array of a layer call (x, dy, adapters, bias, outputs,
  *     masks, saved T0, gradients) start on a 16-byte boundary: the kernels move
  *     16-byte vectors, and an unaligned pointer is refused with
- *     QLORA_ERR_INVALID_ARG.  Workspaces are 256-byte aligned.  The merge, MSE
- *     and AdamW calls take any element-aligned arrays.
+ *     QLORA_ERR_INVALID_ARG.  Workspaces are 256-byte aligned.  The merge, MSE,
+ *     distillation and AdamW calls take any element-aligned arrays, and so do the
+ *     8-bit calls except for their codes; matrices that have a row stride argument
+ *     need not be dense.
  *   - Every call is asynchronous on `stream` (a hipStream_t; NULL = null stream).
  *   - Arguments are validated on the host before anything is launched: on any
  *     error nothing is written and no work is queued.  Errors: a negative
@@ -409,6 +411,116 @@ int qlora_linear_fwd_noalloc(const qlora_nf4_t* w, const void* x, int64_t m, con
 /* Bytes of the scratch array qlora_linear_fwd_noalloc uses on each GPU.  Pure host. */
 size_t qlora_noalloc_scratch_bytes(void);
 
+/* ---------------------------------------------------------------------------
+ * Products in 8-bit integers: the serving form of a merged weight (qlora_merge), one
+ * scale per output channel of the weight and one per token.
+ *   rows to 8 bits  s = fl32(max |x| / 127), c = round-half-even(fl32(x / s)) limited to
+ *                   [-127, 127]; s = 0 and c = 0 for a row of zeros; a row holding an
+ *                   infinity or a NaN has s = NaN and c = 0.
+ *   product         y [m, rows] = RNE_cd(s_i t_j sum_k c[i, k] d[j, k] (+ bias[j])): the integer
+ *                   sum is exact, the scaling and the bias are fp32.  A token whose
+ *                   activations hold an infinity or a NaN has a row of NaN.
+ * ------------------------------------------------------------------------- */
+
+/* Most columns a product takes (the sum of 131072 products of two codes is below 2^31). */
+#define QLORA_INT8_MAX_COLS 131072
+/* Bytes of one row of codes: cols rounded up to whole 128-byte lines; the codes past the
+ * last column are 0. */
+#define QLORA_INT8_LD(cols) ((((int64_t)(cols)) + 127) / 128 * 128)
+
+/*
+ * A weight in 8 bits (one matrix, or one for each expert).  Descriptor memory is the
+ * caller's; the pointers inside are device pointers the caller allocated:
+ *   codes  s8   [experts * rows][QLORA_INT8_LD(cols)]   16-byte aligned
+ *   scale  f32  [experts * rows]
+ */
+typedef struct {
+  int64_t rows; /* output channels (of one expert) */
+  int64_t cols; /* input channels */
+  int32_t experts;  /* 1 for a single matrix */
+  int32_t reserved; /* must be 0 */
+  int8_t* codes;
+  float* scale;
+} qlora_int8_t;
+
+/*
+ * Codes and scales of w [experts * rows, cols] (dtype wd, rows ldw elements apart,
+ * ldw >= cols) into *q.  Any element-aligned w.  An empty weight is a no-op.
+ * Errors: QLORA_ERR_INVALID_ARG (null or unaligned pointers, reserved != 0, experts < 1),
+ * QLORA_ERR_SHAPE (negative shape, ldw < cols), QLORA_ERR_DTYPE, QLORA_ERR_UNSUPPORTED
+ * (cols > QLORA_INT8_MAX_COLS, 2^31 rows or more).
+ */
+int qlora_int8_quantize(const void* w, int64_t ldw, int32_t wd, qlora_int8_t* q, void* stream);
+
+/*
+ * y [m, rows] = x [m, cols] . W^T (+ bias [rows]) with x (dtype cd, rows ldx elements
+ * apart) brought to 8 bits row by row within the call.  w->experts must be 1.  x and y are
+ * element-aligned; y is dense and must not overlap the inputs.  m == 0 is a no-op.
+ * ws: qlora_int8_workspace_bytes(w, m, 0) bytes, 256-byte aligned.
+ * Errors: QLORA_ERR_INVALID_ARG (null or unaligned pointers, experts != 1), QLORA_ERR_SHAPE
+ * (m < 0, empty weight, ldx < cols), QLORA_ERR_DTYPE, QLORA_ERR_WORKSPACE,
+ * QLORA_ERR_UNSUPPORTED (cols > QLORA_INT8_MAX_COLS, m or experts * rows of 2^31 or more).
+ */
+int qlora_int8_linear(const qlora_int8_t* w, const void* x, int64_t m, int64_t ldx, const void* bias,
+                      int32_t cd, void* y, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The same grouped by expert: rows offsets[e] .. offsets[e + 1] - 1 of x and y belong to
+ * expert e (weight e, bias [experts, rows]); offsets: device int32 [experts + 1].  An expert
+ * may have any number of rows, none included.  Rows of y that no expert has (before
+ * offsets[0], from offsets[experts] on) are left as they were.  The offsets are read on the
+ * device only (the call can be captured and replayed with others); they should not
+ * decrease and are limited to [0, m]: where one is smaller than an offset before it, the
+ * rows between stay with the earlier expert.
+ * ws: qlora_int8_workspace_bytes(w, m, 1) bytes.  Errors: as qlora_int8_linear (any
+ * experts >= 1), plus null offsets, and QLORA_ERR_UNSUPPORTED for more than 65535 experts.
+ */
+int qlora_int8_linear_experts(const qlora_int8_t* w, const void* x, int64_t m, int64_t ldx,
+                              const int32_t* offsets, const void* bias, int32_t cd, void* y, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/* Workspace bytes of qlora_int8_linear (grouped 0) or qlora_int8_linear_experts (grouped 1)
+ * on m tokens (reads only the shape of *w); 0 for an invalid query.  Pure host function. */
+size_t qlora_int8_workspace_bytes(const qlora_int8_t* w, int64_t m, int32_t grouped);
+
+/* ---------------------------------------------------------------------------
+ * Distillation: the loss of student logits against a teacher's top logits, and its
+ * gradient (a training loss beside qlora_mse_loss_grad).
+ * ------------------------------------------------------------------------- */
+
+/* Most teacher logits per row. */
+#define QLORA_DISTILL_MAX_K 1024
+
+/*
+ * For row i of logits z [n, vocab] (dtype cd, rows ld elements apart), the teacher's logits
+ * top_values [n, k] (dtype td) at the vocabulary entries top_index [n, k] (int32, or int64
+ * with index_bits 64) and temperature T:
+ *   p = softmax(top_values / T) over the row's present slots, q = softmax(z / T),
+ *   kl_i = T^2 sum_j p_j (log p_j - log q[index_j]),   loss = sum_i w_i kl_i,
+ *   dlogits_i = w_i T (q - p scattered to its indices)   [n, vocab], rows ldd apart.
+ * weight: fp32 [n], or NULL for 1 / n (the mean over the rows).  A slot is absent when its
+ * index lies outside [0, vocab) or its value is -inf; the same index may appear more than
+ * once (its shares add).  A row of weight 0 or without a present slot has kl 0 and gradient 0
+ * whatever its logits hold (NaN and infinities included).  Logits of -inf (forbidden entries)
+ * have q = 0; where p > 0 meets q = 0 the loss is +inf.  Otherwise a NaN or +inf among a
+ * row's logits or teacher values gives NaN.
+ * loss: one device float.  row_kl (nullable): fp32 [n], the kl_i.  dlogits (nullable: loss
+ * only) may be z itself with ldd = ld.  Statistics and sums are fp32 (the sum over the rows
+ * fp64) in a fixed order.  n == 0 writes loss = 0.
+ * ws: qlora_distill_workspace_bytes(n) bytes, 256-byte aligned.
+ * Errors: QLORA_ERR_INVALID_ARG (null pointers, T not positive and finite, index_bits not 32
+ * or 64, pointers that are not element-aligned), QLORA_ERR_SHAPE (n < 0, vocab < 1, k < 1,
+ * ld or ldd < vocab), QLORA_ERR_DTYPE, QLORA_ERR_WORKSPACE, QLORA_ERR_UNSUPPORTED
+ * (k > QLORA_DISTILL_MAX_K, n or vocab of 2^31 or more).
+ */
+int qlora_distill_loss_grad(const void* logits, int64_t n, int64_t vocab, int64_t ld, int32_t cd,
+                            const void* top_values, int32_t td, const void* top_index, int32_t index_bits,
+                            int32_t k, float temperature, const float* weight, float* loss, float* row_kl,
+                            void* dlogits, int64_t ldd, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of qlora_distill_loss_grad; 0 for n < 0.  Pure host function. */
+size_t qlora_distill_workspace_bytes(int64_t n);
+
 /* Workspace size in bytes for op (QLORA_OP_FWD / QLORA_OP_BWD, optionally OR'ed
  * with flags << QLORA_OP_FLAGS_SHIFT) on this layer shape; 0 for an invalid query.
  * Pure host function. */
@@ -447,8 +559,10 @@ enum {
   QLORA_K_BWD_DA,     /* dA = dT^T x */
   QLORA_K_BWD_DB,     /* dB = s dY^T T0 */
   QLORA_K_MERGE,      /* adapter merge into the dense weight */
-  QLORA_K_LOSS,       /* MSE loss and its gradient */
+  QLORA_K_LOSS,       /* MSE or distillation loss and its gradient */
   QLORA_K_OPTIM,      /* AdamW update of an adapter */
+  QLORA_K_INT8_ROWS,  /* rows to 8-bit codes and scales (with the experts' route) */
+  QLORA_K_INT8_GEMM,  /* product in 8-bit integers */
   QLORA_K_COUNT
 };
 int qlora_profile_enable(int32_t on);
