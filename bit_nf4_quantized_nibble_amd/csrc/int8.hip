@@ -34,26 +34,6 @@ __device__ __forceinline__ float scale_of_bits(uint32_t amax) {
   return amax >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : __fdiv_rn(__uint_as_float(amax), 127.f);
 }
 
-template <int CD>
-__global__ __launch_bounds__(kThreads) void k_int8_rows(const void* __restrict__ x, int64_t ldx, int64_t rows,
-                                                        int64_t cols, int64_t ld, int8_t* __restrict__ codes,
-                                                        float* __restrict__ scale) {
-  __shared__ uint32_t red[kThreads / 64];
-  const int64_t row = blockIdx.x;
-  uint32_t amax = 0;
-  for (int64_t k = threadIdx.x; k < cols; k += kThreads)
-    amax = max(amax, __float_as_uint(load_cd<CD>(x, row * ldx + k)) & 0x7fffffffu);
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) amax = max(amax, (uint32_t)__shfl_xor((int)amax, off, 64));
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = amax;
-  __syncthreads();
-  amax = max(max(red[0], red[1]), max(red[2], red[3]));
-  const float s = scale_of_bits(amax);
-  if (threadIdx.x == 0) scale[row] = s;
-  for (int64_t k = threadIdx.x; k < ld; k += kThreads)
-    codes[row * ld + k] = (int8_t)((s > 0.f && k < cols) ? code_of(load_cd<CD>(x, row * ldx + k), s) : 0);
-}
-
 // ------------------------------------------------------------------------ routing
 // Experts' rows for the product kernels, from the caller's offsets: starts[e] is the
 // largest of offsets[0 .. e], limited to [0, m], so no row belongs to two experts
@@ -64,10 +44,16 @@ struct Route {
   int32_t* starts;  // [experts + 1]
   int32_t* count;   // [1]
   int4* tiles;      // [cap]
+  const int32_t* offsets;
+  int experts, tile_m, cap;  // cap 0: starts only
+  int64_t m;
 };
 
-__global__ __launch_bounds__(64) void k_int8_route(const int32_t* __restrict__ offsets, int experts, int64_t m,
-                                                   int tile_m, int cap, Route r) {
+// By one wave: running maximum and running sum over 64 experts at a time.
+__device__ __forceinline__ void route_experts(const Route& r) {
+  const int32_t* offsets = r.offsets;
+  const int experts = r.experts, tile_m = r.tile_m;
+  const int64_t m = r.m;
   const int lane = threadIdx.x;
   int before = 0;  // starts of the chunk's first expert
   int at = 0;      // tiles so far
@@ -88,7 +74,7 @@ __global__ __launch_bounds__(64) void k_int8_route(const int32_t* __restrict__ o
     }
     int start = __shfl_up(end, 1, 64);
     if (lane == 0) start = before;
-    const int n = end - start, t = (n + tile_m - 1) / tile_m;
+    const int n = end - start, t = r.cap ? (n + tile_m - 1) / tile_m : 0;
     int sum = t;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -99,12 +85,108 @@ __global__ __launch_bounds__(64) void k_int8_route(const int32_t* __restrict__ o
       r.starts[e + 1] = end;
       const int first = at + sum - t;
       for (int i = 0; i < t; ++i)
-        if (first + i < cap) r.tiles[first + i] = make_int4(e, start + i * tile_m, min(tile_m, n - i * tile_m), 0);
+        if (first + i < r.cap) r.tiles[first + i] = make_int4(e, start + i * tile_m, min(tile_m, n - i * tile_m), 0);
     }
     before = __shfl(end, 63, 64);
     at += __shfl(sum, 63, 64);
   }
-  if (lane == 0) *r.count = min(at, cap);
+  if (lane == 0) *r.count = min(at, r.cap);
+}
+
+// 8 consecutive elements of a row from column k on, 0 past the last column.
+template <int CD, bool VEC>
+__device__ __forceinline__ void load8(const void* x, int64_t at, int64_t k, int64_t cols, float (&v)[8]) {
+  if (VEC && k + 8 <= cols) {
+    if constexpr (CD == CD_F32) {
+      const f32x4_t a = *(const f32x4_t*)((const float*)x + at + k), b = *(const f32x4_t*)((const float*)x + at + k + 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = a[e];
+        v[4 + e] = b[e];
+      }
+    } else {
+      const u32x4_t a = *(const u32x4_t*)((const uint16_t*)x + at + k);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = from_cd16<CD>((uint16_t)(a[e >> 1] >> (16 * (e & 1))));
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = k + e < cols ? load_cd<CD>(x, at + k + e) : 0.f;
+  }
+}
+
+__device__ __forceinline__ uint32_t amax8(const float (&v)[8], uint32_t m) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7fffffffu);
+  return m;
+}
+
+__device__ __forceinline__ u32x2_t codes8(const float (&v)[8], float s) {
+  u32x2_t o = {0u, 0u};
+  if (s > 0.f)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e >> 2] |= (uint32_t)(code_of(v[e], s) & 255) << (8 * (e & 3));
+  return o;
+}
+
+// Codes and scales of rows, TPR threads to a row.  The row stays in registers between the
+// maximum and the codes (up to kHold runs of 8 elements per thread; longer rows are read
+// again, from the caches): one pass over x.  The workgroup after the last row forms the
+// experts' route (r.starts set), so that it costs no launch of its own.
+constexpr int kHold = 8;
+template <int CD, int TPR, bool VEC>
+__global__ __launch_bounds__(kThreads) void k_int8_rows(const void* __restrict__ x, int64_t ldx, int64_t rows,
+                                                        int64_t cols, int64_t ld, int8_t* __restrict__ codes,
+                                                        float* __restrict__ scale, Route r) {
+  __shared__ uint32_t red[kThreads / 64];
+  const int64_t row = (int64_t)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
+  if (r.starts && blockIdx.x == gridDim.x - 1) {
+    if (threadIdx.x < 64) route_experts(r);
+    return;
+  }
+  const int t = threadIdx.x % TPR;
+  const bool live = row < rows;
+  const int64_t at = row * ldx;
+  float v[kHold][8];
+  uint32_t amax = 0;
+  if (live) {
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+      const int64_t k = 8 * (t + (int64_t)i * TPR);
+      if (k < cols) load8<CD, VEC>(x, at, k, cols, v[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kHold; ++i)
+      if (8 * (t + (int64_t)i * TPR) < cols) amax = amax8(v[i], amax);
+    for (int64_t k = 8 * (t + (int64_t)kHold * TPR); k < cols; k += 8 * TPR) {
+      float w[8];
+      load8<CD, VEC>(x, at, k, cols, w);
+      amax = amax8(w, amax);
+    }
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) amax = max(amax, (uint32_t)__shfl_xor((int)amax, off, 64));
+  if constexpr (TPR > 64) {
+    static_assert(TPR == kThreads, "one row per wave or per workgroup");
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = amax;
+    __syncthreads();
+    amax = max(max(red[0], red[1]), max(red[2], red[3]));
+  }
+  if (!live) return;
+  const float s = scale_of_bits(amax);
+  if (t == 0) scale[row] = s;
+  int8_t* dst = codes + row * ld;
+#pragma unroll
+  for (int i = 0; i < kHold; ++i) {
+    const int64_t k = 8 * (t + (int64_t)i * TPR);
+    if (k < cols) *(u32x2_t*)(dst + k) = codes8(v[i], s);
+    else if (k < ld) *(u32x2_t*)(dst + k) = u32x2_t{0u, 0u};
+  }
+  for (int64_t k = 8 * (t + (int64_t)kHold * TPR); k < ld; k += 8 * TPR) {
+    float w[8];
+    if (k < cols) load8<CD, VEC>(x, at, k, cols, w);
+    *(u32x2_t*)(dst + k) = k < cols ? codes8(w, s) : u32x2_t{0u, 0u};
+  }
 }
 
 // ------------------------------------------------------------------------- product
@@ -126,54 +208,327 @@ __device__ __forceinline__ void store_y(const I8& p, int64_t row, int64_t col, i
   store_cd<CD>(p.y, row * p.n + col, (float)sum * sa * sb + bv);
 }
 
-constexpr int kT = 64;
+// ---------------------------------------------------------------- tiled product
+// A workgroup forms a TM x TN tile of y: NWM x NWN waves, each with WMB x WNB blocks of
+// the 32 x 32 x 32 matrix instruction.  The contraction advances 128 bytes per stage;
+// a stage's operands lie in LDS as rows of 128 bytes [TM token rows | TN weight rows],
+// 16-byte chunk c of row r at chunk c ^ swz(r) (one chunk of 16 consecutive rows then
+// touches every bank group once), copied from global memory without passing through
+// registers.  NS stages are in flight or in use.
+//
+// Stage u is four sub-steps of 32 contraction elements.  The fragments of a sub-step are
+// read while the one before multiplies, across stages too: one barrier per stage, before
+// the last sub-step, is where stage u + 1 has landed and every wave has its last
+// fragments of stage u, so that during the last sub-step the wave reads the first
+// fragments of stage u + 1 and the copies of stage u + NS into stage u's buffer begin.
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+typedef __attribute__((address_space(3))) void lds_void;
 
-template <int CD>
-__global__ __launch_bounds__(kThreads) void k_int8_simple(I8 p) {
-  __shared__ __attribute__((aligned(16))) int8_t as[kT][128 + 16], bs[kT][128 + 16];
-  int e = 0;
-  int64_t m0 = (int64_t)blockIdx.y * kT;
-  int rows = (int)min((int64_t)kT, p.m - m0);
-  if (p.count) {
-    if ((int)blockIdx.y >= *p.count) return;
-    const int4 t = p.tiles[blockIdx.y];
-    e = t.x;
-    m0 = t.y;
-    rows = t.z;
+__device__ __forceinline__ rsrc_t make_rsrc(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, (int)bytes, 0x00020000);
+}
+__device__ __forceinline__ i32x4_t ld128(rsrc_t r, uint32_t voff, uint32_t soff) {
+  return __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)voff, (int)soff, 0));
+}
+__device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+__device__ __forceinline__ void wait_lgkm0() { __builtin_amdgcn_s_waitcnt(0x3f | (7 << 4) | (0 << 8) | (3 << 14)); }
+__device__ __forceinline__ void barrier_only() { asm volatile("s_barrier" ::: "memory"); }
+
+template <int WMB_, int WNB_, int NWM_, int NWN_, int NS_>
+struct Tile {
+  static constexpr int WMB = WMB_, WNB = WNB_, NWM = NWM_, NWN = NWN_, NS = NS_;
+  static constexpr int NW = NWM * NWN, TM = 32 * WMB * NWM, TN = 32 * WNB * NWN;
+  static constexpr int STAGE = (TM + TN) * 128;         // LDS bytes of a stage
+  static constexpr int PER = (TM + TN) / 8 / NW;        // copies (8 rows each) per wave and stage
+  static constexpr int PER_A = TM / 8 / NW;             // the first of them fetch token rows
+  static_assert((TM / 8) % NW == 0 && (TN / 8) % NW == 0 && NW % 2 == 0, "copies split evenly");
+  static constexpr int LDS = NS * STAGE;
+};
+using Full = Tile<4, 2, 2, 4, 2>;  // 256 x 256, eight waves
+using Half = Tile<2, 2, 2, 4, 2>;  // 128 x 256, eight waves
+using Mid = Tile<2, 2, 2, 2, 2>;   // 128 x 128, four waves
+
+// One tile: expert e, token rows m0 .. m0 + rows, columns from n0 on.  lds: T::LDS bytes,
+// then TN scales and TN biases (fp32).
+template <int CD, class T>
+__device__ __forceinline__ void tile_product(const I8& p, char* lds, int e, int64_t m0, int rows, int64_t n0) {
+  constexpr int WMB = T::WMB, WNB = T::WNB, NMF = WMB * WNB, NRD = WMB + WNB;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int h = lane >> 5, r32 = lane & 31;
+  const int wm = (wave / T::NWN) * 32 * WMB, wn = (wave % T::NWN) * 32 * WNB;
+  const int ncols = (int)min((int64_t)T::TN, p.n - n0);
+  const int64_t wrow = (int64_t)e * p.n + n0;  // first weight row of the tile
+
+  float* cs = (float*)(lds + T::LDS);
+  for (int c = tid; c < T::TN; c += 64 * T::NW) {
+    cs[c] = c < ncols ? p.sb[wrow + c] : 0.f;
+    cs[T::TN + c] = (p.bias && c < ncols) ? load_cd<CD>(p.bias, wrow + c) : 0.f;
   }
-  const int64_t n0 = (int64_t)blockIdx.x * kT;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int8_t* bp = p.b + (int64_t)e * p.n * p.ld;
-  i32x16_t acc;
+
+  // copies: instruction i of wave w fills LDS rows 8 (w + NW i) .. + 7 of the stage; lane l
+  // lands in chunk l % 8 of row l / 8 and fetches the logical chunk that lies there
+  const int8_t* abase = p.a + m0 * p.ld;
+  const int8_t* bbase = p.b + wrow * p.ld;
+  const int64_t abytes = (int64_t)rows * p.ld, bbytes = (int64_t)ncols * p.ld;
+  const int crow = 8 * wave + (lane >> 3);
+  const uint32_t coff = (uint32_t)(crow * (int)p.ld + (((lane & 7) ^ swz(crow)) << 4));
+  const uint32_t cstep = (uint32_t)(8 * T::NW * (int)p.ld);
+  const int KT = (int)(p.ld >> 7);
+  auto copy = [&](int stage, int buf, int i) {
+    // past the last stage: an empty buffer, nothing is fetched
+    const bool in = stage < KT;
+    const bool a_side = i < T::PER_A;
+    const rsrc_t r = a_side ? make_rsrc(abase, in ? abytes : 0) : make_rsrc(bbase, in ? bbytes : 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + buf * T::STAGE + (wave + T::NW * i) * 1024), 16,
+                                             (int)(coff + (a_side ? i : i - T::PER_A) * cstep), stage * 128, 0, 0);
+  };
+
+  i32x16_t acc[WMB][WNB];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0;
-  for (int64_t k0 = 0; k0 < p.ld; k0 += 128) {
-    __syncthreads();
-    for (int q = tid; q < kT * 8; q += kThreads) {
-      const int r = q >> 3, c = (q & 7) * 16;
-      u32x4_t va = {0, 0, 0, 0}, vb = {0, 0, 0, 0};
-      if (r < rows) va = *(const u32x4_t*)(p.a + (m0 + r) * p.ld + k0 + c);
-      if (n0 + r < p.n) vb = *(const u32x4_t*)(bp + (n0 + r) * p.ld + k0 + c);
-      *(u32x4_t*)&as[r][c] = va;
-      *(u32x4_t*)&bs[r][c] = vb;
-    }
-    __syncthreads();
-    const int ar = (wave >> 1) * 32 + (lane & 31), br = (wave & 1) * 32 + (lane & 31);
+  for (int i = 0; i < WMB; ++i)
+#pragma unroll
+    for (int j = 0; j < WNB; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
+
+#pragma unroll
+  for (int s = 0; s < T::NS; ++s)
+#pragma unroll
+    for (int i = 0; i < T::PER; ++i) copy(s, s, i);
+
+  const int xr = swz(r32);
+  const int arow = (wm + r32) * 128, brow = (T::TM + wn + r32) * 128;
+  i32x4_t fa[2][WMB], fb[2][WNB];
+  // the t-th fragment of a sub-step in the order of first use: a0, the b's, the other a's
+  auto frag = [&](int set, const char* st, int ks, int t) {
+    const int c = ((2 * ks + h) ^ xr) << 4;
+    if (t == 0) fa[set][0] = *(const i32x4_t*)(st + arow + c);
+    else if (t <= WNB) fb[set][t - 1] = *(const i32x4_t*)(st + brow + (t - 1) * 32 * 128 + c);
+    else fa[set][t - WNB] = *(const i32x4_t*)(st + arow + (t - WNB) * 32 * 128 + c);
+  };
+
+  wait_vmcnt<(T::NS - 1) * T::PER>();  // stage 0 (and the loads of the scales, which are older)
+  wait_lgkm0();
+  barrier_only();
+#pragma unroll
+  for (int t = 0; t < NRD; ++t) frag(0, lds, 0, t);
+  int buf = 0;
+  for (int u = 0; u < KT; ++u) {
+    const char* st = lds + buf * T::STAGE;
+    const int nbuf = buf + 1 == T::NS ? 0 : buf + 1;
+    const char* nx = lds + nbuf * T::STAGE;
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int ks = 0; ks < 4; ++ks) {
-      const int c = (2 * ks + (lane >> 5)) * 16;
-      acc = __builtin_amdgcn_mfma_i32_32x32x32_i8(*(const i32x4_t*)&as[ar][c], *(const i32x4_t*)&bs[br][c], acc, 0, 0,
-                                                  0);
-    }
-  }
-  const int64_t col = n0 + (wave & 1) * 32 + (lane & 31);
-  if (col >= p.n) return;
-  const float sb = p.sb[e * p.n + col];
-  const float bv = p.bias ? load_cd<CD>(p.bias, e * p.n + col) : 0.f;
+      const int set = ks & 1;
+      if (ks == 3) {
+        wait_lgkm0();
+        wait_vmcnt<(T::NS - 2) * T::PER>();  // this wave's copies of stage u + 1
+        barrier_only();
+      }
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int r = (wave >> 1) * 32 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
-    if (r < rows) store_y<CD>(p, m0 + r, col, acc[i], p.sa[m0 + r], sb, bv);
+      for (int t = 0; t < NMF; ++t) {
+        const int i = t / WNB, j = t % WNB;
+        // the weight fragment is the row operand: the block is accumulated transposed
+        acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(fb[set][j], fa[set][i], acc[i][j], 0, 0, 0);
+#pragma unroll
+        for (int q = 0; q < NRD; ++q)
+          if (q * NMF / NRD == t) frag(set ^ 1, ks == 3 ? nx : st, ks == 3 ? 0 : ks + 1, q);
+        if (ks == 3) {
+#pragma unroll
+          for (int q = 0; q < T::PER; ++q)
+            if (q * NMF / T::PER == t) copy(u + T::NS, buf, q);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    buf = nbuf;
+  }
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();  // every copy has ended and every wave is past its reads: the LDS is free
+
+  // Lane (r32, h) of block (i, j) holds row 32 i + r32, columns 32 j + 8 q + 4 h + v of the
+  // wave's part in elements 4 q + v.  32 rows at a time go through the wave's own LDS (16-byte
+  // chunk c of a row at chunk c ^ row) and leave as whole rows of 32 WNB columns.
+  constexpr int ES = CD == CD_F32 ? 4 : 2, RB = 32 * WNB * ES, NC = RB / 16;
+  char* W = lds + wave * (32 * RB);
+  const bool vec = (p.n * ES) % 16 == 0 && ((uintptr_t)p.y & 15) == 0;
+#pragma unroll
+  for (int i = 0; i < WMB; ++i) {
+    const int row = wm + 32 * i + r32;
+    const float sa = row < rows ? p.sa[m0 + row] : 0.f;
+#pragma unroll
+    for (int j = 0; j < WNB; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int c0 = wn + 32 * j + 8 * q + 4 * h;
+        const f32x4_t sb = *(const f32x4_t*)(cs + c0), bv = *(const f32x4_t*)(cs + T::TN + c0);
+        float v[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) v[x] = (float)acc[i][j][4 * q + x] * sa * sb[x] + bv[x];
+        if constexpr (ES == 4) {
+          const f32x4_t o = {v[0], v[1], v[2], v[3]};
+          *(f32x4_t*)(W + r32 * RB + (((8 * j + 2 * q + h) ^ (r32 & (NC - 1))) << 4)) = o;
+        } else {
+          const u32x2_t o = {pack2<CD>(v[0], v[1]), pack2<CD>(v[2], v[3])};
+          *(u32x2_t*)(W + r32 * RB + (((4 * j + q) ^ (r32 & (NC - 1))) << 4) + 8 * h) = o;
+        }
+      }
+    wait_lgkm0();  // the wave reads back only what it wrote
+    asm volatile("" ::: "memory");
+    if (vec) {
+      const int c = lane & (NC - 1), col = wn + c * (16 / ES);
+#pragma unroll
+      for (int it = 0; it < NC / 2; ++it) {
+        const int m = (64 / NC) * it + lane / NC;
+        const u32x4_t v = *(const u32x4_t*)(W + m * RB + ((c ^ (m & (NC - 1))) << 4));
+        const int orow = wm + 32 * i + m;
+        if (orow < rows && col < ncols)  // ncols is a whole number of chunks here
+          __builtin_nontemporal_store(v, (u32x4_t*)((char*)p.y + ((m0 + orow) * p.n + n0 + col) * ES));
+      }
+    } else {
+      for (int q = lane; q < 32 * 32 * WNB; q += 64) {  // element by element: a lane per column
+        const int m = q / (32 * WNB), cc = q % (32 * WNB);
+        const int byte = m * RB + (((cc * ES / 16) ^ (m & (NC - 1))) << 4) + (cc * ES) % 16;
+        const int orow = wm + 32 * i + m;
+        if (orow < rows && wn + cc < ncols) {
+          const int64_t at = (m0 + orow) * p.n + n0 + wn + cc;
+          if constexpr (ES == 4) ((uint32_t*)p.y)[at] = *(const uint32_t*)(W + byte);
+          else ((uint16_t*)p.y)[at] = *(const uint16_t*)(W + byte);
+        }
+      }
+    }
+    wait_lgkm0();  // the reads are done before the next 32 rows overwrite them
+    asm volatile("" ::: "memory");
+  }
+}
+
+// Position of workgroup b among n when each XCD (workgroups b, b + 8, ...) takes a
+// contiguous run of positions, so that its L2 serves neighbouring tiles.
+__device__ __forceinline__ int xcd_run(int b, int n) {
+  const int q = n >> 3, rem = n & 7, x = b & 7;
+  return x * q + min(x, rem) + (b >> 3);
+}
+// Tile t of an order that walks groups of four tile rows column by column.
+__device__ __forceinline__ void grouped_tile(int t, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int per = 4 * tiles_n, g = t / per, u = t % per, gm = min(4, tiles_m - g * 4);
+  tm = g * 4 + u % gm;
+  tn = u / gm;
+}
+
+// Workgroup -> tile.  False: nothing to do (the route has fewer tiles than the grid allows).
+template <class T>
+__device__ __forceinline__ bool tile_of(const I8& p, int& e, int64_t& m0, int& rows, int64_t& n0) {
+  const int tiles_n = (int)((p.n + T::TN - 1) / T::TN);
+  const int tiles_m = p.count ? __builtin_amdgcn_readfirstlane(*p.count) : (int)((p.m + T::TM - 1) / T::TM);
+  if ((int)blockIdx.x >= tiles_m * tiles_n) return false;
+  int tm, tn;
+  grouped_tile(xcd_run(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
+  tm = __builtin_amdgcn_readfirstlane(tm);
+  tn = __builtin_amdgcn_readfirstlane(tn);
+  n0 = (int64_t)tn * T::TN;
+  if (p.count) {
+    const int4 t = p.tiles[tm];
+    e = __builtin_amdgcn_readfirstlane(t.x);
+    m0 = __builtin_amdgcn_readfirstlane(t.y);
+    rows = __builtin_amdgcn_readfirstlane(t.z);
+  } else {
+    e = 0;
+    m0 = (int64_t)tm * T::TM;
+    rows = (int)min((int64_t)T::TM, p.m - m0);
+  }
+  return true;
+}
+
+template <int CD>
+__global__ __launch_bounds__(512, 1) void k_int8_full(I8 p) {
+  __shared__ __attribute__((aligned(1024))) char lds[Full::LDS + 2 * Full::TN * 4];
+  int e, rows;
+  int64_t m0, n0;
+  if (!tile_of<Full>(p, e, m0, rows, n0)) return;
+  if (rows > Half::TM) tile_product<CD, Full>(p, lds, e, m0, rows, n0);
+  else tile_product<CD, Half>(p, lds, e, m0, rows, n0);
+}
+
+template <int CD>
+__global__ __launch_bounds__(256, 2) void k_int8_mid(I8 p) {
+  __shared__ __attribute__((aligned(1024))) char lds[Mid::LDS + 2 * Mid::TN * 4];
+  int e, rows;
+  int64_t m0, n0;
+  if (!tile_of<Mid>(p, e, m0, rows, n0)) return;
+  tile_product<CD, Mid>(p, lds, e, m0, rows, n0);
+}
+
+// ------------------------------------------------------------- a few tokens (decode)
+// At up to 16 tokens per expert the product reads each weight once and does little else:
+// a workgroup takes 16 weight rows of one expert over the whole contraction, its NWV waves
+// dealing out 128-byte lines of it.  Codes go from global memory straight into the
+// 16 x 16 x 64 matrix instruction (lane l: row l % 16, 16 bytes l / 16 of a 64-byte piece),
+// weight rows as one operand and tokens as the other; the waves' sums meet in LDS.
+// More than 16 tokens of an expert: the workgroup goes over its weight rows again for
+// each 16 of them (from the caches).
+template <int CD, int NWV>
+__global__ __launch_bounds__(64 * NWV) void k_int8_few(I8 p, const int32_t* __restrict__ starts) {
+  __shared__ int red[NWV][16][17];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int e = blockIdx.y;
+  int64_t first = 0, end = p.m;
+  if (starts) {
+    first = __builtin_amdgcn_readfirstlane(starts[e]);
+    end = __builtin_amdgcn_readfirstlane(starts[e + 1]);
+  }
+  if (first >= end) return;
+  const int64_t n0 = (int64_t)blockIdx.x * 16;
+  const int ncols = (int)min((int64_t)16, p.n - n0);
+  const int64_t wrow = (int64_t)e * p.n + n0;
+  const rsrc_t rb = make_rsrc(p.b + wrow * p.ld, (int64_t)ncols * p.ld);
+  const uint32_t off = (uint32_t)((lane & 15) * (int)p.ld + (lane >> 4) * 16);
+  const int lines = (int)(p.ld >> 7);
+  for (int64_t m0 = first; m0 < end; m0 += 16) {
+    const int rows = (int)min((int64_t)16, end - m0);
+    const rsrc_t ra = make_rsrc(p.a + m0 * p.ld, (int64_t)rows * p.ld);
+    i32x4_t acc0 = {0, 0, 0, 0}, acc1 = {0, 0, 0, 0};
+    int l = wave;
+    // eight lines at a time: every load is requested before the first product
+    for (; l + 7 * NWV < lines; l += 8 * NWV) {
+      i32x4_t w[16], a[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = ld128(rb, off, (uint32_t)((l + (i >> 1) * NWV) * 128 + (i & 1) * 64));
+#pragma unroll
+      for (int i = 0; i < 16; ++i) a[i] = ld128(ra, off, (uint32_t)((l + (i >> 1) * NWV) * 128 + (i & 1) * 64));
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) {
+        acc0 = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[i], a[i], acc0, 0, 0, 0);
+        acc1 = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[i + 1], a[i + 1], acc1, 0, 0, 0);
+      }
+    }
+    for (; l < lines; l += NWV) {
+      const i32x4_t w0 = ld128(rb, off, (uint32_t)(l * 128)), w1 = ld128(rb, off, (uint32_t)(l * 128 + 64));
+      const i32x4_t a0 = ld128(ra, off, (uint32_t)(l * 128)), a1 = ld128(ra, off, (uint32_t)(l * 128 + 64));
+      acc0 = __builtin_amdgcn_mfma_i32_16x16x64_i8(w0, a0, acc0, 0, 0, 0);
+      acc1 = __builtin_amdgcn_mfma_i32_16x16x64_i8(w1, a1, acc1, 0, 0, 0);
+    }
+    // lane l: token l % 16, weight rows 4 (l / 16) .. + 3
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[wave][lane & 15][4 * (lane >> 4) + i] = acc0[i] + acc1[i];
+    __syncthreads();
+    if (tid < 256) {
+      const int t = tid >> 4, c = tid & 15;
+      int sum = 0;
+#pragma unroll
+      for (int w = 0; w < NWV; ++w) sum += red[w][t][c];
+      if (t < rows && c < ncols)
+        store_y<CD>(p, m0 + t, n0 + c, sum, p.sa[m0 + t], p.sb[wrow + c],
+                    p.bias ? load_cd<CD>(p.bias, wrow + c) : 0.f);
+    }
+    __syncthreads();
   }
 }
 
@@ -185,13 +540,22 @@ struct Plan {
   int cap = 0;
 };
 
+// Which product kernel takes a call: the few-token kernel up to 16 tokens per expert on
+// average, tiles of 128 x 128 up to 512, tiles of 256 x 256 beyond.
+enum Form { FEW, MID, FULL };
+Form form_of(int64_t m, int32_t experts) {
+  const int64_t live = std::max<int64_t>(1, std::min<int64_t>(experts, m));
+  return m <= 16 * live ? FEW : m <= 512 * live ? MID : FULL;
+}
+int tile_rows(int64_t m, int32_t experts) { return form_of(m, experts) == FULL ? Full::TM : Mid::TM; }
+
 Plan plan_int8(int64_t m, int64_t cols, int32_t experts, bool grouped) {
   Plan P;
   size_t off = al((size_t)m * QLORA_INT8_LD(cols));
   P.off_scale = off;
   off += al((size_t)m * 4);
   if (grouped) {
-    P.cap = (int)(m / kT + std::min<int64_t>(experts, m));
+    P.cap = (int)(m / tile_rows(m, experts) + std::min<int64_t>(experts, m));
     P.off_starts = off;
     off += al(((size_t)experts + 1) * 4);
     P.off_count = off;
@@ -203,21 +567,56 @@ Plan plan_int8(int64_t m, int64_t cols, int32_t experts, bool grouped) {
   return P;
 }
 
-int rows_to_int8(int cd, const void* x, int64_t ldx, int64_t rows, int64_t cols, int8_t* codes, float* scale,
-                 hipStream_t s) {
+template <int CD, int TPR>
+int launch_rows(const void* x, int64_t ldx, int64_t rows, int64_t cols, int8_t* codes, float* scale, const Route& r,
+                hipStream_t s) {
   const int64_t ld = QLORA_INT8_LD(cols);
-  const dim3 g((unsigned)rows), b(kThreads);
-  if (cd == CD_BF16) k_int8_rows<CD_BF16><<<g, b, 0, s>>>(x, ldx, rows, cols, ld, codes, scale);
-  else if (cd == CD_F16) k_int8_rows<CD_F16><<<g, b, 0, s>>>(x, ldx, rows, cols, ld, codes, scale);
-  else k_int8_rows<CD_F32><<<g, b, 0, s>>>(x, ldx, rows, cols, ld, codes, scale);
+  const dim3 g((unsigned)(ceil_div(rows, kThreads / TPR) + (r.starts ? 1 : 0))), b(kThreads);
+  if (((uintptr_t)x & 15) == 0 && (rows == 1 || ldx * cd_bytes(CD) % 16 == 0))
+    k_int8_rows<CD, TPR, true><<<g, b, 0, s>>>(x, ldx, rows, cols, ld, codes, scale, r);
+  else
+    k_int8_rows<CD, TPR, false><<<g, b, 0, s>>>(x, ldx, rows, cols, ld, codes, scale, r);
   return check_launch("k_int8_rows");
+}
+
+// A wave per row where that fills the chip and the row fits its registers, else a
+// workgroup per row.
+template <int CD>
+int rows_cd(const void* x, int64_t ldx, int64_t rows, int64_t cols, int8_t* codes, float* scale, const Route& r,
+            hipStream_t s) {
+  if (cols <= 512 || (rows >= 4 * cu_count() && cols <= 64 * 8 * kHold))
+    return launch_rows<CD, 64>(x, ldx, rows, cols, codes, scale, r, s);
+  return launch_rows<CD, kThreads>(x, ldx, rows, cols, codes, scale, r, s);
+}
+
+int rows_to_int8(int cd, const void* x, int64_t ldx, int64_t rows, int64_t cols, int8_t* codes, float* scale,
+                 const Route& r, hipStream_t s) {
+  if (cd == CD_BF16) return rows_cd<CD_BF16>(x, ldx, rows, cols, codes, scale, r, s);
+  if (cd == CD_F16) return rows_cd<CD_F16>(x, ldx, rows, cols, codes, scale, r, s);
+  return rows_cd<CD_F32>(x, ldx, rows, cols, codes, scale, r, s);
+}
+
+template <int CD>
+int product(const I8& p, int32_t experts, int cap, const int32_t* starts, hipStream_t s) {
+  const Form f = form_of(p.m, experts);
+  if (f == FEW) {
+    const dim3 g((unsigned)ceil_div(p.n, 16), (unsigned)experts);
+    k_int8_few<CD, 4><<<g, dim3(256), 0, s>>>(p, starts);
+    return check_launch("k_int8_few");
+  }
+  const int tm = f == FULL ? Full::TM : Mid::TM, tn = f == FULL ? Full::TN : Mid::TN;
+  const int64_t tiles = (starts ? cap : ceil_div(p.m, tm)) * ceil_div(p.n, tn);
+  if (tiles >= (1LL << 31)) return set_error(QLORA_ERR_UNSUPPORTED, "int8: %lld tiles", (long long)tiles);
+  if (f == FULL) k_int8_full<CD><<<dim3((unsigned)tiles), dim3(512), 0, s>>>(p);
+  else k_int8_mid<CD><<<dim3((unsigned)tiles), dim3(256), 0, s>>>(p);
+  return check_launch(f == FULL ? "k_int8_full" : "k_int8_mid");
 }
 
 }  // namespace
 
 int launch_int8_quantize(const void* w, int64_t ldw, int dtype, const qlora_int8_t* q, hipStream_t s) {
   ProfScope prof(QLORA_K_INT8_ROWS, s);
-  return rows_to_int8(dtype, w, ldw, q->experts * q->rows, q->cols, q->codes, q->scale, s);
+  return rows_to_int8(dtype, w, ldw, q->experts * q->rows, q->cols, q->codes, q->scale, Route{}, s);
 }
 
 size_t int8_workspace_bytes(const qlora_int8_t* w, int64_t m, bool grouped) {
@@ -238,24 +637,30 @@ int launch_int8_linear(const qlora_int8_t* w, const void* x, int64_t m, int64_t 
   p.m = m;
   p.n = w->rows;
   p.ld = QLORA_INT8_LD(w->cols);
-  int rc;
+  Route r = {};
+  if (offsets) {
+    const bool tiles = form_of(m, w->experts) != FEW;
+    r.starts = (int32_t*)(base + P.off_starts);
+    r.count = (int32_t*)(base + P.off_count);
+    r.tiles = (int4*)(base + P.off_tiles);
+    r.offsets = offsets;
+    r.experts = w->experts;
+    r.tile_m = tile_rows(m, w->experts);
+    r.cap = tiles ? P.cap : 0;
+    r.m = m;
+    p.count = tiles ? r.count : nullptr;
+    p.tiles = r.tiles;
+  }
   {
     ProfScope prof(QLORA_K_INT8_ROWS, s);
-    if ((rc = rows_to_int8(cd, x, ldx, m, w->cols, (int8_t*)p.a, (float*)p.sa, s))) return rc;
-    if (offsets) {
-      Route r = {(int32_t*)(base + P.off_starts), (int32_t*)(base + P.off_count), (int4*)(base + P.off_tiles)};
-      k_int8_route<<<dim3(1), dim3(64), 0, s>>>(offsets, w->experts, m, kT, P.cap, r);
-      if ((rc = check_launch("k_int8_route"))) return rc;
-      p.count = r.count;
-      p.tiles = r.tiles;
-    }
+    const int rc = rows_to_int8(cd, x, ldx, m, w->cols, (int8_t*)p.a, (float*)p.sa, r, s);
+    if (rc) return rc;
   }
   ProfScope prof(QLORA_K_INT8_GEMM, s);
-  const dim3 g((unsigned)ceil_div(p.n, kT), (unsigned)(offsets ? P.cap : ceil_div(m, kT))), b(kThreads);
-  if (cd == CD_BF16) k_int8_simple<CD_BF16><<<g, b, 0, s>>>(p);
-  else if (cd == CD_F16) k_int8_simple<CD_F16><<<g, b, 0, s>>>(p);
-  else k_int8_simple<CD_F32><<<g, b, 0, s>>>(p);
-  return check_launch("k_int8_simple");
+  const int32_t* starts = offsets ? (const int32_t*)(base + P.off_starts) : nullptr;
+  if (cd == CD_BF16) return product<CD_BF16>(p, w->experts, P.cap, starts, s);
+  if (cd == CD_F16) return product<CD_F16>(p, w->experts, P.cap, starts, s);
+  return product<CD_F32>(p, w->experts, P.cap, starts, s);
 }
 
 }  // namespace qnf4
