@@ -7,7 +7,13 @@
 //   dz = w T (q - p scattered to idx).
 // A slot is absent when its index lies outside [0, V) or its value is -inf.  A row with
 // weight 0 or without a present slot has kl 0 and a zero gradient, whatever its logits
-// hold; they are not read.
+// hold.
+//
+// Bound by HBM: each logit read once, each gradient written once.  A workgroup keeps its
+// row in registers (as loaded, 16 bytes per chunk) between the maximum, the sum and the
+// gradient, and asks for the next row's chunk as soon as it has written the gradient of
+// the one in that register, so reads, writes and the exponentials overlap.  Rows too
+// long for the registers are read a second time (they then come from the caches).
 #include <math.h>
 
 #include <algorithm>
@@ -17,7 +23,6 @@
 namespace qnf4 {
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kMaxK = QLORA_DISTILL_MAX_K;
 
 struct Distill {
@@ -26,119 +31,356 @@ struct Distill {
   void* dz;            // [n][lddz] cd or null
   int64_t lddz;
   const void* u;       // [n][k] teacher values (ud)
-  int ud;
   const void* idx;     // [n][k] int32 or int64
-  int idx64;
-  const float* weight; // [n] or null: 1 / n
+  const float* weight; // [n] or null: w_default
   float* kl;           // [n]
   int64_t n, V;
-  int k;
-  float inv_t, t, w_default;
+  int32_t k, ud, idx64;
+  float t, inv_t, c;   // T, 1 / T, log2(e) / T
+  float w_default;
 };
 
 __device__ __forceinline__ float load_any(const void* p, int64_t i, int cd) {
   return cd == CD_F32 ? load_cd<CD_F32>(p, i) : cd == CD_BF16 ? load_cd<CD_BF16>(p, i) : load_cd<CD_F16>(p, i);
 }
 
-template <bool MAX>
-__device__ __forceinline__ float block_reduce(float v, float* red) {
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) {
-    const float o = __shfl_xor(v, off, 64);
-    v = MAX ? fmaxf(v, o) : v + o;
-  }
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  float s = red[0];
-#pragma unroll
-  for (int w = 1; w < kThreads / 64; ++w) s = MAX ? fmaxf(s, red[w]) : s + red[w];
-  return s;
+// 16 bytes at any element-aligned address (the memory system takes unaligned vectors;
+// rows of an odd vocabulary start anywhere).
+template <int ES>
+struct __attribute__((packed, aligned(ES))) Chunk {
+  u32x4_t v;
+};
+
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+__device__ __forceinline__ rsrc_t make_rsrc(const void* p, int bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, bytes, 0x00020000);
 }
 
 template <int CD>
-__global__ __launch_bounds__(kThreads) void k_distill(Distill p) {
-  __shared__ float red[kThreads / 64];
-  __shared__ int32_t si[kMaxK];   // index of a present slot, -1 of an absent one
-  __shared__ float sp[kMaxK];     // (u - max) / T, then p
-  const int64_t i = blockIdx.x;
-  const int tid = threadIdx.x;
-  const float w = p.weight ? p.weight[i] : p.w_default;
-  float umax = -INFINITY;
-  int any = 0;
-  for (int j = tid; j < p.k; j += kThreads) {
-    const int64_t ix = p.idx64 ? ((const int64_t*)p.idx)[i * p.k + j] : (int64_t)((const int32_t*)p.idx)[i * p.k + j];
-    const float u = load_any(p.u, i * p.k + j, p.ud);
-    const bool here = ix >= 0 && ix < p.V && !(u == -INFINITY);
-    si[j] = here ? (int32_t)ix : -1;
-    sp[j] = u;
-    if (here) umax = fmaxf(umax, u);
-    any |= here;
+struct Elem {
+  static constexpr int ES = CD == CD_F32 ? 4 : 2, PC = 16 / ES;  // elements per chunk
+  __device__ static __forceinline__ float get(const u32x4_t& v, int e) {
+    if constexpr (CD == CD_F32) return __uint_as_float(v[e]);
+    else if constexpr (CD == CD_BF16) return __uint_as_float((e & 1) ? v[e >> 1] & 0xffff0000u : v[e >> 1] << 16);
+    else return from_cd16<CD>((uint16_t)(v[e >> 1] >> (16 * (e & 1))));
   }
-  any = __syncthreads_or(any);
-  if (w == 0.f || !any) {
-    if (tid == 0) p.kl[i] = 0.f;
-    if (p.dz)
-      for (int64_t j = tid; j < p.V; j += kThreads) store_cd<CD>(p.dz, i * p.lddz + j, 0.f);
-    return;
-  }
-  umax = block_reduce<true>(umax, red);
-  float usum = 0.f;
-  for (int j = tid; j < p.k; j += kThreads)
-    if (si[j] >= 0) {
-      const float v = expf((sp[j] - umax) * p.inv_t);
-      usum += v;
-    }
-  usum = block_reduce<false>(usum, red);
-  float m = -INFINITY;
-  for (int64_t j = tid; j < p.V; j += kThreads) m = fmaxf(m, load_cd<CD>(p.z, i * p.ldz + j));
-  m = block_reduce<true>(m, red);
-  float sum = 0.f;
-  for (int64_t j = tid; j < p.V; j += kThreads) sum += expf((load_cd<CD>(p.z, i * p.ldz + j) - m) * p.inv_t);
-  sum = block_reduce<false>(sum, red);
-  const float lsum = logf(sum), lu = logf(usum);
-  float kl = 0.f;
-  for (int j = tid; j < p.k; j += kThreads)
-    if (si[j] >= 0) {
-      const float a = sp[j] - umax, b = load_cd<CD>(p.z, i * p.ldz + si[j]) - m;
-      const float pr = expf(a * p.inv_t) / usum;
-      if (pr != 0.f) kl += pr * ((a - b) * p.inv_t + (lsum - lu));
-    }
-  kl = block_reduce<false>(kl, red);
-  if (tid == 0) p.kl[i] = p.t * p.t * kl;
-  if (!p.dz) return;
-  const float wt = w * p.t;
-  // the slots' gradients are formed before the row is overwritten (dz may be z)
-  float g[kMaxK / kThreads];
+  __device__ static __forceinline__ u32x4_t pack(const float (&g)[PC]) {
+    u32x4_t o;
+    if constexpr (CD == CD_F32) {
 #pragma unroll
-  for (int s = 0; s < kMaxK / kThreads; ++s) {
-    const int j = tid + s * kThreads;
-    g[s] = 0.f;
-    if (j < p.k && si[j] >= 0) {
-      float pr = 0.f;  // an index may appear more than once
-      for (int l = 0; l < p.k; ++l)
-        if (si[l] == si[j]) pr += expf((sp[l] - umax) * p.inv_t) / usum;
-      g[s] = wt * (expf((load_cd<CD>(p.z, i * p.ldz + si[j]) - m) * p.inv_t) / sum - pr);
-    }
-  }
-  __syncthreads();
-  for (int64_t j = tid; j < p.V; j += kThreads)
-    store_cd<CD>(p.dz, i * p.lddz + j, wt * (expf((load_cd<CD>(p.z, i * p.ldz + j) - m) * p.inv_t) / sum));
-  __threadfence_block();
-  __syncthreads();
+      for (int e = 0; e < 4; ++e) o[e] = __float_as_uint(g[e]);
+    } else {
 #pragma unroll
-  for (int s = 0; s < kMaxK / kThreads; ++s) {
-    const int j = tid + s * kThreads;
-    if (j < p.k && si[j] >= 0) store_cd<CD>(p.dz, i * p.lddz + si[j], g[s]);
+      for (int e = 0; e < 4; ++e) o[e] = pack2<CD>(g[2 * e], g[2 * e + 1]);
+    }
+    return o;
+  }
+  __device__ static __forceinline__ u32x4_t load(const char* base, uint32_t off) {
+    return ((const Chunk<ES>*)(base + off))->v;
+  }
+  __device__ static __forceinline__ void store(char* base, uint32_t off, const u32x4_t& o) {
+    ((Chunk<ES>*)(base + off))->v = o;
+  }
+};
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor(v, off, 64));
+  return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off, 64);
+  return v;
+}
+
+// A row's teacher slots in LDS.  Slot j hangs in the list (head / next) of the thread that
+// writes the gradient of the chunk its index lies in: that thread, after its chunks, writes
+// the entries of its list once more with the teacher's share taken off (stores of one thread
+// to one address keep their order).  Two sets, used in turn by the rows that are not left
+// out: a wave that is ahead fills the next such row's set while others still read this
+// row's, and that row's first barrier holds it until they are done.
+template <int TPB>
+struct Slots {
+  int32_t head[TPB];    // first slot of the thread's list, -1: none
+  int32_t next[kMaxK];
+  int32_t idx[kMaxK];   // -1: absent
+  float e[kMaxK];       // exp((u - max) / T)
+  float share[kMaxK];   // p summed over the slots of the same index, at the first of them; else -1
+  float z[kMaxK];       // the student's logit at the index
+  float zmax[TPB / 64], umax[TPB / 64], zsum[TPB / 64], usum[TPB / 64], kl[TPB / 64];  // one per wave
+  int any[TPB / 64];
+};
+// The passes read a chunk's register anew: without this the compiler keeps every converted
+// element and exponential of one pass alive for the next, which takes many times the
+// registers the row itself does.
+__device__ __forceinline__ void opaque(u32x4_t& x) { asm volatile("" : "+v"(x)); }
+
+// NV > 0: rows of at most NV * TPB whole chunks, kept in registers.  NV = 0: rows of any
+// length, read twice.  Entries past the last whole chunk (fewer than a chunk) go one to a
+// thread.
+template <int CD, int TPB, int NV>
+__global__ __launch_bounds__(TPB, TPB == 256 ? 3 : 4) void k_distill(Distill p) {
+  using E = Elem<CD>;
+  constexpr int PC = E::PC, NW = TPB / 64, SPT = (kMaxK + TPB - 1) / TPB, NR = NV > 0 ? NV : 1;
+  __shared__ Slots<TPB> sets[2];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int V = (int)p.V;
+  const int full = V / PC, left = V - full * PC;  // whole chunks, entries past them
+  const uint32_t toff = tid * 16;
+  auto weight_of = [&](int64_t i) { return p.weight ? p.weight[i] : p.w_default; };
+  auto zrow_of = [&](int64_t i) { return (const char*)p.z + i * p.ldz * E::ES; };
+  auto owner = [&](int ix) { return ix < full * PC ? (ix / PC) % TPB : ix - full * PC; };
+
+  u32x4_t v[NR];
+  float vl = -INFINITY;  // the thread's entry past the last whole chunk
+  // A row's whole chunks as a buffer: lanes past them read nothing and write nothing; for a
+  // row that is left out (weight 0, or none) the buffer is empty.
+  auto chunks_of = [&](const void* row, bool there) { return make_rsrc(row, there ? full * 16 : 0); };
+  auto fetch = [&](rsrc_t r, int s) {
+    v[s] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)toff, s * TPB * 16, 0));
+  };
+  auto fetch_left = [&](const char* row) {
+    if (tid < left) vl = load_cd<CD>(row, (int64_t)full * PC + tid);
+  };
+  int64_t i = blockIdx.x;
+  float w = weight_of(i);
+  if (NV > 0 && w != 0.f) {
+#pragma unroll
+    for (int s = 0; s < NV; ++s) fetch(chunks_of(zrow_of(i), true), s);
+    fetch_left(zrow_of(i));
+  }
+  int turn = 0;
+  while (i < p.n) {
+    const char* zr = zrow_of(i);
+    char* dr = p.dz ? (char*)p.dz + i * p.lddz * E::ES : nullptr;
+    const int64_t ni = i + gridDim.x;
+    const float nw = ni < p.n ? weight_of(ni) : 0.f;
+    const char* nz = zrow_of(ni);  // read only where nw is not 0
+    const rsrc_t rn = chunks_of(nz, nw != 0.f);
+    bool live = w != 0.f;
+    Slots<TPB>& S = sets[turn];
+    if (live) turn ^= 1;
+    float m = 0.f, sum = 0.f, umax = 0.f, usum = 0.f;
+    if (live) {
+      // the row's slots, and the largest logit of the thread's entries
+      float su[SPT], sz[SPT];
+      int32_t si[SPT];
+      S.head[tid] = -1;
+      float um = -INFINITY;
+      bool here = false;
+#pragma unroll
+      for (int s = 0; s < SPT; ++s) {
+        const int j = tid + s * TPB;
+        si[s] = -1;
+        if (j < p.k) {
+          const int64_t at = i * p.k + j;
+          const int64_t ix = p.idx64 ? ((const int64_t*)p.idx)[at] : (int64_t)((const int32_t*)p.idx)[at];
+          su[s] = load_any(p.u, at, p.ud);
+          if (ix >= 0 && ix < V && !(su[s] == -INFINITY)) {
+            si[s] = (int32_t)ix;
+            sz[s] = load_cd<CD>(zr, ix);
+            S.z[j] = sz[s];
+            um = fmaxf(um, su[s]);
+            here = true;
+          }
+          S.idx[j] = si[s];
+        }
+      }
+      float zm = -INFINITY, zs = 0.f;
+      if constexpr (NV > 0) {
+#pragma unroll
+        for (int s = 0; s < NV; ++s)
+          if (s * TPB + wave * 64 < full) {
+            opaque(v[s]);
+            float cm = E::get(v[s], 0);
+#pragma unroll
+            for (int e = 1; e < PC; ++e) cm = fmaxf(cm, E::get(v[s], e));
+            zm = fmaxf(zm, s * TPB + tid < full ? cm : -INFINITY);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        zm = fmaxf(zm, vl);
+      } else {
+        // running maximum and sum of the thread's entries
+        auto add = [&](float cm, auto share) {
+          const float nm = fmaxf(zm, cm);
+          // a thread that has met only -inf so far has no share yet
+          zs = (zm == -INFINITY ? 0.f : zs * __builtin_amdgcn_exp2f((zm - nm) * p.c)) + share(nm);
+          zm = nm;
+        };
+        auto part = [&](float y, float nm) { return y == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((y - nm) * p.c); };
+        for (int c0 = 0; c0 < full; c0 += TPB) {
+          if (c0 + tid >= full) break;
+          const u32x4_t x = E::load(zr + (int64_t)c0 * 16, toff);
+          float cm = E::get(x, 0);
+#pragma unroll
+          for (int e = 1; e < PC; ++e) cm = fmaxf(cm, E::get(x, e));
+          add(cm, [&](float nm) {
+            float cs = 0.f;
+#pragma unroll
+            for (int e = 0; e < PC; ++e) cs += part(E::get(x, e), nm);
+            return cs;
+          });
+        }
+        vl = -INFINITY;
+        fetch_left(zr);
+        if (tid < left) add(vl, [&](float nm) { return part(vl, nm); });
+      }
+      const float zm_own = zm;
+      zm = wave_max(zm);
+      um = wave_max(um);
+      const bool wave_here = __any(here);
+      if (lane == 0) {
+        S.zmax[wave] = zm;
+        S.umax[wave] = um;
+        S.any[wave] = wave_here;
+      }
+      __syncthreads();
+      m = S.zmax[0];
+      umax = S.umax[0];
+      int any = S.any[0];
+#pragma unroll
+      for (int x = 1; x < NW; ++x) {
+        m = fmaxf(m, S.zmax[x]);
+        umax = fmaxf(umax, S.umax[x]);
+        any |= S.any[x];
+      }
+      live = any != 0;
+      if (live) {
+        float us = 0.f;
+#pragma unroll
+        for (int s = 0; s < SPT; ++s)
+          if (si[s] >= 0) {
+            const int j = tid + s * TPB;
+            const float ex = __builtin_amdgcn_exp2f((su[s] - umax) * p.c);
+            S.e[j] = ex;
+            us += ex;
+            S.next[j] = atomicExch(&S.head[owner(si[s])], j);
+          }
+        if constexpr (NV > 0) {
+#pragma unroll
+          for (int s = 0; s < NV; ++s) {
+            opaque(v[s]);
+            if (s * TPB + wave * 64 < full) {
+              float cs[2] = {0.f, 0.f};
+#pragma unroll
+              for (int e = 0; e < PC; ++e) cs[e & 1] += __builtin_amdgcn_exp2f((E::get(v[s], e) - m) * p.c);
+              zs += s * TPB + tid < full ? cs[0] + cs[1] : 0.f;
+              __builtin_amdgcn_sched_barrier(0);
+            }
+          }
+          if (tid < left) zs += __builtin_amdgcn_exp2f((vl - m) * p.c);
+        } else {
+          // the thread's share under the row's maximum; all of it -inf: none (a NaN stays)
+          zs = zm_own == -INFINITY && zs == 0.f ? 0.f : zs * __builtin_amdgcn_exp2f((zm_own - m) * p.c);
+        }
+        zs = wave_sum(zs);
+        us = wave_sum(us);
+        if (lane == 0) {
+          S.zsum[wave] = zs;
+          S.usum[wave] = us;
+        }
+        __syncthreads();
+        sum = S.zsum[0];
+        usum = S.usum[0];
+#pragma unroll
+        for (int x = 1; x < NW; ++x) {
+          sum += S.zsum[x];
+          usum += S.usum[x];
+        }
+        // kl, and the share each index carries
+        const float lsum = logf(sum) - logf(usum), uinv = 1.0f / usum;
+        float kl = 0.f;
+#pragma unroll
+        for (int s = 0; s < SPT; ++s)
+          if (si[s] >= 0) {
+            const int j = tid + s * TPB;
+            const float pr = S.e[j] * uinv;
+            if (pr != 0.f) kl += pr * (((su[s] - umax) - (sz[s] - m)) * p.inv_t + lsum);
+            int first = j, same = 0;
+            for (int l = S.head[owner(si[s])]; l >= 0; l = S.next[l])
+              if (S.idx[l] == si[s]) {
+                first = min(first, l);
+                ++same;
+              }
+            float share = -1.f;
+            if (first == j) {
+              share = pr;
+              if (same > 1) {  // in slot order, so that the sum is the same every time
+                share = 0.f;
+                for (int l = j; l < p.k; ++l)
+                  if (S.idx[l] == si[s]) share += S.e[l] * uinv;
+              }
+            }
+            S.share[j] = share;
+          }
+        kl = wave_sum(kl);
+        if (lane == 0) S.kl[wave] = kl;
+        __syncthreads();
+        if (tid == 0) {
+          float t = S.kl[0];
+#pragma unroll
+          for (int x = 1; x < NW; ++x) t += S.kl[x];
+          p.kl[i] = p.t * p.t * t;
+        }
+      }
+    }
+    if (!live && tid == 0) p.kl[i] = 0.f;
+    const float wt = w * p.t, inv = 1.0f / sum, gs = wt * inv;
+    // a chunk's gradient before the teacher's shares; zeros for a row that is left out
+    auto grad = [&](const u32x4_t& x) {
+      u32x4_t o = {0u, 0u, 0u, 0u};
+      if (live) {
+        float g[PC];
+#pragma unroll
+        for (int e = 0; e < PC; ++e) g[e] = gs * __builtin_amdgcn_exp2f((E::get(x, e) - m) * p.c);
+        o = E::pack(g);
+      }
+      return o;
+    };
+    if constexpr (NV > 0) {
+      const rsrc_t rd = chunks_of(dr, dr != nullptr);
+#pragma unroll
+      for (int s = 0; s < NV; ++s) {
+        opaque(v[s]);
+        if (s * TPB + wave * 64 < full)
+          __builtin_amdgcn_raw_buffer_store_b128(grad(v[s]), rd, (int)toff, s * TPB * 16, 0);
+        fetch(rn, s);
+        __builtin_amdgcn_sched_barrier(0);  // one chunk's exponentials at a time
+      }
+    } else if (dr) {
+      for (int c0 = 0; c0 < full; c0 += TPB)
+        if (c0 + tid < full) {
+          u32x4_t x = {0u, 0u, 0u, 0u};
+          if (live) x = E::load(zr + (int64_t)c0 * 16, toff);
+          E::store(dr + (int64_t)c0 * 16, toff, grad(x));
+        }
+    }
+    if (dr) {
+      if (tid < left)
+        store_cd<CD>(dr, (int64_t)full * PC + tid, live ? gs * __builtin_amdgcn_exp2f((vl - m) * p.c) : 0.f);
+      for (int l = live ? S.head[tid] : -1; l >= 0; l = S.next[l]) {
+        const float share = S.share[l];
+        if (share < 0.f) continue;  // a later slot of the same index
+        const float q = __builtin_amdgcn_exp2f((S.z[l] - m) * p.c) * inv;
+        store_cd<CD>(dr, S.idx[l], wt * (q - share));
+      }
+    }
+    if (NV > 0 && nw != 0.f) fetch_left(nz);
+    i = ni;
+    w = nw;
   }
 }
 
 // loss = sum of w_i kl_i in a fixed order, in 64 bits, rounded once.
-__global__ __launch_bounds__(kThreads) void k_distill_sum(const float* __restrict__ kl, const float* __restrict__ weight,
-                                                          int64_t n, float w_default, float* __restrict__ loss) {
-  __shared__ double red[kThreads / 64];
+constexpr int kSumThreads = 1024;
+__global__ __launch_bounds__(kSumThreads) void k_distill_sum(const float* __restrict__ kl,
+                                                             const float* __restrict__ weight, int64_t n,
+                                                             float w_default, float* __restrict__ loss) {
+  __shared__ double red[kSumThreads / 64];
   double acc = 0.0;
-  for (int64_t i = threadIdx.x; i < n; i += kThreads) {
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < n; i += kSumThreads) {
     const float w = weight ? weight[i] : w_default;
     acc += w == 0.f ? 0.0 : (double)w * (double)kl[i];
   }
@@ -146,7 +388,36 @@ __global__ __launch_bounds__(kThreads) void k_distill_sum(const float* __restric
   for (int off = 32; off >= 1; off >>= 1) acc += __shfl_xor(acc, off, 64);
   if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = acc;
   __syncthreads();
-  if (threadIdx.x == 0) loss[0] = (float)((red[0] + red[1]) + (red[2] + red[3]));
+  if (threadIdx.x == 0) {
+    double t = red[0];
+#pragma unroll
+    for (int x = 1; x < kSumThreads / 64; ++x) t += red[x];
+    loss[0] = (float)t;
+  }
+}
+
+// Workgroups: as many as are resident at once at most (each goes through its rows).
+template <int CD, int TPB, int NV>
+void launch_rows(const Distill& p, int per_cu, hipStream_t s) {
+  const int64_t g = std::min<int64_t>(p.n, (int64_t)per_cu * cu_count());
+  k_distill<CD, TPB, NV><<<dim3((unsigned)g), dim3(TPB), 0, s>>>(p);
+}
+
+// Threads and registers for a row of `chunks` 16-byte chunks.  With fewer rows than
+// compute units a row gets 1024 threads as soon as 256 would need more than four chunks
+// each.
+template <int CD>
+int distill_rows(const Distill& p, hipStream_t s) {
+  const int64_t chunks = p.V / Elem<CD>::PC;
+  const bool few = p.n <= cu_count();
+  if (chunks <= 256 * 4) launch_rows<CD, 256, 4>(p, 3, s);
+  else if (chunks <= 256 * 16 && !few) launch_rows<CD, 256, 16>(p, 3, s);
+  else if (chunks <= 1024 * 4) launch_rows<CD, 1024, 4>(p, 1, s);
+  else if (chunks <= 1024 * 8) launch_rows<CD, 1024, 8>(p, 1, s);
+  else if (chunks <= 1024 * 16) launch_rows<CD, 1024, 16>(p, 1, s);
+  else if (chunks <= 1024 * 20) launch_rows<CD, 1024, 20>(p, 1, s);
+  else launch_rows<CD, 1024, 0>(p, 1, s);
+  return check_launch("k_distill");
 }
 
 }  // namespace
@@ -161,26 +432,26 @@ int launch_distill(const void* z, int64_t n, int64_t V, int64_t ldz, int cd, con
   p.dz = dz;
   p.lddz = lddz;
   p.u = u;
-  p.ud = ud;
   p.idx = idx;
-  p.idx64 = idx64;
   p.weight = weight;
   p.kl = kl;
   p.n = n;
   p.V = V;
   p.k = k;
+  p.ud = ud;
+  p.idx64 = idx64;
   p.t = temperature;
-  p.inv_t = 1.0f / temperature;
+  p.inv_t = (float)(1.0 / (double)temperature);
+  p.c = (float)(1.4426950408889634074 / (double)temperature);
   p.w_default = n > 0 ? (float)(1.0 / (double)n) : 0.f;
-  int rc;
   if (n > 0) {
-    const dim3 g((unsigned)n), b(kThreads);
-    if (cd == CD_BF16) k_distill<CD_BF16><<<g, b, 0, s>>>(p);
-    else if (cd == CD_F16) k_distill<CD_F16><<<g, b, 0, s>>>(p);
-    else k_distill<CD_F32><<<g, b, 0, s>>>(p);
-    if ((rc = check_launch("k_distill"))) return rc;
+    int rc;
+    if (cd == CD_BF16) rc = distill_rows<CD_BF16>(p, s);
+    else if (cd == CD_F16) rc = distill_rows<CD_F16>(p, s);
+    else rc = distill_rows<CD_F32>(p, s);
+    if (rc) return rc;
   }
-  k_distill_sum<<<dim3(1), dim3(kThreads), 0, s>>>(kl, weight, n, p.w_default, loss);
+  k_distill_sum<<<dim3(1), dim3(kSumThreads), 0, s>>>(kl, weight, n, p.w_default, loss);
   return check_launch("k_distill_sum");
 }
 
