@@ -121,11 +121,32 @@ __device__ __forceinline__ uint32_t amax8(const float (&v)[8], uint32_t m) {
   return m;
 }
 
+// Eight codes.  x rcp(s) is within 127 * 3 * 2^-24 < 2.4e-5 of the quotient, so where it lies
+// further than 1e-4 from the middle between two integers it rounds to the same integer; the
+// sum with 1.5 * 2^23 does that rounding and leaves the code in the low byte.  A group with
+// an element nearer to a middle (1 in 600) divides, as does a row whose scale the
+// reciprocal does not take (below 2^-100: the quotient's bound needs a normal rcp).  A
+// division for every element took 18.6 instead of 12 us on 4096 x 4096 bf16.
 __device__ __forceinline__ u32x2_t codes8(const float (&v)[8], float s) {
   u32x2_t o = {0u, 0u};
-  if (s > 0.f)
+  if (!(s > 0.f)) return o;
+  const float r = __builtin_amdgcn_rcpf(s);
+  float far = 0.f;
+  uint32_t t[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e >> 2] |= (uint32_t)(code_of(v[e], s) & 255) << (8 * (e & 3));
+  for (int e = 0; e < 8; ++e) {
+    const float q = v[e] * r, sum = q + 12582912.f;
+    far = fmaxf(far, fabsf(q - (sum - 12582912.f)));
+    t[e] = __float_as_uint(sum);
+  }
+  if (far > 0.4999f || s < 0x1p-100f) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = (uint32_t)code_of(v[e], s);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; e += 4)
+    o[e >> 2] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(t[e + 3], t[e + 2], 0x0c0c0400u),
+                                      __builtin_amdgcn_perm(t[e + 1], t[e], 0x0c0c0400u), 0x05040100u);
   return o;
 }
 
@@ -248,60 +269,64 @@ struct Tile {
   static constexpr int PER_A = TM / 8 / NW;             // the first of them fetch token rows
   static_assert((TM / 8) % NW == 0 && (TN / 8) % NW == 0 && NW % 2 == 0, "copies split evenly");
   static constexpr int LDS = NS * STAGE;
+  static constexpr int COEF = 2 * TN + TM;              // scales and biases of the columns, scales of the rows
 };
-using Full = Tile<4, 2, 2, 4, 2>;  // 256 x 256, eight waves
-using Half = Tile<2, 2, 2, 4, 2>;  // 128 x 256, eight waves
-using Mid = Tile<2, 2, 2, 2, 2>;   // 128 x 128, four waves
 
-// One tile: expert e, token rows m0 .. m0 + rows, columns from n0 on.  lds: T::LDS bytes,
-// then TN scales and TN biases (fp32).
-template <int CD, class T>
-__device__ __forceinline__ void tile_product(const I8& p, char* lds, int e, int64_t m0, int rows, int64_t n0) {
-  constexpr int WMB = T::WMB, WNB = T::WNB, NMF = WMB * WNB, NRD = WMB + WNB;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int h = lane >> 5, r32 = lane & 31;
-  const int wm = (wave / T::NWN) * 32 * WMB, wn = (wave % T::NWN) * 32 * WNB;
-  const int ncols = (int)min((int64_t)T::TN, p.n - n0);
-  const int64_t wrow = (int64_t)e * p.n + n0;  // first weight row of the tile
+// Where a tile lies: expert, first token row, token rows, first column.
+struct Place {
+  int e, rows;
+  int64_t m0, n0;
+};
 
-  float* cs = (float*)(lds + T::LDS);
-  for (int c = tid; c < T::TN; c += 64 * T::NW) {
-    cs[c] = c < ncols ? p.sb[wrow + c] : 0.f;
-    cs[T::TN + c] = (p.bias && c < ncols) ? load_cd<CD>(p.bias, wrow + c) : 0.f;
+// The copies of a tile's stages by one wave: instruction i of wave w fills LDS rows
+// 8 (w + NW i) .. + 7 of the stage; lane l lands in chunk l % 8 of row l / 8 and fetches the
+// logical chunk that lies there.
+template <class T>
+struct Copies {
+  const int8_t *a, *b;
+  int64_t abytes, bbytes;
+  uint32_t off, step;
+  int KT, wave;
+  __device__ __forceinline__ Copies(const I8& p, const Place& t, int wave_, int lane) : wave(wave_) {
+    const int ncols = (int)min((int64_t)T::TN, p.n - t.n0), ld = (int)p.ld;
+    a = p.a + t.m0 * p.ld;
+    b = p.b + ((int64_t)t.e * p.n + t.n0) * p.ld;
+    abytes = (int64_t)t.rows * p.ld;
+    bbytes = (int64_t)ncols * p.ld;
+    const int row = 8 * wave + (lane >> 3);
+    off = (uint32_t)(row * ld + (((lane & 7) ^ swz(row)) << 4));
+    step = (uint32_t)(8 * T::NW * ld);
+    KT = ld >> 7;
   }
-
-  // copies: instruction i of wave w fills LDS rows 8 (w + NW i) .. + 7 of the stage; lane l
-  // lands in chunk l % 8 of row l / 8 and fetches the logical chunk that lies there
-  const int8_t* abase = p.a + m0 * p.ld;
-  const int8_t* bbase = p.b + wrow * p.ld;
-  const int64_t abytes = (int64_t)rows * p.ld, bbytes = (int64_t)ncols * p.ld;
-  const int crow = 8 * wave + (lane >> 3);
-  const uint32_t coff = (uint32_t)(crow * (int)p.ld + (((lane & 7) ^ swz(crow)) << 4));
-  const uint32_t cstep = (uint32_t)(8 * T::NW * (int)p.ld);
-  const int KT = (int)(p.ld >> 7);
-  auto copy = [&](int stage, int buf, int i) {
+  __device__ __forceinline__ void one(char* stage_lds, int stage, int i) const {
     // past the last stage: an empty buffer, nothing is fetched
-    const bool in = stage < KT;
-    const bool a_side = i < T::PER_A;
-    const rsrc_t r = a_side ? make_rsrc(abase, in ? abytes : 0) : make_rsrc(bbase, in ? bbytes : 0);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(lds + buf * T::STAGE + (wave + T::NW * i) * 1024), 16,
-                                             (int)(coff + (a_side ? i : i - T::PER_A) * cstep), stage * 128, 0, 0);
-  };
+    const bool in = stage < KT, a_side = i < T::PER_A;
+    const rsrc_t r = a_side ? make_rsrc(a, in ? abytes : 0) : make_rsrc(b, in ? bbytes : 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(stage_lds + (wave + T::NW * i) * 1024), 16,
+                                             (int)(off + (a_side ? i : i - T::PER_A) * step), stage * 128, 0, 0);
+  }
+  __device__ __forceinline__ void all(char* stage_lds, int stage) const {
+#pragma unroll
+    for (int i = 0; i < T::PER; ++i) one(stage_lds, stage, i);
+  }
+};
 
-  i32x16_t acc[WMB][WNB];
+template <class T>
+using Acc = i32x16_t[T::WMB][T::WNB];
+
+// The contraction.  On entry stage 0 lies in LDS for every wave and the copies of stages
+// 1 .. NS - 1 are requested; on return the LDS is free.
+template <class T>
+__device__ __forceinline__ void contract(Acc<T>& acc, char* lds, const Copies<T>& cp, int lane) {
+  constexpr int WMB = T::WMB, WNB = T::WNB, NMF = WMB * WNB, NRD = WMB + WNB;
+  const int h = lane >> 5, r32 = lane & 31;
+  const int wm = (cp.wave / T::NWN) * 32 * WMB, wn = (cp.wave % T::NWN) * 32 * WNB;
 #pragma unroll
   for (int i = 0; i < WMB; ++i)
 #pragma unroll
     for (int j = 0; j < WNB; ++j)
 #pragma unroll
       for (int v = 0; v < 16; ++v) acc[i][j][v] = 0;
-
-#pragma unroll
-  for (int s = 0; s < T::NS; ++s)
-#pragma unroll
-    for (int i = 0; i < T::PER; ++i) copy(s, s, i);
-
   const int xr = swz(r32);
   const int arow = (wm + r32) * 128, brow = (T::TM + wn + r32) * 128;
   i32x4_t fa[2][WMB], fb[2][WNB];
@@ -312,15 +337,11 @@ __device__ __forceinline__ void tile_product(const I8& p, char* lds, int e, int6
     else if (t <= WNB) fb[set][t - 1] = *(const i32x4_t*)(st + brow + (t - 1) * 32 * 128 + c);
     else fa[set][t - WNB] = *(const i32x4_t*)(st + arow + (t - WNB) * 32 * 128 + c);
   };
-
-  wait_vmcnt<(T::NS - 1) * T::PER>();  // stage 0 (and the loads of the scales, which are older)
-  wait_lgkm0();
-  barrier_only();
 #pragma unroll
   for (int t = 0; t < NRD; ++t) frag(0, lds, 0, t);
   int buf = 0;
-  for (int u = 0; u < KT; ++u) {
-    const char* st = lds + buf * T::STAGE;
+  for (int u = 0; u < cp.KT; ++u) {
+    char* st = lds + buf * T::STAGE;
     const int nbuf = buf + 1 == T::NS ? 0 : buf + 1;
     const char* nx = lds + nbuf * T::STAGE;
     __builtin_amdgcn_sched_barrier(0);
@@ -343,7 +364,7 @@ __device__ __forceinline__ void tile_product(const I8& p, char* lds, int e, int6
         if (ks == 3) {
 #pragma unroll
           for (int q = 0; q < T::PER; ++q)
-            if (q * NMF / T::PER == t) copy(u + T::NS, buf, q);
+            if (q * NMF / T::PER == t) cp.one(st, u + T::NS, q);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -351,63 +372,88 @@ __device__ __forceinline__ void tile_product(const I8& p, char* lds, int e, int6
     buf = nbuf;
   }
   __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();  // every copy has ended and every wave is past its reads: the LDS is free
-
-  // Lane (r32, h) of block (i, j) holds row 32 i + r32, columns 32 j + 8 q + 4 h + v of the
-  // wave's part in elements 4 q + v.  32 rows at a time go through the wave's own LDS (16-byte
-  // chunk c of a row at chunk c ^ row) and leave as whole rows of 32 WNB columns.
-  constexpr int ES = CD == CD_F32 ? 4 : 2, RB = 32 * WNB * ES, NC = RB / 16;
-  char* W = lds + wave * (32 * RB);
-  const bool vec = (p.n * ES) % 16 == 0 && ((uintptr_t)p.y & 15) == 0;
-#pragma unroll
-  for (int i = 0; i < WMB; ++i) {
-    const int row = wm + 32 * i + r32;
-    const float sa = row < rows ? p.sa[m0 + row] : 0.f;
-#pragma unroll
-    for (int j = 0; j < WNB; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int c0 = wn + 32 * j + 8 * q + 4 * h;
-        const f32x4_t sb = *(const f32x4_t*)(cs + c0), bv = *(const f32x4_t*)(cs + T::TN + c0);
-        float v[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) v[x] = (float)acc[i][j][4 * q + x] * sa * sb[x] + bv[x];
-        if constexpr (ES == 4) {
-          const f32x4_t o = {v[0], v[1], v[2], v[3]};
-          *(f32x4_t*)(W + r32 * RB + (((8 * j + 2 * q + h) ^ (r32 & (NC - 1))) << 4)) = o;
-        } else {
-          const u32x2_t o = {pack2<CD>(v[0], v[1]), pack2<CD>(v[2], v[3])};
-          *(u32x2_t*)(W + r32 * RB + (((4 * j + q) ^ (r32 & (NC - 1))) << 4) + 8 * h) = o;
-        }
-      }
-    wait_lgkm0();  // the wave reads back only what it wrote
-    asm volatile("" ::: "memory");
-    if (vec) {
-      const int c = lane & (NC - 1), col = wn + c * (16 / ES);
-#pragma unroll
-      for (int it = 0; it < NC / 2; ++it) {
-        const int m = (64 / NC) * it + lane / NC;
-        const u32x4_t v = *(const u32x4_t*)(W + m * RB + ((c ^ (m & (NC - 1))) << 4));
-        const int orow = wm + 32 * i + m;
-        if (orow < rows && col < ncols)  // ncols is a whole number of chunks here
-          __builtin_nontemporal_store(v, (u32x4_t*)((char*)p.y + ((m0 + orow) * p.n + n0 + col) * ES));
-      }
-    } else {
-      for (int q = lane; q < 32 * 32 * WNB; q += 64) {  // element by element: a lane per column
-        const int m = q / (32 * WNB), cc = q % (32 * WNB);
-        const int byte = m * RB + (((cc * ES / 16) ^ (m & (NC - 1))) << 4) + (cc * ES) % 16;
-        const int orow = wm + 32 * i + m;
-        if (orow < rows && wn + cc < ncols) {
-          const int64_t at = (m0 + orow) * p.n + n0 + wn + cc;
-          if constexpr (ES == 4) ((uint32_t*)p.y)[at] = *(const uint32_t*)(W + byte);
-          else ((uint16_t*)p.y)[at] = *(const uint16_t*)(W + byte);
-        }
-      }
-    }
-    wait_lgkm0();  // the reads are done before the next 32 rows overwrite them
-    asm volatile("" ::: "memory");
-  }
+  __syncthreads();  // every copy has ended and every wave is past its reads
 }
+
+// The tile's scales and biases, value i of T::COEF.
+template <int CD, class T>
+__device__ __forceinline__ float coefficient(const I8& p, const Place& t, int i) {
+  const int64_t wrow = (int64_t)t.e * p.n + t.n0;
+  if (i < T::TN) return t.n0 + i < p.n ? p.sb[wrow + i] : 0.f;
+  if (i < 2 * T::TN) return p.bias && t.n0 + i - T::TN < p.n ? load_cd<CD>(p.bias, wrow + i - T::TN) : 0.f;
+  return i - 2 * T::TN < t.rows ? p.sa[t.m0 + i - 2 * T::TN] : 0.f;
+}
+
+// Lane (r32, h) of block (i, j) holds row 32 i + r32, columns 32 j + 8 q + 4 h + v of the
+// wave's part in elements 4 q + v.  32 rows at a time go through the wave's own LDS W (16-byte
+// chunk c of a row at chunk c ^ row) and leave as whole rows of 32 WNB columns.  Where y's rows
+// are whole chunks every wave issues exactly stores() stores (rows and columns past the
+// tile's fall outside their buffer), so a caller can count past them; other rows go element by
+// element, and the wave waits for those.
+template <int CD, class T>
+struct Writer {
+  static constexpr int ES = CD == CD_F32 ? 4 : 2, RB = 32 * T::WNB * ES, NC = RB / 16;
+  static constexpr int stores() { return T::WMB * NC / 2; }
+  __device__ static __forceinline__ void run(const I8& p, const Place& pl, const Acc<T>& acc, const float* coef, char* W,
+                                             int wave, int lane) {
+    constexpr int WMB = T::WMB, WNB = T::WNB;
+    const int h = lane >> 5, r32 = lane & 31;
+    const int wm = (wave / T::NWN) * 32 * WMB, wn = (wave % T::NWN) * 32 * WNB;
+    const int ncols = (int)min((int64_t)T::TN, p.n - pl.n0);
+    const bool vec = (p.n * ES) % 16 == 0 && ((uintptr_t)p.y & 15) == 0 && p.n * ES < (1 << 26);
+#pragma unroll
+    for (int i = 0; i < WMB; ++i) {
+      const float sa = coef[2 * T::TN + wm + 32 * i + r32];
+#pragma unroll
+      for (int j = 0; j < WNB; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int c0 = wn + 32 * j + 8 * q + 4 * h;
+          const f32x4_t sb = *(const f32x4_t*)(coef + c0), bv = *(const f32x4_t*)(coef + T::TN + c0);
+          float v[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) v[x] = (float)acc[i][j][4 * q + x] * sa * sb[x] + bv[x];
+          if constexpr (ES == 4) {
+            const f32x4_t o = {v[0], v[1], v[2], v[3]};
+            *(f32x4_t*)(W + r32 * RB + (((8 * j + 2 * q + h) ^ (r32 & (NC - 1))) << 4)) = o;
+          } else {
+            const u32x2_t o = {pack2<CD>(v[0], v[1]), pack2<CD>(v[2], v[3])};
+            *(u32x2_t*)(W + r32 * RB + (((4 * j + q) ^ (r32 & (NC - 1))) << 4) + 8 * h) = o;
+          }
+        }
+      wait_lgkm0();  // the wave reads back only what it wrote
+      asm volatile("" ::: "memory");
+      const int row0 = wm + 32 * i, left = min(32, pl.rows - row0);  // rows of the tile in these 32
+      const int64_t at0 = (pl.m0 + row0) * p.n + pl.n0 + wn;
+      if (vec) {
+        const int c = lane & (NC - 1);
+        const rsrc_t r = make_rsrc((char*)p.y + at0 * ES, left > 0 ? left * p.n * ES : 0);
+        // ncols is a whole number of chunks here
+        const uint32_t none = wn + c * (16 / ES) < ncols ? 0u : 1u << 31;
+#pragma unroll
+        for (int it = 0; it < NC / 2; ++it) {
+          const int m = (64 / NC) * it + lane / NC;
+          const u32x4_t v = *(const u32x4_t*)(W + m * RB + ((c ^ (m & (NC - 1))) << 4));
+          const uint32_t off = (uint32_t)(m * (int)p.n * ES + c * 16);
+          __builtin_amdgcn_raw_buffer_store_b128(v, r, (int)((m < left ? off : 1u << 31) | none), 0, 2);
+        }
+      } else {
+        for (int q = lane; q < 32 * 32 * WNB; q += 64) {  // a lane per column
+          const int m = q / (32 * WNB), cc = q % (32 * WNB);
+          const int byte = m * RB + (((cc * ES / 16) ^ (m & (NC - 1))) << 4) + (cc * ES) % 16;
+          if (m < left && wn + cc < ncols) {
+            const int64_t at = at0 + (int64_t)m * p.n + cc;
+            if constexpr (ES == 4) ((uint32_t*)p.y)[at] = *(const uint32_t*)(W + byte);
+            else ((uint16_t*)p.y)[at] = *(const uint16_t*)(W + byte);
+          }
+        }
+      }
+      wait_lgkm0();  // the reads are done before the next 32 rows overwrite them
+      asm volatile("" ::: "memory");
+    }
+    if (!vec) wait_vmcnt<0>();
+  }
+};
 
 // Position of workgroup b among n when each XCD (workgroups b, b + 8, ...) takes a
 // contiguous run of positions, so that its L2 serves neighbouring tiles.
@@ -421,61 +467,171 @@ __device__ __forceinline__ void grouped_tile(int t, int tiles_m, int tiles_n, in
   tm = g * 4 + u % gm;
   tn = u / gm;
 }
-
-// Workgroup -> tile.  False: nothing to do (the route has fewer tiles than the grid allows).
 template <class T>
-__device__ __forceinline__ bool tile_of(const I8& p, int& e, int64_t& m0, int& rows, int64_t& n0) {
-  const int tiles_n = (int)((p.n + T::TN - 1) / T::TN);
-  const int tiles_m = p.count ? __builtin_amdgcn_readfirstlane(*p.count) : (int)((p.m + T::TM - 1) / T::TM);
-  if ((int)blockIdx.x >= tiles_m * tiles_n) return false;
+__device__ __forceinline__ int tile_rows_of(const I8& p) {
+  return p.count ? __builtin_amdgcn_readfirstlane(*p.count) : (int)((p.m + T::TM - 1) / T::TM);
+}
+template <class T>
+__device__ __forceinline__ Place place_of(const I8& p, int t, int tiles_m, int tiles_n) {
   int tm, tn;
-  grouped_tile(xcd_run(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n, tm, tn);
+  grouped_tile(t, tiles_m, tiles_n, tm, tn);
   tm = __builtin_amdgcn_readfirstlane(tm);
   tn = __builtin_amdgcn_readfirstlane(tn);
-  n0 = (int64_t)tn * T::TN;
+  Place pl;
+  pl.n0 = (int64_t)tn * T::TN;
   if (p.count) {
-    const int4 t = p.tiles[tm];
-    e = __builtin_amdgcn_readfirstlane(t.x);
-    m0 = __builtin_amdgcn_readfirstlane(t.y);
-    rows = __builtin_amdgcn_readfirstlane(t.z);
+    const int4 r = p.tiles[tm];
+    pl.e = __builtin_amdgcn_readfirstlane(r.x);
+    pl.m0 = __builtin_amdgcn_readfirstlane(r.y);
+    pl.rows = __builtin_amdgcn_readfirstlane(r.z);
   } else {
-    e = 0;
-    m0 = (int64_t)tm * T::TM;
-    rows = (int)min((int64_t)T::TM, p.m - m0);
+    pl.e = 0;
+    pl.m0 = (int64_t)tm * T::TM;
+    pl.rows = (int)min((int64_t)T::TM, p.m - pl.m0);
   }
-  return true;
+  return pl;
 }
 
+// One tile to a workgroup; several workgroups share a compute unit.
+template <int CD, class T, int WGS>
+__global__ __launch_bounds__(64 * T::NW, WGS) void k_int8_tile(I8 p) {
+  // One array for everything: with several, the compiler tells them apart and then waits for
+  // every copy in flight before each fragment it reads (228 -> 324 us on the long prompt).
+  __shared__ __attribute__((aligned(1024))) char lds[T::LDS + T::COEF * 4];
+  float* coef = (float*)(lds + T::LDS);
+  const int tiles_n = (int)((p.n + T::TN - 1) / T::TN), tiles_m = tile_rows_of<T>(p);
+  if ((int)blockIdx.x >= tiles_m * tiles_n) return;
+  const Place pl = place_of<T>(p, xcd_run(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n);
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const Copies<T> cp(p, pl, wave, lane);
+  for (int i = tid; i < T::COEF; i += 64 * T::NW) coef[i] = coefficient<CD, T>(p, pl, i);
+#pragma unroll
+  for (int s = 0; s < T::NS; ++s) cp.all(lds + s * T::STAGE, s);
+  wait_vmcnt<(T::NS - 1) * T::PER>();
+  wait_lgkm0();
+  barrier_only();
+  Acc<T> acc;
+  contract<T>(acc, lds, cp, lane);
+  Writer<CD, T>::run(p, pl, acc, coef, lds + wave * 32 * Writer<CD, T>::RB, wave, lane);
+}
+
+using Full = Tile<4, 2, 2, 4, 2>;  // 256 x 256, eight waves
+using Half = Tile<2, 2, 2, 4, 2>;  // 128 x 256, eight waves
+using Mid = Tile<2, 2, 2, 2, 2>;   // 128 x 128, four waves, two workgroups to a compute unit
+
+// Whole rounds of 256 x 256 tiles, a workgroup to a compute unit going through its tiles.
+// After a tile's last stage the copies of the next tile's first stage are requested, so
+// that they land while the tile's y is scaled and stored (both together took 9 to 14 of 60 us
+// per tile of 4096 columns when each tile waited for itself).  A tile of at most 128 rows,
+// and a last round of at most half the compute units (cut into halves of 128 rows then, two
+// workgroups to a tile), run as 128 x 256.
 template <int CD>
 __global__ __launch_bounds__(512, 1) void k_int8_full(I8 p) {
-  __shared__ __attribute__((aligned(1024))) char lds[Full::LDS + 2 * Full::TN * 4];
-  int e, rows;
-  int64_t m0, n0;
-  if (!tile_of<Full>(p, e, m0, rows, n0)) return;
-  if (rows > Half::TM) tile_product<CD, Full>(p, lds, e, m0, rows, n0);
-  else tile_product<CD, Half>(p, lds, e, m0, rows, n0);
-}
+  constexpr int kStaging = Full::STAGE;  // y passes through what was stage 1
+  static_assert(kStaging + 8 * 32 * Writer<CD, Full>::RB <= Full::LDS, "staging fits");
+  __shared__ __attribute__((aligned(1024))) char lds[Full::LDS + 2 * Full::COEF * 4];  // one array, as above
+  float* coefs = (float*)(lds + Full::LDS);  // two sets, used in turn
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int b = blockIdx.x, G = gridDim.x;
+  const int tiles_n = (int)((p.n + Full::TN - 1) / Full::TN), tiles_m = tile_rows_of<Full>(p);
+  const int total = tiles_m * tiles_n;
+  // The workgroup's tile in round r; rows 0: none (any more).
+  auto item = [&](int r) {
+    Place pl = {0, 0, 0, 0};
+    const int64_t base = (int64_t)r * G;
+    if (base >= total) return pl;
+    const int rem = total - (int)base;
+    if (rem < G && 2 * rem <= G) {
+      if (b >= 2 * rem) return pl;
+      const int pos = xcd_run(b, 2 * rem), half = pos & 1;
+      pl = place_of<Full>(p, (int)base + (pos >> 1), tiles_m, tiles_n);
+      pl.m0 += half * Half::TM;
+      pl.rows = half ? max(0, pl.rows - Half::TM) : min(pl.rows, Half::TM);
+    } else {
+      const int n = min(G, rem);
+      if (b < n) pl = place_of<Full>(p, (int)base + xcd_run(b, n), tiles_m, tiles_n);
+    }
+    return pl;
+  };
+  // value i (of the thread's) among a tile's coefficients: columns at 0 and 256, rows at 512
+  auto coef_of = [&](const Place& pl, int i) {
+    return pl.rows > Half::TM ? coefficient<CD, Full>(p, pl, i)
+                              : i < Half::COEF ? coefficient<CD, Half>(p, pl, i) : 0.f;
+  };
+  static_assert(Full::COEF <= 2 * 512 && Half::TN == Full::TN, "two coefficients to a thread");
+  auto first_stage = [&](const Place& pl) {
+    if (pl.rows > Half::TM) Copies<Full>(p, pl, wave, lane).all(lds, 0);
+    else Copies<Half>(p, pl, wave, lane).all(lds, 0);
+  };
 
-template <int CD>
-__global__ __launch_bounds__(256, 2) void k_int8_mid(I8 p) {
-  __shared__ __attribute__((aligned(1024))) char lds[Mid::LDS + 2 * Mid::TN * 4];
-  int e, rows;
-  int64_t m0, n0;
-  if (!tile_of<Mid>(p, e, m0, rows, n0)) return;
-  tile_product<CD, Mid>(p, lds, e, m0, rows, n0);
+  Place cur = item(0);
+  if (cur.rows == 0) return;
+  for (int i = tid; i < Full::COEF; i += 512) coefs[i] = coef_of(cur, i);
+  first_stage(cur);
+  wait_vmcnt<0>();
+  int set = 0;
+  for (int r = 1;; ++r) {
+    const Place nxt = item(r);
+    float c0 = 0.f, c1 = 0.f;  // the next tile's coefficients arrive during this one's contraction
+    if (nxt.rows) {
+      c0 = coef_of(nxt, tid);
+      if (tid + 512 < Full::COEF) c1 = coef_of(nxt, tid + 512);
+    }
+    wait_lgkm0();
+    barrier_only();  // stage 0 and the coefficients are there, the staging of the tile before is free
+    // Between here and the next tile's first stage: contract, hand over, write.
+    auto work = [&](auto shape) {
+      using T = decltype(shape);
+      const Copies<T> cp(p, cur, wave, lane);
+      cp.all(lds + T::STAGE, 1);
+      Acc<T> acc;
+      contract<T>(acc, lds, cp, lane);
+      if (nxt.rows) {
+        float* to = coefs + (set ^ 1) * Full::COEF;
+        to[tid] = c0;
+        if (tid + 512 < Full::COEF) to[tid + 512] = c1;
+        first_stage(nxt);
+      }
+      Writer<CD, T>::run(p, cur, acc, coefs + set * Full::COEF, lds + kStaging + wave * 32 * Writer<CD, T>::RB, wave, lane);
+      asm volatile("" ::: "memory");
+      // this wave's copies of the next first stage, older than the stores, have landed
+      wait_vmcnt<Writer<CD, T>::stores()>();
+    };
+    if (cur.rows > Half::TM) work(Full{});
+    else work(Half{});
+    if (nxt.rows == 0) return;
+    cur = nxt;
+    set ^= 1;
+  }
 }
 
 // ------------------------------------------------------------- a few tokens (decode)
 // At up to 16 tokens per expert the product reads each weight once and does little else:
-// a workgroup takes 16 weight rows of one expert over the whole contraction, its NWV waves
-// dealing out 128-byte lines of it.  Codes go from global memory straight into the
+// a workgroup of NWV waves takes 16 RB weight rows of one expert over the whole contraction,
+// the waves dealing out 128-byte lines of it.  Codes go from global memory straight into the
 // 16 x 16 x 64 matrix instruction (lane l: row l % 16, 16 bytes l / 16 of a 64-byte piece),
-// weight rows as one operand and tokens as the other; the waves' sums meet in LDS.
+// weight rows as one operand and tokens as the other; 16 pieces of weights per lane are
+// requested before the first product.  The waves' sums meet in LDS.
 // More than 16 tokens of an expert: the workgroup goes over its weight rows again for
 // each 16 of them (from the caches).
-template <int CD, int NWV>
-__global__ __launch_bounds__(64 * NWV) void k_int8_few(I8 p, const int32_t* __restrict__ starts) {
-  __shared__ int red[NWV][16][17];
+// FUSE (one token of one matrix): the workgroup brings the token to 8 bits itself while its
+// weights are on their way, which spares the call a launch (4096 x 4096: 7.4 against 9.6 us;
+// with two tokens the repeated work already costs more than the launch: 11.2 against 9.9).
+constexpr int kFuseBytes = 32768;  // codes of the token in LDS at most
+
+// Source of a call's token when it is not in 8 bits yet.
+struct Raw {
+  const void* x;
+  int64_t cols;
+};
+
+template <int CD, int RB, int NWV, bool FUSE>
+__global__ __launch_bounds__(64 * NWV) void k_int8_few(I8 p, const int32_t* __restrict__ starts, Raw raw) {
+  constexpr int U = 8 / RB;  // lines per batch of loads and wave
+  constexpr int NT = 64 * NWV;
+  __shared__ int red[NWV][16][16 * RB + 1];
+  __shared__ __attribute__((aligned(16))) char tok[FUSE ? kFuseBytes + 16 : 16];
+  __shared__ uint32_t tmax[NWV];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int e = blockIdx.y;
   int64_t first = 0, end = p.m;
@@ -484,49 +640,100 @@ __global__ __launch_bounds__(64 * NWV) void k_int8_few(I8 p, const int32_t* __re
     end = __builtin_amdgcn_readfirstlane(starts[e + 1]);
   }
   if (first >= end) return;
-  const int64_t n0 = (int64_t)blockIdx.x * 16;
-  const int ncols = (int)min((int64_t)16, p.n - n0);
+  const int64_t n0 = (int64_t)blockIdx.x * (16 * RB);
+  const int ncols = (int)min((int64_t)(16 * RB), p.n - n0);
   const int64_t wrow = (int64_t)e * p.n + n0;
-  const rsrc_t rb = make_rsrc(p.b + wrow * p.ld, (int64_t)ncols * p.ld);
-  const uint32_t off = (uint32_t)((lane & 15) * (int)p.ld + (lane >> 4) * 16);
-  const int lines = (int)(p.ld >> 7);
+  const int ld = (int)p.ld, lines = ld >> 7;
+  const uint32_t off = (uint32_t)((lane & 15) * ld + (lane >> 4) * 16);
+  const char* wbase = (const char*)(p.b + wrow * p.ld);
+  i32x4_t w[2 * U * RB];
+  // Each workgroup starts at a line of its own (the order of the sum is free): rows a power of
+  // two apart would otherwise be read at the same few memory channels by all workgroups at
+  // once (16 tokens, 28672 x 4096: 31.4 -> 29.6 us).
+  const int rot = (int)((blockIdx.x * 29u) % (unsigned)lines);
+  auto line_at = [&](int l) { return l + rot >= lines ? l + rot - lines : l + rot; };
+  // the wave's lines l0, l0 + NWV, .. of a batch; past the last line an empty buffer: zeros,
+  // nothing is read
+  auto load_w = [&](int l0) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int l = l0 + NWV * i;
+      const rsrc_t r = make_rsrc(wbase, l < lines ? (int64_t)ncols * ld : 0);
+#pragma unroll
+      for (int q = 0; q < 2 * RB; ++q)
+        w[i * 2 * RB + q] = ld128(r, off + (uint32_t)((q >> 1) * 16 * ld), (uint32_t)(line_at(l) * 128 + (q & 1) * 64));
+    }
+  };
+  float fscale = 0.f;
+  if constexpr (FUSE) {
+    load_w(wave);
+    if (tid < 4) *(uint32_t*)(tok + kFuseBytes + tid * 4) = 0u;  // what the other 15 columns read
+    float v[8];
+    uint32_t amax = 0;
+    for (int k = 8 * tid; k < (int)raw.cols; k += 8 * NT) {
+      load8<CD, true>(raw.x, 0, k, raw.cols, v);
+      amax = amax8(v, amax);
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) amax = max(amax, (uint32_t)__shfl_xor((int)amax, o, 64));
+    if (lane == 0) tmax[wave] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < NWV; ++x) amax = max(amax, tmax[x]);
+    fscale = scale_of_bits(amax);
+    for (int k = 8 * tid; k < ld; k += 8 * NT) {
+      u32x2_t c = {0u, 0u};
+      if (k < raw.cols) {
+        load8<CD, true>(raw.x, 0, k, raw.cols, v);
+        c = codes8(v, fscale);
+      }
+      *(u32x2_t*)(tok + k) = c;
+    }
+    __syncthreads();
+  }
   for (int64_t m0 = first; m0 < end; m0 += 16) {
     const int rows = (int)min((int64_t)16, end - m0);
-    const rsrc_t ra = make_rsrc(p.a + m0 * p.ld, (int64_t)rows * p.ld);
-    i32x4_t acc0 = {0, 0, 0, 0}, acc1 = {0, 0, 0, 0};
-    int l = wave;
-    // eight lines at a time: every load is requested before the first product
-    for (; l + 7 * NWV < lines; l += 8 * NWV) {
-      i32x4_t w[16], a[16];
+    i32x4_t acc[RB][2];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) w[i] = ld128(rb, off, (uint32_t)((l + (i >> 1) * NWV) * 128 + (i & 1) * 64));
+    for (int b = 0; b < RB; ++b) acc[b][0] = acc[b][1] = i32x4_t{0, 0, 0, 0};
+    for (int l0 = wave; l0 < lines; l0 += NWV * U) {
+      i32x4_t a[2 * U];
+      if (!FUSE || l0 != wave) load_w(l0);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) a[i] = ld128(ra, off, (uint32_t)((l + (i >> 1) * NWV) * 128 + (i & 1) * 64));
+      for (int i = 0; i < 2 * U; ++i) {
+        const int l = l0 + NWV * (i >> 1);
+          if constexpr (FUSE) {
+          a[i] = *(const i32x4_t*)(tok + ((lane & 15) == 0 && l < lines ? line_at(l) * 128 + (i & 1) * 64 + (lane >> 4) * 16
+                                                                        : kFuseBytes));
+        } else {
+          const rsrc_t r = make_rsrc(p.a + m0 * p.ld, l < lines ? (int64_t)rows * ld : 0);
+          a[i] = ld128(r, off, (uint32_t)(line_at(l) * 128 + (i & 1) * 64));
+        }
+      }
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        acc0 = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[i], a[i], acc0, 0, 0, 0);
-        acc1 = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[i + 1], a[i + 1], acc1, 0, 0, 0);
-      }
-    }
-    for (; l < lines; l += NWV) {
-      const i32x4_t w0 = ld128(rb, off, (uint32_t)(l * 128)), w1 = ld128(rb, off, (uint32_t)(l * 128 + 64));
-      const i32x4_t a0 = ld128(ra, off, (uint32_t)(l * 128)), a1 = ld128(ra, off, (uint32_t)(l * 128 + 64));
-      acc0 = __builtin_amdgcn_mfma_i32_16x16x64_i8(w0, a0, acc0, 0, 0, 0);
-      acc1 = __builtin_amdgcn_mfma_i32_16x16x64_i8(w1, a1, acc1, 0, 0, 0);
-    }
-    // lane l: token l % 16, weight rows 4 (l / 16) .. + 3
+      for (int i = 0; i < U; ++i)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) red[wave][lane & 15][4 * (lane >> 4) + i] = acc0[i] + acc1[i];
+        for (int q = 0; q < 2 * RB; ++q)
+          acc[q >> 1][q & 1] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[i * 2 * RB + q], a[2 * i + (q & 1)],
+                                                                    acc[q >> 1][q & 1], 0, 0, 0);
+    }
+    // lane l: token l % 16, weight rows 4 (l / 16) .. + 3 of each 16
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        red[wave][lane & 15][16 * b + 4 * (lane >> 4) + i] = acc[b][0][i] + acc[b][1][i];
     __syncthreads();
-    if (tid < 256) {
-      const int t = tid >> 4, c = tid & 15;
-      int sum = 0;
+    for (int q = tid; q < (FUSE ? 16 * RB : 256 * RB); q += NT) {
+      const int t = q / (16 * RB), c = q % (16 * RB);
+      if (t < rows && c < ncols) {
+        int sum = red[0][t][c];
 #pragma unroll
-      for (int w = 0; w < NWV; ++w) sum += red[w][t][c];
-      if (t < rows && c < ncols)
-        store_y<CD>(p, m0 + t, n0 + c, sum, p.sa[m0 + t], p.sb[wrow + c],
+        for (int x = 1; x < NWV; ++x) sum += red[x][t][c];
+        store_y<CD>(p, m0 + t, n0 + c, sum, FUSE ? fscale : p.sa[m0 + t], p.sb[wrow + c],
                     p.bias ? load_cd<CD>(p.bias, wrow + c) : 0.f);
+      }
     }
     __syncthreads();
   }
@@ -596,20 +803,37 @@ int rows_to_int8(int cd, const void* x, int64_t ldx, int64_t rows, int64_t cols,
   return rows_cd<CD_F32>(x, ldx, rows, cols, codes, scale, r, s);
 }
 
+// Weight rows per workgroup.  The tokens' codes are read once for each workgroup, so more rows
+// spare that traffic, as long as there are workgroups enough: at 16 tokens, 16 / 32 / 64 rows
+// take 11.1 / 12.9 / 16.6 us on 4096 x 4096 (256 blocks of 16 rows), 22.2 / 19.0 / 17.3 us on
+// 14336 x 4096 (896) and, with more than eight blocks to a compute unit, 50.9 / 47.9 / 51.4 us
+// on six experts of 14336 x 4096.
+template <int CD, bool FUSE>
+int few_rows(const I8& p, int32_t experts, const int32_t* starts, const Raw& raw, hipStream_t s) {
+  const int64_t blocks = ceil_div(p.n, 16) * std::min<int64_t>(experts, p.m), cus = cu_count();
+  const int rb = blocks < 2 * cus ? 1 : blocks < 3 * cus || blocks >= 8 * cus ? 2 : 4;
+  constexpr int NWV = 4;
+  const dim3 g((unsigned)ceil_div(p.n, 16 * rb), (unsigned)experts), b(64 * NWV);
+  if (rb == 4) k_int8_few<CD, 4, NWV, FUSE><<<g, b, 0, s>>>(p, starts, raw);
+  else if (rb == 2) k_int8_few<CD, 2, NWV, FUSE><<<g, b, 0, s>>>(p, starts, raw);
+  else k_int8_few<CD, 1, NWV, FUSE><<<g, b, 0, s>>>(p, starts, raw);
+  return check_launch("k_int8_few");
+}
+
 template <int CD>
 int product(const I8& p, int32_t experts, int cap, const int32_t* starts, hipStream_t s) {
   const Form f = form_of(p.m, experts);
-  if (f == FEW) {
-    const dim3 g((unsigned)ceil_div(p.n, 16), (unsigned)experts);
-    k_int8_few<CD, 4><<<g, dim3(256), 0, s>>>(p, starts);
-    return check_launch("k_int8_few");
-  }
+  if (f == FEW) return few_rows<CD, false>(p, experts, starts, Raw{}, s);
   const int tm = f == FULL ? Full::TM : Mid::TM, tn = f == FULL ? Full::TN : Mid::TN;
   const int64_t tiles = (starts ? cap : ceil_div(p.m, tm)) * ceil_div(p.n, tn);
   if (tiles >= (1LL << 31)) return set_error(QLORA_ERR_UNSUPPORTED, "int8: %lld tiles", (long long)tiles);
-  if (f == FULL) k_int8_full<CD><<<dim3((unsigned)tiles), dim3(512), 0, s>>>(p);
-  else k_int8_mid<CD><<<dim3((unsigned)tiles), dim3(256), 0, s>>>(p);
-  return check_launch(f == FULL ? "k_int8_full" : "k_int8_mid");
+  if (f == FULL) {
+    const int64_t cus = cu_count();  // as many as tiles, or as halves of tiles in an only round
+    k_int8_full<CD><<<dim3((unsigned)std::min<int64_t>(cus, 2 * tiles)), dim3(512), 0, s>>>(p);
+    return check_launch("k_int8_full");
+  }
+  k_int8_tile<CD, Mid, 2><<<dim3((unsigned)tiles), dim3(64 * Mid::NW), 0, s>>>(p);
+  return check_launch("k_int8_tile");
 }
 
 }  // namespace
@@ -637,6 +861,14 @@ int launch_int8_linear(const qlora_int8_t* w, const void* x, int64_t m, int64_t 
   p.m = m;
   p.n = w->rows;
   p.ld = QLORA_INT8_LD(w->cols);
+  // One token of one matrix, in whole 16-byte vectors: one launch does it all.
+  if (!offsets && m == 1 && p.ld <= kFuseBytes && ((uintptr_t)x & 15) == 0) {
+    ProfScope prof(QLORA_K_INT8_GEMM, s);
+    const Raw raw = {x, w->cols};
+    if (cd == CD_BF16) return few_rows<CD_BF16, true>(p, 1, nullptr, raw, s);
+    if (cd == CD_F16) return few_rows<CD_F16, true>(p, 1, nullptr, raw, s);
+    return few_rows<CD_F32, true>(p, 1, nullptr, raw, s);
+  }
   Route r = {};
   if (offsets) {
     const bool tiles = form_of(m, w->experts) != FEW;
