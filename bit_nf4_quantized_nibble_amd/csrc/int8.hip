@@ -504,9 +504,17 @@ __global__ __launch_bounds__(64 * T::NW, WGS) void k_int8_tile(I8 p) {
   const Place pl = place_of<T>(p, xcd_run(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const Copies<T> cp(p, pl, wave, lane);
-  for (int i = tid; i < T::COEF; i += 64 * T::NW) coef[i] = coefficient<CD, T>(p, pl, i);
+  // the coefficients are requested first and stored once the copies are on their way
+  constexpr int NC = (T::COEF + 64 * T::NW - 1) / (64 * T::NW);
+  float c[NC];
+#pragma unroll
+  for (int i = 0; i < NC; ++i)
+    c[i] = tid + i * 64 * T::NW < T::COEF ? coefficient<CD, T>(p, pl, tid + i * 64 * T::NW) : 0.f;
 #pragma unroll
   for (int s = 0; s < T::NS; ++s) cp.all(lds + s * T::STAGE, s);
+#pragma unroll
+  for (int i = 0; i < NC; ++i)
+    if (tid + i * 64 * T::NW < T::COEF) coef[tid + i * 64 * T::NW] = c[i];
   wait_vmcnt<(T::NS - 1) * T::PER>();
   wait_lgkm0();
   barrier_only();
@@ -518,6 +526,8 @@ __global__ __launch_bounds__(64 * T::NW, WGS) void k_int8_tile(I8 p) {
 using Full = Tile<4, 2, 2, 4, 2>;  // 256 x 256, eight waves
 using Half = Tile<2, 2, 2, 4, 2>;  // 128 x 256, eight waves
 using Mid = Tile<2, 2, 2, 2, 2>;   // 128 x 128, four waves, two workgroups to a compute unit
+using Low = Tile<1, 2, 2, 2, 3>;   // 64 x 128, four waves, two workgroups to a compute unit
+using Small = Tile<1, 1, 2, 2, 4>;  // 64 x 64, four waves, two workgroups to a compute unit
 
 // Whole rounds of 256 x 256 tiles, a workgroup to a compute unit going through its tiles.
 // After a tile's last stage the copies of the next tile's first stage are requested, so
@@ -748,23 +758,41 @@ struct Plan {
 };
 
 // Which product kernel takes a call: the few-token kernel up to 16 tokens per expert on
-// average, tiles of 128 x 128 up to 512, tiles of 256 x 256 beyond.
-enum Form { FEW, MID, FULL };
-Form form_of(int64_t m, int32_t experts) {
-  const int64_t live = std::max<int64_t>(1, std::min<int64_t>(experts, m));
-  return m <= 16 * live ? FEW : m <= 512 * live ? MID : FULL;
+// average, else tiles, the larger the less each operand is read again, the smaller the more
+// of the chip a small product occupies (measured for the whole call, us):
+//                          64 x 64   64 x 128   128 x 128   256 x 256
+//   256 x 4096 x 4096         17.6      18.9        27.8        46        256 tiles of 64 x 64
+//   512 x 4096 x 4096         24.7      21.2        29.8        48        256 of 64 x 128
+//   256 x 14336 x 4096        35.2      28.5        30.3        48        448 of 64 x 128
+//   512 x 14336 x 4096        61.8      49.9        41.1        39.4      112 of 256 x 256
+//   1024 x 14336 x 4096        113        89        74.3        63.5
+//   experts, 64 rows each (1024 x 2048)   52   47.5   55.9      47
+//   experts, 128 rows each (4096 x 4096)  61   60     54.6      64
+//   experts, 256 rows each (14336 x 4096) 293  236    215       180
+enum Form { FEW, SMALL, LOW, MID, FULL };
+Form form_of(int64_t m, int64_t n, int32_t experts) {
+  const int64_t live = std::max<int64_t>(1, std::min<int64_t>(experts, m)), cus = cu_count();
+  if (m <= 16 * live) return FEW;
+  // tile rows: each expert's last one is half full on average
+  auto tiles = [&](int64_t tm, int64_t tn) {
+    return (experts == 1 ? ceil_div(m, tm) : m / tm + (live + 1) / 2) * ceil_div(n, tn);
+  };
+  if (tiles(64, 64) <= cus) return SMALL;
+  if (tiles(64, 128) <= 2 * cus || m < 96 * live) return LOW;
+  return m >= 256 * live && 16 * tiles(256, 256) >= 7 * cus ? FULL : MID;
 }
-int tile_rows(int64_t m, int32_t experts) { return form_of(m, experts) == FULL ? Full::TM : Mid::TM; }
+int tile_rows(Form f) { return f == FULL ? Full::TM : f == MID ? Mid::TM : Low::TM; }
 
-Plan plan_int8(int64_t m, int64_t cols, int32_t experts, bool grouped) {
+Plan plan_int8(const qlora_int8_t* w, int64_t m, bool grouped) {
   Plan P;
-  size_t off = al((size_t)m * QLORA_INT8_LD(cols));
+  size_t off = al((size_t)m * QLORA_INT8_LD(w->cols));
   P.off_scale = off;
   off += al((size_t)m * 4);
   if (grouped) {
-    P.cap = (int)(m / tile_rows(m, experts) + std::min<int64_t>(experts, m));
+    // the smallest tiles have the most rows of them: the size does not depend on the device
+    P.cap = (int)(m / Low::TM + std::min<int64_t>(w->experts, m));
     P.off_starts = off;
-    off += al(((size_t)experts + 1) * 4);
+    off += al(((size_t)w->experts + 1) * 4);
     P.off_count = off;
     off += al(4);
     P.off_tiles = off;
@@ -822,18 +850,19 @@ int few_rows(const I8& p, int32_t experts, const int32_t* starts, const Raw& raw
 
 template <int CD>
 int product(const I8& p, int32_t experts, int cap, const int32_t* starts, hipStream_t s) {
-  const Form f = form_of(p.m, experts);
+  const Form f = form_of(p.m, p.n, experts);
   if (f == FEW) return few_rows<CD, false>(p, experts, starts, Raw{}, s);
-  const int tm = f == FULL ? Full::TM : Mid::TM, tn = f == FULL ? Full::TN : Mid::TN;
+  const int tm = tile_rows(f), tn = f == FULL ? Full::TN : f == MID ? Mid::TN : f == LOW ? Low::TN : Small::TN;
   const int64_t tiles = (starts ? cap : ceil_div(p.m, tm)) * ceil_div(p.n, tn);
   if (tiles >= (1LL << 31)) return set_error(QLORA_ERR_UNSUPPORTED, "int8: %lld tiles", (long long)tiles);
-  if (f == FULL) {
-    const int64_t cus = cu_count();  // as many as tiles, or as halves of tiles in an only round
-    k_int8_full<CD><<<dim3((unsigned)std::min<int64_t>(cus, 2 * tiles)), dim3(512), 0, s>>>(p);
-    return check_launch("k_int8_full");
-  }
-  k_int8_tile<CD, Mid, 2><<<dim3((unsigned)tiles), dim3(64 * Mid::NW), 0, s>>>(p);
-  return check_launch("k_int8_tile");
+  const dim3 g((unsigned)tiles);
+  // the large tiles: a workgroup to a compute unit, or to a half tile in an only round
+  if (f == FULL)
+    k_int8_full<CD><<<dim3((unsigned)std::min<int64_t>(cu_count(), 2 * tiles)), dim3(512), 0, s>>>(p);
+  else if (f == MID) k_int8_tile<CD, Mid, 2><<<g, dim3(64 * Mid::NW), 0, s>>>(p);
+  else if (f == LOW) k_int8_tile<CD, Low, 2><<<g, dim3(64 * Low::NW), 0, s>>>(p);
+  else k_int8_tile<CD, Small, 2><<<g, dim3(64 * Small::NW), 0, s>>>(p);
+  return check_launch(f == FULL ? "k_int8_full" : "k_int8_tile");
 }
 
 }  // namespace
@@ -844,12 +873,12 @@ int launch_int8_quantize(const void* w, int64_t ldw, int dtype, const qlora_int8
 }
 
 size_t int8_workspace_bytes(const qlora_int8_t* w, int64_t m, bool grouped) {
-  return plan_int8(m, w->cols, w->experts, grouped).total;
+  return plan_int8(w, m, grouped).total;
 }
 
 int launch_int8_linear(const qlora_int8_t* w, const void* x, int64_t m, int64_t ldx, const int32_t* offsets,
                        const void* bias, int cd, void* y, void* ws, hipStream_t s) {
-  const Plan P = plan_int8(m, w->cols, w->experts, offsets != nullptr);
+  const Plan P = plan_int8(w, m, offsets != nullptr);
   char* base = (char*)ws;
   I8 p = {};
   p.a = (const int8_t*)(base + P.off_codes);
@@ -871,14 +900,16 @@ int launch_int8_linear(const qlora_int8_t* w, const void* x, int64_t m, int64_t 
   }
   Route r = {};
   if (offsets) {
-    const bool tiles = form_of(m, w->experts) != FEW;
+    const Form f = form_of(m, w->rows, w->experts);
+    const bool tiles = f != FEW;
     r.starts = (int32_t*)(base + P.off_starts);
     r.count = (int32_t*)(base + P.off_count);
     r.tiles = (int4*)(base + P.off_tiles);
     r.offsets = offsets;
     r.experts = w->experts;
-    r.tile_m = tile_rows(m, w->experts);
-    r.cap = tiles ? P.cap : 0;
+    r.tile_m = tile_rows(f);
+    // whole runs of tile_m rows and one partial run for each expert that has a row
+    r.cap = tiles ? (int)(m / r.tile_m + std::min<int64_t>(w->experts, m)) : 0;
     r.m = m;
     p.count = tiles ? r.count : nullptr;
     p.tiles = r.tiles;
@@ -890,9 +921,9 @@ int launch_int8_linear(const qlora_int8_t* w, const void* x, int64_t m, int64_t 
   }
   ProfScope prof(QLORA_K_INT8_GEMM, s);
   const int32_t* starts = offsets ? (const int32_t*)(base + P.off_starts) : nullptr;
-  if (cd == CD_BF16) return product<CD_BF16>(p, w->experts, P.cap, starts, s);
-  if (cd == CD_F16) return product<CD_F16>(p, w->experts, P.cap, starts, s);
-  return product<CD_F32>(p, w->experts, P.cap, starts, s);
+  if (cd == CD_BF16) return product<CD_BF16>(p, w->experts, r.cap, starts, s);
+  if (cd == CD_F16) return product<CD_F16>(p, w->experts, r.cap, starts, s);
+  return product<CD_F32>(p, w->experts, r.cap, starts, s);
 }
 
 }  // namespace qnf4
