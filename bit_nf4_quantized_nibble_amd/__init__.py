@@ -494,29 +494,54 @@ def mse_loss_grad(y, target, dy=None):
     return loss, dy
 
 
-def _on_device(device):
-    """Context in which the library's launches go to ``device`` (a no-op on the current one)."""
+def _launch(device, call, *args):
+    """call(*args, stream) with ``device`` current (its current stream); raises on an error."""
     torch = _torch()
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    if device.index == torch.cuda.current_device():
+        _lib.check(call(*args, torch._C._cuda_getCurrentRawStream(device.index)))
+    else:
+        with torch.cuda.device(device):
+            _lib.check(call(*args, torch._C._cuda_getCurrentRawStream(device.index)))
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+def _check_tensor(name, t, device, dtype, numel):
+    if not t.is_cuda:
+        raise ValueError("%s must be a GPU tensor" % name)
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if t.device != device:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, device))
+    if t.numel() != numel:
+        raise ValueError("%s must hold %d elements, got %d" % (name, numel, t.numel()))
+
+
+def _workspace_on(device, nbytes, workspace):
+    torch = _torch()
+    if workspace is None:
+        return torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    if not workspace.is_cuda or workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on %s" % (device,))
+    return _workspace(nbytes, device, workspace)
 
 
 def _strided_rows(x, cols):
     """x as rows of ``cols`` contiguous elements and the stride between them (a view where
-    the layout allows, else a copy), with the leading dims."""
-    x2, lead = _flatten(x, cols)
-    if x2.shape[0] <= 1:
-        return (x2 if cols <= 1 or x2.stride(1) == 1 else x2.contiguous()), cols, lead
-    if (cols > 1 and x2.stride(1) != 1) or x2.stride(0) < cols:
-        x2 = x2.contiguous()
-    return x2, max(x2.stride(0), cols), lead
+    the layout allows, else a copy), with the leading dims (None: x is 2-D already)."""
+    if x.shape[-1] != cols:
+        raise ValueError("last dim must be %d, got %d" % (cols, x.shape[-1]))
+    lead = None
+    if x.dim() != 2:
+        lead = tuple(x.shape[:-1])
+        x = x.reshape(-1, cols)
+    if x.is_contiguous():
+        return x, cols, lead
+    if x.shape[0] <= 1:
+        return (x if x.stride(1) == 1 else x.contiguous()), cols, lead
+    if (cols > 1 and x.stride(1) != 1) or x.stride(0) < cols:
+        return x.contiguous(), cols, lead
+    return x, x.stride(0), lead
 
 
 @dataclass
@@ -540,7 +565,11 @@ class Int8Weight:
         return self.codes.numel() + 4 * self.scale.numel()
 
     def descriptor(self) -> QloraInt8:
-        return QloraInt8(self.rows, self.cols, self.experts, 0, _ptr(self.codes), _ptr(self.scale))
+        made = self.__dict__.get("_made")
+        if made is None or made[0] is not self.codes or made[1] is not self.scale:
+            d = QloraInt8(self.rows, self.cols, self.experts, 0, _ptr(self.codes), _ptr(self.scale))
+            made = self.__dict__["_made"] = (self.codes, self.scale, d)
+        return made[2]
 
 
 def quantize_int8(w) -> Int8Weight:
@@ -563,9 +592,7 @@ def quantize_int8(w) -> Int8Weight:
         return q
     w2, ldw, _ = _strided_rows(w, cols)
     d = q.descriptor()
-    with _on_device(w.device):
-        _lib.check(_lib.lib().qlora_int8_quantize(_ptr(w2), ldw, dtype_code(w.dtype), ctypes.byref(d),
-                                                  _stream_ptr(w.device)))
+    _launch(w.device, _lib.lib().qlora_int8_quantize, _ptr(w2), ldw, dtype_code(w.dtype), ctypes.byref(d))
     return q
 
 
@@ -577,33 +604,35 @@ def int8_workspace_bytes(w: Int8Weight, m: int, grouped: bool = False) -> int:
 
 def _int8_call(w, x, offsets, bias, out, workspace):
     torch = _torch()
-    dt = x.dtype
+    dt, device = x.dtype, x.device
     code = dtype_code(dt)
     if not x.is_cuda:
         raise ValueError("x must be a GPU tensor")
+    if w.codes.device != device:
+        raise ValueError("w is on %s, x on %s" % (w.codes.device, device))
     x2, ldx, lead = _strided_rows(x, w.cols)
     m = x2.shape[0]
-    y = out if out is not None else torch.empty(m, w.rows, dtype=dt, device=x.device)
-    _need_cuda("out", y, dt)
-    if y.numel() != m * w.rows:
-        raise ValueError("out must hold %d x %d elements" % (m, w.rows))
-    _need_cuda("bias", bias, dt)
-    if bias is not None and bias.numel() != w.rows * (1 if offsets is None else w.experts):
-        raise ValueError("bias must hold one element per output channel (of each expert)")
-    _same_device(x.device, w=w.codes, offsets=offsets, bias=bias, out=out, workspace=workspace)
+    if out is None:
+        y = torch.empty(m, w.rows, dtype=dt, device=device)
+    else:
+        _check_tensor("out", out, device, dt, m * w.rows)
+        y = out
     grouped = offsets is not None
-    d = w.descriptor()
+    if bias is not None:
+        _check_tensor("bias", bias, device, dt, w.rows * (w.experts if grouped else 1))
+    d = ctypes.byref(w.descriptor())
     lib = _lib.lib()
-    ws = _workspace(int(lib.qlora_int8_workspace_bytes(ctypes.byref(d), m, int(grouped))), x.device, workspace)
+    ws = _workspace_on(device, lib.qlora_int8_workspace_bytes(d, m, grouped), workspace)
     ws_bytes = ws.numel() * ws.element_size()
-    with _on_device(x.device):
-        if grouped:
-            _lib.check(lib.qlora_int8_linear_experts(ctypes.byref(d), _ptr(x2), m, ldx, _ptr(offsets), _ptr(bias),
-                                                     code, _ptr(y), _ptr(ws), ws_bytes, _stream_ptr(x.device)))
-        else:
-            _lib.check(lib.qlora_int8_linear(ctypes.byref(d), _ptr(x2), m, ldx, _ptr(bias), code, _ptr(y), _ptr(ws),
-                                             ws_bytes, _stream_ptr(x.device)))
-    return y.reshape(*lead, w.rows)
+    if grouped:
+        _launch(device, lib.qlora_int8_linear_experts, d, x2.data_ptr(), m, ldx, offsets.data_ptr(), _ptr(bias), code,
+                y.data_ptr(), ws.data_ptr(), ws_bytes)
+    else:
+        _launch(device, lib.qlora_int8_linear, d, x2.data_ptr(), m, ldx, _ptr(bias), code, y.data_ptr(),
+                ws.data_ptr(), ws_bytes)
+    if lead is None and y.dim() == 2:
+        return y if y.shape[1] == w.rows else y.view(m, w.rows)
+    return y.view(*((m,) if lead is None else lead), w.rows)
 
 
 def linear_int8(w: Int8Weight, x, bias=None, out=None, workspace=None):
@@ -621,15 +650,12 @@ def linear_int8_experts(w: Int8Weight, x, offsets, bias=None, out=None, workspac
     expert e's weight (and bias[e]).  ``offsets``: int32 GPU tensor [experts + 1], read on the
     device.  Rows that no expert has are left as they were in ``out`` (and are unspecified
     without ``out``)."""
-    torch = _torch()
-    _need_cuda("offsets", offsets, torch.int32)
-    if offsets is None or offsets.numel() != w.experts + 1:
-        raise ValueError("offsets must hold experts + 1 = %d values" % (w.experts + 1))
+    _check_tensor("offsets", offsets, x.device, _torch().int32, w.experts + 1)
     return _int8_call(w, x, offsets, bias, out, workspace)
 
 
 def distill_loss_grad(logits, top_values, top_index, temperature: float = 1.0, weight=None, need_grad: bool = True,
-                      dlogits=None, row_kl=None):
+                      dlogits=None, row_kl=None, workspace=None):
     """loss = sum_i w_i T^2 KL(softmax(top_values_i / T) || softmax(logits_i / T)) (a 1-element
     fp32 GPU tensor) and its gradient with respect to the logits in their dtype (None without
     ``need_grad``).  logits [..., vocab] (rows may be strided); the teacher's logits top_values
@@ -638,46 +664,46 @@ def distill_loss_grad(logits, top_values, top_index, temperature: float = 1.0, w
     0 leaves a row out); ``dlogits`` may be preallocated, ``logits`` itself included;
     ``row_kl`` (fp32, one per row) receives the rows' T^2 KL."""
     torch = _torch()
-    dt = logits.dtype
+    dt, device = logits.dtype, logits.device
     code = dtype_code(dt)
     vocab = logits.shape[-1]
     if not logits.is_cuda:
         raise ValueError("logits must be a GPU tensor")
-    z, ldz, lead = _strided_rows(logits, vocab)
+    z, ldz, _ = _strided_rows(logits, vocab)
     n = z.shape[0]
     k = top_values.shape[-1]
+    if k < 1:
+        raise ValueError("top_values needs at least one slot per row")
     if top_index.dtype not in (torch.int32, torch.int64):
         raise TypeError("top_index must be int32 or int64, got %s" % (top_index.dtype,))
     u, ix = top_values.reshape(-1, k).contiguous(), top_index.reshape(-1, top_index.shape[-1]).contiguous()
-    if tuple(u.shape) != (n, k) or tuple(ix.shape) != (n, k):
+    if u.shape != (n, k) or ix.shape != (n, k):
         raise ValueError("top_values and top_index must be [%d rows, k]" % n)
-    _need_cuda("top_values", u)
-    _need_cuda("top_index", ix)
-    for name, t in (("weight", weight), ("row_kl", row_kl)):
-        _need_cuda(name, t, torch.float32)
-        if t is not None and t.numel() != n:
-            raise ValueError("%s must hold one value per row (%d)" % (name, n))
-    ldd = vocab
+    td = dtype_code(u.dtype)
+    _check_tensor("top_values", u, device, u.dtype, n * k)
+    _check_tensor("top_index", ix, device, ix.dtype, n * k)
+    if weight is not None:
+        _check_tensor("weight", weight, device, torch.float32, n)
+    if row_kl is not None:
+        _check_tensor("row_kl", row_kl, device, torch.float32, n)
+    g, ldd = None, vocab
     if dlogits is not None:
         if not need_grad:
             raise ValueError("dlogits given without need_grad")
-        if not dlogits.is_cuda or dlogits.dtype != dt or dlogits.shape != logits.shape:
+        if not dlogits.is_cuda or dlogits.dtype != dt or dlogits.shape != logits.shape or dlogits.device != device:
             raise ValueError("dlogits must be a GPU tensor like logits")
         d2, ldd, _ = _strided_rows(dlogits, vocab)
         if n and d2.data_ptr() != dlogits.data_ptr():
             raise ValueError("dlogits must have rows of contiguous elements, evenly spaced")
         g = dlogits
-    else:
-        g = torch.empty(*lead, vocab, dtype=dt, device=logits.device) if need_grad else None
-    _same_device(logits.device, top_values=u, top_index=ix, weight=weight, dlogits=dlogits, row_kl=row_kl)
-    loss = torch.empty(1, dtype=torch.float32, device=logits.device)
+    elif need_grad:
+        g = torch.empty(logits.shape, dtype=dt, device=device)
+    loss = torch.empty(1, dtype=torch.float32, device=device)
     lib = _lib.lib()
-    ws = _workspace(int(lib.qlora_distill_workspace_bytes(n)), logits.device)
-    with _on_device(logits.device):
-        _lib.check(lib.qlora_distill_loss_grad(
-            _ptr(z), n, vocab, ldz, code, _ptr(u), dtype_code(u.dtype), _ptr(ix), 8 * ix.element_size(), k,
-            float(temperature), _ptr(weight), _ptr(loss), _ptr(row_kl), _ptr(g), ldd, _ptr(ws), ws.numel(),
-            _stream_ptr(logits.device)))
+    ws = _workspace_on(device, lib.qlora_distill_workspace_bytes(n), workspace)
+    _launch(device, lib.qlora_distill_loss_grad, z.data_ptr(), n, vocab, ldz, code, u.data_ptr(), td, ix.data_ptr(),
+            64 if ix.dtype == torch.int64 else 32, k, float(temperature), _ptr(weight), loss.data_ptr(),
+            _ptr(row_kl), _ptr(g), ldd, ws.data_ptr(), ws.numel() * ws.element_size())
     return loss, g
 
 

@@ -801,6 +801,15 @@ int qlora_distill_loss_grad(const void* logits, int64_t n, int64_t vocab, int64_
       !aligned_to(top_values, cd_bytes(td)) || !aligned_to(top_index, index_bits / 8) || !aligned_to(weight, 4) ||
       !aligned_to(row_kl, 4))
     return set_error(QLORA_ERR_INVALID_ARG, "%s: arrays must be element-aligned", who);
+  if (dlogits && n > 0) {
+    // in place means row by row: any other overlap would have one row's gradient overwrite
+    // another's logits before they are read
+    const int64_t es = cd_bytes(cd), delta = (const char*)dlogits - (const char*)logits;
+    const bool apart = delta >= ((n - 1) * ld + vocab) * es || -delta >= ((n - 1) * ldd + vocab) * es;
+    const int64_t shift = ((delta / es) % ld + ld) % ld;  // within a row of ld elements
+    if (!apart && !(ld == ldd && delta % es == 0 && (delta == 0 || (shift >= vocab && shift <= ld - vocab))))
+      return set_error(QLORA_ERR_INVALID_ARG, "%s: dlogits overlaps logits other than row by row", who);
+  }
   int rc = check_ws(ws, ws_bytes, qlora_distill_workspace_bytes(n), who);
   if (rc) return rc;
   return launch_distill(logits, n, vocab, ld, cd, top_values, td, top_index, index_bits == 64, k, temperature, weight,

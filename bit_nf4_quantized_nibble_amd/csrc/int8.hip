@@ -757,27 +757,39 @@ struct Plan {
   int cap = 0;
 };
 
-// Which product kernel takes a call: the few-token kernel up to 16 tokens per expert on
-// average, else tiles, the larger the less each operand is read again, the smaller the more
-// of the chip a small product occupies (measured for the whole call, us):
-//                          64 x 64   64 x 128   128 x 128   256 x 256
-//   256 x 4096 x 4096         17.6      18.9        27.8        46        256 tiles of 64 x 64
-//   512 x 4096 x 4096         24.7      21.2        29.8        48        256 of 64 x 128
-//   256 x 14336 x 4096        35.2      28.5        30.3        48        448 of 64 x 128
-//   512 x 14336 x 4096        61.8      49.9        41.1        39.4      112 of 256 x 256
-//   1024 x 14336 x 4096        113        89        74.3        63.5
-//   experts, 64 rows each (1024 x 2048)   52   47.5   55.9      47
-//   experts, 128 rows each (4096 x 4096)  61   60     54.6      64
-//   experts, 256 rows each (14336 x 4096) 293  236    215       180
+// Which product kernel takes a call: the few-token kernel or tiles, the larger the less each
+// operand is read again, the smaller the more of the chip a small product occupies
+// (measured for the whole call, us):
+//                            few    64 x 64   64 x 128   128 x 128   256 x 256
+//   8 x 4096 x 4096          11.1     15.7      21.0                           64 tiles of 64 x 64
+//   16 x 14336 x 4096        19.7     20.2      24.3        26.1               224
+//   24 x 14336 x 4096        29.6     20.7      24.4
+//   256 x 4096 x 4096                 17.6      18.9        27.8        46     256
+//   512 x 4096 x 4096                 24.7      21.2        29.8        48     256 tiles of 64 x 128
+//   256 x 14336 x 4096                35.2      28.5        30.3        48     448
+//   512 x 14336 x 4096                61.8      49.9        41.1        39.4   112 tiles of 256 x 256
+//   1024 x 14336 x 4096                113        89        74.3        63.5
+// and of experts, with rows on average:
+//   1 of 2 (4096 x 4096)     14.4     18.3      21.8                          128 tiles of 64 x 64
+//   2 of 8 (4096 x 4096)     27.9     33.9      33.2                          512
+//   4 of 8 (4096 x 4096)     28.3     34.3      33.7                          512
+//   4 of 32 (2048 x 2048)    29.0     30.5      29.3                         1024
+//   8 of 32 (2048 x 2048)    37.9     31.9      30.8                         1024
+//   64 of 64 (1024 x 2048)             52        47.5        55.9        47
+//   128 of 8 (4096 x 4096)             61        60          54.6        64
+//   256 of 8 (14336 x 4096)           293       236         215         180
+// An uneven routing gives some experts several times the average, and the few-token
+// kernel goes over its weights again for each 16 rows, so experts leave it early.
 enum Form { FEW, SMALL, LOW, MID, FULL };
 Form form_of(int64_t m, int64_t n, int32_t experts) {
   const int64_t live = std::max<int64_t>(1, std::min<int64_t>(experts, m)), cus = cu_count();
-  if (m <= 16 * live) return FEW;
   // tile rows: each expert's last one is half full on average
   auto tiles = [&](int64_t tm, int64_t tn) {
-    return (experts == 1 ? ceil_div(m, tm) : m / tm + (live + 1) / 2) * ceil_div(n, tn);
+    return (experts == 1 ? ceil_div(m, tm) : std::max(live, m / tm + (live + 1) / 2)) * ceil_div(n, tn);
   };
-  if (tiles(64, 64) <= cus) return SMALL;
+  const int64_t t64 = tiles(64, 64);
+  if (m <= (experts == 1 ? 16 : 4 * live)) return FEW;
+  if (t64 <= cus || (t64 <= 2 * cus && m <= 16 * live)) return SMALL;
   if (tiles(64, 128) <= 2 * cus || m < 96 * live) return LOW;
   return m >= 256 * live && 16 * tiles(256, 256) >= 7 * cus ? FULL : MID;
 }
@@ -840,11 +852,13 @@ template <int CD, bool FUSE>
 int few_rows(const I8& p, int32_t experts, const int32_t* starts, const Raw& raw, hipStream_t s) {
   const int64_t blocks = ceil_div(p.n, 16) * std::min<int64_t>(experts, p.m), cus = cu_count();
   const int rb = blocks < 2 * cus ? 1 : blocks < 3 * cus || blocks >= 8 * cus ? 2 : 4;
-  constexpr int NWV = 4;
-  const dim3 g((unsigned)ceil_div(p.n, 16 * rb), (unsigned)experts), b(64 * NWV);
-  if (rb == 4) k_int8_few<CD, 4, NWV, FUSE><<<g, b, 0, s>>>(p, starts, raw);
-  else if (rb == 2) k_int8_few<CD, 2, NWV, FUSE><<<g, b, 0, s>>>(p, starts, raw);
-  else k_int8_few<CD, 1, NWV, FUSE><<<g, b, 0, s>>>(p, starts, raw);
+  const unsigned gx = (unsigned)ceil_div(p.n, 16 * rb), gy = (unsigned)experts;
+  // Four waves; eight for one token over a long contraction on few workgroups (4096 x 14336:
+  // 19.5 -> 16.3 us; with more tokens or shorter rows the same or worse).
+  if (FUSE && rb == 1 && p.ld >= 8192) k_int8_few<CD, 1, FUSE ? 8 : 4, FUSE><<<dim3(gx, gy), dim3(512), 0, s>>>(p, starts, raw);
+  else if (rb == 1) k_int8_few<CD, 1, 4, FUSE><<<dim3(gx, gy), dim3(256), 0, s>>>(p, starts, raw);
+  else if (rb == 2) k_int8_few<CD, 2, 4, FUSE><<<dim3(gx, gy), dim3(256), 0, s>>>(p, starts, raw);
+  else k_int8_few<CD, 4, 4, FUSE><<<dim3(gx, gy), dim3(256), 0, s>>>(p, starts, raw);
   return check_launch("k_int8_few");
 }
 

@@ -505,7 +505,7 @@ size_t qlora_int8_workspace_bytes(const qlora_int8_t* w, int64_t m, int32_t grou
  * have q = 0; where p > 0 meets q = 0 the loss is +inf.  Otherwise a NaN or +inf among a
  * row's logits or teacher values gives NaN.
  * loss: one device float.  row_kl (nullable): fp32 [n], the kl_i.  dlogits (nullable: loss
- * only) may be z itself with ldd = ld.  Statistics and sums are fp32 (the sum over the rows
+ * only) may be z itself with ldd = ld; any other overlap with z is refused.  Statistics and sums are fp32 (the sum over the rows
  * fp64) in a fixed order.  n == 0 writes loss = 0.
  * ws: qlora_distill_workspace_bytes(n) bytes, 256-byte aligned.
  * Errors: QLORA_ERR_INVALID_ARG (null pointers, T not positive and finite, index_bits not 32

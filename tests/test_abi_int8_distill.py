@@ -92,18 +92,20 @@ def test_int8_workspace_queries(lib):
 
 
 def distill(lib, z=FAKE, n=4, vocab=100, ld=100, cd=1, u=FAKE, td=0, idx=FAKE, bits=32, k=8, t=1.0, w=None, loss=FAKE,
-            kl=None, dz=FAKE, ldd=100, ws=FAKE, ws_bytes=1 << 20):
+            kl=None, dz=FAKE + 4096, ldd=100, ws=FAKE, ws_bytes=1 << 20):
     return lib.qlora_distill_loss_grad(z, n, vocab, ld, cd, u, td, idx, bits, k, t, w, loss, kl, dz, ldd, ws, ws_bytes,
                                        None)
 
 
 @pytest.mark.parametrize("kw,status", [
     (dict(z=None), INVALID), (dict(u=None), INVALID), (dict(idx=None), INVALID), (dict(loss=None), INVALID),
-    (dict(z=FAKE + 1), INVALID), (dict(dz=FAKE + 1), INVALID), (dict(u=FAKE + 2), INVALID),
+    (dict(z=FAKE + 1), INVALID), (dict(dz=FAKE + 4097), INVALID), (dict(u=FAKE + 2), INVALID),
     (dict(idx=FAKE + 4, bits=64), INVALID), (dict(w=FAKE + 2), INVALID), (dict(kl=FAKE + 1), INVALID),
     (dict(loss=FAKE + 2), INVALID), (dict(bits=16), INVALID), (dict(t=0.0), INVALID), (dict(t=-1.0), INVALID),
     (dict(t=float("nan")), INVALID), (dict(t=float("inf")), INVALID), (dict(n=-1), SHAPE), (dict(vocab=0), SHAPE),
     (dict(k=0), SHAPE), (dict(ld=99), SHAPE), (dict(ldd=99), SHAPE), (dict(cd=3), DTYPE), (dict(td=-1), DTYPE),
+    (dict(dz=FAKE + 200), INVALID), (dict(z=FAKE + 4296), INVALID), (dict(dz=FAKE, z=FAKE, ldd=108), INVALID),
+    (dict(z=FAKE, dz=FAKE + 198, ld=200, ldd=200), INVALID), (dict(z=FAKE, dz=FAKE + 202, ld=200, ldd=200), INVALID),
     (dict(k=1025), UNSUP), (dict(n=1 << 31), UNSUP), (dict(vocab=1 << 31, ld=1 << 31, ldd=1 << 31), UNSUP),
     (dict(ws_bytes=8), WS), (dict(ws=FAKE + 64), WS), (dict(ws=None), WS),
 ])
