@@ -700,7 +700,7 @@ def distill_loss_grad(logits, top_values, top_index, temperature: float = 1.0, w
         g = torch.empty(logits.shape, dtype=dt, device=device)
     loss = torch.empty(1, dtype=torch.float32, device=device)
     lib = _lib.lib()
-    ws = _workspace_on(device, lib.qlora_distill_workspace_bytes(n), workspace)
+    ws = _workspace_on(device, lib.qlora_distill_workspace_bytes(n, vocab, k, code), workspace)
     _launch(device, lib.qlora_distill_loss_grad, z.data_ptr(), n, vocab, ldz, code, u.data_ptr(), td, ix.data_ptr(),
             64 if ix.dtype == torch.int64 else 32, k, float(temperature), _ptr(weight), loss.data_ptr(),
             _ptr(row_kl), _ptr(g), ldd, ws.data_ptr(), ws.numel() * ws.element_size())

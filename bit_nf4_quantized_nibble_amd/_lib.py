@@ -133,7 +133,7 @@ def _declare(lib):
     lib.qlora_int8_workspace_bytes.restype = sz
     lib.qlora_distill_loss_grad.argtypes = [vp, i64, i64, i64, i32, vp, i32, vp, i32, i32, f32, vp, vp, vp, vp, i64,
                                             vp, sz, vp]
-    lib.qlora_distill_workspace_bytes.argtypes = [i64]
+    lib.qlora_distill_workspace_bytes.argtypes = [i64, i64, i32, i32]
     lib.qlora_distill_workspace_bytes.restype = sz
     for name in ("qlora_int8_quantize", "qlora_int8_linear", "qlora_int8_linear_experts", "qlora_distill_loss_grad",
                  "qlora_nf4_quantize", "qlora_nf4_dequantize", "qlora_linear_fwd",

@@ -774,7 +774,11 @@ size_t qlora_int8_workspace_bytes(const qlora_int8_t* w, int64_t m, int32_t grou
   return int8_workspace_bytes(w, m, grouped != 0);
 }
 
-size_t qlora_distill_workspace_bytes(int64_t n) { return n < 0 ? 0 : (size_t)round_up(std::max<int64_t>(n, 1) * 4, 256); }
+size_t qlora_distill_workspace_bytes(int64_t n, int64_t vocab, int32_t k, int32_t cd) {
+  if (n < 0 || n >= (1LL << 31) || vocab < 1 || vocab >= (1LL << 31) || k < 1 || k > QLORA_DISTILL_MAX_K || !valid_cd(cd))
+    return 0;
+  return distill_workspace_bytes(n, vocab, k, cd);
+}
 
 int qlora_distill_loss_grad(const void* logits, int64_t n, int64_t vocab, int64_t ld, int32_t cd,
                             const void* top_values, int32_t td, const void* top_index, int32_t index_bits, int32_t k,
@@ -810,10 +814,10 @@ int qlora_distill_loss_grad(const void* logits, int64_t n, int64_t vocab, int64_
     if (!apart && !(ld == ldd && delta % es == 0 && (delta == 0 || (shift >= vocab && shift <= ld - vocab))))
       return set_error(QLORA_ERR_INVALID_ARG, "%s: dlogits overlaps logits other than row by row", who);
   }
-  int rc = check_ws(ws, ws_bytes, qlora_distill_workspace_bytes(n), who);
+  int rc = check_ws(ws, ws_bytes, distill_workspace_bytes(n, vocab, k, cd), who);
   if (rc) return rc;
   return launch_distill(logits, n, vocab, ld, cd, top_values, td, top_index, index_bits == 64, k, temperature, weight,
-                        loss, row_kl ? row_kl : (float*)ws, dlogits, ldd, (hipStream_t)stream);
+                        loss, row_kl, dlogits, ldd, ws, (hipStream_t)stream);
 }
 
 namespace {

@@ -24,6 +24,7 @@ namespace qnf4 {
 namespace {
 
 constexpr int kMaxK = QLORA_DISTILL_MAX_K;
+constexpr int kFewSlots = 128;  // slots the small form of the LDS arrays holds
 
 struct Distill {
   const void* z;       // [n][ldz] cd
@@ -100,14 +101,14 @@ __device__ __forceinline__ float wave_sum(float v) {
 // to one address keep their order).  Two sets, used in turn by the rows that are not left
 // out: a wave that is ahead fills the next such row's set while others still read this
 // row's, and that row's first barrier holds it until they are done.
-template <int TPB>
+template <int TPB, int KC>
 struct Slots {
   int32_t head[TPB];    // first slot of the thread's list, -1: none
-  int32_t next[kMaxK];
-  int32_t idx[kMaxK];   // -1: absent
-  float e[kMaxK];       // exp((u - max) / T)
-  float share[kMaxK];   // p summed over the slots of the same index, at the first of them; else -1
-  float z[kMaxK];       // the student's logit at the index
+  int32_t next[KC];
+  int32_t idx[KC];   // -1: absent
+  float e[KC];       // exp((u - max) / T)
+  float share[KC];   // p summed over the slots of the same index, at the first of them; else -1
+  float z[KC];       // the student's logit at the index
   float zmax[TPB / 64], umax[TPB / 64], zsum[TPB / 64], usum[TPB / 64], kl[TPB / 64];  // one per wave
   int any[TPB / 64];
 };
@@ -119,11 +120,11 @@ __device__ __forceinline__ void opaque(u32x4_t& x) { asm volatile("" : "+v"(x));
 // NV > 0: rows of at most NV * TPB whole chunks, kept in registers.  NV = 0: rows of any
 // length, read twice.  Entries past the last whole chunk (fewer than a chunk) go one to a
 // thread.
-template <int CD, int TPB, int NV>
+template <int CD, int TPB, int NV, int KC>
 __global__ __launch_bounds__(TPB, TPB == 256 ? 3 : 4) void k_distill(Distill p) {
   using E = Elem<CD>;
-  constexpr int PC = E::PC, NW = TPB / 64, SPT = (kMaxK + TPB - 1) / TPB, NR = NV > 0 ? NV : 1;
-  __shared__ Slots<TPB> sets[2];
+  constexpr int PC = E::PC, NW = TPB / 64, SPT = (KC + TPB - 1) / TPB, NR = NV > 0 ? NV : 1;
+  __shared__ Slots<TPB, KC> sets[2];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int V = (int)p.V;
   const int full = V / PC, left = V - full * PC;  // whole chunks, entries past them
@@ -159,7 +160,7 @@ __global__ __launch_bounds__(TPB, TPB == 256 ? 3 : 4) void k_distill(Distill p) 
     const char* nz = zrow_of(ni);  // read only where nw is not 0
     const rsrc_t rn = chunks_of(nz, nw != 0.f);
     bool live = w != 0.f;
-    Slots<TPB>& S = sets[turn];
+    Slots<TPB, KC>& S = sets[turn];
     if (live) turn ^= 1;
     float m = 0.f, sum = 0.f, umax = 0.f, usum = 0.f;
     if (live) {
@@ -396,11 +397,270 @@ __global__ __launch_bounds__(kSumThreads) void k_distill_sum(const float* __rest
   }
 }
 
+// ------------------------------------------------------------------- a few rows
+// With few rows a workgroup to a row leaves most of the chip idle, so a row is cut into parts
+// of kPartChunks chunks, a workgroup each, in two launches: k_distill_part leaves each part's
+// maximum and sum (and the student's logits at the teacher's entries, before an in-place
+// gradient overwrites them), k_distill_join reads the parts' statistics and writes its part
+// of the gradient.  The first part's workgroup also forms the row's kl, and the last of
+// those workgroups to finish adds the rows up (in row order: the loss does not depend on
+// which one that is).
+constexpr int kPartThreads = 256;
+constexpr int kPartNV = 2;
+constexpr int kPartChunks = kPartThreads * kPartNV;
+
+struct Split {
+  float2* part;     // [n][parts] maximum, sum of exp((z - maximum) / T)
+  float* zslot;     // [n][k] the student's logits at the teacher's entries
+  uint32_t* done;   // rows whose kl is there
+  float* loss;
+  int parts;
+};
+
+// What both kernels do with part `part` of a row: its chunks into registers, the entry past
+// the last whole chunk (last part only) into vl.
+template <int CD>
+struct Part {
+  using E = Elem<CD>;
+  int V, full, left, c0, here;  // here: whole chunks of this part
+  __device__ __forceinline__ Part(int64_t V_, int part, int parts) {
+    V = (int)V_;
+    full = V / E::PC;
+    c0 = part * kPartChunks;
+    here = min(kPartChunks, full - c0);
+    left = part == parts - 1 ? V - full * E::PC : 0;
+  }
+  __device__ __forceinline__ void load(const char* row, u32x4_t (&v)[kPartNV], float& vl) const {
+    const rsrc_t r = make_rsrc(row + (int64_t)c0 * 16, here > 0 ? here * 16 : 0);
+#pragma unroll
+    for (int s = 0; s < kPartNV; ++s)
+      v[s] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                             r, (int)(threadIdx.x * 16), s * kPartThreads * 16, 0));
+    vl = (int)threadIdx.x < left ? load_cd<CD>(row, (int64_t)full * E::PC + threadIdx.x) : -INFINITY;
+  }
+  __device__ __forceinline__ bool has(int s) const { return (int)threadIdx.x + s * kPartThreads < here; }
+};
+
+__device__ __forceinline__ float block_max(float v, float* red) {
+  v = wave_max(v);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+}
+__device__ __forceinline__ float block_sum(float v, float* red) {
+  v = wave_sum(v);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+__device__ __forceinline__ int64_t slot_index(const Distill& p, int64_t at) {
+  return p.idx64 ? ((const int64_t*)p.idx)[at] : (int64_t)((const int32_t*)p.idx)[at];
+}
+
+template <int CD>
+__global__ __launch_bounds__(kPartThreads) void k_distill_part(Distill p, Split sp) {
+  using E = Elem<CD>;
+  __shared__ float red[2][kPartThreads / 64];
+  const int64_t i = blockIdx.y;
+  const int part = blockIdx.x, tid = threadIdx.x;
+  if (i == 0 && part == 0 && tid == 0) *sp.done = 0;  // read by the next launch only
+  if ((p.weight ? p.weight[i] : p.w_default) == 0.f) return;
+  const char* row = (const char*)p.z + i * p.ldz * E::ES;
+  const Part<CD> P(p.V, part, sp.parts);
+  u32x4_t v[kPartNV];
+  float vl;
+  P.load(row, v, vl);
+  if (part == 0)
+    for (int j = tid; j < p.k; j += kPartThreads) {
+      const int64_t ix = slot_index(p, i * p.k + j);
+      if (ix >= 0 && ix < p.V) sp.zslot[i * p.k + j] = load_cd<CD>(row, ix);
+    }
+  float m = vl;
+#pragma unroll
+  for (int s = 0; s < kPartNV; ++s)
+    if (P.has(s))
+#pragma unroll
+      for (int e = 0; e < E::PC; ++e) m = fmaxf(m, E::get(v[s], e));
+  m = block_max(m, red[0]);
+  float sum = 0.f;
+  // a part of nothing but -inf has no share (a NaN in it still counts)
+  auto add = [&](float z) { sum += z == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((z - m) * p.c); };
+#pragma unroll
+  for (int s = 0; s < kPartNV; ++s)
+    if (P.has(s))
+#pragma unroll
+      for (int e = 0; e < E::PC; ++e) add(E::get(v[s], e));
+  add(vl);
+  sum = block_sum(sum, red[1]);
+  if (tid == 0) sp.part[i * sp.parts + part] = make_float2(m, sum);
+}
+
+template <int CD, int KC>
+__global__ __launch_bounds__(kPartThreads) void k_distill_join(Distill p, Split sp) {
+  using E = Elem<CD>;
+  constexpr int TPB = kPartThreads, SPT = (KC + TPB - 1) / TPB;
+  __shared__ __attribute__((aligned(16))) int32_t s_idx[KC];  // the row's slots; -1: absent, or past the last
+  __shared__ float s_e[KC], red[5][TPB / 64];
+  __shared__ int s_last;
+  const int64_t i = blockIdx.y;
+  const int part = blockIdx.x, tid = threadIdx.x;
+  const float w = p.weight ? p.weight[i] : p.w_default;
+  const Part<CD> P(p.V, part, sp.parts);
+  const char* row = (const char*)p.z + i * p.ldz * E::ES;
+  char* dr = p.dz ? (char*)p.dz + i * p.lddz * E::ES : nullptr;
+  float kl = 0.f, m = 0.f, inv = 0.f, umax = -INFINITY, usum = 0.f;
+  bool live = w != 0.f;
+  u32x4_t v[kPartNV];
+  float vl = 0.f, su[SPT], sz[SPT];
+  int32_t si[SPT];
+  if (live) {
+    if (dr) P.load(row, v, vl);
+    bool here = false;
+#pragma unroll
+    for (int s = 0; s < SPT; ++s) {
+      const int j = tid + s * TPB;
+      si[s] = -1;
+      if (j < p.k) {
+        const int64_t at = i * p.k + j, ix = slot_index(p, at);
+        su[s] = load_any(p.u, at, p.ud);
+        if (ix >= 0 && ix < p.V && !(su[s] == -INFINITY)) {
+          si[s] = (int32_t)ix;
+          sz[s] = sp.zslot[at];
+          umax = fmaxf(umax, su[s]);
+          here = true;
+        }
+      }
+      if (j < KC) s_idx[j] = si[s];
+    }
+    // the row's maximum and sum from its parts'
+    float pm = -INFINITY;
+    for (int q = tid; q < sp.parts; q += TPB) pm = fmaxf(pm, sp.part[i * sp.parts + q].x);
+    m = block_max(pm, red[0]);
+    umax = block_max(umax, red[1]);
+    live = __syncthreads_or(here);
+    if (live) {
+      float ps = 0.f, us = 0.f;
+      for (int q = tid; q < sp.parts; q += TPB) {
+        const float2 x = sp.part[i * sp.parts + q];
+        // a part of nothing but -inf adds nothing, unless the whole row is that (NaN)
+        ps += x.x == -INFINITY && x.y == 0.f && m != -INFINITY ? 0.f : x.y * __builtin_amdgcn_exp2f((x.x - m) * p.c);
+      }
+#pragma unroll
+      for (int s = 0; s < SPT; ++s)
+        if (si[s] >= 0) {
+          const float ex = __builtin_amdgcn_exp2f((su[s] - umax) * p.c);
+          s_e[tid + s * TPB] = ex;
+          us += ex;
+        }
+      const float sum = block_sum(ps, red[2]);
+      usum = block_sum(us, red[3]);
+      inv = 1.0f / sum;
+      if (part == 0) {
+        const float lsum = logf(sum) - logf(usum);
+#pragma unroll
+        for (int s = 0; s < SPT; ++s)
+          if (si[s] >= 0) {
+            const float pr = s_e[tid + s * TPB] / usum;
+            if (pr != 0.f) kl += pr * (((su[s] - umax) - (sz[s] - m)) * p.inv_t + lsum);
+          }
+        kl = p.t * p.t * block_sum(kl, red[4]);
+      }
+    }
+  }
+  if (dr) {
+    const float wt = w * p.t, gs = wt * inv;
+    const rsrc_t rd = make_rsrc(dr + (int64_t)P.c0 * 16, P.here > 0 ? P.here * 16 : 0);
+#pragma unroll
+    for (int s = 0; s < kPartNV; ++s) {
+      u32x4_t o = {0u, 0u, 0u, 0u};
+      if (live) {
+        float g[E::PC];
+#pragma unroll
+        for (int e = 0; e < E::PC; ++e) g[e] = gs * __builtin_amdgcn_exp2f((E::get(v[s], e) - m) * p.c);
+        o = E::pack(g);
+      }
+      __builtin_amdgcn_raw_buffer_store_b128(o, rd, (int)(tid * 16), s * TPB * 16, 0);
+    }
+    if (tid < P.left)
+      store_cd<CD>(dr, (int64_t)P.full * E::PC + tid, live ? gs * __builtin_amdgcn_exp2f((vl - m) * p.c) : 0.f);
+    if (live) {
+      // the part's entries that the teacher names, once more with its share taken off: after
+      // every wave's stores above have reached memory
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+      const int first = P.c0 * E::PC, last = P.left ? P.V : (P.c0 + P.here) * E::PC;
+#pragma unroll
+      for (int s = 0; s < SPT; ++s) {
+        const int j = tid + s * TPB;
+        if (si[s] < first || si[s] >= last) continue;  // absent slots are below 0
+        // does another slot name the same entry?  (16 at a time: one after the other, 217 slots
+        // took 15 us)
+        int same = 0;
+        for (int l = 0; l < p.k; l += 16)
+#pragma unroll
+          for (int x = 0; x < 16; x += 4) {
+            const int4 id = *(const int4*)&s_idx[l + x];
+            same += (id.x == si[s]) + (id.y == si[s]) + (id.z == si[s]) + (id.w == si[s]);
+          }
+        float share = s_e[j] / usum;
+        bool mine = true;
+        if (same > 1) {  // the first of them writes, with the shares added in slot order
+          share = 0.f;
+          for (int l = 0; l < p.k; ++l)
+            if (s_idx[l] == si[s]) {
+              mine &= l >= j;
+              share += s_e[l] / usum;
+            }
+        }
+        if (mine) store_cd<CD>(dr, si[s], wt * (__builtin_amdgcn_exp2f((sz[s] - m) * p.c) * inv - share));
+      }
+    }
+  }
+  if (part != 0) return;
+  if (tid == 0) {
+    __hip_atomic_store(&p.kl[i], live ? kl : 0.f, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    s_last = __hip_atomic_fetch_add(sp.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)p.n - 1;
+  }
+  __syncthreads();
+  if (!s_last || tid >= 64) return;
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+  double acc = 0.0;
+  for (int64_t r = tid; r < p.n; r += 64) {
+    const float wr = p.weight ? p.weight[r] : p.w_default;
+    const float x = __hip_atomic_load(&p.kl[r], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    acc += wr == 0.f ? 0.0 : (double)wr * (double)x;
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) acc += __shfl_xor(acc, off, 64);
+  if (tid == 0) sp.loss[0] = (float)acc;
+}
+
+// Rows that are cut into parts: few of them, and longer than two parts.
+constexpr int64_t kSplitRows = 64;
+bool split_rows(int64_t n, int64_t V, int cd) {
+  return n <= kSplitRows && V * cd_bytes(cd) > 2 * kPartChunks * 16 && V * cd_bytes(cd) / 16 <= (1LL << 30);
+}
+int64_t parts_of(int64_t V, int cd) { return std::max<int64_t>(1, ceil_div(V * cd_bytes(cd) / 16, kPartChunks)); }
+
+size_t al(size_t b) { return (b + 255) & ~(size_t)255; }
+
+template <int CD>
+int distill_split(const Distill& p, const Split& sp, hipStream_t s) {
+  const dim3 g((unsigned)sp.parts, (unsigned)p.n), b(kPartThreads);
+  k_distill_part<CD><<<g, b, 0, s>>>(p, sp);
+  const int rc = check_launch("k_distill_part");
+  if (rc) return rc;
+  if (p.k <= kPartThreads) k_distill_join<CD, kPartThreads><<<g, b, 0, s>>>(p, sp);
+  else k_distill_join<CD, kMaxK><<<g, b, 0, s>>>(p, sp);
+  return check_launch("k_distill_join");
+}
+
 // Workgroups: as many as are resident at once at most (each goes through its rows).
-template <int CD, int TPB, int NV>
+template <int CD, int TPB, int NV, int KC>
 void launch_rows(const Distill& p, int per_cu, hipStream_t s) {
   const int64_t g = std::min<int64_t>(p.n, (int64_t)per_cu * cu_count());
-  k_distill<CD, TPB, NV><<<dim3((unsigned)g), dim3(TPB), 0, s>>>(p);
+  k_distill<CD, TPB, NV, KC><<<dim3((unsigned)g), dim3(TPB), 0, s>>>(p);
 }
 
 // Threads and registers for a row of `chunks` 16-byte chunks.  With fewer rows than
@@ -409,22 +669,35 @@ void launch_rows(const Distill& p, int per_cu, hipStream_t s) {
 template <int CD>
 int distill_rows(const Distill& p, hipStream_t s) {
   const int64_t chunks = p.V / Elem<CD>::PC;
-  const bool few = p.n <= cu_count();
-  if (chunks <= 256 * 4) launch_rows<CD, 256, 4>(p, 3, s);
-  else if (chunks <= 256 * 16 && !few) launch_rows<CD, 256, 16>(p, 3, s);
-  else if (chunks <= 1024 * 4) launch_rows<CD, 1024, 4>(p, 1, s);
-  else if (chunks <= 1024 * 8) launch_rows<CD, 1024, 8>(p, 1, s);
-  else if (chunks <= 1024 * 16) launch_rows<CD, 1024, 16>(p, 1, s);
-  else if (chunks <= 1024 * 20) launch_rows<CD, 1024, 20>(p, 1, s);
-  else launch_rows<CD, 1024, 0>(p, 1, s);
+  const bool few = p.n <= cu_count(), slots = p.k <= kFewSlots;
+  if (chunks <= 256 * 4) {
+    if (slots) launch_rows<CD, 256, 4, kFewSlots>(p, 5, s);
+    else launch_rows<CD, 256, 4, kMaxK>(p, 3, s);
+  } else if (chunks <= 256 * 16 && !few) {
+    if (slots) launch_rows<CD, 256, 16, kFewSlots>(p, 3, s);
+    else launch_rows<CD, 256, 16, kMaxK>(p, 3, s);
+  } else if (chunks <= 1024 * 4) launch_rows<CD, 1024, 4, kMaxK>(p, 1, s);
+  else if (chunks <= 1024 * 8) launch_rows<CD, 1024, 8, kMaxK>(p, 1, s);
+  else if (chunks <= 1024 * 16) launch_rows<CD, 1024, 16, kMaxK>(p, 1, s);
+  else if (chunks <= 1024 * 20) launch_rows<CD, 1024, 20, kMaxK>(p, 1, s);
+  else launch_rows<CD, 1024, 0, kMaxK>(p, 1, s);
   return check_launch("k_distill");
 }
 
 }  // namespace
 
+size_t distill_workspace_bytes(int64_t n, int64_t V, int32_t k, int cd) {
+  size_t b = al((size_t)std::max<int64_t>(n, 1) * 4);  // kl
+  if (n > 0 && split_rows(n, V, cd))
+    b += al((size_t)n * parts_of(V, cd) * sizeof(float2)) + al((size_t)n * k * 4) + al(4);
+  return b;
+}
+
 int launch_distill(const void* z, int64_t n, int64_t V, int64_t ldz, int cd, const void* u, int ud, const void* idx,
-                   int idx64, int32_t k, float temperature, const float* weight, float* loss, float* kl, void* dz,
-                   int64_t lddz, hipStream_t s) {
+                   int idx64, int32_t k, float temperature, const float* weight, float* loss, float* row_kl, void* dz,
+                   int64_t lddz, void* ws, hipStream_t s) {
+  char* base = (char*)ws;
+  float* kl = row_kl ? row_kl : (float*)base;
   ProfScope prof(QLORA_K_LOSS, s);
   Distill p = {};
   p.z = z;
@@ -444,6 +717,20 @@ int launch_distill(const void* z, int64_t n, int64_t V, int64_t ldz, int cd, con
   p.inv_t = (float)(1.0 / (double)temperature);
   p.c = (float)(1.4426950408889634074 / (double)temperature);
   p.w_default = n > 0 ? (float)(1.0 / (double)n) : 0.f;
+  if (n > 0 && split_rows(n, V, cd)) {
+    Split sp;
+    sp.parts = (int)parts_of(V, cd);
+    char* at = base + al((size_t)n * 4);
+    sp.part = (float2*)at;
+    at += al((size_t)n * sp.parts * sizeof(float2));
+    sp.zslot = (float*)at;
+    at += al((size_t)n * k * 4);
+    sp.done = (uint32_t*)at;
+    sp.loss = loss;
+    if (cd == CD_BF16) return distill_split<CD_BF16>(p, sp, s);
+    if (cd == CD_F16) return distill_split<CD_F16>(p, sp, s);
+    return distill_split<CD_F32>(p, sp, s);
+  }
   if (n > 0) {
     int rc;
     if (cd == CD_BF16) rc = distill_rows<CD_BF16>(p, s);

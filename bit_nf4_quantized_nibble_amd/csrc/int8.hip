@@ -93,19 +93,27 @@ __device__ __forceinline__ void route_experts(const Route& r) {
   if (lane == 0) *r.count = min(at, r.cap);
 }
 
+// 16 bytes at any element-aligned address: the memory system takes unaligned vectors (rows of
+// odd length start anywhere; element by element a row of 3411 f16 took twice the time).
+template <int ES>
+struct __attribute__((packed, aligned(ES))) Chunk {
+  u32x4_t v;
+};
+
 // 8 consecutive elements of a row from column k on, 0 past the last column.
-template <int CD, bool VEC>
+template <int CD>
 __device__ __forceinline__ void load8(const void* x, int64_t at, int64_t k, int64_t cols, float (&v)[8]) {
-  if (VEC && k + 8 <= cols) {
+  if (k + 8 <= cols) {
     if constexpr (CD == CD_F32) {
-      const f32x4_t a = *(const f32x4_t*)((const float*)x + at + k), b = *(const f32x4_t*)((const float*)x + at + k + 4);
+      const u32x4_t a = ((const Chunk<4>*)((const float*)x + at + k))->v;
+      const u32x4_t b = ((const Chunk<4>*)((const float*)x + at + k + 4))->v;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        v[e] = a[e];
-        v[4 + e] = b[e];
+        v[e] = __uint_as_float(a[e]);
+        v[4 + e] = __uint_as_float(b[e]);
       }
     } else {
-      const u32x4_t a = *(const u32x4_t*)((const uint16_t*)x + at + k);
+      const u32x4_t a = ((const Chunk<2>*)((const uint16_t*)x + at + k))->v;
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = from_cd16<CD>((uint16_t)(a[e >> 1] >> (16 * (e & 1))));
     }
@@ -155,7 +163,7 @@ __device__ __forceinline__ u32x2_t codes8(const float (&v)[8], float s) {
 // again, from the caches): one pass over x.  The workgroup after the last row forms the
 // experts' route (r.starts set), so that it costs no launch of its own.
 constexpr int kHold = 8;
-template <int CD, int TPR, bool VEC>
+template <int CD, int TPR>
 __global__ __launch_bounds__(kThreads) void k_int8_rows(const void* __restrict__ x, int64_t ldx, int64_t rows,
                                                         int64_t cols, int64_t ld, int8_t* __restrict__ codes,
                                                         float* __restrict__ scale, Route r) {
@@ -174,14 +182,14 @@ __global__ __launch_bounds__(kThreads) void k_int8_rows(const void* __restrict__
 #pragma unroll
     for (int i = 0; i < kHold; ++i) {
       const int64_t k = 8 * (t + (int64_t)i * TPR);
-      if (k < cols) load8<CD, VEC>(x, at, k, cols, v[i]);
+      if (k < cols) load8<CD>(x, at, k, cols, v[i]);
     }
 #pragma unroll
     for (int i = 0; i < kHold; ++i)
       if (8 * (t + (int64_t)i * TPR) < cols) amax = amax8(v[i], amax);
     for (int64_t k = 8 * (t + (int64_t)kHold * TPR); k < cols; k += 8 * TPR) {
       float w[8];
-      load8<CD, VEC>(x, at, k, cols, w);
+      load8<CD>(x, at, k, cols, w);
       amax = amax8(w, amax);
     }
   }
@@ -205,7 +213,7 @@ __global__ __launch_bounds__(kThreads) void k_int8_rows(const void* __restrict__
   }
   for (int64_t k = 8 * (t + (int64_t)kHold * TPR); k < ld; k += 8 * TPR) {
     float w[8];
-    if (k < cols) load8<CD, VEC>(x, at, k, cols, w);
+    if (k < cols) load8<CD>(x, at, k, cols, w);
     *(u32x2_t*)(dst + k) = k < cols ? codes8(w, s) : u32x2_t{0u, 0u};
   }
 }
@@ -386,21 +394,24 @@ __device__ __forceinline__ float coefficient(const I8& p, const Place& t, int i)
 
 // Lane (r32, h) of block (i, j) holds row 32 i + r32, columns 32 j + 8 q + 4 h + v of the
 // wave's part in elements 4 q + v.  32 rows at a time go through the wave's own LDS W (16-byte
-// chunk c of a row at chunk c ^ row) and leave as whole rows of 32 WNB columns.  Where y's rows
-// are whole chunks every wave issues exactly stores() stores (rows and columns past the
-// tile's fall outside their buffer), so a caller can count past them; other rows go element by
-// element, and the wave waits for those.
+// chunk c of a row at chunk c ^ row) and leave as 16-byte chunks of whole rows, at whatever
+// address y's rows start (element by element, odd row lengths took three times as long).
+// Every wave issues exactly stores() of these (chunks past the tile's rows and whole chunks of
+// columns fall outside their buffer), so a caller can count past them; the columns past the
+// last whole chunk, and rows too long for a buffer, go element by element, and the wave
+// waits for those.
 template <int CD, class T>
 struct Writer {
-  static constexpr int ES = CD == CD_F32 ? 4 : 2, RB = 32 * T::WNB * ES, NC = RB / 16;
+  static constexpr int ES = CD == CD_F32 ? 4 : 2, RB = 32 * T::WNB * ES, NC = RB / 16, PC = 16 / ES;
   static constexpr int stores() { return T::WMB * NC / 2; }
   __device__ static __forceinline__ void run(const I8& p, const Place& pl, const Acc<T>& acc, const float* coef, char* W,
                                              int wave, int lane) {
     constexpr int WMB = T::WMB, WNB = T::WNB;
     const int h = lane >> 5, r32 = lane & 31;
     const int wm = (wave / T::NWN) * 32 * WMB, wn = (wave % T::NWN) * 32 * WNB;
-    const int ncols = (int)min((int64_t)T::TN, p.n - pl.n0);
-    const bool vec = (p.n * ES) % 16 == 0 && ((uintptr_t)p.y & 15) == 0 && p.n * ES < (1 << 26);
+    // the wave's columns that exist, and those of them in whole chunks
+    const int ncols = (int)max((int64_t)0, min((int64_t)(32 * WNB), p.n - pl.n0 - wn));
+    const int whole = p.n * ES < (1 << 26) ? ncols / PC * PC : 0;
 #pragma unroll
     for (int i = 0; i < WMB; ++i) {
       const float sa = coef[2 * T::TN + wm + 32 * i + r32];
@@ -425,33 +436,31 @@ struct Writer {
       asm volatile("" ::: "memory");
       const int row0 = wm + 32 * i, left = min(32, pl.rows - row0);  // rows of the tile in these 32
       const int64_t at0 = (pl.m0 + row0) * p.n + pl.n0 + wn;
-      if (vec) {
-        const int c = lane & (NC - 1);
-        const rsrc_t r = make_rsrc((char*)p.y + at0 * ES, left > 0 ? left * p.n * ES : 0);
-        // ncols is a whole number of chunks here
-        const uint32_t none = wn + c * (16 / ES) < ncols ? 0u : 1u << 31;
+      const int c = lane & (NC - 1);
+      // up to the end of the last row's whole chunks; other chunks past `whole` are masked
+      const rsrc_t r = make_rsrc((char*)p.y + at0 * ES, left > 0 && whole > 0 ? ((left - 1) * p.n + whole) * ES : 0);
+      const uint32_t none = c * PC < whole ? 0u : 1u << 31;
 #pragma unroll
-        for (int it = 0; it < NC / 2; ++it) {
-          const int m = (64 / NC) * it + lane / NC;
-          const u32x4_t v = *(const u32x4_t*)(W + m * RB + ((c ^ (m & (NC - 1))) << 4));
-          const uint32_t off = (uint32_t)(m * (int)p.n * ES + c * 16);
-          __builtin_amdgcn_raw_buffer_store_b128(v, r, (int)((m < left ? off : 1u << 31) | none), 0, 2);
-        }
-      } else {
-        for (int q = lane; q < 32 * 32 * WNB; q += 64) {  // a lane per column
-          const int m = q / (32 * WNB), cc = q % (32 * WNB);
-          const int byte = m * RB + (((cc * ES / 16) ^ (m & (NC - 1))) << 4) + (cc * ES) % 16;
-          if (m < left && wn + cc < ncols) {
-            const int64_t at = at0 + (int64_t)m * p.n + cc;
-            if constexpr (ES == 4) ((uint32_t*)p.y)[at] = *(const uint32_t*)(W + byte);
-            else ((uint16_t*)p.y)[at] = *(const uint16_t*)(W + byte);
-          }
+      for (int it = 0; it < NC / 2; ++it) {
+        const int m = (64 / NC) * it + lane / NC;
+        const u32x4_t v = *(const u32x4_t*)(W + m * RB + ((c ^ (m & (NC - 1))) << 4));
+        const uint32_t off = (uint32_t)(m * (int)p.n * ES + c * 16);
+        __builtin_amdgcn_raw_buffer_store_b128(v, r, (int)((m < left ? off : 1u << 31) | none), 0, 2);
+      }
+      const int rest = ncols - whole;
+      for (int q = lane; q < 32 * rest; q += 64) {
+        const int m = q / rest, cc = whole + q % rest;
+        const int byte = m * RB + (((cc / PC) ^ (m & (NC - 1))) << 4) + (cc % PC) * ES;
+        if (m < left) {
+          const int64_t at = at0 + (int64_t)m * p.n + cc;
+          if constexpr (ES == 4) ((uint32_t*)p.y)[at] = *(const uint32_t*)(W + byte);
+          else ((uint16_t*)p.y)[at] = *(const uint16_t*)(W + byte);
         }
       }
       wait_lgkm0();  // the reads are done before the next 32 rows overwrite them
       asm volatile("" ::: "memory");
     }
-    if (!vec) wait_vmcnt<0>();
+    if (ncols != whole) wait_vmcnt<0>();
   }
 };
 
@@ -681,7 +690,7 @@ __global__ __launch_bounds__(64 * NWV) void k_int8_few(I8 p, const int32_t* __re
     float v[8];
     uint32_t amax = 0;
     for (int k = 8 * tid; k < (int)raw.cols; k += 8 * NT) {
-      load8<CD, true>(raw.x, 0, k, raw.cols, v);
+      load8<CD>(raw.x, 0, k, raw.cols, v);
       amax = amax8(v, amax);
     }
 #pragma unroll
@@ -694,7 +703,7 @@ __global__ __launch_bounds__(64 * NWV) void k_int8_few(I8 p, const int32_t* __re
     for (int k = 8 * tid; k < ld; k += 8 * NT) {
       u32x2_t c = {0u, 0u};
       if (k < raw.cols) {
-        load8<CD, true>(raw.x, 0, k, raw.cols, v);
+        load8<CD>(raw.x, 0, k, raw.cols, v);
         c = codes8(v, fscale);
       }
       *(u32x2_t*)(tok + k) = c;
@@ -819,10 +828,7 @@ int launch_rows(const void* x, int64_t ldx, int64_t rows, int64_t cols, int8_t* 
                 hipStream_t s) {
   const int64_t ld = QLORA_INT8_LD(cols);
   const dim3 g((unsigned)(ceil_div(rows, kThreads / TPR) + (r.starts ? 1 : 0))), b(kThreads);
-  if (((uintptr_t)x & 15) == 0 && (rows == 1 || ldx * cd_bytes(CD) % 16 == 0))
-    k_int8_rows<CD, TPR, true><<<g, b, 0, s>>>(x, ldx, rows, cols, ld, codes, scale, r);
-  else
-    k_int8_rows<CD, TPR, false><<<g, b, 0, s>>>(x, ldx, rows, cols, ld, codes, scale, r);
+  k_int8_rows<CD, TPR><<<g, b, 0, s>>>(x, ldx, rows, cols, ld, codes, scale, r);
   return check_launch("k_int8_rows");
 }
 
@@ -904,8 +910,8 @@ int launch_int8_linear(const qlora_int8_t* w, const void* x, int64_t m, int64_t 
   p.m = m;
   p.n = w->rows;
   p.ld = QLORA_INT8_LD(w->cols);
-  // One token of one matrix, in whole 16-byte vectors: one launch does it all.
-  if (!offsets && m == 1 && p.ld <= kFuseBytes && ((uintptr_t)x & 15) == 0) {
+  // One token of one matrix: one launch does it all.
+  if (!offsets && m == 1 && p.ld <= kFuseBytes) {
     ProfScope prof(QLORA_K_INT8_GEMM, s);
     const Raw raw = {x, w->cols};
     if (cd == CD_BF16) return few_rows<CD_BF16, true>(p, 1, nullptr, raw, s);

@@ -507,7 +507,7 @@ size_t qlora_int8_workspace_bytes(const qlora_int8_t* w, int64_t m, int32_t grou
  * loss: one device float.  row_kl (nullable): fp32 [n], the kl_i.  dlogits (nullable: loss
  * only) may be z itself with ldd = ld; any other overlap with z is refused.  Statistics and sums are fp32 (the sum over the rows
  * fp64) in a fixed order.  n == 0 writes loss = 0.
- * ws: qlora_distill_workspace_bytes(n) bytes, 256-byte aligned.
+ * ws: qlora_distill_workspace_bytes(n, vocab, k, cd) bytes, 256-byte aligned.
  * Errors: QLORA_ERR_INVALID_ARG (null pointers, T not positive and finite, index_bits not 32
  * or 64, pointers that are not element-aligned), QLORA_ERR_SHAPE (n < 0, vocab < 1, k < 1,
  * ld or ldd < vocab), QLORA_ERR_DTYPE, QLORA_ERR_WORKSPACE, QLORA_ERR_UNSUPPORTED
@@ -518,8 +518,8 @@ int qlora_distill_loss_grad(const void* logits, int64_t n, int64_t vocab, int64_
                             int32_t k, float temperature, const float* weight, float* loss, float* row_kl,
                             void* dlogits, int64_t ldd, void* ws, size_t ws_bytes, void* stream);
 
-/* Workspace bytes of qlora_distill_loss_grad; 0 for n < 0.  Pure host function. */
-size_t qlora_distill_workspace_bytes(int64_t n);
+/* Workspace bytes of qlora_distill_loss_grad; 0 for an invalid query.  Pure host function. */
+size_t qlora_distill_workspace_bytes(int64_t n, int64_t vocab, int32_t k, int32_t cd);
 
 /* Workspace size in bytes for op (QLORA_OP_FWD / QLORA_OP_BWD, optionally OR'ed
  * with flags << QLORA_OP_FLAGS_SHIFT) on this layer shape; 0 for an invalid query.

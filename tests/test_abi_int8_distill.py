@@ -116,4 +116,6 @@ def test_distill_refusals(lib, kw, status):
 
 def test_distill_workspace_queries(lib):
     q = lib.qlora_distill_workspace_bytes
-    assert q(-1) == 0 and q(0) > 0 and q(1000) >= 4000
+    assert q(-1, 10, 1, 1) == 0 and q(0, 10, 1, 1) > 0 and q(1000, 10, 1, 1) >= 4000
+    assert q(4, 0, 1, 1) == 0 and q(4, 10, 0, 1) == 0 and q(4, 10, 1025, 1) == 0 and q(4, 10, 1, 3) == 0
+    assert q(4, 100000, 8, 1) > q(4, 100, 8, 1)  # rows cut into parts

@@ -7,6 +7,8 @@ and of the trees (at most 32); so a probability is off by at most
   rel = u (8 A + V / 256 + 64)
 of itself.  The gradient at an entry is off by |w| T (q + p) rel, then rounded once into its type
 (half a step); kl by rel times the size of the numbers that cancel in it (the oracle's kl_mag)."""
+import warnings
+
 import numpy as np
 import pytest
 import torch
@@ -37,7 +39,8 @@ def make(n, V, k, cd, seed, spread=3.0, pad=0, td="f32"):
 def bounds(z, u, T, V):
     zf = np.where(np.isfinite(to_np(z)), to_np(z), np.nan).astype(np.float64)
     uf = np.where(np.isfinite(to_np(u)), to_np(u), np.nan).astype(np.float64)
-    with np.errstate(all="ignore"):
+    with np.errstate(all="ignore"), warnings.catch_warnings():
+        warnings.simplefilter("ignore")  # rows without a finite value
         A = np.nanmax(np.nanmax(zf, 1) - np.nanmin(zf, 1)) / T
         B = np.nanmax(np.nanmax(uf, 1) - np.nanmin(uf, 1)) / T
     # exponentials of less than -110 vanish in fp32 and in the bound's absolute term
@@ -121,11 +124,63 @@ def test_loss_and_gradient(n, V, k, cd):
     check(z, u, idx, T=1.0, bits=32 if V % 2 else 64)
 
 
+# Up to 64 long rows are cut into parts; more rows stay whole, in registers or (the longest) read twice.
+WHOLE = [(65, 8200, 16), (257, 9001, 200), (300, 32760, 128), (70, 32768, 30), (66, 65536, 64), (65, 128000, 33),
+         (65, 150001, 12), (65, 170007, 5)]
+
+
+@pytest.mark.parametrize("cd", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("n,V,k", WHOLE)
+def test_whole_rows(n, V, k, cd):
+    say("whole rows", n, V, k, cd)
+    z, u, idx = make(n, V, k, cd, n + V + k)
+    w = torch.rand(n, generator=torch.Generator().manual_seed(1)) / n
+    w[torch.randperm(n, generator=torch.Generator().manual_seed(2))[: n // 3]] = 0
+    idx[n - 1] = -1                       # rows left out next to each other and at the end
+    idx[5:8] = -1
+    idx[9, : k // 2] = idx[9, k // 2]
+    check(z, u, idx, T=0.9, w=w, in_place=n % 2 == 0)
+
+
+@pytest.mark.parametrize("V", [8300, 40000, 120001, 171000])
+@pytest.mark.parametrize("n", [64, 65])
+def test_special_values_in_long_rows(V, n):
+    """The same rows with few of them (cut into parts) and with one more (whole)."""
+    say("special values", n, V)
+    z, u, idx = make(n, V, 8, "bf16", V)
+    lowest = torch.finfo(z.dtype).min
+    z[0, :] = float("-inf")                       # nothing allowed: NaN
+    z[1, V - 1] = float("nan")
+    z[2, V // 2] = float("inf")
+    z[3, : V - 9] = float("-inf")                 # whole stretches of nothing
+    z[4, 100:] = float("-inf")
+    z[5, :] = lowest                              # uniform
+    z[6, :] = lowest
+    z[6, V - 1] = 3.0
+    z[7, idx[7, 2]] = float("-inf")               # the teacher wants a forbidden entry
+    idx[3] = torch.arange(V - 8, V)
+    idx[4] = torch.arange(0, 8)
+    idx[5] = torch.arange(V - 8, V)
+    idx[6] = V - 1
+    kl = torch.empty(n, device="cuda")
+    loss, dz = qn.distill_loss_grad(z.cuda(), u.cuda(), idx.cuda(), row_kl=kl)
+    kl, dz = to_np(kl), to_np(dz)
+    assert np.isnan(kl[:3]).all() and np.isnan(dz[:3]).all() and kl[7] == np.inf and np.isfinite(dz[7]).all()
+    assert np.isnan(loss.item()) and np.isfinite(kl[8:]).all()
+    keep = [3, 4, 5, 6] + list(range(8, 20))
+    w = torch.zeros(n)
+    w[keep] = 0.25
+    check(z, u, idx, w=w)
+    check(z, u, idx, w=w, grad=False)
+    check(z, u, idx, w=w, in_place=True)
+
+
 @pytest.mark.parametrize("T", [0.05, 0.7, 2.0, 50.0])
 @pytest.mark.parametrize("cd", ["f32", "bf16", "f16"])
-def test_temperatures(T, cd):
-    say("temperature", T, cd)
-    check(*make(6, 3001, 24, cd, 5), T=T)
+@pytest.mark.parametrize("n,V", [(6, 3001), (6, 40009), (65, 20000)])
+def test_temperatures(n, V, T, cd):
+    say("temperature", n, V, T, cd)
+    check(*make(n, V, 24, cd, 5), T=T)
 
 
 @pytest.mark.parametrize("td", ["f32", "bf16", "f16"])
@@ -142,10 +197,10 @@ def test_weights_and_teacher_types(td, grad):
 
 
 @pytest.mark.parametrize("cd", ["f32", "bf16", "f16"])
-def test_absent_slots_and_empty_rows(cd):
-    say("absent", cd)
-    z, u, idx = make(12, 777, 20, cd, 7)
-    V = 777
+@pytest.mark.parametrize("V", [777, 33333])
+def test_absent_slots_and_empty_rows(V, cd):
+    say("absent", V, cd)
+    z, u, idx = make(12, V, 20, cd, 7)
     idx[0, 3:] = -1
     idx[1, :] = -1                       # an empty row
     idx[2, ::2] = V                      # outside the vocabulary
@@ -162,9 +217,10 @@ def test_absent_slots_and_empty_rows(cd):
     check(z, u, far, bits=64)
 
 
-def test_the_same_index_more_than_once():
-    say("repeated index")
-    z, u, idx = make(5, 300, 40, "f32", 8)
+@pytest.mark.parametrize("n,V", [(5, 300), (5, 30000), (70, 30000)])
+def test_the_same_index_more_than_once(n, V):
+    say("repeated index", n, V)
+    z, u, idx = make(n, V, 40, "f32", 8)
     idx[0, :] = 17
     idx[1, 10:30] = idx[1, 5].item()
     idx[2, 39] = idx[2, 0].item()
@@ -247,9 +303,12 @@ def test_leading_dims():
     assert dz.shape == (3, 4, 100) and torch.equal(dz.view(12, 100), d2) and torch.equal(loss, l2)
 
 
-def test_the_same_bits_every_time():
-    say("deterministic")
-    z, u, idx = make(64, 5000, 16, "bf16", 2)
+@pytest.mark.parametrize("n,V", [(64, 5000), (64, 50000), (65, 50000)])
+def test_the_same_bits_every_time(n, V):
+    say("deterministic", n, V)
+    z, u, idx = make(n, V, 16, "bf16", 2)
+    idx[:, 3] = idx[:, 0]  # shares of one index are added in slot order
+    idx[:, 9] = idx[:, 0]
     a = qn.distill_loss_grad(z.cuda(), u.cuda(), idx.cuda())
     for _ in range(3):
         b = qn.distill_loss_grad(z.cuda(), u.cuda(), idx.cuda())
@@ -276,9 +335,10 @@ def test_gradient_against_differences():
             assert abs(num - dz[i, j].item()) <= 1.5 * h * h / 6 + 20 * 2.0 ** -24 * 8 / (2 * h)
 
 
-def test_captured_and_replayed():
-    say("graph")
-    n, V, k = 20, 3000, 8
+@pytest.mark.parametrize("n,V", [(20, 3000), (20, 40000), (100, 40000)])
+def test_captured_and_replayed(n, V):
+    say("graph", n, V)
+    k = 8
     z, u, idx = (t.cuda() for t in make(n, V, k, "bf16", 4))
     w = torch.ones(n, device="cuda")
     dz = torch.empty_like(z)

@@ -81,7 +81,9 @@ def test_codes_of_strided_rows():
 
 SIZES = [(1, 1, 1), (1, 17, 64), (2, 64, 100), (5, 1000, 129), (16, 512, 1024), (17, 130, 4096), (33, 96, 300),
          (64, 257, 2048), (65, 128, 128), (128, 128, 256), (100, 1003, 511), (255, 300, 777), (256, 512, 1024),
-         (300, 1030, 2047), (513, 640, 384), (1, 4096, 4096), (16, 14336, 512), (3, 200, 14336), (1030, 1290, 640)]
+         (300, 1030, 2047), (513, 640, 384), (1, 4096, 4096), (16, 14336, 512), (3, 200, 14336), (1030, 1290, 640),
+         (1, 40, 16400), (1, 300, 131000), (2, 1001, 640), (15, 9000, 130), (16, 20011, 128), (300, 4099, 129),
+         (520, 3001, 257), (600, 4321, 200), (2049, 2051, 130), (61, 500, 9000), (700, 64, 3328)]
 
 
 @pytest.mark.parametrize("cd", ["f32", "bf16", "f16"])
