@@ -229,6 +229,8 @@ struct I8 {
   int64_t m, n, ld;
   const int32_t* count;  // grouped by expert: tiles[0 .. *count), else null
   const int4* tiles;
+  int* part;         // contraction cut into `split` slices: their sums, tile by tile
+  int split;
 };
 
 // y from the sum: (sum * s) * t + bias, each product rounded to fp32, then to cd.
@@ -305,6 +307,14 @@ struct Copies {
     off = (uint32_t)(row * ld + (((lane & 7) ^ swz(row)) << 4));
     step = (uint32_t)(8 * T::NW * ld);
     KT = ld >> 7;
+  }
+  // only stages k0 .. k1 - 1 of the contraction
+  __device__ __forceinline__ void cut(int k0, int k1) {
+    a += (int64_t)k0 * 128;
+    b += (int64_t)k0 * 128;
+    abytes -= (int64_t)k0 * 128;
+    bbytes -= (int64_t)k0 * 128;
+    KT = k1 - k0;
   }
   __device__ __forceinline__ void one(char* stage_lds, int stage, int i) const {
     // past the last stage: an empty buffer, nothing is fetched
@@ -412,6 +422,7 @@ struct Writer {
     // the wave's columns that exist, and those of them in whole chunks
     const int ncols = (int)max((int64_t)0, min((int64_t)(32 * WNB), p.n - pl.n0 - wn));
     const int whole = p.n * ES < (1 << 26) ? ncols / PC * PC : 0;
+    const bool lines = (p.n * ES) % 128 == 0 && ((uintptr_t)p.y & 127) == 0;  // whole lines are written at once
 #pragma unroll
     for (int i = 0; i < WMB; ++i) {
       const float sa = coef[2 * T::TN + wm + 32 * i + r32];
@@ -445,7 +456,9 @@ struct Writer {
         const int m = (64 / NC) * it + lane / NC;
         const u32x4_t v = *(const u32x4_t*)(W + m * RB + ((c ^ (m & (NC - 1))) << 4));
         const uint32_t off = (uint32_t)(m * (int)p.n * ES + c * 16);
-        __builtin_amdgcn_raw_buffer_store_b128(v, r, (int)((m < left ? off : 1u << 31) | none), 0, 2);
+        const int at = (int)((m < left ? off : 1u << 31) | none);
+        if (lines) __builtin_amdgcn_raw_buffer_store_b128(v, r, at, 0, 2);
+        else __builtin_amdgcn_raw_buffer_store_b128(v, r, at, 0, 0);
       }
       const int rest = ncols - whole;
       for (int q = lane; q < 32 * rest; q += 64) {
@@ -502,20 +515,29 @@ __device__ __forceinline__ Place place_of(const I8& p, int t, int tiles_m, int t
 }
 
 // One tile to a workgroup; several workgroups share a compute unit.
-template <int CD, class T, int WGS>
+// SPLIT: p.split workgroups to a tile, each a slice of the contraction; the sums go to p.part
+// as [slice][tile][TM][TN] and k_int8_join adds them (exactly, so in any order).
+template <int CD, class T, int WGS, bool SPLIT = false>
 __global__ __launch_bounds__(64 * T::NW, WGS) void k_int8_tile(I8 p) {
   // One array for everything: with several, the compiler tells them apart and then waits for
   // every copy in flight before each fragment it reads (228 -> 324 us on the long prompt).
   __shared__ __attribute__((aligned(1024))) char lds[T::LDS + T::COEF * 4];
   float* coef = (float*)(lds + T::LDS);
-  const int tiles_n = (int)((p.n + T::TN - 1) / T::TN), tiles_m = tile_rows_of<T>(p);
-  if ((int)blockIdx.x >= tiles_m * tiles_n) return;
-  const Place pl = place_of<T>(p, xcd_run(blockIdx.x, tiles_m * tiles_n), tiles_m, tiles_n);
+  const int tiles_n = (int)((p.n + T::TN - 1) / T::TN), tiles_m = tile_rows_of<T>(p), total = tiles_m * tiles_n;
+  int b = blockIdx.x, slice = 0;
+  if (SPLIT) {
+    slice = b % p.split;
+    b /= p.split;
+  }
+  if (b >= total) return;
+  const int t = SPLIT ? b : xcd_run(b, total);
+  const Place pl = place_of<T>(p, t, tiles_m, tiles_n);
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const Copies<T> cp(p, pl, wave, lane);
+  Copies<T> cp(p, pl, wave, lane);
+  if (SPLIT) cp.cut(slice * cp.KT / p.split, (slice + 1) * cp.KT / p.split);
   // the coefficients are requested first and stored once the copies are on their way
-  constexpr int NC = (T::COEF + 64 * T::NW - 1) / (64 * T::NW);
-  float c[NC];
+  constexpr int NC = SPLIT ? 0 : (T::COEF + 64 * T::NW - 1) / (64 * T::NW);
+  float c[NC > 0 ? NC : 1];
 #pragma unroll
   for (int i = 0; i < NC; ++i)
     c[i] = tid + i * 64 * T::NW < T::COEF ? coefficient<CD, T>(p, pl, tid + i * 64 * T::NW) : 0.f;
@@ -529,7 +551,43 @@ __global__ __launch_bounds__(64 * T::NW, WGS) void k_int8_tile(I8 p) {
   barrier_only();
   Acc<T> acc;
   contract<T>(acc, lds, cp, lane);
-  Writer<CD, T>::run(p, pl, acc, coef, lds + wave * 32 * Writer<CD, T>::RB, wave, lane);
+  if constexpr (SPLIT) {
+    int* dst = p.part + ((int64_t)slice * total + t) * (T::TM * T::TN);
+    const int wm = (wave / T::NWN) * 32 * T::WMB, wn = (wave % T::NWN) * 32 * T::WNB;
+#pragma unroll
+    for (int i = 0; i < T::WMB; ++i)
+#pragma unroll
+      for (int j = 0; j < T::WNB; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const i32x4_t v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+          *(i32x4_t*)(dst + (wm + 32 * i + (lane & 31)) * T::TN + wn + 32 * j + 8 * q + 4 * (lane >> 5)) = v;
+        }
+  } else {
+    Writer<CD, T>::run(p, pl, acc, coef, lds + wave * 32 * Writer<CD, T>::RB, wave, lane);
+  }
+}
+
+// y from the slices' sums: four columns of a row to a thread.
+template <int CD, class T>
+__global__ __launch_bounds__(kThreads) void k_int8_join(I8 p) {
+  const int tiles_n = (int)((p.n + T::TN - 1) / T::TN), tiles_m = tile_rows_of<T>(p), total = tiles_m * tiles_n;
+  const int t = blockIdx.x;
+  if (t >= total) return;
+  const Place pl = place_of<T>(p, t, tiles_m, tiles_n);
+  const int at = 4 * (blockIdx.y * kThreads + threadIdx.x), row = at / T::TN, col = at % T::TN;
+  if (row >= pl.rows || pl.n0 + col >= p.n) return;
+  const int* src = p.part + (int64_t)t * (T::TM * T::TN) + at;
+  i32x4_t sum = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int s = 0; s < p.split; ++s) sum = sum + *(const i32x4_t*)(src + (int64_t)s * total * (T::TM * T::TN));
+  const int64_t wrow = (int64_t)pl.e * p.n + pl.n0 + col;
+  const float sa = p.sa[pl.m0 + row];
+#pragma unroll
+  for (int x = 0; x < 4; ++x)
+    if (pl.n0 + col + x < p.n)
+      store_y<CD>(p, pl.m0 + row, pl.n0 + col + x, sum[x], sa, p.sb[wrow + x],
+                  p.bias ? load_cd<CD>(p.bias, wrow + x) : 0.f);
 }
 
 using Full = Tile<4, 2, 2, 4, 2>;  // 256 x 256, eight waves
@@ -760,11 +818,17 @@ __global__ __launch_bounds__(64 * NWV) void k_int8_few(I8 p, const int32_t* __re
 
 size_t al(size_t b) { return (b + 255) & ~(size_t)255; }
 
-// Workspace: the tokens' codes and scales, and for the form grouped by expert its route.
-struct Plan {
-  size_t off_codes = 0, off_scale = 0, off_starts = 0, off_count = 0, off_tiles = 0, total = 0;
-  int cap = 0;
-};
+// Slices of the contraction for a product of `tiles` tiles of 64 x 64 that leaves most compute
+// units idle: as many as give 256 workgroups, of six stages at least.  A stage of a lone
+// workgroup takes 0.33 us, the second launch 3 us: 100 x 1000 x 14336 40.1 -> 21.0 us,
+// 61 x 1984 x 6212 23.1 -> 16.5, 768 x 64 x 3328 14.4 -> 13.3; below 24 stages or three slices
+// it is slower (688 x 128 x 2496 12.9 -> 14.1, 128 x 4096 x 4096 17.3 -> 19.9).
+constexpr int kSplitItems = 256;
+int slices(int64_t tiles, int64_t ld) {
+  const int64_t lines = ld >> 7;
+  if (lines < 24 || tiles * 3 > kSplitItems) return 1;
+  return (int)std::min<int64_t>(std::min<int64_t>(8, kSplitItems / tiles), lines / 6);
+}
 
 // Which product kernel takes a call: the few-token kernel or tiles, the larger the less each
 // operand is read again, the smaller the more of the chip a small product occupies
@@ -818,6 +882,12 @@ Plan plan_int8(const qlora_int8_t* w, int64_t m, bool grouped) {
     off += al(4);
     P.off_tiles = off;
     off += al((size_t)P.cap * sizeof(int4));
+  }
+  const int64_t tiles = (grouped ? P.cap : ceil_div(m, Small::TM)) * ceil_div(w->rows, Small::TN);
+  P.split = tiles > 0 ? slices(tiles, QLORA_INT8_LD(w->cols)) : 1;
+  if (P.split > 1) {
+    P.off_part = off;
+    off += (size_t)P.split * tiles * Small::TM * Small::TN * 4;
   }
   P.total = off;
   return P;
@@ -881,7 +951,13 @@ int product(const I8& p, int32_t experts, int cap, const int32_t* starts, hipStr
     k_int8_full<CD><<<dim3((unsigned)std::min<int64_t>(cu_count(), 2 * tiles)), dim3(512), 0, s>>>(p);
   else if (f == MID) k_int8_tile<CD, Mid, 2><<<g, dim3(64 * Mid::NW), 0, s>>>(p);
   else if (f == LOW) k_int8_tile<CD, Low, 2><<<g, dim3(64 * Low::NW), 0, s>>>(p);
-  else k_int8_tile<CD, Small, 2><<<g, dim3(64 * Small::NW), 0, s>>>(p);
+  else if (p.split > 1) {
+    k_int8_tile<CD, Small, 2, true><<<dim3((unsigned)(tiles * p.split)), dim3(64 * Small::NW), 0, s>>>(p);
+    const int rc = check_launch("k_int8_tile");
+    if (rc) return rc;
+    k_int8_join<CD, Small><<<dim3((unsigned)tiles, Small::TM * Small::TN / (4 * kThreads)), dim3(kThreads), 0, s>>>(p);
+    return check_launch("k_int8_join");
+  } else k_int8_tile<CD, Small, 2><<<g, dim3(64 * Small::NW), 0, s>>>(p);
   return check_launch(f == FULL ? "k_int8_full" : "k_int8_tile");
 }
 
@@ -910,6 +986,8 @@ int launch_int8_linear(const qlora_int8_t* w, const void* x, int64_t m, int64_t 
   p.m = m;
   p.n = w->rows;
   p.ld = QLORA_INT8_LD(w->cols);
+  p.part = (int*)(base + P.off_part);
+  p.split = P.split;
   // One token of one matrix: one launch does it all.
   if (!offsets && m == 1 && p.ld <= kFuseBytes) {
     ProfScope prof(QLORA_K_INT8_GEMM, s);

@@ -83,7 +83,8 @@ SIZES = [(1, 1, 1), (1, 17, 64), (2, 64, 100), (5, 1000, 129), (16, 512, 1024), 
          (64, 257, 2048), (65, 128, 128), (128, 128, 256), (100, 1003, 511), (255, 300, 777), (256, 512, 1024),
          (300, 1030, 2047), (513, 640, 384), (1, 4096, 4096), (16, 14336, 512), (3, 200, 14336), (1030, 1290, 640),
          (1, 40, 16400), (1, 300, 131000), (2, 1001, 640), (15, 9000, 130), (16, 20011, 128), (300, 4099, 129),
-         (520, 3001, 257), (600, 4321, 200), (2049, 2051, 130), (61, 500, 9000), (700, 64, 3328)]
+         (520, 3001, 257), (600, 4321, 200), (2049, 2051, 130), (61, 500, 9000), (700, 64, 3328),
+         (17, 64, 131072), (100, 1001, 2600), (20, 3000, 4000)]
 
 
 @pytest.mark.parametrize("cd", ["f32", "bf16", "f16"])
@@ -211,6 +212,8 @@ def check_experts(sizes, n, k, cd, seed, bias=False, before=0, tail=0, offsets=N
     ([0, 300, 0, 5], 257, 130, 0, 130),
     ([128, 129, 127, 0, 256], 300, 384, 7, 0),
     ([700, 0, 3, 400], 520, 200, 0, 33),
+    ([30, 0, 64, 7], 130, 5000, 1, 9),
+    ([100, 5], 70, 3000, 0, 0),
 ])
 def test_experts(sizes, n, k, before, tail, cd):
     say("experts", sizes, n, k, cd, before, tail)
