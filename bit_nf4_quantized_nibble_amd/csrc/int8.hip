@@ -830,6 +830,13 @@ int slices(int64_t tiles, int64_t ld) {
   return (int)std::min<int64_t>(std::min<int64_t>(8, kSplitItems / tiles), lines / 6);
 }
 
+// Workspace: the tokens' codes and scales, for the form grouped by expert its route, and the
+// sums of a cut contraction.
+struct Plan {
+  size_t off_codes = 0, off_scale = 0, off_starts = 0, off_count = 0, off_tiles = 0, off_part = 0, total = 0;
+  int cap = 0, split = 1;
+};
+
 // Which product kernel takes a call: the few-token kernel or tiles, the larger the less each
 // operand is read again, the smaller the more of the chip a small product occupies
 // (measured for the whole call, us):
