@@ -592,7 +592,8 @@ __global__ __launch_bounds__(kThreads) void k_int8_join(I8 p) {
 
 using Full = Tile<4, 2, 2, 4, 2>;  // 256 x 256, eight waves
 using Half = Tile<2, 2, 2, 4, 2>;  // 128 x 256, eight waves
-using Mid = Tile<2, 2, 2, 2, 2>;   // 128 x 128, four waves, two workgroups to a compute unit
+using Wide = Tile<2, 2, 2, 4, 3>;  // 128 x 256, eight waves
+using Mid = Tile<2, 2, 2, 2, 4>;   // 128 x 128, four waves
 using Low = Tile<1, 2, 2, 2, 3>;   // 64 x 128, four waves, two workgroups to a compute unit
 using Small = Tile<1, 1, 2, 2, 4>;  // 64 x 64, four waves, two workgroups to a compute unit
 
@@ -837,43 +838,49 @@ struct Plan {
   int cap = 0, split = 1;
 };
 
-// Which product kernel takes a call: the few-token kernel or tiles, the larger the less each
-// operand is read again, the smaller the more of the chip a small product occupies
-// (measured for the whole call, us):
-//                            few    64 x 64   64 x 128   128 x 128   256 x 256
-//   8 x 4096 x 4096          11.1     15.7      21.0                           64 tiles of 64 x 64
-//   16 x 14336 x 4096        19.7     20.2      24.3        26.1               224
-//   24 x 14336 x 4096        29.6     20.7      24.4
-//   256 x 4096 x 4096                 17.6      18.9        27.8        46     256
-//   512 x 4096 x 4096                 24.7      21.2        29.8        48     256 tiles of 64 x 128
-//   256 x 14336 x 4096                35.2      28.5        30.3        48     448
-//   512 x 14336 x 4096                61.8      49.9        41.1        39.4   112 tiles of 256 x 256
-//   1024 x 14336 x 4096                113        89        74.3        63.5
-// and of experts, with rows on average:
-//   1 of 2 (4096 x 4096)     14.4     18.3      21.8                          128 tiles of 64 x 64
-//   2 of 8 (4096 x 4096)     27.9     33.9      33.2                          512
-//   4 of 8 (4096 x 4096)     28.3     34.3      33.7                          512
-//   4 of 32 (2048 x 2048)    29.0     30.5      29.3                         1024
-//   8 of 32 (2048 x 2048)    37.9     31.9      30.8                         1024
-//   64 of 64 (1024 x 2048)             52        47.5        55.9        47
-//   128 of 8 (4096 x 4096)             61        60          54.6        64
-//   256 of 8 (14336 x 4096)           293       236         215         180
+// Which product kernel takes a call: the few-token kernel, or the smallest tiles that still fit
+// the compute units in one round, 256 x 256 beyond.  Larger tiles read each operand less
+// often, smaller ones occupy more of the chip (whole calls, weights from memory, us):
+//                            few   64 x 64  64 x 128  128 x 128  128 x 256  256 x 256
+//   8 x 4096 x 4096          11.1    15.7     21.0
+//   16 x 14336 x 4096        19.7    20.2     24.3       26.1
+//   24 x 14336 x 4096        29.6    20.7     24.4
+//   64 x 14336 x 4096                22.1     26.9       27.8       35.4       47.3
+//   128 x 14336 x 4096               29.3     27.2       31.1       38.6       50.4
+//   256 x 14336 x 4096               43.8     37.9       31.8       38.5       50.8
+//   512 x 14336 x 4096               67.9     60.1       52.2       40.2       52.8
+//   1024 x 14336 x 4096               114     89.0       90.2                  63.5
+//   512 x 4096 x 4096                26.2     24.2       28.7       36.8       49.1
+//   1024 x 4096 x 4096               46.0     40.0       34.8       39.6       52.1
+//   2048 x 4096 x 4096               78.9     66.4       57.7       46.7       53.4
+// and of experts, by their rows on average:
+//   1 of 2 (4096 x 4096)     14.4    18.3     21.8
+//   4 of 8 (4096 x 4096)     28.3    34.3     33.7
+//   4 of 32 (2048 x 2048)    29.0    30.5     29.3
+//   8 of 32 (2048 x 2048)    37.9    31.9     30.8
+//   32 of 8 (4096 x 4096)            44.8     49.6       41.9       44.6       54.5
+//   64 of 8 (4096 x 4096)            51.3     48.3       44.4       48.5       57.6
+//   64 of 64 (1024 x 2048)           49.5     47.5       54.3       55.1       47.6
+//   128 of 8 (4096 x 4096)           65.8     64.7       63.5       53.3       63.0
+//   192 of 8 (14336 x 4096)           249      203        173        155        174
+//   256 of 8 (4096 x 4096)           96.5     86.1       83.2       83.0       74.2
 // An uneven routing gives some experts several times the average, and the few-token
 // kernel goes over its weights again for each 16 rows, so experts leave it early.
-enum Form { FEW, SMALL, LOW, MID, FULL };
+enum Form { FEW, SMALL, LOW, MID, WIDE, FULL };
 Form form_of(int64_t m, int64_t n, int32_t experts) {
   const int64_t live = std::max<int64_t>(1, std::min<int64_t>(experts, m)), cus = cu_count();
-  // tile rows: each expert's last one is half full on average
-  auto tiles = [&](int64_t tm, int64_t tn) {
-    return (experts == 1 ? ceil_div(m, tm) : std::max(live, m / tm + (live + 1) / 2)) * ceil_div(n, tn);
-  };
-  const int64_t t64 = tiles(64, 64);
   if (m <= (experts == 1 ? 16 : 4 * live)) return FEW;
-  if (t64 <= cus || (t64 <= 2 * cus && m <= 16 * live)) return SMALL;
-  if (tiles(64, 128) <= 2 * cus || m < 96 * live) return LOW;
-  return m >= 256 * live && 16 * tiles(256, 256) >= 7 * cus ? FULL : MID;
+  // tile rows: each expert's last one is half full on average
+  auto one_round = [&](int64_t tm, int64_t tn) {
+    return (experts == 1 ? ceil_div(m, tm) : std::max(live, m / tm + (live + 1) / 2)) * ceil_div(n, tn) <= cus;
+  };
+  if (one_round(64, 64)) return SMALL;
+  if (experts == 1) return one_round(64, 128) ? LOW : one_round(128, 128) ? MID : one_round(128, 256) ? WIDE : FULL;
+  if (m >= 256 * live) return FULL;
+  return m >= 96 * live ? WIDE : one_round(128, 128) ? MID : LOW;
 }
-int tile_rows(Form f) { return f == FULL ? Full::TM : f == MID ? Mid::TM : Low::TM; }
+static_assert(Wide::TN == Full::TN && Mid::TN == Low::TN && Wide::TM == Mid::TM && Low::TM == Small::TM, "by form");
+int tile_rows(Form f) { return f == FULL ? Full::TM : f == WIDE || f == MID ? Mid::TM : Low::TM; }
 
 Plan plan_int8(const qlora_int8_t* w, int64_t m, bool grouped) {
   Plan P;
@@ -949,14 +956,15 @@ template <int CD>
 int product(const I8& p, int32_t experts, int cap, const int32_t* starts, hipStream_t s) {
   const Form f = form_of(p.m, p.n, experts);
   if (f == FEW) return few_rows<CD, false>(p, experts, starts, Raw{}, s);
-  const int tm = tile_rows(f), tn = f == FULL ? Full::TN : f == MID ? Mid::TN : f == LOW ? Low::TN : Small::TN;
+  const int tm = tile_rows(f), tn = f >= WIDE ? Full::TN : f >= LOW ? Low::TN : Small::TN;
   const int64_t tiles = (starts ? cap : ceil_div(p.m, tm)) * ceil_div(p.n, tn);
   if (tiles >= (1LL << 31)) return set_error(QLORA_ERR_UNSUPPORTED, "int8: %lld tiles", (long long)tiles);
   const dim3 g((unsigned)tiles);
   // the large tiles: a workgroup to a compute unit, or to a half tile in an only round
   if (f == FULL)
     k_int8_full<CD><<<dim3((unsigned)std::min<int64_t>(cu_count(), 2 * tiles)), dim3(512), 0, s>>>(p);
-  else if (f == MID) k_int8_tile<CD, Mid, 2><<<g, dim3(64 * Mid::NW), 0, s>>>(p);
+  else if (f == WIDE) k_int8_tile<CD, Wide, 1><<<g, dim3(64 * Wide::NW), 0, s>>>(p);
+  else if (f == MID) k_int8_tile<CD, Mid, 1><<<g, dim3(64 * Mid::NW), 0, s>>>(p);
   else if (f == LOW) k_int8_tile<CD, Low, 2><<<g, dim3(64 * Low::NW), 0, s>>>(p);
   else if (p.split > 1) {
     k_int8_tile<CD, Small, 2, true><<<dim3((unsigned)(tiles * p.split)), dim3(64 * Small::NW), 0, s>>>(p);
