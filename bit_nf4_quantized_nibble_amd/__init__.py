@@ -676,12 +676,15 @@ def distill_loss_grad(logits, top_values, top_index, temperature: float = 1.0, w
         raise ValueError("top_values needs at least one slot per row")
     if top_index.dtype not in (torch.int32, torch.int64):
         raise TypeError("top_index must be int32 or int64, got %s" % (top_index.dtype,))
-    u, ix = top_values.reshape(-1, k).contiguous(), top_index.reshape(-1, top_index.shape[-1]).contiguous()
+    u, ix = top_values, top_index
+    if u.dim() != 2 or ix.dim() != 2:
+        u, ix = u.reshape(-1, k), ix.reshape(-1, ix.shape[-1])
     if u.shape != (n, k) or ix.shape != (n, k):
         raise ValueError("top_values and top_index must be [%d rows, k]" % n)
+    if u.device != device or ix.device != device:
+        raise ValueError("top_values and top_index must be on %s" % (device,))
+    u, ix = u.contiguous(), ix.contiguous()
     td = dtype_code(u.dtype)
-    _check_tensor("top_values", u, device, u.dtype, n * k)
-    _check_tensor("top_index", ix, device, ix.dtype, n * k)
     if weight is not None:
         _check_tensor("weight", weight, device, torch.float32, n)
     if row_kl is not None:

@@ -45,13 +45,8 @@ __device__ __forceinline__ float load_any(const void* p, int64_t i, int cd) {
   return cd == CD_F32 ? load_cd<CD_F32>(p, i) : cd == CD_BF16 ? load_cd<CD_BF16>(p, i) : load_cd<CD_F16>(p, i);
 }
 
-// 16 bytes at any element-aligned address (the memory system takes unaligned vectors;
-// rows of an odd vocabulary start anywhere).
-template <int ES>
-struct __attribute__((packed, aligned(ES))) Chunk {
-  u32x4_t v;
-};
-
+// Rows start at any element: the memory system takes 16-byte vectors at any address, and a
+// buffer's end keeps the lanes past the last whole chunk from reading or writing.
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 __device__ __forceinline__ rsrc_t make_rsrc(const void* p, int bytes) {
   return __builtin_amdgcn_make_buffer_rsrc((void*)p, (short)0, bytes, 0x00020000);
@@ -75,12 +70,6 @@ struct Elem {
       for (int e = 0; e < 4; ++e) o[e] = pack2<CD>(g[2 * e], g[2 * e + 1]);
     }
     return o;
-  }
-  __device__ static __forceinline__ u32x4_t load(const char* base, uint32_t off) {
-    return ((const Chunk<ES>*)(base + off))->v;
-  }
-  __device__ static __forceinline__ void store(char* base, uint32_t off, const u32x4_t& o) {
-    ((Chunk<ES>*)(base + off))->v = o;
   }
 };
 
@@ -121,7 +110,7 @@ __device__ __forceinline__ void opaque(u32x4_t& x) { asm volatile("" : "+v"(x));
 // length, read twice.  Entries past the last whole chunk (fewer than a chunk) go one to a
 // thread.
 template <int CD, int TPB, int NV, int KC>
-__global__ __launch_bounds__(TPB, TPB == 256 ? 3 : 4) void k_distill(Distill p) {
+__global__ __launch_bounds__(TPB, TPB <= 256 ? 3 : 4) void k_distill(Distill p) {
   using E = Elem<CD>;
   constexpr int PC = E::PC, NW = TPB / 64, SPT = (KC + TPB - 1) / TPB, NR = NV > 0 ? NV : 1;
   __shared__ Slots<TPB, KC> sets[2];
@@ -202,7 +191,8 @@ __global__ __launch_bounds__(TPB, TPB == 256 ? 3 : 4) void k_distill(Distill p) 
           }
         zm = fmaxf(zm, vl);
       } else {
-        // running maximum and sum of the thread's entries
+        // running maximum and sum of the thread's entries, four chunks at a time while the next
+        // four are on their way
         auto add = [&](float cm, auto share) {
           const float nm = fmaxf(zm, cm);
           // a thread that has met only -inf so far has no share yet
@@ -210,18 +200,36 @@ __global__ __launch_bounds__(TPB, TPB == 256 ? 3 : 4) void k_distill(Distill p) 
           zm = nm;
         };
         auto part = [&](float y, float nm) { return y == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((y - nm) * p.c); };
-        for (int c0 = 0; c0 < full; c0 += TPB) {
-          if (c0 + tid >= full) break;
-          const u32x4_t x = E::load(zr + (int64_t)c0 * 16, toff);
-          float cm = E::get(x, 0);
+        constexpr int B = 4;
+        u32x4_t x[2][B];
+        auto ask = [&](u32x4_t (&to)[B], int c0) {  // past the last whole chunk: an empty buffer
+          const int here = min(max(full - c0, 0), B * TPB);
+          const rsrc_t r = make_rsrc(zr + (int64_t)c0 * 16, here * 16);
 #pragma unroll
-          for (int e = 1; e < PC; ++e) cm = fmaxf(cm, E::get(x, e));
-          add(cm, [&](float nm) {
-            float cs = 0.f;
+          for (int s = 0; s < B; ++s)
+            to[s] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)toff, s * TPB * 16, 0));
+        };
+        auto take = [&](const u32x4_t (&of)[B], int c0) {
 #pragma unroll
-            for (int e = 0; e < PC; ++e) cs += part(E::get(x, e), nm);
-            return cs;
-          });
+          for (int s = 0; s < B; ++s)
+            if (c0 + s * TPB + tid < full) {
+              float cm = E::get(of[s], 0);
+#pragma unroll
+              for (int e = 1; e < PC; ++e) cm = fmaxf(cm, E::get(of[s], e));
+              add(cm, [&](float nm) {
+                float cs = 0.f;
+#pragma unroll
+                for (int e = 0; e < PC; ++e) cs += part(E::get(of[s], e), nm);
+                return cs;
+              });
+            }
+        };
+        ask(x[0], 0);
+        for (int c0 = 0; c0 < full; c0 += 2 * B * TPB) {
+          ask(x[1], c0 + B * TPB);
+          take(x[0], c0);
+          ask(x[0], c0 + 2 * B * TPB);
+          take(x[1], c0 + B * TPB);
         }
         vl = -INFINITY;
         fetch_left(zr);
@@ -350,12 +358,30 @@ __global__ __launch_bounds__(TPB, TPB == 256 ? 3 : 4) void k_distill(Distill p) 
         __builtin_amdgcn_sched_barrier(0);  // one chunk's exponentials at a time
       }
     } else if (dr) {
-      for (int c0 = 0; c0 < full; c0 += TPB)
-        if (c0 + tid < full) {
-          u32x4_t x = {0u, 0u, 0u, 0u};
-          if (live) x = E::load(zr + (int64_t)c0 * 16, toff);
-          E::store(dr + (int64_t)c0 * 16, toff, grad(x));
-        }
+      constexpr int B = 4;
+      u32x4_t x[2][B];
+      auto ask = [&](u32x4_t (&to)[B], int c0) {
+        const int here = min(max(full - c0, 0), B * TPB);
+        const rsrc_t r = make_rsrc(zr + (int64_t)c0 * 16, live ? here * 16 : 0);
+#pragma unroll
+        for (int s = 0; s < B; ++s)
+          to[s] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(r, (int)toff, s * TPB * 16, 0));
+      };
+      auto give = [&](const u32x4_t (&of)[B], int c0) {
+        const int here = min(max(full - c0, 0), B * TPB);
+        const rsrc_t r = make_rsrc(dr + (int64_t)c0 * 16, here * 16);
+#pragma unroll
+        for (int s = 0; s < B; ++s)
+          if (c0 + s * TPB + wave * 64 < full)
+            __builtin_amdgcn_raw_buffer_store_b128(grad(of[s]), r, (int)toff, s * TPB * 16, 0);
+      };
+      ask(x[0], 0);
+      for (int c0 = 0; c0 < full; c0 += 2 * B * TPB) {
+        ask(x[1], c0 + B * TPB);
+        give(x[0], c0);
+        ask(x[0], c0 + 2 * B * TPB);
+        give(x[1], c0 + B * TPB);
+      }
     }
     if (dr) {
       if (tid < left)
@@ -660,31 +686,44 @@ int distill_split(const Distill& p, const Split& sp, hipStream_t s) {
   return check_launch("k_distill_join");
 }
 
-// Workgroups: as many as are resident at once at most (each goes through its rows).
+// Workgroups of 1024 threads: as many as are resident at once, each going through its rows;
+// smaller ones: one to a row, several to a compute unit (4096 x 32000 bf16: 111.8 us, going
+// through rows 117.6; 4096 x 30000, loss alone: 50.6 against 56.5).
 template <int CD, int TPB, int NV, int KC>
 void launch_rows(const Distill& p, int per_cu, hipStream_t s) {
-  const int64_t g = std::min<int64_t>(p.n, (int64_t)per_cu * cu_count());
+  const int64_t g = TPB < 1024 ? p.n : std::min<int64_t>(p.n, (int64_t)per_cu * cu_count());
   k_distill<CD, TPB, NV, KC><<<dim3((unsigned)g), dim3(TPB), 0, s>>>(p);
 }
 
-// Threads and registers for a row of `chunks` 16-byte chunks.  With fewer rows than
-// compute units a row gets 1024 threads as soon as 256 would need more than four chunks
-// each.
+// Threads and registers for a row of `chunks` 16-byte chunks.  With a gradient the row is kept
+// where registers hold it: a wave for each of very many short rows (8192 x 2678 bf16: 31.0
+// against 41.4 us; 1216 x 4000: 12.5 against 11.1), 256 threads (several rows to a compute
+// unit), then 1024; with no more rows than compute units 1024 from four chunks each on.  The loss alone
+// reads a row once either way and does better with small workgroups that hold nothing
+// (4096 x 128000 bf16: 199 against 278 us, 1024 x 32000: 20.7 against 27.6).
 template <int CD>
 int distill_rows(const Distill& p, hipStream_t s) {
   const int64_t chunks = p.V / Elem<CD>::PC;
   const bool few = p.n <= cu_count(), slots = p.k <= kFewSlots;
-  if (chunks <= 256 * 4) {
-    if (slots) launch_rows<CD, 256, 4, kFewSlots>(p, 5, s);
-    else launch_rows<CD, 256, 4, kMaxK>(p, 3, s);
+  if (chunks <= 64 * 8 && slots && p.n >= 8 * cu_count()) {
+    launch_rows<CD, 64, 8, kFewSlots>(p, 1, s);
+  } else if (chunks <= 256 * 4) {
+    if (slots) launch_rows<CD, 256, 4, kFewSlots>(p, 1, s);
+    else launch_rows<CD, 256, 4, kMaxK>(p, 1, s);
+  } else if (!p.dz && few) {
+    launch_rows<CD, 1024, 0, kMaxK>(p, 1, s);
+  } else if (!p.dz) {
+    if (slots) launch_rows<CD, 256, 0, kFewSlots>(p, 1, s);
+    else launch_rows<CD, 256, 0, kMaxK>(p, 1, s);
   } else if (chunks <= 256 * 16 && !few) {
-    if (slots) launch_rows<CD, 256, 16, kFewSlots>(p, 3, s);
-    else launch_rows<CD, 256, 16, kMaxK>(p, 3, s);
+    if (slots && chunks <= 256 * 8) launch_rows<CD, 256, 8, kFewSlots>(p, 1, s);
+    else if (slots) launch_rows<CD, 256, 16, kFewSlots>(p, 1, s);
+    else launch_rows<CD, 256, 16, kMaxK>(p, 1, s);
   } else if (chunks <= 1024 * 4) launch_rows<CD, 1024, 4, kMaxK>(p, 1, s);
   else if (chunks <= 1024 * 8) launch_rows<CD, 1024, 8, kMaxK>(p, 1, s);
   else if (chunks <= 1024 * 16) launch_rows<CD, 1024, 16, kMaxK>(p, 1, s);
   else if (chunks <= 1024 * 20) launch_rows<CD, 1024, 20, kMaxK>(p, 1, s);
-  else launch_rows<CD, 1024, 0, kMaxK>(p, 1, s);
+  else launch_rows<CD, 1024, 0, kMaxK>(p, 2, s);
   return check_launch("k_distill");
 }
 

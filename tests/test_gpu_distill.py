@@ -125,7 +125,7 @@ def test_loss_and_gradient(n, V, k, cd):
 
 
 # Up to 64 long rows are cut into parts; more rows stay whole, in registers or (the longest) read twice.
-WHOLE = [(65, 8200, 16), (257, 9001, 200), (300, 32760, 128), (70, 32768, 30), (66, 65536, 64), (65, 128000, 33),
+WHOLE = [(2100, 1, 1), (2100, 100, 128), (2101, 4099, 40), (2100, 300, 129), (65, 8200, 16), (257, 9001, 200), (300, 16391, 20), (300, 32760, 128), (270, 20000, 130), (70, 32768, 30), (66, 65536, 64), (65, 128000, 33),
          (65, 150001, 12), (65, 170007, 5)]
 
 
@@ -140,6 +140,7 @@ def test_whole_rows(n, V, k, cd):
     idx[5:8] = -1
     idx[9, : k // 2] = idx[9, k // 2]
     check(z, u, idx, T=0.9, w=w, in_place=n % 2 == 0)
+    check(z, u, idx, T=0.9, w=w, grad=False)
 
 
 @pytest.mark.parametrize("V", [8300, 40000, 120001, 171000])
