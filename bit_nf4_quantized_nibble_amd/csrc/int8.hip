@@ -100,26 +100,21 @@ struct __attribute__((packed, aligned(ES))) Chunk {
   u32x4_t v;
 };
 
-// 8 consecutive elements of a row from column k on, 0 past the last column.
+// 8 consecutive elements of a row from column k on.
 template <int CD>
-__device__ __forceinline__ void load8(const void* x, int64_t at, int64_t k, int64_t cols, float (&v)[8]) {
-  if (k + 8 <= cols) {
-    if constexpr (CD == CD_F32) {
-      const u32x4_t a = ((const Chunk<4>*)((const float*)x + at + k))->v;
-      const u32x4_t b = ((const Chunk<4>*)((const float*)x + at + k + 4))->v;
+__device__ __forceinline__ void load8(const void* x, int64_t at, float (&v)[8]) {
+  if constexpr (CD == CD_F32) {
+    const u32x4_t a = ((const Chunk<4>*)((const float*)x + at))->v;
+    const u32x4_t b = ((const Chunk<4>*)((const float*)x + at + 4))->v;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] = __uint_as_float(a[e]);
-        v[4 + e] = __uint_as_float(b[e]);
-      }
-    } else {
-      const u32x4_t a = ((const Chunk<2>*)((const uint16_t*)x + at + k))->v;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = from_cd16<CD>((uint16_t)(a[e >> 1] >> (16 * (e & 1))));
+    for (int e = 0; e < 4; ++e) {
+      v[e] = __uint_as_float(a[e]);
+      v[4 + e] = __uint_as_float(b[e]);
     }
   } else {
+    const u32x4_t a = ((const Chunk<2>*)((const uint16_t*)x + at))->v;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = k + e < cols ? load_cd<CD>(x, at + k + e) : 0.f;
+    for (int e = 0; e < 8; ++e) v[e] = from_cd16<CD>((uint16_t)(a[e >> 1] >> (16 * (e & 1))));
   }
 }
 
@@ -129,43 +124,53 @@ __device__ __forceinline__ uint32_t amax8(const float (&v)[8], uint32_t m) {
   return m;
 }
 
-// Eight codes.  x rcp(s) is within 127 * 3 * 2^-24 < 2.4e-5 of the quotient, so where it lies
-// further than 1e-4 from the middle between two integers it rounds to the same integer; the
-// sum with 1.5 * 2^23 does that rounding and leaves the code in the low byte.  A group with
-// an element nearer to a middle (1 in 600) divides, as does a row whose scale the
-// reciprocal does not take (below 2^-100: the quotient's bound needs a normal rcp).  A
-// division for every element took 18.6 instead of 12 us on 4096 x 4096 bf16.
-__device__ __forceinline__ u32x2_t codes8(const float (&v)[8], float s) {
-  u32x2_t o = {0u, 0u};
-  if (!(s > 0.f)) return o;
-  const float r = __builtin_amdgcn_rcpf(s);
-  float far = 0.f;
-  uint32_t t[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float q = v[e] * r, sum = q + 12582912.f;
-    far = fmaxf(far, fabsf(q - (sum - 12582912.f)));
-    t[e] = __float_as_uint(sum);
-  }
-  if (far > 0.4999f || s < 0x1p-100f) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) t[e] = (uint32_t)code_of(v[e], s);
-  }
+// Eight codes without a division: with r = RN(1 / s), two steps q <- q + (x - q s) r, each a
+// remainder that is exact in one fused multiply-add, turn x r into the correctly rounded
+// quotient (P. Markstein's theorem on division by fused multiply-add, 1990: a correctly rounded
+// reciprocal and a quotient within one ulp give it in one step; the first brings the quotient
+// there).  The sum with 1.5 * 2^23 then rounds to the nearest integer, ties to even, and
+// leaves the code in the low byte.  Ties are common in 16-bit rows (half the largest value has
+// the quotient 63.5), so nothing that treats them apart is cheap: 4096 x 4096 bf16 takes
+// 18.6 us with divisions, 16.7 with divisions only near ties, 11.5 so.
+// A row with a scale below 2^-100, whose remainders might not be exact, is divided (r is NaN).
+__device__ __forceinline__ float scale_rcp(float s) {
+  return s >= 0x1p-100f ? __fdiv_rn(1.0f, s) : __uint_as_float(0x7fc00000u);
+}
+__device__ __forceinline__ u32x2_t pack_codes(const uint32_t (&t)[8]) {
+  u32x2_t o;
 #pragma unroll
   for (int e = 0; e < 8; e += 4)
     o[e >> 2] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(t[e + 3], t[e + 2], 0x0c0c0400u),
                                       __builtin_amdgcn_perm(t[e + 1], t[e], 0x0c0c0400u), 0x05040100u);
   return o;
 }
+__device__ __forceinline__ u32x2_t codes8(const float (&v)[8], float s, float r) {
+  uint32_t t[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    float q = v[e] * r;
+    q = fmaf(fmaf(-q, s, v[e]), r, q);
+    q = fmaf(fmaf(-q, s, v[e]), r, q);
+    t[e] = __float_as_uint(q + 12582912.f);
+  }
+  return pack_codes(t);
+}
+__device__ __forceinline__ u32x2_t codes8_by_division(const float (&v)[8], float s) {
+  uint32_t t[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) t[e] = s > 0.f ? (uint32_t)code_of(v[e], s) : 0u;
+  return pack_codes(t);
+}
 
 // Codes and scales of rows, TPR threads to a row.  The row stays in registers between the
-// maximum and the codes (up to kHold runs of 8 elements per thread; longer rows are read
-// again, from the caches): one pass over x.  The workgroup after the last row forms the
-// experts' route (r.starts set), so that it costs no launch of its own.
-constexpr int kHold = 8;
-template <int CD, int TPR>
+// maximum and the codes (up to HOLD groups of 8 elements per thread; the rest is read again,
+// from the caches).  The columns past the last whole group go one to a thread.  Most threads
+// run this code once, so its size counts as its registers do: held groups are unrolled.
+// The workgroup after the last row forms the experts' route (r.starts set), so that it costs
+// no launch of its own.
+template <int CD, int TPR, int HOLD>
 __global__ __launch_bounds__(kThreads) void k_int8_rows(const void* __restrict__ x, int64_t ldx, int64_t rows,
-                                                        int64_t cols, int64_t ld, int8_t* __restrict__ codes,
+                                                        int cols, int ld, int8_t* __restrict__ codes,
                                                         float* __restrict__ scale, Route r) {
   __shared__ uint32_t red[kThreads / 64];
   const int64_t row = (int64_t)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
@@ -176,22 +181,24 @@ __global__ __launch_bounds__(kThreads) void k_int8_rows(const void* __restrict__
   const int t = threadIdx.x % TPR;
   const bool live = row < rows;
   const int64_t at = row * ldx;
-  float v[kHold][8];
+  const int groups = cols / 8, rest = cols % 8;
+  float v[HOLD][8], last = 0.f;
   uint32_t amax = 0;
   if (live) {
 #pragma unroll
-    for (int i = 0; i < kHold; ++i) {
-      const int64_t k = 8 * (t + (int64_t)i * TPR);
-      if (k < cols) load8<CD>(x, at, k, cols, v[i]);
-    }
+    for (int i = 0; i < HOLD; ++i)
+      if (t + i * TPR < groups) load8<CD>(x, at + 8 * (t + i * TPR), v[i]);
+    if (t < rest) last = load_cd<CD>(x, at + 8 * groups + t);
 #pragma unroll
-    for (int i = 0; i < kHold; ++i)
-      if (8 * (t + (int64_t)i * TPR) < cols) amax = amax8(v[i], amax);
-    for (int64_t k = 8 * (t + (int64_t)kHold * TPR); k < cols; k += 8 * TPR) {
+    for (int i = 0; i < HOLD; ++i)
+      if (t + i * TPR < groups) amax = amax8(v[i], amax);
+#pragma unroll 1
+    for (int g = t + HOLD * TPR; g < groups; g += TPR) {
       float w[8];
-      load8<CD>(x, at, k, cols, w);
+      load8<CD>(x, at + 8 * g, w);
       amax = amax8(w, amax);
     }
+    amax = max(amax, __float_as_uint(last) & 0x7fffffffu);
   }
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) amax = max(amax, (uint32_t)__shfl_xor((int)amax, off, 64));
@@ -202,20 +209,26 @@ __global__ __launch_bounds__(kThreads) void k_int8_rows(const void* __restrict__
     amax = max(max(red[0], red[1]), max(red[2], red[3]));
   }
   if (!live) return;
-  const float s = scale_of_bits(amax);
+  const float s = scale_of_bits(amax), rcp = scale_rcp(s);
   if (t == 0) scale[row] = s;
   int8_t* dst = codes + row * ld;
+  if (rcp == rcp) {
 #pragma unroll
-  for (int i = 0; i < kHold; ++i) {
-    const int64_t k = 8 * (t + (int64_t)i * TPR);
-    if (k < cols) *(u32x2_t*)(dst + k) = codes8(v[i], s);
-    else if (k < ld) *(u32x2_t*)(dst + k) = u32x2_t{0u, 0u};
+    for (int i = 0; i < HOLD; ++i)
+      if (t + i * TPR < groups) *(u32x2_t*)(dst + 8 * (t + i * TPR)) = codes8(v[i], s, rcp);
   }
-  for (int64_t k = 8 * (t + (int64_t)kHold * TPR); k < ld; k += 8 * TPR) {
+  // the groups that were not held; all of them, divided, under a scale near zero (or no number)
+#pragma unroll 1
+  for (int g = rcp == rcp ? t + HOLD * TPR : t; g < groups; g += TPR) {
     float w[8];
-    if (k < cols) load8<CD>(x, at, k, cols, w);
-    *(u32x2_t*)(dst + k) = k < cols ? codes8(w, s) : u32x2_t{0u, 0u};
+    load8<CD>(x, at + 8 * g, w);
+    u32x2_t o;
+    if (rcp == rcp) o = codes8(w, s, rcp);
+    else o = codes8_by_division(w, s);
+    *(u32x2_t*)(dst + 8 * g) = o;
   }
+  if (t < 8 && 8 * groups + t < ld) dst[8 * groups + t] = (int8_t)(t < rest && s > 0.f ? code_of(last, s) : 0);
+  for (int z = groups + 1 + t; z < ld / 8; z += TPR) *(u32x2_t*)(dst + 8 * z) = u32x2_t{0u, 0u};
 }
 
 // ------------------------------------------------------------------------- product
@@ -748,10 +761,13 @@ __global__ __launch_bounds__(64 * NWV) void k_int8_few(I8 p, const int32_t* __re
     if (tid < 4) *(uint32_t*)(tok + kFuseBytes + tid * 4) = 0u;  // what the other 15 columns read
     float v[8];
     uint32_t amax = 0;
-    for (int k = 8 * tid; k < (int)raw.cols; k += 8 * NT) {
-      load8<CD>(raw.x, 0, k, raw.cols, v);
+    const int groups = (int)raw.cols / 8, rest = (int)raw.cols % 8;
+    for (int g = tid; g < groups; g += NT) {
+      load8<CD>(raw.x, 8 * g, v);
       amax = amax8(v, amax);
     }
+    const float last = tid < rest ? load_cd<CD>(raw.x, 8 * groups + tid) : 0.f;
+    amax = max(amax, __float_as_uint(last) & 0x7fffffffu);
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) amax = max(amax, (uint32_t)__shfl_xor((int)amax, o, 64));
     if (lane == 0) tmax[wave] = amax;
@@ -759,14 +775,18 @@ __global__ __launch_bounds__(64 * NWV) void k_int8_few(I8 p, const int32_t* __re
 #pragma unroll
     for (int x = 0; x < NWV; ++x) amax = max(amax, tmax[x]);
     fscale = scale_of_bits(amax);
-    for (int k = 8 * tid; k < ld; k += 8 * NT) {
+    const float rcp = scale_rcp(fscale);
+    for (int g = tid; g < ld / 8; g += NT) {
       u32x2_t c = {0u, 0u};
-      if (k < raw.cols) {
-        load8<CD>(raw.x, 0, k, raw.cols, v);
-        c = codes8(v, fscale);
+      if (g < groups) {
+        load8<CD>(raw.x, 8 * g, v);
+        if (rcp == rcp) c = codes8(v, fscale, rcp);
+        else c = codes8_by_division(v, fscale);
       }
-      *(u32x2_t*)(tok + k) = c;
+      if (g != groups) *(u32x2_t*)(tok + 8 * g) = c;
     }
+    if (tid < 8 && 8 * groups + tid < ld)
+      tok[8 * groups + tid] = (char)(tid < rest && fscale > 0.f ? code_of(last, fscale) : 0);
     __syncthreads();
   }
   for (int64_t m0 = first; m0 < end; m0 += 16) {
@@ -907,23 +927,26 @@ Plan plan_int8(const qlora_int8_t* w, int64_t m, bool grouped) {
   return P;
 }
 
-template <int CD, int TPR>
+template <int CD, int TPR, int HOLD>
 int launch_rows(const void* x, int64_t ldx, int64_t rows, int64_t cols, int8_t* codes, float* scale, const Route& r,
                 hipStream_t s) {
-  const int64_t ld = QLORA_INT8_LD(cols);
+  const int ld = (int)QLORA_INT8_LD(cols);
   const dim3 g((unsigned)(ceil_div(rows, kThreads / TPR) + (r.starts ? 1 : 0))), b(kThreads);
-  k_int8_rows<CD, TPR><<<g, b, 0, s>>>(x, ldx, rows, cols, ld, codes, scale, r);
+  k_int8_rows<CD, TPR, HOLD><<<g, b, 0, s>>>(x, ldx, rows, (int)cols, ld, codes, scale, r);
   return check_launch("k_int8_rows");
 }
 
-// A wave per row where that fills the chip and the row fits its registers, else a
-// workgroup per row.
+// A wave per row where rows are short, or enough to fill the chip and not long, else a
+// workgroup per row.  Holding two groups to a thread (and reading what exceeds them again)
+// beats holding eight for all but long rows: 8192 x 4096 bf16 17.9 against 20.6 us, 16 x 4096
+// 3.5 against 3.8, but 4096 x 14336 41.2 against 34.1.
 template <int CD>
 int rows_cd(const void* x, int64_t ldx, int64_t rows, int64_t cols, int8_t* codes, float* scale, const Route& r,
             hipStream_t s) {
-  if (cols <= 512 || (rows >= 4 * cu_count() && cols <= 64 * 8 * kHold))
-    return launch_rows<CD, 64>(x, ldx, rows, cols, codes, scale, r, s);
-  return launch_rows<CD, kThreads>(x, ldx, rows, cols, codes, scale, r, s);
+  if (cols <= 512 || (rows >= 4 * cu_count() && cols <= 4096))
+    return launch_rows<CD, 64, 2>(x, ldx, rows, cols, codes, scale, r, s);
+  if (cols <= 4096) return launch_rows<CD, kThreads, 2>(x, ldx, rows, cols, codes, scale, r, s);
+  return launch_rows<CD, kThreads, 8>(x, ldx, rows, cols, codes, scale, r, s);
 }
 
 int rows_to_int8(int cd, const void* x, int64_t ldx, int64_t rows, int64_t cols, int8_t* codes, float* scale,

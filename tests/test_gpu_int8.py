@@ -50,6 +50,30 @@ def test_codes_and_scales(rows, cols, cd):
     assert not to_np(q.codes)[0, :, cols:].any()
 
 
+@pytest.mark.parametrize("cd", ["f32", "bf16", "f16"])
+def test_codes_next_to_the_middle(cd):
+    """Values at, just below and just above the middle between two codes, under many scales:
+    the quotient's rounding to binary32 decides."""
+    say("codes: next to the middle", cd)
+    g = torch.Generator().manual_seed(5)
+    rows = 3000
+    amax = torch.randn(rows, generator=g).abs().add(0.01) * torch.pow(10.0, torch.randint(-4, 4, (rows,), generator=g))
+    amax = amax.to(TORCH_DT[cd]).float()
+    scale = amax / 127
+    mid = (torch.arange(-127, 127).float() + 0.5)[None, :] * scale[:, None]
+    steps = [mid, torch.nextafter(mid, mid * 2), torch.nextafter(mid, mid * 0)]
+    w = torch.cat([amax[:, None]] + steps + [amax[:, None] * 0.5, amax[:, None] * 0.25], 1).to(TORCH_DT[cd])
+    w = w.float().clamp(-amax[:, None], amax[:, None]).to(TORCH_DT[cd])
+    q = qn.quantize_int8(w.cuda())
+    codes, sc = oi.rows_to_int8(to_np(w))
+    assert np.array_equal(to_np(q.scale)[0], sc)
+    assert np.array_equal(to_np(q.codes)[0, :, :w.shape[1]], codes)
+    x = w[:1].cuda()  # the same by the launch that takes one token
+    y = qn.linear_int8(qn.quantize_int8(torch.eye(w.shape[1], device="cuda")), x)
+    one = to_np(y)[0].astype(np.float64) / float(sc[0])
+    assert np.abs(one - codes[0]).max() <= 127 * (torch.finfo(TORCH_DT[cd]).eps + 2.0 ** -22)
+
+
 def test_codes_at_ties_and_extremes():
     say("codes: ties and extremes")
     t = 2.0 ** -149
