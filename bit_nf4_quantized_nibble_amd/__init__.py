@@ -558,6 +558,10 @@ class Int8Weight:
         return self.codes.shape[0]
 
     @property
+    def shape(self) -> Tuple[int, ...]:
+        return (self.rows, self.cols) if self.experts == 1 else (self.experts, self.rows, self.cols)
+
+    @property
     def device(self):
         return self.codes.device
 
@@ -567,6 +571,13 @@ class Int8Weight:
     def descriptor(self) -> QloraInt8:
         made = self.__dict__.get("_made")
         if made is None or made[0] is not self.codes or made[1] is not self.scale:
+            torch = _torch()
+            ld = (self.cols + 127) // 128 * 128
+            for name, t, dt, shape in (("codes", self.codes, torch.int8, (self.experts, self.rows, ld)),
+                                       ("scale", self.scale, torch.float32, (self.experts, self.rows))):
+                if t.dtype != dt or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda or \
+                        t.device != self.codes.device:
+                    raise ValueError("%s must be a contiguous %s GPU tensor of shape %s" % (name, dt, shape))
             d = QloraInt8(self.rows, self.cols, self.experts, 0, _ptr(self.codes), _ptr(self.scale))
             made = self.__dict__["_made"] = (self.codes, self.scale, d)
         return made[2]

@@ -794,8 +794,8 @@ int qlora_distill_loss_grad(const void* logits, int64_t n, int64_t vocab, int64_
     return set_error(QLORA_ERR_UNSUPPORTED, "%s: k = %d (at most %d)", who, k, QLORA_DISTILL_MAX_K);
   if (n >= (1LL << 31) || vocab >= (1LL << 31))
     return set_error(QLORA_ERR_UNSUPPORTED, "%s: 2^31 rows or vocabulary entries, or more", who);
-  if (!(temperature > 0.f) || !isfinite(temperature))
-    return set_error(QLORA_ERR_INVALID_ARG, "%s: temperature %g must be positive and finite", who, temperature);
+  if (!(temperature >= 1e-6f && temperature <= 1e6f))  // T^2 and 1 / T stay well inside fp32
+    return set_error(QLORA_ERR_INVALID_ARG, "%s: temperature %g outside [1e-6, 1e6]", who, temperature);
   if (index_bits != 32 && index_bits != 64)
     return set_error(QLORA_ERR_INVALID_ARG, "%s: index_bits %d (32 or 64)", who, index_bits);
   if (!loss || !aligned_to(loss, 4)) return set_error(QLORA_ERR_INVALID_ARG, "%s: null or unaligned loss", who);

@@ -49,6 +49,10 @@ struct Route {
   int64_t m;
 };
 
+// Tile i of expert e's n rows from `start` on.
+__device__ __forceinline__ void put_tile(const Route& r, int at, int e, int start, int n, int i) {
+  if (at < r.cap) r.tiles[at] = make_int4(e, start + i * r.tile_m, min(r.tile_m, n - i * r.tile_m), 0);
+}
 // By one wave: running maximum and running sum over 64 experts at a time.
 __device__ __forceinline__ void route_experts(const Route& r) {
   const int32_t* offsets = r.offsets;
@@ -84,8 +88,15 @@ __device__ __forceinline__ void route_experts(const Route& r) {
     if (e < experts) {
       r.starts[e + 1] = end;
       const int first = at + sum - t;
-      for (int i = 0; i < t; ++i)
-        if (first + i < r.cap) r.tiles[first + i] = make_int4(e, start + i * tile_m, min(tile_m, n - i * tile_m), 0);
+      if (t <= 4)  // most experts have a few tiles: each lane writes its own
+        for (int i = 0; i < t; ++i) put_tile(r, first + i, e, start, n, i);
+    }
+    // the others by the whole wave
+    for (uint64_t many = __ballot(e < experts && t > 4); many; many &= many - 1) {
+      const int l = (int)__builtin_ctzll(many);
+      const int le = e0 + l, ls = __shfl(start, l, 64), ln = __shfl(n, l, 64), lt = __shfl(t, l, 64);
+      const int lf = at + __shfl(sum, l, 64) - lt;
+      for (int i = lane; i < lt; i += 64) put_tile(r, lf + i, le, ls, ln, i);
     }
     before = __shfl(end, 63, 64);
     at += __shfl(sum, 63, 64);

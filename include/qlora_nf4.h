@@ -508,7 +508,7 @@ size_t qlora_int8_workspace_bytes(const qlora_int8_t* w, int64_t m, int32_t grou
  * only) may be z itself with ldd = ld; any other overlap with z is refused.  Statistics and sums are fp32 (the sum over the rows
  * fp64) in a fixed order.  n == 0 writes loss = 0.
  * ws: qlora_distill_workspace_bytes(n, vocab, k, cd) bytes, 256-byte aligned.
- * Errors: QLORA_ERR_INVALID_ARG (null pointers, T not positive and finite, index_bits not 32
+ * Errors: QLORA_ERR_INVALID_ARG (null pointers, T outside [1e-6, 1e6], index_bits not 32
  * or 64, pointers that are not element-aligned), QLORA_ERR_SHAPE (n < 0, vocab < 1, k < 1,
  * ld or ldd < vocab), QLORA_ERR_DTYPE, QLORA_ERR_WORKSPACE, QLORA_ERR_UNSUPPORTED
  * (k > QLORA_DISTILL_MAX_K, n or vocab of 2^31 or more).

@@ -102,7 +102,7 @@ def distill(lib, z=FAKE, n=4, vocab=100, ld=100, cd=1, u=FAKE, td=0, idx=FAKE, b
     (dict(z=FAKE + 1), INVALID), (dict(dz=FAKE + 4097), INVALID), (dict(u=FAKE + 2), INVALID),
     (dict(idx=FAKE + 4, bits=64), INVALID), (dict(w=FAKE + 2), INVALID), (dict(kl=FAKE + 1), INVALID),
     (dict(loss=FAKE + 2), INVALID), (dict(bits=16), INVALID), (dict(t=0.0), INVALID), (dict(t=-1.0), INVALID),
-    (dict(t=float("nan")), INVALID), (dict(t=float("inf")), INVALID), (dict(n=-1), SHAPE), (dict(vocab=0), SHAPE),
+    (dict(t=float("nan")), INVALID), (dict(t=float("inf")), INVALID), (dict(t=9e-7), INVALID), (dict(t=2e6), INVALID), (dict(n=-1), SHAPE), (dict(vocab=0), SHAPE),
     (dict(k=0), SHAPE), (dict(ld=99), SHAPE), (dict(ldd=99), SHAPE), (dict(cd=3), DTYPE), (dict(td=-1), DTYPE),
     (dict(dz=FAKE + 200), INVALID), (dict(z=FAKE + 4296), INVALID), (dict(dz=FAKE, z=FAKE, ldd=108), INVALID),
     (dict(z=FAKE, dz=FAKE + 198, ld=200, ldd=200), INVALID), (dict(z=FAKE, dz=FAKE + 202, ld=200, ldd=200), INVALID),

@@ -149,6 +149,24 @@ def test_largest_sums_do_not_overflow(m):
     check(torch.from_numpy(y).bfloat16(), ref, mag, "bf16")
 
 
+@pytest.mark.parametrize("k", [300, 5000])
+def test_one_token_that_is_zero_or_not_finite(k):
+    say("one special token", k)
+    _, w, b = tensors(1, 40, k, "bf16", k, bias=True)
+    q = qn.quantize_int8(w.cuda())
+    x = torch.zeros(1, k, dtype=torch.bfloat16)
+    assert torch.equal(qn.linear_int8(q, x.cuda(), bias=b.cuda()).cpu()[0], b)
+    for at, v in ((0, "nan"), (k - 1, "inf"), (k // 2, "-inf")):
+        x = torch.ones(1, k, dtype=torch.bfloat16)
+        x[0, at] = float(v)
+        assert np.isnan(to_np(qn.linear_int8(q, x.cuda(), bias=b.cuda()))).all()
+    x = torch.zeros(1, k)
+    x[0, 5], x[0, 6] = 190 * 2.0 ** -149, -2.0 ** -149   # a scale of one subnormal step
+    qf = qn.quantize_int8(w.float().cuda() * 1e30)
+    ref, mag = oi.product(to_np(x), to_np(qf.codes)[0, :, :k], to_np(qf.scale)[0])
+    check(qn.linear_int8(qf, x.cuda()), ref, mag, "f32")
+
+
 @pytest.mark.parametrize("m", [3, 100, 600])
 def test_rows_that_are_zero_or_not_finite(m):
     say("special rows", m)
@@ -209,6 +227,9 @@ def check_experts(sizes, n, k, cd, seed, bias=False, before=0, tail=0, offsets=N
     x, w, b = tensors(m, n, k, cd, seed, experts=E, bias=bias)
     q = qn.quantize_int8(w.cuda())
     off = np.r_[0, np.cumsum(sizes)] + before if offsets is None else np.asarray(offsets)
+    covered = oi.clean_offsets(off, m)
+    x[: covered[0]] = float("nan")  # rows of no expert: whatever they hold
+    x[covered[-1]:] = float("inf")
     keep = torch.randn(m, n, generator=torch.Generator().manual_seed(1)).to(TORCH_DT[cd])
     out = keep.cuda()
     y = qn.linear_int8_experts(q, x.cuda(), torch.tensor(off, dtype=torch.int32, device="cuda"),
@@ -257,6 +278,14 @@ def test_many_experts(E, m):
 def test_offsets_out_of_order_or_range(offsets):
     say("offsets", offsets)
     check_experts([25, 25, 25, 25], 90, 150, "bf16", 3, offsets=offsets)
+
+
+def test_long_runs_of_tiles():
+    """Experts with many tiles between experts with one or none (the route is written by lane or
+    by the whole wave)."""
+    say("long runs of tiles")
+    check_experts([1500, 0, 3, 2600, 1, 700, 0, 0, 64, 257], 40, 130, "bf16", 12, before=3, tail=2)
+    check_experts([5] * 30 + [900, 0, 1200] + [7] * 60 + [400], 40, 130, "bf16", 13)
 
 
 def test_all_rows_to_one_expert_of_many():
@@ -340,6 +369,9 @@ def test_python_refusals():
         (lambda: qn.quantize_int8(torch.zeros(8, 16, dtype=torch.int32, device="cuda")), TypeError),
         (lambda: qn.quantize_int8(torch.zeros(1, 131073, device="cuda")), qn.QloraError),
         (lambda: qn.linear_int8(qe, x), ValueError),
+        (lambda: qn.linear_int8(qn.Int8Weight(8, 16, q.codes[:, :, :16].contiguous(), q.scale), x), ValueError),
+        (lambda: qn.linear_int8(qn.Int8Weight(8, 16, q.codes, q.scale.double()), x), ValueError),
+        (lambda: qn.linear_int8(qn.Int8Weight(9, 16, q.codes, q.scale), x), ValueError),
         (lambda: qn.linear_int8(q, x[:, :15]), ValueError),
         (lambda: qn.linear_int8(q, x.cpu()), ValueError),
         (lambda: qn.linear_int8(q, x.double()), TypeError),
