@@ -52,7 +52,17 @@ def _torch():
     return torch
 
 
+_dtype_codes = {}
+
+
 def dtype_code(dtype) -> int:
+    code = _dtype_codes.get(dtype)
+    if code is None:
+        code = _dtype_codes[dtype] = _find_dtype_code(dtype)
+    return code
+
+
+def _find_dtype_code(dtype) -> int:
     torch = _torch()
     if dtype == torch.float32:
         return _lib.QLORA_F32

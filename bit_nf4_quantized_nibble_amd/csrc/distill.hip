@@ -698,9 +698,10 @@ void launch_rows(const Distill& p, int per_cu, hipStream_t s) {
 // Threads and registers for a row of `chunks` 16-byte chunks.  With a gradient the row is kept
 // where registers hold it: a wave for each of very many short rows (8192 x 2678 bf16: 31.0
 // against 41.4 us; 1216 x 4000: 12.5 against 11.1), 256 threads (several rows to a compute
-// unit), then 1024; with no more rows than compute units 1024 from four chunks each on.  The loss alone
-// reads a row once either way and does better with small workgroups that hold nothing
-// (4096 x 128000 bf16: 199 against 278 us, 1024 x 32000: 20.7 against 27.6).
+// unit), 512 (two: 2000 x 50000 bf16 87.6 us, 106.5 with one of 1024), then 1024; with no
+// more rows than compute units 1024 from four chunks each on.  The loss alone reads a row
+// once either way and does better with small workgroups that hold nothing (4096 x 128000 bf16:
+// 187 against 278 us, 1024 x 32000: 20.7 against 27.6).
 template <int CD>
 int distill_rows(const Distill& p, hipStream_t s) {
   const int64_t chunks = p.V / Elem<CD>::PC;
@@ -719,6 +720,9 @@ int distill_rows(const Distill& p, hipStream_t s) {
     if (slots && chunks <= 256 * 8) launch_rows<CD, 256, 8, kFewSlots>(p, 1, s);
     else if (slots) launch_rows<CD, 256, 16, kFewSlots>(p, 1, s);
     else launch_rows<CD, 256, 16, kMaxK>(p, 1, s);
+  } else if (chunks <= 512 * 16 && !few) {
+    if (slots) launch_rows<CD, 512, 16, kFewSlots>(p, 1, s);
+    else launch_rows<CD, 512, 16, kMaxK>(p, 1, s);
   } else if (chunks <= 1024 * 4) launch_rows<CD, 1024, 4, kMaxK>(p, 1, s);
   else if (chunks <= 1024 * 8) launch_rows<CD, 1024, 8, kMaxK>(p, 1, s);
   else if (chunks <= 1024 * 16) launch_rows<CD, 1024, 16, kMaxK>(p, 1, s);

@@ -895,19 +895,22 @@ struct Plan {
 //   128 of 8 (4096 x 4096)           65.8     64.7       63.5       53.3       63.0
 //   192 of 8 (14336 x 4096)           249      203        173        155        174
 //   256 of 8 (4096 x 4096)           96.5     86.1       83.2       83.0       74.2
+// Long rows of few outputs leave the few-token kernel with few workgroups; the smallest tiles
+// cut the contraction (16 x 512 x 16384 22.6 -> 16.0 us, 4 x 1024 x 14336 20.3 -> 17.5, 2 x 64 x
+// 131072 113 -> 72; but 16 x 256 x 4096 9.0 -> 10.7, 4 x 4096 x 8192 15.4 -> 17.3).
 // An uneven routing gives some experts several times the average, and the few-token
 // kernel goes over its weights again for each 16 rows, so experts leave it early.
 enum Form { FEW, SMALL, LOW, MID, WIDE, FULL };
-Form form_of(int64_t m, int64_t n, int32_t experts) {
+Form form_of(int64_t m, int64_t n, int64_t ld, int32_t experts) {
   const int64_t live = std::max<int64_t>(1, std::min<int64_t>(experts, m)), cus = cu_count();
-  if (m <= (experts == 1 ? 16 : 4 * live)) return FEW;
+  if (m <= (experts == 1 ? 16 : 4 * live)) return experts == 1 && ld > 8192 && n <= 2048 ? SMALL : FEW;
   // tile rows: each expert's last one is half full on average
   auto one_round = [&](int64_t tm, int64_t tn) {
     return (experts == 1 ? ceil_div(m, tm) : std::max(live, m / tm + (live + 1) / 2)) * ceil_div(n, tn) <= cus;
   };
   if (one_round(64, 64)) return SMALL;
-  if (experts == 1) return one_round(64, 128) ? LOW : one_round(128, 128) ? MID : one_round(128, 256) ? WIDE : FULL;
-  if (m >= 256 * live) return FULL;
+  if (experts == 1 || m >= 256 * live)
+    return one_round(64, 128) ? LOW : one_round(128, 128) ? MID : one_round(128, 256) ? WIDE : FULL;
   return m >= 96 * live ? WIDE : one_round(128, 128) ? MID : LOW;
 }
 static_assert(Wide::TN == Full::TN && Mid::TN == Low::TN && Wide::TM == Mid::TM && Low::TM == Small::TM, "by form");
@@ -979,7 +982,8 @@ int few_rows(const I8& p, int32_t experts, const int32_t* starts, const Raw& raw
   const unsigned gx = (unsigned)ceil_div(p.n, 16 * rb), gy = (unsigned)experts;
   // Four waves; eight for one token over a long contraction on few workgroups (4096 x 14336:
   // 19.5 -> 16.3 us; with more tokens or shorter rows the same or worse).
-  if (FUSE && rb == 1 && p.ld >= 8192) k_int8_few<CD, 1, FUSE ? 8 : 4, FUSE><<<dim3(gx, gy), dim3(512), 0, s>>>(p, starts, raw);
+  constexpr int W = FUSE ? 8 : 4;
+  if (FUSE && rb == 1 && p.ld >= 8192) k_int8_few<CD, 1, W, FUSE><<<dim3(gx, gy), dim3(64 * W), 0, s>>>(p, starts, raw);
   else if (rb == 1) k_int8_few<CD, 1, 4, FUSE><<<dim3(gx, gy), dim3(256), 0, s>>>(p, starts, raw);
   else if (rb == 2) k_int8_few<CD, 2, 4, FUSE><<<dim3(gx, gy), dim3(256), 0, s>>>(p, starts, raw);
   else k_int8_few<CD, 4, 4, FUSE><<<dim3(gx, gy), dim3(256), 0, s>>>(p, starts, raw);
@@ -988,7 +992,7 @@ int few_rows(const I8& p, int32_t experts, const int32_t* starts, const Raw& raw
 
 template <int CD>
 int product(const I8& p, int32_t experts, int cap, const int32_t* starts, hipStream_t s) {
-  const Form f = form_of(p.m, p.n, experts);
+  const Form f = form_of(p.m, p.n, p.ld, experts);
   if (f == FEW) return few_rows<CD, false>(p, experts, starts, Raw{}, s);
   const int tm = tile_rows(f), tn = f >= WIDE ? Full::TN : f >= LOW ? Low::TN : Small::TN;
   const int64_t tiles = (starts ? cap : ceil_div(p.m, tm)) * ceil_div(p.n, tn);
@@ -1047,7 +1051,7 @@ int launch_int8_linear(const qlora_int8_t* w, const void* x, int64_t m, int64_t 
   }
   Route r = {};
   if (offsets) {
-    const Form f = form_of(m, w->rows, w->experts);
+    const Form f = form_of(m, w->rows, p.ld, w->experts);
     const bool tiles = f != FEW;
     r.starts = (int32_t*)(base + P.off_starts);
     r.count = (int32_t*)(base + P.off_count);

@@ -126,7 +126,8 @@ def test_loss_and_gradient(n, V, k, cd):
 
 # Up to 64 long rows are cut into parts; more rows stay whole, in registers or (the longest) read twice.
 WHOLE = [(2100, 1, 1), (2100, 100, 128), (2101, 4099, 40), (2100, 300, 129), (65, 8200, 16), (257, 9001, 200), (300, 16391, 20), (300, 32760, 128), (270, 20000, 130), (70, 32768, 30), (66, 65536, 64), (65, 128000, 33),
-         (65, 150001, 12), (65, 170007, 5)]
+         (65, 150001, 12), (65, 170007, 5),
+         (258, 40000, 30), (257, 65001, 140)]
 
 
 @pytest.mark.parametrize("cd", ["f32", "bf16", "f16"])
