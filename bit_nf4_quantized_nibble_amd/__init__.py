@@ -578,6 +578,9 @@ class Int8Weight:
     def size_bytes(self) -> int:
         return self.codes.numel() + 4 * self.scale.numel()
 
+    def __getstate__(self):  # the descriptor holds addresses: a copy makes its own
+        return {k: v for k, v in self.__dict__.items() if k != "_made"}
+
     def descriptor(self) -> QloraInt8:
         made = self.__dict__.get("_made")
         if made is None or made[0] is not self.codes or made[1] is not self.scale:
@@ -660,7 +663,7 @@ def linear_int8(w: Int8Weight, x, bias=None, out=None, workspace=None):
     """y = x . W^T (+ bias) in 8-bit integers: each row of x gets a scale of its own and is
     brought to 8 bits within the call, the sums are exact, y has x's dtype.  Leading dims of
     x are flattened to tokens; rows of x may be strided.  ``out`` may supply a preallocated
-    output."""
+    output, which must not overlap x."""
     if w.experts != 1:
         raise ValueError("w holds %d experts: linear_int8_experts takes those" % w.experts)
     return _int8_call(w, x, None, bias, out, workspace)

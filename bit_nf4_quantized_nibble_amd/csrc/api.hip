@@ -729,6 +729,10 @@ int int8_impl(const qlora_int8_t* w, const void* x, int64_t m, int64_t ldx, cons
   if (!aligned_to(x, es) || !aligned_to(y, es) || !aligned_to(bias, es))
     return set_error(QLORA_ERR_INVALID_ARG, "%s: x, y and bias must be element-aligned", who);
   if ((rc = check_ws(ws, ws_bytes, int8_workspace_bytes(w, m, offsets != nullptr), who))) return rc;
+  // one token's workgroups read x while others store y already
+  const int64_t ahead = (const char*)y - (const char*)x;
+  if (ahead < ((m - 1) * ldx + w->cols) * es && -ahead < m * w->rows * es)
+    return set_error(QLORA_ERR_INVALID_ARG, "%s: y overlaps x", who);
   return launch_int8_linear(w, x, m, ldx, offsets, bias, cd, y, ws, (hipStream_t)stream);
 }
 }  // namespace

@@ -811,7 +811,7 @@ __global__ __launch_bounds__(64 * NWV) void k_int8_few(I8 p, const int32_t* __re
 #pragma unroll
       for (int i = 0; i < 2 * U; ++i) {
         const int l = l0 + NWV * (i >> 1);
-          if constexpr (FUSE) {
+        if constexpr (FUSE) {
           a[i] = *(const i32x4_t*)(tok + ((lane & 15) == 0 && l < lines ? line_at(l) * 128 + (i & 1) * 64 + (lane >> 4) * 16
                                                                         : kFuseBytes));
         } else {

@@ -455,10 +455,11 @@ int qlora_int8_quantize(const void* w, int64_t ldw, int32_t wd, qlora_int8_t* q,
 /*
  * y [m, rows] = x [m, cols] . W^T (+ bias [rows]) with x (dtype cd, rows ldx elements
  * apart) brought to 8 bits row by row within the call.  w->experts must be 1.  x and y are
- * element-aligned; y is dense and must not overlap the inputs.  m == 0 is a no-op.
+ * element-aligned; y is dense and must not overlap the inputs (memory between x's first and
+ * last element is refused).  m == 0 is a no-op.
  * ws: qlora_int8_workspace_bytes(w, m, 0) bytes, 256-byte aligned.
- * Errors: QLORA_ERR_INVALID_ARG (null or unaligned pointers, experts != 1), QLORA_ERR_SHAPE
- * (m < 0, empty weight, ldx < cols), QLORA_ERR_DTYPE, QLORA_ERR_WORKSPACE,
+ * Errors: QLORA_ERR_INVALID_ARG (null or unaligned pointers, y over x, experts != 1),
+ * QLORA_ERR_SHAPE (m < 0, empty weight, ldx < cols), QLORA_ERR_DTYPE, QLORA_ERR_WORKSPACE,
  * QLORA_ERR_UNSUPPORTED (cols > QLORA_INT8_MAX_COLS, m or experts * rows of 2^31 or more).
  */
 int qlora_int8_linear(const qlora_int8_t* w, const void* x, int64_t m, int64_t ldx, const void* bias,
@@ -505,8 +506,8 @@ size_t qlora_int8_workspace_bytes(const qlora_int8_t* w, int64_t m, int32_t grou
  * have q = 0; where p > 0 meets q = 0 the loss is +inf.  Otherwise a NaN or +inf among a
  * row's logits or teacher values gives NaN.
  * loss: one device float.  row_kl (nullable): fp32 [n], the kl_i.  dlogits (nullable: loss
- * only) may be z itself with ldd = ld; any other overlap with z is refused.  Statistics and sums are fp32 (the sum over the rows
- * fp64) in a fixed order.  n == 0 writes loss = 0.
+ * only) may be z itself with ldd = ld; any other overlap with z is refused.  Statistics and
+ * sums are fp32 (the sum over the rows fp64) in a fixed order.  n == 0 writes loss = 0.
  * ws: qlora_distill_workspace_bytes(n, vocab, k, cd) bytes, 256-byte aligned.
  * Errors: QLORA_ERR_INVALID_ARG (null pointers, T outside [1e-6, 1e6], index_bits not 32
  * or 64, pointers that are not element-aligned), QLORA_ERR_SHAPE (n < 0, vocab < 1, k < 1,

@@ -78,6 +78,10 @@ def test_linear_shapes(lib):
     assert linear(lib, desc(experts=2), grouped=True, offsets=None) == INVALID
     assert linear(lib, desc(experts=2), grouped=True, offsets=FAKE + 2) == INVALID
     assert linear(lib, desc(experts=65536), grouped=True) == UNSUP
+    for grouped in (False, True):  # y over x: at its start, its last element, and x at y's last
+        for m, y in ((5, FAKE), (5, FAKE + 5 * 192 - 2), (5, FAKE - 5 * 128 + 2), (1, FAKE + 190), (1, FAKE - 126)):
+            assert linear(lib, desc(), m=m, y=y, grouped=grouped) == INVALID
+            assert b"overlaps" in lib.qlora_last_error()
     assert linear(lib, desc(), m=0, x=None, y=None, ws=None, ws_bytes=0) == OK
     assert linear(lib, desc(experts=3), m=0, x=None, y=None, ws=None, ws_bytes=0, grouped=True) == OK
 

@@ -136,6 +136,29 @@ def test_product_of_a_large_prompt():
     check(torch.from_numpy(y[rows]).bfloat16(), ref, mag, "bf16")
 
 
+def test_output_over_the_input_is_refused():
+    say("y over x")
+    q = qn.quantize_int8(torch.randn(64, 64, device="cuda"))
+    x = torch.randn(3, 64, device="cuda")
+    kept = x.clone()
+    for part in (slice(0, 1), slice(0, 3)):
+        with pytest.raises(qn.QloraError):
+            qn.linear_int8(q, x[part], out=x[part])
+    torch.cuda.synchronize()
+    assert torch.equal(x, kept)
+
+
+def test_a_used_weight_can_be_copied_and_pickled():
+    import copy
+    import pickle
+    say("copies of a weight")
+    w, x = torch.randn(70, 130, device="cuda"), torch.randn(2, 130, device="cuda")
+    q = qn.quantize_int8(w)
+    y = qn.linear_int8(q, x)
+    for c in (copy.deepcopy(q), copy.copy(q), pickle.loads(pickle.dumps(q))):
+        assert torch.equal(qn.linear_int8(c, x), y)
+
+
 @pytest.mark.parametrize("m", [1, 40, 300])
 def test_largest_sums_do_not_overflow(m):
     """Every code at its limit over the most columns: the sum passes 2^30."""
