@@ -645,12 +645,17 @@ __global__ __launch_bounds__(kPartThreads) void k_distill_join(Distill p, Split 
   }
   if (part != 0) return;
   if (tid == 0) {
-    __hip_atomic_store(&p.kl[i], live ? kl : 0.f, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    s_last = __hip_atomic_fetch_add(sp.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)p.n - 1;
+    // The kl is exchanged, and the count raised once that has answered: both act where every
+    // compute unit sees them, so who counts the last row sees every kl.  (A release would have
+    // the XCD write back all of its L2, gradients included, for each row.)
+    float old = __hip_atomic_exchange(&p.kl[i], live ? kl : 0.f, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    asm volatile("" : "+v"(old)::"memory");
+    __builtin_amdgcn_s_waitcnt(0);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup");
+    s_last = __hip_atomic_fetch_add(sp.done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)p.n - 1;
   }
   __syncthreads();
   if (!s_last || tid >= 64) return;
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
   double acc = 0.0;
   for (int64_t r = tid; r < p.n; r += 64) {
     const float wr = p.weight ? p.weight[r] : p.w_default;
@@ -662,14 +667,20 @@ __global__ __launch_bounds__(kPartThreads) void k_distill_join(Distill p, Split 
   if (tid == 0) sp.loss[0] = (float)acc;
 }
 
-// Rows that are cut into parts: a few long ones.  A row to a workgroup takes 9.7 / 13.5 / 21.6 /
-// 33.7 us at 32000 / 64000 / 128000 / 200000 bf16 whether there are 8 or 64 rows; in parts, 8
-// rows take 9.5 / 9.5 / 10.0 / 11.1 us, 32 rows 13.9 / 16.1 / 15.2 us from 64000 on, and 64
-// rows 20.6 / 26.6 / 24.1 us.
-constexpr int64_t kSplitRows = 64;
+// Rows that are cut into parts: a few long ones, more of them the longer they are (with the
+// gradient; whole rows against rows in parts, us):
+//            32000 bf16   64000 bf16   128000 bf16   250000 bf16   128000 f32   250000 f32
+//   8 rows    9.5   8.9   13.3   9.3   21.7    9.3   39.2   10.7   27.0  10.7   45.7   11.7
+//   32       10.2   9.8   14.2  10.6   22.5   12.5   40.7   16.7   29.4  16.1   54.9   24.3
+//   64       10.3  11.1   14.8  12.8   24.9   17.5   41.7   25.6   33.0  24.7   64.3   39.3
+//   96       10.6  12.4   16.5  14.8   27.0   23.8   49.6   34.8   42.3  33.1   86.3   55.0
+//   160                                                            49.1  47.3    114   95.9
+//   256                                33.4   48.4                 83.5  78.7    159    149
+// The loss alone gains from about the same rows on.
+constexpr int64_t kSplitRows = 256;
 bool split_rows(int64_t n, int64_t V, int cd) {
   const int64_t bytes = V * cd_bytes(cd);
-  return n <= kSplitRows && bytes >= std::max<int64_t>(49152, n * 4096);
+  return n <= kSplitRows && bytes >= std::max<int64_t>(49152, n * (n <= 64 ? 2048 : 4096));
 }
 int64_t parts_of(int64_t V, int cd) { return std::max<int64_t>(1, ceil_div(V * cd_bytes(cd) / 16, kPartChunks)); }
 
@@ -681,8 +692,9 @@ int distill_split(const Distill& p, const Split& sp, hipStream_t s) {
   k_distill_part<CD><<<g, b, 0, s>>>(p, sp);
   const int rc = check_launch("k_distill_part");
   if (rc) return rc;
-  if (p.k <= kPartThreads) k_distill_join<CD, kPartThreads><<<g, b, 0, s>>>(p, sp);
-  else k_distill_join<CD, kMaxK><<<g, b, 0, s>>>(p, sp);
+  const dim3 gj(p.dz ? g.x : 1, g.y);  // the loss alone: what the first part's workgroup does
+  if (p.k <= kPartThreads) k_distill_join<CD, kPartThreads><<<gj, b, 0, s>>>(p, sp);
+  else k_distill_join<CD, kMaxK><<<gj, b, 0, s>>>(p, sp);
   return check_launch("k_distill_join");
 }
 

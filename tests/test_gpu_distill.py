@@ -124,10 +124,10 @@ def test_loss_and_gradient(n, V, k, cd):
     check(z, u, idx, T=1.0, bits=32 if V % 2 else 64)
 
 
-# Up to 64 long rows are cut into parts; more rows stay whole, in registers or (the longest) read twice.
+# Up to 256 long rows are cut into parts; others stay whole, in registers or (the longest) read twice.
 WHOLE = [(2100, 1, 1), (2100, 100, 128), (2101, 4099, 40), (2100, 300, 129), (65, 8200, 16), (257, 9001, 200), (300, 16391, 20), (300, 32760, 128), (270, 20000, 130), (70, 32768, 30), (66, 65536, 64), (65, 128000, 33),
          (65, 150001, 12), (65, 170007, 5),
-         (258, 40000, 30), (257, 65001, 140)]
+         (258, 40000, 30), (257, 65001, 140), (180, 150001, 12), (180, 170007, 5), (256, 262145, 9), (96, 131072, 17)]
 
 
 @pytest.mark.parametrize("cd", ["f32", "bf16", "f16"])
@@ -145,9 +145,9 @@ def test_whole_rows(n, V, k, cd):
 
 
 @pytest.mark.parametrize("V", [8300, 40000, 120001, 171000])
-@pytest.mark.parametrize("n", [64, 65])
+@pytest.mark.parametrize("n", [64, 65, 257])
 def test_special_values_in_long_rows(V, n):
-    """The same rows with few of them (cut into parts) and with one more (whole)."""
+    """The same rows with few of them (cut into parts) and with more (whole)."""
     say("special values", n, V)
     z, u, idx = make(n, V, 8, "bf16", V)
     lowest = torch.finfo(z.dtype).min
