@@ -35,17 +35,17 @@ __device__ __forceinline__ float scale_of_bits(uint32_t amax) {
 }
 
 // ------------------------------------------------------------------------ routing
-// Experts' rows for the product kernels, from the caller's offsets: starts[e] is the
-// largest of offsets[0 .. e], limited to [0, m], so no row belongs to two experts
-// whatever the offsets hold; tiles[t] = {expert, first row, rows, 0} for each run of at
-// most tile_m rows of one expert, in order, `count` of them (at most cap: m / tile_m
-// whole runs and one partial run for each expert that has a row).
+// Experts' rows for the product kernels, from the caller's offsets: expert e's rows end at
+// the largest of offsets[0 .. e + 1], limited to [0, m], and begin where those of the expert
+// before end, so no row belongs to two experts whatever the offsets hold; tiles[t] = {expert,
+// first row, rows, 0} for each run of at most tile_m rows of one expert, in order, `count` of
+// them (at most cap: m / tile_m whole runs and one partial run for each expert that has a
+// row).
 struct Route {
-  int32_t* starts;  // [experts + 1]
   int32_t* count;   // [1]
   int4* tiles;      // [cap]
   const int32_t* offsets;
-  int experts, tile_m, cap;  // cap 0: starts only
+  int experts, tile_m, cap;
   int64_t m;
 };
 
@@ -59,13 +59,12 @@ __device__ __forceinline__ void route_experts(const Route& r) {
   const int experts = r.experts, tile_m = r.tile_m;
   const int64_t m = r.m;
   const int lane = threadIdx.x;
-  int before = 0;  // starts of the chunk's first expert
+  int before = 0;  // where the rows of the chunk's first expert begin
   int at = 0;      // tiles so far
   {
     const int o = offsets[0];
     before = (int)min((int64_t)max(o, 0), m);
   }
-  if (lane == 0) r.starts[0] = before;
   for (int e0 = 0; e0 < experts; e0 += 64) {
     const int e = e0 + lane;
     int end = before;
@@ -78,7 +77,7 @@ __device__ __forceinline__ void route_experts(const Route& r) {
     }
     int start = __shfl_up(end, 1, 64);
     if (lane == 0) start = before;
-    const int n = end - start, t = r.cap ? (n + tile_m - 1) / tile_m : 0;
+    const int n = end - start, t = (int)(((uint32_t)n + (uint32_t)tile_m - 1u) / (uint32_t)tile_m);
     int sum = t;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -86,7 +85,6 @@ __device__ __forceinline__ void route_experts(const Route& r) {
       if (lane >= off) sum += v;
     }
     if (e < experts) {
-      r.starts[e + 1] = end;
       const int first = at + sum - t;
       if (t <= 4)  // most experts have a few tiles: each lane writes its own
         for (int i = 0; i < t; ++i) put_tile(r, first + i, e, start, n, i);
@@ -177,7 +175,7 @@ __device__ __forceinline__ u32x2_t codes8_by_division(const float (&v)[8], float
 // maximum and the codes (up to HOLD groups of 8 elements per thread; the rest is read again,
 // from the caches).  The columns past the last whole group go one to a thread.  Most threads
 // run this code once, so its size counts as its registers do: held groups are unrolled.
-// The workgroup after the last row forms the experts' route (r.starts set), so that it costs
+// The workgroup after the last row forms the experts' route (r.offsets set), so that it costs
 // no launch of its own.
 template <int CD, int TPR, int HOLD>
 __global__ __launch_bounds__(kThreads) void k_int8_rows(const void* __restrict__ x, int64_t ldx, int64_t rows,
@@ -185,7 +183,7 @@ __global__ __launch_bounds__(kThreads) void k_int8_rows(const void* __restrict__
                                                         float* __restrict__ scale, Route r) {
   __shared__ uint32_t red[kThreads / 64];
   const int64_t row = (int64_t)blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
-  if (r.starts && blockIdx.x == gridDim.x - 1) {
+  if (r.offsets && blockIdx.x == gridDim.x - 1) {
     if (threadIdx.x < 64) route_experts(r);
     return;
   }
@@ -728,20 +726,25 @@ struct Raw {
 };
 
 template <int CD, int RB, int NWV, bool FUSE>
-__global__ __launch_bounds__(64 * NWV) void k_int8_few(I8 p, const int32_t* __restrict__ starts, Raw raw) {
+__global__ __launch_bounds__(64 * NWV) void k_int8_few(I8 p, const int32_t* __restrict__ count,
+                                                       const int4* __restrict__ runs, Raw raw) {
   constexpr int U = 8 / RB;  // lines per batch of loads and wave
   constexpr int NT = 64 * NWV;
   __shared__ int red[NWV][16][16 * RB + 1];
   __shared__ __attribute__((aligned(16))) char tok[FUSE ? kFuseBytes + 16 : 16];
   __shared__ uint32_t tmax[NWV];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int e = blockIdx.y;
+  int e = 0;
   int64_t first = 0, end = p.m;
-  if (starts) {
-    first = __builtin_amdgcn_readfirstlane(starts[e]);
-    end = __builtin_amdgcn_readfirstlane(starts[e + 1]);
+  if (count) {
+    // both requested at once: past the count, a run is read (there is room for it) but not used
+    const int live = *count;
+    const int4 run = runs[blockIdx.y];
+    e = __builtin_amdgcn_readfirstlane(run.x);
+    first = __builtin_amdgcn_readfirstlane(run.y);
+    end = first + __builtin_amdgcn_readfirstlane(run.z);
+    if ((int)blockIdx.y >= __builtin_amdgcn_readfirstlane(live)) return;
   }
-  if (first >= end) return;
   const int64_t n0 = (int64_t)blockIdx.x * (16 * RB);
   const int ncols = (int)min((int64_t)(16 * RB), p.n - n0);
   const int64_t wrow = (int64_t)e * p.n + n0;
@@ -865,7 +868,7 @@ int slices(int64_t tiles, int64_t ld) {
 // Workspace: the tokens' codes and scales, for the form grouped by expert its route, and the
 // sums of a cut contraction.
 struct Plan {
-  size_t off_codes = 0, off_scale = 0, off_starts = 0, off_count = 0, off_tiles = 0, off_part = 0, total = 0;
+  size_t off_codes = 0, off_scale = 0, off_count = 0, off_tiles = 0, off_part = 0, total = 0;
   int cap = 0, split = 1;
 };
 
@@ -895,6 +898,11 @@ struct Plan {
 //   128 of 8 (4096 x 4096)           65.8     64.7       63.5       53.3       63.0
 //   192 of 8 (14336 x 4096)           249      203        173        155        174
 //   256 of 8 (4096 x 4096)           96.5     86.1       83.2       83.0       74.2
+//   28 of 32 (1024 x 4096)           46.0     50.8
+//   28 of 16 (4096 x 4096)           75.4     81.6
+//   25 of 40 (3000 x 1111)           40.9     37.6
+//   160 of 4 (2112 x 1785)           16.5     15.4                  21.0
+//   112 of 4 (2048 x 7168)           42.9     37.5                  59.0
 // Long rows of few outputs leave the few-token kernel with few workgroups; the smallest tiles
 // cut the contraction (16 x 512 x 16384 22.6 -> 16.0 us, 4 x 1024 x 14336 20.3 -> 17.5, 2 x 64 x
 // 131072 113 -> 72; but 16 x 256 x 4096 9.0 -> 10.7, 4 x 4096 x 8192 15.4 -> 17.3).
@@ -909,9 +917,10 @@ Form form_of(int64_t m, int64_t n, int64_t ld, int32_t experts) {
     return (experts == 1 ? ceil_div(m, tm) : std::max(live, m / tm + (live + 1) / 2)) * ceil_div(n, tn) <= cus;
   };
   if (one_round(64, 64)) return SMALL;
-  if (experts == 1 || m >= 256 * live)
-    return one_round(64, 128) ? LOW : one_round(128, 128) ? MID : one_round(128, 256) ? WIDE : FULL;
-  return m >= 96 * live ? WIDE : one_round(128, 128) ? MID : LOW;
+  if (one_round(64, 128)) return LOW;
+  if (one_round(128, 128)) return MID;
+  if (experts > 1 && m < 96 * live) return m <= 32 * live && ld > 2048 ? SMALL : LOW;
+  return one_round(128, 256) || (experts > 1 && m < 256 * live) ? WIDE : FULL;
 }
 static_assert(Wide::TN == Full::TN && Mid::TN == Low::TN && Wide::TM == Mid::TM && Low::TM == Small::TM, "by form");
 int tile_rows(Form f) { return f == FULL ? Full::TM : f == WIDE || f == MID ? Mid::TM : Low::TM; }
@@ -924,8 +933,6 @@ Plan plan_int8(const qlora_int8_t* w, int64_t m, bool grouped) {
   if (grouped) {
     // the smallest tiles have the most rows of them: the size does not depend on the device
     P.cap = (int)(m / Low::TM + std::min<int64_t>(w->experts, m));
-    P.off_starts = off;
-    off += al(((size_t)w->experts + 1) * 4);
     P.off_count = off;
     off += al(4);
     P.off_tiles = off;
@@ -945,7 +952,7 @@ template <int CD, int TPR, int HOLD>
 int launch_rows(const void* x, int64_t ldx, int64_t rows, int64_t cols, int8_t* codes, float* scale, const Route& r,
                 hipStream_t s) {
   const int ld = (int)QLORA_INT8_LD(cols);
-  const dim3 g((unsigned)(ceil_div(rows, kThreads / TPR) + (r.starts ? 1 : 0))), b(kThreads);
+  const dim3 g((unsigned)(ceil_div(rows, kThreads / TPR) + (r.offsets ? 1 : 0))), b(kThreads);
   k_int8_rows<CD, TPR, HOLD><<<g, b, 0, s>>>(x, ldx, rows, (int)cols, ld, codes, scale, r);
   return check_launch("k_int8_rows");
 }
@@ -976,26 +983,26 @@ int rows_to_int8(int cd, const void* x, int64_t ldx, int64_t rows, int64_t cols,
 // 14336 x 4096 (896) and, with more than eight blocks to a compute unit, 50.9 / 47.9 / 51.4 us
 // on six experts of 14336 x 4096.
 template <int CD, bool FUSE>
-int few_rows(const I8& p, int32_t experts, const int32_t* starts, const Raw& raw, hipStream_t s) {
-  const int64_t blocks = ceil_div(p.n, 16) * std::min<int64_t>(experts, p.m), cus = cu_count();
+int few_rows(const I8& p, int runs, const Raw& raw, hipStream_t s) {
+  const int64_t blocks = ceil_div(p.n, 16) * runs, cus = cu_count();
   const int rb = blocks < 2 * cus ? 1 : blocks < 3 * cus || blocks >= 8 * cus ? 2 : 4;
-  const unsigned gx = (unsigned)ceil_div(p.n, 16 * rb), gy = (unsigned)experts;
+  const unsigned gx = (unsigned)ceil_div(p.n, 16 * rb), gy = (unsigned)runs;
   // Four waves; eight for one token over a long contraction on few workgroups (4096 x 14336:
   // 19.5 -> 16.3 us; with more tokens or shorter rows the same or worse).
   constexpr int W = FUSE ? 8 : 4;
-  if (FUSE && rb == 1 && p.ld >= 8192) k_int8_few<CD, 1, W, FUSE><<<dim3(gx, gy), dim3(64 * W), 0, s>>>(p, starts, raw);
-  else if (rb == 1) k_int8_few<CD, 1, 4, FUSE><<<dim3(gx, gy), dim3(256), 0, s>>>(p, starts, raw);
-  else if (rb == 2) k_int8_few<CD, 2, 4, FUSE><<<dim3(gx, gy), dim3(256), 0, s>>>(p, starts, raw);
-  else k_int8_few<CD, 4, 4, FUSE><<<dim3(gx, gy), dim3(256), 0, s>>>(p, starts, raw);
+  if (FUSE && rb == 1 && p.ld >= 8192) k_int8_few<CD, 1, W, FUSE><<<dim3(gx, gy), dim3(64 * W), 0, s>>>(p, p.count, p.tiles, raw);
+  else if (rb == 1) k_int8_few<CD, 1, 4, FUSE><<<dim3(gx, gy), dim3(256), 0, s>>>(p, p.count, p.tiles, raw);
+  else if (rb == 2) k_int8_few<CD, 2, 4, FUSE><<<dim3(gx, gy), dim3(256), 0, s>>>(p, p.count, p.tiles, raw);
+  else k_int8_few<CD, 4, 4, FUSE><<<dim3(gx, gy), dim3(256), 0, s>>>(p, p.count, p.tiles, raw);
   return check_launch("k_int8_few");
 }
 
 template <int CD>
-int product(const I8& p, int32_t experts, int cap, const int32_t* starts, hipStream_t s) {
+int product(const I8& p, int32_t experts, int cap, hipStream_t s) {
   const Form f = form_of(p.m, p.n, p.ld, experts);
-  if (f == FEW) return few_rows<CD, false>(p, experts, starts, Raw{}, s);
+  if (f == FEW) return few_rows<CD, false>(p, p.count ? cap : 1, Raw{}, s);
   const int tm = tile_rows(f), tn = f >= WIDE ? Full::TN : f >= LOW ? Low::TN : Small::TN;
-  const int64_t tiles = (starts ? cap : ceil_div(p.m, tm)) * ceil_div(p.n, tn);
+  const int64_t tiles = (p.count ? cap : ceil_div(p.m, tm)) * ceil_div(p.n, tn);
   if (tiles >= (1LL << 31)) return set_error(QLORA_ERR_UNSUPPORTED, "int8: %lld tiles", (long long)tiles);
   const dim3 g((unsigned)tiles);
   // the large tiles: a workgroup to a compute unit, or to a half tile in an only round
@@ -1045,24 +1052,24 @@ int launch_int8_linear(const qlora_int8_t* w, const void* x, int64_t m, int64_t 
   if (!offsets && m == 1 && p.ld <= kFuseBytes) {
     ProfScope prof(QLORA_K_INT8_GEMM, s);
     const Raw raw = {x, w->cols};
-    if (cd == CD_BF16) return few_rows<CD_BF16, true>(p, 1, nullptr, raw, s);
-    if (cd == CD_F16) return few_rows<CD_F16, true>(p, 1, nullptr, raw, s);
-    return few_rows<CD_F32, true>(p, 1, nullptr, raw, s);
+    if (cd == CD_BF16) return few_rows<CD_BF16, true>(p, 1, raw, s);
+    if (cd == CD_F16) return few_rows<CD_F16, true>(p, 1, raw, s);
+    return few_rows<CD_F32, true>(p, 1, raw, s);
   }
   Route r = {};
   if (offsets) {
     const Form f = form_of(m, w->rows, p.ld, w->experts);
-    const bool tiles = f != FEW;
-    r.starts = (int32_t*)(base + P.off_starts);
     r.count = (int32_t*)(base + P.off_count);
     r.tiles = (int4*)(base + P.off_tiles);
     r.offsets = offsets;
     r.experts = w->experts;
-    r.tile_m = tile_rows(f);
-    // whole runs of tile_m rows and one partial run for each expert that has a row
-    r.cap = tiles ? (int)(m / r.tile_m + std::min<int64_t>(w->experts, m)) : 0;
+    const int live = (int)std::min<int64_t>(w->experts, m);
+    // whole runs of tile_m rows and one partial run for each expert that has a row; for the
+    // few-token kernel an expert's rows are one run
+    r.tile_m = f == FEW ? (int)m : tile_rows(f);
+    r.cap = f == FEW ? live : (int)(m / r.tile_m) + live;
     r.m = m;
-    p.count = tiles ? r.count : nullptr;
+    p.count = r.count;
     p.tiles = r.tiles;
   }
   {
@@ -1071,10 +1078,9 @@ int launch_int8_linear(const qlora_int8_t* w, const void* x, int64_t m, int64_t 
     if (rc) return rc;
   }
   ProfScope prof(QLORA_K_INT8_GEMM, s);
-  const int32_t* starts = offsets ? (const int32_t*)(base + P.off_starts) : nullptr;
-  if (cd == CD_BF16) return product<CD_BF16>(p, w->experts, r.cap, starts, s);
-  if (cd == CD_F16) return product<CD_F16>(p, w->experts, r.cap, starts, s);
-  return product<CD_F32>(p, w->experts, r.cap, starts, s);
+  if (cd == CD_BF16) return product<CD_BF16>(p, w->experts, r.cap, s);
+  if (cd == CD_F16) return product<CD_F16>(p, w->experts, r.cap, s);
+  return product<CD_F32>(p, w->experts, r.cap, s);
 }
 
 }  // namespace qnf4
