@@ -857,11 +857,12 @@ size_t al(size_t b) { return (b + 255) & ~(size_t)255; }
 // units idle: as many as give 256 workgroups, of six stages at least.  A stage of a lone
 // workgroup takes 0.33 us, the second launch 3 us: 100 x 1000 x 14336 40.1 -> 21.0 us,
 // 61 x 1984 x 6212 23.1 -> 16.5, 768 x 64 x 3328 14.4 -> 13.3; below 24 stages or three slices
-// it is slower (688 x 128 x 2496 12.9 -> 14.1, 128 x 4096 x 4096 17.3 -> 19.9).
+// it is slower (688 x 128 x 2496 12.9 -> 14.1, 128 x 4096 x 4096 17.3 -> 19.9), two slices gain
+// from 40 stages on (500 x 1000 x 14336 42.5 -> 32.4, 1000 x 500 x 5120 21.7 -> 21.1).
 constexpr int kSplitItems = 256;
 int slices(int64_t tiles, int64_t ld) {
   const int64_t lines = ld >> 7;
-  if (lines < 24 || tiles * 3 > kSplitItems) return 1;
+  if (lines < 24 || tiles * (lines < 40 ? 3 : 2) > kSplitItems) return 1;
   return (int)std::min<int64_t>(std::min<int64_t>(8, kSplitItems / tiles), lines / 6);
 }
 
