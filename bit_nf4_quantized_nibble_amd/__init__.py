@@ -724,7 +724,7 @@ def distill_loss_grad(logits, top_values, top_index, temperature: float = 1.0, w
             raise ValueError("dlogits must have rows of contiguous elements, evenly spaced")
         g = dlogits
     elif need_grad:
-        g = torch.empty(logits.shape, dtype=dt, device=device)
+        g = torch.empty_like(logits, memory_format=torch.contiguous_format)
     loss = torch.empty(1, dtype=torch.float32, device=device)
     lib = _lib.lib()
     ws = _workspace_on(device, lib.qlora_distill_workspace_bytes(n, vocab, k, code), workspace)

@@ -16,6 +16,7 @@
 #include <vector>
 
 #include "common.h"
+#include "int8_distill.h"
 
 namespace qnf4 {
 

@@ -378,15 +378,6 @@ int launch_mse(const void* y, const void* t, int64_t n, int cd, float* loss, voi
                hipStream_t s);
 int launch_adamw(float* theta, const float* g, float* m, float* v, int64_t n, const qlora_adamw_t& o, int32_t step,
                  void* theta_cd, int cd, hipStream_t s);
-// int8.hip and distill.hip
-int launch_int8_quantize(const void* w, int64_t ldw, int dtype, const qlora_int8_t* q, hipStream_t s);
-size_t int8_workspace_bytes(const qlora_int8_t* w, int64_t m, bool grouped);
-int launch_int8_linear(const qlora_int8_t* w, const void* x, int64_t m, int64_t ldx, const int32_t* offsets,
-                       const void* bias, int cd, void* y, void* ws, hipStream_t s);
-int launch_distill(const void* z, int64_t n, int64_t V, int64_t ldz, int cd, const void* u, int ud, const void* idx,
-                   int idx64, int32_t k, float temperature, const float* weight, float* loss, float* row_kl, void* dz,
-                   int64_t lddz, void* ws, hipStream_t s);
-size_t distill_workspace_bytes(int64_t n, int64_t V, int32_t k, int cd);
 size_t stack_workspace_bytes(const qlora_stack_layer_t* layers, int32_t L, int64_t m, int32_t r, int cd,
                              int32_t flags);
 int launch_stack_step(const qlora_stack_layer_t* layers, int32_t L, const void* x, int64_t m, const void* target,

@@ -18,7 +18,7 @@
 
 #include <algorithm>
 
-#include "common.h"
+#include "int8_distill.h"
 
 namespace qnf4 {
 namespace {

@@ -10,7 +10,7 @@
 // zero adds nothing, so every kernel reads whole 128-byte rows whatever cols is.
 #include <algorithm>
 
-#include "common.h"
+#include "int8_distill.h"
 
 namespace qnf4 {
 namespace {
