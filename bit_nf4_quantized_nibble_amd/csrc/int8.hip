@@ -866,11 +866,15 @@ int slices(int64_t tiles, int64_t ld) {
   return (int)std::min<int64_t>(std::min<int64_t>(8, kSplitItems / tiles), lines / 6);
 }
 
+// The product's kernels: few tokens, tiles by size.
+enum Form { FEW, SMALL, LOW, MID, WIDE, FULL };
+
 // Workspace: the tokens' codes and scales, for the form grouped by expert its route, and the
 // sums of a cut contraction.
 struct Plan {
   size_t off_codes = 0, off_scale = 0, off_count = 0, off_tiles = 0, off_part = 0, total = 0;
   int cap = 0, split = 1;
+  Form cut = SMALL;  // tiles of a cut contraction
 };
 
 // Which product kernel takes a call: the few-token kernel, or the smallest tiles that still fit
@@ -909,7 +913,6 @@ struct Plan {
 // 131072 113 -> 72; but 16 x 256 x 4096 9.0 -> 10.7, 4 x 4096 x 8192 15.4 -> 17.3).
 // An uneven routing gives some experts several times the average, and the few-token
 // kernel goes over its weights again for each 16 rows, so experts leave it early.
-enum Form { FEW, SMALL, LOW, MID, WIDE, FULL };
 Form form_of(int64_t m, int64_t n, int64_t ld, int32_t experts) {
   const int64_t live = std::max<int64_t>(1, std::min<int64_t>(experts, m)), cus = cu_count();
   if (m <= (experts == 1 ? 16 : 4 * live)) return experts == 1 && ld > 8192 && n <= 2048 ? SMALL : FEW;
@@ -939,11 +942,22 @@ Plan plan_int8(const qlora_int8_t* w, int64_t m, bool grouped) {
     P.off_tiles = off;
     off += al((size_t)P.cap * sizeof(int4));
   }
-  const int64_t tiles = (grouped ? P.cap : ceil_div(m, Small::TM)) * ceil_div(w->rows, Small::TN);
+  int64_t tiles = (grouped ? P.cap : ceil_div(m, Small::TM)) * ceil_div(w->rows, Small::TN);
   P.split = tiles > 0 ? slices(tiles, QLORA_INT8_LD(w->cols)) : 1;
+  int64_t tile = Small::TM * Small::TN;
+  // Where the 64 x 64 tiles are too many for that: 128 x 128 in two to four slices, from 56
+  // stages on (300 x 4096 x 14336 62.8 -> 48.0 us, 640 x 800 x 14336 43.9 -> 36.4, 260 x 4096 x
+  // 7168 33.9 -> 31.2, 2000 x 500 x 8192 34.7 -> 36.0; 300 x 2048 x 5200 21.0 -> 22.5).
+  const int64_t mid = ceil_div(m, Mid::TM) * ceil_div(w->rows, Mid::TN);
+  if (P.split == 1 && !grouped && m > 16 && QLORA_INT8_LD(w->cols) >= 56 * 128 && 2 * mid <= kSplitItems) {
+    P.cut = MID;
+    P.split = (int)std::min<int64_t>(4, kSplitItems / mid);
+    tiles = mid;
+    tile = Mid::TM * Mid::TN;
+  }
   if (P.split > 1) {
     P.off_part = off;
-    off += (size_t)P.split * tiles * Small::TM * Small::TN * 4;
+    off += (size_t)P.split * tiles * tile * 4;
   }
   P.total = off;
   return P;
@@ -998,9 +1012,22 @@ int few_rows(const I8& p, int runs, const Raw& raw, hipStream_t s) {
   return check_launch("k_int8_few");
 }
 
+// The contraction in p.split slices, and the sum of those.
+template <int CD, class T, int WGS>
+int cut_product(const I8& p, int cap, hipStream_t s) {
+  const int64_t tiles = (p.count ? cap : ceil_div(p.m, T::TM)) * ceil_div(p.n, T::TN);
+  k_int8_tile<CD, T, WGS, true><<<dim3((unsigned)(tiles * p.split)), dim3(64 * T::NW), 0, s>>>(p);
+  const int rc = check_launch("k_int8_tile");
+  if (rc) return rc;
+  k_int8_join<CD, T><<<dim3((unsigned)tiles, T::TM * T::TN / (4 * kThreads)), dim3(kThreads), 0, s>>>(p);
+  return check_launch("k_int8_join");
+}
+
 template <int CD>
-int product(const I8& p, int32_t experts, int cap, hipStream_t s) {
+int product(const I8& p, int32_t experts, int cap, Form cut, hipStream_t s) {
   const Form f = form_of(p.m, p.n, p.ld, experts);
+  if (p.split > 1 && cut == MID) return cut_product<CD, Mid, 1>(p, cap, s);
+  if (p.split > 1 && f == SMALL) return cut_product<CD, Small, 2>(p, cap, s);
   if (f == FEW) return few_rows<CD, false>(p, p.count ? cap : 1, Raw{}, s);
   const int tm = tile_rows(f), tn = f >= WIDE ? Full::TN : f >= LOW ? Low::TN : Small::TN;
   const int64_t tiles = (p.count ? cap : ceil_div(p.m, tm)) * ceil_div(p.n, tn);
@@ -1012,13 +1039,7 @@ int product(const I8& p, int32_t experts, int cap, hipStream_t s) {
   else if (f == WIDE) k_int8_tile<CD, Wide, 1><<<g, dim3(64 * Wide::NW), 0, s>>>(p);
   else if (f == MID) k_int8_tile<CD, Mid, 1><<<g, dim3(64 * Mid::NW), 0, s>>>(p);
   else if (f == LOW) k_int8_tile<CD, Low, 2><<<g, dim3(64 * Low::NW), 0, s>>>(p);
-  else if (p.split > 1) {
-    k_int8_tile<CD, Small, 2, true><<<dim3((unsigned)(tiles * p.split)), dim3(64 * Small::NW), 0, s>>>(p);
-    const int rc = check_launch("k_int8_tile");
-    if (rc) return rc;
-    k_int8_join<CD, Small><<<dim3((unsigned)tiles, Small::TM * Small::TN / (4 * kThreads)), dim3(kThreads), 0, s>>>(p);
-    return check_launch("k_int8_join");
-  } else k_int8_tile<CD, Small, 2><<<g, dim3(64 * Small::NW), 0, s>>>(p);
+  else k_int8_tile<CD, Small, 2><<<g, dim3(64 * Small::NW), 0, s>>>(p);
   return check_launch(f == FULL ? "k_int8_full" : "k_int8_tile");
 }
 
@@ -1079,9 +1100,9 @@ int launch_int8_linear(const qlora_int8_t* w, const void* x, int64_t m, int64_t 
     if (rc) return rc;
   }
   ProfScope prof(QLORA_K_INT8_GEMM, s);
-  if (cd == CD_BF16) return product<CD_BF16>(p, w->experts, r.cap, s);
-  if (cd == CD_F16) return product<CD_F16>(p, w->experts, r.cap, s);
-  return product<CD_F32>(p, w->experts, r.cap, s);
+  if (cd == CD_BF16) return product<CD_BF16>(p, w->experts, r.cap, P.cut, s);
+  if (cd == CD_F16) return product<CD_F16>(p, w->experts, r.cap, P.cut, s);
+  return product<CD_F32>(p, w->experts, r.cap, P.cut, s);
 }
 
 }  // namespace qnf4

@@ -108,7 +108,7 @@ SIZES = [(1, 1, 1), (1, 17, 64), (2, 64, 100), (5, 1000, 129), (16, 512, 1024), 
          (300, 1030, 2047), (513, 640, 384), (1, 4096, 4096), (16, 14336, 512), (3, 200, 14336), (1030, 1290, 640),
          (1, 40, 16400), (1, 300, 131000), (2, 1001, 640), (15, 9000, 130), (16, 20011, 128), (300, 4099, 129),
          (520, 3001, 257), (600, 4321, 200), (2049, 2051, 130), (61, 500, 9000), (700, 64, 3328),
-         (17, 64, 131072), (100, 1001, 2600), (20, 3000, 4000), (3, 2100, 8300), (16, 2049, 8193), (7, 1001, 8400), (500, 1000, 5200)]
+         (17, 64, 131072), (100, 1001, 2600), (20, 3000, 4000), (3, 2100, 8300), (16, 2049, 8193), (7, 1001, 8400), (500, 1000, 5200), (300, 4096, 7168), (130, 3001, 7200), (250, 700, 14336), (17, 16384, 7300)]
 
 
 @pytest.mark.parametrize("cd", ["f32", "bf16", "f16"])
