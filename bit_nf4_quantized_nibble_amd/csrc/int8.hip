@@ -949,7 +949,7 @@ Plan plan_int8(const qlora_int8_t* w, int64_t m, bool grouped) {
   // stages on (300 x 4096 x 14336 62.8 -> 48.0 us, 640 x 800 x 14336 43.9 -> 36.4, 260 x 4096 x
   // 7168 33.9 -> 31.2, 2000 x 500 x 8192 34.7 -> 36.0; 300 x 2048 x 5200 21.0 -> 22.5).
   const int64_t mid = ceil_div(m, Mid::TM) * ceil_div(w->rows, Mid::TN);
-  if (P.split == 1 && !grouped && m > 16 && QLORA_INT8_LD(w->cols) >= 56 * 128 && 2 * mid <= kSplitItems) {
+  if (P.split == 1 && !grouped && m > 16 && QLORA_INT8_LD(w->cols) >= 56 * 128 && mid > 0 && 2 * mid <= kSplitItems) {
     P.cut = MID;
     P.split = (int)std::min<int64_t>(4, kSplitItems / mid);
     tiles = mid;

@@ -481,7 +481,8 @@ int qlora_int8_linear_experts(const qlora_int8_t* w, const void* x, int64_t m, i
                               size_t ws_bytes, void* stream);
 
 /* Workspace bytes of qlora_int8_linear (grouped 0) or qlora_int8_linear_experts (grouped 1)
- * on m tokens (reads only the shape of *w); 0 for an invalid query.  Pure host function. */
+ * on m tokens (reads only the shape of *w); 0 for an invalid query.  Fewer tokens may need more
+ * (sums of a cut contraction): ask for each m.  Pure host function. */
 size_t qlora_int8_workspace_bytes(const qlora_int8_t* w, int64_t m, int32_t grouped);
 
 /* ---------------------------------------------------------------------------

@@ -93,6 +93,10 @@ def test_int8_workspace_queries(lib):
     assert q(ctypes.byref(desc()), 10, 0) >= 10 * 128
     assert q(ctypes.byref(desc()), -1, 0) == 0 and q(None, 4, 0) == 0
     assert q(ctypes.byref(desc(codes=None, scale=None)), 4, 0) > 0  # shapes only
+    for rows, cols in ((0, 96), (0, 14336), (0, 131072), (64, 0)):  # empty weights
+        for m in (0, 1, 100, 5000):
+            for grouped in (0, 1):
+                assert q(ctypes.byref(desc(rows=rows, cols=cols)), m, grouped) <= m * (131072 + 4) + 100000
 
 
 def distill(lib, z=FAKE, n=4, vocab=100, ld=100, cd=1, u=FAKE, td=0, idx=FAKE, bits=32, k=8, t=1.0, w=None, loss=FAKE,
