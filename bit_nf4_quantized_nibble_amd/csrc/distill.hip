@@ -195,8 +195,9 @@ __global__ __launch_bounds__(TPB, TPB <= 256 ? 3 : 4) void k_distill(Distill p) 
         // four are on their way
         auto add = [&](float cm, auto share) {
           const float nm = fmaxf(zm, cm);
-          // a thread that has met only -inf so far has no share yet
-          zs = (zm == -INFINITY ? 0.f : zs * __builtin_amdgcn_exp2f((zm - nm) * p.c)) + share(nm);
+          // a thread that has met only -inf so far has no share yet, and one that has met NaN as
+          // well (fmaxf passes over it) has a NaN, which stays
+          zs = (zm == -INFINITY ? zs : zs * __builtin_amdgcn_exp2f((zm - nm) * p.c)) + share(nm);
           zm = nm;
         };
         auto part = [&](float y, float nm) { return y == -INFINITY ? 0.f : __builtin_amdgcn_exp2f((y - nm) * p.c); };
