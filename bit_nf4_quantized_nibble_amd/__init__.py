@@ -32,6 +32,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 from dataclasses import dataclass
 from typing import Optional, Tuple
 
@@ -506,12 +507,12 @@ def mse_loss_grad(y, target, dy=None):
 
 def _launch(device, call, *args):
     """call(*args, stream) with ``device`` current (its current stream); raises on an error."""
-    torch = _torch()
-    if device.index == torch.cuda.current_device():
-        _lib.check(call(*args, torch._C._cuda_getCurrentRawStream(device.index)))
+    cuda, index = _torch()._C, device.index
+    if index == cuda._cuda_getDevice():
+        _lib.check(call(*args, cuda._cuda_getCurrentRawStream(index)))
     else:
-        with torch.cuda.device(device):
-            _lib.check(call(*args, torch._C._cuda_getCurrentRawStream(device.index)))
+        with _torch().cuda.device(device):
+            _lib.check(call(*args, cuda._cuda_getCurrentRawStream(index)))
 
 
 def _check_tensor(name, t, device, dtype, numel):
@@ -582,18 +583,27 @@ class Int8Weight:
         return {k: v for k, v in self.__dict__.items() if k != "_made"}
 
     def descriptor(self) -> QloraInt8:
+        return self._described()[0]
+
+    def _described(self):
+        """The descriptor, and (rows, cols, experts)."""
+        # Kept between calls as long as all it was made from is the same: the tensors' storages
+        # can be replaced under them (``codes.data = ...``), and the fields assigned.
+        c, s = self.codes, self.scale
+        key = (self.rows, self.cols, c.data_ptr(), s.data_ptr(), c.shape, s.shape, c.dtype, s.dtype, c.is_contiguous(),
+               s.is_contiguous())
         made = self.__dict__.get("_made")
-        if made is None or made[0] is not self.codes or made[1] is not self.scale:
+        if made is None or made[0] != key:
             torch = _torch()
             ld = (self.cols + 127) // 128 * 128
-            for name, t, dt, shape in (("codes", self.codes, torch.int8, (self.experts, self.rows, ld)),
-                                       ("scale", self.scale, torch.float32, (self.experts, self.rows))):
+            for name, t, dt, shape in (("codes", c, torch.int8, (self.experts, self.rows, ld)),
+                                       ("scale", s, torch.float32, (self.experts, self.rows))):
                 if t.dtype != dt or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda or \
-                        t.device != self.codes.device:
+                        t.device != c.device:
                     raise ValueError("%s must be a contiguous %s GPU tensor of shape %s" % (name, dt, shape))
-            d = QloraInt8(self.rows, self.cols, self.experts, 0, _ptr(self.codes), _ptr(self.scale))
-            made = self.__dict__["_made"] = (self.codes, self.scale, d)
-        return made[2]
+            shape = (self.rows, self.cols, self.experts)
+            made = self.__dict__["_made"] = (key, (QloraInt8(*shape, 0, _ptr(c), _ptr(s)), shape))
+        return made[1]
 
 
 def quantize_int8(w) -> Int8Weight:
@@ -626,6 +636,13 @@ def int8_workspace_bytes(w: Int8Weight, m: int, grouped: bool = False) -> int:
     return int(_lib.lib().qlora_int8_workspace_bytes(ctypes.byref(d), m, int(grouped)))
 
 
+@functools.lru_cache(maxsize=4096)
+def _int8_bytes(shape, m, grouped):
+    """The same from the weight's rows, cols and experts alone."""
+    d = QloraInt8(*shape, 0, None, None)
+    return int(_lib.lib().qlora_int8_workspace_bytes(ctypes.byref(d), m, grouped))
+
+
 def _int8_call(w, x, offsets, bias, out, workspace):
     torch = _torch()
     dt, device = x.dtype, x.device
@@ -644,9 +661,10 @@ def _int8_call(w, x, offsets, bias, out, workspace):
     grouped = offsets is not None
     if bias is not None:
         _check_tensor("bias", bias, device, dt, w.rows * (w.experts if grouped else 1))
-    d = ctypes.byref(w.descriptor())
+    d, shape = w._described()
     lib = _lib.lib()
-    ws = _workspace_on(device, lib.qlora_int8_workspace_bytes(d, m, grouped), workspace)
+    ws = _workspace_on(device, _int8_bytes(shape, m, grouped), workspace)
+    d = ctypes.byref(d)
     ws_bytes = ws.numel() * ws.element_size()
     if grouped:
         _launch(device, lib.qlora_int8_linear_experts, d, x2.data_ptr(), m, ldx, offsets.data_ptr(), _ptr(bias), code,
