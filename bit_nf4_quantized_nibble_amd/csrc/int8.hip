@@ -255,10 +255,20 @@ struct I8 {
   int split;
 };
 
-// y from the sum: (sum * s) * t + bias, each product rounded to fp32, then to cd.
+// y from the sum, before it is rounded into its type: fl32(fl32(fl32(sum) s) t + bias), the second
+// product and the bias in one step.  Every kernel forms y by this, and an f16 value is rounded to
+// fp32 first in all of them: left alone, the compiler fuses the step with the conversion where a
+// value is converted by itself (one rounding) and not where two are packed (two), and a token's y
+// would differ by an f16 step from one batch size to another.
+template <int CD>
+__device__ __forceinline__ float scaled(int sum, float sa, float sb, float bv) {
+  float v = fmaf((float)sum * sa, sb, bv);
+  if constexpr (CD == CD_F16) asm("" : "+v"(v));
+  return v;
+}
 template <int CD>
 __device__ __forceinline__ void store_y(const I8& p, int64_t row, int64_t col, int sum, float sa, float sb, float bv) {
-  store_cd<CD>(p.y, row * p.n + col, (float)sum * sa * sb + bv);
+  store_cd<CD>(p.y, row * p.n + col, scaled<CD>(sum, sa, sb, bv));
 }
 
 // ---------------------------------------------------------------- tiled product
@@ -456,7 +466,7 @@ struct Writer {
           const f32x4_t sb = *(const f32x4_t*)(coef + c0), bv = *(const f32x4_t*)(coef + T::TN + c0);
           float v[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) v[x] = (float)acc[i][j][4 * q + x] * sa * sb[x] + bv[x];
+          for (int x = 0; x < 4; ++x) v[x] = scaled<CD>(acc[i][j][4 * q + x], sa, sb[x], bv[x]);
           if constexpr (ES == 4) {
             const f32x4_t o = {v[0], v[1], v[2], v[3]};
             *(f32x4_t*)(W + r32 * RB + (((8 * j + 2 * q + h) ^ (r32 & (NC - 1))) << 4)) = o;
