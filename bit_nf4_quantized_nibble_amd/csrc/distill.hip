@@ -37,7 +37,7 @@ struct Distill {
   float* kl;           // [n]
   int64_t n, V;
   int32_t k, ud, idx64;
-  float t, inv_t, c;   // T, 1 / T, log2(e) / T
+  float t, c;          // T, log2(e) / T
   float w_default;
 };
 
@@ -298,15 +298,17 @@ __global__ __launch_bounds__(TPB, TPB <= 256 ? 3 : 4) void k_distill(Distill p) 
           sum += S.zsum[x];
           usum += S.usum[x];
         }
-        // kl, and the share each index carries
-        const float lsum = logf(sum) - logf(usum), uinv = 1.0f / usum;
+        // kl = sum_j T p_j (u_j - z_j + T log(...)), with no 1 / T: fp32 holds a difference against
+        // a logit at the type's lowest value, but not its quotient by a T below 1; and the share
+        // each index carries
+        const float lsum = p.t * (logf(sum) - logf(usum)), uinv = 1.0f / usum;
         float kl = 0.f;
 #pragma unroll
         for (int s = 0; s < SPT; ++s)
           if (si[s] >= 0) {
             const int j = tid + s * TPB;
             const float pr = S.e[j] * uinv;
-            if (pr != 0.f) kl += pr * (((su[s] - umax) - (sz[s] - m)) * p.inv_t + lsum);
+            if (pr != 0.f) kl += pr * p.t * (((su[s] - umax) - (sz[s] - m)) + lsum);
             int first = j, same = 0;
             for (int l = S.head[owner(si[s])]; l >= 0; l = S.next[l])
               if (S.idx[l] == si[s]) {
@@ -331,7 +333,7 @@ __global__ __launch_bounds__(TPB, TPB <= 256 ? 3 : 4) void k_distill(Distill p) 
           float t = S.kl[0];
 #pragma unroll
           for (int x = 1; x < NW; ++x) t += S.kl[x];
-          p.kl[i] = p.t * p.t * t;
+          p.kl[i] = t;
         }
       }
     }
@@ -584,14 +586,14 @@ __global__ __launch_bounds__(kPartThreads) void k_distill_join(Distill p, Split 
       usum = block_sum(us, red[3]);
       inv = 1.0f / sum;
       if (part == 0) {
-        const float lsum = logf(sum) - logf(usum);
+        const float lsum = p.t * (logf(sum) - logf(usum));
 #pragma unroll
         for (int s = 0; s < SPT; ++s)
           if (si[s] >= 0) {
             const float pr = s_e[tid + s * TPB] / usum;
-            if (pr != 0.f) kl += pr * (((su[s] - umax) - (sz[s] - m)) * p.inv_t + lsum);
+            if (pr != 0.f) kl += pr * p.t * (((su[s] - umax) - (sz[s] - m)) + lsum);
           }
-        kl = p.t * p.t * block_sum(kl, red[4]);
+        kl = block_sum(kl, red[4]);
       }
     }
   }
@@ -774,7 +776,6 @@ int launch_distill(const void* z, int64_t n, int64_t V, int64_t ldz, int cd, con
   p.ud = ud;
   p.idx64 = idx64;
   p.t = temperature;
-  p.inv_t = (float)(1.0 / (double)temperature);
   p.c = (float)(1.4426950408889634074 / (double)temperature);
   p.w_default = n > 0 ? (float)(1.0 / (double)n) : 0.f;
   if (n > 0 && split_rows(n, V, cd)) {

@@ -13,7 +13,7 @@ pytestmark = pytest.mark.gpu
 
 # rows, vocabulary, with the gradient: streamed (the loss alone on whole rows, and rows longer than
 # the registers), kept in registers, cut into parts
-FORMS = [(300, 9001, False), (300, 32000, False), (100, 32003, False), (90, 170007, True), (90, 170007, False),
+FORMS = [(300, 9001, False), (300, 32000, False), (100, 32003, False), (90, 170007, True), (90, 170007, False), (90, 90001, True),
          (300, 9001, True), (300, 500, True), (300, 500, False), (12, 60003, True), (12, 60003, False)]
 
 
@@ -49,3 +49,20 @@ def test_nan_among_the_first_entries(n, V, grad, cd):
     w = torch.zeros(n)
     w[6:14] = 0.25
     check(z, u, idx, w=w, grad=grad)
+
+
+@pytest.mark.parametrize("cd", ["f32", "bf16"])
+@pytest.mark.parametrize("n,V,grad", [(300, 500, True), (300, 9001, False), (12, 60003, True), (300, 32000, True)])
+@pytest.mark.parametrize("T", [0.25, 0.75])
+def test_teacher_entries_at_the_lowest_value(T, n, V, grad, cd):
+    """A teacher's entry that the student masks with the type's lowest value: kl = T p |lowest|
+    and a little, which fp32 holds below T = 1."""
+    say("lowest", T, n, V, grad, cd)
+    z, u, idx = make(n, V, 8, cd, V + n)
+    lowest = torch.finfo(z.dtype).min
+    z[0, idx[0, 0]] = lowest
+    z[1, idx[1]] = lowest
+    z[2, V // 2:] = lowest
+    w = torch.zeros(n)
+    w[:12] = 1.0 / 64
+    check(z, u, idx, T=T, w=w, grad=grad)
