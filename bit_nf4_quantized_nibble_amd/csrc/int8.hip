@@ -260,9 +260,15 @@ struct I8 {
 // fp32 first in all of them: left alone, the compiler fuses the step with the conversion where a
 // value is converted by itself (one rounding) and not where two are packed (two), and a token's y
 // would differ by an f16 step from one batch size to another.
-template <int CD>
+// FAR: the token's scale may be so large (2^96: the sum is below 2^31) that its product with the
+// sum leaves fp32's range while y need not; such a token's sum takes the channel's scale first.
+// (A small sum times a scale near zero loses nothing: the product of an integer and a subnormal
+// number is exact as long as it is subnormal.)
+constexpr float kFarScale = 0x1p96f;
+template <int CD, bool FAR = true>
 __device__ __forceinline__ float scaled(int sum, float sa, float sb, float bv) {
-  float v = fmaf((float)sum * sa, sb, bv);
+  const bool far = FAR && sa >= kFarScale;
+  float v = fmaf((float)sum * (far ? sb : sa), far ? sa : sb, bv);
   if constexpr (CD == CD_F16) asm("" : "+v"(v));
   return v;
 }
@@ -448,6 +454,21 @@ struct Writer {
   static constexpr int stores() { return T::WMB * NC / 2; }
   __device__ static __forceinline__ void run(const I8& p, const Place& pl, const Acc<T>& acc, const float* coef, char* W,
                                              int wave, int lane) {
+    // far tokens (no f16 value is one) have code of their own: selecting the order for every
+    // element would cost the others two instructions each
+    bool far = false;
+    if constexpr (CD != CD_F16) {
+#pragma unroll
+      for (int i = 0; i < T::WMB; ++i)
+        far |= coef[2 * T::TN + (wave / T::NWN) * 32 * T::WMB + 32 * i + (lane & 31)] >= kFarScale;
+      far = __any(far);
+    }
+    if (far) rows<true>(p, pl, acc, coef, W, wave, lane);
+    else rows<false>(p, pl, acc, coef, W, wave, lane);
+  }
+  template <bool FAR>
+  __device__ static __forceinline__ void rows(const I8& p, const Place& pl, const Acc<T>& acc, const float* coef, char* W,
+                                              int wave, int lane) {
     constexpr int WMB = T::WMB, WNB = T::WNB;
     const int h = lane >> 5, r32 = lane & 31;
     const int wm = (wave / T::NWN) * 32 * WMB, wn = (wave % T::NWN) * 32 * WNB;
@@ -466,7 +487,7 @@ struct Writer {
           const f32x4_t sb = *(const f32x4_t*)(coef + c0), bv = *(const f32x4_t*)(coef + T::TN + c0);
           float v[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) v[x] = scaled<CD>(acc[i][j][4 * q + x], sa, sb[x], bv[x]);
+          for (int x = 0; x < 4; ++x) v[x] = scaled<CD, FAR>(acc[i][j][4 * q + x], sa, sb[x], bv[x]);
           if constexpr (ES == 4) {
             const f32x4_t o = {v[0], v[1], v[2], v[3]};
             *(f32x4_t*)(W + r32 * RB + (((8 * j + 2 * q + h) ^ (r32 & (NC - 1))) << 4)) = o;

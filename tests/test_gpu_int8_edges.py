@@ -62,3 +62,32 @@ def test_experts_have_the_bits_of_the_single_product(cd):
         s = slice(off[e], off[e + 1])
         one = qn.linear_int8(qn.quantize_int8(w[e].cuda()), x[s].cuda(), bias=b[e].cuda())
         assert torch.equal(y[s], one), "expert %d" % e
+
+
+@pytest.mark.parametrize("cd", ["f32", "bf16"])
+@pytest.mark.parametrize("m,n,k", [(1, 300, 384), (7, 300, 384), (60, 300, 384), (300, 4131, 384), (600, 4131, 384),
+                                   (2049, 4131, 384), (4153, 4131, 384), (4, 500, 14336), (100, 1003, 14336),
+                                   (300, 4096, 7168)])
+def test_products_that_pass_the_range_on_the_way(m, n, k, cd):
+    """Tokens near the type's largest value on weights near zero: sum * s leaves fp32's range, y
+    does not.  Ordinary tokens and zeros stand among them."""
+    say("far tokens", m, n, k, cd)
+    x, w, b = tensors(m, n, k, cd, m + n, bias=True)
+    w = (w.float() * 1e-31).to(w.dtype)
+    w[3] = 0
+    xf = x.float()
+    xf[::2] = xf[::2] / xf[::2].abs().amax(1, keepdim=True) * 3e38
+    xf[1::4] *= 1e30
+    if m > 4:
+        xf[4] = 0
+    x = xf.to(x.dtype)
+    assert not x.isinf().any()
+    q = qn.quantize_int8(w.cuda())
+    y = qn.linear_int8(q, x.cuda(), bias=b.cuda())
+    at = np.r_[0:min(m, 40), max(0, m - 40):m]
+    ref, mag = oi.product(to_np(x)[at], *oi.rows_to_int8(to_np(w)), to_np(b))
+    assert np.abs(ref).max() > 1e6
+    check(y[torch.from_numpy(at).cuda()], ref, mag, cd)
+    e = qn.linear_int8_experts(qn.quantize_int8(w[None].cuda()), x.cuda(),
+                               torch.tensor([0, m], dtype=torch.int32, device="cuda"), bias=b[None].cuda())
+    assert torch.equal(e, y)
