@@ -703,10 +703,12 @@ int distill_split(const Distill& p, const Split& sp, hipStream_t s) {
 
 // Workgroups of 1024 threads: as many as are resident at once, each going through its rows;
 // smaller ones: one to a row, several to a compute unit (4096 x 32000 bf16: 111.8 us, going
-// through rows 117.6; 4096 x 30000, loss alone: 50.6 against 56.5).
+// through rows 117.6; 4096 x 30000, loss alone: 50.6 against 56.5), as
+// far as a launch of fewer than 2^32 threads has them.
 template <int CD, int TPB, int NV, int KC>
 void launch_rows(const Distill& p, int per_cu, hipStream_t s) {
-  const int64_t g = TPB < 1024 ? p.n : std::min<int64_t>(p.n, (int64_t)per_cu * cu_count());
+  const int64_t most = TPB < 1024 ? (1LL << 31) / TPB : (int64_t)per_cu * cu_count();
+  const int64_t g = std::min(p.n, most);
   k_distill<CD, TPB, NV, KC><<<dim3((unsigned)g), dim3(TPB), 0, s>>>(p);
 }
 

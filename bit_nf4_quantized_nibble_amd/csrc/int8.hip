@@ -749,6 +749,7 @@ __global__ __launch_bounds__(512, 1) void k_int8_full(I8 p) {
 // weights are on their way, which spares the call a launch (4096 x 4096: 7.4 against 9.6 us;
 // with two tokens the repeated work already costs more than the launch: 11.2 against 9.9).
 constexpr int kFuseBytes = 32768;  // codes of the token in LDS at most
+constexpr int64_t kFewBlocks = 1 << 22;  // workgroups along x; the weight's other rows along z
 
 // Source of a call's token when it is not in 8 bits yet.
 struct Raw {
@@ -776,7 +777,8 @@ __global__ __launch_bounds__(64 * NWV) void k_int8_few(I8 p, const int32_t* __re
     end = first + __builtin_amdgcn_readfirstlane(run.z);
     if ((int)blockIdx.y >= __builtin_amdgcn_readfirstlane(live)) return;
   }
-  const int64_t n0 = (int64_t)blockIdx.x * (16 * RB);
+  const int64_t n0 = (blockIdx.z * kFewBlocks + blockIdx.x) * (16 * RB);
+  if (n0 >= p.n) return;
   const int ncols = (int)min((int64_t)(16 * RB), p.n - n0);
   const int64_t wrow = (int64_t)e * p.n + n0;
   const int ld = (int)p.ld, lines = ld >> 7;
@@ -957,7 +959,8 @@ Form form_of(int64_t m, int64_t n, int64_t ld, int32_t experts) {
   if (experts > 1 && m < 96 * live) return m <= 32 * live && ld > 2048 ? SMALL : LOW;
   return one_round(128, 256) || (experts > 1 && m < 256 * live) ? WIDE : FULL;
 }
-static_assert(Wide::TN == Full::TN && Mid::TN == Low::TN && Wide::TM == Mid::TM && Low::TM == Small::TM, "by form");
+static_assert(Wide::TN == Full::TN && Mid::TN == Low::TN && Wide::TM == Mid::TM && Low::TM == Small::TM &&
+                  Mid::NW == Low::NW && Low::NW == Small::NW, "by form");
 int tile_rows(Form f) { return f == FULL ? Full::TM : f == WIDE || f == MID ? Mid::TM : Low::TM; }
 
 Plan plan_int8(const qlora_int8_t* w, int64_t m, bool grouped) {
@@ -994,13 +997,22 @@ Plan plan_int8(const qlora_int8_t* w, int64_t m, bool grouped) {
   return P;
 }
 
+// A launch has fewer than 2^32 threads: more rows than that go in several.
 template <int CD, int TPR, int HOLD>
 int launch_rows(const void* x, int64_t ldx, int64_t rows, int64_t cols, int8_t* codes, float* scale, const Route& r,
                 hipStream_t s) {
   const int ld = (int)QLORA_INT8_LD(cols);
-  const dim3 g((unsigned)(ceil_div(rows, kThreads / TPR) + (r.offsets ? 1 : 0))), b(kThreads);
-  k_int8_rows<CD, TPR, HOLD><<<g, b, 0, s>>>(x, ldx, rows, (int)cols, ld, codes, scale, r);
-  return check_launch("k_int8_rows");
+  const int64_t most = (1LL << 31) / TPR;
+  for (int64_t r0 = 0; r0 < rows; r0 += most) {
+    const int64_t n = std::min(most, rows - r0);
+    const Route here = r0 + n == rows ? r : Route{};
+    const dim3 g((unsigned)(ceil_div(n, kThreads / TPR) + (here.offsets ? 1 : 0))), b(kThreads);
+    k_int8_rows<CD, TPR, HOLD><<<g, b, 0, s>>>((const char*)x + r0 * ldx * cd_bytes(CD), ldx, n, (int)cols, ld,
+                                               codes + r0 * ld, scale + r0, here);
+    const int rc = check_launch("k_int8_rows");
+    if (rc) return rc;
+  }
+  return QLORA_OK;
 }
 
 // A wave per row where rows are short, or enough to fill the chip and not long, else a
@@ -1032,14 +1044,15 @@ template <int CD, bool FUSE>
 int few_rows(const I8& p, int runs, const Raw& raw, hipStream_t s) {
   const int64_t blocks = ceil_div(p.n, 16) * runs, cus = cu_count();
   const int rb = blocks < 2 * cus ? 1 : blocks < 3 * cus || blocks >= 8 * cus ? 2 : 4;
-  const unsigned gx = (unsigned)ceil_div(p.n, 16 * rb), gy = (unsigned)runs;
+  const int64_t gx = ceil_div(p.n, 16 * rb);
+  const dim3 g((unsigned)std::min(gx, kFewBlocks), (unsigned)runs, (unsigned)ceil_div(gx, kFewBlocks));
   // Four waves; eight for one token over a long contraction on few workgroups (4096 x 14336:
   // 19.5 -> 16.3 us; with more tokens or shorter rows the same or worse).
   constexpr int W = FUSE ? 8 : 4;
-  if (FUSE && rb == 1 && p.ld >= 8192) k_int8_few<CD, 1, W, FUSE><<<dim3(gx, gy), dim3(64 * W), 0, s>>>(p, p.count, p.tiles, raw);
-  else if (rb == 1) k_int8_few<CD, 1, 4, FUSE><<<dim3(gx, gy), dim3(256), 0, s>>>(p, p.count, p.tiles, raw);
-  else if (rb == 2) k_int8_few<CD, 2, 4, FUSE><<<dim3(gx, gy), dim3(256), 0, s>>>(p, p.count, p.tiles, raw);
-  else k_int8_few<CD, 4, 4, FUSE><<<dim3(gx, gy), dim3(256), 0, s>>>(p, p.count, p.tiles, raw);
+  if (FUSE && rb == 1 && p.ld >= 8192) k_int8_few<CD, 1, W, FUSE><<<g, dim3(64 * W), 0, s>>>(p, p.count, p.tiles, raw);
+  else if (rb == 1) k_int8_few<CD, 1, 4, FUSE><<<g, dim3(256), 0, s>>>(p, p.count, p.tiles, raw);
+  else if (rb == 2) k_int8_few<CD, 2, 4, FUSE><<<g, dim3(256), 0, s>>>(p, p.count, p.tiles, raw);
+  else k_int8_few<CD, 4, 4, FUSE><<<g, dim3(256), 0, s>>>(p, p.count, p.tiles, raw);
   return check_launch("k_int8_few");
 }
 
@@ -1054,15 +1067,18 @@ int cut_product(const I8& p, int cap, hipStream_t s) {
   return check_launch("k_int8_join");
 }
 
+// Tiles of a form: `cap` rows of them, or (0) of one matrix.
+int64_t tiles_of(Form f, int64_t m, int64_t n, int cap) {
+  const int tn = f >= WIDE ? Full::TN : f >= LOW ? Low::TN : Small::TN;
+  return (cap ? cap : ceil_div(m, tile_rows(f))) * ceil_div(n, tn);
+}
+
 template <int CD>
-int product(const I8& p, int32_t experts, int cap, Form cut, hipStream_t s) {
-  const Form f = form_of(p.m, p.n, p.ld, experts);
+int product(const I8& p, Form f, int cap, Form cut, hipStream_t s) {
   if (p.split > 1 && cut == MID) return cut_product<CD, Mid, 1>(p, cap, s);
   if (p.split > 1 && f == SMALL) return cut_product<CD, Small, 2>(p, cap, s);
   if (f == FEW) return few_rows<CD, false>(p, p.count ? cap : 1, Raw{}, s);
-  const int tm = tile_rows(f), tn = f >= WIDE ? Full::TN : f >= LOW ? Low::TN : Small::TN;
-  const int64_t tiles = (p.count ? cap : ceil_div(p.m, tm)) * ceil_div(p.n, tn);
-  if (tiles >= (1LL << 31)) return set_error(QLORA_ERR_UNSUPPORTED, "int8: %lld tiles", (long long)tiles);
+  const int64_t tiles = tiles_of(f, p.m, p.n, p.count ? cap : 0);
   const dim3 g((unsigned)tiles);
   // the large tiles: a workgroup to a compute unit, or to a half tile in an only round
   if (f == FULL)
@@ -1109,9 +1125,9 @@ int launch_int8_linear(const qlora_int8_t* w, const void* x, int64_t m, int64_t 
     if (cd == CD_F16) return few_rows<CD_F16, true>(p, 1, raw, s);
     return few_rows<CD_F32, true>(p, 1, raw, s);
   }
+  const Form f = form_of(m, w->rows, p.ld, w->experts);
   Route r = {};
   if (offsets) {
-    const Form f = form_of(m, w->rows, p.ld, w->experts);
     r.count = (int32_t*)(base + P.off_count);
     r.tiles = (int4*)(base + P.off_tiles);
     r.offsets = offsets;
@@ -1125,15 +1141,22 @@ int launch_int8_linear(const qlora_int8_t* w, const void* x, int64_t m, int64_t 
     p.count = r.count;
     p.tiles = r.tiles;
   }
+  if (f != FEW) {
+    // before anything is launched: the kernels count tiles in 31 bits, and the tiles of all forms
+    // but the largest (whose workgroups go through theirs) are one launch, of fewer than 2^32 threads
+    const int64_t tiles = tiles_of(f, m, p.n, r.cap), threads = f == FULL ? 1 : 64 * (f == WIDE ? Wide::NW : Mid::NW);
+    if (tiles >= (1LL << 31) || tiles * threads >= (1LL << 32))
+      return set_error(QLORA_ERR_UNSUPPORTED, "int8: %lld tiles in one call", (long long)tiles);
+  }
   {
     ProfScope prof(QLORA_K_INT8_ROWS, s);
     const int rc = rows_to_int8(cd, x, ldx, m, w->cols, (int8_t*)p.a, (float*)p.sa, r, s);
     if (rc) return rc;
   }
   ProfScope prof(QLORA_K_INT8_GEMM, s);
-  if (cd == CD_BF16) return product<CD_BF16>(p, w->experts, r.cap, P.cut, s);
-  if (cd == CD_F16) return product<CD_F16>(p, w->experts, r.cap, P.cut, s);
-  return product<CD_F32>(p, w->experts, r.cap, P.cut, s);
+  if (cd == CD_BF16) return product<CD_BF16>(p, f, r.cap, P.cut, s);
+  if (cd == CD_F16) return product<CD_F16>(p, f, r.cap, P.cut, s);
+  return product<CD_F32>(p, f, r.cap, P.cut, s);
 }
 
 }  // namespace qnf4

@@ -127,3 +127,13 @@ def test_distill_workspace_queries(lib):
     assert q(-1, 10, 1, 1) == 0 and q(0, 10, 1, 1) > 0 and q(1000, 10, 1, 1) >= 4000
     assert q(4, 0, 1, 1) == 0 and q(4, 10, 0, 1) == 0 and q(4, 10, 1025, 1) == 0 and q(4, 10, 1, 3) == 0
     assert q(4, 100000, 8, 1) > q(4, 100, 8, 1)  # rows cut into parts
+
+
+def test_tiles_beyond_one_launch_are_refused_before_any_work(lib):
+    """A launch has fewer than 2^32 threads: experts' tiles of more are refused on the host."""
+    d = desc(rows=32000, cols=64, experts=65535)
+    assert linear(lib, d, m=65535 * 60, grouped=True, ws_bytes=1 << 62, x=FAKE, y=FAKE + (1 << 40)) == UNSUP
+    assert b"tiles" in lib.qlora_last_error()
+    d = desc(rows=(1 << 31) - 1, cols=64)
+    assert linear(lib, d, m=(1 << 31) - 1, ws_bytes=1 << 62, x=FAKE, y=FAKE + (1 << 40)) == UNSUP
+    assert b"tiles" in lib.qlora_last_error()
