@@ -946,9 +946,15 @@ struct Plan {
 // 131072 113 -> 72; but 16 x 256 x 4096 9.0 -> 10.7, 4 x 4096 x 8192 15.4 -> 17.3).
 // An uneven routing gives some experts several times the average, and the few-token
 // kernel goes over its weights again for each 16 rows, so experts leave it early.
+int64_t live_experts(int64_t m, int32_t experts) { return std::max<int64_t>(1, std::min<int64_t>(experts, m)); }
+bool few_tokens(int64_t m, int32_t experts) { return m <= (experts == 1 ? 16 : 4 * live_experts(m, experts)); }
+bool long_rows_of_few(int64_t n, int64_t ld, int32_t experts) { return experts == 1 && ld > 8192 && n <= 2048; }
+// One token of one matrix: one launch does it all.
+bool one_launch(int64_t m, int64_t ld, bool grouped) { return !grouped && m == 1 && ld <= kFuseBytes; }
+
 Form form_of(int64_t m, int64_t n, int64_t ld, int32_t experts) {
-  const int64_t live = std::max<int64_t>(1, std::min<int64_t>(experts, m)), cus = cu_count();
-  if (m <= (experts == 1 ? 16 : 4 * live)) return experts == 1 && ld > 8192 && n <= 2048 ? SMALL : FEW;
+  const int64_t live = live_experts(m, experts), cus = cu_count();
+  if (few_tokens(m, experts)) return long_rows_of_few(n, ld, experts) ? SMALL : FEW;
   // tile rows: each expert's last one is half full on average
   auto one_round = [&](int64_t tm, int64_t tn) {
     return (experts == 1 ? ceil_div(m, tm) : std::max(live, m / tm + (live + 1) / 2)) * ceil_div(n, tn) <= cus;
@@ -965,7 +971,8 @@ int tile_rows(Form f) { return f == FULL ? Full::TM : f == WIDE || f == MID ? Mi
 
 Plan plan_int8(const qlora_int8_t* w, int64_t m, bool grouped) {
   Plan P;
-  size_t off = al((size_t)m * QLORA_INT8_LD(w->cols));
+  const int64_t ld = QLORA_INT8_LD(w->cols);
+  size_t off = al((size_t)(m * ld));
   P.off_scale = off;
   off += al((size_t)m * 4);
   if (grouped) {
@@ -976,14 +983,16 @@ Plan plan_int8(const qlora_int8_t* w, int64_t m, bool grouped) {
     P.off_tiles = off;
     off += al((size_t)P.cap * sizeof(int4));
   }
+  P.total = off;
+  if (one_launch(m, ld, grouped) || (few_tokens(m, w->experts) && !long_rows_of_few(w->rows, ld, w->experts))) return P;
   int64_t tiles = (grouped ? P.cap : ceil_div(m, Small::TM)) * ceil_div(w->rows, Small::TN);
-  P.split = tiles > 0 ? slices(tiles, QLORA_INT8_LD(w->cols)) : 1;
+  P.split = tiles > 0 ? slices(tiles, ld) : 1;
   int64_t tile = Small::TM * Small::TN;
   // Where the 64 x 64 tiles are too many for that: 128 x 128 in two to four slices, from 56
   // stages on (300 x 4096 x 14336 62.8 -> 48.0 us, 640 x 800 x 14336 43.9 -> 36.4, 260 x 4096 x
   // 7168 33.9 -> 31.2, 2000 x 500 x 8192 34.7 -> 36.0; 300 x 2048 x 5200 21.0 -> 22.5).
   const int64_t mid = ceil_div(m, Mid::TM) * ceil_div(w->rows, Mid::TN);
-  if (P.split == 1 && !grouped && m > 16 && QLORA_INT8_LD(w->cols) >= 56 * 128 && mid > 0 && 2 * mid <= kSplitItems) {
+  if (P.split == 1 && !grouped && m > 16 && ld >= 56 * 128 && mid > 0 && 2 * mid <= kSplitItems) {
     P.cut = MID;
     P.split = (int)std::min<int64_t>(4, kSplitItems / mid);
     tiles = mid;
@@ -1117,8 +1126,7 @@ int launch_int8_linear(const qlora_int8_t* w, const void* x, int64_t m, int64_t 
   p.ld = QLORA_INT8_LD(w->cols);
   p.part = (int*)(base + P.off_part);
   p.split = P.split;
-  // One token of one matrix: one launch does it all.
-  if (!offsets && m == 1 && p.ld <= kFuseBytes) {
+  if (one_launch(m, p.ld, offsets != nullptr)) {
     ProfScope prof(QLORA_K_INT8_GEMM, s);
     const Raw raw = {x, w->cols};
     if (cd == CD_BF16) return few_rows<CD_BF16, true>(p, 1, raw, s);

@@ -137,3 +137,22 @@ def test_tiles_beyond_one_launch_are_refused_before_any_work(lib):
     d = desc(rows=(1 << 31) - 1, cols=64)
     assert linear(lib, d, m=(1 << 31) - 1, ws_bytes=1 << 62, x=FAKE, y=FAKE + (1 << 40)) == UNSUP
     assert b"tiles" in lib.qlora_last_error()
+
+
+def test_workspaces_hold_the_slices_only_where_the_contraction_is_cut(lib):
+    def q(rows, cols, m, experts=1, grouped=0):
+        return lib.qlora_int8_workspace_bytes(ctypes.byref(desc(rows=rows, cols=cols, experts=experts)), m, grouped)
+
+    def tokens(cols, m):
+        ld = (cols + 127) // 128 * 128
+        return (m * ld + 255) // 256 * 256 + (4 * m + 255) // 256 * 256
+
+    # one launch, or the few-token kernel: the tokens' codes and scales alone
+    for rows, cols, m in ((4096, 14336, 1), (512, 16384, 1), (64, 32768, 1), (4096, 14336, 2), (4096, 14336, 16),
+                          (4096, 4096, 16), (2049, 16384, 9)):
+        assert q(rows, cols, m) == tokens(cols, m), (rows, cols, m)
+    for m in (1, 8, 16):  # by expert: the run list besides
+        assert q(2048, 14336, m, experts=4, grouped=1) <= tokens(14336, m) + 4096, m
+    # slices of a long contraction
+    for rows, cols, m in ((512, 16384, 16), (64, 131072, 1), (1000, 14336, 100), (4096, 14336, 300)):
+        assert q(rows, cols, m) > tokens(cols, m) + 4 * rows * m, (rows, cols, m)
