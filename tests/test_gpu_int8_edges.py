@@ -91,3 +91,44 @@ def test_products_that_pass_the_range_on_the_way(m, n, k, cd):
     e = qn.linear_int8_experts(qn.quantize_int8(w[None].cuda()), x.cuda(),
                                torch.tensor([0, m], dtype=torch.int32, device="cuda"), bias=b[None].cuda())
     assert torch.equal(e, y)
+
+
+@pytest.mark.parametrize("cd", ["f32", "bf16", "f16"])
+def test_large_prompt_with_bias_and_odd_rows(cd):
+    """Several rounds of the largest tiles, the last one in halves: biases and scales handed from tile
+    to tile, rows of y that start anywhere, columns behind the last whole 16 bytes."""
+    m, n, k = 4096 + 57, 4096 + 35, 384
+    say("large prompt", m, n, k, cd)
+    x, w, b = tensors(m, n, k, cd, 15, bias=True)
+    y = qn.linear_int8(qn.quantize_int8(w.cuda()), x.cuda(), bias=b.cuda())
+    codes, scale = oi.rows_to_int8(to_np(w))
+    rows = np.r_[0:20, 120:136, 250:262, 2040:2056, 3960:3975, m - 70:m]
+    ref, mag = oi.product(to_np(x)[rows], codes, scale, to_np(b))
+    check(y[torch.from_numpy(rows).cuda()], ref, mag, cd)
+    cols = np.r_[0:5, n - 37:n]
+    ref, mag = oi.product(to_np(x), codes[cols], scale[cols], to_np(b)[cols])
+    check(y[:, torch.from_numpy(cols).cuda()], ref, mag, cd, "columns")
+
+
+@pytest.mark.parametrize("cd", ["f32", "bf16", "f16"])
+def test_experts_of_many_rows(cd):
+    """The same by expert: uneven, hundreds of rows each on average, more than one round of tiles."""
+    sizes, n, k, before, tail = [900, 1, 0, 513, 129, 1400, 256], 9001, 200, 5, 9
+    say("experts of many rows", cd)
+    m = before + sum(sizes) + tail
+    x, w, b = tensors(m, n, k, cd, 16, experts=len(sizes), bias=True)
+    off = np.r_[0, np.cumsum(sizes)] + before
+    out = torch.full((m, n), 7.0, dtype=TORCH_DT[cd], device="cuda")
+    y = qn.linear_int8_experts(qn.quantize_int8(w.cuda()), x.cuda(), torch.tensor(off, dtype=torch.int32, device="cuda"),
+                               bias=b.cuda(), out=out)
+    assert (y[:before] == 7.0).all() and (y[m - tail:] == 7.0).all()
+    for e, s in enumerate(sizes):
+        rows = np.unique(np.r_[0:min(s, 6), min(s, 126):min(s, 131), min(s, 254):min(s, 259), max(0, s - 5):s]).astype(int)
+        if s == 0:
+            continue
+        codes, scale = oi.rows_to_int8(to_np(w[e]))
+        ref, mag = oi.product(to_np(x)[off[e] + rows], codes, scale, to_np(b[e]))
+        check(y[torch.from_numpy(off[e] + rows).cuda()], ref, mag, cd, "expert %d" % e)
+        cols = np.r_[0:3, n - 11:n]
+        ref, mag = oi.product(to_np(x)[off[e]:off[e + 1]], codes[cols], scale[cols], to_np(b[e])[cols])
+        check(y[int(off[e]):int(off[e + 1])][:, torch.from_numpy(cols).cuda()], ref, mag, cd, "columns of expert %d" % e)
