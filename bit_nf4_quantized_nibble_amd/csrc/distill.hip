@@ -679,7 +679,9 @@ __global__ __launch_bounds__(kPartThreads) void k_distill_join(Distill p, Split 
 //   96       10.6  12.4   16.5  14.8   27.0   23.8   49.6   34.8   42.3  33.1   86.3   55.0
 //   160                                                            49.1  47.3    114   95.9
 //   256                                33.4   48.4                 83.5  78.7    159    149
-// The loss alone gains from about the same rows on.
+// The loss alone gains from about the same rows on.  The rule is coarser than the table: it leaves
+// 32 rows of 32000 bf16, 64 and 96 of 64000, 96 of 128000, and of f32 160 of 128000 and 256 of 128000
+// and 250000 whole, where parts are 4 to 14% faster.
 constexpr int64_t kSplitRows = 256;
 bool split_rows(int64_t n, int64_t V, int cd) {
   const int64_t bytes = V * cd_bytes(cd);

@@ -647,8 +647,10 @@ using Full = Tile<4, 2, 2, 4, 2>;  // 256 x 256, eight waves
 using Half = Tile<2, 2, 2, 4, 2>;  // 128 x 256, eight waves
 using Wide = Tile<2, 2, 2, 4, 3>;  // 128 x 256, eight waves
 using Mid = Tile<2, 2, 2, 2, 4>;   // 128 x 128, four waves
-using Low = Tile<1, 2, 2, 2, 3>;   // 64 x 128, four waves, two workgroups to a compute unit
-using Small = Tile<1, 1, 2, 2, 4>;  // 64 x 64, four waves, two workgroups to a compute unit
+// Two workgroups of these fit a compute unit.  Experts of few rows use that (several rounds); a
+// dense call takes them where one round holds all tiles, one to a compute unit.
+using Low = Tile<1, 2, 2, 2, 3>;   // 64 x 128, four waves
+using Small = Tile<1, 1, 2, 2, 4>;  // 64 x 64, four waves
 
 // Whole rounds of 256 x 256 tiles, a workgroup to a compute unit going through its tiles.
 // After a tile's last stage the copies of the next tile's first stage are requested, so
@@ -745,9 +747,10 @@ __global__ __launch_bounds__(512, 1) void k_int8_full(I8 p) {
 // requested before the first product.  The waves' sums meet in LDS.
 // More than 16 tokens of an expert: the workgroup goes over its weight rows again for
 // each 16 of them (from the caches).
-// FUSE (one token of one matrix): the workgroup brings the token to 8 bits itself while its
-// weights are on their way, which spares the call a launch (4096 x 4096: 7.4 against 9.6 us;
-// with two tokens the repeated work already costs more than the launch: 11.2 against 9.9).
+// FUSE (one token of one matrix): the workgroup brings the token to 8 bits itself, which spares
+// the call a launch (4096 x 4096: 7.4 against 9.6 us; with two tokens the repeated work already
+// costs more than the launch: 11.2 against 9.9).  The first weights are requested before the
+// token and loads return in order, so the codes are formed once those weights have arrived.
 constexpr int kFuseBytes = 32768;  // codes of the token in LDS at most
 constexpr int64_t kFewBlocks = 1 << 22;  // workgroups along x; the weight's other rows along z
 
@@ -946,6 +949,9 @@ struct Plan {
 // 131072 113 -> 72; but 16 x 256 x 4096 9.0 -> 10.7, 4 x 4096 x 8192 15.4 -> 17.3).
 // An uneven routing gives some experts several times the average, and the few-token
 // kernel goes over its weights again for each 16 rows, so experts leave it early.
+// The rule follows the best column but for two rows of the experts' table: 32 of 8 and 28 of 32
+// fill one round of 64 x 128 tiles to the last compute unit and take them (49.6 and 50.8 us), where
+// 128 x 128 (41.9) and 64 x 64 (46.0) are faster.
 int64_t live_experts(int64_t m, int32_t experts) { return std::max<int64_t>(1, std::min<int64_t>(experts, m)); }
 bool few_tokens(int64_t m, int32_t experts) { return m <= (experts == 1 ? 16 : 4 * live_experts(m, experts)); }
 bool long_rows_of_few(int64_t n, int64_t ld, int32_t experts) { return experts == 1 && ld > 8192 && n <= 2048; }

@@ -418,8 +418,10 @@ size_t qlora_noalloc_scratch_bytes(void);
  *                   [-127, 127]; s = 0 and c = 0 for a row of zeros; a row holding an
  *                   infinity or a NaN has s = NaN and c = 0.
  *   product         y [m, rows] = RNE_cd(s_i t_j sum_k c[i, k] d[j, k] (+ bias[j])): the integer
- *                   sum is exact, the scaling and the bias are fp32.  A token whose
- *                   activations hold an infinity or a NaN has a row of NaN.
+ *                   sum is exact, the scaling and the bias are fp32 (also where y is f16: rounded
+ *                   to fp32, then into its type), and nothing overflows on the way to a y that
+ *                   does not.  A token's y has the same bits whatever other tokens a call holds.
+ *                   A token whose activations hold an infinity or a NaN has a row of NaN.
  * ------------------------------------------------------------------------- */
 
 /* Most columns a product takes (the sum of 131072 products of two codes is below 2^31). */
@@ -460,7 +462,8 @@ int qlora_int8_quantize(const void* w, int64_t ldw, int32_t wd, qlora_int8_t* q,
  * ws: qlora_int8_workspace_bytes(w, m, 0) bytes, 256-byte aligned.
  * Errors: QLORA_ERR_INVALID_ARG (null or unaligned pointers, y over x, experts != 1),
  * QLORA_ERR_SHAPE (m < 0, empty weight, ldx < cols), QLORA_ERR_DTYPE, QLORA_ERR_WORKSPACE,
- * QLORA_ERR_UNSUPPORTED (cols > QLORA_INT8_MAX_COLS, m or experts * rows of 2^31 or more).
+ * QLORA_ERR_UNSUPPORTED (cols > QLORA_INT8_MAX_COLS, m or experts * rows of 2^31 or more, or
+ * more tiles of y than one launch takes: from 2^23 on, which only thousands of experts reach).
  */
 int qlora_int8_linear(const qlora_int8_t* w, const void* x, int64_t m, int64_t ldx, const void* bias,
                       int32_t cd, void* y, void* ws, size_t ws_bytes, void* stream);
@@ -520,7 +523,8 @@ int qlora_distill_loss_grad(const void* logits, int64_t n, int64_t vocab, int64_
                             int32_t k, float temperature, const float* weight, float* loss, float* row_kl,
                             void* dlogits, int64_t ldd, void* ws, size_t ws_bytes, void* stream);
 
-/* Workspace bytes of qlora_distill_loss_grad; 0 for an invalid query.  Pure host function. */
+/* Workspace bytes of qlora_distill_loss_grad; 0 for an invalid query.  Fewer rows may need more
+ * (rows cut into parts): ask for each n.  Pure host function. */
 size_t qlora_distill_workspace_bytes(int64_t n, int64_t vocab, int32_t k, int32_t cd);
 
 /* Workspace size in bytes for op (QLORA_OP_FWD / QLORA_OP_BWD, optionally OR'ed
