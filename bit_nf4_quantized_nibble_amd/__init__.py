@@ -20,6 +20,10 @@ Public API (names follow the pages' problem statement):
     distill_loss_grad(logits, top_values, top_index, temperature=1.0, weight=None, need_grad=True, dlogits=None,
                       row_kl=None) -> (loss [1] fp32, dlogits or None)
     StackLayer.create(q, a32, b32, dtype) ; stack_train_step(layers, x, target, alpha, step, ...)
+    linear_fwd_dropout(q, x, lora_a, lora_b, alpha, p, seed, ...) ; linear_bwd_dropout(q, x, dy, ..., p, seed, ...)
+    linear_fwd_gated((q_gate, q_up), x, lora_as, lora_bs, alphas, act="silu", bias=None, save=False) -> h
+    linear_bwd_gated((q_gate, q_up), x, dh, lora_as, lora_bs, alphas, pre, act="silu", ...) -> (dX, dAs, dBs)
+    quantize_fp8(w) -> Fp8Weight ; linear_fp8(w, x, bias=None)
     quantize_int8(w) -> Int8Weight ; linear_int8(w, x, bias=None) ; linear_int8_experts(w, x, offsets, bias=None)
     workspace_bytes(op, m, rows, cols, r, dtype, flags=0) ; levels()
 
@@ -37,7 +41,7 @@ from dataclasses import dataclass
 from typing import Optional, Tuple
 
 from . import _lib
-from ._lib import QloraError, QloraInt8, QloraNf4  # noqa: F401
+from ._lib import QloraError, QloraFp8, QloraInt8, QloraNf4  # noqa: F401
 
 __all__ = ["NF4Weight", "quantize", "dequantize", "linear_fwd", "linear_bwd", "merge", "workspace_bytes",
            "linear_fwd_noalloc", "linear_fwd_cached",
@@ -45,7 +49,9 @@ __all__ = ["NF4Weight", "quantize", "dequantize", "linear_fwd", "linear_bwd", "m
            "adamw_step", "StackLayer", "stack_train_step", "stack_workspace_bytes",
            "linear_fwd_group", "linear_bwd_group", "group_workspace_bytes",
            "Int8Weight", "quantize_int8", "linear_int8", "linear_int8_experts", "int8_workspace_bytes",
-           "distill_loss_grad"]
+           "distill_loss_grad", "linear_fwd_dropout", "linear_bwd_dropout",
+           "linear_fwd_gated", "linear_bwd_gated", "gated_workspace_bytes", "Fp8Weight", "quantize_fp8", "linear_fp8",
+           "fp8_workspace_bytes"]
 
 
 def _torch():
@@ -464,6 +470,184 @@ def linear_bwd(q: NF4Weight, x, dy, lora_a, lora_b, alpha: float, t_saved=None, 
     return dx, da, db
 
 
+def _check_like(name, t, device, dtype, shape):
+    """A contiguous ``dtype`` tensor of ``shape`` on ``device``."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError("%s must be a GPU tensor on %s" % (name, device))
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must be contiguous and of shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+def _check_adapter(q, lora_a, lora_b, device, dtype, at=""):
+    if q.device != device:
+        raise ValueError("the weight%s is on %s, x on %s" % (at, q.device, device))
+    if lora_a.dim() != 2:
+        raise ValueError("lora_a%s must be [r, %d]" % (at, q.cols))
+    r = lora_a.shape[0]
+    _check_like("lora_a" + at, lora_a, device, dtype, (r, q.cols))
+    _check_like("lora_b" + at, lora_b, device, dtype, (q.rows, r))
+    return r
+
+
+def _grad_code(grad_dtype, dtype):
+    torch = _torch()
+    grad_dtype = torch.float32 if grad_dtype is None else grad_dtype
+    if grad_dtype not in (torch.float32, dtype):
+        raise TypeError("grad_dtype must be torch.float32 or %s, got %s" % (dtype, grad_dtype))
+    return grad_dtype, dtype_code(grad_dtype)
+
+
+def _dropout_call(q, x, lora_a, lora_b, p, seed, rslora, path):
+    """What the two seeded dropout calls share: (x as tokens, lead, rank, flags)."""
+    torch = _torch()
+    if not x.is_cuda:
+        raise ValueError("x must be a GPU tensor")
+    dtype_code(x.dtype)
+    x2, lead = _flatten(x, q.cols)
+    r = _check_adapter(q, lora_a, lora_b, x.device, x.dtype)
+    _check_like("seed", seed, x.device, torch.int64, (2,))
+    if not 0.0 <= p < 1.0:
+        raise ValueError("p must lie in [0, 1), got %r" % (p,))
+    return x2.contiguous(), lead, r, _flags(rslora, path)
+
+
+def linear_fwd_dropout(q: NF4Weight, x, lora_a, lora_b, alpha: float, p: float, seed, bias=None, save_t: bool = False,
+                       rslora: bool = False, workspace=None, out=None, path: str = "auto"):
+    """``linear_fwd`` with LoRA dropout whose mask is drawn on the fly and never stored: the
+    low-rank branch reads x * M / (1 - p), M[i, k] from Philox 4x32-10 under ``seed``, an int64
+    GPU tensor [2] = (seed, offset) that is read on the device (a captured call draws anew at each
+    replay that finds other values there).  p counts in 65536ths (rounded to the nearest, at most
+    65535).  Returns y, or (y, T0) with T0 = (x M) A^T in fp32 when save_t; the backward takes
+    the same seed and offset."""
+    torch = _torch()
+    x2, lead, r, flags = _dropout_call(q, x, lora_a, lora_b, p, seed, rslora, path)
+    dt, m = x2.dtype, x2.shape[0]
+    if bias is not None:
+        _check_tensor("bias", bias, x.device, dt, q.rows)
+    if out is None:
+        y = torch.empty(m, q.rows, dtype=dt, device=x.device)
+    else:
+        _check_tensor("out", out, x.device, dt, m * q.rows)
+        y = out
+    t0 = torch.empty(m, r, dtype=torch.float32, device=x.device) if save_t else None
+    if m:
+        ws = _workspace_on(x.device, workspace_bytes(_lib.QLORA_OP_FWD, m, q.rows, q.cols, r, dt,
+                                                     flags | _lib.QLORA_FLAG_DROPOUT), workspace)
+        d = q.descriptor()
+        _launch(x.device, _lib.lib().qlora_linear_fwd_dropout_seeded, ctypes.byref(d), _ptr(x2), m, _ptr(lora_a),
+                _ptr(lora_b), r, float(alpha), flags, _ptr(bias), dtype_code(dt), _ptr(seed), float(p), _ptr(y), _ptr(t0),
+                _ptr(ws), ws.numel() * ws.element_size())
+    y = y.view(*lead, q.rows)
+    return (y, t0) if save_t else y
+
+
+def linear_bwd_dropout(q: NF4Weight, x, dy, lora_a, lora_b, alpha: float, p: float, seed, t_saved=None,
+                       need_dx: bool = True, rslora: bool = False, grad_dtype=None, workspace=None, path: str = "auto"):
+    """Gradients of ``linear_fwd_dropout`` with the base frozen, under the forward's p and seed:
+    (dX or None, dA [r, cols], dB [rows, r]); ``t_saved`` is the forward's T0 (else recomputed).
+    ``grad_dtype``: torch.float32 (the default, what ``adamw_step`` takes) or x's dtype."""
+    torch = _torch()
+    x2, lead, r, flags = _dropout_call(q, x, lora_a, lora_b, p, seed, rslora, path)
+    dt, m = x2.dtype, x2.shape[0]
+    dy2 = _flatten(dy, q.rows)[0].contiguous()
+    _check_like("dy", dy2, x.device, dt, (m, q.rows))
+    if t_saved is not None:
+        _check_like("t_saved", t_saved, x.device, torch.float32, (m, r))
+    gt, gd = _grad_code(grad_dtype, dt)
+    dx = torch.empty(m, q.cols, dtype=dt, device=x.device) if need_dx else None
+    da = torch.empty(r, q.cols, dtype=gt, device=x.device)
+    db = torch.empty(q.rows, r, dtype=gt, device=x.device)
+    ws = _workspace_on(x.device, workspace_bytes(_lib.QLORA_OP_BWD, m, q.rows, q.cols, r, dt,
+                                                 flags | _lib.QLORA_FLAG_DROPOUT), workspace)
+    d = q.descriptor()
+    _launch(x.device, _lib.lib().qlora_linear_bwd_dropout_seeded, ctypes.byref(d), _ptr(x2), _ptr(dy2), m, _ptr(lora_a),
+            _ptr(lora_b), r, float(alpha), flags, dtype_code(dt), _ptr(seed), float(p), _ptr(t_saved), gd, _ptr(dx),
+            _ptr(da), _ptr(db), _ptr(ws), ws.numel() * ws.element_size())
+    return (None if dx is None else dx.view(*lead, q.cols)), da, db
+
+
+def gated_workspace_bytes(op: int, qs, m: int, ranks, dtype) -> int:
+    """Workspace bytes of linear_fwd_gated (op QLORA_OP_FWD) or linear_bwd_gated (QLORA_OP_BWD)."""
+    ga = _GroupArgs(qs)
+    ga.r = (ctypes.c_int32 * ga.g)(*[int(r) for r in ranks])
+    return int(_lib.lib().qlora_gated_workspace_bytes(op, ga.w, m, ga.r, dtype_code(dtype)))
+
+
+def _gated_call(qs, x, lora_as, lora_bs, alphas, act):
+    if len(qs) != 2 or len(lora_as) != 2 or len(lora_bs) != 2 or len(alphas) != 2:
+        raise ValueError("a gated block takes two projections (gate, up) with an adapter and an alpha each")
+    if act not in _lib.QLORA_ACTS:
+        raise ValueError("act must be one of %s, got %r" % (sorted(_lib.QLORA_ACTS), act))
+    if qs[0].rows != qs[1].rows or qs[0].cols != qs[1].cols:
+        raise ValueError("gate is [%d, %d], up [%d, %d]" % (qs[0].rows, qs[0].cols, qs[1].rows, qs[1].cols))
+    if not x.is_cuda:
+        raise ValueError("x must be a GPU tensor")
+    dtype_code(x.dtype)
+    x2, lead = _flatten(x, qs[0].cols)
+    ranks = [_check_adapter(q, a, b, x.device, x.dtype, "[%d]" % i)
+             for i, (q, a, b) in enumerate(zip(qs, lora_as, lora_bs))]
+    return x2.contiguous(), lead, ranks, _GroupArgs(qs, lora_as, lora_bs, alphas)
+
+
+def linear_fwd_gated(qs, x, lora_as, lora_bs, alphas, act: str = "silu", bias=None, save: bool = False,
+                     rslora: bool = False, workspace=None, out=None):
+    """The gated feed-forward block over two projections of the same x, qs = (gate, up):
+    h [m, rows] = act(g) u with g and u as ``linear_fwd`` gives them; act "silu", "gelu" or
+    "gelu_tanh"; bias, if given, is [2 rows] (gate, then up).  With ``save`` returns (h, pre, ts)
+    for the backward: pre [m, 2 rows] = [g | u] in x's dtype, ts the T0_i = x A_i^T in fp32."""
+    torch = _torch()
+    x2, lead, ranks, ga = _gated_call(qs, x, lora_as, lora_bs, alphas, act)
+    dt, m, rows, device = x2.dtype, x2.shape[0], qs[0].rows, x.device
+    if bias is not None:
+        _check_tensor("bias", bias, device, dt, 2 * rows)
+    if out is None:
+        h = torch.empty(m, rows, dtype=dt, device=device)
+    else:
+        _check_tensor("out", out, device, dt, m * rows)
+        h = out
+    pre = torch.empty(m, 2 * rows, dtype=dt, device=device) if save else None
+    ts = [torch.empty(m, r, dtype=torch.float32, device=device) for r in ranks] if save else None
+    if m:
+        lib, code = _lib.lib(), dtype_code(dt)
+        ws = _workspace_on(device, int(lib.qlora_gated_workspace_bytes(_lib.QLORA_OP_FWD, ga.w, m, ga.r, code)), workspace)
+        _launch(device, lib.qlora_linear_fwd_gated, ga.w, _ptr(x2), m, ga.a, ga.b, ga.r, ga.alpha,
+                _lib.QLORA_FLAG_RSLORA if rslora else 0, _lib.QLORA_ACTS[act], _ptr(bias), code, _ptr(h), _ptr(pre),
+                _GroupArgs.ptrs(ts), _ptr(ws), ws.numel() * ws.element_size())
+    h = h.view(*lead, rows)
+    return (h, pre, ts) if save else h
+
+
+def linear_bwd_gated(qs, x, dh, lora_as, lora_bs, alphas, pre, act: str = "silu", t_saved=None, need_dx: bool = True,
+                     rslora: bool = False, grad_dtype=None, workspace=None):
+    """Gradients of ``linear_fwd_gated`` with the bases frozen, from dh [m, rows] and the ``pre``
+    it saved: (dX or None, [dA_gate, dA_up], [dB_gate, dB_up]).  ``t_saved``: its ts (else
+    recomputed).  ``grad_dtype``: the adapters' gradients in torch.float32 (the default, what
+    ``adamw_step`` takes) or x's dtype."""
+    torch = _torch()
+    x2, lead, ranks, ga = _gated_call(qs, x, lora_as, lora_bs, alphas, act)
+    dt, m, rows, cols, device = x2.dtype, x2.shape[0], qs[0].rows, qs[0].cols, x.device
+    dh2 = _flatten(dh, rows)[0].contiguous()
+    _check_like("dh", dh2, device, dt, (m, rows))
+    _check_tensor("pre", pre, device, dt, m * 2 * rows)
+    if t_saved is not None:
+        if len(t_saved) != 2:
+            raise ValueError("t_saved must hold two tensors")
+        for i, (t, r) in enumerate(zip(t_saved, ranks)):
+            _check_like("t_saved[%d]" % i, t, device, torch.float32, (m, r))
+    gt, gd = _grad_code(grad_dtype, dt)
+    dx = torch.empty(m, cols, dtype=dt, device=device) if need_dx else None
+    das = [torch.empty(r, cols, dtype=gt, device=device) for r in ranks]
+    dbs = [torch.empty(rows, r, dtype=gt, device=device) for r in ranks]
+    lib, code = _lib.lib(), dtype_code(dt)
+    ws = _workspace_on(device, int(lib.qlora_gated_workspace_bytes(_lib.QLORA_OP_BWD, ga.w, m, ga.r, code)), workspace)
+    _launch(device, lib.qlora_linear_bwd_gated, ga.w, _ptr(x2), _ptr(dh2), _ptr(pre), m, ga.a, ga.b, ga.r, ga.alpha,
+            _lib.QLORA_FLAG_RSLORA if rslora else 0, _lib.QLORA_ACTS[act], code, _GroupArgs.ptrs(t_saved), gd, _ptr(dx),
+            _GroupArgs.ptrs(das), _GroupArgs.ptrs(dbs), _ptr(ws), ws.numel() * ws.element_size())
+    return (None if dx is None else dx.view(*lead, cols)), das, dbs
+
+
 def merge(q: NF4Weight, lora_a, lora_b, alpha: float, rslora: bool = False, out=None):
     """Dense merged weight RNE(w_hat + s B A) [rows, cols] in the adapters' dtype
     (never re-quantized to NF4).  ``out`` may supply a preallocated output."""
@@ -694,6 +878,114 @@ def linear_int8_experts(w: Int8Weight, x, offsets, bias=None, out=None, workspac
     without ``out``)."""
     _check_tensor("offsets", offsets, x.device, _torch().int32, w.experts + 1)
     return _int8_call(w, x, offsets, bias, out, workspace)
+
+
+@dataclass
+class Fp8Weight:
+    """A weight [rows, cols] in 8-bit floats (e4m3) with a power-of-two scale for each block of
+    128 x 128, held in device memory."""
+    rows: int
+    cols: int
+    codes: "object"        # uint8 [rows, ld], ld = cols rounded up to 128, zeros past cols
+    scale: "object"        # uint8 [ceil(rows / 128), ceil(cols / 512) * 4]: exponents + 127
+
+    @property
+    def shape(self) -> Tuple[int, ...]:
+        return (self.rows, self.cols)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def size_bytes(self) -> int:
+        return self.codes.numel() + self.scale.numel()
+
+    def __getstate__(self):  # the descriptor holds addresses: a copy makes its own
+        return {k: v for k, v in self.__dict__.items() if k != "_made"}
+
+    def descriptor(self) -> QloraFp8:
+        # Kept between calls as long as all it was made from is the same (as Int8Weight's).
+        c, s = self.codes, self.scale
+        key = (self.rows, self.cols, c.data_ptr(), s.data_ptr(), c.shape, s.shape, c.dtype, s.dtype, c.is_contiguous(),
+               s.is_contiguous())
+        made = self.__dict__.get("_made")
+        if made is None or made[0] != key:
+            torch = _torch()
+            for name, t, shape in (("codes", c, _fp8_shapes(self.rows, self.cols)[0]),
+                                   ("scale", s, _fp8_shapes(self.rows, self.cols)[1])):
+                if t.dtype != torch.uint8 or tuple(t.shape) != shape or not t.is_contiguous() or not t.is_cuda or \
+                        t.device != c.device:
+                    raise ValueError("%s must be a contiguous uint8 GPU tensor of shape %s" % (name, shape))
+            made = self.__dict__["_made"] = (key, QloraFp8(self.rows, self.cols, 0, _ptr(c), _ptr(s)))
+        return made[1]
+
+
+def _fp8_shapes(rows, cols):
+    return (rows, (cols + 127) // 128 * 128), ((rows + 127) // 128, (cols + 511) // 512 * 4)
+
+
+def quantize_fp8(w) -> Fp8Weight:
+    """8-bit floats and one power-of-two scale per block of 128 x 128 of a [rows, cols] weight
+    (fp32, bf16 or f16; for instance the dense result of ``merge``).  Rows may be strided."""
+    torch = _torch()
+    if not w.is_cuda:
+        raise ValueError("w must be a GPU tensor")
+    if w.dim() != 2:
+        raise ValueError("w must be [rows, cols]")
+    rows, cols = w.shape
+    if cols > _lib.QLORA_FP8_MAX_COLS:  # before anything is allocated
+        raise QloraError(-4, "fp8_quantize: %d cols (at most %d)" % (cols, _lib.QLORA_FP8_MAX_COLS))
+    code = dtype_code(w.dtype)
+    shapes = _fp8_shapes(rows, cols)
+    q = Fp8Weight(rows, cols, torch.empty(shapes[0], dtype=torch.uint8, device=w.device),
+                  torch.empty(shapes[1], dtype=torch.uint8, device=w.device))
+    if rows == 0 or cols == 0:
+        return q
+    w2, ldw, _ = _strided_rows(w, cols)
+    d = q.descriptor()
+    _launch(w.device, _lib.lib().qlora_fp8_quantize, _ptr(w2), ldw, code, ctypes.byref(d))
+    return q
+
+
+@functools.lru_cache(maxsize=4096)
+def _fp8_bytes(rows, cols, m, code):
+    d = QloraFp8(rows, cols, 0, None, None)
+    return int(_lib.lib().qlora_fp8_workspace_bytes(ctypes.byref(d), m, code))
+
+
+def fp8_workspace_bytes(w: Fp8Weight, m: int, dtype) -> int:
+    """Workspace bytes of linear_fp8 on m tokens of ``dtype``."""
+    return _fp8_bytes(w.rows, w.cols, m, dtype_code(dtype))
+
+
+def linear_fp8(w: Fp8Weight, x, bias=None, out=None, workspace=None):
+    """y = x . W^T (+ bias) in 8-bit floats: each block of 128 columns of a row of x gets a scale
+    of its own and is brought to 8 bits within the call, the products are summed in fp32, y has x's
+    dtype.  Leading dims of x are flattened to tokens; rows of x may be strided.  ``out`` may
+    supply a preallocated output, which must not overlap x."""
+    torch = _torch()
+    dt, device = x.dtype, x.device
+    code = dtype_code(dt)
+    if not x.is_cuda:
+        raise ValueError("x must be a GPU tensor")
+    if w.codes.device != device:
+        raise ValueError("w is on %s, x on %s" % (w.codes.device, device))
+    x2, ldx, lead = _strided_rows(x, w.cols)
+    m = x2.shape[0]
+    if out is None:
+        y = torch.empty(m, w.rows, dtype=dt, device=device)
+    else:
+        _check_tensor("out", out, device, dt, m * w.rows)
+        y = out
+    if bias is not None:
+        _check_tensor("bias", bias, device, dt, w.rows)
+    d = ctypes.byref(w.descriptor())
+    ws = _workspace_on(device, _fp8_bytes(w.rows, w.cols, m, code), workspace)
+    _launch(device, _lib.lib().qlora_fp8_linear, d, x2.data_ptr(), m, ldx, _ptr(bias), code, y.data_ptr(), ws.data_ptr(),
+            ws.numel() * ws.element_size())
+    if lead is None and y.dim() == 2:
+        return y if y.shape[1] == w.rows else y.view(m, w.rows)
+    return y.view(*((m,) if lead is None else lead), w.rows)
 
 
 def distill_loss_grad(logits, top_values, top_index, temperature: float = 1.0, weight=None, need_grad: bool = True,

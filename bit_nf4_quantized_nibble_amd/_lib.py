@@ -32,14 +32,19 @@ EXPORTED = (
     "qlora_linear_fwd_group", "qlora_linear_bwd_group", "qlora_group_workspace_bytes",
     "qlora_int8_quantize", "qlora_int8_linear", "qlora_int8_linear_experts", "qlora_int8_workspace_bytes",
     "qlora_distill_loss_grad", "qlora_distill_workspace_bytes",
+    "qlora_fp8_quantize", "qlora_fp8_linear", "qlora_fp8_workspace_bytes",
+    "qlora_linear_fwd_gated", "qlora_linear_bwd_gated", "qlora_gated_workspace_bytes",
+    "qlora_linear_fwd_dropout_seeded", "qlora_linear_bwd_dropout_seeded",
 )
 QLORA_GROUP_MAX = 8
 QLORA_MSE_WORKSPACE_BYTES = 4096
 QLORA_INT8_MAX_COLS = 131072
 QLORA_DISTILL_MAX_K = 1024
+QLORA_FP8_MAX_COLS = 131072
+QLORA_ACTS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
 KERNEL_KINDS = ("quantize", "dequantize", "lora_down", "reduce", "fwd_gemm", "gemv",
                 "bwd_dt", "bwd_dx", "bwd_da", "bwd_db", "merge", "loss", "optim",
-                "int8_rows", "int8_gemm")
+                "int8_rows", "int8_gemm", "fp8_rows", "fp8_gemm", "gate")
 
 
 class QloraNf4(ctypes.Structure):
@@ -62,6 +67,12 @@ class QloraInt8(ctypes.Structure):
     """Mirror of qlora_int8_t."""
     _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("experts", ctypes.c_int32),
                 ("reserved", ctypes.c_int32), ("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class QloraFp8(ctypes.Structure):
+    """Mirror of qlora_fp8_t."""
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("reserved", ctypes.c_int64),
+                ("codes", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
 
 
 class QloraAdamW(ctypes.Structure):
@@ -135,7 +146,22 @@ def _declare(lib):
                                             vp, sz, vp]
     lib.qlora_distill_workspace_bytes.argtypes = [i64, i64, i32, i32]
     lib.qlora_distill_workspace_bytes.restype = sz
-    for name in ("qlora_int8_quantize", "qlora_int8_linear", "qlora_int8_linear_experts", "qlora_distill_loss_grad",
+    PF = ctypes.POINTER(QloraFp8)
+    lib.qlora_fp8_quantize.argtypes = [vp, i64, i32, PF, vp]
+    lib.qlora_fp8_linear.argtypes = [PF, vp, i64, i64, vp, i32, vp, vp, sz, vp]
+    lib.qlora_fp8_workspace_bytes.argtypes = [PF, i64, i32]
+    lib.qlora_fp8_workspace_bytes.restype = sz
+    lib.qlora_linear_fwd_gated.argtypes = [vp, vp, i64, vp, vp, vp, vp, i32, i32, vp, i32, vp, vp, vp, vp, sz, vp]
+    lib.qlora_linear_bwd_gated.argtypes = [vp, vp, vp, vp, i64, vp, vp, vp, vp, i32, i32, i32, vp, i32, vp, vp, vp, vp,
+                                           sz, vp]
+    lib.qlora_gated_workspace_bytes.argtypes = [i32, vp, i64, vp, i32]
+    lib.qlora_gated_workspace_bytes.restype = sz
+    lib.qlora_linear_fwd_dropout_seeded.argtypes = [P, vp, i64, vp, vp, i32, f32, i32, vp, i32, vp, f32, vp, vp, vp, sz,
+                                                    vp]
+    lib.qlora_linear_bwd_dropout_seeded.argtypes = [P, vp, vp, i64, vp, vp, i32, f32, i32, i32, vp, f32, vp, i32, vp, vp,
+                                                    vp, vp, sz, vp]
+    for name in ("qlora_fp8_quantize", "qlora_fp8_linear", "qlora_linear_fwd_gated", "qlora_linear_bwd_gated",
+                 "qlora_linear_fwd_dropout_seeded", "qlora_linear_bwd_dropout_seeded", "qlora_int8_quantize", "qlora_int8_linear", "qlora_int8_linear_experts", "qlora_distill_loss_grad",
                  "qlora_nf4_quantize", "qlora_nf4_dequantize", "qlora_linear_fwd",
                  "qlora_linear_bwd", "qlora_nf4_levels", "qlora_abi_version",
                  "qlora_profile_enable", "qlora_profile_read", "qlora_merge", "qlora_mse_loss_grad",

@@ -17,6 +17,7 @@
 
 #include "common.h"
 #include "int8_distill.h"
+#include "mlp.h"
 
 namespace qnf4 {
 
@@ -230,7 +231,8 @@ int64_t g_prof_n[QLORA_K_COUNT];
 
 const char* kKernelNames[QLORA_K_COUNT] = {
     "quantize", "dequantize", "lora_down", "reduce", "fwd_gemm", "gemv",
-    "bwd_dt",   "bwd_dx",     "bwd_da",    "bwd_db", "merge", "loss", "optim", "int8_rows", "int8_gemm"};
+    "bwd_dt",   "bwd_dx",     "bwd_da",    "bwd_db", "merge", "loss", "optim", "int8_rows", "int8_gemm",
+    "fp8_rows", "fp8_gemm",   "gate"};
 
 // Wait for every recorded pair and fold it into the totals (lock held).
 int prof_drain() {
@@ -390,13 +392,13 @@ size_t qlora_workspace_bytes(int32_t op, int64_t m, int64_t rows, int64_t cols, 
 namespace {
 int fwd_impl(const qlora_nf4_t* w, const void* x, int64_t m, const void* lora_a, const void* lora_b, int32_t r,
              float alpha, int32_t flags, const void* bias, int32_t cd, const uint8_t* mask, float p, void* y,
-             float* t_save, void* ws, size_t ws_bytes, void* stream, const char* who) {
+             float* t_save, void* ws, size_t ws_bytes, void* stream, const char* who, const Seeded* sd = nullptr) {
   int rc = validate_layer(w, x, m, lora_a, lora_b, r, alpha, flags, cd, who);
   if (rc) return rc;
   if (!y) return set_error(QLORA_ERR_INVALID_ARG, "%s: null y", who);
   if ((rc = check_aligned(who, "y, bias, t_save and the dropout mask", {y, bias, t_save, mask}))) return rc;
   if (m == 0) return QLORA_OK;
-  if (mask) flags |= QLORA_FLAG_DROPOUT;
+  if (mask || sd) flags |= QLORA_FLAG_DROPOUT;
   if ((rc = check_ws(ws, ws_bytes, fwd_workspace_bytes(m, w->rows, w->cols, r, cd, flags), who))) return rc;
   if ((rc = check_tables(who))) return rc;
   LayerCall c;
@@ -404,7 +406,7 @@ int fwd_impl(const qlora_nf4_t* w, const void* x, int64_t m, const void* lora_a,
   c.cd = cd;
   c.m = m;
   c.r = r;
-  c.scale = mask ? (float)((double)lora_scale(alpha, r, flags) / (1.0 - (double)p)) : lora_scale(alpha, r, flags);
+  c.scale = mask || sd ? (float)((double)lora_scale(alpha, r, flags) / (1.0 - (double)p)) : lora_scale(alpha, r, flags);
   c.flags = flags;
   c.x = x;
   c.drop_mask = mask;
@@ -414,20 +416,20 @@ int fwd_impl(const qlora_nf4_t* w, const void* x, int64_t m, const void* lora_a,
   c.ws = ws;
   c.ws_bytes = ws_bytes;
   c.stream = (hipStream_t)stream;
-  return launch_forward(c, y, t_save);
+  return sd ? launch_forward_seeded(c, *sd, y, t_save) : launch_forward(c, y, t_save);
 }
 
 int bwd_impl(const qlora_nf4_t* w, const void* x, const void* dy, int64_t m, const void* lora_a,
              const void* lora_b, int32_t r, float alpha, int32_t flags, int32_t cd, const uint8_t* mask, float p,
-             const float* t_saved, void* dx, float* d_a, float* d_b, void* ws, size_t ws_bytes, void* stream,
-             const char* who) {
+             const float* t_saved, void* dx, void* d_a, void* d_b, void* ws, size_t ws_bytes, void* stream,
+             const char* who, const Seeded* sd = nullptr, int32_t gd = QLORA_F32) {
   int rc = validate_layer(w, x, m, lora_a, lora_b, r, alpha, flags, cd, who);
   if (rc) return rc;
   if (!dy || !d_a || !d_b) return set_error(QLORA_ERR_INVALID_ARG, "%s: null dy / d_a / d_b", who);
   if ((rc = check_aligned(who, "dy, dx, d_a, d_b, t_saved and the dropout mask", {dy, dx, d_a, d_b, t_saved, mask})))
     return rc;
   if (m == 0) return set_error(QLORA_ERR_SHAPE, "%s: m must be >= 1 (dA, dB would be all zero)", who);
-  if (mask) flags |= QLORA_FLAG_DROPOUT;
+  if (mask || sd) flags |= QLORA_FLAG_DROPOUT;
   if ((rc = check_ws(ws, ws_bytes, bwd_workspace_bytes(m, w->rows, w->cols, r, cd, flags), who))) return rc;
   if ((rc = check_tables(who))) return rc;
   LayerCall c;
@@ -435,7 +437,7 @@ int bwd_impl(const qlora_nf4_t* w, const void* x, const void* dy, int64_t m, con
   c.cd = cd;
   c.m = m;
   c.r = r;
-  c.scale = mask ? (float)((double)lora_scale(alpha, r, flags) / (1.0 - (double)p)) : lora_scale(alpha, r, flags);
+  c.scale = mask || sd ? (float)((double)lora_scale(alpha, r, flags) / (1.0 - (double)p)) : lora_scale(alpha, r, flags);
   c.flags = flags;
   c.x = x;
   c.drop_mask = mask;
@@ -445,7 +447,24 @@ int bwd_impl(const qlora_nf4_t* w, const void* x, const void* dy, int64_t m, con
   c.ws = ws;
   c.ws_bytes = ws_bytes;
   c.stream = (hipStream_t)stream;
-  return launch_backward(c, dy, t_saved, dx, d_a, d_b);
+  return launch_backward_as(c, sd, dy, t_saved, dx, d_a, d_b, gd);
+}
+
+int check_gd(int32_t gd, int32_t cd, const char* who) {
+  if (gd != QLORA_F32 && gd != cd)
+    return set_error(QLORA_ERR_DTYPE, "%s: gradients in dtype %d (fp32 or the compute dtype)", who, gd);
+  return QLORA_OK;
+}
+
+// The generator of a seeded call, and its rate: a whole number of 65536ths.
+int make_seeded(const uint64_t* seed, float& p, Seeded& sd, const char* who) {
+  if (!seed || ((uintptr_t)seed & 7u))
+    return set_error(QLORA_ERR_INVALID_ARG, "%s: seed must be non-null and 8-byte aligned", who);
+  if (!(p >= 0.f && p < 1.f)) return set_error(QLORA_ERR_INVALID_ARG, "%s: dropout rate %g outside [0, 1)", who, p);
+  sd.seed = seed;
+  sd.threshold = (uint32_t)std::min(65535.0, floor((double)p * 65536.0 + 0.5));
+  p = (float)sd.threshold / 65536.f;
+  return QLORA_OK;
 }
 
 int check_dropout(const uint8_t* mask, float p, const char* who) {
@@ -607,7 +626,7 @@ int build_group(int32_t g, const qlora_nf4_t* const* w, const void* x, int64_t m
   return QLORA_OK;
 }
 
-int check_group_ptrs(const char* who, int32_t g, float* const* a, const char* name) {
+int check_group_ptrs(const char* who, int32_t g, const void* const* a, const char* name) {
   if (!a) return QLORA_OK;
   for (int i = 0; i < g; ++i)
     if (a[i] && !aligned16(a[i])) return set_error(QLORA_ERR_INVALID_ARG, "%s: %s[%d] must be 16-byte aligned", who, name, i);
@@ -626,7 +645,7 @@ int qlora_linear_fwd_group(int32_t g, const qlora_nf4_t* const* w, const void* x
   if (rc) return rc;
   if (!y) return set_error(QLORA_ERR_INVALID_ARG, "%s: null y", who);
   if ((rc = check_aligned(who, "y and bias", {y, bias}))) return rc;
-  if ((rc = check_group_ptrs(who, g, t_save, "t_save"))) return rc;
+  if ((rc = check_group_ptrs(who, g, (const void* const*)t_save, "t_save"))) return rc;
   if (m == 0) return QLORA_OK;
   if ((rc = check_ws(ws, ws_bytes, group_workspace_bytes(QLORA_OP_FWD, gc), who))) return rc;
   if ((rc = check_tables(who))) return rc;
@@ -647,8 +666,8 @@ int qlora_linear_bwd_group(int32_t g, const qlora_nf4_t* const* w, const void* x
   for (int i = 0; i < g; ++i)
     if (!d_a[i] || !d_b[i]) return set_error(QLORA_ERR_INVALID_ARG, "%s: null d_a[%d] / d_b[%d]", who, i, i);
   if ((rc = check_aligned(who, "dy and dx", {dy, dx}))) return rc;
-  if ((rc = check_group_ptrs(who, g, d_a, "d_a")) || (rc = check_group_ptrs(who, g, d_b, "d_b")) ||
-      (rc = check_group_ptrs(who, g, (float* const*)t_saved, "t_saved")))
+  if ((rc = check_group_ptrs(who, g, (const void* const*)d_a, "d_a")) || (rc = check_group_ptrs(who, g, (const void* const*)d_b, "d_b")) ||
+      (rc = check_group_ptrs(who, g, (const void* const*)t_saved, "t_saved")))
     return rc;
   if (m == 0) return set_error(QLORA_ERR_SHAPE, "%s: m must be >= 1 (dA, dB would be all zero)", who);
   if ((rc = check_ws(ws, ws_bytes, group_workspace_bytes(QLORA_OP_BWD, gc), who))) return rc;
@@ -664,6 +683,102 @@ size_t qlora_group_workspace_bytes(int32_t op, int32_t g, const qlora_nf4_t* con
                   gc))
     return 0;
   return group_workspace_bytes(op, gc);
+}
+
+namespace {
+// The gated block's two projections (a group of two with equal rows).
+int build_gated(const qlora_nf4_t* const* w, const void* x, int64_t m, const void* const* lora_a,
+                const void* const* lora_b, const int32_t* r, const float* alpha, int32_t flags, int32_t cd, void* ws,
+                size_t ws_bytes, void* stream, bool query, const char* who, GroupCall& gc) {
+  const int rc = build_group(2, w, x, m, lora_a, lora_b, r, alpha, flags, cd, ws, ws_bytes, stream, query, who, gc);
+  if (rc) return rc;
+  if (w[0]->rows != w[1]->rows)
+    return set_error(QLORA_ERR_SHAPE, "%s: gate has %lld rows, up %lld", who, (long long)w[0]->rows,
+                     (long long)w[1]->rows);
+  return QLORA_OK;
+}
+int check_act(int32_t act, const char* who) {
+  if (act < QLORA_ACT_SILU || act > QLORA_ACT_GELU_TANH)
+    return set_error(QLORA_ERR_INVALID_ARG, "%s: unknown activation %d", who, act);
+  return QLORA_OK;
+}
+}  // namespace
+
+int qlora_linear_fwd_gated(const qlora_nf4_t* const* w, const void* x, int64_t m, const void* const* lora_a,
+                           const void* const* lora_b, const int32_t* r, const float* alpha, int32_t flags, int32_t act,
+                           const void* bias, int32_t cd, void* h, void* pre, float* const* t_save, void* ws,
+                           size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  const char* who = "linear_fwd_gated";
+  GroupCall gc;
+  int rc = build_gated(w, x, m, lora_a, lora_b, r, alpha, flags, cd, ws, ws_bytes, stream, false, who, gc);
+  if (rc || (rc = check_act(act, who))) return rc;
+  if (!h) return set_error(QLORA_ERR_INVALID_ARG, "%s: null h", who);
+  if ((rc = check_aligned(who, "h, pre and bias", {h, pre, bias}))) return rc;
+  if ((rc = check_group_ptrs(who, 2, (const void* const*)t_save, "t_save"))) return rc;
+  if (m == 0) return QLORA_OK;
+  if ((rc = check_ws(ws, ws_bytes, gated_workspace_bytes(QLORA_OP_FWD, gc), who))) return rc;
+  if ((rc = check_tables(who))) return rc;
+  return launch_gated_fwd(gc, act, bias, h, pre, t_save, ws, (hipStream_t)stream);
+}
+
+int qlora_linear_bwd_gated(const qlora_nf4_t* const* w, const void* x, const void* dh, const void* pre, int64_t m,
+                           const void* const* lora_a, const void* const* lora_b, const int32_t* r, const float* alpha,
+                           int32_t flags, int32_t act, int32_t cd, const float* const* t_saved, int32_t gd, void* dx,
+                           void* const* d_a, void* const* d_b, void* ws, size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  const char* who = "linear_bwd_gated";
+  GroupCall gc;
+  int rc = build_gated(w, x, m, lora_a, lora_b, r, alpha, flags, cd, ws, ws_bytes, stream, false, who, gc);
+  if (rc || (rc = check_act(act, who)) || (rc = check_gd(gd, cd, who))) return rc;
+  if (!dh || !pre || !d_a || !d_b || !d_a[0] || !d_a[1] || !d_b[0] || !d_b[1])
+    return set_error(QLORA_ERR_INVALID_ARG, "%s: null dh / pre / d_a / d_b", who);
+  if ((rc = check_aligned(who, "dh, pre and dx", {dh, pre, dx}))) return rc;
+  if ((rc = check_group_ptrs(who, 2, d_a, "d_a")) || (rc = check_group_ptrs(who, 2, d_b, "d_b")) ||
+      (rc = check_group_ptrs(who, 2, (const void* const*)t_saved, "t_saved")))
+    return rc;
+  if (m == 0) return set_error(QLORA_ERR_SHAPE, "%s: m must be >= 1 (dA, dB would be all zero)", who);
+  if ((rc = check_ws(ws, ws_bytes, gated_workspace_bytes(QLORA_OP_BWD, gc), who))) return rc;
+  if ((rc = check_tables(who))) return rc;
+  return launch_gated_bwd(gc, act, dh, pre, t_saved, dx, d_a, d_b, gd, ws, (hipStream_t)stream);
+}
+
+size_t qlora_gated_workspace_bytes(int32_t op, const qlora_nf4_t* const* w, int64_t m, const int32_t* r, int32_t cd) {
+  if (op != QLORA_OP_FWD && op != QLORA_OP_BWD) return 0;
+  GroupCall gc;
+  if (build_gated(w, nullptr, m, nullptr, nullptr, r, nullptr, 0, cd, nullptr, 0, nullptr, true, "gated_workspace", gc))
+    return 0;
+  return gated_workspace_bytes(op, gc);
+}
+
+int qlora_linear_fwd_dropout_seeded(const qlora_nf4_t* w, const void* x, int64_t m, const void* lora_a,
+                                    const void* lora_b, int32_t r, float alpha, int32_t flags, const void* bias,
+                                    int32_t cd, const uint64_t* seed, float p, void* y, float* t_save, void* ws,
+                                    size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  const char* who = "linear_fwd_dropout_seeded";
+  Seeded sd;
+  const int rc = make_seeded(seed, p, sd, who);
+  if (rc) return rc;
+  if (m >= (1LL << 32) || (w && w->cols >= (1LL << 32)))
+    return set_error(QLORA_ERR_UNSUPPORTED, "%s: 2^32 tokens or columns, or more", who);
+  return fwd_impl(w, x, m, lora_a, lora_b, r, alpha, flags, bias, cd, nullptr, p, y, t_save, ws, ws_bytes, stream, who,
+                  &sd);
+}
+
+int qlora_linear_bwd_dropout_seeded(const qlora_nf4_t* w, const void* x, const void* dy, int64_t m, const void* lora_a,
+                                    const void* lora_b, int32_t r, float alpha, int32_t flags, int32_t cd,
+                                    const uint64_t* seed, float p, const float* t_saved, int32_t gd, void* dx, void* d_a,
+                                    void* d_b, void* ws, size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  const char* who = "linear_bwd_dropout_seeded";
+  Seeded sd;
+  int rc = make_seeded(seed, p, sd, who);
+  if (rc || (rc = check_gd(gd, cd, who))) return rc;
+  if (m >= (1LL << 32) || (w && w->cols >= (1LL << 32)))
+    return set_error(QLORA_ERR_UNSUPPORTED, "%s: 2^32 tokens or columns, or more", who);
+  return bwd_impl(w, x, dy, m, lora_a, lora_b, r, alpha, flags, cd, nullptr, p, t_saved, dx, d_a, d_b, ws, ws_bytes,
+                  stream, who, &sd, gd);
 }
 
 int qlora_linear_bwd_dropout(const qlora_nf4_t* w, const void* x, const void* dy, int64_t m,
@@ -777,6 +892,69 @@ size_t qlora_int8_workspace_bytes(const qlora_int8_t* w, int64_t m, int32_t grou
   if (m < 0 || m >= (1LL << 31) || validate_int8(w, false, "int8_workspace")) return 0;
   if (grouped ? w->experts > 65535 : w->experts != 1) return 0;
   return int8_workspace_bytes(w, m, grouped != 0);
+}
+
+namespace {
+int validate_fp8(const qlora_fp8_t* q, bool need_data, const char* who) {
+  if (!q) return set_error(QLORA_ERR_INVALID_ARG, "%s: null descriptor", who);
+  if (q->reserved != 0) return set_error(QLORA_ERR_INVALID_ARG, "%s: reserved field must be 0", who);
+  if (q->rows < 0 || q->cols < 0) return set_error(QLORA_ERR_SHAPE, "%s: negative shape", who);
+  if (q->cols > QLORA_FP8_MAX_COLS)
+    return set_error(QLORA_ERR_UNSUPPORTED, "%s: %lld cols (at most %d)", who, (long long)q->cols, QLORA_FP8_MAX_COLS);
+  if (q->rows >= (1LL << 31))
+    return set_error(QLORA_ERR_UNSUPPORTED, "%s: %lld rows (fewer than 2^31)", who, (long long)q->rows);
+  if (!need_data || q->rows == 0 || q->cols == 0) return QLORA_OK;
+  if (!q->codes || !q->scale) return set_error(QLORA_ERR_INVALID_ARG, "%s: null codes / scale", who);
+  if (!aligned16(q->codes) || !aligned_to(q->scale, 4))
+    return set_error(QLORA_ERR_INVALID_ARG, "%s: codes must be 16-byte aligned, scale 4-byte aligned", who);
+  return QLORA_OK;
+}
+}  // namespace
+
+int qlora_fp8_quantize(const void* w, int64_t ldw, int32_t wd, qlora_fp8_t* q, void* stream) {
+  g_err[0] = 0;
+  const char* who = "fp8_quantize";
+  int rc = validate_fp8(q, true, who);
+  if (rc) return rc;
+  if (!valid_cd(wd)) return set_error(QLORA_ERR_DTYPE, "%s: bad dtype %d", who, wd);
+  if (ldw < q->cols)
+    return set_error(QLORA_ERR_SHAPE, "%s: row stride %lld below the %lld columns", who, (long long)ldw,
+                     (long long)q->cols);
+  if (q->rows == 0 || q->cols == 0) return QLORA_OK;
+  if (!w) return set_error(QLORA_ERR_INVALID_ARG, "%s: null weight", who);
+  if (!aligned_to(w, cd_bytes(wd))) return set_error(QLORA_ERR_INVALID_ARG, "%s: weight must be element-aligned", who);
+  return launch_fp8_quantize(w, ldw, wd, q, (hipStream_t)stream);
+}
+
+int qlora_fp8_linear(const qlora_fp8_t* w, const void* x, int64_t m, int64_t ldx, const void* bias, int32_t cd, void* y,
+                     void* ws, size_t ws_bytes, void* stream) {
+  g_err[0] = 0;
+  const char* who = "fp8_linear";
+  int rc = validate_fp8(w, true, who);
+  if (rc) return rc;
+  if (!valid_cd(cd)) return set_error(QLORA_ERR_DTYPE, "%s: bad compute dtype %d", who, cd);
+  if (w->rows < 1 || w->cols < 1) return set_error(QLORA_ERR_SHAPE, "%s: empty weight", who);
+  if (m < 0) return set_error(QLORA_ERR_SHAPE, "%s: negative m", who);
+  if (m >= (1LL << 31)) return set_error(QLORA_ERR_UNSUPPORTED, "%s: %lld tokens (fewer than 2^31)", who, (long long)m);
+  if (ldx < w->cols)
+    return set_error(QLORA_ERR_SHAPE, "%s: row stride %lld of x below its %lld columns", who, (long long)ldx,
+                     (long long)w->cols);
+  if (m == 0) return QLORA_OK;
+  if (!x || !y) return set_error(QLORA_ERR_INVALID_ARG, "%s: null x / y", who);
+  const int es = cd_bytes(cd);
+  if (!aligned_to(x, es) || !aligned_to(y, es) || !aligned_to(bias, es))
+    return set_error(QLORA_ERR_INVALID_ARG, "%s: x, y and bias must be element-aligned", who);
+  if ((rc = check_ws(ws, ws_bytes, fp8_workspace_bytes(w, m, cd), who))) return rc;
+  // one token's workgroups read x while others store y already
+  const int64_t ahead = (const char*)y - (const char*)x;
+  if (ahead < ((m - 1) * ldx + w->cols) * es && -ahead < m * w->rows * es)
+    return set_error(QLORA_ERR_INVALID_ARG, "%s: y overlaps x", who);
+  return launch_fp8_linear(w, x, m, ldx, bias, cd, y, ws, (hipStream_t)stream);
+}
+
+size_t qlora_fp8_workspace_bytes(const qlora_fp8_t* w, int64_t m, int32_t cd) {
+  if (m < 0 || m >= (1LL << 31) || !valid_cd(cd) || validate_fp8(w, false, "fp8_workspace")) return 0;
+  return fp8_workspace_bytes(w, m, cd);
 }
 
 size_t qlora_distill_workspace_bytes(int64_t n, int64_t vocab, int32_t k, int32_t cd) {

@@ -26,7 +26,7 @@
 
 #include <algorithm>
 
-#include "common.h"
+#include "mlp.h"
 
 namespace qnf4 {
 
@@ -410,7 +410,7 @@ Split choose_split(int64_t tiles, int64_t k, int bk) {
   if (S > steps) S = steps;
   if (S > 64) S = 64;
   if (S < 1) S = 1;
-  int64_t chunk = round_up(ceil_div(k, S), bk);
+  int64_t chunk = std::max<int64_t>(bk, round_up(ceil_div(k, S), bk));  // a query may have no tokens
   Split sp;
   sp.S = (int)ceil_div(k, chunk);
   sp.chunk = chunk;
@@ -590,7 +590,7 @@ int lora_down(const LayerCall& c, const void* lx, const Split& sp, float* part, 
 }
 
 template <int CD>
-int forward_gemm(const LayerCall& c, void* y, float* t_save) {
+int forward_gemm(const LayerCall& c, const Seeded* sd, void* y, float* t_save) {
   const int64_t M = c.m, N = c.w.rows, K = c.w.cols;
   FwdPlan P = plan_fwd(M, N, K, c.r, CD, c.flags);
   char* ws = (char*)c.ws;
@@ -600,8 +600,10 @@ int forward_gemm(const LayerCall& c, void* y, float* t_save) {
   const bool fast = fast_layout(c.w);
   // input of the low-rank branch: x, or x M with LoRA dropout
   const void* lx = c.x;
-  if (c.drop_mask) {
-    if ((rc = apply_mask(CD, c.x, c.drop_mask, M * K, ws + P.off_xm, c.stream))) return rc;
+  if (c.drop_mask || sd) {
+    rc = sd ? apply_seeded(CD, c.x, *sd, M, K, ws + P.off_xm, c.stream)
+            : apply_mask(CD, c.x, c.drop_mask, M * K, ws + P.off_xm, c.stream);
+    if (rc) return rc;
     lx = ws + P.off_xm;
   }
   // T0 = x A^T (fp32, saved on request) and T = s T0 in cd for the GEMM's tail.  On
@@ -649,9 +651,11 @@ int forward_gemm(const LayerCall& c, void* y, float* t_save) {
   return run_gemm<CD, 128, 128, LK_ROWS, LK_NF4_ROWS, LK_ROWS, LK_ROWS, EPI_CD>(p, 1, QLORA_K_FWD_GEMM, c.stream);
 }
 
+// The adapters' gradients in fp32, or (gd = CD) in the call's own type.
 template <int CD>
-int backward_gemm(const LayerCall& c, const void* dy, const float* t_saved, void* dx, float* d_a,
-                  float* d_b) {
+int backward_gemm(const LayerCall& c, const Seeded* sd, const void* dy, const float* t_saved, void* dx, void* d_a,
+                  void* d_b, int gd) {
+  const bool g32 = gd == CD_F32;
   const int64_t M = c.m, N = c.w.rows, K = c.w.cols, r = c.r;
   BwdPlan P = plan_bwd(M, N, K, c.r, CD, c.flags);
   const bool fast = fast_layout(c.w);
@@ -664,8 +668,10 @@ int backward_gemm(const LayerCall& c, const void* dy, const float* t_saved, void
   int rc;
   // input of the low-rank branch: x, or x M with LoRA dropout
   const void* lx = c.x;
-  if (c.drop_mask) {
-    if ((rc = apply_mask(CD, c.x, c.drop_mask, M * K, ws + P.off_xm, c.stream))) return rc;
+  if (c.drop_mask || sd) {
+    rc = sd ? apply_seeded(CD, c.x, *sd, M, K, ws + P.off_xm, c.stream)
+            : apply_mask(CD, c.x, c.drop_mask, M * K, ws + P.off_xm, c.stream);
+    if (rc) return rc;
     lx = ws + P.off_xm;
   }
 
@@ -771,7 +777,7 @@ int backward_gemm(const LayerCall& c, const void* dy, const float* t_saved, void
   // dense GEMM, or the fused dequant.  With LoRA dropout the GEMM gets a zero dT
   // (base product only) and the masked low-rank term is added afterwards.
   const void* dt_gemm = dtcd;
-  if (dx && c.drop_mask) {
+  if (dx && (c.drop_mask || sd)) {
     if ((rc = zero_fill(ws + P.off_zero, M * P.r_pad * cd_bytes(CD), c.stream))) return rc;
     dt_gemm = ws + P.off_zero;
   }
@@ -801,6 +807,7 @@ int backward_gemm(const LayerCall& c, const void* dy, const float* t_saved, void
   if (dx && c.drop_mask &&
       (rc = rank_add_masked(CD, dx, c.drop_mask, dtcd, P.r_pad, c.lora_a, r, M, K, c.stream)))
     return rc;
+  if (dx && sd && (rc = rank_add_seeded(CD, dx, *sd, dtcd, P.r_pad, c.lora_a, r, M, K, c.stream))) return rc;
 
   // dA = dT^T x and dB = s dY^T T0 (contractions over tokens): on the skinny path
   // both products, then one launch that reduces both.
@@ -830,14 +837,11 @@ int backward_gemm(const LayerCall& c, const void* dy, const float* t_saved, void
     ra.S = Sa;
     ra.P = K;
     ra.R = r;
-    ra.out32 = d_a;
-    ra.trans = true;
     rb.part = part2;
     rb.S = Sb;
     rb.P = N;
     rb.R = r;
-    rb.sc32 = c.scale;
-    rb.out32 = d_b;
+    gradient_jobs(ra, rb, c.scale, d_a, d_b, g32);
     return skinny_reduce_jobs(CD, ra, &rb, c.stream);
   }
   // dA = dT^T x  (contraction over tokens).
@@ -846,7 +850,13 @@ int backward_gemm(const LayerCall& c, const void* dy, const float* t_saved, void
     if ((rc = transpose_small(CD, dtcd, false, P.r_pad, M, r, 1.0f, dtt, P.m_pad, c.stream))) return rc;
     int S;
     if ((rc = skinny(CD, true, lx, K, M, dtt, P.m_pad, K, r, P.m_pad, part, &S, c.stream, QLORA_K_BWD_DA))) return rc;
-    if ((rc = skinny_reduce(CD, part, S, K, r, 1.0f, d_a, true, 0.f, nullptr, 0, c.stream))) return rc;
+    SkRed ra, none;
+    ra.part = part;
+    ra.S = S;
+    ra.P = K;
+    ra.R = r;
+    gradient_jobs(ra, none, 1.0f, d_a, nullptr, g32);
+    if ((rc = skinny_reduce_jobs(CD, ra, nullptr, c.stream))) return rc;
   } else {
     GemmParams p = base_params(c);
     p.a1 = opnd<CD>(dtcd, P.r_pad, r, M);  // source [m][t]
@@ -860,7 +870,7 @@ int backward_gemm(const LayerCall& c, const void* dy, const float* t_saved, void
     p.split_stride = r * K;
     rc = run_gemm<CD, 64, 128, LK_COLS, LK_COLS, LK_NONE, LK_NONE, EPI_F32_PARTIAL>(p, P.sda.S, QLORA_K_BWD_DA, c.stream);
     if (rc) return rc;
-    rc = run_reduce<CD>(part, P.sda, r, K, 1.0f, d_a, 0.f, nullptr, 0, c.stream);
+    rc = run_reduce<CD>(part, P.sda, r, K, 1.0f, g32 ? (float*)d_a : nullptr, 1.0f, g32 ? nullptr : d_a, K, c.stream);
     if (rc) return rc;
   }
 
@@ -878,7 +888,8 @@ int backward_gemm(const LayerCall& c, const void* dy, const float* t_saved, void
     p.split_stride = N * r;
     rc = run_gemm<CD, 128, 64, LK_COLS, LK_COLS_F32, LK_NONE, LK_NONE, EPI_F32_PARTIAL>(p, P.sdb.S, QLORA_K_BWD_DB, c.stream);
     if (rc) return rc;
-    rc = run_reduce<CD>(part, P.sdb, N, r, c.scale, d_b, 0.f, nullptr, 0, c.stream);
+    rc = run_reduce<CD>(part, P.sdb, N, r, c.scale, g32 ? (float*)d_b : nullptr, c.scale, g32 ? nullptr : d_b, r,
+                        c.stream);
     if (rc) return rc;
   }
   return QLORA_OK;
@@ -959,19 +970,35 @@ bool gemv_route(const LayerCall& c) {
 int launch_forward(const LayerCall& c, void* y, float* t_save) {
   if (gemv_route(c)) return gemv_forward(c, y, t_save);
   switch (c.cd) {
-    case CD_BF16: return forward_gemm<CD_BF16>(c, y, t_save);
-    case CD_F16: return forward_gemm<CD_F16>(c, y, t_save);
-    case CD_F32: return forward_gemm<CD_F32>(c, y, t_save);
+    case CD_BF16: return forward_gemm<CD_BF16>(c, nullptr, y, t_save);
+    case CD_F16: return forward_gemm<CD_F16>(c, nullptr, y, t_save);
+    case CD_F32: return forward_gemm<CD_F32>(c, nullptr, y, t_save);
+  }
+  return set_error(QLORA_ERR_DTYPE, "forward: bad compute dtype %d", c.cd);
+}
+
+// The forward with seeded dropout: as with a stored mask, never the decode GEMV (c.flags holds
+// QLORA_FLAG_DROPOUT).
+int launch_forward_seeded(const LayerCall& c, const Seeded& sd, void* y, float* t_save) {
+  switch (c.cd) {
+    case CD_BF16: return forward_gemm<CD_BF16>(c, &sd, y, t_save);
+    case CD_F16: return forward_gemm<CD_F16>(c, &sd, y, t_save);
+    case CD_F32: return forward_gemm<CD_F32>(c, &sd, y, t_save);
   }
   return set_error(QLORA_ERR_DTYPE, "forward: bad compute dtype %d", c.cd);
 }
 
 int launch_backward(const LayerCall& c, const void* dy, const float* t_saved, void* dx, float* d_a,
                     float* d_b) {
+  return launch_backward_as(c, nullptr, dy, t_saved, dx, d_a, d_b, CD_F32);
+}
+
+int launch_backward_as(const LayerCall& c, const Seeded* sd, const void* dy, const float* t_saved, void* dx, void* d_a,
+                       void* d_b, int gd) {
   switch (c.cd) {
-    case CD_BF16: return backward_gemm<CD_BF16>(c, dy, t_saved, dx, d_a, d_b);
-    case CD_F16: return backward_gemm<CD_F16>(c, dy, t_saved, dx, d_a, d_b);
-    case CD_F32: return backward_gemm<CD_F32>(c, dy, t_saved, dx, d_a, d_b);
+    case CD_BF16: return backward_gemm<CD_BF16>(c, sd, dy, t_saved, dx, d_a, d_b, gd);
+    case CD_F16: return backward_gemm<CD_F16>(c, sd, dy, t_saved, dx, d_a, d_b, gd);
+    case CD_F32: return backward_gemm<CD_F32>(c, sd, dy, t_saved, dx, d_a, d_b, gd);
   }
   return set_error(QLORA_ERR_DTYPE, "backward: bad compute dtype %d", c.cd);
 }

@@ -332,13 +332,13 @@ bool skinny_ok(int cd, int64_t r) { return (cd == CD_BF16 || cd == CD_F16) && r 
 // Slices of the contraction: about 256 workgroups, at most 8 slices (the partial
 // sums are written and read back once more).
 void skinny_split(int64_t P, int64_t Kc, int* S, int64_t* kslice) {
-  const int64_t tiles = ceil_div(P, BP);
+  const int64_t tiles = std::max<int64_t>(1, ceil_div(P, BP));  // a query may have no rows
   int64_t s = ceil_div(256, tiles);
   const int64_t steps = Kc / BK;
   if (s > steps) s = steps;
   if (s > kRedMaxS) s = kRedMaxS;
   if (s < 1) s = 1;
-  const int64_t ks = round_up(ceil_div(Kc, s), BK);
+  const int64_t ks = std::max<int64_t>(BK, round_up(ceil_div(Kc, s), BK));  // nor a contraction
   *kslice = ks;
   *S = (int)ceil_div(Kc, ks);
 }

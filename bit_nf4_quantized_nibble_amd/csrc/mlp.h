@@ -1,0 +1,45 @@
+// mlp.h -- host entry points of the 8-bit floating-point product (fp8.hip), of the gated block
+// (gated.hip) and of the layer with seeded dropout (gemm.hip, dropout.hip).
+#pragma once
+#include "common.h"
+#include "philox.h"
+
+namespace qnf4 {
+int launch_fp8_quantize(const void* w, int64_t ldw, int dtype, const qlora_fp8_t* q, hipStream_t s);
+size_t fp8_workspace_bytes(const qlora_fp8_t* w, int64_t m, int cd);
+int launch_fp8_linear(const qlora_fp8_t* w, const void* x, int64_t m, int64_t ldx, const void* bias, int cd, void* y,
+                      void* ws, hipStream_t s);
+
+// The layer with an optional seeded dropout (null: none) and the adapters' gradients in gd (fp32 or
+// the call's own type).
+int launch_forward_seeded(const LayerCall& c, const Seeded& sd, void* y, float* t_save);
+int launch_backward_as(const LayerCall& c, const Seeded* sd, const void* dy, const float* t_saved, void* dx, void* d_a,
+                       void* d_b, int gd);
+// Where the reductions of dA (ra, its sums [cols][r]) and dB (rb, [rows][r], times scale) write:
+// fp32, or rounded into the call's type.
+inline void gradient_jobs(SkRed& ra, SkRed& rb, float scale, void* d_a, void* d_b, bool g32) {
+  rb.sc32 = rb.sccd = scale;
+  if (g32) {
+    ra.out32 = (float*)d_a;
+    ra.trans = true;
+    rb.out32 = (float*)d_b;
+  } else {
+    ra.outt = d_a;  // the transposed copy: [r][cols]
+    ra.ldt = ra.P;
+    rb.outcd = d_b;
+    rb.ldcd = rb.R;
+  }
+}
+int apply_seeded(int cd, const void* x, const Seeded& sd, int64_t rows, int64_t cols, void* out, hipStream_t s);
+int rank_add_seeded(int cd, void* dx, const Seeded& sd, const void* dt, int64_t ld_dt, const void* a, int32_t r, int64_t M,
+                    int64_t K, hipStream_t s);
+
+int launch_backward_group_as(const GroupCall& gc, const void* dy, const float* const* t_saved, void* dx,
+                             void* const* d_a, void* const* d_b, int gd, void* ws, hipStream_t s);
+
+size_t gated_workspace_bytes(int op, const GroupCall& gc);
+int launch_gated_fwd(const GroupCall& gc, int act, const void* bias, void* h, void* pre, float* const* t_save, void* ws,
+                     hipStream_t s);
+int launch_gated_bwd(const GroupCall& gc, int act, const void* dh, const void* pre, const float* const* t_saved, void* dx,
+                     void* const* d_a, void* const* d_b, int gd, void* ws, hipStream_t s);
+}  // namespace qnf4

@@ -23,11 +23,11 @@
  *     never allocates or frees device memory.  Matrices are row-major and dense.
  *     The fp32 weight and the codes of quantize / dequantize, the dequantized
  *     output, and every array of a layer call (x, dy, adapters, bias, outputs,
- *     masks, saved T0, gradients) start on a 16-byte boundary: the kernels move
+ *     masks, saved T0 and pre-activations, gradients) start on a 16-byte boundary: the kernels move
  *     16-byte vectors, and an unaligned pointer is refused with
  *     QLORA_ERR_INVALID_ARG.  Workspaces are 256-byte aligned.  The merge, MSE,
  *     distillation and AdamW calls take any element-aligned arrays, and so do the
- *     8-bit calls except for their codes; matrices that have a row stride argument
+ *     8-bit calls (integer and floating point) except for their codes; matrices that have a row stride argument
  *     need not be dense.
  *   - Every call is asynchronous on `stream` (a hipStream_t; NULL = null stream).
  *   - Arguments are validated on the host before anything is launched: on any
@@ -232,6 +232,48 @@ int qlora_linear_bwd_group(int32_t g, const qlora_nf4_t* const* w, const void* x
                            void* dx, float* const* d_a, float* const* d_b, void* ws, size_t ws_bytes,
                            void* stream);
 
+/*
+ * The gated feed-forward block over two projections of the same input (w[0] the gate, w[1] the up
+ * projection, equal rows and cols):
+ *   g = x Wg~^T + s_g (x Ag^T) Bg^T (+ bias[0 .. rows)),  u likewise (+ bias[rows .. 2 rows)),
+ *   h [m, rows] = act(g) u.
+ * h is rounded once, from fp32, where the tiled path runs (bf16 / f16, more than 64 tokens, rows a
+ * multiple of 64, ranks <= 64, the layouts of qlora_linear_fwd_group's); elsewhere g and u are
+ * rounded into cd first.  pre (nullable) [m, 2 rows] receives [g | u] in cd, t_save (nullable
+ * array of nullable pointers) T0_i = x A_i^T fp32 [m, r_i]: what the backward takes.
+ * act: QLORA_ACT_SILU z / (1 + exp(-z)); QLORA_ACT_GELU z Phi(z); QLORA_ACT_GELU_TANH
+ * z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2.
+ * flags: QLORA_FLAG_RSLORA only.  ws: qlora_gated_workspace_bytes(QLORA_OP_FWD, ...) bytes.
+ * Outputs must not overlap each other or the inputs.  m == 0 is a no-op.
+ * Errors: as qlora_linear_fwd_group, plus QLORA_ERR_INVALID_ARG for an unknown act and
+ * QLORA_ERR_SHAPE for differing rows.
+ */
+enum { QLORA_ACT_SILU = 0, QLORA_ACT_GELU = 1, QLORA_ACT_GELU_TANH = 2 };
+int qlora_linear_fwd_gated(const qlora_nf4_t* const* w, const void* x, int64_t m, const void* const* lora_a,
+                           const void* const* lora_b, const int32_t* r, const float* alpha, int32_t flags,
+                           int32_t act, const void* bias, int32_t cd, void* h, void* pre, float* const* t_save,
+                           void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Backward of the gated block with the base weights frozen, from dh [m, rows] and the pre the
+ * forward saved:
+ *   dg = dh u act'(g),  du = dh act(g)   (fp32, rounded into cd)
+ * and the group's backward of [dg | du]: dX [m, cols] (skipped when dx == NULL), dA_i, dB_i.
+ * gd: type of the adapters' gradients, QLORA_F32 (what qlora_adamw_step takes) or cd.
+ * t_saved (nullable array of nullable pointers): the forward's T0_i, else recomputed.
+ * ws: qlora_gated_workspace_bytes(QLORA_OP_BWD, ...) bytes.
+ * Errors: as qlora_linear_bwd_group and qlora_linear_fwd_gated, QLORA_ERR_DTYPE for another gd.
+ */
+int qlora_linear_bwd_gated(const qlora_nf4_t* const* w, const void* x, const void* dh, const void* pre, int64_t m,
+                           const void* const* lora_a, const void* const* lora_b, const int32_t* r,
+                           const float* alpha, int32_t flags, int32_t act, int32_t cd,
+                           const float* const* t_saved, int32_t gd, void* dx, void* const* d_a, void* const* d_b,
+                           void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes for qlora_linear_fwd_gated (op QLORA_OP_FWD) or qlora_linear_bwd_gated
+ * (QLORA_OP_BWD) on these two weights; 0 for an invalid query.  Pure host function. */
+size_t qlora_gated_workspace_bytes(int32_t op, const qlora_nf4_t* const* w, int64_t m, const int32_t* r, int32_t cd);
+
 /* Workspace bytes for qlora_linear_fwd_group (op QLORA_OP_FWD) or
  * qlora_linear_bwd_group (QLORA_OP_BWD) on these g weights; 0 for an invalid query.
  * Pure host function. */
@@ -367,6 +409,29 @@ int qlora_linear_bwd_dropout(const qlora_nf4_t* w, const void* x, const void* dy
                              int32_t cd, const uint8_t* mask, float p, const float* t_saved, void* dx,
                              float* d_a, float* d_b, void* ws, size_t ws_bytes, void* stream);
 
+/*
+ * The layer with LoRA dropout whose mask is drawn from a counter and never stored.  The
+ * results are those of the calls above with the mask
+ *   M[i, k] = w >= round(65536 p),  w the 16-bit half k % 8 (low halves first) of the four words
+ *   Philox 4x32-10 (Salmon et al., SC 2011) gives for the counter {k / 8, i, offset low, offset
+ *   high} and the key {seed low, seed high},
+ * and the rate round(65536 p) / 65536 in the place of p.  seed: device u64 [2] = {seed, offset}, 8-byte
+ * aligned, read on the device when the kernels run: the backward takes the values the forward had, a
+ * captured call draws another mask at each replay that finds other values there, and calls with
+ * other offsets under one seed draw independent masks.  m and cols below 2^32.
+ * gd: type of the adapters' gradients, QLORA_F32 or cd.  Workspaces as for the calls above.
+ * Errors: those of the calls above, QLORA_ERR_INVALID_ARG for a null or unaligned seed, and
+ * QLORA_ERR_DTYPE for another gd.
+ */
+int qlora_linear_fwd_dropout_seeded(const qlora_nf4_t* w, const void* x, int64_t m, const void* lora_a,
+                                    const void* lora_b, int32_t r, float alpha, int32_t flags, const void* bias,
+                                    int32_t cd, const uint64_t* seed, float p, void* y, float* t_save, void* ws,
+                                    size_t ws_bytes, void* stream);
+int qlora_linear_bwd_dropout_seeded(const qlora_nf4_t* w, const void* x, const void* dy, int64_t m,
+                                    const void* lora_a, const void* lora_b, int32_t r, float alpha, int32_t flags,
+                                    int32_t cd, const uint64_t* seed, float p, const float* t_saved, int32_t gd,
+                                    void* dx, void* d_a, void* d_b, void* ws, size_t ws_bytes, void* stream);
+
 /* Cached-dequant forward (qlora-rs CONFIG "cache_dequantized"; the memory-for-speed
  * trade-off of BOOK "Tooling" and the README's on-the-fly versus cached dequant):
  * the caller dequantizes the frozen weight once with qlora_nf4_dequantize(w, cd,
@@ -489,6 +554,64 @@ int qlora_int8_linear_experts(const qlora_int8_t* w, const void* x, int64_t m, i
 size_t qlora_int8_workspace_bytes(const qlora_int8_t* w, int64_t m, int32_t grouped);
 
 /* ---------------------------------------------------------------------------
+ * Products in 8-bit floating point (e4m3: 4 exponent bits, 3 mantissa bits, largest value 448) with
+ * a scale for each block of 128: another serving form of a merged weight.
+ *   block    s = 2^e, e the smallest integer >= -127 with max |x| <= 448 s; codes RNE_e4m3(x / s).
+ *            Activations: 128 consecutive columns of a row; weights: 128 rows by 128 columns.
+ *            A block that holds an infinity or a NaN has s = 1 and NaN codes.
+ *   product  y [m, rows] = RNE_cd(sum_k xq[i, k] wq[j, k] (+ bias[j])) over the values that the codes
+ *            stand for, summed in fp32.  bf16 and f16 sums come from the 8-bit matrix instruction, which
+ *            keeps about 19 bits of each group of products (relative error of the sums 1e-5 to
+ *            1e-4, of their norm); fp32 sums from exact products.
+ * ------------------------------------------------------------------------- */
+
+#define QLORA_FP8_MAX_COLS 131072
+/* Bytes of one row of codes: cols rounded up to whole blocks; the codes past the last column
+ * are 0. */
+#define QLORA_FP8_LD(cols) ((((int64_t)(cols)) + 127) / 128 * 128)
+/* Bytes of one row block's scales: the column blocks rounded up to four. */
+#define QLORA_FP8_LDS(cols) ((((int64_t)(cols)) + 511) / 512 * 4)
+
+/*
+ * A weight in 8-bit floats.  Descriptor memory is the caller's; the pointers inside are device
+ * pointers the caller allocated:
+ *   codes  e4m3 [rows][QLORA_FP8_LD(cols)]                       16-byte aligned
+ *   scale  u8   [ceil(rows / 128)][QLORA_FP8_LDS(cols)]          4-byte aligned; e + 127 (127 past the last)
+ */
+typedef struct {
+  int64_t rows; /* output channels */
+  int64_t cols; /* input channels */
+  int64_t reserved; /* must be 0 */
+  uint8_t* codes;
+  uint8_t* scale;
+} qlora_fp8_t;
+
+/*
+ * Codes and scales of w [rows, cols] (dtype wd, rows ldw elements apart, ldw >= cols) into *q.
+ * Any element-aligned w.  An empty weight is a no-op.
+ * Errors: QLORA_ERR_INVALID_ARG (null or unaligned pointers, reserved != 0), QLORA_ERR_SHAPE
+ * (negative shape, ldw < cols), QLORA_ERR_DTYPE, QLORA_ERR_UNSUPPORTED (cols > QLORA_FP8_MAX_COLS,
+ * 2^31 rows or more).
+ */
+int qlora_fp8_quantize(const void* w, int64_t ldw, int32_t wd, qlora_fp8_t* q, void* stream);
+
+/*
+ * y [m, rows] = x [m, cols] . W^T (+ bias [rows]) with x (dtype cd, rows ldx elements apart)
+ * brought to 8 bits block by block within the call.  x and y are element-aligned; y is dense and
+ * must not overlap the inputs (memory between x's first and last element is refused).  m == 0 is
+ * a no-op.  ws: qlora_fp8_workspace_bytes(w, m, cd) bytes, 256-byte aligned.
+ * Errors: QLORA_ERR_INVALID_ARG (null or unaligned pointers, y over x), QLORA_ERR_SHAPE (m < 0,
+ * empty weight, ldx < cols), QLORA_ERR_DTYPE, QLORA_ERR_WORKSPACE, QLORA_ERR_UNSUPPORTED (cols >
+ * QLORA_FP8_MAX_COLS, rows or m of 2^31 or more, more tiles of y than one launch takes).
+ */
+int qlora_fp8_linear(const qlora_fp8_t* w, const void* x, int64_t m, int64_t ldx, const void* bias, int32_t cd,
+                     void* y, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of qlora_fp8_linear (reads only the shape of *w); 0 for an invalid query.
+ * Fewer tokens may need more: ask for each m.  Pure host function. */
+size_t qlora_fp8_workspace_bytes(const qlora_fp8_t* w, int64_t m, int32_t cd);
+
+/* ---------------------------------------------------------------------------
  * Distillation: the loss of student logits against a teacher's top logits, and its
  * gradient (a training loss beside qlora_mse_loss_grad).
  * ------------------------------------------------------------------------- */
@@ -569,6 +692,9 @@ enum {
   QLORA_K_OPTIM,      /* AdamW update of an adapter */
   QLORA_K_INT8_ROWS,  /* rows to 8-bit codes and scales (with the experts' route) */
   QLORA_K_INT8_GEMM,  /* product in 8-bit integers */
+  QLORA_K_FP8_ROWS,   /* values to 8-bit floats and block scales */
+  QLORA_K_FP8_GEMM,   /* product in 8-bit floats */
+  QLORA_K_GATE,       /* the gated block's activation by itself, and its gradient */
   QLORA_K_COUNT
 };
 int qlora_profile_enable(int32_t on);

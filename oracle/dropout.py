@@ -41,3 +41,35 @@ def backward(x, W, A, B, dY, s: float, mask, p: float):
     dA = dT.T @ xd
     dB = s * dY.T @ (xd @ A.T)
     return dX, dA, dB
+
+
+def philox(counter, key):
+    """The four words of Philox 4x32-10 (Salmon et al., SC 2011) for one counter (four words) and
+    key (two), in Python's integers."""
+    c, k = list(counter), list(key)
+    for _ in range(10):
+        a, b = 0xD2511F53 * c[0], 0xCD9E8D57 * c[2]
+        c = [(b >> 32) ^ c[1] ^ k[0], b & 0xFFFFFFFF, (a >> 32) ^ c[3] ^ k[1], a & 0xFFFFFFFF]
+        k = [(k[0] + 0x9E3779B9) & 0xFFFFFFFF, (k[1] + 0xBB67AE85) & 0xFFFFFFFF]
+    return c
+
+
+def threshold(p: float) -> int:
+    return min(65535, int(np.floor(float(np.float32(p)) * 65536 + 0.5)))
+
+
+def drawn_mask(m: int, cols: int, seed: int, offset: int, p: float):
+    """The keep mask [m, cols] (u8) the seeded dropout draws, word by word in numpy."""
+    lo, t = np.uint64(0xFFFFFFFF), threshold(p)
+    seed, offset = seed & ((1 << 64) - 1), offset & ((1 << 64) - 1)
+    groups = -(-cols // 8)
+    c = [np.broadcast_to(np.arange(groups, dtype=np.uint64), (m, groups)),
+         np.broadcast_to(np.arange(m, dtype=np.uint64)[:, None], (m, groups)),
+         np.full((m, groups), offset & 0xFFFFFFFF, np.uint64), np.full((m, groups), offset >> 32, np.uint64)]
+    k = [seed & 0xFFFFFFFF, seed >> 32]
+    for _ in range(10):
+        a, b = c[0] * np.uint64(0xD2511F53), c[2] * np.uint64(0xCD9E8D57)
+        c = [(b >> np.uint64(32)) ^ c[1] ^ np.uint64(k[0]), b & lo, (a >> np.uint64(32)) ^ c[3] ^ np.uint64(k[1]), a & lo]
+        k = [(k[0] + 0x9E3779B9) & 0xFFFFFFFF, (k[1] + 0xBB67AE85) & 0xFFFFFFFF]
+    halves = np.stack([h for w in c for h in (w & np.uint64(0xFFFF), w >> np.uint64(16))], axis=2)
+    return (halves.reshape(m, groups * 8)[:, :cols] >= t).astype(np.uint8)
