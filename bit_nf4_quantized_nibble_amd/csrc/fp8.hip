@@ -236,7 +236,8 @@ struct Copies8 {
     for (int i = 0; i < T::WMB; ++i) s[0][i] = (int)((uint32_t)s[1][i] >> (8 * (stage & 3)));
     sb[0] = sb[1];
   }
-  __device__ __forceinline__ void middle(Acc<T>&, int) const {}
+  __device__ __forceinline__ void stage(int) const {}
+  __device__ __forceinline__ void slot(int) const {}
 };
 
 // Word i (of 4 bytes) of a tile's coefficients: biases as fp32, then the exponents of its blocks.
@@ -479,7 +480,7 @@ __global__ __launch_bounds__(512, 1) void k_fp8_full(F8 p) {
     auto work = [&](auto shape) {
       using T = decltype(shape);
       const char* coef = coefs + set * Coef<Full>::BYTES;
-      const Copies8<T> cp(p, cur, ring, coef, wave, lane);
+      Copies8<T> cp(p, cur, ring, coef, wave, lane);
       cp.all(lds + T::STAGE, 1);
       Acc<T> acc;
       zero<T>(acc);

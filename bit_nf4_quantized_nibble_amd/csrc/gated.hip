@@ -9,6 +9,7 @@
 // saves for the backward.
 #include <algorithm>
 
+#include "act.h"
 #include "mlp.h"
 
 namespace qnf4 {
@@ -16,76 +17,82 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// act(z) and its derivative, in fp32.
-//   silu       z q,  q = 1 / (1 + exp(-z));          derivative q + z q (1 - q)
-//   gelu       z c,  c = erfc(-z / sqrt 2) / 2;      derivative c + z exp(-z^2 / 2) / sqrt(2 pi)
-//   gelu_tanh  z q(2 t),  t = sqrt(2 / pi) (z + 0.044715 z^3)  (1/2 (1 + tanh t) = q(2 t))
-// 1 - q is formed as q(-z): no cancellation where q is near 1.
-__device__ __forceinline__ float sigmoid(float z) { return 1.f / (1.f + __expf(-z)); }
-constexpr float kTanhA = 1.5957691216057308f;           // 2 sqrt(2 / pi)
-constexpr float kTanhB = kTanhA * 0.044715f;
-// The cubic's argument: beyond 30 q is 0 or 1, and z^3 must not leave fp32's range.
-__device__ __forceinline__ float limited(float z) { return fminf(fmaxf(z, -30.f), 30.f); }
-__device__ __forceinline__ float tanh_arg(float z) {
-  const float l = limited(z);
-  return l * fmaf(kTanhB * l, l, kTanhA);
-}
-template <int ACT>
-__device__ __forceinline__ float act_of(float z) {
-  if constexpr (ACT == QLORA_ACT_SILU) return z * sigmoid(z);
-  else if constexpr (ACT == QLORA_ACT_GELU) return z * (0.5f * erfcf(-0.70710678118654752f * z));
-  else return z * sigmoid(tanh_arg(z));
-}
-template <int ACT>
-__device__ __forceinline__ void act_grad(float z, float& value, float& slope) {
-  if constexpr (ACT == QLORA_ACT_GELU) {
-    const float c = 0.5f * erfcf(-0.70710678118654752f * z);
-    value = z * c;
-    slope = fmaf(z * 0.39894228040143268f, __expf(-0.5f * z * z), c);
-  } else if constexpr (ACT == QLORA_ACT_SILU) {
-    const float q = sigmoid(z);
-    value = z * q;
-    slope = fmaf(value, sigmoid(-z), q);
+// E consecutive elements of a row (16 bytes where E = 8: rows of whole chunks), as fp32.
+template <int CD, int E>
+__device__ __forceinline__ void load_n(const void* p, int64_t at, float (&v)[E]) {
+  if constexpr (E == 8) {
+    const u32x4_t w = *(const u32x4_t*)((const uint16_t*)p + at);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = from_cd16<CD>((uint16_t)(w[e >> 1] >> (16 * (e & 1))));
   } else {
-    const float t = tanh_arg(z), q = sigmoid(t), zl = limited(z);
-    value = z * q;
-    slope = fmaf(value * sigmoid(-t), fmaf(3.f * kTanhB * zl, zl, kTanhA), q);
+    v[0] = load_cd<CD>(p, at);
+  }
+}
+template <int CD, int E>
+__device__ __forceinline__ void store_n(void* p, int64_t at, const float (&v)[E]) {
+  if constexpr (E == 8) {
+    const u32x4_t w = {pack2<CD>(v[0], v[1]), pack2<CD>(v[2], v[3]), pack2<CD>(v[4], v[5]), pack2<CD>(v[6], v[7])};
+    *(u32x4_t*)((uint16_t*)p + at) = w;
+  } else {
+    store_cd<CD>(p, at, v[0]);
   }
 }
 
-// h [m][n] = act(pre[:, :n]) pre[:, n:], one element to a thread.
-template <int CD, int ACT>
+// h [m][n] = act(pre[:, :n]) pre[:, n:], E elements of a row to a thread.
+template <int CD, int ACT, int E>
 __global__ __launch_bounds__(kThreads) void k_gate(const void* __restrict__ pre, int64_t n, int64_t total,
                                                    void* __restrict__ h) {
+  const int64_t per = n / E;
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
-    const int64_t row = i / n, at = 2 * n * row + (i - row * n);
-    store_cd<CD>(h, i, act_of<ACT>(load_cd<CD>(pre, at)) * load_cd<CD>(pre, at + n));
+    const int64_t row = i / per, at = 2 * n * row + E * (i - row * per);
+    float g[E], u[E];
+    load_n<CD, E>(pre, at, g);
+    load_n<CD, E>(pre, at + n, u);
+#pragma unroll
+    for (int e = 0; e < E; ++e) g[e] = act_of<ACT>(g[e]) * u[e];
+    store_n<CD, E>(h, E * i, g);
   }
 }
 
 // dpre [m][2 n] from dh [m][n] and pre.
-template <int CD, int ACT>
+template <int CD, int ACT, int E>
 __global__ __launch_bounds__(kThreads) void k_gate_bwd(const void* __restrict__ pre, const void* __restrict__ dh,
                                                        int64_t n, int64_t total, void* __restrict__ dpre) {
+  const int64_t per = n / E;
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
-    const int64_t row = i / n, at = 2 * n * row + (i - row * n);
-    const float d = load_cd<CD>(dh, i);
-    float value, slope;
-    act_grad<ACT>(load_cd<CD>(pre, at), value, slope);
-    store_cd<CD>(dpre, at, d * load_cd<CD>(pre, at + n) * slope);
-    store_cd<CD>(dpre, at + n, d * value);
+    const int64_t row = i / per, at = 2 * n * row + E * (i - row * per);
+    float d[E], g[E], u[E];
+    load_n<CD, E>(dh, E * i, d);
+    load_n<CD, E>(pre, at, g);
+    load_n<CD, E>(pre, at + n, u);
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      float value, slope;
+      act_grad<ACT>(g[e], value, slope);
+      g[e] = d[e] * u[e] * slope;
+      u[e] = d[e] * value;
+    }
+    store_n<CD, E>(dpre, at, g);
+    store_n<CD, E>(dpre, at + n, u);
   }
 }
 
 int64_t al(int64_t b) { return round_up(b, 256); }
 unsigned grid_for(int64_t n) { return (unsigned)std::max<int64_t>(1, std::min<int64_t>(1 << 16, ceil_div(n, kThreads))); }
 
+template <int CD, int ACT, int E>
+int gate_n(const void* pre, const void* dh, int64_t n, int64_t total, void* out, hipStream_t s) {
+  ProfScope prof(QLORA_K_GATE, s);
+  const dim3 g(grid_for(total / E)), b(kThreads);
+  if (dh) k_gate_bwd<CD, ACT, E><<<g, b, 0, s>>>(pre, dh, n, total / E, out);
+  else k_gate<CD, ACT, E><<<g, b, 0, s>>>(pre, n, total / E, out);
+  return check_launch(dh ? "k_gate_bwd" : "k_gate");
+}
 template <int CD, int ACT>
 int gate_t(const void* pre, const void* dh, int64_t n, int64_t total, void* out, hipStream_t s) {
-  ProfScope prof(QLORA_K_GATE, s);
-  if (dh) k_gate_bwd<CD, ACT><<<dim3(grid_for(total)), dim3(kThreads), 0, s>>>(pre, dh, n, total, out);
-  else k_gate<CD, ACT><<<dim3(grid_for(total)), dim3(kThreads), 0, s>>>(pre, n, total, out);
-  return check_launch(dh ? "k_gate_bwd" : "k_gate");
+  if constexpr (CD != CD_F32)
+    if (n % 8 == 0) return gate_n<CD, ACT, 8>(pre, dh, n, total, out, s);
+  return gate_n<CD, ACT, 1>(pre, dh, n, total, out, s);
 }
 template <int CD>
 int gate_cd(int act, const void* pre, const void* dh, int64_t n, int64_t total, void* out, hipStream_t s) {
@@ -100,16 +107,123 @@ int gate(int cd, int act, const void* pre, const void* dh, int64_t m, int64_t n,
   return gate_cd<CD_F32>(act, pre, dh, n, m * n, out, s);
 }
 
+// How a forward runs, and its workspace.
+//   DECODE   up to 64 tokens on the split-K GEMV: both projections' partial sums, one epilogue
+//   TILED    W~ of both in the workspace, T = s x A^T by the rank-product kernels, then the gated GEMM
+//   GROUP    every other layout and fp32: the group call gives [g | u], then k_gate
+enum Way { DECODE, TILED, GROUP };
+struct FwdPlan {
+  Way way;
+  int64_t wd, t, bpad[2], part[2], total;
+};
+FwdPlan plan_fwd(const GroupCall& gc) {
+  FwdPlan P = {};
+  const LayerCall &c0 = gc.c[0], &c1 = gc.c[1];
+  const int64_t m = c0.m, n = c0.w.rows, K = c0.w.cols, es = cd_bytes(c0.cd);
+  if (m > 0 && gemv_gated_ok(gc.c)) {
+    P.way = DECODE;
+    P.total = (int64_t)gemv_gated_workspace_bytes(gc.c);
+  } else if (m > 16 && gemm16_ok(c0.cd, m, n, K) && fast_layout(c0.w) && fast_layout(c1.w) && skinny_ok(c0.cd, c0.r) &&
+             skinny_ok(c1.cd, c1.r) && dense256_ok(c0, false) && dense256_ok(c1, false)) {
+    P.way = TILED;
+    int64_t o = 0;
+    P.wd = o; o += al(2 * n * K * es);
+    P.t = o; o += al(m * 128 * es);
+    for (int i = 0; i < 2; ++i) {
+      const int32_t r = gc.c[i].r;
+      P.bpad[i] = o; o += r % 8 ? al(n * round_up(r, 8) * es) : 0;
+      P.part[i] = o; o += al((int64_t)skinny_part_bytes(m, K));
+    }
+    P.total = o;
+  } else {
+    P.way = GROUP;
+    P.total = al(m * gc.N * es) + (int64_t)group_workspace_bytes(QLORA_OP_FWD, gc);
+  }
+  return P;
+}
+
+// dst [n][ld] = src [n][r] with zeros from column r on: rows of lora_b as whole 16-byte chunks.
+__global__ __launch_bounds__(kThreads) void k_pad_rows(const uint16_t* __restrict__ src, int r, int64_t n, int ld,
+                                                       uint16_t* __restrict__ dst) {
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n * ld; i += (int64_t)gridDim.x * kThreads) {
+    const int64_t row = i / ld;
+    const int c = (int)(i - row * ld);
+    dst[i] = c < r ? src[row * r + c] : (uint16_t)0;
+  }
+}
+
+int forward_tiled(const GroupCall& gc, const FwdPlan& P, int act, const void* bias, void* h, void* pre,
+                  float* const* t_save, char* ws, hipStream_t s) {
+  const LayerCall& c0 = gc.c[0];
+  const int64_t m = c0.m, n = c0.w.rows, K = c0.w.cols, es = cd_bytes(c0.cd);
+  SkSpec specs[2];
+  float* parts[2];
+  int S[2], rc;
+  for (int i = 0; i < 2; ++i) {
+    specs[i].a = c0.x;
+    specs[i].lda = K;
+    specs[i].arows = m;
+    specs[i].b = gc.c[i].lora_a;
+    specs[i].ldb = K;
+    specs[i].P = m;
+    specs[i].R = gc.c[i].r;
+    specs[i].Kc = K;
+    parts[i] = (float*)(ws + P.part[i]);
+  }
+  if ((rc = skinny_many(c0.cd, specs, parts, S, 2, s, QLORA_K_LORA_DOWN))) return rc;
+  Nf4W w[2];
+  void* out[2];
+  SkRed red[2];
+  const void* b[2];
+  int64_t ldb[2];
+  for (int i = 0; i < 2; ++i) {
+    const LayerCall& c = gc.c[i];
+    w[i] = c.w;
+    out[i] = ws + P.wd + i * n * K * es;
+    red[i].part = parts[i];
+    red[i].S = S[i];
+    red[i].P = m;
+    red[i].R = c.r;
+    red[i].out32 = t_save ? t_save[i] : nullptr;
+    red[i].sccd = c.scale;
+    red[i].outcd = ws + P.t + i * 64 * es;
+    red[i].ldcd = 128;
+    red[i].wcd = 64;
+    b[i] = c.lora_b;
+    ldb[i] = round_up(c.r, 8);
+    if (c.r % 8) {
+      ProfScope prof(QLORA_K_REDUCE, s);
+      b[i] = ws + P.bpad[i];
+      k_pad_rows<<<dim3(grid_for(n * ldb[i])), dim3(kThreads), 0, s>>>((const uint16_t*)c.lora_b, c.r, n, (int)ldb[i],
+                                                                       (uint16_t*)(ws + P.bpad[i]));
+      if ((rc = check_launch("k_pad_rows"))) return rc;
+    }
+  }
+  // W~ of both, the reductions of T riding on the launch
+  if ((rc = dequant_group_into(w, 2, c0.cd, out, red, s))) return rc;
+  return gemm16_gated(c0.cd, c0.x, m, n, K, out, ws + P.t, b, ldb, bias, act, h, pre, s);
+}
+
 }  // namespace
 
-// [g | u] (or its gradient) and the group call's own workspace.
 size_t gated_workspace_bytes(int op, const GroupCall& gc) {
-  return (size_t)al(gc.c[0].m * gc.N * cd_bytes(gc.c[0].cd)) + group_workspace_bytes(op, gc);
+  if (op == QLORA_OP_FWD) return (size_t)plan_fwd(gc).total;
+  return (size_t)al(gc.c[0].m * gc.N * cd_bytes(gc.c[0].cd)) + group_workspace_bytes(op, gc);  // [dg | du] first
 }
 
 int launch_gated_fwd(const GroupCall& gc, int act, const void* bias, void* h, void* pre, float* const* t_save, void* ws,
                      hipStream_t s) {
+  const FwdPlan P = plan_fwd(gc);
   const LayerCall& c = gc.c[0];
+  if (P.way == DECODE) {
+    LayerCall pair[2] = {gc.c[0], gc.c[1]};
+    for (int i = 0; i < 2; ++i) {
+      pair[i].bias = bias ? (const char*)bias + i * c.w.rows * cd_bytes(c.cd) : nullptr;
+      pair[i].ws = ws;
+    }
+    return gemv_gated(pair, act, h, pre, t_save);
+  }
+  if (P.way == TILED) return forward_tiled(gc, P, act, bias, h, pre, t_save, (char*)ws, s);
   void* z = pre ? pre : ws;
   const int rc = launch_forward_group(gc, bias, z, t_save, (char*)ws + al(c.m * gc.N * cd_bytes(c.cd)), s);
   return rc ? rc : gate(c.cd, act, z, nullptr, c.m, c.w.rows, h, s);

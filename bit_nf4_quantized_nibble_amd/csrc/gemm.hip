@@ -776,15 +776,19 @@ int backward_gemm(const LayerCall& c, const Seeded* sd, const void* dy, const fl
   // dX = dY W~ + dT A (the contraction runs over W's rows): W~^T written once and a
   // dense GEMM, or the fused dequant.  With LoRA dropout the GEMM gets a zero dT
   // (base product only) and the masked low-rank term is added afterwards.
+  // With a drawn mask the tiled GEMM adds that term itself.
+  const bool masked = sd && dense_dx && P.r_pad <= 64 && gemm16_ok(CD, M, K, N);
   const void* dt_gemm = dtcd;
-  if (dx && (c.drop_mask || sd)) {
+  if (dx && (c.drop_mask || sd) && !masked) {
     if ((rc = zero_fill(ws + P.off_zero, M * P.r_pad * cd_bytes(CD), c.stream))) return rc;
     dt_gemm = ws + P.off_zero;
   }
   if (dense_dx) {
     void* wdt = ws + P.off_wdt;
     if ((rc = dequant_into(c.w, CD, wdt, true, c.stream, red_dt_pending ? &red_dt : nullptr))) return rc;
-    if ((rc = dense256_dx(c, dy, wdt, dt_gemm, P.r_pad, dx, P.dsp, ws + P.off_split, at))) return rc;
+    rc = masked ? gemm16_masked_dx(CD, dy, M, K, N, wdt, dtcd, P.r_pad, at, P.r_pad, *sd, dx, c.stream)
+                : dense256_dx(c, dy, wdt, dt_gemm, P.r_pad, dx, P.dsp, ws + P.off_split, at);
+    if (rc) return rc;
   } else if (dx && fast && fused256_ok(c, true)) {
     rc = fused256_dx(c, dy, dt_gemm, P.r_pad, dx, P.dsp, ws + P.off_split);
     if (rc) return rc;
@@ -807,7 +811,7 @@ int backward_gemm(const LayerCall& c, const Seeded* sd, const void* dy, const fl
   if (dx && c.drop_mask &&
       (rc = rank_add_masked(CD, dx, c.drop_mask, dtcd, P.r_pad, c.lora_a, r, M, K, c.stream)))
     return rc;
-  if (dx && sd && (rc = rank_add_seeded(CD, dx, *sd, dtcd, P.r_pad, c.lora_a, r, M, K, c.stream))) return rc;
+  if (dx && sd && !masked && (rc = rank_add_seeded(CD, dx, *sd, dtcd, P.r_pad, c.lora_a, r, M, K, c.stream))) return rc;
 
   // dA = dT^T x and dB = s dY^T T0 (contractions over tokens): on the skinny path
   // both products, then one launch that reduces both.

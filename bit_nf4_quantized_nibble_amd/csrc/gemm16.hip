@@ -1,0 +1,452 @@
+// gemm16.hip -- two 16-bit GEMMs that do more than a product on their way out (gfx950):
+//
+//   gated      h = act(g) u with [g | u] = [x | T] [W~ | B]^T (+ bias) of two projections
+//   masked dX  dX = dY W~ + (dT A) M with M drawn as the products run
+//
+// Both stand on the contraction of tile.h.
+//
+// Gated: a tile's 2 C columns are C columns of the gate and the same C of the up projection, in runs
+// of 32 that alternate, so that a wave's two blocks of columns are g and u of the same 32 columns and
+// h is formed in registers.  The low-rank part is two more stages: T_g against B_g with zeros in the
+// up rows, then T_u against B_u with zeros in the gate rows.
+//
+// Masked: a lane's accumulators hold halves of the groups of eight columns that one counter of the
+// generator serves.  One counter's rounds run beside the products of each stage, one round to a
+// product (two 64-bit products, half the time of a matrix instruction, on the vector pipe that the
+// contraction leaves idle), and leave four mask bits for each group; the low-rank part is multiplied
+// after the last stage into sums of its own, masked and added.
+#include <algorithm>
+#include <type_traits>
+
+#include "act.h"
+#include "mlp.h"
+#include "tile.h"
+
+namespace qnf4 {
+namespace {
+
+using namespace tile;
+
+struct G16 {
+  const void* x;       // [m][K] cd: x, or dY
+  const void *w0, *w1; // [n][K] cd: W~ of the gate and of the up projection, or W~^T and null
+  const void* t;       // [m][ldt] cd: T_g in columns 0 .., T_u in columns 64 .., or dT
+  int64_t ldt;
+  const void *l0, *l1; // [n][ld_l] cd: lora_b of the two, or A^T and null
+  int64_t ldl0, ldl1;  // multiples of 8; columns from there on count as zeros
+  const void* bias;    // [2 n] cd or null
+  void* out;           // [m][n] cd: h, or dX
+  void* pre;           // [m][2 n] cd or null
+  int64_t m, n, K;
+  Seeded sd;
+};
+
+struct Place {
+  int rows;
+  int64_t m0, n0;
+};
+
+// Columns of the output that a tile forms.
+template <class T, bool GATED>
+constexpr int cols_of() { return GATED ? T::TN / 2 : T::TN; }
+
+// The copies of a tile's stages by one wave: instruction i of wave w fills LDS rows
+// 8 (w + NW i) .. + 7 of the stage; lane l lands in chunk l % 8 of row l / 8 and fetches the
+// logical chunk that lies there.  begin() sets up what a stage's copies read.
+template <class T, bool GATED>
+struct Copies16 {
+  static constexpr int NW = T::NW;
+  const G16& p;
+  Place pl;
+  int KM, KT, wave, lane, chunk;
+  int64_t ncols;
+  rsrc_t ra, rb[2];
+  uint32_t oa, ob, sa, sb, so;
+  __device__ __forceinline__ Copies16(const G16& p_, const Place& t, int wave_, int lane_)
+      : p(p_), pl(t), wave(wave_), lane(lane_) {
+    KM = (int)(p.K >> 6);
+    KT = KM + (GATED ? 2 : 0);
+    chunk = (lane & 7) ^ swz(8 * wave + (lane >> 3));
+    ncols = min((int64_t)cols_of<T, GATED>(), p.n - t.n0);
+  }
+  // row of the W-side operand (within its tile) of this lane in copy 0, and the operand of copy i
+  __device__ __forceinline__ int brow() const { return (GATED ? 8 * (wave & 3) : 8 * wave) + (lane >> 3); }
+  __device__ __forceinline__ int side(int i) const { return !GATED ? 0 : NW == 8 ? wave >> 2 : i & 1; }
+  static constexpr int bstep() { return GATED ? 32 : 8 * NW; }
+  static constexpr int bindex(int i) { return GATED && NW == 4 ? i >> 1 : i; }
+  __device__ __forceinline__ void begin(int stage) {
+    const int arow = 8 * wave + (lane >> 3);
+    if (stage < KM) {
+      const uint32_t k2 = (uint32_t)p.K * 2;
+      ra = make_rsrc((const char*)p.x + pl.m0 * p.K * 2, (int64_t)pl.rows * k2);
+      rb[0] = make_rsrc((const char*)p.w0 + pl.n0 * p.K * 2, ncols * k2);
+      if (GATED) rb[1] = make_rsrc((const char*)p.w1 + pl.n0 * p.K * 2, ncols * k2);
+      oa = arow * k2 + 16 * chunk;
+      ob = brow() * k2 + 16 * chunk;
+      sa = 8 * NW * k2;
+      sb = bstep() * k2;
+      so = (uint32_t)stage * 128;
+    } else {
+      // the low-rank part, or (past it) empty buffers: nothing is fetched
+      const int u = stage - KM;
+      const bool in = u < (GATED ? 2 : 1);
+      const int64_t ldl = u ? p.ldl1 : p.ldl0;
+      ra = make_rsrc((const char*)p.t + (pl.m0 * p.ldt + 64 * u) * 2, in ? (pl.rows * p.ldt - 64 * u) * 2 : 0);
+      const void* l = u ? p.l1 : p.l0;
+      const rsrc_t some = make_rsrc((const char*)l + pl.n0 * ldl * 2, in ? ncols * ldl * 2 : 0), none = make_rsrc(p.x, 0);
+      rb[0] = u ? none : some;
+      if (GATED) rb[1] = u ? some : none;
+      // columns that are not there are zeros on both sides: what lies in their place may be no number
+      oa = (uint32_t)(arow * (int)p.ldt * 2 + 16 * chunk) | (8 * chunk < p.ldt ? 0u : 1u << 31);
+      ob = (uint32_t)(brow() * (int)ldl * 2 + 16 * chunk) | (8 * chunk < ldl ? 0u : 1u << 31);
+      sa = (uint32_t)(8 * NW * (int)p.ldt * 2);
+      sb = (uint32_t)(bstep() * (int)ldl * 2);
+      so = 0;
+    }
+  }
+  __device__ __forceinline__ void one(char* stage_lds, int, int i) const {
+    char* dst = stage_lds + (wave + NW * i) * 1024;
+    const int b = i - T::PER_A;
+    if (b < 0) copy16(ra, dst, oa + i * sa, so);
+    else copy16(GATED && side(b) ? rb[1] : rb[0], dst, ob + bindex(b) * sb, so);
+  }
+  __device__ __forceinline__ void all(char* stage_lds, int stage) {
+    begin(stage);
+#pragma unroll
+    for (int i = 0; i < T::PER; ++i) one(stage_lds, stage, i);
+  }
+  __device__ __forceinline__ void scales(int, int (&)[T::WMB], int&) const {}
+  __device__ __forceinline__ void shift(int, int (&)[2][T::WMB], int (&)[2]) const {}
+  __device__ __forceinline__ void stage(int) const {}
+  __device__ __forceinline__ void slot(int) const {}
+};
+
+// The same with a counter of the mask beside each stage's products: counter u (of GROUPS) serves
+// rows 32 (u / (4 WNB)) + lane % 32 and columns 8 (u % (4 WNB)) .. + 7 of the wave's part, of
+// which this lane holds four.
+template <class T>
+struct Masked16 : Copies16<T, false> {
+  static constexpr int PER_ROW = 4 * T::WNB, GROUPS = T::WMB * PER_ROW;
+  static_assert(4 * PER_ROW <= 32, "a row's bits are one word");
+  static_assert(4 * T::WMB * T::WNB >= kPhiloxRounds + 2, "a counter's rounds fit one stage");
+  PhiloxKey key;
+  uint32_t c[4], bits[T::WMB], row, group, threshold;
+  int now;
+  __device__ __forceinline__ Masked16(const G16& p, const Place& t, int wave, int lane)
+      : Copies16<T, false>(p, t, wave, lane), key(philox_key(p.sd)), threshold(p.sd.threshold) {
+    row = (uint32_t)(t.m0 + (wave / T::NWN) * 32 * T::WMB + (lane & 31));
+    group = (uint32_t)((t.n0 + (wave % T::NWN) * 32 * T::WNB) >> 3);
+#pragma unroll
+    for (int i = 0; i < T::WMB; ++i) bits[i] = 0;
+  }
+  __device__ __forceinline__ void start(int u) {
+    c[0] = group + (uint32_t)(u % PER_ROW);
+    c[1] = row + 32u * (uint32_t)(u / PER_ROW);
+    c[2] = key.o0;
+    c[3] = key.o1;
+  }
+  __device__ __forceinline__ void finish(int u) {
+    const bool h = this->lane >= 32;  // columns 4 h .. 4 h + 3: words 2 h and 2 h + 1
+    const uint32_t lo = h ? c[2] : c[0], hi = h ? c[3] : c[1];
+    uint32_t b = (lo & 0xffffu) >= threshold ? 1u : 0u;
+    b |= (lo >> 16) >= threshold ? 2u : 0u;
+    b |= (hi & 0xffffu) >= threshold ? 4u : 0u;
+    b |= (hi >> 16) >= threshold ? 8u : 0u;
+    b <<= 4 * (u % PER_ROW);
+#pragma unroll
+    for (int i = 0; i < T::WMB; ++i) bits[i] |= u / PER_ROW == i ? b : 0u;
+  }
+  __device__ __forceinline__ void stage(int u) { now = u; }
+  __device__ __forceinline__ void slot(int s) {
+    if (now >= GROUPS) return;
+    if (s == 0) start(now);
+    else if (s <= kPhiloxRounds) philox_round(key, s - 1, c);
+    else if (s == kPhiloxRounds + 1) finish(now);
+  }
+  // the counters that had no stage
+  __device__ __forceinline__ void rest() {
+    for (int u = this->KM; u < GROUPS; ++u) {
+      start(u);
+#pragma unroll
+      for (int i = 0; i < kPhiloxRounds; ++i) philox_round(key, i, c);
+      finish(u);
+    }
+  }
+};
+
+// 16-byte chunks of `rows` rows of RB bytes in W (chunk c of row r at chunk c ^ (r % NC)) to columns
+// col0 .. of rows row0 .. of y [..][ld]; every wave issues exactly NC / 2 stores (chunks outside fall
+// past the buffer), then element by element what fills no chunk, and waits for that.
+template <int RB>
+struct Rows16 {
+  static constexpr int NC = RB / 16;
+  __device__ static __forceinline__ int at(int r, int byte) { return r * RB + (((byte >> 4) ^ (r & (NC - 1))) << 4) + (byte & 15); }
+  __device__ static __forceinline__ void store(const char* W, void* y, int64_t ld, int64_t row0, int64_t col0, int left,
+                                               int ncols, int lane) {
+    const int whole = ld < (1 << 25) ? ncols & ~7 : 0;
+    const bool lines = (ld * 2) % 128 == 0 && ((uintptr_t)y & 127) == 0;
+    char* base = (char*)y + (row0 * ld + col0) * 2;
+    const rsrc_t r = make_rsrc(base, left > 0 && whole > 0 ? ((left - 1) * ld + whole) * 2 : 0);
+    const int c = lane & (NC - 1);
+    const uint32_t none = c * 8 < whole ? 0u : 1u << 31;
+#pragma unroll
+    for (int it = 0; it < NC / 2; ++it) {
+      const int m = (64 / NC) * it + lane / NC;
+      const u32x4_t v = *(const u32x4_t*)(W + m * RB + ((c ^ (m & (NC - 1))) << 4));
+      const uint32_t off = (uint32_t)(m * (int)ld * 2 + c * 16);
+      const int o = (int)((m < left ? off : 1u << 31) | none);
+      if (lines) __builtin_amdgcn_raw_buffer_store_b128(v, r, o, 0, 2);
+      else __builtin_amdgcn_raw_buffer_store_b128(v, r, o, 0, 0);
+    }
+    if (ncols > whole) {
+      const int rest = ncols - whole;
+      for (int q = lane; q < 32 * rest; q += 64) {
+        const int m = q / rest, cc = whole + q % rest;
+        if (m < left) ((uint16_t*)base)[m * ld + cc] = *(const uint16_t*)(W + at(m, 2 * cc));
+      }
+      wait_vmcnt<0>();
+    }
+  }
+};
+
+// h (and pre) of a wave's blocks: lane (r32, h) of block (i, j) holds row 32 i + r32, columns
+// 8 q + 4 h + v in elements 4 q + v; j = 0 is g, j = 1 is u.  coef: the tile's biases, gate then up.
+template <int CD, int ACT, class T>
+__device__ __forceinline__ void write_gated(const G16& p, const Place& pl, const Acc<T>& acc, const float* coef, char* W,
+                                            int wave, int lane) {
+  constexpr int C = cols_of<T, true>();
+  const int h = lane >> 5, r32 = lane & 31;
+  const int wm = (wave / T::NWN) * 32 * T::WMB, wc = (wave % T::NWN) * 32;  // the wave's 32 columns
+  const int ncols = (int)max((int64_t)0, min((int64_t)32, p.n - pl.n0 - wc));
+#pragma unroll
+  for (int i = 0; i < T::WMB; ++i) {
+    const int row0 = wm + 32 * i, left = min(32, pl.rows - row0);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const f32x4_t bg = *(const f32x4_t*)(coef + wc + 8 * q + 4 * h), bu = *(const f32x4_t*)(coef + C + wc + 8 * q + 4 * h);
+      float g[4], u[4], o[4];
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        g[v] = acc[i][0][4 * q + v] + bg[v];
+        u[v] = acc[i][1][4 * q + v] + bu[v];
+        o[v] = act_of<ACT>(g[v]) * u[v];
+      }
+      const int at = Rows16<64>::at(r32, 16 * q + 8 * h);
+      *(u32x2_t*)(W + at) = u32x2_t{pack2<CD>(o[0], o[1]), pack2<CD>(o[2], o[3])};
+      if (p.pre) {
+        *(u32x2_t*)(W + 2048 + at) = u32x2_t{pack2<CD>(g[0], g[1]), pack2<CD>(g[2], g[3])};
+        *(u32x2_t*)(W + 4096 + at) = u32x2_t{pack2<CD>(u[0], u[1]), pack2<CD>(u[2], u[3])};
+      }
+    }
+    wait_lgkm0();  // the wave reads back only what it wrote
+    asm volatile("" ::: "memory");
+    Rows16<64>::store(W, p.out, p.n, pl.m0 + row0, pl.n0 + wc, left, ncols, lane);
+    if (p.pre) {
+      Rows16<64>::store(W + 2048, p.pre, 2 * p.n, pl.m0 + row0, pl.n0 + wc, left, ncols, lane);
+      Rows16<64>::store(W + 4096, p.pre, 2 * p.n, pl.m0 + row0, p.n + pl.n0 + wc, left, ncols, lane);
+    }
+    wait_lgkm0();  // the reads are done before the next 32 rows overwrite them
+    asm volatile("" ::: "memory");
+  }
+}
+
+// dX of a wave's blocks: the masked low-rank sums (operands in LDS at `st`, as a stage) added.
+template <int CD, class T>
+__device__ __forceinline__ void add_masked(Acc<T>& acc, const Masked16<T>& cp, const char* st, int wave, int lane) {
+  const int h = lane >> 5, r32 = lane & 31, xr = swz(r32);
+  const int wm = (wave / T::NWN) * 32 * T::WMB, wn = (wave % T::NWN) * 32 * T::WNB;
+  const char *a = st + (wm + r32) * 128, *b = st + (T::TM + wn + r32) * 128;
+#pragma unroll
+  for (int i = 0; i < T::WMB; ++i)
+#pragma unroll
+    for (int j = 0; j < T::WNB; ++j) {
+      f32x16_t low;
+#pragma unroll
+      for (int v = 0; v < 16; ++v) low[v] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < 4; ++ks)
+        Half16<CD>::mma(low, Half16<CD>::read(b + j * 32 * 128, ks, h, xr), Half16<CD>::read(a + i * 32 * 128, ks, h, xr), 0, 0);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+          acc[i][j][4 * q + v] += cp.bits[i] >> (4 * (4 * j + q) + v) & 1u ? low[4 * q + v] : 0.f;
+    }
+}
+template <int CD, class T>
+__device__ __forceinline__ void write_plain(const G16& p, const Place& pl, const Acc<T>& acc, char* W, int wave, int lane) {
+  constexpr int RB = 64 * T::WNB;
+  const int h = lane >> 5, r32 = lane & 31;
+  const int wm = (wave / T::NWN) * 32 * T::WMB, wn = (wave % T::NWN) * 32 * T::WNB;
+  const int ncols = (int)max((int64_t)0, min((int64_t)(32 * T::WNB), p.n - pl.n0 - wn));
+#pragma unroll
+  for (int i = 0; i < T::WMB; ++i) {
+#pragma unroll
+    for (int j = 0; j < T::WNB; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *(u32x2_t*)(W + Rows16<RB>::at(r32, 64 * j + 16 * q + 8 * h)) =
+            u32x2_t{pack2<CD>(acc[i][j][4 * q], acc[i][j][4 * q + 1]), pack2<CD>(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3])};
+    wait_lgkm0();
+    asm volatile("" ::: "memory");
+    Rows16<RB>::store(W, p.out, p.n, pl.m0 + wm + 32 * i, pl.n0 + wn, min(32, pl.rows - wm - 32 * i), ncols, lane);
+    wait_lgkm0();
+    asm volatile("" ::: "memory");
+  }
+}
+
+// A workgroup goes through its tiles.  After a tile's last stage the copies of the next tile's first
+// stage are requested, so that they land while this one's outputs are formed and stored; those pass
+// through what were the other stages.
+template <int CD, class T, bool GATED, int WGS>
+__global__ __launch_bounds__(64 * T::NW, WGS) void k_gemm16(G16 p, int act) {
+  constexpr int C = cols_of<T, GATED>(), COEF = GATED ? 2 * C : 0, STAGING = GATED ? 6144 : 2048 * T::WNB;
+  // masked: the low-rank operands lie in the buffer of stage KM, wherever that is; the staging goes
+  // where they were once every wave has read them
+  static_assert((GATED ? T::LDS - T::STAGE : T::STAGE) >= T::NW * STAGING, "staging fits");
+  __shared__ __attribute__((aligned(1024))) char lds[T::LDS + 2 * COEF * 4];  // one array: see fp8.hip
+  float* coefs = (float*)(lds + T::LDS);  // two sets, used in turn
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int tiles_n = (int)((p.n + C - 1) / C), tiles_m = (int)((p.m + T::TM - 1) / T::TM), total = tiles_m * tiles_n;
+  const int G = gridDim.x, b = blockIdx.x;
+  auto item = [&](int r) {
+    Place pl = {0, 0, 0};
+    const int64_t base = (int64_t)r * G;
+    const int n = (int)min((int64_t)G, total - base);
+    if (b >= n) return pl;
+    int tm, tn;
+    grouped_tile((int)base + xcd_run(b, n), tiles_m, tiles_n, tm, tn);
+    pl.m0 = (int64_t)__builtin_amdgcn_readfirstlane(tm) * T::TM;
+    pl.n0 = (int64_t)__builtin_amdgcn_readfirstlane(tn) * C;
+    pl.rows = (int)min((int64_t)T::TM, p.m - pl.m0);
+    return pl;
+  };
+  auto coef_of = [&](const Place& pl, int i) {
+    const int64_t col = pl.n0 + (i >= C ? i - C : i);
+    return p.bias && col < p.n ? load_cd<CD>(p.bias, col + (i >= C ? p.n : 0)) : 0.f;
+  };
+  using Copier = std::conditional_t<GATED, Copies16<T, GATED>, Masked16<T>>;
+
+  Place cur = item(0);
+  if (cur.rows == 0) return;
+  if (GATED)
+    for (int i = tid; i < COEF; i += 64 * T::NW) coefs[i] = coef_of(cur, i);
+  Copies16<T, GATED>(p, cur, wave, lane).all(lds, 0);
+  wait_vmcnt<0>();
+  int set = 0;
+  for (int r = 1;; ++r) {
+    const Place nxt = item(r);
+    static_assert(COEF <= 64 * T::NW, "one coefficient to a thread");
+    const float c = GATED && nxt.rows && tid < COEF ? coef_of(nxt, tid) : 0.f;
+    wait_lgkm0();
+    barrier_only();  // stage 0 and the coefficients are there, the staging of the tile before is free
+    Copier cp(p, cur, wave, lane);
+#pragma unroll
+    for (int s = 1; s < T::NS; ++s) cp.all(lds + s * T::STAGE, s);
+    Acc<T> acc;
+    zero<T>(acc);
+    contract<T, Half16<CD>>(acc, lds, cp, wave, lane);
+    if constexpr (!GATED) {
+      cp.rest();
+      const int at = cp.KM % T::NS;
+      add_masked<CD, T>(acc, cp, lds + at * T::STAGE, wave, lane);
+      __syncthreads();  // every wave is past the low-rank operands
+    }
+    if (nxt.rows) {
+      if (GATED && tid < COEF) coefs[(set ^ 1) * COEF + tid] = c;
+      Copies16<T, GATED>(p, nxt, wave, lane).all(lds, 0);
+    }
+    char* W = lds + T::STAGE + wave * STAGING;
+    constexpr int STORES = GATED ? T::WMB * 2 : T::WMB * 2 * T::WNB;
+    if constexpr (GATED) {
+      const float* co = coefs + set * COEF;
+      if (act == QLORA_ACT_SILU) write_gated<CD, QLORA_ACT_SILU, T>(p, cur, acc, co, W, wave, lane);
+      else if (act == QLORA_ACT_GELU) write_gated<CD, QLORA_ACT_GELU, T>(p, cur, acc, co, W, wave, lane);
+      else write_gated<CD, QLORA_ACT_GELU_TANH, T>(p, cur, acc, co, W, wave, lane);
+    } else {
+      write_plain<CD, T>(p, cur, acc, W, wave, lane);
+    }
+    if (nxt.rows == 0) return;
+    asm volatile("" ::: "memory");
+    wait_vmcnt<STORES>();  // this wave's copies of the next first stage, older than the stores, have landed
+    cur = nxt;
+    set ^= 1;
+  }
+}
+
+using Full = Tile<4, 2, 2, 4, 2>;  // 256 rows x 256 columns (128 of each projection), eight waves
+using Wide = Tile<2, 2, 2, 4, 3>;  // 128 x 256, eight waves
+using Mid = Tile<2, 2, 2, 2, 4>;   // 128 x 128, four waves
+using Low = Tile<1, 2, 2, 2, 3>;   // 64 x 128, four waves; two workgroups fit a compute unit
+
+template <int CD, class T, bool GATED, int WGS>
+int run(const G16& p, int act, int kind, hipStream_t s) {
+  const int64_t tiles = ceil_div(p.m, T::TM) * ceil_div(p.n, cols_of<T, GATED>());
+  ProfScope prof(kind, s);
+  k_gemm16<CD, T, GATED, WGS><<<dim3((unsigned)std::min<int64_t>(tiles, cu_count() * WGS)), dim3(64 * T::NW), 0, s>>>(p, act);
+  return check_launch("k_gemm16");
+}
+
+// The smallest tiles that fit the compute units in one round, the largest beyond.
+template <int CD, bool GATED>
+int run_cd(const G16& p, int act, int kind, hipStream_t s) {
+  auto one_round = [&](int64_t tm, int64_t tn) {
+    return ceil_div(p.m, tm) * ceil_div(p.n, GATED ? tn / 2 : tn) <= cu_count();
+  };
+  if constexpr (GATED)
+    if (one_round(64, 128)) return run<CD, Low, GATED, 2>(p, act, kind, s);
+  if (one_round(128, 128)) return run<CD, Mid, GATED, 1>(p, act, kind, s);
+  if (one_round(128, 256)) return run<CD, Wide, GATED, 1>(p, act, kind, s);
+  return run<CD, Full, GATED, 1>(p, act, kind, s);
+}
+
+}  // namespace
+
+// Whether the kernels take a call: 16-bit operands, whole stages of K, offsets within a tile below 2^31.
+bool gemm16_ok(int cd, int64_t m, int64_t n, int64_t K) {
+  return (cd == CD_BF16 || cd == CD_F16) && K % 64 == 0 && K > 0 && K < (1 << 21) && m > 0 && m < (1LL << 31) && n > 0 &&
+         n < (1LL << 31) && ceil_div(m, 64) * ceil_div(n, 64) < (1LL << 31);
+}
+
+// h (and pre, if not null) of x [m][K], W~ w[i] [n][K], T [m][128] (T_i in columns 64 i ..), lora_b b[i] [n][ldb[i]]
+// with ldb a multiple of 8.
+int gemm16_gated(int cd, const void* x, int64_t m, int64_t n, int64_t K, const void* const* w, const void* t,
+                 const void* const* b, const int64_t* ldb, const void* bias, int act, void* h, void* pre, hipStream_t s) {
+  G16 p = {};
+  p.x = x;
+  p.w0 = w[0];
+  p.w1 = w[1];
+  p.t = t;
+  p.ldt = 128;
+  p.l0 = b[0];
+  p.l1 = b[1];
+  p.ldl0 = ldb[0];
+  p.ldl1 = ldb[1];
+  p.bias = bias;
+  p.out = h;
+  p.pre = pre;
+  p.m = m;
+  p.n = n;
+  p.K = K;
+  return cd == CD_BF16 ? run_cd<CD_BF16, true>(p, act, QLORA_K_FWD_GEMM, s) : run_cd<CD_F16, true>(p, act, QLORA_K_FWD_GEMM, s);
+}
+
+// dX [m][n] = dY [m][K] W~^T wt [n][K] + (dT [m][ldt] A^T at [n][lda]) M, ldt and lda multiples of 8, at most 64.
+int gemm16_masked_dx(int cd, const void* dy, int64_t m, int64_t n, int64_t K, const void* wt, const void* dt, int64_t ldt,
+                     const void* at, int64_t lda, const Seeded& sd, void* dx, hipStream_t s) {
+  G16 p = {};
+  p.x = dy;
+  p.w0 = wt;
+  p.t = dt;
+  p.ldt = ldt;
+  p.l0 = at;
+  p.ldl0 = lda;
+  p.out = dx;
+  p.m = m;
+  p.n = n;
+  p.K = K;
+  p.sd = sd;
+  return cd == CD_BF16 ? run_cd<CD_BF16, false>(p, 0, QLORA_K_BWD_DX, s) : run_cd<CD_F16, false>(p, 0, QLORA_K_BWD_DX, s);
+}
+
+}  // namespace qnf4

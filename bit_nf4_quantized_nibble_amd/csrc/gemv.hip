@@ -26,7 +26,8 @@
 // (T = s x A^T) and k_gemv (one wavefront per output row on the VALU).
 #include <algorithm>
 
-#include "common.h"
+#include "act.h"
+#include "mlp.h"
 
 namespace qnf4 {
 namespace {
@@ -351,7 +352,7 @@ __device__ __forceinline__ void reduce_store(const GemvP& p, const WaveView& v, 
 // requested before the previous tile is decoded); workgroups from G on take one
 // 32-row block of lora_a each.
 template <int CD, int DQ, int NBK, int MT, int LOOP>
-__global__ __launch_bounds__(kGemvThreads) void k_gemv_k(GemvP p, Nf4Tables tab) {
+__device__ __forceinline__ void gemv_body(const GemvP& p, const Nf4Tables& tab) {
   __shared__ __attribute__((aligned(16))) float2 s_pair[256];
   __shared__ __attribute__((aligned(16))) float s_sc[4][kRows][8];  // per wave: block scales [row][block of the sub-slice]
   __shared__ __attribute__((aligned(16))) unsigned char s_tile[4 * kRows * 128];  // per wave: swizzled code tile
@@ -454,6 +455,72 @@ __global__ __launch_bounds__(kGemvThreads) void k_gemv_k(GemvP p, Nf4Tables tab)
       run_tile(tb, (int64_t)rb * kRows);
       if (rt >= nt) break;
     }
+  }
+}
+
+template <int CD, int DQ, int NBK, int MT, int LOOP>
+__global__ __launch_bounds__(kGemvThreads) void k_gemv_k(GemvP p, Nf4Tables tab) {
+  gemv_body<CD, DQ, NBK, MT, LOOP>(p, tab);
+}
+
+// The gate and the up projection of a gated block in one launch (blockIdx.z): up to 16 tokens of the
+// same x, weights of the same shape and layout; their ranks may differ, so a workgroup past its own
+// projection's row blocks of lora_a leaves.
+struct GemvPair {
+  GemvP p[2];
+};
+template <int CD, int DQ, int NBK>
+__global__ __launch_bounds__(kGemvThreads) void k_gemv_pair(GemvPair ps, Nf4Tables tab) {
+  const GemvP& p = ps.p[blockIdx.z];
+  if ((int64_t)blockIdx.x - p.G >= (p.r + kRows - 1) / kRows) return;
+  gemv_body<CD, DQ, NBK, 1, 0>(p, tab);
+}
+
+// h[m, n] = act(g) u from the partials of the gate (ps.p[0]) and of the up projection (ps.p[1]).
+// Workgroup: 128 columns of one token; threads 0 .. 127 form g, the others u, and g's threads h.
+// Sums over slices run in slice order.
+template <int CD>
+__global__ __launch_bounds__(kThreads) void k_gemv_gated_epi(GemvPair ps, int act, void* __restrict__ h,
+                                                             void* __restrict__ pre) {
+  extern __shared__ __attribute__((aligned(16))) float s_t[];  // [2][r of the larger rank rounded up to 8]
+  __shared__ float s_u[128];
+  const int tid = threadIdx.x, side = __builtin_amdgcn_readfirstlane(tid >> 7), c = tid & 127;
+  const GemvP& p = ps.p[side];
+  const int64_t m = blockIdx.y, N = p.w.rows, n = (int64_t)blockIdx.x * 128 + c, nc = min(n, N - 1);
+  const int64_t ss = p.mp * p.ld;
+  const float* part = p.part + m * p.ld;
+  float* t = s_t + side * ((max(ps.p[0].r, ps.p[1].r) + 7) & ~7);
+  float z = 0.f;
+#pragma unroll 4
+  for (int i = 0; i < p.S; ++i) z += part[i * ss + nc];
+  const float bias = p.bias ? load_cd<CD>(p.bias, nc) : 0.f;
+  for (int e = c; e < p.r; e += 128) {
+    float sum = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < p.S; ++i) sum += part[i * ss + p.n_pad + e];
+    t[e] = sum * p.scale;
+    if (p.t0 && blockIdx.x == 0) p.t0[m * p.r + e] = sum;
+  }
+  __syncthreads();
+  float lora = 0.f;
+  if ((p.r & 7) == 0) {  // rows of lora_b are whole 16-byte chunks
+#pragma unroll 2
+    for (int e = 0; e < p.r; e += 8) {
+      const u32x4_t b = *(const u32x4_t*)((const uint16_t*)p.B + nc * p.r + e);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) lora = fmaf(t[e + k], from_cd16<CD>((uint16_t)(b[k >> 1] >> (16 * (k & 1)))), lora);
+    }
+  } else {
+    for (int e = 0; e < p.r; ++e) lora = fmaf(t[e], load_cd<CD>(p.B, nc * p.r + e), lora);
+  }
+  z += lora + bias;
+  if (side) s_u[c] = z;
+  if (pre && n < N) store_cd<CD>(pre, m * 2 * N + side * N + n, z);
+  __syncthreads();
+  if (!side && n < N) {
+    const float a = act == QLORA_ACT_SILU ? act_of<QLORA_ACT_SILU>(z)
+                    : act == QLORA_ACT_GELU ? act_of<QLORA_ACT_GELU>(z) : act_of<QLORA_ACT_GELU_TANH>(z);
+    store_cd<CD>(h, m * N + n, a * s_u[c]);
   }
 }
 
@@ -691,6 +758,86 @@ bool mfma_form_ok(const LayerCall& c) {
          (int64_t)P.S * P.mp * P.ld * 4 < 0x7fff0000LL;
 }
 
+// The kernel's view of a call whose partial sums start at `part` (null y: the caller's epilogue).
+GemvP gemv_params(const LayerCall& c, const GemvPlan& P, float* part, void* y, float* t_save) {
+  GemvP p = {};
+  p.w = c.w;
+  p.x = c.x;
+  p.M = c.m;
+  p.A = c.lora_a;
+  p.B = c.lora_b;
+  p.r = c.r;
+  p.scale = c.scale;
+  p.bias = c.bias;
+  p.y = y;
+  p.ldy = c.ldy ? c.ldy : c.w.rows;
+  p.t0 = t_save;
+  p.part = part;
+  p.n_pad = P.n_pad;
+  p.ld = P.ld;
+  p.mp = P.mp;
+  p.S = P.S;
+  return p;
+}
+
+// The partial sums of one projection.
+template <int CD>
+int gemv_partials(const LayerCall& c, const GemvPlan& P, GemvP& p) {
+  ProfScope prof(QLORA_K_GEMV, c.stream);
+  const int nbk = c.w.bs_shift >= 8 ? 1 : 1 << (8 - c.w.bs_shift);  // blocks per 256-element sub-slice
+  const int mt = (int)(P.mp / 16);  // token groups of 16 (1, 2 or 4)
+  const int64_t nt = P.n_pad / kRows, lt = P.r_pad / kRows;  // W tiles, lora_a row blocks
+  const int64_t slots = gemv_loop_slots(mt), g_loop = std::max<int64_t>(1, slots / P.S);
+  // measured: the looping form wins with two or more token groups (x re-reads
+  // dominate), at most 8 slices and at least 3 tiles per workgroup; at one
+  // token group many independent workgroups hide latency better
+  const bool loop = mt >= 2 && P.S <= 8 && nt >= 3 * g_loop;
+  p.G = (int32_t)(loop ? g_loop : nt);
+  const dim3 grid((unsigned)(p.G + lt), (unsigned)P.S);
+  launch_gemv_k<CD>(p, grid, c.w.dq, loop, nbk, mt, c.stream);
+  return check_launch("k_gemv_k");
+}
+
+template <int CD, int DQ>
+void launch_pair(const GemvPair& ps, dim3 grid, int nbk, hipStream_t st) {
+  const dim3 blk(kGemvThreads);
+  if (nbk == 1) k_gemv_pair<CD, DQ, 1><<<grid, blk, 0, st>>>(ps, host_tables());
+  else if (nbk == 2) k_gemv_pair<CD, DQ, 2><<<grid, blk, 0, st>>>(ps, host_tables());
+  else if (nbk == 4) k_gemv_pair<CD, DQ, 4><<<grid, blk, 0, st>>>(ps, host_tables());
+  else k_gemv_pair<CD, DQ, 8><<<grid, blk, 0, st>>>(ps, host_tables());
+}
+
+template <int CD>
+int gemv_gated_t(const LayerCall* c, int act, void* h, void* pre, float* const* t_save) {
+  GemvPair ps;
+  char* ws = (char*)c[0].ws;
+  GemvPlan P[2];
+  for (int i = 0; i < 2; ++i) {
+    P[i] = plan_gemv(c[i].m, c[i].w.rows, c[i].w.cols, c[i].r, CD);
+    ps.p[i] = gemv_params(c[i], P[i], (float*)(ws + P[i].off_part), nullptr, t_save ? t_save[i] : nullptr);
+    ws += P[i].total;
+  }
+  const Nf4W &a = c[0].w, &b = c[1].w;
+  int rc;
+  if (P[0].mp == 16 && a.bs_shift == b.bs_shift && a.dq == b.dq) {
+    ProfScope prof(QLORA_K_GEMV, c[0].stream);
+    const int nbk = a.bs_shift >= 8 ? 1 : 1 << (8 - a.bs_shift);
+    ps.p[0].G = ps.p[1].G = (int32_t)(P[0].n_pad / kRows);
+    const dim3 grid((unsigned)(ps.p[0].G + std::max(P[0].r_pad, P[1].r_pad) / kRows), (unsigned)P[0].S, 2);
+    if (a.dq) launch_pair<CD, 1>(ps, grid, nbk, c[0].stream);
+    else launch_pair<CD, 0>(ps, grid, nbk, c[0].stream);
+    if ((rc = check_launch("k_gemv_pair"))) return rc;
+  } else {
+    for (int i = 0; i < 2; ++i)
+      if ((rc = gemv_partials<CD>(c[i], P[i], ps.p[i]))) return rc;
+  }
+  ProfScope prof(QLORA_K_GATE, c[0].stream);
+  const size_t lds = 2 * (size_t)round_up(std::max(c[0].r, c[1].r), 8) * sizeof(float);
+  k_gemv_gated_epi<CD><<<dim3((unsigned)ceil_div(a.rows, 128), (unsigned)c[0].m), dim3(kThreads), lds, c[0].stream>>>(
+      ps, act, h, pre);
+  return check_launch("k_gemv_gated_epi");
+}
+
 template <int CD>
 int gemv_forward_t(const LayerCall& c, void* y, float* t_save) {
   const GemvPlan P = plan_gemv(c.m, c.w.rows, c.w.cols, c.r, c.cd);
@@ -699,39 +846,9 @@ int gemv_forward_t(const LayerCall& c, void* y, float* t_save) {
   char* ws = (char*)c.ws;
   if constexpr (CD != CD_F32) {
     if (mfma) {
-      GemvP p = {};
-      p.w = c.w;
-      p.x = c.x;
-      p.M = c.m;
-      p.A = c.lora_a;
-      p.B = c.lora_b;
-      p.r = c.r;
-      p.scale = c.scale;
-      p.bias = c.bias;
-      p.y = y;
-      p.ldy = c.ldy ? c.ldy : c.w.rows;
-      p.t0 = t_save;
-      p.part = (float*)(ws + P.off_part);
-      p.n_pad = P.n_pad;
-      p.ld = P.ld;
-      p.mp = P.mp;
-      p.S = P.S;
-      {
-        ProfScope prof(QLORA_K_GEMV, c.stream);
-        const int nbk = c.w.bs_shift >= 8 ? 1 : 1 << (8 - c.w.bs_shift);  // blocks per 256-element sub-slice
-        const int mt = (int)(P.mp / 16);  // token groups of 16 (1, 2 or 4)
-        const int64_t nt = P.n_pad / kRows, lt = P.r_pad / kRows;  // W tiles, lora_a row blocks
-        const int64_t slots = gemv_loop_slots(mt), g_loop = std::max<int64_t>(1, slots / P.S);
-        // measured: the looping form wins with two or more token groups (x re-reads
-        // dominate), at most 8 slices and at least 3 tiles per workgroup; at one
-        // token group many independent workgroups hide latency better
-        const bool loop = mt >= 2 && P.S <= 8 && nt >= 3 * g_loop;
-        p.G = (int32_t)(loop ? g_loop : nt);
-        const dim3 grid((unsigned)(p.G + lt), (unsigned)P.S);
-        launch_gemv_k<CD>(p, grid, c.w.dq, loop, nbk, mt, c.stream);
-        int rc = check_launch("k_gemv_k");
-        if (rc) return rc;
-      }
+      GemvP p = gemv_params(c, P, (float*)(ws + P.off_part), y, t_save);
+      const int rc = gemv_partials<CD>(c, P, p);
+      if (rc) return rc;
       ProfScope prof(QLORA_K_REDUCE, c.stream);
       // tokens per epilogue workgroup (T's rows for them sit in LDS): one up to 16
       // tokens (the most workgroups; re-reading lora_b is cheap), above that 8 when
@@ -768,6 +885,19 @@ int gemv_forward_t(const LayerCall& c, void* y, float* t_save) {
 }  // namespace
 
 bool gemv_mfma_ok(const LayerCall& c) { return mfma_form_ok(c); }
+
+// Whether the gated block's decode form takes the pair: both projections on the split-K form, whose
+// ranks' T fits LDS.  Its workspace: the partial sums of both, in c[0].ws.
+bool gemv_gated_ok(const LayerCall* c) {
+  return gemv_route(c[0]) && gemv_route(c[1]) && mfma_form_ok(c[0]) && mfma_form_ok(c[1]) && c[0].r <= 4096 && c[1].r <= 4096;
+}
+size_t gemv_gated_workspace_bytes(const LayerCall* c) {
+  return gemv_workspace_bytes(c[0].m, c[0].w.rows, c[0].w.cols, c[0].r, c[0].cd) +
+         gemv_workspace_bytes(c[1].m, c[1].w.rows, c[1].w.cols, c[1].r, c[1].cd);
+}
+int gemv_gated(const LayerCall* c, int act, void* h, void* pre, float* const* t_save) {
+  return c[0].cd == CD_BF16 ? gemv_gated_t<CD_BF16>(c, act, h, pre, t_save) : gemv_gated_t<CD_F16>(c, act, h, pre, t_save);
+}
 
 size_t gemv_workspace_bytes(int64_t m, int64_t rows, int64_t cols, int32_t r, int cd) {
   return (size_t)plan_gemv(m, rows, cols, r, cd).total;

@@ -37,6 +37,18 @@ int rank_add_seeded(int cd, void* dx, const Seeded& sd, const void* dt, int64_t 
 int launch_backward_group_as(const GroupCall& gc, const void* dy, const float* const* t_saved, void* dx,
                              void* const* d_a, void* const* d_b, int gd, void* ws, hipStream_t s);
 
+// gemv.hip: the gated block's forward of up to 64 tokens (c: gate and up).
+size_t gemv_workspace_bytes(int64_t m, int64_t rows, int64_t cols, int32_t r, int cd);
+bool gemv_gated_ok(const LayerCall* c);
+size_t gemv_gated_workspace_bytes(const LayerCall* c);
+int gemv_gated(const LayerCall* c, int act, void* h, void* pre, float* const* t_save);
+// gemm16.hip
+bool gemm16_ok(int cd, int64_t m, int64_t n, int64_t K);
+int gemm16_gated(int cd, const void* x, int64_t m, int64_t n, int64_t K, const void* const* w, const void* t,
+                 const void* const* b, const int64_t* ldb, const void* bias, int act, void* h, void* pre, hipStream_t s);
+int gemm16_masked_dx(int cd, const void* dy, int64_t m, int64_t n, int64_t K, const void* wt, const void* dt, int64_t ldt,
+                     const void* at, int64_t lda, const Seeded& sd, void* dx, hipStream_t s);
+
 size_t gated_workspace_bytes(int op, const GroupCall& gc);
 int launch_gated_fwd(const GroupCall& gc, int act, const void* bias, void* h, void* pre, float* const* t_save, void* ws,
                      hipStream_t s);

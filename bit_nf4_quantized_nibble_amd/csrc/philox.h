@@ -28,20 +28,22 @@ __device__ __forceinline__ PhiloxKey philox_key(const Seeded& s) {
   return {(uint32_t)k, (uint32_t)(k >> 32), (uint32_t)o, (uint32_t)(o >> 32)};
 }
 
+// Round i of a counter's words.
+constexpr int kPhiloxRounds = 10;
+__device__ __forceinline__ void philox_round(const PhiloxKey& key, int i, uint32_t (&c)[4]) {
+  const uint64_t a = (uint64_t)c[0] * 0xD2511F53u, b = (uint64_t)c[2] * 0xCD9E8D57u;
+  c[0] = (uint32_t)(b >> 32) ^ c[1] ^ (key.k0 + (uint32_t)i * 0x9E3779B9u);
+  c[1] = (uint32_t)b;
+  c[2] = (uint32_t)(a >> 32) ^ c[3] ^ (key.k1 + (uint32_t)i * 0xBB67AE85u);
+  c[3] = (uint32_t)a;
+}
+
 // The four words of columns 8 group .. 8 group + 7 of a row.
 __device__ __forceinline__ u32x4_t philox(const PhiloxKey& key, uint32_t group, uint32_t row) {
-  uint32_t c0 = group, c1 = row, c2 = key.o0, c3 = key.o1, k0 = key.k0, k1 = key.k1;
+  uint32_t c[4] = {group, row, key.o0, key.o1};
 #pragma unroll
-  for (int i = 0; i < 10; ++i) {
-    const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
-    c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
-    c1 = (uint32_t)b;
-    c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
-    c3 = (uint32_t)a;
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
-  }
-  return u32x4_t{c0, c1, c2, c3};
+  for (int i = 0; i < kPhiloxRounds; ++i) philox_round(key, i, c);
+  return u32x4_t{c[0], c[1], c[2], c[3]};
 }
 __device__ __forceinline__ bool keeps(const u32x4_t& w, int e, uint32_t threshold) {
   return ((w[e >> 1] >> (16 * (e & 1))) & 0xffffu) >= threshold;

@@ -144,10 +144,10 @@ __device__ __forceinline__ void zero(Acc<T>& acc) {
 // last stage it brings zeros or nothing anyone reads); cp.begin(stage) is called when a stage's
 // copies begin, cp.scales(stage, ..) when its first fragments are read and cp.shift(stage, ..) once the
 // stage before is done (what scales() has read becomes the scales in use: no product waits for the
-// read), and cp.middle(acc, stage) before its products.  On entry stage 0 lies in LDS for every wave and the copies of stages
+// read); cp.stage(stage) begins a stage, cp.slot(s) runs beside its product s (what it does hides behind the matrix pipe).  On entry stage 0 lies in LDS for every wave and the copies of stages
 // 1 .. NS - 1 are requested; on return the LDS is free.
 template <class T, class KIND, class C>
-__device__ __forceinline__ void contract(Acc<T>& acc, char* lds, const C& cp, int wave, int lane) {
+__device__ __forceinline__ void contract(Acc<T>& acc, char* lds, C& cp, int wave, int lane) {
   constexpr int WMB = T::WMB, WNB = T::WNB, NMF = WMB * WNB, SUB = KIND::SUB, SETS = KIND::SETS;
   // where in the last sub-step the barrier stands: before the first read of the next stage
   constexpr int BAR = SETS == 2 || NMF < 4 ? 0 : NMF < 8 ? 1 : 2;
@@ -172,7 +172,7 @@ __device__ __forceinline__ void contract(Acc<T>& acc, char* lds, const C& cp, in
     char* st = lds + buf * T::STAGE;
     const int nbuf = buf + 1 == T::NS ? 0 : buf + 1;
     const char* nx = lds + nbuf * T::STAGE;
-    cp.middle(acc, u);
+    cp.stage(u);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int ks = 0; ks < SUB; ++ks) {
@@ -190,6 +190,7 @@ __device__ __forceinline__ void contract(Acc<T>& acc, char* lds, const C& cp, in
         }
         const int i = t % WMB, j = t / WMB;
         KIND::mma(acc[i][j], fb[set][j], fa[set][i], sb[0], sa[0][i]);
+        cp.slot(ks * NMF + t);
         if constexpr (SETS == 2) {
 #pragma unroll
           for (int q = 0; q < WMB + WNB; ++q)
