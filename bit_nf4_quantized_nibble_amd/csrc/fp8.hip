@@ -236,6 +236,7 @@ struct Copies8 {
     for (int i = 0; i < T::WMB; ++i) s[0][i] = (int)((uint32_t)s[1][i] >> (8 * (stage & 3)));
     sb[0] = sb[1];
   }
+  static constexpr int kSlots = 0;
   __device__ __forceinline__ void stage(int) const {}
   __device__ __forceinline__ void slot(int) const {}
 };

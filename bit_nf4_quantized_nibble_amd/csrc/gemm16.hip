@@ -50,12 +50,16 @@ struct Place {
 template <class T, bool GATED>
 constexpr int cols_of() { return GATED ? T::TN / 2 : T::TN; }
 
-// The copies of a tile's stages by one wave: instruction i of wave w fills LDS rows
+// Waves that copy: four of the largest tile's eight (contract_two), else all.
+template <class T>
+constexpr int copying() { return T::TM == 256 ? 4 : T::NW; }
+
+// The copies of a tile's stages by one wave: instruction i of copying wave w fills LDS rows
 // 8 (w + NW i) .. + 7 of the stage; lane l lands in chunk l % 8 of row l / 8 and fetches the
 // logical chunk that lies there.  begin() sets up what a stage's copies read.
 template <class T, bool GATED>
 struct Copies16 {
-  static constexpr int NW = T::NW;
+  static constexpr int NW = copying<T>(), PER_A = T::TM / 8 / NW, PER = (T::TM + T::TN) / 8 / NW, kSlots = 0;
   const G16& p;
   Place pl;
   int KM, KT, wave, lane, chunk;
@@ -106,14 +110,15 @@ struct Copies16 {
   }
   __device__ __forceinline__ void one(char* stage_lds, int, int i) const {
     char* dst = stage_lds + (wave + NW * i) * 1024;
-    const int b = i - T::PER_A;
+    const int b = i - PER_A;
     if (b < 0) copy16(ra, dst, oa + i * sa, so);
     else copy16(GATED && side(b) ? rb[1] : rb[0], dst, ob + bindex(b) * sb, so);
   }
   __device__ __forceinline__ void all(char* stage_lds, int stage) {
+    if (NW < T::NW && wave >= NW) return;
     begin(stage);
 #pragma unroll
-    for (int i = 0; i < T::PER; ++i) one(stage_lds, stage, i);
+    for (int i = 0; i < PER; ++i) one(stage_lds, stage, i);
   }
   __device__ __forceinline__ void scales(int, int (&)[T::WMB], int&) const {}
   __device__ __forceinline__ void shift(int, int (&)[2][T::WMB], int (&)[2]) const {}
@@ -126,7 +131,7 @@ struct Copies16 {
 // which this lane holds four.
 template <class T>
 struct Masked16 : Copies16<T, false> {
-  static constexpr int PER_ROW = 4 * T::WNB, GROUPS = T::WMB * PER_ROW;
+  static constexpr int PER_ROW = 4 * T::WNB, GROUPS = T::WMB * PER_ROW, kSlots = GROUPS;
   static_assert(4 * PER_ROW <= 32, "a row's bits are one word");
   static_assert(4 * T::WMB * T::WNB >= kPhiloxRounds + 2, "a counter's rounds fit one stage");
   PhiloxKey key;
@@ -158,7 +163,6 @@ struct Masked16 : Copies16<T, false> {
   }
   __device__ __forceinline__ void stage(int u) { now = u; }
   __device__ __forceinline__ void slot(int s) {
-    if (now >= GROUPS) return;
     if (s == 0) start(now);
     else if (s <= kPhiloxRounds) philox_round(key, s - 1, c);
     else if (s == kPhiloxRounds + 1) finish(now);
@@ -332,7 +336,8 @@ __global__ __launch_bounds__(64 * T::NW, WGS) void k_gemm16(G16 p, int act) {
   if (GATED)
     for (int i = tid; i < COEF; i += 64 * T::NW) coefs[i] = coef_of(cur, i);
   Copies16<T, GATED>(p, cur, wave, lane).all(lds, 0);
-  wait_vmcnt<0>();
+  constexpr bool TWO = copying<T>() < T::NW;
+  if (!TWO) wait_vmcnt<0>();
   int set = 0;
   for (int r = 1;; ++r) {
     const Place nxt = item(r);
@@ -341,11 +346,15 @@ __global__ __launch_bounds__(64 * T::NW, WGS) void k_gemm16(G16 p, int act) {
     wait_lgkm0();
     barrier_only();  // stage 0 and the coefficients are there, the staging of the tile before is free
     Copier cp(p, cur, wave, lane);
-#pragma unroll
-    for (int s = 1; s < T::NS; ++s) cp.all(lds + s * T::STAGE, s);
     Acc<T> acc;
     zero<T>(acc);
-    contract<T, Half16<CD>>(acc, lds, cp, wave, lane);
+    if constexpr (TWO) {
+      contract_two<T, Half16<CD>>(acc, lds, cp, wave, lane);
+    } else {
+#pragma unroll
+      for (int s = 1; s < T::NS; ++s) cp.all(lds + s * T::STAGE, s);
+      contract<T, Half16<CD>>(acc, lds, cp, wave, lane);
+    }
     if constexpr (!GATED) {
       cp.rest();
       const int at = cp.KM % T::NS;
@@ -368,7 +377,7 @@ __global__ __launch_bounds__(64 * T::NW, WGS) void k_gemm16(G16 p, int act) {
     }
     if (nxt.rows == 0) return;
     asm volatile("" ::: "memory");
-    wait_vmcnt<STORES>();  // this wave's copies of the next first stage, older than the stores, have landed
+    if (!TWO) wait_vmcnt<STORES>();  // this wave's copies of the next first stage, older than the stores, have landed
     cur = nxt;
     set ^= 1;
   }

@@ -18,6 +18,8 @@
 // outer loop: four or more products of 64 cycles lie between a fragment's read and its use).
 #pragma once
 
+#include <type_traits>
+
 #include "common.h"
 
 namespace qnf4 {
@@ -144,7 +146,8 @@ __device__ __forceinline__ void zero(Acc<T>& acc) {
 // last stage it brings zeros or nothing anyone reads); cp.begin(stage) is called when a stage's
 // copies begin, cp.scales(stage, ..) when its first fragments are read and cp.shift(stage, ..) once the
 // stage before is done (what scales() has read becomes the scales in use: no product waits for the
-// read); cp.stage(stage) begins a stage, cp.slot(s) runs beside its product s (what it does hides behind the matrix pipe).  On entry stage 0 lies in LDS for every wave and the copies of stages
+// read).  In the first C::kSlots stages cp.stage(stage) begins a stage and cp.slot(s) runs beside its
+// product s (what it does hides behind the matrix pipe).  On entry stage 0 lies in LDS for every wave and the copies of stages
 // 1 .. NS - 1 are requested; on return the LDS is free.
 template <class T, class KIND, class C>
 __device__ __forceinline__ void contract(Acc<T>& acc, char* lds, C& cp, int wave, int lane) {
@@ -167,52 +170,121 @@ __device__ __forceinline__ void contract(Acc<T>& acc, char* lds, C& cp, int wave
   for (int t = 0; t < WMB + WNB; ++t) frag(0, lds, 0, t);
   cp.scales(0, sa[1], sb[1]);
   cp.shift(0, sa, sb);
-  int buf = 0;
-  for (int u = 0; u < cp.KT; ++u) {
-    char* st = lds + buf * T::STAGE;
-    const int nbuf = buf + 1 == T::NS ? 0 : buf + 1;
-    const char* nx = lds + nbuf * T::STAGE;
-    cp.stage(u);
-    __builtin_amdgcn_sched_barrier(0);
+  int buf = 0, u = 0;
+  auto run = [&](auto slots, int end) {
+    for (; u < end; ++u) {
+      char* st = lds + buf * T::STAGE;
+      const int nbuf = buf + 1 == T::NS ? 0 : buf + 1;
+      const char* nx = lds + nbuf * T::STAGE;
+      if (slots) cp.stage(u);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int ks = 0; ks < SUB; ++ks) {
-      const int set = SETS == 2 ? ks & 1 : 0, next = SETS == 2 ? set ^ 1 : 0;
-      const bool last = ks == SUB - 1;
-      const char* from = last ? nx : st;
-      const int nks = last ? 0 : ks + 1;
+      for (int ks = 0; ks < SUB; ++ks) {
+        const int set = SETS == 2 ? ks & 1 : 0, next = SETS == 2 ? set ^ 1 : 0;
+        const bool last = ks == SUB - 1;
+        const char* from = last ? nx : st;
+        const int nks = last ? 0 : ks + 1;
 #pragma unroll
-      for (int t = 0; t < NMF; ++t) {
-        if (last && t == BAR) {
-          wait_lgkm0();
-          wait_vmcnt<(T::NS - 2) * T::PER>();  // this wave's copies of stage u + 1
-          barrier_only();
-          cp.begin(u + T::NS);
+        for (int t = 0; t < NMF; ++t) {
+          if (last && t == BAR) {
+            wait_lgkm0();
+            wait_vmcnt<(T::NS - 2) * T::PER>();  // this wave's copies of stage u + 1
+            barrier_only();
+            cp.begin(u + T::NS);
+          }
+          const int i = t % WMB, j = t / WMB;
+          KIND::mma(acc[i][j], fb[set][j], fa[set][i], sb[0], sa[0][i]);
+          if (slots) cp.slot(ks * NMF + t);
+          if constexpr (SETS == 2) {
+#pragma unroll
+            for (int q = 0; q < WMB + WNB; ++q)
+              if (q * NMF / (WMB + WNB) == t) frag(next, from, nks, q);
+          } else {
+            if (i == WMB - 1) frag(0, from, nks, j);
+            if (j == WNB - 1) frag(0, from, nks, WNB + i);
+          }
+          if (last && t >= BAR) {
+            if (t == BAR) cp.scales(u + 1, sa[1], sb[1]);
+#pragma unroll
+            for (int q = 0; q < T::PER; ++q)
+              if (BAR + q * (NMF - BAR) / T::PER == t) cp.one(st, u + T::NS, q);
+          }
+          __builtin_amdgcn_sched_barrier(0);
         }
-        const int i = t % WMB, j = t / WMB;
-        KIND::mma(acc[i][j], fb[set][j], fa[set][i], sb[0], sa[0][i]);
-        cp.slot(ks * NMF + t);
-        if constexpr (SETS == 2) {
-#pragma unroll
-          for (int q = 0; q < WMB + WNB; ++q)
-            if (q * NMF / (WMB + WNB) == t) frag(next, from, nks, q);
-        } else {
-          if (i == WMB - 1) frag(0, from, nks, j);
-          if (j == WNB - 1) frag(0, from, nks, WNB + i);
-        }
-        if (last && t >= BAR) {
-          if (t == BAR) cp.scales(u + 1, sa[1], sb[1]);
-#pragma unroll
-          for (int q = 0; q < T::PER; ++q)
-            if (BAR + q * (NMF - BAR) / T::PER == t) cp.one(st, u + T::NS, q);
-        }
-        __builtin_amdgcn_sched_barrier(0);
       }
+      cp.shift(u + 1, sa, sb);
+      buf = nbuf;
     }
-    cp.shift(u + 1, sa, sb);
-    buf = nbuf;
-  }
+  };
+  if constexpr (C::kSlots > 0) run(std::true_type{}, min(cp.KT, C::kSlots));
+  run(std::false_type{}, cp.KT);
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();  // every copy has ended and every wave is past its reads
+}
+
+// The same for the largest 16-bit tile, two buffers, eight waves of which the first four (one to a
+// SIMD) copy: stage u + 1's A rows beside the first sub-step's products and its W-side rows beside the
+// second's, one copy to a product; one barrier per stage, at its start.  cp counts copies by four
+// waves.  SLOTS: cp.slot() runs beside the products.
+template <class T, class KIND, bool COPY, bool SLOTS, class C>
+__device__ __forceinline__ void stage_two(Acc<T>& acc, char* lds, int u, C& cp, int arow, int brow, int xr, int h) {
+  constexpr int WMB = T::WMB, WNB = T::WNB, NMF = WMB * WNB;
+  static_assert(T::NS == 2 && T::TM == 256 && T::TN == 256 && NMF == 8 && KIND::SUB == 4, "the largest tile");
+  char *st = lds + (u & 1) * T::STAGE, *nx = lds + ((u & 1) ^ 1) * T::STAGE;
+  typename KIND::frag_t fa[2][WMB], fb[2][WNB];
+  // fragment t in the order of first use: b0 a0 b1 a1 a2 a3
+  auto frag = [&](int set, int ks, int t) {
+    if (t == 0 || t == 2) fb[set][t >> 1] = KIND::read(st + brow + (t >> 1) * 32 * 128, ks, h, xr);
+    else fa[set][t == 1 ? 0 : t - 2] = KIND::read(st + arow + (t == 1 ? 0 : t - 2) * 32 * 128, ks, h, xr);
+  };
+#pragma unroll
+  for (int t = 0; t < 6; ++t) frag(0, 0, t);
+  if (COPY) cp.begin(u + 1);
+  if (SLOTS) cp.stage(u);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int ks = 0; ks < 4; ++ks) {
+    const int set = ks & 1;
+#pragma unroll
+    for (int t = 0; t < NMF; ++t) {
+      const int i = t / WNB, j = t % WNB;
+      KIND::mma(acc[i][j], fb[set][j], fa[set][i], 0, 0);
+      if (SLOTS) cp.slot(ks * NMF + t);
+      if (ks < 3) {
+#pragma unroll
+        for (int q = 0; q < 6; ++q)
+          if (q * NMF / 6 == t) frag(set ^ 1, ks + 1, q);
+      }
+      if (COPY && ks < 2) cp.one(nx, u + 1, 8 * ks + t);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+template <class T, class KIND, bool COPY, class C>
+__device__ __forceinline__ void stages_two(Acc<T>& acc, char* lds, C& cp, int arow, int brow, int xr, int h) {
+  int u = 0;
+  if constexpr (C::kSlots > 0)
+    for (; u < min(cp.KT, C::kSlots); ++u) {
+      __builtin_amdgcn_s_waitcnt(0);  // this wave's copies of stage u and its fragment reads
+      barrier_only();
+      stage_two<T, KIND, COPY, true>(acc, lds, u, cp, arow, brow, xr, h);
+    }
+  for (; u < cp.KT; ++u) {
+    __builtin_amdgcn_s_waitcnt(0);
+    barrier_only();
+    stage_two<T, KIND, COPY, false>(acc, lds, u, cp, arow, brow, xr, h);
+  }
+}
+// On entry the copying waves have requested stage 0; on return the LDS is free.
+template <class T, class KIND, class C>
+__device__ __forceinline__ void contract_two(Acc<T>& acc, char* lds, C& cp, int wave, int lane) {
+  const int r32 = lane & 31, h = lane >> 5, xr = swz(r32);
+  const int arow = ((wave / T::NWN) * 32 * T::WMB + r32) * 128;
+  const int brow = (T::TM + (wave % T::NWN) * 32 * T::WNB + r32) * 128;
+  if (wave < 4) stages_two<T, KIND, true>(acc, lds, cp, arow, brow, xr, h);
+  else stages_two<T, KIND, false>(acc, lds, cp, arow, brow, xr, h);
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
 }
 
 // Position of workgroup b among n when each XCD (workgroups b, b + 8, ...) takes a
