@@ -52,7 +52,7 @@ constexpr int cols_of() { return GATED ? T::TN / 2 : T::TN; }
 
 // Waves that copy: four of the largest tile's eight (contract_two), else all.
 template <class T>
-constexpr int copying() { return T::TM == 256 ? 4 : T::NW; }
+constexpr int copying() { return T::TM == 256 && T::NS == 2 ? 4 : T::NW; }
 
 // The copies of a tile's stages by one wave: instruction i of copying wave w fills LDS rows
 // 8 (w + NW i) .. + 7 of the stage; lane l lands in chunk l % 8 of row l / 8 and fetches the
@@ -214,43 +214,49 @@ struct Rows16 {
 };
 
 // h (and pre) of a wave's blocks: lane (r32, h) of block (i, j) holds row 32 i + r32, columns
-// 8 q + 4 h + v in elements 4 q + v; j = 0 is g, j = 1 is u.  coef: the tile's biases, gate then up.
+// 8 q + 4 h + v in elements 4 q + v; an even j is g, the next is u of the same 32 columns.  Its 16 WNB
+// columns of h, g and u pass one after the other through W: rows of whole 128-byte lines where WNB = 4.
+// coef: the tile's biases, gate then up.
 template <int CD, int ACT, class T>
-__device__ __forceinline__ void write_gated(const G16& p, const Place& pl, const Acc<T>& acc, const float* coef, char* W,
+__device__ __forceinline__ void write_gated(const G16& p, const Place& pl, Acc<T>& acc, const float* coef, char* W,
                                             int wave, int lane) {
-  constexpr int C = cols_of<T, true>();
+  constexpr int C = cols_of<T, true>(), PAIRS = T::WNB / 2, RB = 64 * PAIRS;
   const int h = lane >> 5, r32 = lane & 31;
-  const int wm = (wave / T::NWN) * 32 * T::WMB, wc = (wave % T::NWN) * 32;  // the wave's 32 columns
-  const int ncols = (int)max((int64_t)0, min((int64_t)32, p.n - pl.n0 - wc));
+  const int wm = (wave / T::NWN) * 32 * T::WMB, wc = (wave % T::NWN) * 32 * PAIRS;
+  const int ncols = (int)max((int64_t)0, min((int64_t)(32 * PAIRS), p.n - pl.n0 - wc));
 #pragma unroll
   for (int i = 0; i < T::WMB; ++i) {
     const int row0 = wm + 32 * i, left = min(32, pl.rows - row0);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const f32x4_t bg = *(const f32x4_t*)(coef + wc + 8 * q + 4 * h), bu = *(const f32x4_t*)(coef + C + wc + 8 * q + 4 * h);
-      float g[4], u[4], o[4];
+    for (int part = 0; part < 3; ++part) {  // h, g, u
+      if (part && !p.pre) break;
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        g[v] = acc[i][0][4 * q + v] + bg[v];
-        u[v] = acc[i][1][4 * q + v] + bu[v];
-        o[v] = act_of<ACT>(g[v]) * u[v];
-      }
-      const int at = Rows16<64>::at(r32, 16 * q + 8 * h);
-      *(u32x2_t*)(W + at) = u32x2_t{pack2<CD>(o[0], o[1]), pack2<CD>(o[2], o[3])};
-      if (p.pre) {
-        *(u32x2_t*)(W + 2048 + at) = u32x2_t{pack2<CD>(g[0], g[1]), pack2<CD>(g[2], g[3])};
-        *(u32x2_t*)(W + 4096 + at) = u32x2_t{pack2<CD>(u[0], u[1]), pack2<CD>(u[2], u[3])};
-      }
+      for (int j = 0; j < PAIRS; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float o[4];
+          if (part == 0) {
+            const int at = wc + 32 * j + 8 * q + 4 * h;
+            const f32x4_t bg = *(const f32x4_t*)(coef + at), bu = *(const f32x4_t*)(coef + C + at);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              acc[i][2 * j][4 * q + v] += bg[v];
+              acc[i][2 * j + 1][4 * q + v] += bu[v];
+              o[v] = act_of<ACT>(acc[i][2 * j][4 * q + v]) * acc[i][2 * j + 1][4 * q + v];
+            }
+          } else {
+#pragma unroll
+            for (int v = 0; v < 4; ++v) o[v] = acc[i][2 * j + part - 1][4 * q + v];
+          }
+          *(u32x2_t*)(W + Rows16<RB>::at(r32, 64 * j + 16 * q + 8 * h)) = u32x2_t{pack2<CD>(o[0], o[1]), pack2<CD>(o[2], o[3])};
+        }
+      wait_lgkm0();  // the wave reads back only what it wrote
+      asm volatile("" ::: "memory");
+      Rows16<RB>::store(W, part ? p.pre : p.out, part ? 2 * p.n : p.n, pl.m0 + row0, pl.n0 + wc + (part == 2 ? p.n : 0), left,
+                        ncols, lane);
+      wait_lgkm0();  // the reads are done before the next rows overwrite them
+      asm volatile("" ::: "memory");
     }
-    wait_lgkm0();  // the wave reads back only what it wrote
-    asm volatile("" ::: "memory");
-    Rows16<64>::store(W, p.out, p.n, pl.m0 + row0, pl.n0 + wc, left, ncols, lane);
-    if (p.pre) {
-      Rows16<64>::store(W + 2048, p.pre, 2 * p.n, pl.m0 + row0, pl.n0 + wc, left, ncols, lane);
-      Rows16<64>::store(W + 4096, p.pre, 2 * p.n, pl.m0 + row0, p.n + pl.n0 + wc, left, ncols, lane);
-    }
-    wait_lgkm0();  // the reads are done before the next 32 rows overwrite them
-    asm volatile("" ::: "memory");
   }
 }
 
@@ -299,91 +305,115 @@ __device__ __forceinline__ void write_plain(const G16& p, const Place& pl, const
   }
 }
 
+// The tile of half the rows that an incomplete last round takes, two workgroups to a tile.
+template <class T>
+struct HalfOf {
+  using type = T;
+};
+template <int WMB, int WNB, int NWM, int NWN>
+struct HalfOf<Tile<WMB, WNB, NWM, NWN, 2>> {
+  using type = Tile<WMB / 2, WNB, NWM, NWN, 2>;
+};
+
 // A workgroup goes through its tiles.  After a tile's last stage the copies of the next tile's first
 // stage are requested, so that they land while this one's outputs are formed and stored; those pass
-// through what were the other stages.
+// through LDS behind that stage.  A last round of at most half the workgroups runs as tiles of half
+// the rows (the largest tiles).
 template <int CD, class T, bool GATED, int WGS>
 __global__ __launch_bounds__(64 * T::NW, WGS) void k_gemm16(G16 p, int act) {
-  constexpr int C = cols_of<T, GATED>(), COEF = GATED ? 2 * C : 0, STAGING = GATED ? 6144 : 2048 * T::WNB;
-  // masked: the low-rank operands lie in the buffer of stage KM, wherever that is; the staging goes
-  // where they were once every wave has read them
-  static_assert((GATED ? T::LDS - T::STAGE : T::STAGE) >= T::NW * STAGING, "staging fits");
+  using H = typename HalfOf<T>::type;
+  constexpr bool HALVES = !std::is_same_v<T, H>;
+  constexpr int C = cols_of<T, GATED>(), COEF = GATED ? 2 * C : 0, STAGING = GATED ? 1024 * T::WNB : 2048 * T::WNB;
+  static_assert(T::LDS - T::STAGE >= T::NW * STAGING, "staging fits");
   __shared__ __attribute__((aligned(1024))) char lds[T::LDS + 2 * COEF * 4];  // one array: see fp8.hip
   float* coefs = (float*)(lds + T::LDS);  // two sets, used in turn
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int tiles_n = (int)((p.n + C - 1) / C), tiles_m = (int)((p.m + T::TM - 1) / T::TM), total = tiles_m * tiles_n;
   const int G = gridDim.x, b = blockIdx.x;
+  // The workgroup's tile in round r; rows 0: none (any more).
   auto item = [&](int r) {
     Place pl = {0, 0, 0};
     const int64_t base = (int64_t)r * G;
-    const int n = (int)min((int64_t)G, total - base);
-    if (b >= n) return pl;
+    if (base >= total) return pl;
+    const int rem = total - (int)base, n = min(G, rem);
+    const bool cut = HALVES && 2 * rem <= G;
+    if (b >= (cut ? 2 * rem : n)) return pl;
+    const int pos = xcd_run(b, cut ? 2 * rem : n), half = cut ? pos & 1 : 0;
     int tm, tn;
-    grouped_tile((int)base + xcd_run(b, n), tiles_m, tiles_n, tm, tn);
-    pl.m0 = (int64_t)__builtin_amdgcn_readfirstlane(tm) * T::TM;
+    grouped_tile((int)base + (cut ? pos >> 1 : pos), tiles_m, tiles_n, tm, tn);
+    pl.m0 = (int64_t)__builtin_amdgcn_readfirstlane(tm) * T::TM + half * H::TM;
     pl.n0 = (int64_t)__builtin_amdgcn_readfirstlane(tn) * C;
-    pl.rows = (int)min((int64_t)T::TM, p.m - pl.m0);
+    pl.rows = (int)max((int64_t)0, min((int64_t)(cut ? H::TM : T::TM), p.m - pl.m0));
     return pl;
   };
   auto coef_of = [&](const Place& pl, int i) {
     const int64_t col = pl.n0 + (i >= C ? i - C : i);
     return p.bias && col < p.n ? load_cd<CD>(p.bias, col + (i >= C ? p.n : 0)) : 0.f;
   };
-  using Copier = std::conditional_t<GATED, Copies16<T, GATED>, Masked16<T>>;
+  auto first_stage = [&](const Place& pl) {
+    if (HALVES && pl.rows <= H::TM) Copies16<H, GATED>(p, pl, wave, lane).all(lds, 0);
+    else Copies16<T, GATED>(p, pl, wave, lane).all(lds, 0);
+  };
 
   Place cur = item(0);
   if (cur.rows == 0) return;
   if (GATED)
     for (int i = tid; i < COEF; i += 64 * T::NW) coefs[i] = coef_of(cur, i);
-  Copies16<T, GATED>(p, cur, wave, lane).all(lds, 0);
-  constexpr bool TWO = copying<T>() < T::NW;
-  if (!TWO) wait_vmcnt<0>();
+  first_stage(cur);
   int set = 0;
   for (int r = 1;; ++r) {
     const Place nxt = item(r);
     static_assert(COEF <= 64 * T::NW, "one coefficient to a thread");
     const float c = GATED && nxt.rows && tid < COEF ? coef_of(nxt, tid) : 0.f;
-    wait_lgkm0();
-    barrier_only();  // stage 0 and the coefficients are there, the staging of the tile before is free
-    Copier cp(p, cur, wave, lane);
-    Acc<T> acc;
-    zero<T>(acc);
-    if constexpr (TWO) {
-      contract_two<T, Half16<CD>>(acc, lds, cp, wave, lane);
-    } else {
+    auto work = [&](auto shape) {
+      using U = decltype(shape);
+      using Copier = std::conditional_t<GATED, Copies16<U, GATED>, Masked16<U>>;
+      Copier cp(p, cur, wave, lane);
+      Acc<U> acc;
+      zero<U>(acc);
+      if constexpr (copying<U>() < U::NW) {
+        wait_lgkm0();
+        barrier_only();  // the coefficients are there, the staging of the tile before is free
+        contract_two<U, Half16<CD>>(acc, lds, cp, wave, lane);
+      } else {
+        wait_vmcnt<0>();
+        wait_lgkm0();
+        barrier_only();  // and stage 0
 #pragma unroll
-      for (int s = 1; s < T::NS; ++s) cp.all(lds + s * T::STAGE, s);
-      contract<T, Half16<CD>>(acc, lds, cp, wave, lane);
-    }
-    if constexpr (!GATED) {
-      cp.rest();
-      const int at = cp.KM % T::NS;
-      add_masked<CD, T>(acc, cp, lds + at * T::STAGE, wave, lane);
-      __syncthreads();  // every wave is past the low-rank operands
-    }
-    if (nxt.rows) {
-      if (GATED && tid < COEF) coefs[(set ^ 1) * COEF + tid] = c;
-      Copies16<T, GATED>(p, nxt, wave, lane).all(lds, 0);
-    }
-    char* W = lds + T::STAGE + wave * STAGING;
-    constexpr int STORES = GATED ? T::WMB * 2 : T::WMB * 2 * T::WNB;
-    if constexpr (GATED) {
-      const float* co = coefs + set * COEF;
-      if (act == QLORA_ACT_SILU) write_gated<CD, QLORA_ACT_SILU, T>(p, cur, acc, co, W, wave, lane);
-      else if (act == QLORA_ACT_GELU) write_gated<CD, QLORA_ACT_GELU, T>(p, cur, acc, co, W, wave, lane);
-      else write_gated<CD, QLORA_ACT_GELU_TANH, T>(p, cur, acc, co, W, wave, lane);
-    } else {
-      write_plain<CD, T>(p, cur, acc, W, wave, lane);
-    }
+        for (int s = 1; s < U::NS; ++s) cp.all(lds + s * U::STAGE, s);
+        contract<U, Half16<CD>>(acc, lds, cp, wave, lane);
+      }
+      if constexpr (!GATED) {
+        cp.rest();
+        add_masked<CD, U>(acc, cp, lds + cp.KM % U::NS * U::STAGE, wave, lane);
+        __syncthreads();  // every wave is past the low-rank operands
+      }
+      if (nxt.rows) {
+        if (GATED && tid < COEF) coefs[(set ^ 1) * COEF + tid] = c;
+        first_stage(nxt);
+      }
+      char* W = lds + T::STAGE + wave * STAGING;
+      if constexpr (GATED) {
+        const float* co = coefs + set * COEF;
+        if (act == QLORA_ACT_SILU) write_gated<CD, QLORA_ACT_SILU, U>(p, cur, acc, co, W, wave, lane);
+        else if (act == QLORA_ACT_GELU) write_gated<CD, QLORA_ACT_GELU, U>(p, cur, acc, co, W, wave, lane);
+        else write_gated<CD, QLORA_ACT_GELU_TANH, U>(p, cur, acc, co, W, wave, lane);
+      } else {
+        write_plain<CD, U>(p, cur, acc, W, wave, lane);
+      }
+    };
+    if (HALVES && cur.rows <= H::TM) work(H{});
+    else work(T{});
     if (nxt.rows == 0) return;
-    asm volatile("" ::: "memory");
-    if (!TWO) wait_vmcnt<STORES>();  // this wave's copies of the next first stage, older than the stores, have landed
     cur = nxt;
     set ^= 1;
   }
 }
 
-using Full = Tile<4, 2, 2, 4, 2>;  // 256 rows x 256 columns (128 of each projection), eight waves
+// 256 rows x 256 columns (128 of each projection), eight waves; a gated wave takes 64 rows of 64
+// columns of h, whole lines of the outputs, a masked one 128 rows, whose mask bits fill four words
+using FullGated = Tile<2, 4, 4, 2, 2>;
+using FullMasked = Tile<4, 2, 2, 4, 2>;
 using Wide = Tile<2, 2, 2, 4, 3>;  // 128 x 256, eight waves
 using Mid = Tile<2, 2, 2, 2, 4>;   // 128 x 128, four waves
 using Low = Tile<1, 2, 2, 2, 3>;   // 64 x 128, four waves; two workgroups fit a compute unit
@@ -406,7 +436,7 @@ int run_cd(const G16& p, int act, int kind, hipStream_t s) {
     if (one_round(64, 128)) return run<CD, Low, GATED, 2>(p, act, kind, s);
   if (one_round(128, 128)) return run<CD, Mid, GATED, 1>(p, act, kind, s);
   if (one_round(128, 256)) return run<CD, Wide, GATED, 1>(p, act, kind, s);
-  return run<CD, Full, GATED, 1>(p, act, kind, s);
+  return run<CD, std::conditional_t<GATED, FullGated, FullMasked>, GATED, 1>(p, act, kind, s);
 }
 
 }  // namespace

@@ -232,10 +232,11 @@ __device__ __forceinline__ void stage_two(Acc<T>& acc, char* lds, int u, C& cp, 
   static_assert(T::NS == 2 && T::TM == 256 && T::TN == 256 && NMF == 8 && KIND::SUB == 4, "the largest tile");
   char *st = lds + (u & 1) * T::STAGE, *nx = lds + ((u & 1) ^ 1) * T::STAGE;
   typename KIND::frag_t fa[2][WMB], fb[2][WNB];
-  // fragment t in the order of first use: b0 a0 b1 a1 a2 a3
+  // fragment t in the order of first use: b0 a0, the other b's, the other a's
   auto frag = [&](int set, int ks, int t) {
-    if (t == 0 || t == 2) fb[set][t >> 1] = KIND::read(st + brow + (t >> 1) * 32 * 128, ks, h, xr);
-    else fa[set][t == 1 ? 0 : t - 2] = KIND::read(st + arow + (t == 1 ? 0 : t - 2) * 32 * 128, ks, h, xr);
+    const int b = t == 0 ? 0 : t >= 2 && t <= WNB ? t - 1 : -1, a = t == 1 ? 0 : t - WNB;
+    if (b >= 0) fb[set][b] = KIND::read(st + brow + b * 32 * 128, ks, h, xr);
+    else fa[set][a] = KIND::read(st + arow + a * 32 * 128, ks, h, xr);
   };
 #pragma unroll
   for (int t = 0; t < 6; ++t) frag(0, 0, t);
