@@ -100,18 +100,11 @@ int gate_cd(int act, const void* pre, const void* dh, int64_t n, int64_t total, 
   if (act == QLORA_ACT_GELU) return gate_t<CD, QLORA_ACT_GELU>(pre, dh, n, total, out, s);
   return gate_t<CD, QLORA_ACT_GELU_TANH>(pre, dh, n, total, out, s);
 }
-// dh null: out = h [m][n]; else out = dpre [m][2 n].
-int gate(int cd, int act, const void* pre, const void* dh, int64_t m, int64_t n, void* out, hipStream_t s) {
-  if (cd == CD_BF16) return gate_cd<CD_BF16>(act, pre, dh, n, m * n, out, s);
-  if (cd == CD_F16) return gate_cd<CD_F16>(act, pre, dh, n, m * n, out, s);
-  return gate_cd<CD_F32>(act, pre, dh, n, m * n, out, s);
-}
-
 // How a forward runs, and its workspace.
 //   DECODE   up to 64 tokens on the split-K GEMV: both projections' partial sums, one epilogue
 //   TILED    W~ of both in the workspace, T = s x A^T by the rank-product kernels, then the gated GEMM
-//   GROUP    every other layout and fp32: the group call gives [g | u], then k_gate
-enum Way { DECODE, TILED, GROUP };
+//   PLANES   every other layout and fp32
+enum Way { DECODE, TILED, PLANES };
 struct FwdPlan {
   Way way;
   int64_t wd, t, bpad[2], part[2], total;
@@ -136,8 +129,8 @@ FwdPlan plan_fwd(const GroupCall& gc) {
     }
     P.total = o;
   } else {
-    P.way = GROUP;
-    P.total = al(m * gc.N * es) + (int64_t)group_workspace_bytes(QLORA_OP_FWD, gc);
+    P.way = PLANES;
+    P.total = planes_workspace(QLORA_OP_FWD, gc.c, 2, false);
   }
   return P;
 }
@@ -150,6 +143,13 @@ __global__ __launch_bounds__(kThreads) void k_pad_rows(const uint16_t* __restric
     const int c = (int)(i - row * ld);
     dst[i] = c < r ? src[row * r + c] : (uint16_t)0;
   }
+}
+
+// Whether the group call's tuned kernels take a backward.
+bool tuned_bwd(const GroupCall& gc) {
+  const LayerCall &c0 = gc.c[0], &c1 = gc.c[1];
+  return c0.cd != CD_F32 && c0.w.rows % 64 == 0 && fast_layout(c0.w) && fast_layout(c1.w) && skinny_ok(c0.cd, c0.r) &&
+         skinny_ok(c1.cd, c1.r);
 }
 
 int forward_tiled(const GroupCall& gc, const FwdPlan& P, int act, const void* bias, void* h, void* pre,
@@ -206,8 +206,16 @@ int forward_tiled(const GroupCall& gc, const FwdPlan& P, int act, const void* bi
 
 }  // namespace
 
+// dh null: out = h [m][n]; else out = dpre [m][2 n].
+int gate(int cd, int act, const void* pre, const void* dh, int64_t m, int64_t n, void* out, hipStream_t s) {
+  if (cd == CD_BF16) return gate_cd<CD_BF16>(act, pre, dh, n, m * n, out, s);
+  if (cd == CD_F16) return gate_cd<CD_F16>(act, pre, dh, n, m * n, out, s);
+  return gate_cd<CD_F32>(act, pre, dh, n, m * n, out, s);
+}
+
 size_t gated_workspace_bytes(int op, const GroupCall& gc) {
   if (op == QLORA_OP_FWD) return (size_t)plan_fwd(gc).total;
+  if (!tuned_bwd(gc)) return (size_t)planes_workspace(op, gc.c, 2, false);
   return (size_t)al(gc.c[0].m * gc.N * cd_bytes(gc.c[0].cd)) + group_workspace_bytes(op, gc);  // [dg | du] first
 }
 
@@ -224,14 +232,17 @@ int launch_gated_fwd(const GroupCall& gc, int act, const void* bias, void* h, vo
     return gemv_gated(pair, act, h, pre, t_save);
   }
   if (P.way == TILED) return forward_tiled(gc, P, act, bias, h, pre, t_save, (char*)ws, s);
-  void* z = pre ? pre : ws;
-  const int rc = launch_forward_group(gc, bias, z, t_save, (char*)ws + al(c.m * gc.N * cd_bytes(c.cd)), s);
-  return rc ? rc : gate(c.cd, act, z, nullptr, c.m, c.w.rows, h, s);
+  const PlanesFwd q = {gc.c, 2, nullptr, act, bias, h, pre, t_save};
+  return planes_forward(q, ws, nullptr);
 }
 
 int launch_gated_bwd(const GroupCall& gc, int act, const void* dh, const void* pre, const float* const* t_saved, void* dx,
                      void* const* d_a, void* const* d_b, int gd, void* ws, hipStream_t s) {
   const LayerCall& c = gc.c[0];
+  if (!tuned_bwd(gc)) {
+    const PlanesBwd q = {gc.c, 2, nullptr, act, dh, pre, t_saved, dx, d_a, d_b, gd};
+    return planes_backward(q, ws, nullptr);
+  }
   const int rc = gate(c.cd, act, pre, dh, c.m, c.w.rows, ws, s);
   return rc ? rc : launch_backward_group_as(gc, ws, t_saved, dx, d_a, d_b, gd,
                                             (char*)ws + al(c.m * gc.N * cd_bytes(c.cd)), s);

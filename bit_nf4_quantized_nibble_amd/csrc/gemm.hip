@@ -953,18 +953,39 @@ inline bool gemv_candidate(int64_t m, int32_t flags) {
   return m <= kGemvMaxM || (m <= kGemvMfmaMaxM && !(flags & (QLORA_FLAG_FUSED | QLORA_FLAG_DEQUANT_GEMM)));
 }
 
+// Whether a seeded call is none of the tuned kernels'.
+bool planes_seeded(int op, const LayerCall& c) {
+  const bool tuned = c.cd != CD_F32 && fast_layout(c.w) && (op == QLORA_OP_FWD || c.w.rows % 64 == 0) && skinny_ok(c.cd, c.r);
+  return !tuned && !(c.flags & (QLORA_FLAG_FUSED | QLORA_FLAG_DEQUANT_GEMM));
+}
+// What it may need: a query does not know the block size.
+int64_t planes_seeded_bytes(int op, int64_t m, int64_t rows, int64_t cols, int32_t r, int cd, int32_t flags) {
+  if (!(flags & QLORA_FLAG_DROPOUT)) return 0;
+  LayerCall c = {};
+  c.m = m;
+  c.w.rows = rows;
+  c.w.cols = cols;
+  c.r = r;
+  c.cd = cd;
+  c.flags = flags;
+  c.w.bs = 2;  // not the tuned kernels'
+  return planes_seeded(op, c) ? planes_workspace(op, &c, 1, true) : 0;
+}
+
 size_t fwd_workspace_bytes(int64_t m, int64_t rows, int64_t cols, int32_t r, int cd, int32_t flags) {
   // A GEMV candidate may still run on the GEMM path (a layout the GEMV does not take:
   // the query does not see the block size): room for both.  At most 16 tokens the
   // GEMM path is the generic engine, which needs only T and the rank-product partial
   // sums (the start of its plan).
   const FwdPlan P = plan_fwd(m, rows, cols, r, cd, flags);
-  if (!gemv_candidate(m, flags)) return (size_t)P.total;
+  if (!gemv_candidate(m, flags))
+    return (size_t)std::max(P.total, planes_seeded_bytes(QLORA_OP_FWD, m, rows, cols, r, cd, flags));
   return std::max(gemv_workspace_bytes(m, rows, cols, r, cd), (size_t)(m <= kGemvMaxM ? P.off_wd : P.total));
 }
 
 size_t bwd_workspace_bytes(int64_t m, int64_t rows, int64_t cols, int32_t r, int cd, int32_t flags) {
-  return (size_t)plan_bwd(m, rows, cols, r, cd, flags).total;
+  return (size_t)std::max(plan_bwd(m, rows, cols, r, cd, flags).total,
+                          planes_seeded_bytes(QLORA_OP_BWD, m, rows, cols, r, cd, flags));
 }
 
 bool gemv_route(const LayerCall& c) {
@@ -984,6 +1005,10 @@ int launch_forward(const LayerCall& c, void* y, float* t_save) {
 // The forward with seeded dropout: as with a stored mask, never the decode GEMV (c.flags holds
 // QLORA_FLAG_DROPOUT).
 int launch_forward_seeded(const LayerCall& c, const Seeded& sd, void* y, float* t_save) {
+  if (planes_seeded(QLORA_OP_FWD, c)) {
+    const PlanesFwd q = {&c, 1, &sd, 0, c.bias, y, nullptr, t_save ? &t_save : nullptr};
+    return planes_forward(q, c.ws, nullptr);
+  }
   switch (c.cd) {
     case CD_BF16: return forward_gemm<CD_BF16>(c, &sd, y, t_save);
     case CD_F16: return forward_gemm<CD_F16>(c, &sd, y, t_save);
@@ -999,6 +1024,10 @@ int launch_backward(const LayerCall& c, const void* dy, const float* t_saved, vo
 
 int launch_backward_as(const LayerCall& c, const Seeded* sd, const void* dy, const float* t_saved, void* dx, void* d_a,
                        void* d_b, int gd) {
+  if (sd && planes_seeded(QLORA_OP_BWD, c)) {
+    const PlanesBwd q = {&c, 1, sd, 0, dy, nullptr, t_saved ? &t_saved : nullptr, dx, &d_a, &d_b, gd};
+    return planes_backward(q, c.ws, nullptr);
+  }
   switch (c.cd) {
     case CD_BF16: return backward_gemm<CD_BF16>(c, sd, dy, t_saved, dx, d_a, d_b, gd);
     case CD_F16: return backward_gemm<CD_F16>(c, sd, dy, t_saved, dx, d_a, d_b, gd);

@@ -49,6 +49,38 @@ int gemm16_gated(int cd, const void* x, int64_t m, int64_t n, int64_t K, const v
 int gemm16_masked_dx(int cd, const void* dy, int64_t m, int64_t n, int64_t K, const void* wt, const void* dt, int64_t ldt,
                      const void* at, int64_t lda, const Seeded& sd, void* dx, hipStream_t s);
 
+// planes.hip: the seeded layer (g = 1) and the gated block (g = 2) in every layout and type.
+struct PlanesFwd {
+  const LayerCall* c;
+  int g;
+  const Seeded* sd;  // g = 1
+  int act;           // g = 2
+  const void* bias;  // [g rows] or null
+  void* out;         // y, or h
+  void* pre;
+  float* const* t_save;
+};
+struct PlanesBwd {
+  const LayerCall* c;
+  int g;
+  const Seeded* sd;  // g = 1
+  int act;           // g = 2
+  const void* dy;    // dY, or dh
+  const void* pre;
+  const float* const* t_saved;
+  void* dx;
+  void* const* d_a;
+  void* const* d_b;
+  int gd;
+};
+// need not null: only the workspace's size is wanted (pointers are not read).
+int planes_forward(const PlanesFwd& q, void* ws, int64_t* need);
+int planes_backward(const PlanesBwd& q, void* ws, int64_t* need);
+// The most that such a call needs, whatever its block size and whichever of its outputs are wanted.
+int64_t planes_workspace(int op, const LayerCall* c, int g, bool seeded);
+// gated.hip: h [m][n] from pre (dh null), or [dg | du] from pre and dh
+int gate(int cd, int act, const void* pre, const void* dh, int64_t m, int64_t n, void* out, hipStream_t s);
+
 size_t gated_workspace_bytes(int op, const GroupCall& gc);
 int launch_gated_fwd(const GroupCall& gc, int act, const void* bias, void* h, void* pre, float* const* t_save, void* ws,
                      hipStream_t s);

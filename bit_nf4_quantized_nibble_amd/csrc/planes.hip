@@ -1,0 +1,968 @@
+// planes.hip -- the layer with seeded dropout and the gated block, forward and backward, for every
+// layout and type that the tuned kernels do not take (gfx950): any even block size, rows and columns
+// that fill no tile, blocks that run across rows, fp32.
+//
+// Every product is brought to one form, C[i, j] = sum_k a[i, k] b[j, k] of 16-bit operands with k
+// contiguous, rows of whole stages of 64 elements (zeros behind the last), 16-byte aligned:
+//
+//   pack     one launch writes every operand of a call that is not of that form already: padded copies
+//            and transposes of x, dY, A, B, W~ from its codes, x under the drawn mask, dg and du from
+//            the saved g and u
+//   product  one launch per level of dependence runs all products of that level, each cut into slices
+//            of its contraction where its tiles alone would leave compute units idle
+//   join     one launch adds the slices in their order and forms what leaves: outputs (bias, gate, mask
+//            of the low-rank part), or the rank operands T and dT of the next level
+//
+// An fp32 operand is three planes of bf16 whose sum it is (24 bits in three times 8): six of the
+// nine products of planes, those above 2^-22 of the largest, give the sum to fp32's accuracy at
+// a sixth of the bf16 rate, which is still above the rate of the fp32 matrix instruction.  The rank
+// operands are sums themselves and are kept in two planes (16 or more bits) of a 16-bit type.
+#include <algorithm>
+
+#include "act.h"
+#include "mlp.h"
+#include "tile.h"
+
+namespace qnf4 {
+namespace {
+
+using namespace tile;
+
+constexpr int kThreads = 256;
+
+// ------------------------------------------------------------------------ planes
+// v as the sum of `planes` 16-bit values of type KD, each the rounded rest of those before it.
+template <int KD>
+__device__ __forceinline__ void split(float v, int planes, uint16_t (&o)[3]) {
+  o[0] = to_cd16<KD>(v);
+  if (planes == 1) return;
+  float h = from_cd16<KD>(o[0]);
+  if (KD == CD_BF16 && fabsf(h) == INFINITY && fabsf(v) < INFINITY) {  // rounded past the largest value
+    o[0] = (o[0] & 0x8000u) | 0x7f7fu;
+    h = from_cd16<KD>(o[0]);
+  }
+  float rest = fabsf(h) < INFINITY ? v - h : 0.f;
+  o[1] = to_cd16<KD>(rest);
+  if (planes > 2) o[2] = to_cd16<KD>(rest - from_cd16<KD>(o[1]));
+}
+
+// Where a matrix's planes lie: element (i, k) of plane q at p[i ld + q step + k].
+struct Planes {
+  uint16_t* p = nullptr;
+  int64_t ld = 0, step = 0;
+  int n = 1;  // planes
+};
+
+// -------------------------------------------------------------------------- pack
+enum Source { SRC_CD, SRC_F32, SRC_NF4, SRC_GATE, SRC_UP };
+struct Pack {
+  int src = SRC_CD, w = 0;  // w: which weight (SRC_NF4)
+  const void* p = nullptr;
+  const void* dh = nullptr;  // SRC_GATE, SRC_UP: p is pre [rows][2 cols], dh [rows][cols]
+  int64_t rows = 0, cols = 0;
+  bool drawn = false;  // under the drawn mask
+  Planes rowwise;      // [rows][wide]
+  int64_t wide = 0;
+  Planes across;       // [cols][tall], the transpose
+  int64_t tall = 0;
+  uint32_t tiles_x = 0, end = 0;  // workgroups before `end` are this job's or an earlier one's
+};
+constexpr int kPacks = 14;
+struct Packs {
+  Pack j[kPacks];
+  Nf4W w[2];
+  float lv[16];
+  Seeded sd;
+  int n, act;
+};
+
+// Eight consecutive elements (k0 .. k0 + 7, k0 a multiple of 8) of row i, zeros outside.
+template <int CD>
+__device__ __forceinline__ void fetch_linear(const void* p, int64_t at, int left, float (&v)[8]) {
+  if constexpr (CD == CD_F32) {
+    if (left >= 8 && (at & 3) == 0) {
+#pragma unroll
+      for (int d = 0; d < 2; ++d) {
+        const f32x4_t t = *(const f32x4_t*)((const float*)p + at + 4 * d);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[4 * d + e] = t[e];
+      }
+      return;
+    }
+  } else if (left >= 8 && (at & 7) == 0) {
+    const u32x4_t t = *(const u32x4_t*)((const uint16_t*)p + at);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = from_cd16<CD>((uint16_t)(t[e >> 1] >> (16 * (e & 1))));
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = e < left ? load_cd<CD>(p, at + e) : 0.f;
+}
+template <int CD>
+__device__ __forceinline__ void fetch_nf4(const Nf4W& w, const float* lv, int64_t at, int left, float (&v)[8]) {
+  uint32_t codes;  // nibble e: element at + e
+  if ((at & 7) == 0 && left >= 8) {
+    const uint32_t c = *(const uint32_t*)(w.codes + (at >> 1));
+    codes = (c >> 4 & 0x0f0f0f0fu) | (c << 4 & 0xf0f0f0f0u);  // the element in the high half of a byte comes first
+  } else {
+    codes = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t byte = w.codes[(at + min(e, left - 1)) >> 1];
+      codes |= ((at + e) & 1 ? byte & 15u : byte >> 4) << (4 * e);
+    }
+  }
+  const int64_t b0 = block_of(w, at);
+  if (w.bs >= 8) {  // at most two blocks
+    const int n = min(8, left), cut = (int)min((int64_t)8, (b0 + 1) * w.bs - at);
+    const float s0 = block_scale(w, b0), s1 = cut < n ? block_scale(w, b0 + 1) : 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = e < left ? fl32_mul(lv[codes >> (4 * e) & 15u], e < cut ? s0 : s1) : 0.f;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      v[e] = e < left ? fl32_mul(lv[codes >> (4 * e) & 15u], block_scale(w, block_of(w, at + e))) : 0.f;
+  }
+  if constexpr (CD != CD_F32) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = from_cd16<CD>(to_cd16<CD>(v[e]));
+  }
+}
+
+// A workgroup takes 64 x 64 elements of a job; a thread takes eight columns of two rows.
+template <int CD>
+__global__ __launch_bounds__(kThreads) void k_pack(Packs ps) {
+  constexpr int KD = CD == CD_F32 ? CD_BF16 : CD, LD = 72;  // LDS rows of 64 elements and a pad of 16 bytes
+  __shared__ __attribute__((aligned(16))) uint16_t tile[3][64 * LD];
+  __shared__ float lv[16];
+  const int tid = threadIdx.x;
+  int job = 0;
+  while (blockIdx.x >= ps.j[job].end) ++job;
+  const Pack& j = ps.j[job];
+  const uint32_t b = blockIdx.x - (job ? ps.j[job - 1].end : 0);
+  const int64_t i0 = (int64_t)(b / j.tiles_x) * 64, k0 = (int64_t)(b % j.tiles_x) * 64;
+  if (tid < 16) lv[tid] = ps.lv[tid];
+  __syncthreads();
+  const int c = tid & 7;
+  const int64_t k = k0 + 8 * c;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int r = (tid >> 3) + 32 * half;
+    const int64_t i = i0 + r;
+    const int left = (int)min((int64_t)8, j.cols - k);
+    float v[8];
+    if (i < j.rows && left > 0) {
+      if (j.src == SRC_CD) fetch_linear<CD>(j.p, i * j.cols + k, left, v);
+      else if (j.src == SRC_F32) fetch_linear<CD_F32>(j.p, i * j.cols + k, left, v);
+      else if (j.src == SRC_NF4) fetch_nf4<CD>(ps.w[j.w], lv, i * j.cols + k, left, v);
+      else {
+        float g[8], u[8];
+        fetch_linear<CD>(j.p, 2 * i * j.cols + k, left, g);
+        fetch_linear<CD>(j.p, (2 * i + 1) * j.cols + k, left, u);
+        fetch_linear<CD>(j.dh, i * j.cols + k, left, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float value, slope;
+          if (ps.act == QLORA_ACT_SILU) act_grad<QLORA_ACT_SILU>(g[e], value, slope);
+          else if (ps.act == QLORA_ACT_GELU) act_grad<QLORA_ACT_GELU>(g[e], value, slope);
+          else act_grad<QLORA_ACT_GELU_TANH>(g[e], value, slope);
+          v[e] = e < left ? v[e] * (j.src == SRC_GATE ? u[e] * slope : value) : 0.f;
+        }
+      }
+      if (j.drawn) {
+        const u32x4_t w = philox(philox_key(ps.sd), (uint32_t)(k >> 3), (uint32_t)i);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = keeps(w, e, ps.sd.threshold) ? v[e] : 0.f;
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 0.f;
+    }
+    const int planes = max(j.rowwise.n, j.across.n);
+    u32x4_t o[3];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      uint16_t h[3];
+      split<KD>(v[e], planes, h);
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        if (q >= planes) break;
+        o[q][e >> 1] = e & 1 ? o[q][e >> 1] | (uint32_t)h[q] << 16 : h[q];
+        if (j.across.p) tile[q][(8 * c + e) * LD + r] = h[q];
+      }
+    }
+    if (j.rowwise.p && i < j.rows && k < j.wide) {
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+        if (q < j.rowwise.n) *(u32x4_t*)(j.rowwise.p + i * j.rowwise.ld + q * j.rowwise.step + k) = o[q];
+    }
+  }
+  if (!j.across.p) return;
+  __syncthreads();
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    const int r = (tid >> 3) + 32 * half;
+    if (k0 + r < j.cols && i0 + 8 * c < j.tall) {
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+        if (q < j.across.n)
+          *(u32x4_t*)(j.across.p + (k0 + r) * j.across.ld + q * j.across.step + i0 + 8 * c) =
+              *(const u32x4_t*)&tile[q][r * LD + 8 * c];
+    }
+  }
+}
+
+// ----------------------------------------------------------------------- product
+// One stretch of a contraction: planes of a against planes of b, `seq` the pairs of planes (four bits
+// each: plane of a, plane of b << 2) that every 64 elements go through.
+struct Seg {
+  const uint16_t *a, *b;
+  int64_t lda, ldb;
+  int32_t stepa, stepb, pairs, KM;
+  uint32_t seq;
+};
+constexpr int kSegs = 4;
+struct Prod {
+  Seg s[kSegs];
+  int64_t m, n;
+  float* part;        // [S][m][ldp] fp32, or null:
+  void* out;          // [m][ldo] in the call's type
+  int64_t ldp, ldo;
+  const void* bias;   // with out
+  int32_t nseg, steps, per, S, tiles_m, tiles_n;  // steps in all, and per slice
+  uint32_t end;       // workgroups before it are this product's or an earlier one's
+};
+constexpr int kProds = 6;
+struct Prods {
+  Prod p[kProds];
+};
+
+template <class T>
+struct CopiesP {
+  static constexpr int NW = T::NW, kSlots = 0;
+  const Prod& p;
+  int KT, left, g, k, q, lane;
+  int64_t m0, n0, rows, cols;
+  int arow, chunk;
+  rsrc_t ra, rb;
+  uint32_t oa, ob, sa, sb, soa, sob;
+  int wave;
+  __device__ __forceinline__ CopiesP(const Prod& p_, int64_t m0_, int64_t n0_, int first, int count, int wave_, int lane_)
+      : p(p_), KT(count), left(count), lane(lane_), m0(m0_), n0(n0_), wave(wave_) {
+    rows = min((int64_t)T::TM, p.m - m0);
+    cols = min((int64_t)T::TN, p.n - n0);
+    arow = 8 * wave + (lane >> 3);
+    chunk = (lane & 7) ^ swz(arow);
+    g = 0;
+    while (g + 1 < p.nseg && first >= p.s[g].pairs * p.s[g].KM) first -= p.s[g].pairs * p.s[g].KM, ++g;
+    k = first / p.s[g].pairs;
+    q = first - k * p.s[g].pairs;
+    enter();
+  }
+  __device__ __forceinline__ void enter() {
+    const Seg& e = p.s[g];
+    ra = make_rsrc(e.a + m0 * e.lda, rows * e.lda * 2);
+    rb = make_rsrc(e.b + n0 * e.ldb, cols * e.ldb * 2);
+    oa = (uint32_t)(arow * (int)e.lda * 2 + 16 * chunk);
+    ob = (uint32_t)(arow * (int)e.ldb * 2 + 16 * chunk);
+    sa = (uint32_t)(8 * NW * (int)e.lda * 2);
+    sb = (uint32_t)(8 * NW * (int)e.ldb * 2);
+  }
+  // the stages come in order
+  __device__ __forceinline__ void begin(int) {
+    if (left <= 0) {
+      ra = rb = make_rsrc(p.s[0].a, 0);
+      return;
+    }
+    const Seg& e = p.s[g];
+    const uint32_t pair = e.seq >> (4 * q);
+    soa = (uint32_t)(((pair & 3u) * (uint32_t)e.stepa + 64u * (uint32_t)k) * 2u);
+    sob = (uint32_t)((((pair >> 2) & 3u) * (uint32_t)e.stepb + 64u * (uint32_t)k) * 2u);
+  }
+  __device__ __forceinline__ void next() {
+    if (--left <= 0) return;
+    if (++q == p.s[g].pairs) {
+      q = 0;
+      if (++k == p.s[g].KM) {
+        k = 0;
+        ++g;
+        enter();
+      }
+    }
+  }
+  __device__ __forceinline__ void one(char* dst, int, int i) {
+    char* d = dst + (wave + NW * i) * 1024;
+    if (i < T::PER_A) copy16(ra, d, oa + i * sa, soa);
+    else copy16(rb, d, ob + (i - T::PER_A) * sb, sob);
+    if (i == T::PER - 1) next();
+  }
+  __device__ __forceinline__ void all(char* dst) {
+    begin(0);
+#pragma unroll
+    for (int i = 0; i < T::PER; ++i) one(dst, 0, i);
+  }
+  __device__ __forceinline__ void scales(int, int (&)[T::WMB], int&) const {}
+  __device__ __forceinline__ void shift(int, int (&)[2][T::WMB], int (&)[2]) const {}
+  __device__ __forceinline__ void stage(int) const {}
+  __device__ __forceinline__ void slot(int) const {}
+};
+
+// A workgroup forms one tile of one slice of one product.
+template <int CD, class T>
+__global__ __launch_bounds__(64 * T::NW) void k_product(Prods ps) {
+  constexpr int KD = CD == CD_F32 ? CD_BF16 : CD;
+  __shared__ __attribute__((aligned(1024))) char lds[T::LDS];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int job = 0;
+  while (blockIdx.x >= ps.p[job].end) ++job;
+  const Prod& p = ps.p[job];
+  const uint32_t first = job ? ps.p[job - 1].end : 0;
+  const int tiles = p.tiles_m * p.tiles_n, b = (int)(blockIdx.x - first);
+  int z = 0, t;
+  int tm, tn;
+  if (p.S == 1) {
+    t = xcd_run(b, tiles);
+  } else {
+    z = b / tiles;
+    t = b - z * tiles;
+  }
+  grouped_tile(t, p.tiles_m, p.tiles_n, tm, tn);
+  const int64_t m0 = (int64_t)__builtin_amdgcn_readfirstlane(tm) * T::TM;
+  const int64_t n0 = (int64_t)__builtin_amdgcn_readfirstlane(tn) * T::TN;
+  z = __builtin_amdgcn_readfirstlane(z);
+  CopiesP<T> cp(p, m0, n0, z * p.per, min(p.per, p.steps - z * p.per), wave, lane);
+  Acc<T> acc;
+  zero<T>(acc);
+#pragma unroll
+  for (int s = 0; s < T::NS; ++s) cp.all(lds + s * T::STAGE);
+  wait_vmcnt<(T::NS - 1) * T::PER>();
+  wait_lgkm0();
+  barrier_only();
+  contract<T, Half16<KD>>(acc, lds, cp, wave, lane);
+
+  const int h = lane >> 5, r32 = lane & 31;
+  const int64_t row0 = m0 + (wave / T::NWN) * 32 * T::WMB + r32, col0 = n0 + (wave % T::NWN) * 32 * T::WNB + 4 * h;
+  float* part = p.part ? p.part + (int64_t)z * p.m * p.ldp : nullptr;
+#pragma unroll
+  for (int i = 0; i < T::WMB; ++i) {
+    const int64_t row = row0 + 32 * i;
+    if (row >= p.m) continue;
+#pragma unroll
+    for (int j = 0; j < T::WNB; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int64_t col = col0 + 32 * j + 8 * q;
+        if (col >= p.n) continue;
+        f32x4_t v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        if (part) {
+          *(f32x4_t*)(part + row * p.ldp + col) = v;  // ldp is a multiple of four
+          continue;
+        }
+        const bool whole = col + 4 <= p.n;
+        if (p.bias) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] += whole || col + e < p.n ? load_cd<CD>(p.bias, col + e) : 0.f;
+        }
+        const int64_t at = row * p.ldo + col;
+        if (whole && CD == CD_F32 && (at & 3) == 0) *(f32x4_t*)((float*)p.out + at) = v;
+        else if (whole && CD != CD_F32 && (at & 3) == 0)
+          *(u32x2_t*)((uint16_t*)p.out + at) = u32x2_t{pack2<KD>(v[0], v[1]), pack2<KD>(v[2], v[3])};
+        else
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (col + e < p.n) store_cd<CD>(p.out, at + e, v[e]);
+      }
+  }
+}
+
+// -------------------------------------------------------------------------- join
+enum JoinKind { JOIN_OUT, JOIN_RANK, JOIN_GATE };
+struct Join {
+  int kind = JOIN_OUT, S = 0;
+  const float* part = nullptr;  // [S][m][ldp]
+  const float* low = nullptr;   // [m][ldp], JOIN_OUT: added under the drawn mask; JOIN_GATE: the up projection's parts
+  int64_t m = 0, n = 0, ldp = 0;
+  float scale = 1.f;
+  const void* bias = nullptr;
+  void* out = nullptr;  // [m][n] of type `type`: scale * sum (+ bias); JOIN_GATE: h
+  int type = 0;
+  void* pre = nullptr;  // JOIN_GATE: [m][2 n] or null
+  float* raw = nullptr;  // JOIN_RANK: the sums [m][n] or null
+  Planes rowwise, across;  // JOIN_RANK: scale * sum, [m][wide] and [n][tall]
+  int64_t wide = 0, tall = 0;
+  uint32_t per = 0, end = 0;  // groups of four columns to a row; workgroups as in Pack
+};
+constexpr int kJoins = 6;
+struct Joins {
+  Join j[kJoins];
+  Seeded sd;
+  int act;
+};
+
+__device__ __forceinline__ f32x4_t sum_of(const float* part, int S, int64_t stride, int64_t at) {
+  f32x4_t s = *(const f32x4_t*)(part + at);
+  for (int z = 1; z < S; z += 4) {  // four loads are on their way at once
+    f32x4_t v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = *(const f32x4_t*)(part + (z + e < S ? z + e : 0) * stride + at);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (z + e < S) s += v[e];
+  }
+  return s;
+}
+__device__ __forceinline__ void store_any(int type, void* p, int64_t at, float v) {
+  if (type == CD_F32) store_cd<CD_F32>(p, at, v);
+  else if (type == CD_BF16) store_cd<CD_BF16>(p, at, v);
+  else store_cd<CD_F16>(p, at, v);
+}
+__device__ __forceinline__ void store4(int type, void* p, int64_t at, const f32x4_t& v, int left) {
+  if (left >= 4 && (at & 3) == 0) {
+    if (type == CD_F32) *(f32x4_t*)((float*)p + at) = v;
+    else if (type == CD_BF16) *(u32x2_t*)((uint16_t*)p + at) = u32x2_t{pack2<CD_BF16>(v[0], v[1]), pack2<CD_BF16>(v[2], v[3])};
+    else *(u32x2_t*)((uint16_t*)p + at) = u32x2_t{pack2<CD_F16>(v[0], v[1]), pack2<CD_F16>(v[2], v[3])};
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (e < left) store_any(type, p, at + e, v[e]);
+}
+
+// A thread takes four columns of a row.
+template <int CD>
+__global__ __launch_bounds__(kThreads) void k_join(Joins js) {
+  constexpr int KD = CD == CD_F32 ? CD_BF16 : CD;
+  int job = 0;
+  while (blockIdx.x >= js.j[job].end) ++job;
+  const Join& j = js.j[job];
+  const int64_t idx = (int64_t)(blockIdx.x - (job ? js.j[job - 1].end : 0)) * kThreads + threadIdx.x;
+  if (j.kind == JOIN_RANK) {
+    // rows next to each other in neighbouring lanes: the transposed planes are written in lines
+    const int64_t rows = max(j.m, j.tall), g = idx / rows, i = idx - g * rows, t = 4 * g;
+    if (g >= j.per) return;
+    f32x4_t s = {0.f, 0.f, 0.f, 0.f};
+    if (i < j.m && t < j.n) s = sum_of(j.part, j.S, j.m * j.ldp, i * j.ldp + t);
+    uint16_t h[4][3];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (j.raw && i < j.m && t + e < j.n) j.raw[i * j.n + t + e] = s[e];
+      split<KD>(t + e < j.n ? j.scale * s[e] : 0.f, max(j.rowwise.n, j.across.n), h[e]);
+    }
+#pragma unroll
+    for (int q = 0; q < 3; ++q) {
+      if (j.rowwise.p && q < j.rowwise.n && i < j.m && t < j.wide)
+        *(u32x2_t*)(j.rowwise.p + i * j.rowwise.ld + q * j.rowwise.step + t) =
+            u32x2_t{h[0][q] | (uint32_t)h[1][q] << 16, h[2][q] | (uint32_t)h[3][q] << 16};
+      if (j.across.p && q < j.across.n && i < j.tall) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (t + e < j.n) j.across.p[(t + e) * j.across.ld + q * j.across.step + i] = h[e][q];
+      }
+    }
+    return;
+  }
+  const int64_t i = idx / j.per, k = 4 * (idx - i * j.per);
+  if (i >= j.m) return;
+  const int64_t at = i * j.ldp + k;
+  const int left = (int)min((int64_t)4, j.n - k);
+  f32x4_t s = sum_of(j.part, j.S, j.m * j.ldp, at);
+  if (j.kind == JOIN_OUT) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      s[e] *= j.scale;
+      if (j.bias && e < left) s[e] += load_cd<CD>(j.bias, k + e);
+    }
+    if (j.low) {
+      const f32x4_t l = *(const f32x4_t*)(j.low + at);
+      const u32x4_t w = philox(philox_key(js.sd), (uint32_t)(k >> 3), (uint32_t)i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[e] += keeps(w, (int)(k & 4) + e, js.sd.threshold) ? l[e] : 0.f;
+    }
+    store4(j.type, j.out, i * j.n + k, s, left);
+    return;
+  }
+  f32x4_t u = sum_of(j.low, j.S, j.m * j.ldp, at), o;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (j.bias && e < left) {
+      s[e] += load_cd<CD>(j.bias, k + e);
+      u[e] += load_cd<CD>(j.bias, j.n + k + e);
+    }
+    o[e] = (js.act == QLORA_ACT_SILU ? act_of<QLORA_ACT_SILU>(s[e])
+            : js.act == QLORA_ACT_GELU ? act_of<QLORA_ACT_GELU>(s[e])
+                                       : act_of<QLORA_ACT_GELU_TANH>(s[e])) * u[e];
+  }
+  store4(CD, j.out, i * j.n + k, o, left);
+  if (j.pre) {
+    store4(CD, j.pre, 2 * i * j.n + k, s, left);
+    store4(CD, j.pre, (2 * i + 1) * j.n + k, u, left);
+  }
+}
+
+// -------------------------------------------------------------------------- host
+using Low = Tile<1, 2, 2, 2, 3>;   // 64 x 128, four waves; two workgroups fit a compute unit
+using Wide = Tile<2, 2, 2, 4, 3>;  // 128 x 256, eight waves
+
+// One call: its workspace (sizing: only its size is wanted), and its launches' job lists.
+template <int CD>
+struct Run {
+  static constexpr int kPlanes = CD == CD_F32 ? 3 : 1;      // of an operand
+  static constexpr int kRankPlanes = CD == CD_F32 ? 3 : 2;  // of T and dT
+  char* base;
+  bool sizing;
+  hipStream_t s;
+  int64_t used = 0;
+  Packs packs = {};
+  Prods prods = {};
+  Joins joins = {};
+  int np = 0, nj = 0, rc = QLORA_OK;
+  bool big = false;
+
+  bool dry() const { return sizing; }
+  void* take(int64_t bytes) {
+    void* p = sizing ? nullptr : base + used;
+    used += round_up(bytes, 256);
+    return p;
+  }
+  Planes planes(int64_t rows, int64_t cols, int n) {
+    Planes o;
+    o.step = round_up(cols, 64);
+    o.ld = o.step * n;
+    o.n = n;
+    o.p = (uint16_t*)take(rows * o.ld * 2);
+    return o;
+  }
+  // A matrix that lies in the form of an operand already.
+  Planes as_is(const void* p, int64_t cols) {
+    Planes o;
+    o.p = (uint16_t*)p;
+    o.ld = o.step = cols;
+    return o;
+  }
+
+  Pack& pack(int src, const void* p, int64_t rows, int64_t cols) {
+    Pack& j = packs.j[packs.n++];
+    j = Pack();
+    j.src = src;
+    j.p = p;
+    j.rows = rows;
+    j.cols = cols;
+    j.rowwise.n = j.across.n = 0;
+    return j;
+  }
+  Planes rowwise(Pack& j, int n = kPlanes) {
+    j.wide = round_up(j.cols, 64);
+    return j.rowwise = planes(j.rows, j.cols, n);
+  }
+  Planes across(Pack& j, int n = kPlanes) {
+    j.tall = round_up(j.rows, 64);
+    return j.across = planes(j.cols, j.rows, n);
+  }
+  // [rows][cols] of the call's type as a row operand
+  Planes operand(const void* p, int64_t rows, int64_t cols, bool drawn = false) {
+    if (kPlanes == 1 && cols % 64 == 0 && !drawn) return as_is(p, cols);
+    Pack& j = pack(SRC_CD, p, rows, cols);
+    j.drawn = drawn;
+    return rowwise(j);
+  }
+  void run_packs(const LayerCall* c, int g, const Seeded* sd, int act) {
+    int64_t blocks = 0;
+    for (int i = 0; i < packs.n; ++i) {
+      Pack& j = packs.j[i];
+      const int64_t rows = std::max(j.rows, j.across.n ? j.tall : 0), cols = std::max(j.cols, j.rowwise.n ? j.wide : 0);
+      j.tiles_x = (uint32_t)ceil_div(cols, 64);
+      blocks += j.tiles_x * ceil_div(rows, 64);
+      if (blocks > 0x7fffffff) return fail();
+      j.end = (uint32_t)blocks;
+    }
+    if (dry() || rc || blocks == 0) return;
+    for (int i = 0; i < g; ++i) packs.w[i] = c[i].w;
+    for (int i = 0; i < 16; ++i) packs.lv[i] = host_tables().lv[i];
+    if (sd) packs.sd = *sd;
+    packs.act = act;
+    ProfScope prof(QLORA_K_DEQUANTIZE, s);
+    k_pack<CD><<<dim3((unsigned)blocks), dim3(kThreads), 0, s>>>(packs);
+    rc = check_launch("k_pack");
+  }
+
+  void fail() {
+    rc = set_error(QLORA_ERR_UNSUPPORTED, "layer: operand too large");
+  }
+  static Seg seg(const Planes& a, const Planes& b, int64_t k) {
+    Seg e = {};
+    e.a = a.p;
+    e.b = b.p;
+    e.lda = a.ld;
+    e.ldb = b.ld;
+    e.stepa = (int32_t)a.step;
+    e.stepb = (int32_t)b.step;
+    e.KM = (int32_t)ceil_div(k, 64);
+    // the pairs of planes whose product is not below the last bits kept
+    const int deepest = std::max(a.n, b.n);
+    for (int i = 0; i < a.n; ++i)
+      for (int l = 0; l < b.n && i + l < deepest; ++l) e.seq |= (uint32_t)(i | l << 2) << (4 * e.pairs++);
+    return e;
+  }
+  Prod& product(int64_t m, int64_t n) {
+    Prod& p = prods.p[np++];
+    p = Prod{};
+    p.m = m;
+    p.n = n;
+    p.S = 1;
+    p.ldp = round_up(n, 4);
+    return p;
+  }
+  static void add(Prod& p, const Seg& e) {
+    p.s[p.nseg++] = e;
+    p.steps += e.pairs * e.KM;
+  }
+  static int64_t low_tiles(int64_t m, int64_t n) {
+    return std::max<int64_t>(1, ceil_div(m, Low::TM) * ceil_div(n, Low::TN));  // a query may have no tokens
+  }
+  // Slices of a contraction: workgroups for every compute unit, at least four stages to each.
+  static int slices(int64_t m, int64_t n, int steps) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>({ceil_div(256, low_tiles(m, n)), steps / 4, 32}));
+  }
+  // partial sums of p for S slices, the last `extra` left to another product
+  float* parts(Prod& p, int S, int extra = 0) {
+    p.per = std::max(1, (int)ceil_div(p.steps, S));
+    p.S = std::max(1, (int)ceil_div(p.steps, p.per));
+    return p.part = (float*)take((p.S + extra) * p.m * p.ldp * 4);
+  }
+  template <class T>
+  void launch(int kind) {
+    int64_t blocks = 0;
+    for (int i = 0; i < np; ++i) {
+      Prod& p = prods.p[i];
+      if (p.per == 0) p.per = p.steps;
+      const int64_t tm = ceil_div(p.m, T::TM), tn = ceil_div(p.n, T::TN);
+      blocks += tm * tn * p.S;
+      if (blocks > 0x7fffffff) return fail();
+      p.tiles_m = (int32_t)tm;
+      p.tiles_n = (int32_t)tn;
+      p.end = (uint32_t)blocks;
+      for (int e = 0; e < p.nseg; ++e)
+        if (std::max(p.s[e].lda, p.s[e].ldb) * 2 * std::max(T::TM, T::TN) >= (1LL << 31)) return fail();
+    }
+    if (dry() || rc || blocks == 0) return;
+    ProfScope prof(kind, s);
+    k_product<CD, T><<<dim3((unsigned)blocks), dim3(64 * T::NW), 0, s>>>(prods);
+    rc = check_launch("k_product");
+  }
+  void run_products(int kind) {
+    if (big) launch<Wide>(kind);
+    else launch<Low>(kind);
+    np = 0;
+  }
+
+  Join& join(int kind, const Prod& p, const float* part) {
+    Join& j = joins.j[nj++];
+    j = Join();
+    j.kind = kind;
+    j.S = p.S;
+    j.part = part;
+    j.m = p.m;
+    j.n = p.n;
+    j.ldp = p.ldp;
+    j.type = CD;
+    j.rowwise.n = j.across.n = 0;
+    return j;
+  }
+  void run_joins(const Seeded* sd, int act) {
+    int64_t blocks = 0;
+    for (int i = 0; i < nj; ++i) {
+      Join& j = joins.j[i];
+      j.per = (uint32_t)ceil_div(std::max(j.n, j.wide), 4);
+      const int64_t rows = std::max(j.m, j.tall);
+      blocks += ceil_div(rows * j.per, kThreads);
+      if (blocks > 0x7fffffff) return fail();
+      j.end = (uint32_t)blocks;
+    }
+    if (!dry() && !rc && blocks) {
+      if (sd) joins.sd = *sd;
+      joins.act = act;
+      ProfScope prof(QLORA_K_REDUCE, s);
+      k_join<CD><<<dim3((unsigned)blocks), dim3(kThreads), 0, s>>>(joins);
+      rc = check_launch("k_join");
+    }
+    nj = 0;
+  }
+};
+
+// Tiles from which a product is not cut: its output leaves from the product itself.
+constexpr int64_t kDirectTiles = 160;
+
+template <int CD>
+int forward(const PlanesFwd& q, char* ws, int64_t* need) {
+  const LayerCall& c0 = q.c[0];
+  const int64_t m = c0.m, n = c0.w.rows, K = c0.w.cols;
+  const bool gated = q.g == 2;
+  Run<CD> run;
+  run.base = ws;
+  run.sizing = need != nullptr;
+  run.s = c0.stream;
+  const bool direct = Run<CD>::low_tiles(m, n) * q.g >= kDirectTiles;
+  // the gated GEMM with its own epilogue
+  const bool fused = gated && direct && CD != CD_F32 && c0.r <= 64 && q.c[1].r <= 64 && gemm16_ok(CD, m, n, round_up(K, 64));
+
+  const Planes x = run.operand(c0.x, m, K), xm = q.sd ? run.operand(c0.x, m, K, true) : x;
+  Planes a[2], b[2], w[2], t[2];
+  for (int i = 0; i < q.g; ++i) {
+    const LayerCall& c = q.c[i];
+    a[i] = run.operand(c.lora_a, c.r, K);
+    b[i] = run.operand(c.lora_b, n, c.r);
+    Pack& j = run.pack(SRC_NF4, nullptr, n, K);
+    j.w = i;
+    w[i] = run.rowwise(j);
+  }
+  run.run_packs(q.c, q.g, q.sd, 0);
+
+  Prod rank[2], main[2];
+  float* parts[2];
+  for (int i = 0; i < q.g; ++i) {
+    Prod& p = run.product(m, q.c[i].r);
+    run.add(p, run.seg(xm, a[i], K));
+    run.parts(p, run.slices(m, p.n, p.steps));
+    rank[i] = p;
+  }
+  if (!direct) {
+    int S = 32;
+    for (int i = 0; i < q.g; ++i) {
+      Prod& p = run.product(m, n);
+      run.add(p, run.seg(x, w[i], K));
+      S = std::min(S, run.slices(m, q.g * n, p.steps));
+      parts[i] = run.parts(p, S, 1);
+      main[i] = p;
+    }
+  }
+  run.run_products(QLORA_K_FWD_GEMM);
+
+  uint16_t* both = fused ? (uint16_t*)run.take(m * 128 * 2) : nullptr;
+  for (int i = 0; i < q.g; ++i) {
+    const LayerCall& c = q.c[i];
+    Join& j = run.join(JOIN_RANK, rank[i], rank[i].part);
+    j.raw = q.t_save ? q.t_save[i] : nullptr;
+    j.scale = c.scale;
+    j.wide = round_up(c.r, 64);
+    if (fused) {
+      j.rowwise.p = both ? both + 64 * i : nullptr;
+      j.rowwise.ld = 128;
+      j.rowwise.n = 1;
+    } else {
+      j.rowwise = run.planes(m, c.r, Run<CD>::kRankPlanes);
+    }
+    t[i] = j.rowwise;
+  }
+  run.run_joins(nullptr, 0);
+
+  if (fused) {
+    if (need) *need = run.used;
+    if (run.dry() || run.rc) return run.rc;
+    const void* wp[2] = {w[0].p, w[1].p};
+    const void* bp[2] = {b[0].p, b[1].p};
+    const int64_t ldb[2] = {b[0].ld, b[1].ld};
+    return gemm16_gated(CD, x.p, m, n, x.ld, wp, both, bp, ldb, q.bias, q.act, q.out, q.pre, c0.stream);
+  }
+  // [g | u] where the gate reads it
+  void* z = gated && direct ? (q.pre ? q.pre : run.take(m * 2 * n * cd_bytes(CD))) : q.out;
+  for (int i = 0; i < q.g; ++i) {
+    Prod& p = run.product(m, n);
+    if (direct) {
+      run.add(p, run.seg(x, w[i], K));
+      p.out = (char*)z + i * n * cd_bytes(CD);
+      p.ldo = q.g * n;
+      p.bias = q.bias ? (const char*)q.bias + i * n * cd_bytes(CD) : nullptr;
+    } else {
+      p.part = run.dry() ? nullptr : parts[i] + main[i].S * m * p.ldp;
+    }
+    run.add(p, run.seg(t[i], b[i], q.c[i].r));
+  }
+  run.big = direct && ceil_div(m, Wide::TM) * ceil_div(n, Wide::TN) * q.g >= 224;
+  run.run_products(QLORA_K_FWD_GEMM);
+  if (!direct) {
+    main[0].S += 1;  // and the low-rank part
+    Join& j = run.join(gated ? JOIN_GATE : JOIN_OUT, main[0], parts[0]);
+    j.bias = q.bias;
+    j.out = q.out;
+    j.pre = q.pre;
+    if (gated) j.low = parts[1];
+    run.run_joins(nullptr, q.act);
+  }
+  if (need) *need = run.used;
+  if (run.dry() || run.rc || !gated || !direct) return run.rc;
+  return gate(CD, q.act, z, nullptr, m, n, q.out, c0.stream);
+}
+
+template <int CD>
+int backward(const PlanesBwd& q, char* ws, int64_t* need) {
+  const LayerCall& c0 = q.c[0];
+  const int64_t m = c0.m, n = c0.w.rows, K = c0.w.cols;
+  const bool gated = q.g == 2, g32 = q.gd == CD_F32;
+  Run<CD> run;
+  run.base = ws;
+  run.sizing = need != nullptr;
+  run.s = c0.stream;
+  const bool direct = q.dx && Run<CD>::low_tiles(m, K) >= kDirectTiles;
+  // the masked GEMM draws the mask beside its products
+  const bool fused = direct && q.sd && CD != CD_F32 && c0.r <= 64 && gemm16_ok(CD, m, K, round_up(n, 64));
+  const bool whole = direct && !q.sd;  // dX leaves from one product
+  const bool saved = q.t_saved != nullptr;
+
+  Planes d[2], dt_[2], wt[2], at[2], bt[2], t0t[2], dtr[2], dtt[2], a[2], xm;
+  for (int i = 0; i < q.g; ++i) {
+    const LayerCall& c = q.c[i];
+    if (gated) {
+      Pack& j = run.pack(i ? SRC_UP : SRC_GATE, q.pre, m, n);
+      j.dh = q.dy;
+      d[i] = run.rowwise(j);
+      dt_[i] = run.across(j);
+    } else {
+      Pack& j = run.pack(SRC_CD, q.dy, m, n);
+      d[i] = Run<CD>::kPlanes == 1 && n % 64 == 0 ? run.as_is(q.dy, n) : run.rowwise(j);
+      dt_[i] = run.across(j);
+    }
+    bt[i] = run.across(run.pack(SRC_CD, c.lora_b, n, c.r));
+    if (q.dx) {
+      Pack& j = run.pack(SRC_NF4, nullptr, n, K);
+      j.w = i;
+      wt[i] = run.across(j);
+      at[i] = run.across(run.pack(SRC_CD, c.lora_a, c.r, K));
+    }
+    if (saved) t0t[i] = run.across(run.pack(SRC_F32, q.t_saved[i], m, c.r), Run<CD>::kRankPlanes);
+    else a[i] = run.operand(c.lora_a, c.r, K);
+  }
+  Pack& jx = run.pack(SRC_CD, c0.x, m, K);
+  jx.drawn = q.sd != nullptr;
+  const Planes xt = run.across(jx);
+  if (!saved) xm = Run<CD>::kPlanes == 1 && K % 64 == 0 && !q.sd ? run.as_is(c0.x, K) : run.rowwise(jx);
+  run.run_packs(q.c, q.g, q.sd, q.act);
+
+  Prod rank[2], rank0[2], da[2], db[2], main = {};
+  auto grad_b = [&](int i) {
+    Prod& p = run.product(n, q.c[i].r);
+    run.add(p, run.seg(dt_[i], t0t[i], m));
+    run.parts(p, run.slices(n, p.n, p.steps));
+    db[i] = p;
+  };
+  for (int i = 0; i < q.g; ++i) {
+    Prod& p = run.product(m, q.c[i].r);
+    run.add(p, run.seg(d[i], bt[i], n));
+    run.parts(p, run.slices(m, p.n, p.steps));
+    rank[i] = p;
+    if (saved) {
+      grad_b(i);
+    } else {
+      Prod& o = run.product(m, q.c[i].r);
+      run.add(o, run.seg(xm, a[i], K));
+      run.parts(o, run.slices(m, o.n, o.steps));
+      rank0[i] = o;
+    }
+  }
+  float* parts = nullptr;
+  if (q.dx && !whole && !fused) {
+    Prod& p = run.product(m, K);
+    for (int i = 0; i < q.g; ++i) run.add(p, run.seg(d[i], wt[i], n));
+    parts = run.parts(p, run.slices(m, K, p.steps), 1);
+    main = p;
+  }
+  run.run_products(QLORA_K_BWD_DX);
+
+  for (int i = 0; i < q.g; ++i) {
+    const LayerCall& c = q.c[i];
+    Join& j = run.join(JOIN_RANK, rank[i], rank[i].part);
+    j.scale = c.scale;
+    j.wide = round_up(c.r, 64);
+    j.tall = round_up(m, 64);
+    if (q.dx) dtr[i] = j.rowwise = run.planes(m, c.r, fused ? 1 : Run<CD>::kRankPlanes);
+    dtt[i] = j.across = run.planes(c.r, m, Run<CD>::kRankPlanes);
+    if (!saved) {
+      Join& o = run.join(JOIN_RANK, rank0[i], rank0[i].part);
+      o.tall = round_up(m, 64);
+      t0t[i] = o.across = run.planes(c.r, m, Run<CD>::kRankPlanes);
+    }
+  }
+  run.run_joins(nullptr, 0);
+
+  for (int i = 0; i < q.g; ++i) {
+    Prod& p = run.product(q.c[i].r, K);
+    run.add(p, run.seg(dtt[i], xt, m));
+    run.parts(p, run.slices(p.m, K, p.steps));
+    da[i] = p;
+    if (!saved) grad_b(i);
+  }
+  if (parts || (run.dry() && q.dx && !whole && !fused)) {  // the low-rank part of dX, a slice of its own
+    Prod& p = run.product(m, K);
+    for (int i = 0; i < q.g; ++i) run.add(p, run.seg(dtr[i], at[i], q.c[i].r));
+    p.part = run.dry() ? nullptr : parts + main.S * m * p.ldp;
+  }
+  run.run_products(QLORA_K_BWD_DA);
+  if (whole) {
+    Prod& p = run.product(m, K);
+    for (int i = 0; i < q.g; ++i) run.add(p, run.seg(d[i], wt[i], n));
+    for (int i = 0; i < q.g; ++i) run.add(p, run.seg(dtr[i], at[i], q.c[i].r));
+    p.out = q.dx;
+    p.ldo = K;
+    run.big = ceil_div(m, Wide::TM) * ceil_div(K, Wide::TN) >= 224;
+    run.run_products(QLORA_K_BWD_DX);
+  }
+  for (int i = 0; i < q.g && !run.dry(); ++i) {
+    Join& ja = run.join(JOIN_OUT, da[i], da[i].part);
+    ja.out = q.d_a[i];
+    Join& jb = run.join(JOIN_OUT, db[i], db[i].part);
+    jb.out = q.d_b[i];
+    jb.scale = q.c[i].scale;
+    ja.type = jb.type = g32 ? CD_F32 : CD;
+  }
+  if (parts) {
+    main.S += q.sd ? 0 : 1;  // the low-rank part is the slice behind the last, under the mask if there is one
+    Join& j = run.join(JOIN_OUT, main, parts);
+    j.out = q.dx;
+    if (q.sd) j.low = parts + main.S * m * main.ldp;
+  }
+  run.run_joins(q.sd, 0);
+  if (need) *need = run.used;
+  if (run.dry() || run.rc || !fused) return run.rc;
+  return gemm16_masked_dx(CD, d[0].p, m, K, d[0].ld, wt[0].p, dtr[0].p, dtr[0].ld, at[0].p, at[0].ld, *q.sd, q.dx,
+                          c0.stream);
+}
+
+}  // namespace
+
+// A call is sized before its first launch, so that one that does not fit is refused whole.
+int planes_forward(const PlanesFwd& q, void* ws, int64_t* need) {
+  int64_t n;
+  if (!need)
+    if (const int rc = planes_forward(q, nullptr, &n)) return rc;
+  if (q.c[0].cd == CD_BF16) return forward<CD_BF16>(q, (char*)ws, need);
+  if (q.c[0].cd == CD_F16) return forward<CD_F16>(q, (char*)ws, need);
+  return forward<CD_F32>(q, (char*)ws, need);
+}
+int planes_backward(const PlanesBwd& q, void* ws, int64_t* need) {
+  int64_t n;
+  if (!need)
+    if (const int rc = planes_backward(q, nullptr, &n)) return rc;
+  if (q.c[0].cd == CD_BF16) return backward<CD_BF16>(q, (char*)ws, need);
+  if (q.c[0].cd == CD_F16) return backward<CD_F16>(q, (char*)ws, need);
+  return backward<CD_F32>(q, (char*)ws, need);
+}
+
+int64_t planes_workspace(int op, const LayerCall* c, int g, bool seeded) {
+  static const Seeded some = {};
+  static const float* const none[2] = {};
+  static char out;
+  int64_t most = 0;
+  if (op == QLORA_OP_FWD) {
+    PlanesFwd q = {c, g, seeded ? &some : nullptr, 0, nullptr, nullptr, nullptr, nullptr};
+    return planes_forward(q, nullptr, &most) ? 0 : most;
+  }
+  for (int i = 0; i < 4; ++i) {  // T saved or not, dX wanted or not
+    PlanesBwd q = {c, g, seeded ? &some : nullptr, 0, nullptr, nullptr, i & 1 ? none : nullptr, i & 2 ? &out : nullptr,
+                   nullptr, nullptr, CD_F32};
+    int64_t need = 0;
+    if (planes_backward(q, nullptr, &need)) return 0;
+    most = std::max(most, need);
+  }
+  return most;
+}
+
+}  // namespace qnf4
