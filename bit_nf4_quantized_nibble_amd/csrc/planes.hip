@@ -46,6 +46,28 @@ __device__ __forceinline__ void split(float v, int planes, uint16_t (&o)[3]) {
   if (planes > 2) o[2] = to_cd16<KD>(rest - from_cd16<KD>(o[1]));
 }
 
+// A weight as three planes: its first 8 bits, the next 8 and the last (cut off, not rounded: a third of
+// the work; x is rounded, so that the products left out stay below 2^-25 of the largest).
+__device__ __forceinline__ void cut3(float v, uint32_t (&o)[3]) {
+  o[0] = __float_as_uint(v) & 0xffff0000u;
+  const float r = v - __uint_as_float(o[0]);
+  o[1] = __float_as_uint(r) & 0xffff0000u;
+  o[2] = __float_as_uint(r - __uint_as_float(o[1]));
+}
+// Planes of two weights, the first in the low halves.
+template <int CD, int P>
+__device__ __forceinline__ void pack_weights(float a, float b, uint32_t (&o)[P]) {
+  if constexpr (P == 1) {
+    o[0] = pack2<CD>(a, b);
+  } else {
+    uint32_t x[3], y[3];
+    cut3(a, x);
+    cut3(b, y);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) o[q] = __builtin_amdgcn_perm(y[q], x[q], 0x07060302u);
+  }
+}
+
 // Where a matrix's planes lie: element (i, k) of plane q at p[i ld + q step + k].
 struct Planes {
   uint16_t* p = nullptr;
@@ -76,64 +98,99 @@ struct Packs {
   int n, act;
 };
 
-// Eight consecutive elements (k0 .. k0 + 7, k0 a multiple of 8) of row i, zeros outside.
+// Eight consecutive elements from `at` of which `left` (> 0) are there, zeros behind: vectors need
+// no alignment beyond the element's.
 template <int CD>
 __device__ __forceinline__ void fetch_linear(const void* p, int64_t at, int left, float (&v)[8]) {
-  if constexpr (CD == CD_F32) {
-    if (left >= 8 && (at & 3) == 0) {
+  if (left >= 8) {
+    if constexpr (CD == CD_F32) {
+      __builtin_memcpy(v, (const float*)p + at, 32);
+    } else {
+      u32x4_t t;
+      __builtin_memcpy(&t, (const uint16_t*)p + at, 16);
 #pragma unroll
-      for (int d = 0; d < 2; ++d) {
-        const f32x4_t t = *(const f32x4_t*)((const float*)p + at + 4 * d);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[4 * d + e] = t[e];
-      }
-      return;
+      for (int e = 0; e < 8; ++e) v[e] = from_cd16<CD>((uint16_t)(t[e >> 1] >> (16 * (e & 1))));
     }
-  } else if (left >= 8 && (at & 7) == 0) {
-    const u32x4_t t = *(const u32x4_t*)((const uint16_t*)p + at);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = from_cd16<CD>((uint16_t)(t[e >> 1] >> (16 * (e & 1))));
     return;
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = e < left ? load_cd<CD>(p, at + e) : 0.f;
 }
-template <int CD>
-__device__ __forceinline__ void fetch_nf4(const Nf4W& w, const float* lv, int64_t at, int left, float (&v)[8]) {
-  uint32_t codes;  // nibble e: element at + e
-  if ((at & 7) == 0 && left >= 8) {
-    const uint32_t c = *(const uint32_t*)(w.codes + (at >> 1));
-    codes = (c >> 4 & 0x0f0f0f0fu) | (c << 4 & 0xf0f0f0f0u);  // the element in the high half of a byte comes first
+
+// Eight weights from flat index `at` as they are stored: their codes (element e in nibble e) and the
+// scales of the block they begin in and, from element `cut` on, of the next (blocks of eight or more).
+struct Eight {
+  uint32_t codes, q0, q1;  // q: the scale's bits, or its code
+  float t0, t1;            // the second-level scales
+  int cut;
+};
+__device__ __forceinline__ uint32_t nibbles(uint32_t c) {  // the element in the high half of a byte comes first
+  return (c >> 4 & 0x0f0f0f0fu) | (c << 4 & 0xf0f0f0f0u);
+}
+__device__ __forceinline__ Eight load_eight(const Nf4W& w, int64_t at, int left) {
+  Eight o = {};
+  if (left <= 0) return o;
+  const int64_t byte = at >> 1;
+  if (byte + 8 <= (w.rows * w.cols) >> 1) {
+    u32x2_t c;
+    __builtin_memcpy(&c, w.codes + byte, 8);
+    o.codes = __builtin_amdgcn_alignbit(nibbles(c[1]), nibbles(c[0]), (uint32_t)(at & 1) * 4);
   } else {
-    codes = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const uint32_t byte = w.codes[(at + min(e, left - 1)) >> 1];
-      codes |= ((at + e) & 1 ? byte & 15u : byte >> 4) << (4 * e);
+      const uint32_t b = w.codes[(at + min(e, left - 1)) >> 1];
+      o.codes |= ((at + e) & 1 ? b & 15u : b >> 4) << (4 * e);
     }
   }
-  const int64_t b0 = block_of(w, at);
-  if (w.bs >= 8) {  // at most two blocks
-    const int n = min(8, left), cut = (int)min((int64_t)8, (b0 + 1) * w.bs - at);
-    const float s0 = block_scale(w, b0), s1 = cut < n ? block_scale(w, b0 + 1) : 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = e < left ? fl32_mul(lv[codes >> (4 * e) & 15u], e < cut ? s0 : s1) : 0.f;
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      v[e] = e < left ? fl32_mul(lv[codes >> (4 * e) & 15u], block_scale(w, block_of(w, at + e))) : 0.f;
+  if (w.bs_shift >= 3 && (w.cols & 7) == 0) {  // eight that begin at a multiple of eight lie in one block
+    const int64_t b = at >> w.bs_shift;
+    o.cut = 8;
+    if (w.dq) {
+      o.q0 = w.absmax_q[b];
+      o.t0 = w.scale2[group_of(w, b)];
+    } else {
+      o.q0 = __float_as_uint(w.absmax[b]);
+    }
+    return o;
   }
-  if constexpr (CD != CD_F32) {
+  const int64_t b0 = block_of(w, at);
+  o.cut = (int)min((int64_t)8, (b0 + 1) * w.bs - at);
+  const int64_t b1 = o.cut < left ? b0 + 1 : b0;
+  if (w.dq) {
+    o.q0 = w.absmax_q[b0];
+    o.q1 = w.absmax_q[b1];
+    o.t0 = w.scale2[group_of(w, b0)];
+    o.t1 = w.scale2[group_of(w, b1)];
+  } else {
+    o.q0 = __float_as_uint(w.absmax[b0]);
+    o.q1 = __float_as_uint(w.absmax[b1]);
+  }
+  return o;
+}
+// Their values in the call's type, zeros from `left` on.
+template <int CD>
+__device__ __forceinline__ void value_eight(const Nf4W& w, const float* lv, const Eight& c, int64_t at, int left,
+                                            float (&v)[8]) {
+  const float s0 = w.dq ? (float)c.q0 * c.t0 : __uint_as_float(c.q0), s1 = w.dq ? (float)c.q1 * c.t1 : __uint_as_float(c.q1);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = from_cd16<CD>(to_cd16<CD>(v[e]));
+  for (int e = 0; e < 8; ++e) {
+    float s = e < c.cut ? s0 : s1;
+    if (w.bs < 8 && e < left) s = block_scale(w, block_of(w, at + e));  // up to four blocks
+    const float x = fl32_mul(lv[c.codes >> (4 * e) & 15u], s);
+    v[e] = e >= left ? 0.f : CD == CD_F32 ? x : from_cd16<CD == CD_F32 ? CD_BF16 : CD>(to_cd16<CD == CD_F32 ? CD_BF16 : CD>(x));
   }
 }
 
-// A workgroup takes 64 x 64 elements of a job; a thread takes eight columns of two rows.
+// A workgroup takes 64 x 64 elements of a job; a thread takes eight columns of two neighbouring rows, all
+// of whose loads leave before the first is used.  The transpose passes through LDS as words of two rows:
+// column k's row of 128 bytes begins 32 banks further for each eight columns, its 16-byte chunk c lies at
+// c ^ (k / 8) % 8, so that the lanes of a write (eight columns apart, or four words) touch every bank once.
 template <int CD>
 __global__ __launch_bounds__(kThreads) void k_pack(Packs ps) {
-  constexpr int KD = CD == CD_F32 ? CD_BF16 : CD, LD = 72;  // LDS rows of 64 elements and a pad of 16 bytes
-  __shared__ __attribute__((aligned(16))) uint16_t tile[3][64 * LD];
+  constexpr int KD = CD == CD_F32 ? CD_BF16 : CD;
+  constexpr int MAX = CD == CD_F32 ? 3 : 2;  // planes
+  __shared__ __attribute__((aligned(16))) char tile[MAX][72 * 128];
+  auto chunk_at = [](int col, int c) { return (col + (col >> 3)) * 128 + ((c ^ (col >> 3)) << 4); };
   __shared__ float lv[16];
   const int tid = threadIdx.x;
   int job = 0;
@@ -142,72 +199,102 @@ __global__ __launch_bounds__(kThreads) void k_pack(Packs ps) {
   const uint32_t b = blockIdx.x - (job ? ps.j[job - 1].end : 0);
   const int64_t i0 = (int64_t)(b / j.tiles_x) * 64, k0 = (int64_t)(b % j.tiles_x) * 64;
   if (tid < 16) lv[tid] = ps.lv[tid];
-  __syncthreads();
-  const int c = tid & 7;
-  const int64_t k = k0 + 8 * c;
+  const int c = tid & 7, r = tid >> 3;
+  const int64_t k = k0 + 8 * c, row[2] = {i0 + 2 * r, i0 + 2 * r + 1};
+  int left[2];
+  float v[2][8];
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int r = (tid >> 3) + 32 * half;
-    const int64_t i = i0 + r;
-    const int left = (int)min((int64_t)8, j.cols - k);
-    float v[8];
-    if (i < j.rows && left > 0) {
-      if (j.src == SRC_CD) fetch_linear<CD>(j.p, i * j.cols + k, left, v);
-      else if (j.src == SRC_F32) fetch_linear<CD_F32>(j.p, i * j.cols + k, left, v);
-      else if (j.src == SRC_NF4) fetch_nf4<CD>(ps.w[j.w], lv, i * j.cols + k, left, v);
-      else {
-        float g[8], u[8];
-        fetch_linear<CD>(j.p, 2 * i * j.cols + k, left, g);
-        fetch_linear<CD>(j.p, (2 * i + 1) * j.cols + k, left, u);
-        fetch_linear<CD>(j.dh, i * j.cols + k, left, v);
+  for (int h = 0; h < 2; ++h) {
+    left[h] = row[h] < j.rows ? (int)max((int64_t)0, min((int64_t)8, j.cols - k)) : 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[h][e] = 0.f;
+  }
+  if (j.src == SRC_NF4) {
+    const Nf4W& w = ps.w[j.w];
+    Eight raw[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) raw[h] = load_eight(w, row[h] * j.cols + k, left[h]);
+    __syncthreads();  // the levels are there
+#pragma unroll
+    for (int h = 0; h < 2; ++h) value_eight<CD>(w, lv, raw[h], row[h] * j.cols + k, left[h], v[h]);
+  } else if (j.src == SRC_CD) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (left[h] > 0) fetch_linear<CD>(j.p, row[h] * j.cols + k, left[h], v[h]);
+  } else if (j.src == SRC_F32) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (left[h] > 0) fetch_linear<CD_F32>(j.p, row[h] * j.cols + k, left[h], v[h]);
+  } else {
+    float g[2][8], u[2][8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (left[h] > 0) {
+        fetch_linear<CD>(j.p, 2 * row[h] * j.cols + k, left[h], g[h]);
+        fetch_linear<CD>(j.p, (2 * row[h] + 1) * j.cols + k, left[h], u[h]);
+        fetch_linear<CD>(j.dh, row[h] * j.cols + k, left[h], v[h]);
+      }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (left[h] > 0) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           float value, slope;
-          if (ps.act == QLORA_ACT_SILU) act_grad<QLORA_ACT_SILU>(g[e], value, slope);
-          else if (ps.act == QLORA_ACT_GELU) act_grad<QLORA_ACT_GELU>(g[e], value, slope);
-          else act_grad<QLORA_ACT_GELU_TANH>(g[e], value, slope);
-          v[e] = e < left ? v[e] * (j.src == SRC_GATE ? u[e] * slope : value) : 0.f;
+          if (ps.act == QLORA_ACT_SILU) act_grad<QLORA_ACT_SILU>(g[h][e], value, slope);
+          else if (ps.act == QLORA_ACT_GELU) act_grad<QLORA_ACT_GELU>(g[h][e], value, slope);
+          else act_grad<QLORA_ACT_GELU_TANH>(g[h][e], value, slope);
+          v[h][e] = e < left[h] ? v[h][e] * (j.src == SRC_GATE ? u[h][e] * slope : value) : 0.f;
         }
       }
-      if (j.drawn) {
-        const u32x4_t w = philox(philox_key(ps.sd), (uint32_t)(k >> 3), (uint32_t)i);
+  }
+  const int planes = max(j.rowwise.n, j.across.n);
+  uint16_t p[2][8][3];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = keeps(w, e, ps.sd.threshold) ? v[e] : 0.f;
-      }
-    } else {
+  for (int h = 0; h < 2; ++h) {
+    if (j.drawn && left[h] > 0) {
+      const u32x4_t w = philox(philox_key(ps.sd), (uint32_t)(k >> 3), (uint32_t)row[h]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.f;
+      for (int e = 0; e < 8; ++e) v[h][e] = keeps(w, e, ps.sd.threshold) ? v[h][e] : 0.f;
     }
-    const int planes = max(j.rowwise.n, j.across.n);
-    u32x4_t o[3];
+    u32x4_t o[MAX];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      uint16_t h[3];
-      split<KD>(v[e], planes, h);
+      if (CD == CD_F32 && j.src == SRC_NF4) {
+        uint32_t w[3];
+        cut3(v[h][e], w);
 #pragma unroll
-      for (int q = 0; q < 3; ++q) {
-        if (q >= planes) break;
-        o[q][e >> 1] = e & 1 ? o[q][e >> 1] | (uint32_t)h[q] << 16 : h[q];
-        if (j.across.p) tile[q][(8 * c + e) * LD + r] = h[q];
+        for (int q = 0; q < 3; ++q) p[h][e][q] = (uint16_t)(w[q] >> 16);
+      } else {
+        split<KD>(v[h][e], planes, p[h][e]);
       }
-    }
-    if (j.rowwise.p && i < j.rows && k < j.wide) {
 #pragma unroll
-      for (int q = 0; q < 3; ++q)
-        if (q < j.rowwise.n) *(u32x4_t*)(j.rowwise.p + i * j.rowwise.ld + q * j.rowwise.step + k) = o[q];
+      for (int q = 0; q < MAX; ++q)
+        if (q < planes) o[q][e >> 1] = e & 1 ? o[q][e >> 1] | (uint32_t)p[h][e][q] << 16 : p[h][e][q];
+    }
+    if (j.rowwise.p && row[h] < j.rows && k < j.wide) {
+#pragma unroll
+      for (int q = 0; q < MAX; ++q)
+        if (q < j.rowwise.n) *(u32x4_t*)(j.rowwise.p + row[h] * j.rowwise.ld + q * j.rowwise.step + k) = o[q];
     }
   }
   if (!j.across.p) return;
+#pragma unroll
+  for (int q = 0; q < MAX; ++q)
+    if (q < j.across.n) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        *(uint32_t*)(tile[q] + chunk_at(8 * c + e, r >> 2) + 4 * (r & 3)) = p[0][e][q] | (uint32_t)p[1][e][q] << 16;
+    }
   __syncthreads();
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    const int r = (tid >> 3) + 32 * half;
-    if (k0 + r < j.cols && i0 + 8 * c < j.tall) {
+  for (int h = 0; h < 2; ++h) {
+    const int y = r + 32 * h;
+    if (k0 + y < j.cols && i0 + 8 * c < j.tall) {
 #pragma unroll
-      for (int q = 0; q < 3; ++q)
+      for (int q = 0; q < MAX; ++q)
         if (q < j.across.n)
-          *(u32x4_t*)(j.across.p + (k0 + r) * j.across.ld + q * j.across.step + i0 + 8 * c) =
-              *(const u32x4_t*)&tile[q][r * LD + 8 * c];
+          *(u32x4_t*)(j.across.p + (k0 + y) * j.across.ld + q * j.across.step + i0 + 8 * c) =
+              *(const u32x4_t*)(tile[q] + chunk_at(y, c));
     }
   }
 }
@@ -220,6 +307,7 @@ struct Seg {
   int64_t lda, ldb;
   int32_t stepa, stepb, pairs, KM;
   uint32_t seq;
+  int32_t w;  // b is weight w - 1 from its codes (k_decode), w < 0: weight -w - 1 across its rows; 0: planes
 };
 constexpr int kSegs = 4;
 struct Prod {
@@ -375,6 +463,241 @@ __global__ __launch_bounds__(64 * T::NW) void k_product(Prods ps) {
   }
 }
 
+// The same where b may be W~ from its codes, which every row of tiles decodes anew: products of few rows,
+// weights whose blocks are powers of two of 32 or more within a row.  A stage of such a product is 64
+// elements of all planes; of planes it is one pair.  The codes come three stages ahead into registers
+// (a stage is shorter than a read from memory), the copies of the other operand one; a stage's codes
+// are decoded into the buffer that the products of the stage before do not read.
+struct Weights {
+  Nf4W w[2];
+  float lv[16];
+};
+template <int CD, class T>
+struct Decode {
+  static constexpr int KD = CD == CD_F32 ? CD_BF16 : CD, P = CD == CD_F32 ? 3 : 1, THREADS = 64 * T::NW;
+  static constexpr int A = T::TM * 128, B = T::TN * 128, STAGE = P * (A + B);
+  static constexpr int CA = T::TM / 8 / T::NW, CB = T::TN / 8 / T::NW;  // copies of a plane by a wave
+  static constexpr int WORDS = T::TN * 64 / 8 / THREADS;                // of eight codes to a thread and stage
+  static constexpr int AHEAD = 3;
+  static_assert(T::TN == 128 && CA * 8 * T::NW == T::TM && (WORDS == 2 || WORDS == 4), "whole copies");
+  using K = Half16<KD>;
+  struct Raw {
+    uint32_t word[WORDS], scale[2];
+    float second[2];
+  };
+
+  // The weights of a word of eight codes: element e is the high half of byte e / 2 first.
+  __device__ static __forceinline__ void weights(const char* lv, uint32_t c, float s, float (&v)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int bit = 4 * (e ^ 1);
+      const uint32_t four = bit >= 2 ? c >> (bit - 2) : c << 2;
+      const float l = *(const float*)(lv + (four & 60u));
+      v[e] = CD == CD_F16 ? fl32_mul(l, s) : l * s;
+    }
+  }
+  // A stage's products: PAIRS of planes (or one).
+  template <bool ALL>
+  __device__ static __forceinline__ void multiply(Acc<T>& acc, const char* now, int wave, int lane) {
+    constexpr int N = ALL ? P : 1;
+    const int h = lane >> 5, r32 = lane & 31, xr = swz(r32);
+    const char* a = now + ((wave / T::NWN) * 32 * T::WMB + r32) * 128;
+    const char* b = now + P * A + ((wave % T::NWN) * 32 * T::WNB + r32) * 128;
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      i32x4_t fa[N][T::WMB], fb[N][T::WNB];
+#pragma unroll
+      for (int s = 0; s < N; ++s) {
+#pragma unroll
+        for (int i = 0; i < T::WMB; ++i) fa[s][i] = K::read(a + s * A + i * 32 * 128, ks, h, xr);
+#pragma unroll
+        for (int j = 0; j < T::WNB; ++j) fb[s][j] = K::read(b + s * B + j * 32 * 128, ks, h, xr);
+      }
+#pragma unroll
+      for (int sa = 0; sa < N; ++sa)
+#pragma unroll
+        for (int sb = 0; sa + sb < N; ++sb)
+#pragma unroll
+          for (int i = 0; i < T::WMB; ++i)
+#pragma unroll
+            for (int j = 0; j < T::WNB; ++j) K::mma(acc[i][j], fb[sb][j], fa[sa][i], 0, 0);
+    }
+  }
+  // Copies of 64 elements of rows of `ld` elements, R of them to a wave.
+  template <int R>
+  __device__ static __forceinline__ void copies(rsrc_t r, char* dst, int64_t ld, uint32_t so, int wave, int lane) {
+    const int row = 8 * wave + (lane >> 3), chunk = (lane & 7) ^ swz(row);
+    const uint32_t o = (uint32_t)(row * (int)ld * 2 + 16 * chunk), step = (uint32_t)(8 * T::NW * (int)ld * 2);
+#pragma unroll
+    for (int i = 0; i < R; ++i) copy16(r, dst + (wave + T::NW * i) * 1024, o + i * step, so);
+  }
+
+  // Stages first .. first + KT - 1 of planes against planes.
+  __device__ static __forceinline__ void plain(Acc<T>& acc, char* lds, const Prod& p, int first, int KT, int64_t m0,
+                                               int64_t n0, int wave, int lane) {
+    const Seg& e = p.s[0];
+    const rsrc_t ra = make_rsrc(e.a + m0 * e.lda, min((int64_t)T::TM, p.m - m0) * e.lda * 2);
+    const rsrc_t rb = make_rsrc(e.b + n0 * e.ldb, min((int64_t)T::TN, p.n - n0) * e.ldb * 2);
+    auto ask = [&](int u, char* buf) {
+      const int k = (first + u) / e.pairs;
+      const uint32_t pair = e.seq >> (4 * (first + u - k * e.pairs));
+      copies<CA>(ra, buf, e.lda, ((pair & 3u) * (uint32_t)e.stepa + 64u * (uint32_t)k) * 2u, wave, lane);
+      copies<CB>(rb, buf + P * A, e.ldb, (((pair >> 2) & 3u) * (uint32_t)e.stepb + 64u * (uint32_t)k) * 2u, wave, lane);
+    };
+    ask(0, lds);
+    for (int u = 0; u < KT; ++u) {
+      __builtin_amdgcn_s_waitcnt(0);
+      barrier_only();
+      if (u + 1 < KT) ask(u + 1, lds + ((u & 1) ^ 1) * STAGE);
+      multiply<false>(acc, lds + (u & 1) * STAGE, wave, lane);
+    }
+  }
+
+  // The same against W~ (ACROSS: W~^T).  A thread takes 8 WORDS codes of a row of W, or (across) 4 WORDS of
+  // two neighbouring rows, whose values it stores as words of two.
+  template <bool ACROSS>
+  __device__ static __forceinline__ void coded(Acc<T>& acc, char* lds, const char* lv, const Prod& p, const Nf4W& w,
+                                               int first, int KT, int64_t m0, int64_t n0, int wave, int lane) {
+    constexpr int ROWS = ACROSS ? 2 : 1, EACH = WORDS / ROWS;
+    const Seg& e = p.s[0];
+    const rsrc_t ra = make_rsrc(e.a + m0 * e.lda, min((int64_t)T::TM, p.m - m0) * e.lda * 2);
+    const int tid = 64 * wave + lane, t = tid & 31;
+    const int64_t r0 = ACROSS ? 64 * (int64_t)first + 2 * t : n0 + tid / (8 / WORDS);
+    const int64_t c0 = ACROSS ? n0 + 4 * WORDS * (tid >> 5) : 64 * (int64_t)first + 8 * WORDS * (tid % (8 / WORDS));
+    const int64_t at0 = r0 * w.cols + c0, step = ACROSS ? 64 * w.cols : 64;
+    // rows of W from here on, counted from r0, are not there
+    const int64_t rows = (ACROSS ? c0 < w.cols : r0 < w.rows) ? w.rows - r0 : 0;
+    const bool dq = w.dq != 0;
+    const uint8_t *codes = w.codes, *absmax_q = w.absmax_q;
+    const float *absmax = w.absmax, *scale2 = w.scale2;
+    const int bs_shift = w.bs_shift, g_shift = w.g_shift;
+    auto load = [&](int u, Raw& o) {
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) {
+        const bool ok = u < KT && (ACROSS ? 64 * (int64_t)u + i : 0) < rows;
+        const int64_t at = ok ? at0 + i * w.cols + u * step : 0, b = at >> bs_shift;
+        if constexpr (EACH == 4) {
+          const u32x4_t c = *(const u32x4_t*)(codes + (at >> 1));
+#pragma unroll
+          for (int x = 0; x < 4; ++x) o.word[x] = c[x];
+        } else if constexpr (EACH == 2) {
+          const u32x2_t c = *(const u32x2_t*)(codes + (at >> 1));
+          o.word[2 * i] = c[0];
+          o.word[2 * i + 1] = c[1];
+        } else {
+          o.word[i] = *(const uint32_t*)(codes + (at >> 1));
+        }
+        if (dq) {
+          o.scale[i] = absmax_q[b];
+          o.second[i] = scale2[b >> g_shift];
+        } else {
+          o.scale[i] = __float_as_uint(absmax[b]);
+        }
+        if (!ok) o.scale[i] = 0, o.second[i] = 0.f;
+      }
+    };
+    auto decode = [&](const Raw& o, char* buf) {
+      char* b = buf + P * A;
+      float s[2];
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i) s[i] = dq ? (float)o.scale[i] * o.second[i] : __uint_as_float(o.scale[i]);
+#pragma unroll
+      for (int i = 0; i < EACH; ++i) {
+        float v[ROWS][8];
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) weights(lv, o.word[i + r * EACH], s[r], v[r]);
+        if constexpr (!ACROSS) {
+          const int row = tid / (8 / WORDS), c = WORDS * (tid % (8 / WORDS)) + i;
+          uint32_t w[4][P];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) pack_weights<CD, P>(v[0][2 * x], v[0][2 * x + 1], w[x]);
+#pragma unroll
+          for (int u = 0; u < P; ++u)
+            *(u32x4_t*)(b + u * B + row * 128 + ((c ^ swz(row)) << 4)) = u32x4_t{w[0][u], w[1][u], w[2][u], w[3][u]};
+        } else {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int row = 4 * WORDS * (tid >> 5) + 8 * i + x;
+            uint32_t w[P];
+            pack_weights<CD, P>(v[0][x], v[ROWS - 1][x], w);
+#pragma unroll
+            for (int u = 0; u < P; ++u)
+              *(uint32_t*)(b + u * B + row * 128 + (((t >> 2) ^ swz(row)) << 4) + 4 * (t & 3)) = w[u];
+          }
+        }
+      }
+    };
+    auto ask = [&](int u, char* buf) {
+#pragma unroll
+      for (int q = 0; q < P; ++q)
+        copies<CA>(ra, buf + q * A, e.lda, ((uint32_t)q * (uint32_t)e.stepa + 64u * (uint32_t)(first + u)) * 2u, wave, lane);
+    };
+    Raw raw[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) load(i, raw[i]);
+    ask(0, lds);
+    decode(raw[0], lds);
+    for (int u0 = 0; u0 < KT; u0 += AHEAD) {
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const int u = u0 + i;
+        if (u >= KT) break;
+        char *now = lds + (u & 1) * STAGE, *next = lds + ((u & 1) ^ 1) * STAGE;
+        // this wave's copies of the stage (at least 2 ROWS loads of codes and scales left after them) and its
+        // decoded rows
+        __builtin_amdgcn_sched_barrier(0);
+        if (u == 0) wait_vmcnt<0>();
+        else wait_vmcnt<2 * ROWS>();
+        wait_lgkm0();
+        barrier_only();
+        if (u + 1 < KT) ask(u + 1, next);
+        __builtin_amdgcn_sched_barrier(0);
+        load(u + AHEAD, raw[i]);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply<true>(acc, now, wave, lane);
+        decode(raw[(i + 1) % AHEAD], next);
+      }
+    }
+  }
+};
+
+template <int CD, class T>
+__global__ __launch_bounds__(64 * T::NW) void k_decode(Prods ps, Weights ws) {
+  using D = Decode<CD, T>;
+  __shared__ __attribute__((aligned(1024))) char lds[2 * D::STAGE];
+  __shared__ float lv[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  int job = 0;
+  while (blockIdx.x >= ps.p[job].end) ++job;
+  const Prod& p = ps.p[job];
+  const int tiles = p.tiles_m * p.tiles_n, b = (int)(blockIdx.x - (job ? ps.p[job - 1].end : 0));
+  const int z = b / tiles, t = b - z * tiles;
+  const int64_t m0 = (int64_t)(t % p.tiles_m) * T::TM, n0 = (int64_t)(t / p.tiles_m) * T::TN;
+  const int first = z * p.per, KT = min(p.per, p.steps - first), kind = p.s[0].w;
+  if (tid < 16) lv[tid] = ws.lv[tid];
+  __syncthreads();
+  Acc<T> acc;
+  zero<T>(acc);
+  if (kind > 0) D::template coded<false>(acc, lds, (const char*)lv, p, ws.w[kind - 1], first, KT, m0, n0, wave, lane);
+  else if (kind < 0) D::template coded<true>(acc, lds, (const char*)lv, p, ws.w[-kind - 1], first, KT, m0, n0, wave, lane);
+  else D::plain(acc, lds, p, first, KT, m0, n0, wave, lane);
+
+  const int h = lane >> 5, r32 = lane & 31;
+  const int64_t row0 = m0 + (wave / T::NWN) * 32 * T::WMB + r32, col0 = n0 + (wave % T::NWN) * 32 * T::WNB + 4 * h;
+  float* part = p.part + (int64_t)z * p.m * p.ldp;
+#pragma unroll
+  for (int i = 0; i < T::WMB; ++i)
+#pragma unroll
+    for (int j = 0; j < T::WNB; ++j)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int64_t row = row0 + 32 * i, col = col0 + 32 * j + 8 * v;
+        if (row < p.m && col < p.n)
+          *(f32x4_t*)(part + row * p.ldp + col) =
+              f32x4_t{acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2], acc[i][j][4 * v + 3]};
+      }
+}
+
 // -------------------------------------------------------------------------- join
 enum JoinKind { JOIN_OUT, JOIN_RANK, JOIN_GATE };
 struct Join {
@@ -502,6 +825,10 @@ __global__ __launch_bounds__(kThreads) void k_join(Joins js) {
 // -------------------------------------------------------------------------- host
 using Low = Tile<1, 2, 2, 2, 3>;   // 64 x 128, four waves; two workgroups fit a compute unit
 using Wide = Tile<2, 2, 2, 4, 3>;  // 128 x 256, eight waves
+// k_decode's: 64 or 128 x 128, four waves and 48 or 64 KB of LDS; with three planes 64 x 128, eight waves, 144 KB
+using FewRows = Tile<1, 2, 2, 2, 2>;
+using SomeRows = Tile<2, 2, 2, 2, 2>;
+using FewRows3 = Tile<1, 1, 2, 4, 2>;
 
 // One call: its workspace (sizing: only its size is wanted), and its launches' job lists.
 template <int CD>
@@ -516,7 +843,7 @@ struct Run {
   Prods prods = {};
   Joins joins = {};
   int np = 0, nj = 0, rc = QLORA_OK;
-  bool big = false;
+  bool big = false, decodes = false;
 
   bool dry() const { return sizing; }
   void* take(int64_t bytes) {
@@ -603,6 +930,15 @@ struct Run {
       for (int l = 0; l < b.n && i + l < deepest; ++l) e.seq |= (uint32_t)(i | l << 2) << (4 * e.pairs++);
     return e;
   }
+  // a against W~ of weight i (across: W~^T) from its codes
+  Seg seg_w(const Planes& a, int i, bool across, int64_t k) {
+    decodes = true;
+    Seg e = seg(a, Planes(), k);
+    e.pairs = 1;
+    e.seq = 0;
+    e.w = across ? -(i + 1) : i + 1;
+    return e;
+  }
   Prod& product(int64_t m, int64_t n) {
     Prod& p = prods.p[np++];
     p = Prod{};
@@ -620,17 +956,17 @@ struct Run {
     return std::max<int64_t>(1, ceil_div(m, Low::TM) * ceil_div(n, Low::TN));  // a query may have no tokens
   }
   // Slices of a contraction: workgroups for every compute unit, at least four stages to each.
-  static int slices(int64_t m, int64_t n, int steps) {
-    return (int)std::max<int64_t>(1, std::min<int64_t>({ceil_div(256, low_tiles(m, n)), steps / 4, 32}));
+  static int slices(int64_t m, int64_t n, int steps, int64_t groups = 256) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>({ceil_div(groups, low_tiles(m, n)), steps / 4, 32}));
   }
-  // partial sums of p for S slices, the last `extra` left to another product
-  float* parts(Prod& p, int S, int extra = 0) {
+  // partial sums of p for S slices, and of `more` - 1 products alike and `extra` slices of another behind them
+  float* parts(Prod& p, int S, int extra = 0, int more = 1) {
     p.per = std::max(1, (int)ceil_div(p.steps, S));
     p.S = std::max(1, (int)ceil_div(p.steps, p.per));
-    return p.part = (float*)take((p.S + extra) * p.m * p.ldp * 4);
+    return p.part = (float*)take((more * p.S + extra) * p.m * p.ldp * 4);
   }
-  template <class T>
-  void launch(int kind) {
+  template <class T, bool DECODE>
+  void launch(int kind, const LayerCall* c, int g) {
     int64_t blocks = 0;
     for (int i = 0; i < np; ++i) {
       Prod& p = prods.p[i];
@@ -646,13 +982,29 @@ struct Run {
     }
     if (dry() || rc || blocks == 0) return;
     ProfScope prof(kind, s);
-    k_product<CD, T><<<dim3((unsigned)blocks), dim3(64 * T::NW), 0, s>>>(prods);
-    rc = check_launch("k_product");
+    const dim3 grid((unsigned)blocks), threads(64 * T::NW);
+    if constexpr (DECODE) {
+      Weights w;
+      for (int i = 0; i < g; ++i) w.w[i] = c[i].w;
+      for (int i = 0; i < 16; ++i) w.lv[i] = host_tables().lv[i];
+      k_decode<CD, T><<<grid, threads, 0, s>>>(prods, w);
+    } else {
+      k_product<CD, T><<<grid, threads, 0, s>>>(prods);
+    }
+    rc = check_launch(DECODE ? "k_decode" : "k_product");
   }
-  void run_products(int kind) {
-    if (big) launch<Wide>(kind);
-    else launch<Low>(kind);
+  void run_products(int kind, const LayerCall* c, int g) {
+    if (decodes) {
+      if constexpr (CD == CD_F32) launch<FewRows3, true>(kind, c, g);
+      else if (c->m <= FewRows::TM) launch<FewRows, true>(kind, c, g);
+      else launch<SomeRows, true>(kind, c, g);
+    } else if (big) {
+      launch<Wide, false>(kind, c, g);
+    } else {
+      launch<Low, false>(kind, c, g);
+    }
     np = 0;
+    decodes = false;
   }
 
   Join& join(int kind, const Prod& p, const float* part) {
@@ -691,6 +1043,14 @@ struct Run {
 
 // Tiles from which a product is not cut: its output leaves from the product itself.
 constexpr int64_t kDirectTiles = 160;
+// Rows up to which W~ is decoded by the product that reads it.
+constexpr int64_t kDecodeRows = 128;
+bool decodable(const LayerCall* c, int g) {
+  for (int i = 0; i < g; ++i)
+    if (!fast_layout(c[i].w) || c[i].w.bs_shift < 0 || (c[i].w.dq && c[i].w.g_shift < 0)) return false;
+  return c[0].m <= kDecodeRows;
+}
+constexpr int64_t decode_groups(int cd) { return cd == CD_F32 ? 256 : 512; }
 
 template <int CD>
 int forward(const PlanesFwd& q, char* ws, int64_t* need) {
@@ -701,7 +1061,8 @@ int forward(const PlanesFwd& q, char* ws, int64_t* need) {
   run.base = ws;
   run.sizing = need != nullptr;
   run.s = c0.stream;
-  const bool direct = Run<CD>::low_tiles(m, n) * q.g >= kDirectTiles;
+  const bool decode = decodable(q.c, q.g);
+  const bool direct = !decode && Run<CD>::low_tiles(m, n) * q.g >= kDirectTiles;
   // the gated GEMM with its own epilogue
   const bool fused = gated && direct && CD != CD_F32 && c0.r <= 64 && q.c[1].r <= 64 && gemm16_ok(CD, m, n, round_up(K, 64));
 
@@ -711,6 +1072,7 @@ int forward(const PlanesFwd& q, char* ws, int64_t* need) {
     const LayerCall& c = q.c[i];
     a[i] = run.operand(c.lora_a, c.r, K);
     b[i] = run.operand(c.lora_b, n, c.r);
+    if (decode) continue;
     Pack& j = run.pack(SRC_NF4, nullptr, n, K);
     j.w = i;
     w[i] = run.rowwise(j);
@@ -729,13 +1091,13 @@ int forward(const PlanesFwd& q, char* ws, int64_t* need) {
     int S = 32;
     for (int i = 0; i < q.g; ++i) {
       Prod& p = run.product(m, n);
-      run.add(p, run.seg(x, w[i], K));
-      S = std::min(S, run.slices(m, q.g * n, p.steps));
+      run.add(p, decode ? run.seg_w(x, i, false, K) : run.seg(x, w[i], K));
+      S = std::min(S, run.slices(m, q.g * n, p.steps, decode ? decode_groups(CD) : 256));
       parts[i] = run.parts(p, S, 1);
       main[i] = p;
     }
   }
-  run.run_products(QLORA_K_FWD_GEMM);
+  run.run_products(QLORA_K_FWD_GEMM, q.c, q.g);
 
   uint16_t* both = fused ? (uint16_t*)run.take(m * 128 * 2) : nullptr;
   for (int i = 0; i < q.g; ++i) {
@@ -778,7 +1140,7 @@ int forward(const PlanesFwd& q, char* ws, int64_t* need) {
     run.add(p, run.seg(t[i], b[i], q.c[i].r));
   }
   run.big = direct && ceil_div(m, Wide::TM) * ceil_div(n, Wide::TN) * q.g >= 224;
-  run.run_products(QLORA_K_FWD_GEMM);
+  run.run_products(QLORA_K_FWD_GEMM, q.c, q.g);
   if (!direct) {
     main[0].S += 1;  // and the low-rank part
     Join& j = run.join(gated ? JOIN_GATE : JOIN_OUT, main[0], parts[0]);
@@ -802,7 +1164,8 @@ int backward(const PlanesBwd& q, char* ws, int64_t* need) {
   run.base = ws;
   run.sizing = need != nullptr;
   run.s = c0.stream;
-  const bool direct = q.dx && Run<CD>::low_tiles(m, K) >= kDirectTiles;
+  const bool decode = q.dx && decodable(q.c, q.g);
+  const bool direct = q.dx && !decode && Run<CD>::low_tiles(m, K) >= kDirectTiles;
   // the masked GEMM draws the mask beside its products
   const bool fused = direct && q.sd && CD != CD_F32 && c0.r <= 64 && gemm16_ok(CD, m, K, round_up(n, 64));
   const bool whole = direct && !q.sd;  // dX leaves from one product
@@ -823,9 +1186,11 @@ int backward(const PlanesBwd& q, char* ws, int64_t* need) {
     }
     bt[i] = run.across(run.pack(SRC_CD, c.lora_b, n, c.r));
     if (q.dx) {
-      Pack& j = run.pack(SRC_NF4, nullptr, n, K);
-      j.w = i;
-      wt[i] = run.across(j);
+      if (!decode) {
+        Pack& j = run.pack(SRC_NF4, nullptr, n, K);
+        j.w = i;
+        wt[i] = run.across(j);
+      }
       at[i] = run.across(run.pack(SRC_CD, c.lora_a, c.r, K));
     }
     if (saved) t0t[i] = run.across(run.pack(SRC_F32, q.t_saved[i], m, c.r), Run<CD>::kRankPlanes);
@@ -861,11 +1226,19 @@ int backward(const PlanesBwd& q, char* ws, int64_t* need) {
   float* parts = nullptr;
   if (q.dx && !whole && !fused) {
     Prod& p = run.product(m, K);
-    for (int i = 0; i < q.g; ++i) run.add(p, run.seg(d[i], wt[i], n));
-    parts = run.parts(p, run.slices(m, K, p.steps), 1);
+    for (int i = 0; i < (decode ? 1 : q.g); ++i) run.add(p, decode ? run.seg_w(d[i], i, true, n) : run.seg(d[i], wt[i], n));
+    parts = run.parts(p, run.slices(m, decode ? q.g * K : K, p.steps, decode ? decode_groups(CD) : 256), 1, decode ? q.g : 1);
     main = p;
+    if (decode && gated) {  // one weight to a product: the second's slices behind the first's
+      Prod& o = run.product(m, K);
+      run.add(o, run.seg_w(d[1], 1, true, n));
+      o.per = p.per;
+      o.S = p.S;
+      o.part = run.dry() ? nullptr : parts + p.S * m * p.ldp;
+      main.S = 2 * p.S;
+    }
   }
-  run.run_products(QLORA_K_BWD_DX);
+  run.run_products(QLORA_K_BWD_DX, q.c, q.g);
 
   for (int i = 0; i < q.g; ++i) {
     const LayerCall& c = q.c[i];
@@ -895,7 +1268,7 @@ int backward(const PlanesBwd& q, char* ws, int64_t* need) {
     for (int i = 0; i < q.g; ++i) run.add(p, run.seg(dtr[i], at[i], q.c[i].r));
     p.part = run.dry() ? nullptr : parts + main.S * m * p.ldp;
   }
-  run.run_products(QLORA_K_BWD_DA);
+  run.run_products(QLORA_K_BWD_DA, q.c, q.g);
   if (whole) {
     Prod& p = run.product(m, K);
     for (int i = 0; i < q.g; ++i) run.add(p, run.seg(d[i], wt[i], n));
@@ -903,7 +1276,7 @@ int backward(const PlanesBwd& q, char* ws, int64_t* need) {
     p.out = q.dx;
     p.ldo = K;
     run.big = ceil_div(m, Wide::TM) * ceil_div(K, Wide::TN) >= 224;
-    run.run_products(QLORA_K_BWD_DX);
+    run.run_products(QLORA_K_BWD_DX, q.c, q.g);
   }
   for (int i = 0; i < q.g && !run.dry(); ++i) {
     Join& ja = run.join(JOIN_OUT, da[i], da[i].part);
