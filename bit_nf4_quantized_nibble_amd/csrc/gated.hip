@@ -103,7 +103,9 @@ int gate_cd(int act, const void* pre, const void* dh, int64_t n, int64_t total, 
 // How a forward runs, and its workspace.
 //   DECODE   up to 64 tokens on the split-K GEMV: both projections' partial sums, one epilogue
 //   TILED    W~ of both in the workspace, T = s x A^T by the rank-product kernels, then the gated GEMM
-//   PLANES   every other layout and fp32
+//   PLANES   every other layout, fp32, and up to 128 tokens of large weights, which that way decodes in the
+//            product (128 tokens, bf16: 89 us against 122 at 14336 x 4096, 103 against 186 at
+//            4096 x 14336, but 51 against 48 at 4096 x 4096 and 26 against 17 at 512 x 512)
 enum Way { DECODE, TILED, PLANES };
 struct FwdPlan {
   Way way;
@@ -116,7 +118,7 @@ FwdPlan plan_fwd(const GroupCall& gc) {
   if (m > 0 && gemv_gated_ok(gc.c)) {
     P.way = DECODE;
     P.total = (int64_t)gemv_gated_workspace_bytes(gc.c);
-  } else if (m > 16 && gemm16_ok(c0.cd, m, n, K) && fast_layout(c0.w) && fast_layout(c1.w) && skinny_ok(c0.cd, c0.r) &&
+  } else if (m > 16 && !(m <= 128 && n * K >= 1 << 25) && gemm16_ok(c0.cd, m, n, K) && fast_layout(c0.w) && fast_layout(c1.w) && skinny_ok(c0.cd, c0.r) &&
              skinny_ok(c1.cd, c1.r) && dense256_ok(c0, false) && dense256_ok(c1, false)) {
     P.way = TILED;
     int64_t o = 0;
@@ -145,9 +147,13 @@ __global__ __launch_bounds__(kThreads) void k_pad_rows(const uint16_t* __restric
   }
 }
 
-// Whether the group call's tuned kernels take a backward.
+// Whether the group call's tuned kernels take a backward: with few tokens or small weights the other way
+// has fewer launches and, up to 256 tokens, no copy of W~ (bf16: 1 token of 14336 x 4096 88 us against 169,
+// 128 tokens 138 against 210; 1024 x 512 x 512 37 against 54, 1024 x 2048 x 2048 82 against 90, but
+// 2048 x 2048 x 2048 109 against 106, 512 x 4096 x 4096 136 against 113).
 bool tuned_bwd(const GroupCall& gc) {
   const LayerCall &c0 = gc.c[0], &c1 = gc.c[1];
+  if (c0.m <= 128 || c0.m * c0.w.rows * c0.w.cols <= 1LL << 32) return false;
   return c0.cd != CD_F32 && c0.w.rows % 64 == 0 && fast_layout(c0.w) && fast_layout(c1.w) && skinny_ok(c0.cd, c0.r) &&
          skinny_ok(c1.cd, c1.r);
 }

@@ -953,9 +953,18 @@ inline bool gemv_candidate(int64_t m, int32_t flags) {
   return m <= kGemvMaxM || (m <= kGemvMfmaMaxM && !(flags & (QLORA_FLAG_FUSED | QLORA_FLAG_DEQUANT_GEMM)));
 }
 
-// Whether a seeded call is none of the tuned kernels'.
+// Whether a seeded call is none of the tuned kernels': another layout or type, or few tokens or a small
+// weight, where the other way has fewer launches and no copy of W~ (forward, bf16: 1 token of
+// 4096 x 14336 43 us against 68, 64 tokens 51 against 74, 256 x 1024 x 1024 26 against 30, but
+// 128 tokens of 14336 x 4096 65 against 59, 512 x 4096 x 4096 69 against 58; backward: 1 token of
+// 14336 x 4096 52 against 142, 128 tokens 80 against 148, 512 x 2048 x 2048 41 against 46, but
+// 2048 x 1024 x 1024 49 against 44).
 bool planes_seeded(int op, const LayerCall& c) {
-  const bool tuned = c.cd != CD_F32 && fast_layout(c.w) && (op == QLORA_OP_FWD || c.w.rows % 64 == 0) && skinny_ok(c.cd, c.r);
+  const int64_t n = c.w.rows, K = c.w.cols;
+  const bool small = op == QLORA_OP_FWD
+                         ? c.m <= 64 || (c.m <= 128 && n <= 2 * K) || (n * K <= 1 << 22 && c.m * n * K <= 1LL << 33)
+                         : c.m <= 128 || c.m * n * K <= 1LL << 31;
+  const bool tuned = !small && c.cd != CD_F32 && fast_layout(c.w) && (op == QLORA_OP_FWD || c.w.rows % 64 == 0) && skinny_ok(c.cd, c.r);
   return !tuned && !(c.flags & (QLORA_FLAG_FUSED | QLORA_FLAG_DEQUANT_GEMM));
 }
 // What it may need: a query does not know the block size.
