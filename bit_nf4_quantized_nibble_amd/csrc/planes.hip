@@ -956,8 +956,14 @@ struct Run {
     return std::max<int64_t>(1, ceil_div(m, Low::TM) * ceil_div(n, Low::TN));  // a query may have no tokens
   }
   // Slices of a contraction: workgroups for every compute unit, at least four stages to each.
-  static int slices(int64_t m, int64_t n, int steps, int64_t groups = 256) {
-    return (int)std::max<int64_t>(1, std::min<int64_t>({ceil_div(groups, low_tiles(m, n)), steps / 4, 32}));
+  static int slices(int64_t m, int64_t n, int steps) {
+    return (int)std::max<int64_t>(1, std::min<int64_t>({ceil_div(256, low_tiles(m, n)), steps / 4, 32}));
+  }
+  // The same where the product decodes: as many workgroups as run at once (48 KB of LDS each, 64 KB, 144 KB).
+  static int decode_slices(int64_t m, int64_t n, int steps) {
+    const int64_t at_once = 256 * (CD == CD_F32 ? 1 : m <= FewRows::TM ? 3 : 2);
+    const int64_t tiles = ceil_div(n, 128) * ceil_div(m, CD == CD_F32 || m <= FewRows::TM ? 64 : 128);
+    return (int)std::max<int64_t>(1, std::min<int64_t>({at_once / std::max<int64_t>(1, tiles), steps / 4, 32}));
   }
   // partial sums of p for S slices, and of `more` - 1 products alike and `extra` slices of another behind them
   float* parts(Prod& p, int S, int extra = 0, int more = 1) {
@@ -1052,7 +1058,6 @@ bool decodable(const LayerCall* c, int g) {
     if (!fast_layout(c[i].w) || c[i].w.bs_shift < 0 || (c[i].w.dq && c[i].w.g_shift < 0)) return false;
   return c[0].m <= decode_rows(c[0].cd);
 }
-constexpr int64_t decode_groups(int cd) { return cd == CD_F32 ? 256 : 512; }
 
 template <int CD>
 int forward(const PlanesFwd& q, char* ws, int64_t* need) {
@@ -1094,7 +1099,7 @@ int forward(const PlanesFwd& q, char* ws, int64_t* need) {
     for (int i = 0; i < q.g; ++i) {
       Prod& p = run.product(m, n);
       run.add(p, decode ? run.seg_w(x, i, false, K) : run.seg(x, w[i], K));
-      S = std::min(S, run.slices(m, q.g * n, p.steps, decode ? decode_groups(CD) : 256));
+      S = std::min(S, decode ? run.decode_slices(m, q.g * n, p.steps) : run.slices(m, q.g * n, p.steps));
       parts[i] = run.parts(p, S, 1);
       main[i] = p;
     }
@@ -1229,7 +1234,7 @@ int backward(const PlanesBwd& q, char* ws, int64_t* need) {
   if (q.dx && !whole && !fused) {
     Prod& p = run.product(m, K);
     for (int i = 0; i < (decode ? 1 : q.g); ++i) run.add(p, decode ? run.seg_w(d[i], i, true, n) : run.seg(d[i], wt[i], n));
-    parts = run.parts(p, run.slices(m, decode ? q.g * K : K, p.steps, decode ? decode_groups(CD) : 256), 1, decode ? q.g : 1);
+    parts = run.parts(p, decode ? run.decode_slices(m, q.g * K, p.steps) : run.slices(m, K, p.steps), 1, decode ? q.g : 1);
     main = p;
     if (decode && gated) {  // one weight to a product: the second's slices behind the first's
       Prod& o = run.product(m, K);
