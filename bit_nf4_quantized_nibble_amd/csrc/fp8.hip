@@ -236,9 +236,6 @@ struct Copies8 {
     for (int i = 0; i < T::WMB; ++i) s[0][i] = (int)((uint32_t)s[1][i] >> (8 * (stage & 3)));
     sb[0] = sb[1];
   }
-  static constexpr int kSlots = 0;
-  __device__ __forceinline__ void stage(int) const {}
-  __device__ __forceinline__ void slot(int) const {}
 };
 
 // Word i (of 4 bytes) of a tile's coefficients: biases as fp32, then the exponents of its blocks.

@@ -533,7 +533,8 @@ BwdPlan plan_bwd(int64_t m, int64_t rows, int64_t cols, int32_t r, int cd, int32
   P.off_xm = P.off_wdt + (P.dense ? al(rows * cols * es) : 0);
   const bool drop = (flags & QLORA_FLAG_DROPOUT) != 0;
   P.off_zero = P.off_xm + (drop ? al(m * cols * es) : 0);
-  P.off_split = P.off_zero + (drop ? al(m * P.r_pad * es) : 0);
+  // (or the mask's bits)
+  P.off_split = P.off_zero + (drop ? al(m * std::max<int64_t>(P.r_pad * es, ceil_div(cols, 8))) : 0);
   P.dsp = dense_split(m, cols, rows, !P.dense);
   // A^T [cols][r_pad] in cd: the W-side rows of the dense dX GEMM's low-rank tail
   P.off_at = P.off_split + (big_tiles(cd) ? al(dense_split_bytes(P.dsp)) : 0);
@@ -601,7 +602,7 @@ int forward_gemm(const LayerCall& c, const Seeded* sd, void* y, float* t_save) {
   // input of the low-rank branch: x, or x M with LoRA dropout
   const void* lx = c.x;
   if (c.drop_mask || sd) {
-    rc = sd ? apply_seeded(CD, c.x, *sd, M, K, ws + P.off_xm, c.stream)
+    rc = sd ? apply_seeded(CD, c.x, *sd, M, K, ws + P.off_xm, nullptr, c.stream)
             : apply_mask(CD, c.x, c.drop_mask, M * K, ws + P.off_xm, c.stream);
     if (rc) return rc;
     lx = ws + P.off_xm;
@@ -666,10 +667,14 @@ int backward_gemm(const LayerCall& c, const Seeded* sd, const void* dy, const fl
   void* dtcd = ws + P.off_dtcd;
   float* part = (float*)(ws + P.off_part);
   int rc;
+  const bool dense_dx = dx && P.dense && dense256_ok(c, true);
+  // with a drawn mask the tiled dX GEMM adds the masked term itself, from the mask's bits (in place of the
+  // zero operand that the other GEMMs get)
+  const bool masked = sd && dense_dx && P.r_pad <= 64 && gemm16_ok(CD, M, K, N);
   // input of the low-rank branch: x, or x M with LoRA dropout
   const void* lx = c.x;
   if (c.drop_mask || sd) {
-    rc = sd ? apply_seeded(CD, c.x, *sd, M, K, ws + P.off_xm, c.stream)
+    rc = sd ? apply_seeded(CD, c.x, *sd, M, K, ws + P.off_xm, masked ? ws + P.off_zero : nullptr, c.stream)
             : apply_mask(CD, c.x, c.drop_mask, M * K, ws + P.off_xm, c.stream);
     if (rc) return rc;
     lx = ws + P.off_xm;
@@ -695,7 +700,6 @@ int backward_gemm(const LayerCall& c, const Seeded* sd, const void* dy, const fl
   void* t0t = ws + P.off_t0t;
   // A^T [K][r_pad] (zero past r) for the low-rank tail of the dense dX GEMM; its
   // transpose shares a launch with B^T's on the skinny path.
-  const bool dense_dx = dx && P.dense && dense256_ok(c, true);
   void* at = dense_dx ? (void*)(ws + P.off_at) : nullptr;
   TransposeSpec ta;
   ta.src = c.lora_a;
@@ -776,8 +780,6 @@ int backward_gemm(const LayerCall& c, const Seeded* sd, const void* dy, const fl
   // dX = dY W~ + dT A (the contraction runs over W's rows): W~^T written once and a
   // dense GEMM, or the fused dequant.  With LoRA dropout the GEMM gets a zero dT
   // (base product only) and the masked low-rank term is added afterwards.
-  // With a drawn mask the tiled GEMM adds that term itself.
-  const bool masked = sd && dense_dx && P.r_pad <= 64 && gemm16_ok(CD, M, K, N);
   const void* dt_gemm = dtcd;
   if (dx && (c.drop_mask || sd) && !masked) {
     if ((rc = zero_fill(ws + P.off_zero, M * P.r_pad * cd_bytes(CD), c.stream))) return rc;
@@ -786,7 +788,7 @@ int backward_gemm(const LayerCall& c, const Seeded* sd, const void* dy, const fl
   if (dense_dx) {
     void* wdt = ws + P.off_wdt;
     if ((rc = dequant_into(c.w, CD, wdt, true, c.stream, red_dt_pending ? &red_dt : nullptr))) return rc;
-    rc = masked ? gemm16_masked_dx(CD, dy, M, K, N, wdt, dtcd, P.r_pad, at, P.r_pad, *sd, dx, c.stream)
+    rc = masked ? gemm16_masked_dx(CD, dy, M, K, N, wdt, dtcd, P.r_pad, at, P.r_pad, ws + P.off_zero, K / 32, dx, c.stream)
                 : dense256_dx(c, dy, wdt, dt_gemm, P.r_pad, dx, P.dsp, ws + P.off_split, at);
     if (rc) return rc;
   } else if (dx && fast && fused256_ok(c, true)) {

@@ -1,7 +1,7 @@
 // gemm16.hip -- two 16-bit GEMMs that do more than a product on their way out (gfx950):
 //
 //   gated      h = act(g) u with [g | u] = [x | T] [W~ | B]^T (+ bias) of two projections
-//   masked dX  dX = dY W~ + (dT A) M with M drawn as the products run
+//   masked dX  dX = dY W~ + (dT A) M with M as bits
 //
 // Both stand on the contraction of tile.h.
 //
@@ -10,11 +10,11 @@
 // h is formed in registers.  The low-rank part is two more stages: T_g against B_g with zeros in the
 // up rows, then T_u against B_u with zeros in the gate rows.
 //
-// Masked: a lane's accumulators hold halves of the groups of eight columns that one counter of the
-// generator serves.  One counter's rounds run beside the products of each stage, one round to a
-// product (two 64-bit products, half the time of a matrix instruction, on the vector pipe that the
-// contraction leaves idle), and leave four mask bits for each group; the low-rank part is multiplied
-// after the last stage into sums of its own, masked and added.
+// Masked: the low-rank part is multiplied after the last stage into sums of its own, masked and added.
+// The mask comes as bits, which the launch that masks x for dA leaves behind at no cost of its own (it
+// waits for memory): drawn here, a counter beside the products of each stage, it cost 70 us of 500
+// (4096 tokens, 4096 x 14336) although the vector pipe stands idle there, as the products run at the
+// card's power limit.
 #include <algorithm>
 #include <type_traits>
 
@@ -38,7 +38,8 @@ struct G16 {
   void* out;           // [m][n] cd: h, or dX
   void* pre;           // [m][2 n] cd or null
   int64_t m, n, K;
-  Seeded sd;
+  const uint32_t* bits;  // [m][ldbits]: column k of the mask in bit k % 32 of word k / 32
+  int64_t ldbits;
 };
 
 struct Place {
@@ -59,7 +60,7 @@ constexpr int copying() { return T::TM == 256 && T::NS == 2 ? 4 : T::NW; }
 // logical chunk that lies there.  begin() sets up what a stage's copies read.
 template <class T, bool GATED>
 struct Copies16 {
-  static constexpr int NW = copying<T>(), PER_A = T::TM / 8 / NW, PER = (T::TM + T::TN) / 8 / NW, kSlots = 0;
+  static constexpr int NW = copying<T>(), PER_A = T::TM / 8 / NW, PER = (T::TM + T::TN) / 8 / NW;
   const G16& p;
   Place pl;
   int KM, KT, wave, lane, chunk;
@@ -122,60 +123,6 @@ struct Copies16 {
   }
   __device__ __forceinline__ void scales(int, int (&)[T::WMB], int&) const {}
   __device__ __forceinline__ void shift(int, int (&)[2][T::WMB], int (&)[2]) const {}
-  __device__ __forceinline__ void stage(int) const {}
-  __device__ __forceinline__ void slot(int) const {}
-};
-
-// The same with a counter of the mask beside each stage's products: counter u (of GROUPS) serves
-// rows 32 (u / (4 WNB)) + lane % 32 and columns 8 (u % (4 WNB)) .. + 7 of the wave's part, of
-// which this lane holds four.
-template <class T>
-struct Masked16 : Copies16<T, false> {
-  static constexpr int PER_ROW = 4 * T::WNB, GROUPS = T::WMB * PER_ROW, kSlots = GROUPS;
-  static_assert(4 * PER_ROW <= 32, "a row's bits are one word");
-  static_assert(4 * T::WMB * T::WNB >= kPhiloxRounds + 2, "a counter's rounds fit one stage");
-  PhiloxKey key;
-  uint32_t c[4], bits[T::WMB], row, group, threshold;
-  int now;
-  __device__ __forceinline__ Masked16(const G16& p, const Place& t, int wave, int lane)
-      : Copies16<T, false>(p, t, wave, lane), key(philox_key(p.sd)), threshold(p.sd.threshold) {
-    row = (uint32_t)(t.m0 + (wave / T::NWN) * 32 * T::WMB + (lane & 31));
-    group = (uint32_t)((t.n0 + (wave % T::NWN) * 32 * T::WNB) >> 3);
-#pragma unroll
-    for (int i = 0; i < T::WMB; ++i) bits[i] = 0;
-  }
-  __device__ __forceinline__ void start(int u) {
-    c[0] = group + (uint32_t)(u % PER_ROW);
-    c[1] = row + 32u * (uint32_t)(u / PER_ROW);
-    c[2] = key.o0;
-    c[3] = key.o1;
-  }
-  __device__ __forceinline__ void finish(int u) {
-    const bool h = this->lane >= 32;  // columns 4 h .. 4 h + 3: words 2 h and 2 h + 1
-    const uint32_t lo = h ? c[2] : c[0], hi = h ? c[3] : c[1];
-    uint32_t b = (lo & 0xffffu) >= threshold ? 1u : 0u;
-    b |= (lo >> 16) >= threshold ? 2u : 0u;
-    b |= (hi & 0xffffu) >= threshold ? 4u : 0u;
-    b |= (hi >> 16) >= threshold ? 8u : 0u;
-    b <<= 4 * (u % PER_ROW);
-#pragma unroll
-    for (int i = 0; i < T::WMB; ++i) bits[i] |= u / PER_ROW == i ? b : 0u;
-  }
-  __device__ __forceinline__ void stage(int u) { now = u; }
-  __device__ __forceinline__ void slot(int s) {
-    if (s == 0) start(now);
-    else if (s <= kPhiloxRounds) philox_round(key, s - 1, c);
-    else if (s == kPhiloxRounds + 1) finish(now);
-  }
-  // the counters that had no stage
-  __device__ __forceinline__ void rest() {
-    for (int u = this->KM; u < GROUPS; ++u) {
-      start(u);
-#pragma unroll
-      for (int i = 0; i < kPhiloxRounds; ++i) philox_round(key, i, c);
-      finish(u);
-    }
-  }
 };
 
 // 16-byte chunks of `rows` rows of RB bytes in W (chunk c of row r at chunk c ^ (r % NC)) to columns
@@ -262,9 +209,17 @@ __device__ __forceinline__ void write_gated(const G16& p, const Place& pl, Acc<T
 
 // dX of a wave's blocks: the masked low-rank sums (operands in LDS at `st`, as a stage) added.
 template <int CD, class T>
-__device__ __forceinline__ void add_masked(Acc<T>& acc, const Masked16<T>& cp, const char* st, int wave, int lane) {
+__device__ __forceinline__ void add_masked(Acc<T>& acc, const G16& p, const Place& pl, const char* st, int wave, int lane) {
   const int h = lane >> 5, r32 = lane & 31, xr = swz(r32);
   const int wm = (wave / T::NWN) * 32 * T::WMB, wn = (wave % T::NWN) * 32 * T::WNB;
+  uint32_t bits[T::WMB][T::WNB];
+  const rsrc_t rm = make_rsrc(p.bits + pl.m0 * p.ldbits, pl.rows * p.ldbits * 4);
+#pragma unroll
+  for (int i = 0; i < T::WMB; ++i)
+#pragma unroll
+    for (int j = 0; j < T::WNB; ++j)
+      bits[i][j] = __builtin_amdgcn_raw_buffer_load_b32(rm, ((wm + 32 * i + r32) * (int)p.ldbits + (int)((pl.n0 + wn) >> 5) + j) * 4,
+                                                        0, 0) >> (4 * h);
   const char *a = st + (wm + r32) * 128, *b = st + (T::TM + wn + r32) * 128;
 #pragma unroll
   for (int i = 0; i < T::WMB; ++i)
@@ -280,7 +235,10 @@ __device__ __forceinline__ void add_masked(Acc<T>& acc, const Masked16<T>& cp, c
       for (int q = 0; q < 4; ++q)
 #pragma unroll
         for (int v = 0; v < 4; ++v)
-          acc[i][j][4 * q + v] += cp.bits[i] >> (4 * (4 * j + q) + v) & 1u ? low[4 * q + v] : 0.f;
+          acc[i][j][4 * q + v] += bits[i][j] >> (8 * q + v) & 1u ? low[4 * q + v] : 0.f;
+      // one block's operands at a time: the sums leave room for no more
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("" ::: "memory");
     }
 }
 template <int CD, class T>
@@ -367,25 +325,28 @@ __global__ __launch_bounds__(64 * T::NW, WGS) void k_gemm16(G16 p, int act) {
     const float c = GATED && nxt.rows && tid < COEF ? coef_of(nxt, tid) : 0.f;
     auto work = [&](auto shape) {
       using U = decltype(shape);
-      using Copier = std::conditional_t<GATED, Copies16<U, GATED>, Masked16<U>>;
-      Copier cp(p, cur, wave, lane);
+      // the lane counts as unknown here and after the contraction: addresses of either shape and of the
+      // outputs, formed ahead of all tiles, would be kept through the contraction and pushed out to memory
+      int ln = lane;
+      asm volatile("" : "+v"(ln));
+      Copies16<U, GATED> cp(p, cur, wave, ln);
       Acc<U> acc;
       zero<U>(acc);
       if constexpr (copying<U>() < U::NW) {
         wait_lgkm0();
         barrier_only();  // the coefficients are there, the staging of the tile before is free
-        contract_two<U, Half16<CD>>(acc, lds, cp, wave, lane);
+        contract_two<U, Half16<CD>>(acc, lds, cp, wave, ln);
       } else {
         wait_vmcnt<0>();
         wait_lgkm0();
         barrier_only();  // and stage 0
 #pragma unroll
         for (int s = 1; s < U::NS; ++s) cp.all(lds + s * U::STAGE, s);
-        contract<U, Half16<CD>>(acc, lds, cp, wave, lane);
+        contract<U, Half16<CD>>(acc, lds, cp, wave, ln);
       }
+      asm volatile("" : "+v"(ln));
       if constexpr (!GATED) {
-        cp.rest();
-        add_masked<CD, U>(acc, cp, lds + cp.KM % U::NS * U::STAGE, wave, lane);
+        add_masked<CD, U>(acc, p, cur, lds + cp.KM % U::NS * U::STAGE, wave, ln);
         __syncthreads();  // every wave is past the low-rank operands
       }
       if (nxt.rows) {
@@ -395,11 +356,11 @@ __global__ __launch_bounds__(64 * T::NW, WGS) void k_gemm16(G16 p, int act) {
       char* W = lds + T::STAGE + wave * STAGING;
       if constexpr (GATED) {
         const float* co = coefs + set * COEF;
-        if (act == QLORA_ACT_SILU) write_gated<CD, QLORA_ACT_SILU, U>(p, cur, acc, co, W, wave, lane);
-        else if (act == QLORA_ACT_GELU) write_gated<CD, QLORA_ACT_GELU, U>(p, cur, acc, co, W, wave, lane);
-        else write_gated<CD, QLORA_ACT_GELU_TANH, U>(p, cur, acc, co, W, wave, lane);
+        if (act == QLORA_ACT_SILU) write_gated<CD, QLORA_ACT_SILU, U>(p, cur, acc, co, W, wave, ln);
+        else if (act == QLORA_ACT_GELU) write_gated<CD, QLORA_ACT_GELU, U>(p, cur, acc, co, W, wave, ln);
+        else write_gated<CD, QLORA_ACT_GELU_TANH, U>(p, cur, acc, co, W, wave, ln);
       } else {
-        write_plain<CD, U>(p, cur, acc, W, wave, lane);
+        write_plain<CD, U>(p, cur, acc, W, wave, ln);
       }
     };
     if (HALVES && cur.rows <= H::TM) work(H{});
@@ -470,9 +431,10 @@ int gemm16_gated(int cd, const void* x, int64_t m, int64_t n, int64_t K, const v
   return cd == CD_BF16 ? run_cd<CD_BF16, true>(p, act, QLORA_K_FWD_GEMM, s) : run_cd<CD_F16, true>(p, act, QLORA_K_FWD_GEMM, s);
 }
 
-// dX [m][n] = dY [m][K] W~^T wt [n][K] + (dT [m][ldt] A^T at [n][lda]) M, ldt and lda multiples of 8, at most 64.
+// dX [m][n] = dY [m][K] W~^T wt [n][K] + (dT [m][ldt] A^T at [n][lda]) M, ldt and lda multiples of 8, at most 64;
+// bits [m][ldbits] words of M's bits.
 int gemm16_masked_dx(int cd, const void* dy, int64_t m, int64_t n, int64_t K, const void* wt, const void* dt, int64_t ldt,
-                     const void* at, int64_t lda, const Seeded& sd, void* dx, hipStream_t s) {
+                     const void* at, int64_t lda, const void* bits, int64_t ldbits, void* dx, hipStream_t s) {
   G16 p = {};
   p.x = dy;
   p.w0 = wt;
@@ -484,7 +446,8 @@ int gemm16_masked_dx(int cd, const void* dy, int64_t m, int64_t n, int64_t K, co
   p.m = m;
   p.n = n;
   p.K = K;
-  p.sd = sd;
+  p.bits = (const uint32_t*)bits;
+  p.ldbits = ldbits;
   return cd == CD_BF16 ? run_cd<CD_BF16, false>(p, 0, QLORA_K_BWD_DX, s) : run_cd<CD_F16, false>(p, 0, QLORA_K_BWD_DX, s);
 }
 

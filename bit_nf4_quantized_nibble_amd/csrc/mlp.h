@@ -30,7 +30,8 @@ inline void gradient_jobs(SkRed& ra, SkRed& rb, float scale, void* d_a, void* d_
     rb.ldcd = rb.R;
   }
 }
-int apply_seeded(int cd, const void* x, const Seeded& sd, int64_t rows, int64_t cols, void* out, hipStream_t s);
+// out = x M, and (bits not null, cols a multiple of 32) M's bits, rows of cols / 32 words.
+int apply_seeded(int cd, const void* x, const Seeded& sd, int64_t rows, int64_t cols, void* out, void* bits, hipStream_t s);
 int rank_add_seeded(int cd, void* dx, const Seeded& sd, const void* dt, int64_t ld_dt, const void* a, int32_t r, int64_t M,
                     int64_t K, hipStream_t s);
 
@@ -47,7 +48,7 @@ bool gemm16_ok(int cd, int64_t m, int64_t n, int64_t K);
 int gemm16_gated(int cd, const void* x, int64_t m, int64_t n, int64_t K, const void* const* w, const void* t,
                  const void* const* b, const int64_t* ldb, const void* bias, int act, void* h, void* pre, hipStream_t s);
 int gemm16_masked_dx(int cd, const void* dy, int64_t m, int64_t n, int64_t K, const void* wt, const void* dt, int64_t ldt,
-                     const void* at, int64_t lda, const Seeded& sd, void* dx, hipStream_t s);
+                     const void* at, int64_t lda, const void* bits, int64_t ldbits, void* dx, hipStream_t s);
 
 // planes.hip: the seeded layer (g = 1) and the gated block (g = 2) in every layout and type.
 struct PlanesFwd {

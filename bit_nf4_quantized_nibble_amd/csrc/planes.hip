@@ -83,6 +83,8 @@ struct Pack {
   const void* dh = nullptr;  // SRC_GATE, SRC_UP: p is pre [rows][2 cols], dh [rows][cols]
   int64_t rows = 0, cols = 0;
   bool drawn = false;  // under the drawn mask
+  uint8_t* bits = nullptr;  // its bits, rows of wbits bytes
+  int64_t wbits = 0;
   Planes rowwise;      // [rows][wide]
   int64_t wide = 0;
   Planes across;       // [cols][tall], the transpose
@@ -255,6 +257,12 @@ __global__ __launch_bounds__(kThreads) void k_pack(Packs ps) {
       const u32x4_t w = philox(philox_key(ps.sd), (uint32_t)(k >> 3), (uint32_t)row[h]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[h][e] = keeps(w, e, ps.sd.threshold) ? v[h][e] : 0.f;
+      if (j.bits) {
+        uint32_t b = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) b |= keeps(w, e, ps.sd.threshold) ? 1u << e : 0u;
+        j.bits[row[h] * j.wbits + (k >> 3)] = (uint8_t)b;
+      }
     }
     u32x4_t o[MAX];
 #pragma unroll
@@ -327,7 +335,7 @@ struct Prods {
 
 template <class T>
 struct CopiesP {
-  static constexpr int NW = T::NW, kSlots = 0;
+  static constexpr int NW = T::NW;
   const Prod& p;
   int KT, left, g, k, q, lane;
   int64_t m0, n0, rows, cols;
@@ -391,8 +399,6 @@ struct CopiesP {
   }
   __device__ __forceinline__ void scales(int, int (&)[T::WMB], int&) const {}
   __device__ __forceinline__ void shift(int, int (&)[2][T::WMB], int (&)[2]) const {}
-  __device__ __forceinline__ void stage(int) const {}
-  __device__ __forceinline__ void slot(int) const {}
 };
 
 // A workgroup forms one tile of one slice of one product.
@@ -1173,7 +1179,7 @@ int backward(const PlanesBwd& q, char* ws, int64_t* need) {
   run.s = c0.stream;
   const bool decode = q.dx && decodable(q.c, q.g);
   const bool direct = q.dx && !decode && Run<CD>::low_tiles(m, K) >= kDirectTiles;
-  // the masked GEMM draws the mask beside its products
+  // the masked GEMM adds the low-rank part itself
   const bool fused = direct && q.sd && CD != CD_F32 && c0.r <= 64 && gemm16_ok(CD, m, K, round_up(n, 64));
   const bool whole = direct && !q.sd;  // dX leaves from one product
   const bool saved = q.t_saved != nullptr;
@@ -1205,6 +1211,10 @@ int backward(const PlanesBwd& q, char* ws, int64_t* need) {
   }
   Pack& jx = run.pack(SRC_CD, c0.x, m, K);
   jx.drawn = q.sd != nullptr;
+  if (fused) {
+    jx.wbits = round_up(K, 32) / 8;
+    jx.bits = (uint8_t*)run.take(m * jx.wbits);
+  }
   const Planes xt = run.across(jx);
   if (!saved) xm = Run<CD>::kPlanes == 1 && K % 64 == 0 && !q.sd ? run.as_is(c0.x, K) : run.rowwise(jx);
   run.run_packs(q.c, q.g, q.sd, q.act);
@@ -1302,7 +1312,8 @@ int backward(const PlanesBwd& q, char* ws, int64_t* need) {
   run.run_joins(q.sd, 0);
   if (need) *need = run.used;
   if (run.dry() || run.rc || !fused) return run.rc;
-  return gemm16_masked_dx(CD, d[0].p, m, K, d[0].ld, wt[0].p, dtr[0].p, dtr[0].ld, at[0].p, at[0].ld, *q.sd, q.dx,
+  return gemm16_masked_dx(CD, d[0].p, m, K, d[0].ld, wt[0].p, dtr[0].p, dtr[0].ld, at[0].p, at[0].ld, jx.bits,
+                          jx.wbits / 4, q.dx,
                           c0.stream);
 }
 

@@ -146,9 +146,8 @@ __device__ __forceinline__ void zero(Acc<T>& acc) {
 // last stage it brings zeros or nothing anyone reads); cp.begin(stage) is called when a stage's
 // copies begin, cp.scales(stage, ..) when its first fragments are read and cp.shift(stage, ..) once the
 // stage before is done (what scales() has read becomes the scales in use: no product waits for the
-// read).  In the first C::kSlots stages cp.stage(stage) begins a stage and cp.slot(s) runs beside its
-// product s (what it does hides behind the matrix pipe).  On entry stage 0 lies in LDS for every wave and the copies of stages
-// 1 .. NS - 1 are requested; on return the LDS is free.
+// read).  On entry stage 0 lies in LDS for every wave and the copies of stages 1 .. NS - 1 are requested;
+// on return the LDS is free.
 template <class T, class KIND, class C>
 __device__ __forceinline__ void contract(Acc<T>& acc, char* lds, C& cp, int wave, int lane) {
   constexpr int WMB = T::WMB, WNB = T::WNB, NMF = WMB * WNB, SUB = KIND::SUB, SETS = KIND::SETS;
@@ -170,78 +169,74 @@ __device__ __forceinline__ void contract(Acc<T>& acc, char* lds, C& cp, int wave
   for (int t = 0; t < WMB + WNB; ++t) frag(0, lds, 0, t);
   cp.scales(0, sa[1], sb[1]);
   cp.shift(0, sa, sb);
-  int buf = 0, u = 0;
-  auto run = [&](auto slots, int end) {
-    for (; u < end; ++u) {
-      char* st = lds + buf * T::STAGE;
-      const int nbuf = buf + 1 == T::NS ? 0 : buf + 1;
-      const char* nx = lds + nbuf * T::STAGE;
-      if (slots) cp.stage(u);
-      __builtin_amdgcn_sched_barrier(0);
+  int buf = 0;
+  for (int u = 0; u < cp.KT; ++u) {
+    char* st = lds + buf * T::STAGE;
+    const int nbuf = buf + 1 == T::NS ? 0 : buf + 1;
+    const char* nx = lds + nbuf * T::STAGE;
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int ks = 0; ks < SUB; ++ks) {
-        const int set = SETS == 2 ? ks & 1 : 0, next = SETS == 2 ? set ^ 1 : 0;
-        const bool last = ks == SUB - 1;
-        const char* from = last ? nx : st;
-        const int nks = last ? 0 : ks + 1;
+    for (int ks = 0; ks < SUB; ++ks) {
+      const int set = SETS == 2 ? ks & 1 : 0, next = SETS == 2 ? set ^ 1 : 0;
+      const bool last = ks == SUB - 1;
+      const char* from = last ? nx : st;
+      const int nks = last ? 0 : ks + 1;
 #pragma unroll
-        for (int t = 0; t < NMF; ++t) {
-          if (last && t == BAR) {
-            wait_lgkm0();
-            wait_vmcnt<(T::NS - 2) * T::PER>();  // this wave's copies of stage u + 1
-            barrier_only();
-            cp.begin(u + T::NS);
-          }
-          const int i = t % WMB, j = t / WMB;
-          KIND::mma(acc[i][j], fb[set][j], fa[set][i], sb[0], sa[0][i]);
-          if (slots) cp.slot(ks * NMF + t);
-          if constexpr (SETS == 2) {
-#pragma unroll
-            for (int q = 0; q < WMB + WNB; ++q)
-              if (q * NMF / (WMB + WNB) == t) frag(next, from, nks, q);
-          } else {
-            if (i == WMB - 1) frag(0, from, nks, j);
-            if (j == WNB - 1) frag(0, from, nks, WNB + i);
-          }
-          if (last && t >= BAR) {
-            if (t == BAR) cp.scales(u + 1, sa[1], sb[1]);
-#pragma unroll
-            for (int q = 0; q < T::PER; ++q)
-              if (BAR + q * (NMF - BAR) / T::PER == t) cp.one(st, u + T::NS, q);
-          }
-          __builtin_amdgcn_sched_barrier(0);
+      for (int t = 0; t < NMF; ++t) {
+        if (last && t == BAR) {
+          wait_lgkm0();
+          wait_vmcnt<(T::NS - 2) * T::PER>();  // this wave's copies of stage u + 1
+          barrier_only();
+          cp.begin(u + T::NS);
         }
+        const int i = t % WMB, j = t / WMB;
+        KIND::mma(acc[i][j], fb[set][j], fa[set][i], sb[0], sa[0][i]);
+        if constexpr (SETS == 2) {
+#pragma unroll
+          for (int q = 0; q < WMB + WNB; ++q)
+            if (q * NMF / (WMB + WNB) == t) frag(next, from, nks, q);
+        } else {
+          if (i == WMB - 1) frag(0, from, nks, j);
+          if (j == WNB - 1) frag(0, from, nks, WNB + i);
+        }
+        if (last && t >= BAR) {
+          if (t == BAR) cp.scales(u + 1, sa[1], sb[1]);
+#pragma unroll
+          for (int q = 0; q < T::PER; ++q)
+            if (BAR + q * (NMF - BAR) / T::PER == t) cp.one(st, u + T::NS, q);
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
-      cp.shift(u + 1, sa, sb);
-      buf = nbuf;
     }
-  };
-  if constexpr (C::kSlots > 0) run(std::true_type{}, min(cp.KT, C::kSlots));
-  run(std::false_type{}, cp.KT);
+    cp.shift(u + 1, sa, sb);
+    buf = nbuf;
+  }
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();  // every copy has ended and every wave is past its reads
 }
 
 // The same for the largest 16-bit tile, two buffers, eight waves of which the first four (one to a
-// SIMD) copy: stage u + 1's A rows beside the first sub-step's products and its W-side rows beside the
-// second's, one copy to a product; one barrier per stage, at its start.  cp counts copies by four
-// waves.  SLOTS: cp.slot() runs beside the products.
-template <class T, class KIND, bool COPY, bool SLOTS, class C>
-__device__ __forceinline__ void stage_two(Acc<T>& acc, char* lds, int u, C& cp, int arow, int brow, int xr, int h) {
-  constexpr int WMB = T::WMB, WNB = T::WNB, NMF = WMB * WNB;
+// SIMD) copy, one copy to a product.  One barrier per stage, in its last sub-step: there the next stage
+// has landed and every wave holds its last fragments of this one, so that the first fragments of the next
+// stage are read beside the last products, and this buffer takes the copies of the stage after it, from
+// there into the second sub-step of the next stage.  cp counts copies by four waves.
+template <class T, class KIND>
+struct Frags {
+  typename KIND::frag_t a[2][T::WMB], b[2][T::WNB];
+  int arow, brow, xr, h;
+  // fragment t in the order of first use: b0 a0, the other b's, the other a's
+  __device__ __forceinline__ void read(int set, const char* st, int ks, int t) {
+    const int i = t == 0 ? 0 : t >= 2 && t <= T::WNB ? t - 1 : -1, j = t == 1 ? 0 : t - T::WNB;
+    if (i >= 0) b[set][i] = KIND::read(st + brow + i * 32 * 128, ks, h, xr);
+    else a[set][j] = KIND::read(st + arow + j * 32 * 128, ks, h, xr);
+  }
+};
+constexpr int kBarrierAt = 2;  // products of the last sub-step before the barrier
+template <class T, class KIND, bool COPY, class C>
+__device__ __forceinline__ void stage_two(Acc<T>& acc, char* lds, int u, C& cp, Frags<T, KIND>& f) {
+  constexpr int WMB = T::WMB, WNB = T::WNB, NMF = WMB * WNB, EARLY = NMF - kBarrierAt;
   static_assert(T::NS == 2 && T::TM == 256 && T::TN == 256 && NMF == 8 && KIND::SUB == 4, "the largest tile");
   char *st = lds + (u & 1) * T::STAGE, *nx = lds + ((u & 1) ^ 1) * T::STAGE;
-  typename KIND::frag_t fa[2][WMB], fb[2][WNB];
-  // fragment t in the order of first use: b0 a0, the other b's, the other a's
-  auto frag = [&](int set, int ks, int t) {
-    const int b = t == 0 ? 0 : t >= 2 && t <= WNB ? t - 1 : -1, a = t == 1 ? 0 : t - WNB;
-    if (b >= 0) fb[set][b] = KIND::read(st + brow + b * 32 * 128, ks, h, xr);
-    else fa[set][a] = KIND::read(st + arow + a * 32 * 128, ks, h, xr);
-  };
-#pragma unroll
-  for (int t = 0; t < 6; ++t) frag(0, 0, t);
-  if (COPY) cp.begin(u + 1);
-  if (SLOTS) cp.stage(u);
   __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
   for (int ks = 0; ks < 4; ++ks) {
@@ -249,41 +244,47 @@ __device__ __forceinline__ void stage_two(Acc<T>& acc, char* lds, int u, C& cp, 
 #pragma unroll
     for (int t = 0; t < NMF; ++t) {
       const int i = t / WNB, j = t % WNB;
-      KIND::mma(acc[i][j], fb[set][j], fa[set][i], 0, 0);
-      if (SLOTS) cp.slot(ks * NMF + t);
-      if (ks < 3) {
-#pragma unroll
-        for (int q = 0; q < 6; ++q)
-          if (q * NMF / 6 == t) frag(set ^ 1, ks + 1, q);
+      if (ks == 3 && t == kBarrierAt) {
+        __builtin_amdgcn_s_waitcnt(0);  // this wave's copies of stage u + 1 and its reads of this one
+        barrier_only();
+        if (COPY) cp.begin(u + 2);
       }
-      if (COPY && ks < 2) cp.one(nx, u + 1, 8 * ks + t);
+      KIND::mma(acc[i][j], f.b[set][j], f.a[set][i], 0, 0);
+#pragma unroll
+      for (int q = 0; q < WMB + WNB; ++q) {
+        if (ks < 3 && q * NMF / (WMB + WNB) == t) f.read(set ^ 1, st, ks + 1, q);
+        if (ks == 3 && kBarrierAt + q * EARLY / (WMB + WNB) == t) f.read(0, nx, 0, q);
+      }
+      if (COPY && ks == 3 && t >= kBarrierAt) cp.one(st, u + 2, t - kBarrierAt);
+      if (COPY && 8 * ks + t < 16 - EARLY) cp.one(nx, u + 1, EARLY + 8 * ks + t);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
 }
 template <class T, class KIND, bool COPY, class C>
-__device__ __forceinline__ void stages_two(Acc<T>& acc, char* lds, C& cp, int arow, int brow, int xr, int h) {
-  int u = 0;
-  if constexpr (C::kSlots > 0)
-    for (; u < min(cp.KT, C::kSlots); ++u) {
-      __builtin_amdgcn_s_waitcnt(0);  // this wave's copies of stage u and its fragment reads
-      barrier_only();
-      stage_two<T, KIND, COPY, true>(acc, lds, u, cp, arow, brow, xr, h);
-    }
-  for (; u < cp.KT; ++u) {
-    __builtin_amdgcn_s_waitcnt(0);
-    barrier_only();
-    stage_two<T, KIND, COPY, false>(acc, lds, u, cp, arow, brow, xr, h);
+__device__ __forceinline__ void stages_two(Acc<T>& acc, char* lds, C& cp, Frags<T, KIND>& f) {
+  __builtin_amdgcn_s_waitcnt(0);  // this wave's copies of stage 0
+  barrier_only();
+  if (COPY) {
+    cp.begin(1);
+#pragma unroll
+    for (int i = 0; i < T::WMB * T::WNB - kBarrierAt; ++i) cp.one(lds + T::STAGE, 1, i);
   }
+#pragma unroll
+  for (int t = 0; t < T::WMB + T::WNB; ++t) f.read(0, lds, 0, t);
+  for (int u = 0; u < cp.KT; ++u) stage_two<T, KIND, COPY>(acc, lds, u, cp, f);
 }
 // On entry the copying waves have requested stage 0; on return the LDS is free.
 template <class T, class KIND, class C>
 __device__ __forceinline__ void contract_two(Acc<T>& acc, char* lds, C& cp, int wave, int lane) {
-  const int r32 = lane & 31, h = lane >> 5, xr = swz(r32);
-  const int arow = ((wave / T::NWN) * 32 * T::WMB + r32) * 128;
-  const int brow = (T::TM + (wave % T::NWN) * 32 * T::WNB + r32) * 128;
-  if (wave < 4) stages_two<T, KIND, true>(acc, lds, cp, arow, brow, xr, h);
-  else stages_two<T, KIND, false>(acc, lds, cp, arow, brow, xr, h);
+  const int r32 = lane & 31;
+  Frags<T, KIND> f;
+  f.h = lane >> 5;
+  f.xr = swz(r32);
+  f.arow = ((wave / T::NWN) * 32 * T::WMB + r32) * 128;
+  f.brow = (T::TM + (wave % T::NWN) * 32 * T::WNB + r32) * 128;
+  if (wave < 4) stages_two<T, KIND, true>(acc, lds, cp, f);
+  else stages_two<T, KIND, false>(acc, lds, cp, f);
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
 }
