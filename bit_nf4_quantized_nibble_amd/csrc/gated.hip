@@ -250,7 +250,7 @@ int launch_gated_bwd(const GroupCall& gc, int act, const void* dh, const void* p
     return planes_backward(q, ws, nullptr);
   }
   const int rc = gate(c.cd, act, pre, dh, c.m, c.w.rows, ws, s);
-  return rc ? rc : launch_backward_group_as(gc, ws, t_saved, dx, d_a, d_b, gd,
+  return rc ? rc : launch_backward_group_as(gc, ws, t_saved, dx, d_a, d_b, gd, true,
                                             (char*)ws + al(c.m * gc.N * cd_bytes(c.cd)), s);
 }
 

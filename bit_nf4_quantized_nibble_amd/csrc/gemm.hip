@@ -590,10 +590,22 @@ int lora_down(const LayerCall& c, const void* lx, const Split& sp, float* part, 
   return run_reduce<CD>(part, sp, c.m, c.r, sc32, out32, sccd, outcd, r_pad, c.stream);
 }
 
+// Whether a seeded forward writes W~ and multiplies by gemm16_plain (bf16: 512 tokens of 4096 x 4096 45 us
+// against the fused kernel's 56, 1024 tokens 61 against 77, 4096 tokens of 14336 x 4096 417 against the
+// dense GEMM's 439); up to 768 tokens of larger weights the fused kernel's cut of the contraction wins (512 tokens
+// of 4096 x 14336 103 against 124, 256 of 14336 x 4096 68 against 72).
+bool seeded_g16(const LayerCall& c) {
+  if (c.m <= kFusedFwdMaxM && c.w.rows * c.w.cols >= 1 << 25) return false;
+  return fast_layout(c.w) && c.r % 8 == 0 && skinny_ok(c.cd, c.r) && gemm16_ok(c.cd, c.m, c.w.rows, c.w.cols) &&
+         dense256_ok(c, false) && !(c.flags & QLORA_FLAG_FUSED);
+}
+
 template <int CD>
 int forward_gemm(const LayerCall& c, const Seeded* sd, void* y, float* t_save) {
   const int64_t M = c.m, N = c.w.rows, K = c.w.cols;
-  FwdPlan P = plan_fwd(M, N, K, c.r, CD, c.flags);
+  // the seeded forward's tuned way writes W~ and multiplies by gemm16_plain, whatever the tokens
+  const bool g16 = sd && seeded_g16(c);
+  FwdPlan P = plan_fwd(M, N, K, c.r, CD, c.flags | (g16 ? QLORA_FLAG_DEQUANT_GEMM : 0));
   char* ws = (char*)c.ws;
   void* tcd = ws + P.off_tcd;
   float* part = (float*)(ws + P.off_part);
@@ -632,6 +644,8 @@ int forward_gemm(const LayerCall& c, const Seeded* sd, void* y, float* t_save) {
   if (dense) {
     void* wd = ws + P.off_wd;
     if ((rc = dequant_into(c.w, CD, wd, false, c.stream, red_pending ? &red : nullptr))) return rc;
+    if (g16)
+      return gemm16_plain(CD, c.x, M, N, K, wd, tcd, P.r_pad, c.lora_b, c.r, c.bias, y, QLORA_K_FWD_GEMM, c.stream);
     return dense256_forward(c, wd, tcd, P.r_pad, y, P.dsp, ws + P.off_split);
   }
   if (fast && fused256_ok(c, false)) return fused256_forward(c, tcd, P.r_pad, y, P.dsp, ws + P.off_split);
@@ -988,7 +1002,9 @@ size_t fwd_workspace_bytes(int64_t m, int64_t rows, int64_t cols, int32_t r, int
   // the query does not see the block size): room for both.  At most 16 tokens the
   // GEMM path is the generic engine, which needs only T and the rank-product partial
   // sums (the start of its plan).
-  const FwdPlan P = plan_fwd(m, rows, cols, r, cd, flags);
+  FwdPlan P = plan_fwd(m, rows, cols, r, cd, flags);
+  if (flags & QLORA_FLAG_DROPOUT && !(flags & QLORA_FLAG_FUSED))  // the seeded call's
+    P.total = std::max(P.total, plan_fwd(m, rows, cols, r, cd, flags | QLORA_FLAG_DEQUANT_GEMM).total);
   if (!gemv_candidate(m, flags))
     return (size_t)std::max(P.total, planes_seeded_bytes(QLORA_OP_FWD, m, rows, cols, r, cd, flags));
   return std::max(gemv_workspace_bytes(m, rows, cols, r, cd), (size_t)(m <= kGemvMaxM ? P.off_wd : P.total));

@@ -1,9 +1,10 @@
-// gemm16.hip -- two 16-bit GEMMs that do more than a product on their way out (gfx950):
+// gemm16.hip -- 16-bit GEMMs with a low-rank part (gfx950):
 //
+//   plain      y = [x | T] [W~ | B]^T (+ bias)
 //   gated      h = act(g) u with [g | u] = [x | T] [W~ | B]^T (+ bias) of two projections
 //   masked dX  dX = dY W~ + (dT A) M with M as bits
 //
-// Both stand on the contraction of tile.h.
+// All stand on the contraction of tile.h; the low-rank part is one or more stages behind the last.
 //
 // Gated: a tile's 2 C columns are C columns of the gate and the same C of the up projection, in runs
 // of 32 that alternate, so that a wave's two blocks of columns are g and u of the same 32 columns and
@@ -30,17 +31,19 @@ using namespace tile;
 struct G16 {
   const void* x;       // [m][K] cd: x, or dY
   const void *w0, *w1; // [n][K] cd: W~ of the gate and of the up projection, or W~^T and null
-  const void* t;       // [m][ldt] cd: T_g in columns 0 .., T_u in columns 64 .., or dT
+  const void* t;       // [m][ldt] cd: T_g in columns 0 .., T_u in columns 64 .., or T or dT
   int64_t ldt;
-  const void *l0, *l1; // [n][ld_l] cd: lora_b of the two, or A^T and null
+  const void *l0, *l1; // [n][ld_l] cd: lora_b of the two, or lora_b or A^T and null
   int64_t ldl0, ldl1;  // multiples of 8; columns from there on count as zeros
-  const void* bias;    // [2 n] cd or null
-  void* out;           // [m][n] cd: h, or dX
+  const void* bias;    // [2 n] (gated) or [n] (plain) cd or null
+  void* out;           // [m][n] cd: h, y or dX
   void* pre;           // [m][2 n] cd or null
   int64_t m, n, K;
   const uint32_t* bits;  // [m][ldbits]: column k of the mask in bit k % 32 of word k / 32
   int64_t ldbits;
 };
+
+enum Mode { PLAIN, GATED, MASKED };
 
 struct Place {
   int rows;
@@ -48,8 +51,8 @@ struct Place {
 };
 
 // Columns of the output that a tile forms.
-template <class T, bool GATED>
-constexpr int cols_of() { return GATED ? T::TN / 2 : T::TN; }
+template <class T, int MODE>
+constexpr int cols_of() { return MODE == GATED ? T::TN / 2 : T::TN; }
 
 // Waves that copy: four of the largest tile's eight (contract_two), else all.
 template <class T>
@@ -58,7 +61,7 @@ constexpr int copying() { return T::TM == 256 && T::NS == 2 ? 4 : T::NW; }
 // The copies of a tile's stages by one wave: instruction i of copying wave w fills LDS rows
 // 8 (w + NW i) .. + 7 of the stage; lane l lands in chunk l % 8 of row l / 8 and fetches the
 // logical chunk that lies there.  begin() sets up what a stage's copies read.
-template <class T, bool GATED>
+template <class T, int MODE>
 struct Copies16 {
   static constexpr int NW = copying<T>(), PER_A = T::TM / 8 / NW, PER = (T::TM + T::TN) / 8 / NW;
   const G16& p;
@@ -70,22 +73,22 @@ struct Copies16 {
   __device__ __forceinline__ Copies16(const G16& p_, const Place& t, int wave_, int lane_)
       : p(p_), pl(t), wave(wave_), lane(lane_) {
     KM = (int)(p.K >> 6);
-    KT = KM + (GATED ? 2 : 0);
+    KT = KM + (MODE == GATED ? 2 : MODE == PLAIN ? (int)((p.ldt + 63) >> 6) : 0);
     chunk = (lane & 7) ^ swz(8 * wave + (lane >> 3));
-    ncols = min((int64_t)cols_of<T, GATED>(), p.n - t.n0);
+    ncols = min((int64_t)cols_of<T, MODE>(), p.n - t.n0);
   }
   // row of the W-side operand (within its tile) of this lane in copy 0, and the operand of copy i
-  __device__ __forceinline__ int brow() const { return (GATED ? 8 * (wave & 3) : 8 * wave) + (lane >> 3); }
-  __device__ __forceinline__ int side(int i) const { return !GATED ? 0 : NW == 8 ? wave >> 2 : i & 1; }
-  static constexpr int bstep() { return GATED ? 32 : 8 * NW; }
-  static constexpr int bindex(int i) { return GATED && NW == 4 ? i >> 1 : i; }
+  __device__ __forceinline__ int brow() const { return (MODE == GATED ? 8 * (wave & 3) : 8 * wave) + (lane >> 3); }
+  __device__ __forceinline__ int side(int i) const { return MODE != GATED ? 0 : NW == 8 ? wave >> 2 : i & 1; }
+  static constexpr int bstep() { return MODE == GATED ? 32 : 8 * NW; }
+  static constexpr int bindex(int i) { return MODE == GATED && NW == 4 ? i >> 1 : i; }
   __device__ __forceinline__ void begin(int stage) {
     const int arow = 8 * wave + (lane >> 3);
     if (stage < KM) {
       const uint32_t k2 = (uint32_t)p.K * 2;
       ra = make_rsrc((const char*)p.x + pl.m0 * p.K * 2, (int64_t)pl.rows * k2);
       rb[0] = make_rsrc((const char*)p.w0 + pl.n0 * p.K * 2, ncols * k2);
-      if (GATED) rb[1] = make_rsrc((const char*)p.w1 + pl.n0 * p.K * 2, ncols * k2);
+      if (MODE == GATED) rb[1] = make_rsrc((const char*)p.w1 + pl.n0 * p.K * 2, ncols * k2);
       oa = arow * k2 + 16 * chunk;
       ob = brow() * k2 + 16 * chunk;
       sa = 8 * NW * k2;
@@ -93,17 +96,18 @@ struct Copies16 {
       so = (uint32_t)stage * 128;
     } else {
       // the low-rank part, or (past it) empty buffers: nothing is fetched
-      const int u = stage - KM;
-      const bool in = u < (GATED ? 2 : 1);
-      const int64_t ldl = u ? p.ldl1 : p.ldl0;
+      const int u = stage - KM, at = MODE == PLAIN ? 64 * u : 0;  // first column of the W-side operand
+      const bool in = u < (MODE == GATED ? 2 : MODE == PLAIN ? KT - KM : 1);
+      const int64_t ldl = MODE == GATED && u ? p.ldl1 : p.ldl0;
       ra = make_rsrc((const char*)p.t + (pl.m0 * p.ldt + 64 * u) * 2, in ? (pl.rows * p.ldt - 64 * u) * 2 : 0);
-      const void* l = u ? p.l1 : p.l0;
-      const rsrc_t some = make_rsrc((const char*)l + pl.n0 * ldl * 2, in ? ncols * ldl * 2 : 0), none = make_rsrc(p.x, 0);
-      rb[0] = u ? none : some;
-      if (GATED) rb[1] = u ? some : none;
+      const void* l = MODE == GATED && u ? p.l1 : p.l0;
+      const rsrc_t some = make_rsrc((const char*)l + (pl.n0 * ldl + at) * 2, in ? (ncols * ldl - at) * 2 : 0);
+      const rsrc_t none = make_rsrc(p.x, 0);
+      rb[0] = MODE == GATED && u ? none : some;
+      if (MODE == GATED) rb[1] = u ? some : none;
       // columns that are not there are zeros on both sides: what lies in their place may be no number
-      oa = (uint32_t)(arow * (int)p.ldt * 2 + 16 * chunk) | (8 * chunk < p.ldt ? 0u : 1u << 31);
-      ob = (uint32_t)(brow() * (int)ldl * 2 + 16 * chunk) | (8 * chunk < ldl ? 0u : 1u << 31);
+      oa = (uint32_t)(arow * (int)p.ldt * 2 + 16 * chunk) | (64 * u + 8 * chunk < p.ldt ? 0u : 1u << 31);
+      ob = (uint32_t)(brow() * (int)ldl * 2 + 16 * chunk) | (at + 8 * chunk < ldl ? 0u : 1u << 31);
       sa = (uint32_t)(8 * NW * (int)p.ldt * 2);
       sb = (uint32_t)(bstep() * (int)ldl * 2);
       so = 0;
@@ -113,7 +117,7 @@ struct Copies16 {
     char* dst = stage_lds + (wave + NW * i) * 1024;
     const int b = i - PER_A;
     if (b < 0) copy16(ra, dst, oa + i * sa, so);
-    else copy16(GATED && side(b) ? rb[1] : rb[0], dst, ob + bindex(b) * sb, so);
+    else copy16(MODE == GATED && side(b) ? rb[1] : rb[0], dst, ob + bindex(b) * sb, so);
   }
   __device__ __forceinline__ void all(char* stage_lds, int stage) {
     if (NW < T::NW && wave >= NW) return;
@@ -167,7 +171,7 @@ struct Rows16 {
 template <int CD, int ACT, class T>
 __device__ __forceinline__ void write_gated(const G16& p, const Place& pl, Acc<T>& acc, const float* coef, char* W,
                                             int wave, int lane) {
-  constexpr int C = cols_of<T, true>(), PAIRS = T::WNB / 2, RB = 64 * PAIRS;
+  constexpr int C = cols_of<T, GATED>(), PAIRS = T::WNB / 2, RB = 64 * PAIRS;
   const int h = lane >> 5, r32 = lane & 31;
   const int wm = (wave / T::NWN) * 32 * T::WMB, wc = (wave % T::NWN) * 32 * PAIRS;
   const int ncols = (int)max((int64_t)0, min((int64_t)(32 * PAIRS), p.n - pl.n0 - wc));
@@ -241,8 +245,10 @@ __device__ __forceinline__ void add_masked(Acc<T>& acc, const G16& p, const Plac
       asm volatile("" ::: "memory");
     }
 }
-template <int CD, class T>
-__device__ __forceinline__ void write_plain(const G16& p, const Place& pl, const Acc<T>& acc, char* W, int wave, int lane) {
+// coef: with BIAS the tile's biases.
+template <int CD, class T, bool BIAS>
+__device__ __forceinline__ void write_plain(const G16& p, const Place& pl, const Acc<T>& acc, const float* coef, char* W,
+                                            int wave, int lane) {
   constexpr int RB = 64 * T::WNB;
   const int h = lane >> 5, r32 = lane & 31;
   const int wm = (wave / T::NWN) * 32 * T::WMB, wn = (wave % T::NWN) * 32 * T::WNB;
@@ -252,9 +258,11 @@ __device__ __forceinline__ void write_plain(const G16& p, const Place& pl, const
 #pragma unroll
     for (int j = 0; j < T::WNB; ++j)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *(u32x2_t*)(W + Rows16<RB>::at(r32, 64 * j + 16 * q + 8 * h)) =
-            u32x2_t{pack2<CD>(acc[i][j][4 * q], acc[i][j][4 * q + 1]), pack2<CD>(acc[i][j][4 * q + 2], acc[i][j][4 * q + 3])};
+      for (int q = 0; q < 4; ++q) {
+        f32x4_t v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        if (BIAS) v += *(const f32x4_t*)(coef + wn + 32 * j + 8 * q + 4 * h);
+        *(u32x2_t*)(W + Rows16<RB>::at(r32, 64 * j + 16 * q + 8 * h)) = u32x2_t{pack2<CD>(v[0], v[1]), pack2<CD>(v[2], v[3])};
+      }
     wait_lgkm0();
     asm volatile("" ::: "memory");
     Rows16<RB>::store(W, p.out, p.n, pl.m0 + wm + 32 * i, pl.n0 + wn, min(32, pl.rows - wm - 32 * i), ncols, lane);
@@ -277,11 +285,11 @@ struct HalfOf<Tile<WMB, WNB, NWM, NWN, 2>> {
 // stage are requested, so that they land while this one's outputs are formed and stored; those pass
 // through LDS behind that stage.  A last round of at most half the workgroups runs as tiles of half
 // the rows (the largest tiles).
-template <int CD, class T, bool GATED, int WGS>
+template <int CD, class T, int MODE, int WGS>
 __global__ __launch_bounds__(64 * T::NW, WGS) void k_gemm16(G16 p, int act) {
   using H = typename HalfOf<T>::type;
   constexpr bool HALVES = !std::is_same_v<T, H>;
-  constexpr int C = cols_of<T, GATED>(), COEF = GATED ? 2 * C : 0, STAGING = GATED ? 1024 * T::WNB : 2048 * T::WNB;
+  constexpr int C = cols_of<T, MODE>(), COEF = MODE == GATED ? 2 * C : MODE == PLAIN ? C : 0, STAGING = MODE == GATED ? 1024 * T::WNB : 2048 * T::WNB;
   static_assert(T::LDS - T::STAGE >= T::NW * STAGING, "staging fits");
   __shared__ __attribute__((aligned(1024))) char lds[T::LDS + 2 * COEF * 4];  // one array: see fp8.hip
   float* coefs = (float*)(lds + T::LDS);  // two sets, used in turn
@@ -309,27 +317,27 @@ __global__ __launch_bounds__(64 * T::NW, WGS) void k_gemm16(G16 p, int act) {
     return p.bias && col < p.n ? load_cd<CD>(p.bias, col + (i >= C ? p.n : 0)) : 0.f;
   };
   auto first_stage = [&](const Place& pl) {
-    if (HALVES && pl.rows <= H::TM) Copies16<H, GATED>(p, pl, wave, lane).all(lds, 0);
-    else Copies16<T, GATED>(p, pl, wave, lane).all(lds, 0);
+    if (HALVES && pl.rows <= H::TM) Copies16<H, MODE>(p, pl, wave, lane).all(lds, 0);
+    else Copies16<T, MODE>(p, pl, wave, lane).all(lds, 0);
   };
 
   Place cur = item(0);
   if (cur.rows == 0) return;
-  if (GATED)
+  if (COEF)
     for (int i = tid; i < COEF; i += 64 * T::NW) coefs[i] = coef_of(cur, i);
   first_stage(cur);
   int set = 0;
   for (int r = 1;; ++r) {
     const Place nxt = item(r);
     static_assert(COEF <= 64 * T::NW, "one coefficient to a thread");
-    const float c = GATED && nxt.rows && tid < COEF ? coef_of(nxt, tid) : 0.f;
+    const float c = COEF && nxt.rows && tid < COEF ? coef_of(nxt, tid) : 0.f;
     auto work = [&](auto shape) {
       using U = decltype(shape);
       // the lane counts as unknown here and after the contraction: addresses of either shape and of the
       // outputs, formed ahead of all tiles, would be kept through the contraction and pushed out to memory
       int ln = lane;
       asm volatile("" : "+v"(ln));
-      Copies16<U, GATED> cp(p, cur, wave, ln);
+      Copies16<U, MODE> cp(p, cur, wave, ln);
       Acc<U> acc;
       zero<U>(acc);
       if constexpr (copying<U>() < U::NW) {
@@ -345,22 +353,22 @@ __global__ __launch_bounds__(64 * T::NW, WGS) void k_gemm16(G16 p, int act) {
         contract<U, Half16<CD>>(acc, lds, cp, wave, ln);
       }
       asm volatile("" : "+v"(ln));
-      if constexpr (!GATED) {
+      if constexpr (MODE == MASKED) {
         add_masked<CD, U>(acc, p, cur, lds + cp.KM % U::NS * U::STAGE, wave, ln);
         __syncthreads();  // every wave is past the low-rank operands
       }
       if (nxt.rows) {
-        if (GATED && tid < COEF) coefs[(set ^ 1) * COEF + tid] = c;
+        if (COEF && tid < COEF) coefs[(set ^ 1) * COEF + tid] = c;
         first_stage(nxt);
       }
       char* W = lds + T::STAGE + wave * STAGING;
-      if constexpr (GATED) {
+      if constexpr (MODE == GATED) {
         const float* co = coefs + set * COEF;
         if (act == QLORA_ACT_SILU) write_gated<CD, QLORA_ACT_SILU, U>(p, cur, acc, co, W, wave, ln);
         else if (act == QLORA_ACT_GELU) write_gated<CD, QLORA_ACT_GELU, U>(p, cur, acc, co, W, wave, ln);
         else write_gated<CD, QLORA_ACT_GELU_TANH, U>(p, cur, acc, co, W, wave, ln);
       } else {
-        write_plain<CD, U>(p, cur, acc, W, wave, ln);
+        write_plain<CD, U, MODE == PLAIN>(p, cur, acc, coefs + set * COEF, W, wave, ln);
       }
     };
     if (HALVES && cur.rows <= H::TM) work(H{});
@@ -372,32 +380,32 @@ __global__ __launch_bounds__(64 * T::NW, WGS) void k_gemm16(G16 p, int act) {
 }
 
 // 256 rows x 256 columns (128 of each projection), eight waves; a gated wave takes 64 rows of 64
-// columns of h, whole lines of the outputs, a masked one 128 rows, whose mask bits fill four words
+// columns of h, whole lines of the outputs
 using FullGated = Tile<2, 4, 4, 2, 2>;
-using FullMasked = Tile<4, 2, 2, 4, 2>;
+using Full = Tile<4, 2, 2, 4, 2>;
 using Wide = Tile<2, 2, 2, 4, 3>;  // 128 x 256, eight waves
 using Mid = Tile<2, 2, 2, 2, 4>;   // 128 x 128, four waves
 using Low = Tile<1, 2, 2, 2, 3>;   // 64 x 128, four waves; two workgroups fit a compute unit
 
-template <int CD, class T, bool GATED, int WGS>
+template <int CD, class T, int MODE, int WGS>
 int run(const G16& p, int act, int kind, hipStream_t s) {
-  const int64_t tiles = ceil_div(p.m, T::TM) * ceil_div(p.n, cols_of<T, GATED>());
+  const int64_t tiles = ceil_div(p.m, T::TM) * ceil_div(p.n, cols_of<T, MODE>());
   ProfScope prof(kind, s);
-  k_gemm16<CD, T, GATED, WGS><<<dim3((unsigned)std::min<int64_t>(tiles, cu_count() * WGS)), dim3(64 * T::NW), 0, s>>>(p, act);
+  k_gemm16<CD, T, MODE, WGS><<<dim3((unsigned)std::min<int64_t>(tiles, cu_count() * WGS)), dim3(64 * T::NW), 0, s>>>(p, act);
   return check_launch("k_gemm16");
 }
 
 // The smallest tiles that fit the compute units in one round, the largest beyond.
-template <int CD, bool GATED>
+template <int CD, int MODE>
 int run_cd(const G16& p, int act, int kind, hipStream_t s) {
   auto one_round = [&](int64_t tm, int64_t tn) {
-    return ceil_div(p.m, tm) * ceil_div(p.n, GATED ? tn / 2 : tn) <= cu_count();
+    return ceil_div(p.m, tm) * ceil_div(p.n, MODE == GATED ? tn / 2 : tn) <= cu_count();
   };
-  if constexpr (GATED)
-    if (one_round(64, 128)) return run<CD, Low, GATED, 2>(p, act, kind, s);
-  if (one_round(128, 128)) return run<CD, Mid, GATED, 1>(p, act, kind, s);
-  if (one_round(128, 256)) return run<CD, Wide, GATED, 1>(p, act, kind, s);
-  return run<CD, std::conditional_t<GATED, FullGated, FullMasked>, GATED, 1>(p, act, kind, s);
+  if constexpr (MODE != MASKED)
+    if (one_round(64, 128)) return run<CD, Low, MODE, 2>(p, act, kind, s);
+  if (one_round(128, 128)) return run<CD, Mid, MODE, 1>(p, act, kind, s);
+  if (one_round(128, 256)) return run<CD, Wide, MODE, 1>(p, act, kind, s);
+  return run<CD, std::conditional_t<MODE == GATED, FullGated, Full>, MODE, 1>(p, act, kind, s);
 }
 
 }  // namespace
@@ -428,7 +436,7 @@ int gemm16_gated(int cd, const void* x, int64_t m, int64_t n, int64_t K, const v
   p.m = m;
   p.n = n;
   p.K = K;
-  return cd == CD_BF16 ? run_cd<CD_BF16, true>(p, act, QLORA_K_FWD_GEMM, s) : run_cd<CD_F16, true>(p, act, QLORA_K_FWD_GEMM, s);
+  return cd == CD_BF16 ? run_cd<CD_BF16, GATED>(p, act, QLORA_K_FWD_GEMM, s) : run_cd<CD_F16, GATED>(p, act, QLORA_K_FWD_GEMM, s);
 }
 
 // dX [m][n] = dY [m][K] W~^T wt [n][K] + (dT [m][ldt] A^T at [n][lda]) M, ldt and lda multiples of 8, at most 64;
@@ -448,7 +456,26 @@ int gemm16_masked_dx(int cd, const void* dy, int64_t m, int64_t n, int64_t K, co
   p.K = K;
   p.bits = (const uint32_t*)bits;
   p.ldbits = ldbits;
-  return cd == CD_BF16 ? run_cd<CD_BF16, false>(p, 0, QLORA_K_BWD_DX, s) : run_cd<CD_F16, false>(p, 0, QLORA_K_BWD_DX, s);
+  return cd == CD_BF16 ? run_cd<CD_BF16, MASKED>(p, 0, QLORA_K_BWD_DX, s) : run_cd<CD_F16, MASKED>(p, 0, QLORA_K_BWD_DX, s);
+}
+
+// y [m][n] = [x [m][K] | t [m][ldt]] [w [n][K] | l [n][ldl]]^T (+ bias), ldt and ldl multiples of 8; x and w rows
+// of K elements.
+int gemm16_plain(int cd, const void* x, int64_t m, int64_t n, int64_t K, const void* w, const void* t, int64_t ldt,
+                 const void* l, int64_t ldl, const void* bias, void* y, int kind, hipStream_t s) {
+  G16 p = {};
+  p.x = x;
+  p.w0 = w;
+  p.t = t;
+  p.ldt = ldt;
+  p.l0 = l;
+  p.ldl0 = ldl;
+  p.bias = bias;
+  p.out = y;
+  p.m = m;
+  p.n = n;
+  p.K = K;
+  return cd == CD_BF16 ? run_cd<CD_BF16, PLAIN>(p, 0, kind, s) : run_cd<CD_F16, PLAIN>(p, 0, kind, s);
 }
 
 }  // namespace qnf4

@@ -324,12 +324,12 @@ int launch_forward_group(const GroupCall& gc, const void* bias, void* y, float* 
 
 int launch_backward_group(const GroupCall& gc, const void* dy, const float* const* t_saved, void* dx,
                           float* const* d_a, float* const* d_b, void* ws, hipStream_t s) {
-  return launch_backward_group_as(gc, dy, t_saved, dx, (void* const*)d_a, (void* const*)d_b, CD_F32, ws, s);
+  return launch_backward_group_as(gc, dy, t_saved, dx, (void* const*)d_a, (void* const*)d_b, CD_F32, false, ws, s);
 }
 
 // The adapters' gradients in fp32, or (gd = the call's type) rounded into it.
 int launch_backward_group_as(const GroupCall& gc, const void* dy, const float* const* t_saved, void* dx,
-                             void* const* d_a, void* const* d_b, int gd, void* ws, hipStream_t s) {
+                             void* const* d_a, void* const* d_b, int gd, bool g16, void* ws, hipStream_t s) {
   const GBwd P = plan_gbwd(gc);
   char* w = (char*)ws;
   const LayerCall& c0 = gc.c[0];
@@ -425,7 +425,10 @@ int launch_backward_group_as(const GroupCall& gc, const void* dy, const float* c
   }
   if (dx) {
     LayerCall cc = concat_call(gc);
-    if ((rc = dense256_dx(cc, dy, w + P.wdt, w + P.dtcd, gc.RP, dx, P.sp, w + P.split, w + P.at))) return rc;
+    rc = g16 ? gemm16_plain(cc.cd, dy, m, K, gc.N, w + P.wdt, w + P.dtcd, gc.RP, w + P.at, gc.RP, nullptr, dx,
+                            QLORA_K_BWD_DX, s)
+             : dense256_dx(cc, dy, w + P.wdt, w + P.dtcd, gc.RP, dx, P.sp, w + P.split, w + P.at);
+    if (rc) return rc;
   }
   // dA_i = dT_i^T x and dB_i = s_i dY_i^T T0_i: both products in one launch, both
   // reductions in the next

@@ -35,8 +35,9 @@ int apply_seeded(int cd, const void* x, const Seeded& sd, int64_t rows, int64_t 
 int rank_add_seeded(int cd, void* dx, const Seeded& sd, const void* dt, int64_t ld_dt, const void* a, int32_t r, int64_t M,
                     int64_t K, hipStream_t s);
 
+// g16: dX by gemm16_plain.
 int launch_backward_group_as(const GroupCall& gc, const void* dy, const float* const* t_saved, void* dx,
-                             void* const* d_a, void* const* d_b, int gd, void* ws, hipStream_t s);
+                             void* const* d_a, void* const* d_b, int gd, bool g16, void* ws, hipStream_t s);
 
 // gemv.hip: the gated block's forward of up to 64 tokens (c: gate and up).
 size_t gemv_workspace_bytes(int64_t m, int64_t rows, int64_t cols, int32_t r, int cd);
@@ -47,6 +48,8 @@ int gemv_gated(const LayerCall* c, int act, void* h, void* pre, float* const* t_
 bool gemm16_ok(int cd, int64_t m, int64_t n, int64_t K);
 int gemm16_gated(int cd, const void* x, int64_t m, int64_t n, int64_t K, const void* const* w, const void* t,
                  const void* const* b, const int64_t* ldb, const void* bias, int act, void* h, void* pre, hipStream_t s);
+int gemm16_plain(int cd, const void* x, int64_t m, int64_t n, int64_t K, const void* w, const void* t, int64_t ldt,
+                 const void* l, int64_t ldl, const void* bias, void* y, int kind, hipStream_t s);
 int gemm16_masked_dx(int cd, const void* dy, int64_t m, int64_t n, int64_t K, const void* wt, const void* dt, int64_t ldt,
                      const void* at, int64_t lda, const void* bits, int64_t ldbits, void* dx, hipStream_t s);
 

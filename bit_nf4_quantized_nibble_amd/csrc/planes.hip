@@ -89,10 +89,24 @@ struct Pack {
   int64_t wide = 0;
   Planes across;       // [cols][tall], the transpose
   int64_t tall = 0;
-  uint32_t tiles_x = 0, end = 0;  // workgroups before `end` are this job's or an earlier one's
+  uint32_t tiles_x = 0;
 };
+// The job of a workgroup: job i has those below end[i] that no earlier one has (all ends are read at once).
+template <int N>
+__device__ __forceinline__ int job_of(const uint32_t (&end)[N], uint32_t b, uint32_t& first) {
+  int job = 0;
+  first = 0;
+#pragma unroll
+  for (int i = 0; i < N - 1; ++i)
+    if (b >= end[i]) {
+      job = i + 1;
+      first = end[i];
+    }
+  return job;
+}
 constexpr int kPacks = 14;
 struct Packs {
+  uint32_t end[kPacks];
   Pack j[kPacks];
   Nf4W w[2];
   float lv[16];
@@ -195,10 +209,10 @@ __global__ __launch_bounds__(kThreads) void k_pack(Packs ps) {
   auto chunk_at = [](int col, int c) { return (col + (col >> 3)) * 128 + ((c ^ (col >> 3)) << 4); };
   __shared__ float lv[16];
   const int tid = threadIdx.x;
-  int job = 0;
-  while (blockIdx.x >= ps.j[job].end) ++job;
+  uint32_t first;
+  const int job = job_of(ps.end, blockIdx.x, first);
   const Pack& j = ps.j[job];
-  const uint32_t b = blockIdx.x - (job ? ps.j[job - 1].end : 0);
+  const uint32_t b = blockIdx.x - first;
   const int64_t i0 = (int64_t)(b / j.tiles_x) * 64, k0 = (int64_t)(b % j.tiles_x) * 64;
   if (tid < 16) lv[tid] = ps.lv[tid];
   const int c = tid & 7, r = tid >> 3;
@@ -326,10 +340,10 @@ struct Prod {
   int64_t ldp, ldo;
   const void* bias;   // with out
   int32_t nseg, steps, per, S, tiles_m, tiles_n;  // steps in all, and per slice
-  uint32_t end;       // workgroups before it are this product's or an earlier one's
 };
 constexpr int kProds = 6;
 struct Prods {
+  uint32_t end[kProds];
   Prod p[kProds];
 };
 
@@ -407,11 +421,9 @@ __global__ __launch_bounds__(64 * T::NW) void k_product(Prods ps) {
   constexpr int KD = CD == CD_F32 ? CD_BF16 : CD;
   __shared__ __attribute__((aligned(1024))) char lds[T::LDS];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  int job = 0;
-  while (blockIdx.x >= ps.p[job].end) ++job;
-  const Prod& p = ps.p[job];
-  const uint32_t first = job ? ps.p[job - 1].end : 0;
-  const int tiles = p.tiles_m * p.tiles_n, b = (int)(blockIdx.x - first);
+  uint32_t start;
+  const Prod& p = ps.p[job_of(ps.end, blockIdx.x, start)];
+  const int tiles = p.tiles_m * p.tiles_n, b = (int)(blockIdx.x - start);
   int z = 0, t;
   int tm, tn;
   if (p.S == 1) {
@@ -673,10 +685,9 @@ __global__ __launch_bounds__(64 * T::NW) void k_decode(Prods ps, Weights ws) {
   __shared__ __attribute__((aligned(1024))) char lds[2 * D::STAGE];
   __shared__ float lv[16];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  int job = 0;
-  while (blockIdx.x >= ps.p[job].end) ++job;
-  const Prod& p = ps.p[job];
-  const int tiles = p.tiles_m * p.tiles_n, b = (int)(blockIdx.x - (job ? ps.p[job - 1].end : 0));
+  uint32_t start;
+  const Prod& p = ps.p[job_of(ps.end, blockIdx.x, start)];
+  const int tiles = p.tiles_m * p.tiles_n, b = (int)(blockIdx.x - start);
   const int z = b / tiles, t = b - z * tiles;
   const int64_t m0 = (int64_t)(t % p.tiles_m) * T::TM, n0 = (int64_t)(t / p.tiles_m) * T::TN;
   const int first = z * p.per, KT = min(p.per, p.steps - first), kind = p.s[0].w;
@@ -719,10 +730,11 @@ struct Join {
   float* raw = nullptr;  // JOIN_RANK: the sums [m][n] or null
   Planes rowwise, across;  // JOIN_RANK: scale * sum, [m][wide] and [n][tall]
   int64_t wide = 0, tall = 0;
-  uint32_t per = 0, end = 0;  // groups of four columns to a row; workgroups as in Pack
+  uint32_t per = 0;  // groups of four columns to a row
 };
 constexpr int kJoins = 6;
 struct Joins {
+  uint32_t end[kJoins];
   Join j[kJoins];
   Seeded sd;
   int act;
@@ -761,10 +773,9 @@ __device__ __forceinline__ void store4(int type, void* p, int64_t at, const f32x
 template <int CD>
 __global__ __launch_bounds__(kThreads) void k_join(Joins js) {
   constexpr int KD = CD == CD_F32 ? CD_BF16 : CD;
-  int job = 0;
-  while (blockIdx.x >= js.j[job].end) ++job;
-  const Join& j = js.j[job];
-  const int64_t idx = (int64_t)(blockIdx.x - (job ? js.j[job - 1].end : 0)) * kThreads + threadIdx.x;
+  uint32_t first;
+  const Join& j = js.j[job_of(js.end, blockIdx.x, first)];
+  const int64_t idx = (int64_t)(blockIdx.x - first) * kThreads + threadIdx.x;
   if (j.kind == JOIN_RANK) {
     // rows next to each other in neighbouring lanes: the transposed planes are written in lines
     const int64_t rows = max(j.m, j.tall), g = idx / rows, i = idx - g * rows, t = 4 * g;
@@ -906,8 +917,9 @@ struct Run {
       j.tiles_x = (uint32_t)ceil_div(cols, 64);
       blocks += j.tiles_x * ceil_div(rows, 64);
       if (blocks > 0x7fffffff) return fail();
-      j.end = (uint32_t)blocks;
+      packs.end[i] = (uint32_t)blocks;
     }
+    for (int i = packs.n; i < kPacks; ++i) packs.end[i] = 0xffffffffu;
     if (dry() || rc || blocks == 0) return;
     for (int i = 0; i < g; ++i) packs.w[i] = c[i].w;
     for (int i = 0; i < 16; ++i) packs.lv[i] = host_tables().lv[i];
@@ -988,10 +1000,11 @@ struct Run {
       if (blocks > 0x7fffffff) return fail();
       p.tiles_m = (int32_t)tm;
       p.tiles_n = (int32_t)tn;
-      p.end = (uint32_t)blocks;
+      prods.end[i] = (uint32_t)blocks;
       for (int e = 0; e < p.nseg; ++e)
         if (std::max(p.s[e].lda, p.s[e].ldb) * 2 * std::max(T::TM, T::TN) >= (1LL << 31)) return fail();
     }
+    for (int i = np; i < kProds; ++i) prods.end[i] = 0xffffffffu;
     if (dry() || rc || blocks == 0) return;
     ProfScope prof(kind, s);
     const dim3 grid((unsigned)blocks), threads(64 * T::NW);
@@ -1040,8 +1053,9 @@ struct Run {
       const int64_t rows = std::max(j.m, j.tall);
       blocks += ceil_div(rows * j.per, kThreads);
       if (blocks > 0x7fffffff) return fail();
-      j.end = (uint32_t)blocks;
+      joins.end[i] = (uint32_t)blocks;
     }
+    for (int i = nj; i < kJoins; ++i) joins.end[i] = 0xffffffffu;
     if (!dry() && !rc && blocks) {
       if (sd) joins.sd = *sd;
       joins.act = act;
