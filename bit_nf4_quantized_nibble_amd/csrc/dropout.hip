@@ -30,19 +30,12 @@ __global__ __launch_bounds__(kThreads) void k_apply_mask(const void* __restrict_
 // out = x where the generator keeps it, else zero: a row's 8 columns of one counter to a thread.
 template <int CD>
 __global__ __launch_bounds__(kThreads) void k_apply_seeded(const void* __restrict__ x, Seeded sd, int64_t rows,
-                                                           int64_t cols, void* __restrict__ out,
-                                                           uint8_t* __restrict__ bits) {
+                                                           int64_t cols, void* __restrict__ out) {
   const PhiloxKey key = philox_key(sd);
   const int64_t groups = (cols + 7) / 8, total = rows * groups;
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
     const int64_t row = i / groups, g = i - row * groups, at = row * cols + 8 * g;
     const u32x4_t w = philox(key, (uint32_t)g, (uint32_t)row);
-    if (bits) {
-      uint32_t b = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) b |= keeps(w, e, sd.threshold) ? 1u << e : 0u;
-      bits[i] = (uint8_t)b;
-    }
     if (CD != CD_F32 && cols % 8 == 0) {
       u32x4_t v = *(const u32x4_t*)((const uint16_t*)x + at);
 #pragma unroll
@@ -195,14 +188,13 @@ int rank_add_seeded(int cd, void* dx, const Seeded& sd, const void* dt, int64_t 
   return rank_add(cd, dx, DrawnMask{sd}, dt, ld_dt, a, r, M, K, s);
 }
 
-int apply_seeded(int cd, const void* x, const Seeded& sd, int64_t rows, int64_t cols, void* out, void* bits, hipStream_t s) {
-  uint8_t* b8 = (uint8_t*)bits;
+int apply_seeded(int cd, const void* x, const Seeded& sd, int64_t rows, int64_t cols, void* out, hipStream_t s) {
   const int64_t n = rows * ceil_div(cols, 8);
   if (n == 0) return QLORA_OK;
   const dim3 g((unsigned)std::min<int64_t>(1 << 16, ceil_div(n, kThreads))), b(kThreads);
-  if (cd == CD_BF16) k_apply_seeded<CD_BF16><<<g, b, 0, s>>>(x, sd, rows, cols, out, b8);
-  else if (cd == CD_F16) k_apply_seeded<CD_F16><<<g, b, 0, s>>>(x, sd, rows, cols, out, b8);
-  else k_apply_seeded<CD_F32><<<g, b, 0, s>>>(x, sd, rows, cols, out, b8);
+  if (cd == CD_BF16) k_apply_seeded<CD_BF16><<<g, b, 0, s>>>(x, sd, rows, cols, out);
+  else if (cd == CD_F16) k_apply_seeded<CD_F16><<<g, b, 0, s>>>(x, sd, rows, cols, out);
+  else k_apply_seeded<CD_F32><<<g, b, 0, s>>>(x, sd, rows, cols, out);
   return check_launch("k_apply_seeded");
 }
 

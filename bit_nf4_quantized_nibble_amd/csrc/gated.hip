@@ -138,8 +138,15 @@ FwdPlan plan_fwd(const GroupCall& gc) {
 }
 
 // dst [n][ld] = src [n][r] with zeros from column r on: rows of lora_b as whole 16-byte chunks.
-__global__ __launch_bounds__(kThreads) void k_pad_rows(const uint16_t* __restrict__ src, int r, int64_t n, int ld,
-                                                       uint16_t* __restrict__ dst) {
+struct PadRows {
+  const uint16_t* src;
+  uint16_t* dst;
+  int r, ld;
+};
+__global__ __launch_bounds__(kThreads) void k_pad_rows(PadRows a, PadRows b, int64_t n) {
+  const uint16_t* src = blockIdx.y ? b.src : a.src;
+  uint16_t* dst = blockIdx.y ? b.dst : a.dst;
+  const int r = blockIdx.y ? b.r : a.r, ld = blockIdx.y ? b.ld : a.ld;
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n * ld; i += (int64_t)gridDim.x * kThreads) {
     const int64_t row = i / ld;
     const int c = (int)(i - row * ld);
@@ -182,6 +189,8 @@ int forward_tiled(const GroupCall& gc, const FwdPlan& P, int act, const void* bi
   SkRed red[2];
   const void* b[2];
   int64_t ldb[2];
+  PadRows pads[2];
+  int np = 0;
   for (int i = 0; i < 2; ++i) {
     const LayerCall& c = gc.c[i];
     w[i] = c.w;
@@ -198,12 +207,15 @@ int forward_tiled(const GroupCall& gc, const FwdPlan& P, int act, const void* bi
     b[i] = c.lora_b;
     ldb[i] = round_up(c.r, 8);
     if (c.r % 8) {
-      ProfScope prof(QLORA_K_REDUCE, s);
       b[i] = ws + P.bpad[i];
-      k_pad_rows<<<dim3(grid_for(n * ldb[i])), dim3(kThreads), 0, s>>>((const uint16_t*)c.lora_b, c.r, n, (int)ldb[i],
-                                                                       (uint16_t*)(ws + P.bpad[i]));
-      if ((rc = check_launch("k_pad_rows"))) return rc;
+      pads[np++] = PadRows{(const uint16_t*)c.lora_b, (uint16_t*)(ws + P.bpad[i]), c.r, (int)ldb[i]};
     }
+  }
+  if (np) {
+    ProfScope prof(QLORA_K_REDUCE, s);
+    const dim3 grid(grid_for(n * std::max(pads[0].ld, pads[np - 1].ld)), np);
+    k_pad_rows<<<grid, dim3(kThreads), 0, s>>>(pads[0], pads[np - 1], n);
+    if ((rc = check_launch("k_pad_rows"))) return rc;
   }
   // W~ of both, the reductions of T riding on the launch
   if ((rc = dequant_group_into(w, 2, c0.cd, out, red, s))) return rc;

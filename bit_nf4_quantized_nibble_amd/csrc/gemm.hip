@@ -590,6 +590,17 @@ int lora_down(const LayerCall& c, const void* lx, const Split& sp, float* part, 
   return run_reduce<CD>(part, sp, c.m, c.r, sc32, out32, sccd, outcd, r_pad, c.stream);
 }
 
+// x A^T as a rank product.
+SkSpec down_spec(const LayerCall& c) {
+  SkSpec p;
+  p.a = c.x;
+  p.lda = p.ldb = p.Kc = c.w.cols;
+  p.arows = p.P = c.m;
+  p.b = c.lora_a;
+  p.R = c.r;
+  return p;
+}
+
 // Whether a seeded forward writes W~ and multiplies by gemm16_plain (bf16: 512 tokens of 4096 x 4096 45 us
 // against the fused kernel's 56, 1024 tokens 61 against 77, 4096 tokens of 14336 x 4096 417 against the
 // dense GEMM's 439); up to 768 tokens of larger weights the fused kernel's cut of the contraction wins (512 tokens
@@ -613,8 +624,9 @@ int forward_gemm(const LayerCall& c, const Seeded* sd, void* y, float* t_save) {
   const bool fast = fast_layout(c.w);
   // input of the low-rank branch: x, or x M with LoRA dropout
   const void* lx = c.x;
-  if (c.drop_mask || sd) {
-    rc = sd ? apply_seeded(CD, c.x, *sd, M, K, ws + P.off_xm, nullptr, c.stream)
+  const bool draws = sd && fast && skinny_ok(CD, c.r);  // the rank product masks x itself
+  if (c.drop_mask || (sd && !draws)) {
+    rc = sd ? apply_seeded(CD, c.x, *sd, M, K, ws + P.off_xm, c.stream)
             : apply_mask(CD, c.x, c.drop_mask, M * K, ws + P.off_xm, c.stream);
     if (rc) return rc;
     lx = ws + P.off_xm;
@@ -627,7 +639,10 @@ int forward_gemm(const LayerCall& c, const Seeded* sd, void* y, float* t_save) {
   bool red_pending = false;
   if (fast && skinny_ok(CD, c.r)) {
     int S;
-    if ((rc = skinny(CD, false, lx, K, M, c.lora_a, K, M, c.r, K, part, &S, c.stream, QLORA_K_LORA_DOWN))) return rc;
+    if ((rc = draws ? skinny_drawn(CD, false, down_spec(c), part, &S, nullptr, nullptr, nullptr, *sd, nullptr, 0, c.stream,
+                                   QLORA_K_LORA_DOWN)
+                    : skinny(CD, false, lx, K, M, c.lora_a, K, M, c.r, K, part, &S, c.stream, QLORA_K_LORA_DOWN)))
+      return rc;
     red.part = part;
     red.S = S;
     red.P = M;
@@ -684,11 +699,12 @@ int backward_gemm(const LayerCall& c, const Seeded* sd, const void* dy, const fl
   const bool dense_dx = dx && P.dense && dense256_ok(c, true);
   // with a drawn mask the tiled dX GEMM adds the masked term itself, from the mask's bits (in place of the
   // zero operand that the other GEMMs get)
-  const bool masked = sd && dense_dx && P.r_pad <= 64 && gemm16_ok(CD, M, K, N);
+  const bool masked = sd && dense_dx && P.sk_n && P.r_pad <= 64 && gemm16_ok(CD, M, K, N);
   // input of the low-rank branch: x, or x M with LoRA dropout
   const void* lx = c.x;
-  if (c.drop_mask || sd) {
-    rc = sd ? apply_seeded(CD, c.x, *sd, M, K, ws + P.off_xm, masked ? ws + P.off_zero : nullptr, c.stream)
+  const bool draws = sd && P.sk_n;  // the rank products mask x themselves
+  if (c.drop_mask || (sd && !draws)) {
+    rc = sd ? apply_seeded(CD, c.x, *sd, M, K, ws + P.off_xm, c.stream)
             : apply_mask(CD, c.x, c.drop_mask, M * K, ws + P.off_xm, c.stream);
     if (rc) return rc;
     lx = ws + P.off_xm;
@@ -699,7 +715,10 @@ int backward_gemm(const LayerCall& c, const Seeded* sd, const void* dy, const fl
   if (!T0) {
     if (P.sk) {
       int S;
-      if ((rc = skinny(CD, false, lx, K, M, c.lora_a, K, M, r, K, part, &S, c.stream, QLORA_K_LORA_DOWN))) return rc;
+      if ((rc = draws ? skinny_drawn(CD, false, down_spec(c), part, &S, nullptr, nullptr, nullptr, *sd, nullptr, 0, c.stream,
+                                     QLORA_K_LORA_DOWN)
+                      : skinny(CD, false, lx, K, M, c.lora_a, K, M, r, K, part, &S, c.stream, QLORA_K_LORA_DOWN)))
+        return rc;
       if ((rc = skinny_reduce(CD, part, S, M, r, 1.0f, t0, false, 0.f, nullptr, 0, c.stream))) return rc;
     } else if ((rc = lora_down<CD>(c, lx, P.st, part, t0, 1.0f, nullptr, 0.f, 0))) {
       return rc;
@@ -791,6 +810,34 @@ int backward_gemm(const LayerCall& c, const Seeded* sd, const void* dy, const fl
     if (rc) return rc;
   }
 
+  // dA's and dB's products (one launch) on the skinny path.  Under a drawn mask they run ahead of dX and leave
+  // the mask's bits for it.
+  float* part2 = (float*)(ws + P.off_part2);
+  int Sa = 0, Sb = 0;
+  auto gradient_products = [&]() -> int {
+    SkSpec pa, pb;  // dA: x^T against dT^T;  dB: dY^T against T0^T
+    pa.a = lx;
+    pa.lda = K;
+    pa.arows = M;
+    pa.b = dtt;
+    pa.ldb = P.m_pad;
+    pa.P = K;
+    pa.R = r;
+    pa.Kc = P.m_pad;
+    pb.a = dy;
+    pb.lda = N;
+    pb.arows = M;
+    pb.b = t0t;
+    pb.ldb = P.m_pad;
+    pb.P = N;
+    pb.R = r;
+    pb.Kc = P.m_pad;
+    if (draws)
+      return skinny_drawn(CD, true, pa, part, &Sa, &pb, part2, &Sb, *sd, masked ? ws + P.off_zero : nullptr, K / 32, c.stream,
+                          QLORA_K_BWD_DA);
+    return skinny_jobs(CD, true, pa, part, &Sa, &pb, part2, &Sb, c.stream, QLORA_K_BWD_DA);
+  };
+
   // dX = dY W~ + dT A (the contraction runs over W's rows): W~^T written once and a
   // dense GEMM, or the fused dequant.  With LoRA dropout the GEMM gets a zero dT
   // (base product only) and the masked low-rank term is added afterwards.
@@ -802,6 +849,7 @@ int backward_gemm(const LayerCall& c, const Seeded* sd, const void* dy, const fl
   if (dense_dx) {
     void* wdt = ws + P.off_wdt;
     if ((rc = dequant_into(c.w, CD, wdt, true, c.stream, red_dt_pending ? &red_dt : nullptr))) return rc;
+    if (masked && (rc = gradient_products())) return rc;
     rc = masked ? gemm16_masked_dx(CD, dy, M, K, N, wdt, dtcd, P.r_pad, at, P.r_pad, ws + P.off_zero, K / 32, dx, c.stream)
                 : dense256_dx(c, dy, wdt, dt_gemm, P.r_pad, dx, P.dsp, ws + P.off_split, at);
     if (rc) return rc;
@@ -832,26 +880,7 @@ int backward_gemm(const LayerCall& c, const Seeded* sd, const void* dy, const fl
   // dA = dT^T x and dB = s dY^T T0 (contractions over tokens): on the skinny path
   // both products, then one launch that reduces both.
   if (P.sk_n) {
-    float* part2 = (float*)(ws + P.off_part2);
-    int Sa, Sb;
-    SkSpec pa, pb;  // dA: x^T against dT^T;  dB: dY^T against T0^T (one launch)
-    pa.a = lx;
-    pa.lda = K;
-    pa.arows = M;
-    pa.b = dtt;
-    pa.ldb = P.m_pad;
-    pa.P = K;
-    pa.R = r;
-    pa.Kc = P.m_pad;
-    pb.a = dy;
-    pb.lda = N;
-    pb.arows = M;
-    pb.b = t0t;
-    pb.ldb = P.m_pad;
-    pb.P = N;
-    pb.R = r;
-    pb.Kc = P.m_pad;
-    if ((rc = skinny_jobs(CD, true, pa, part, &Sa, &pb, part2, &Sb, c.stream, QLORA_K_BWD_DA))) return rc;
+    if (!masked && (rc = gradient_products())) return rc;
     SkRed ra, rb;
     ra.part = part;
     ra.S = Sa;

@@ -12,10 +12,9 @@
 // up rows, then T_u against B_u with zeros in the gate rows.
 //
 // Masked: the low-rank part is multiplied after the last stage into sums of its own, masked and added.
-// The mask comes as bits, which the launch that masks x for dA leaves behind at no cost of its own (it
-// waits for memory): drawn here, a counter beside the products of each stage, it cost 70 us of 500
-// (4096 tokens, 4096 x 14336) although the vector pipe stands idle there, as the products run at the
-// card's power limit.
+// The mask comes as bits, which the launch that draws it for dA leaves behind: drawn here, a counter beside
+// the products of each stage, it cost 70 us of 500 (4096 tokens, 4096 x 14336) although the vector pipe stands
+// idle there, as the products run at the card's power limit.
 #include <algorithm>
 #include <type_traits>
 

@@ -26,7 +26,7 @@
 //       puts the two row groups a read instruction touches on distinct banks.
 #include <algorithm>
 
-#include "common.h"
+#include "mlp.h"
 #include "reduce_dev.h"
 
 namespace qnf4 {
@@ -76,6 +76,16 @@ struct SkP {
   int64_t P, R, Kc;
   int64_t kslice;   // contraction per slice (multiple of 64)
   float* part;      // [S][P][64] fp32
+};
+
+// The mask of a seeded layer's x (job 0 of a launch).  A wave masks the 16-byte chunks that it has copied, eight
+// columns of one row each and so one counter, between their arrival and the barrier; the counter's rounds
+// run before that, while the copies are under way (4096 tokens, 4096 x 14336, backward: the product takes 61 us
+// in place of 38, bound by the generator's 64-bit products; the pass that wrote x M took 39 of its own).
+struct SkMask {
+  Seeded sd;
+  uint8_t* bits;    // TN, or null: the mask's bits, [arows][ldbits] bytes
+  int64_t ldbits;
 };
 
 // Copy of one stage's Bop tile (64 rows of 64 elements): DMA instruction d of wave
@@ -132,6 +142,59 @@ __device__ __forceinline__ void copy_a_tn(const SkP& p, rsrc_t ra, char* dst, in
     __builtin_amdgcn_raw_ptr_buffer_load_lds(
         ra, (lds_void*)(dst + (4 * d + wave) * 1024), 16,
         (int)oob_unless(ok, (uint32_t)(((k + row) * p.lda + p0 + 8 * c) * 2)), 0, 0, 0);
+  }
+}
+
+// Row and column group (of eight) of the chunk this lane brings in copy d of a stage.
+template <bool TN>
+__device__ __forceinline__ void place_of(int64_t p0, int64_t k, int wave, int lane, int d, int64_t& row, int64_t& group) {
+  if (TN) {
+    const int r = 4 * (4 * d + wave) + (lane >> 4);
+    row = k + r;
+    group = (p0 >> 3) + ((lane & 15) ^ (r & 15));
+  } else {
+    const int r = 8 * (4 * d + wave) + (lane >> 3);
+    row = p0 + r;
+    group = (k >> 3) + ((lane & 7) ^ swz(r));
+  }
+}
+// The masks of a stage's four chunks, a byte to each.
+template <bool TN>
+__device__ __forceinline__ uint32_t draw(const SkMask& m, const PhiloxKey& key, int64_t p0, int64_t k, int wave, int lane) {
+  uint32_t all = 0;
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    int64_t row, group;
+    place_of<TN>(p0, k, wave, lane, d, row, group);
+    const u32x4_t w = philox(key, (uint32_t)group, (uint32_t)row);
+    uint32_t b = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) b |= keeps(w, e, m.sd.threshold) ? 1u << e : 0u;
+    all |= b << (8 * d);
+  }
+  return all;
+}
+__device__ __forceinline__ void store_bits(const SkMask& m, const SkP& p, uint32_t all, int64_t p0, int64_t k, int wave,
+                                           int lane) {
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    int64_t row, group;
+    place_of<true>(p0, k, wave, lane, d, row, group);
+    if (row < p.arows && 8 * group < p.P) m.bits[row * m.ldbits + group] = (uint8_t)(all >> (8 * d));
+  }
+}
+__device__ __forceinline__ void mask_chunks(char* stage, uint32_t all, int wave, int lane) {
+#pragma unroll
+  for (int d = 0; d < 4; ++d) {
+    u32x4_t* at = (u32x4_t*)(stage + (4 * d + wave) * 1024 + lane * 16);
+    u32x4_t v = *at;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int bit = 8 * d + 2 * j;
+      const uint32_t lo = (uint32_t)((int)(all << (31 - bit)) >> 31), hi = (uint32_t)((int)(all << (30 - bit)) >> 31);
+      v[j] &= (lo & 0xffffu) | (hi & 0xffff0000u);
+    }
+    *at = v;
   }
 }
 
@@ -205,10 +268,10 @@ struct SkP2 {
   TrJob tr;     // tr.tiles == 0: none
 };
 
-// MODE: 0 NT, 1 TN (Aop forms), 2 NT with the BT Bop.
+// MODE: 0 NT, 1 TN (Aop forms), 2 NT with the BT Bop; 3 and 4: NT and TN with job 0's Aop under a mask.
 template <int CD, int MODE>
-__global__ __launch_bounds__(kThreads) void k_skinny(SkP2 ps) {
-  constexpr bool TN = MODE == 1, BT = MODE == 2;
+__global__ __launch_bounds__(kThreads) void k_skinny(SkP2 ps, SkMask mask) {
+  constexpr bool TN = MODE == 1 || MODE == 4, BT = MODE == 2, MASK = MODE >= 3;
   __shared__ __attribute__((aligned(1024))) char lds[NBUF * STAGE];  // stage b: [A | B]
   const int jb = blockIdx.z;
   if (jb == (int)ps.nj) {
@@ -262,6 +325,13 @@ __global__ __launch_bounds__(kThreads) void k_skinny(SkP2 ps) {
 #pragma unroll
   for (int d = 0; d < DEPTH; ++d)
     if (d < nst) copy(d);
+  const bool masked = MASK && jb == 0;
+  PhiloxKey key = {};
+  uint32_t keep = 0;
+  if (masked) {
+    key = philox_key(mask.sd);
+    keep = draw<TN>(mask, key, p0, k0, wave, lane);
+  }
   for (int s = 0; s < nst; ++s) {
     // stage s landed in every wave (the up to DEPTH - 1 later stages may still fly;
     // a wave sees its copies complete in issue order); stage s - 1's reads done
@@ -270,9 +340,13 @@ __global__ __launch_bounds__(kThreads) void k_skinny(SkP2 ps) {
     else if (ahead == 2) wait_vm<2 * kCopies>();
     else if (ahead == 1) wait_vm<kCopies>();
     else wait_vm<0>();
+    if (masked) mask_chunks(lds + (s % NBUF) * STAGE, keep, wave, lane);
     __builtin_amdgcn_s_waitcnt(0x3f | (7 << 4) | (0 << 8) | (3 << 14));  // lgkmcnt(0)
     barrier_only();
+    // ahead of the next copies, whose count the waits go by
+    if (TN && masked && mask.bits) store_bits(mask, p, keep, p0, k0 + (int64_t)s * BK, wave, lane);
     if (s + DEPTH < nst) copy(s + DEPTH);  // into the buffer stage s - 1 used
+    if (masked && s + 1 < nst) keep = draw<TN>(mask, key, p0, k0 + (int64_t)(s + 1) * BK, wave, lane);
     const char* As = lds + (s % NBUF) * STAGE;
     const char* Bs = As + A_BYTES;
 #pragma unroll
@@ -418,13 +492,13 @@ int skinny_jobs(int cd, bool tn, const SkSpec& a, float* part, int* S_out, const
   ProfScope prof(kind, s);
   const int mode = tn ? 1 : a.bt ? 2 : 0;
   if (cd == CD_BF16) {
-    if (mode == 1) k_skinny<CD_BF16, 1><<<grid, dim3(kThreads), 0, s>>>(ps);
-    else if (mode == 2) k_skinny<CD_BF16, 2><<<grid, dim3(kThreads), 0, s>>>(ps);
-    else k_skinny<CD_BF16, 0><<<grid, dim3(kThreads), 0, s>>>(ps);
+    if (mode == 1) k_skinny<CD_BF16, 1><<<grid, dim3(kThreads), 0, s>>>(ps, SkMask{});
+    else if (mode == 2) k_skinny<CD_BF16, 2><<<grid, dim3(kThreads), 0, s>>>(ps, SkMask{});
+    else k_skinny<CD_BF16, 0><<<grid, dim3(kThreads), 0, s>>>(ps, SkMask{});
   } else {
-    if (mode == 1) k_skinny<CD_F16, 1><<<grid, dim3(kThreads), 0, s>>>(ps);
-    else if (mode == 2) k_skinny<CD_F16, 2><<<grid, dim3(kThreads), 0, s>>>(ps);
-    else k_skinny<CD_F16, 0><<<grid, dim3(kThreads), 0, s>>>(ps);
+    if (mode == 1) k_skinny<CD_F16, 1><<<grid, dim3(kThreads), 0, s>>>(ps, SkMask{});
+    else if (mode == 2) k_skinny<CD_F16, 2><<<grid, dim3(kThreads), 0, s>>>(ps, SkMask{});
+    else k_skinny<CD_F16, 0><<<grid, dim3(kThreads), 0, s>>>(ps, SkMask{});
   }
   return check_launch("k_skinny");
 }
@@ -449,12 +523,38 @@ int skinny_many(int cd, const SkSpec* specs, float* const* parts, int* S_out, in
     }
     ProfScope prof(kind, s);
     const dim3 grid(gx, gy, ps.nj);
-    if (cd == CD_BF16) k_skinny<CD_BF16, 0><<<grid, dim3(kThreads), 0, s>>>(ps);
-    else k_skinny<CD_F16, 0><<<grid, dim3(kThreads), 0, s>>>(ps);
+    if (cd == CD_BF16) k_skinny<CD_BF16, 0><<<grid, dim3(kThreads), 0, s>>>(ps, SkMask{});
+    else k_skinny<CD_F16, 0><<<grid, dim3(kThreads), 0, s>>>(ps, SkMask{});
     int rc = check_launch("k_skinny");
     if (rc) return rc;
   }
   return QLORA_OK;
+}
+
+int skinny_drawn(int cd, bool tn, const SkSpec& a, float* part, int* S_out, const SkSpec* b2, float* part2, int* S2,
+                 const Seeded& sd, void* bits, int64_t ldbits, hipStream_t s, int kind) {
+  SkP2 ps = {};
+  int rc = skinny_params(tn, a, part, ps.j[0], S_out);
+  if (rc || (b2 && (rc = skinny_params(tn, *b2, part2, ps.j[1], S2)))) return rc;
+  if (a.bt || (b2 && !tn)) return set_error(QLORA_ERR_UNSUPPORTED, "rank product: form not taken under a mask");
+  ps.nj = b2 ? 2 : 1;
+  ps.nx[0] = (uint32_t)ceil_div(a.P, BP);
+  ps.ny[0] = (uint32_t)*S_out;
+  if (b2) {
+    ps.nx[1] = (uint32_t)ceil_div(b2->P, BP);
+    ps.ny[1] = (uint32_t)*S2;
+  }
+  const SkMask m = {sd, (uint8_t*)bits, 4 * ldbits};
+  const dim3 grid(std::max(ps.nx[0], ps.nx[1]), std::max(ps.ny[0], ps.ny[1]), ps.nj);
+  ProfScope prof(kind, s);
+  if (cd == CD_BF16) {
+    if (tn) k_skinny<CD_BF16, 4><<<grid, dim3(kThreads), 0, s>>>(ps, m);
+    else k_skinny<CD_BF16, 3><<<grid, dim3(kThreads), 0, s>>>(ps, m);
+  } else {
+    if (tn) k_skinny<CD_F16, 4><<<grid, dim3(kThreads), 0, s>>>(ps, m);
+    else k_skinny<CD_F16, 3><<<grid, dim3(kThreads), 0, s>>>(ps, m);
+  }
+  return check_launch("k_skinny");
 }
 
 int skinny(int cd, bool tn, const void* a, int64_t lda, int64_t arows, const void* b, int64_t ldb, int64_t P,

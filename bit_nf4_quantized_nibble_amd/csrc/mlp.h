@@ -30,8 +30,12 @@ inline void gradient_jobs(SkRed& ra, SkRed& rb, float scale, void* d_a, void* d_
     rb.ldcd = rb.R;
   }
 }
-// out = x M, and (bits not null, cols a multiple of 32) M's bits, rows of cols / 32 words.
-int apply_seeded(int cd, const void* x, const Seeded& sd, int64_t rows, int64_t cols, void* out, void* bits, hipStream_t s);
+// out = x M
+int apply_seeded(int cd, const void* x, const Seeded& sd, int64_t rows, int64_t cols, void* out, hipStream_t s);
+// lora.hip: one rank product (and, TN, a second without a mask) whose Aop, x [rows][cols], counts under the
+// drawn mask.  NT: x A^T; TN: bits not null: the mask's bits are left there, rows of ldbits words.
+int skinny_drawn(int cd, bool tn, const SkSpec& a, float* part, int* S_out, const SkSpec* b2, float* part2, int* S2,
+                 const Seeded& sd, void* bits, int64_t ldbits, hipStream_t s, int kind);
 int rank_add_seeded(int cd, void* dx, const Seeded& sd, const void* dt, int64_t ld_dt, const void* a, int32_t r, int64_t M,
                     int64_t K, hipStream_t s);
 
