@@ -25,7 +25,7 @@
 // kernels place its output columns (forward) or add its dX in fp32 (backward).
 #include <algorithm>
 
-#include "mlp.h"
+#include "common.h"
 
 namespace qnf4 {
 namespace {
@@ -324,12 +324,6 @@ int launch_forward_group(const GroupCall& gc, const void* bias, void* y, float* 
 
 int launch_backward_group(const GroupCall& gc, const void* dy, const float* const* t_saved, void* dx,
                           float* const* d_a, float* const* d_b, void* ws, hipStream_t s) {
-  return launch_backward_group_as(gc, dy, t_saved, dx, (void* const*)d_a, (void* const*)d_b, CD_F32, false, ws, s);
-}
-
-// The adapters' gradients in fp32, or (gd = the call's type) rounded into it.
-int launch_backward_group_as(const GroupCall& gc, const void* dy, const float* const* t_saved, void* dx,
-                             void* const* d_a, void* const* d_b, int gd, bool g16, void* ws, hipStream_t s) {
   const GBwd P = plan_gbwd(gc);
   char* w = (char*)ws;
   const LayerCall& c0 = gc.c[0];
@@ -341,8 +335,8 @@ int launch_backward_group_as(const GroupCall& gc, const void* dy, const float* c
       c.ws = w + P.single;
       if ((rc = copy_cols(c.cd, (const char*)dy + gc.off[i] * es, gc.N, w + P.dy, c.w.rows, m, c.w.rows, s)))
         return rc;
-      if ((rc = launch_backward_as(c, nullptr, w + P.dy, t_saved ? t_saved[i] : nullptr, dx ? w + P.dxi : nullptr,
-                                   d_a[i], d_b[i], gd)))
+      if ((rc = launch_backward(c, w + P.dy, t_saved ? t_saved[i] : nullptr, dx ? w + P.dxi : nullptr, d_a[i],
+                                d_b[i])))
         return rc;
       if (dx && (rc = acc_terms(c.cd, w + P.dxi, (float*)(w + P.acc), dx, m * K, i == 0, i + 1 == gc.g, s)))
         return rc;
@@ -425,10 +419,7 @@ int launch_backward_group_as(const GroupCall& gc, const void* dy, const float* c
   }
   if (dx) {
     LayerCall cc = concat_call(gc);
-    rc = g16 ? gemm16_plain(cc.cd, dy, m, K, gc.N, w + P.wdt, w + P.dtcd, gc.RP, w + P.at, gc.RP, nullptr, dx,
-                            QLORA_K_BWD_DX, s)
-             : dense256_dx(cc, dy, w + P.wdt, w + P.dtcd, gc.RP, dx, P.sp, w + P.split, w + P.at);
-    if (rc) return rc;
+    if ((rc = dense256_dx(cc, dy, w + P.wdt, w + P.dtcd, gc.RP, dx, P.sp, w + P.split, w + P.at))) return rc;
   }
   // dA_i = dT_i^T x and dB_i = s_i dY_i^T T0_i: both products in one launch, both
   // reductions in the next
@@ -458,11 +449,14 @@ int launch_backward_group_as(const GroupCall& gc, const void* dy, const float* c
     ra.S = Sa;
     ra.P = K;
     ra.R = c.r;
+    ra.out32 = d_a[i];
+    ra.trans = true;
     rb.part = part2;
     rb.S = Sb;
     rb.P = c.w.rows;
     rb.R = c.r;
-    gradient_jobs(ra, rb, c.scale, d_a[i], d_b[i], gd == CD_F32);
+    rb.sc32 = c.scale;
+    rb.out32 = d_b[i];
     if ((rc = skinny_reduce_jobs(c.cd, ra, &rb, s))) return rc;
   }
   return QLORA_OK;

@@ -39,10 +39,6 @@ int skinny_drawn(int cd, bool tn, const SkSpec& a, float* part, int* S_out, cons
 int rank_add_seeded(int cd, void* dx, const Seeded& sd, const void* dt, int64_t ld_dt, const void* a, int32_t r, int64_t M,
                     int64_t K, hipStream_t s);
 
-// g16: dX by gemm16_plain.
-int launch_backward_group_as(const GroupCall& gc, const void* dy, const float* const* t_saved, void* dx,
-                             void* const* d_a, void* const* d_b, int gd, bool g16, void* ws, hipStream_t s);
-
 // gemv.hip: the gated block's forward of up to 64 tokens (c: gate and up).
 size_t gemv_workspace_bytes(int64_t m, int64_t rows, int64_t cols, int32_t r, int cd);
 bool gemv_gated_ok(const LayerCall* c);
@@ -86,8 +82,8 @@ int planes_forward(const PlanesFwd& q, void* ws, int64_t* need);
 int planes_backward(const PlanesBwd& q, void* ws, int64_t* need);
 // The most that such a call needs, whatever its block size and whichever of its outputs are wanted.
 int64_t planes_workspace(int op, const LayerCall* c, int g, bool seeded);
-// gated.hip: h [m][n] from pre (dh null), or [dg | du] from pre and dh
-int gate(int cd, int act, const void* pre, const void* dh, int64_t m, int64_t n, void* out, hipStream_t s);
+// gated.hip: h [m][n] from pre
+int gate(int cd, int act, const void* pre, int64_t m, int64_t n, void* h, hipStream_t s);
 
 size_t gated_workspace_bytes(int op, const GroupCall& gc);
 int launch_gated_fwd(const GroupCall& gc, int act, const void* bias, void* h, void* pre, float* const* t_save, void* ws,

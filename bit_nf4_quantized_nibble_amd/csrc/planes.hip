@@ -1179,7 +1179,7 @@ int forward(const PlanesFwd& q, char* ws, int64_t* need) {
   }
   if (need) *need = run.used;
   if (run.dry() || run.rc || !gated || !direct) return run.rc;
-  return gate(CD, q.act, z, nullptr, m, n, q.out, c0.stream);
+  return gate(CD, q.act, z, m, n, q.out, c0.stream);
 }
 
 template <int CD>

@@ -125,7 +125,10 @@ def test_gated_workspace(lib):
     g = Gated(lib)
     q = lambda op=0, m=100, cd=1, w=g.w: lib.qlora_gated_workspace_bytes(op, w, m, g.r, cd)
     for op in (0, 1):
-        assert q(op) >= lib.qlora_group_workspace_bytes(op, 2, g.w, 100, g.r, 1) and q(op) % 256 == 0
+        for m in (1, 100, 300, 5000):
+            for cd in (0, 1, 2):
+                assert q(op, m, cd) > 0 and q(op, m, cd) % 256 == 0
+        assert q(op, 5000) > q(op, 300)
     assert q(2) == 0 and q(cd=9) == 0 and q(m=-1) == 0 and q(w=Gated(lib, d1=ndesc(rows=128)).w) == 0
 
 
