@@ -476,7 +476,7 @@ def _check_like(name, t, device, dtype, shape):
         raise ValueError("%s must be a GPU tensor on %s" % (name, device))
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be contiguous and of shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
@@ -575,6 +575,31 @@ def gated_workspace_bytes(op: int, qs, m: int, ranks, dtype) -> int:
     return int(_lib.lib().qlora_gated_workspace_bytes(op, ga.w, m, ga.r, dtype_code(dtype)))
 
 
+_Two = ctypes.c_void_p * 2
+_TwoInts = ctypes.c_int32 * 2
+_TwoFloats = ctypes.c_float * 2
+_TwoWeights = _lib.QloraNf4 * 2
+
+
+def _two(ts):
+    return None if ts is None else _Two(_ptr(ts[0]), _ptr(ts[1]))
+
+
+class _GatedArgs:
+    """ctypes arrays of a gated block's two projections (kept alive with it)."""
+
+    __slots__ = ("descs", "w", "r", "a", "b", "alpha")
+
+    def __init__(self, qs, ranks, lora_as, lora_bs, alphas):
+        self.descs = _TwoWeights(qs[0].descriptor(), qs[1].descriptor())
+        at = ctypes.addressof(self.descs)
+        self.w = _Two(at, at + ctypes.sizeof(_lib.QloraNf4))
+        self.r = _TwoInts(*ranks)
+        self.a = _two(lora_as)
+        self.b = _two(lora_bs)
+        self.alpha = _TwoFloats(float(alphas[0]), float(alphas[1]))
+
+
 def _gated_call(qs, x, lora_as, lora_bs, alphas, act):
     if len(qs) != 2 or len(lora_as) != 2 or len(lora_bs) != 2 or len(alphas) != 2:
         raise ValueError("a gated block takes two projections (gate, up) with an adapter and an alpha each")
@@ -588,7 +613,7 @@ def _gated_call(qs, x, lora_as, lora_bs, alphas, act):
     x2, lead = _flatten(x, qs[0].cols)
     ranks = [_check_adapter(q, a, b, x.device, x.dtype, "[%d]" % i)
              for i, (q, a, b) in enumerate(zip(qs, lora_as, lora_bs))]
-    return x2.contiguous(), lead, ranks, _GroupArgs(qs, lora_as, lora_bs, alphas)
+    return x2.contiguous(), lead, ranks, _GatedArgs(qs, ranks, lora_as, lora_bs, alphas)
 
 
 def linear_fwd_gated(qs, x, lora_as, lora_bs, alphas, act: str = "silu", bias=None, save: bool = False,
@@ -614,7 +639,7 @@ def linear_fwd_gated(qs, x, lora_as, lora_bs, alphas, act: str = "silu", bias=No
         ws = _workspace_on(device, int(lib.qlora_gated_workspace_bytes(_lib.QLORA_OP_FWD, ga.w, m, ga.r, code)), workspace)
         _launch(device, lib.qlora_linear_fwd_gated, ga.w, _ptr(x2), m, ga.a, ga.b, ga.r, ga.alpha,
                 _lib.QLORA_FLAG_RSLORA if rslora else 0, _lib.QLORA_ACTS[act], _ptr(bias), code, _ptr(h), _ptr(pre),
-                _GroupArgs.ptrs(ts), _ptr(ws), ws.numel() * ws.element_size())
+                _two(ts), _ptr(ws), ws.numel() * ws.element_size())
     h = h.view(*lead, rows)
     return (h, pre, ts) if save else h
 
@@ -643,8 +668,8 @@ def linear_bwd_gated(qs, x, dh, lora_as, lora_bs, alphas, pre, act: str = "silu"
     lib, code = _lib.lib(), dtype_code(dt)
     ws = _workspace_on(device, int(lib.qlora_gated_workspace_bytes(_lib.QLORA_OP_BWD, ga.w, m, ga.r, code)), workspace)
     _launch(device, lib.qlora_linear_bwd_gated, ga.w, _ptr(x2), _ptr(dh2), _ptr(pre), m, ga.a, ga.b, ga.r, ga.alpha,
-            _lib.QLORA_FLAG_RSLORA if rslora else 0, _lib.QLORA_ACTS[act], code, _GroupArgs.ptrs(t_saved), gd, _ptr(dx),
-            _GroupArgs.ptrs(das), _GroupArgs.ptrs(dbs), _ptr(ws), ws.numel() * ws.element_size())
+            _lib.QLORA_FLAG_RSLORA if rslora else 0, _lib.QLORA_ACTS[act], code, _two(t_saved), gd, _ptr(dx),
+            _two(das), _two(dbs), _ptr(ws), ws.numel() * ws.element_size())
     return (None if dx is None else dx.view(*lead, cols)), das, dbs
 
 

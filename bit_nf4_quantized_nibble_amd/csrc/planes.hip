@@ -1351,23 +1351,17 @@ int planes_backward(const PlanesBwd& q, void* ws, int64_t* need) {
   return backward<CD_F32>(q, (char*)ws, need);
 }
 
+// A backward that wants dX and forms T itself takes every buffer that another does.
 int64_t planes_workspace(int op, const LayerCall* c, int g, bool seeded) {
   static const Seeded some = {};
-  static const float* const none[2] = {};
   static char out;
-  int64_t most = 0;
+  int64_t need = 0;
   if (op == QLORA_OP_FWD) {
-    PlanesFwd q = {c, g, seeded ? &some : nullptr, 0, nullptr, nullptr, nullptr, nullptr};
-    return planes_forward(q, nullptr, &most) ? 0 : most;
+    const PlanesFwd q = {c, g, seeded ? &some : nullptr, 0, nullptr, nullptr, nullptr, nullptr};
+    return planes_forward(q, nullptr, &need) ? 0 : need;
   }
-  for (int i = 0; i < 4; ++i) {  // T saved or not, dX wanted or not
-    PlanesBwd q = {c, g, seeded ? &some : nullptr, 0, nullptr, nullptr, i & 1 ? none : nullptr, i & 2 ? &out : nullptr,
-                   nullptr, nullptr, CD_F32};
-    int64_t need = 0;
-    if (planes_backward(q, nullptr, &need)) return 0;
-    most = std::max(most, need);
-  }
-  return most;
+  const PlanesBwd q = {c, g, seeded ? &some : nullptr, 0, nullptr, nullptr, nullptr, &out, nullptr, nullptr, CD_F32};
+  return planes_backward(q, nullptr, &need) ? 0 : need;
 }
 
 }  // namespace qnf4
