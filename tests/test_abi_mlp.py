@@ -186,3 +186,14 @@ def test_workspace_queries_of_no_tokens(lib):
             lib.qlora_gated_workspace_bytes(op, g.w, 0, g.r, cd)
     for cd in (1, 2):
         lib.qlora_workspace_bytes(2, 0, 256, 64, 8, cd)
+
+
+def test_operands_past_the_tiles_reach(lib):
+    """A row so long that a tile's rows span 2^31 bytes is refused before anything is launched."""
+    long = lambda cols: ndesc(rows=64, cols=cols)
+    for cd, cols in ((0, 1 << 22), (1, 1 << 24)):
+        g = Gated(lib, d0=long(cols), d1=long(cols))
+        assert g.fwd(cd=cd, m=20 if cd == 0 else 200) == UNSUP and lib.qlora_last_error()
+        assert g.bwd(cd=cd) == UNSUP
+        assert drop_fwd(lib, d=long(cols), cd=cd) == UNSUP and drop_bwd(lib, d=long(cols), cd=cd) == UNSUP
+        assert lib.qlora_gated_workspace_bytes(1, g.w, 100, g.r, cd) == 0
