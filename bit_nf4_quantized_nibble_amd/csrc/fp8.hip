@@ -478,18 +478,23 @@ __global__ __launch_bounds__(512, 1) void k_fp8_full(F8 p) {
     auto work = [&](auto shape) {
       using T = decltype(shape);
       const char* coef = coefs + set * Coef<Full>::BYTES;
-      Copies8<T> cp(p, cur, ring, coef, wave, lane);
+      // the lane counts as unknown here and after the contraction: addresses formed ahead of all tiles would
+      // be kept through it and pushed out to memory there
+      int ln = lane;
+      asm volatile("" : "+v"(ln));
+      Copies8<T> cp(p, cur, ring, coef, wave, ln);
       cp.all(lds + T::STAGE, 1);
       Acc<T> acc;
       zero<T>(acc);
-      contract<T, Float8<CD == CD_F32>>(acc, lds, cp, wave, lane);
+      contract<T, Float8<CD == CD_F32>>(acc, lds, cp, wave, ln);
+      asm volatile("" : "+v"(ln));
       if (nxt.rows) {
         uint32_t* to = (uint32_t*)(coefs + (set ^ 1) * Coef<Full>::BYTES);
         if (tid < nc) to[tid] = c0;
         if (tid + 512 < nc) to[tid + 512] = c1;
         first_stage(nxt);
       }
-      Writer<CD, T>::run(p, cur, acc, coef, lds + kStaging + wave * 32 * Writer<CD, T>::RB, wave, lane);
+      Writer<CD, T>::run(p, cur, acc, coef, lds + kStaging + wave * 32 * Writer<CD, T>::RB, wave, ln);
       asm volatile("" ::: "memory");
       // this wave's copies of the next first stage, older than the stores, have landed
       wait_vmcnt<Writer<CD, T>::stores()>();
