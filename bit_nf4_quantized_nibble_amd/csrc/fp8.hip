@@ -643,6 +643,10 @@ __global__ __launch_bounds__(64 * NWV) void k_fp8_few(F8 p, Raw raw) {
 
 size_t al(size_t b) { return (b + 255) & ~(size_t)255; }
 
+// Slices of a contraction: where the smallest tiles are few and the rows long, up to eight, of six lines
+// of 128 codes or more, as long as the pieces are not more than the compute units (64 x 1024 x 4096 and
+// 16 x 4096 x 14336 are as fast in one piece; 64 x 4096 x 14336 18.1 us in four, 23.0 in two; 256 x 1024 x 14336
+// 18.7 in four, 24.6 in one).
 constexpr int kSplitItems = 256;
 int slices(int64_t tiles, int64_t ld) {
   const int64_t lines = ld >> 7;
@@ -654,12 +658,24 @@ int slices(int64_t tiles, int64_t ld) {
 enum Form { FEW, SMALL, LOW, MID, WIDE, FULL };
 
 bool few_tokens(int64_t m) { return m <= 16; }
-bool long_rows_of_few(int64_t n, int64_t ld) { return ld > 8192 && n <= 2048; }
-bool fused_rows(int64_t m) { return m <= 4; }
+// Up to four tokens the product brings x to 8 bits itself, every workgroup anew, and saves a launch, until what it
+// repeats costs more (us, this way and with the launch: 1 token of 4096 x 4096 9.5 and 12.5, of
+// 4096 x 14336 11.8 and 14.9; 4 tokens of 8192 x 4096 10.8 and 12.2, of 14336 x 4096 16.5 and 15.4, of
+// 4096 x 14336 18.2 and 15.4; 8 tokens of 4096 x 4096 11.7 and 10.5 without the launch's cost on the host).
+bool fused_rows(int64_t m, int64_t n, int64_t ld) { return m <= 4 && m * n * ld <= 1LL << 27; }
+// Few tokens on tiles all the same: rows so long that the few-token kernel's waves, a row of W each, are too few; and
+// in 16 bits so many rows that the smallest tiles fill the card (16 tokens of 14336 x 4096: 14.7 us against
+// 17.0; but of 8192 x 4096 14.1 against 12.7, of 4096 x 14336 31 against 18, in fp32 24 against 18).
+bool few_on_tiles(int64_t n, int64_t ld, int cd) {
+  return (ld > 8192 && n <= 2048) || (cd != CD_F32 && ceil_div(n, 64) >= 192 && ld <= 4096);
+}
 
+// us by form, bf16, m x n x k: 512 x 2048 x 2048 SMALL 10.9, LOW 12.0, MID 15.0; 1024 x 2048 x 2048 14.0, 13.2, 15.9;
+// 1024 x 4096 x 4096 37, 28, 25.9, WIDE 31.7, FULL 40.8; 2048 x 4096 x 4096 67, 53, 48, 39.9, 46.0;
+// 4096 x 4096 x 4096 123, 97, 90, 74, 69.9: the smallest tiles that take one round.
 Form form_of(int64_t m, int64_t n, int64_t ld, int cd) {
   const int64_t cus = cu_count();
-  if (few_tokens(m)) return long_rows_of_few(n, ld) && !fused_rows(m) ? SMALL : FEW;
+  if (few_tokens(m)) return few_on_tiles(n, ld, cd) && !fused_rows(m, n, ld) ? SMALL : FEW;
   auto one_round = [&](int64_t tm, int64_t tn) { return ceil_div(m, tm) * ceil_div(n, tn) <= cus; };
   if (one_round(64, 64)) return SMALL;
   if (one_round(64, 128)) return LOW;
@@ -667,7 +683,6 @@ Form form_of(int64_t m, int64_t n, int64_t ld, int cd) {
   // fp32 results' bf16 fragments and block sums do not fit the registers beside 256 x 256 sums
   return one_round(128, 256) || cd == CD_F32 ? WIDE : FULL;
 }
-
 // Workspace: the tokens' codes and exponents, and the sums of a cut contraction.
 struct Plan {
   size_t off_scale = 0, off_part = 0, total = 0;
@@ -681,7 +696,7 @@ Plan plan_fp8(const qlora_fp8_t* w, int64_t m, int cd) {
   P.stride = round_up(m, 64);
   P.off_scale = al((size_t)(m * ld));
   P.off_part = P.total = P.off_scale + al((size_t)(ceil_div(ld, 512) * P.stride * 4));
-  if (m == 0 || w->rows == 0 || (few_tokens(m) && (fused_rows(m) || !long_rows_of_few(w->rows, ld)))) return P;
+  if (m == 0 || w->rows == 0 || (few_tokens(m) && (fused_rows(m, w->rows, ld) || !few_on_tiles(w->rows, ld, cd)))) return P;
   int64_t tiles = ceil_div(m, Small::TM) * ceil_div(w->rows, Small::TN), tile = Small::TM * Small::TN;
   P.split = slices(tiles, ld);
   const int64_t mid = ceil_div(m, Mid::TM) * ceil_div(w->rows, Mid::TN);
@@ -770,7 +785,7 @@ int product(const F8& p, Form f, Form cut, hipStream_t s) {
 
 template <int CD>
 int linear_cd(const F8& p, const void* x, int64_t ldx, int64_t cols, Form cut, hipStream_t s) {
-  if (fused_rows(p.m)) {
+  if (fused_rows(p.m, p.n, p.ld)) {
     ProfScope prof(QLORA_K_FP8_GEMM, s);
     return few_rows<CD, true>(p, Raw{x, ldx, (int)cols}, s);
   }

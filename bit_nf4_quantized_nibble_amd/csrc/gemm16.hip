@@ -394,7 +394,10 @@ int run(const G16& p, int act, int kind, hipStream_t s) {
   return check_launch("k_gemm16");
 }
 
-// The smallest tiles that fit the compute units in one round, the largest beyond.
+// The smallest tiles that fit the compute units in one round, the largest beyond (us by Low, Mid, Wide, the
+// largest, of the whole call, bf16: gated 512 x 2048 x 2048 36, 38, 46, 58, 2048 x 4096 x 1024 79, 77, 70, 59; plain
+// 512 x 4096 x 4096 44, 51, 65, 85, 1024 x 4096 x 4096 62, 57, 67, 86, 2048 x 4096 x 4096 106, 96, 84, 92; masked
+// 1024 x 4096 x 4096 -, 73, 83, 108, 2048 x 4096 x 4096 -, 115, 102, 119).
 template <int CD, int MODE>
 int run_cd(const G16& p, int act, int kind, hipStream_t s) {
   auto one_round = [&](int64_t tm, int64_t tn) {

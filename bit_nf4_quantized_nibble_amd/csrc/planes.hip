@@ -973,7 +973,9 @@ struct Run {
   static int64_t low_tiles(int64_t m, int64_t n) {
     return std::max<int64_t>(1, ceil_div(m, Low::TM) * ceil_div(n, Low::TN));  // a query may have no tokens
   }
-  // Slices of a contraction: workgroups for every compute unit, at least four stages to each.
+  // Slices of a contraction: workgroups for every compute unit, at least four stages to each (bf16 calls of 16 to 333
+  // tokens take 2 to 6 % more at one stage, the same at six; fp32 ones are best at two of the longer stages that
+  // decode: 42 tokens of 1472 x 1280, seeded backward, 41, 39.1, 42.0, 47.5 us at 1, 2, 4, 6).
   static int slices(int64_t m, int64_t n, int steps) {
     return (int)std::max<int64_t>(1, std::min<int64_t>({ceil_div(256, low_tiles(m, n)), steps / 4, 32}));
   }
@@ -981,7 +983,7 @@ struct Run {
   static int decode_slices(int64_t m, int64_t n, int steps) {
     const int64_t at_once = 256 * (CD == CD_F32 ? 1 : m <= FewRows::TM ? 3 : 2);
     const int64_t tiles = ceil_div(n, 128) * ceil_div(m, CD == CD_F32 || m <= FewRows::TM ? 64 : 128);
-    return (int)std::max<int64_t>(1, std::min<int64_t>({at_once / std::max<int64_t>(1, tiles), steps / 4, 32}));
+    return (int)std::max<int64_t>(1, std::min<int64_t>({at_once / std::max<int64_t>(1, tiles), steps / (CD == CD_F32 ? 2 : 4), 32}));
   }
   // partial sums of p for S slices, and of `more` - 1 products alike and `extra` slices of another behind them
   float* parts(Prod& p, int S, int extra = 0, int more = 1) {
@@ -1067,8 +1069,12 @@ struct Run {
   }
 };
 
-// Tiles from which a product is not cut: its output leaves from the product itself.
+// Tiles from which a product is not cut: its output leaves from the product itself (gated backward, us cut
+// and not: 600 x 1501 x 960 bf16 53 and 66, fp32 98 and 172; 1000 x 3001 x 1984 bf16 113 and 107, fp32 372 and 329).
 constexpr int64_t kDirectTiles = 160;
+// Larger tiles from this many on (fp32, us with the small ones and these: seeded forward of 2000 x 2944 x 2048, 192
+// of them, 237 and 202, of 4000 x 3968 x 4096, 512, 1115 and 860; gated backward of 2000 x 3001 x 2048, 128, 532 and 605).
+constexpr int64_t kWideTiles = 176;
 // Rows up to which W~ is decoded by the product that reads it: every 128 rows (64 in fp32) decode it
 // again.  Written first and read back, the gated backward of 256 rows takes 122 us against 87 (4096 x 4096),
 // 385 against 229 (14336 x 4096).
@@ -1166,7 +1172,7 @@ int forward(const PlanesFwd& q, char* ws, int64_t* need) {
     }
     run.add(p, run.seg(t[i], b[i], q.c[i].r));
   }
-  run.big = direct && ceil_div(m, Wide::TM) * ceil_div(n, Wide::TN) * q.g >= 224;
+  run.big = direct && ceil_div(m, Wide::TM) * ceil_div(n, Wide::TN) * q.g >= kWideTiles;
   run.run_products(QLORA_K_FWD_GEMM, q.c, q.g);
   if (!direct) {
     main[0].S += 1;  // and the low-rank part
@@ -1306,7 +1312,7 @@ int backward(const PlanesBwd& q, char* ws, int64_t* need) {
     for (int i = 0; i < q.g; ++i) run.add(p, run.seg(dtr[i], at[i], q.c[i].r));
     p.out = q.dx;
     p.ldo = K;
-    run.big = ceil_div(m, Wide::TM) * ceil_div(K, Wide::TN) >= 224;
+    run.big = ceil_div(m, Wide::TM) * ceil_div(K, Wide::TN) >= kWideTiles;
     run.run_products(QLORA_K_BWD_DX, q.c, q.g);
   }
   for (int i = 0; i < q.g && !run.dry(); ++i) {
