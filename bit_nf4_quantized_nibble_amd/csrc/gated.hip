@@ -523,6 +523,7 @@ int launch_gated_fwd(const GroupCall& gc, int act, const void* bias, void* h, vo
 
 int launch_gated_bwd(const GroupCall& gc, int act, const void* dh, const void* pre, const float* const* t_saved, void* dx,
                      void* const* d_a, void* const* d_b, int gd, void* ws, hipStream_t s) {
+  if (t_saved && !(t_saved[0] && t_saved[1])) t_saved = nullptr;  // both are formed where one is missing
   if (tuned_bwd(gc)) return backward_tiled(gc, act, dh, pre, t_saved, dx, d_a, d_b, gd, (char*)ws, s);
   const PlanesBwd q = {gc.c, 2, nullptr, act, dh, pre, t_saved, dx, d_a, d_b, gd};
   return planes_backward(q, ws, nullptr);

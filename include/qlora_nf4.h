@@ -237,8 +237,7 @@ int qlora_linear_bwd_group(int32_t g, const qlora_nf4_t* const* w, const void* x
  * projection, equal rows and cols):
  *   g = x Wg~^T + s_g (x Ag^T) Bg^T (+ bias[0 .. rows)),  u likewise (+ bias[rows .. 2 rows)),
  *   h [m, rows] = act(g) u.
- * h is rounded once, from fp32, where the tiled path runs (bf16 / f16, more than 64 tokens, rows a
- * multiple of 64, ranks <= 64, the layouts of qlora_linear_fwd_group's); elsewhere g and u are
+ * h is rounded once, from fp32 (many tokens with a rank above 64 in a 16-bit cd: g and u are
  * rounded into cd first.  pre (nullable) [m, 2 rows] receives [g | u] in cd, t_save (nullable
  * array of nullable pointers) T0_i = x A_i^T fp32 [m, r_i]: what the backward takes.
  * act: QLORA_ACT_SILU z / (1 + exp(-z)); QLORA_ACT_GELU z Phi(z); QLORA_ACT_GELU_TANH
@@ -260,7 +259,8 @@ int qlora_linear_fwd_gated(const qlora_nf4_t* const* w, const void* x, int64_t m
  *   dg = dh u act'(g),  du = dh act(g)   (fp32, rounded into cd)
  * and the group's backward of [dg | du]: dX [m, cols] (skipped when dx == NULL), dA_i, dB_i.
  * gd: type of the adapters' gradients, QLORA_F32 (what qlora_adamw_step takes) or cd.
- * t_saved (nullable array of nullable pointers): the forward's T0_i, else recomputed.
+ * t_saved (nullable array of nullable pointers): the forward's T0_i, else recomputed (both where
+ * one is missing).  Every layout qlora_nf4_quantize accepts, up to rows of 2^31 bytes / 128.
  * ws: qlora_gated_workspace_bytes(QLORA_OP_BWD, ...) bytes.
  * Errors: as qlora_linear_bwd_group and qlora_linear_fwd_gated, QLORA_ERR_DTYPE for another gd.
  */
@@ -410,7 +410,8 @@ int qlora_linear_bwd_dropout(const qlora_nf4_t* w, const void* x, const void* dy
                              float* d_a, float* d_b, void* ws, size_t ws_bytes, void* stream);
 
 /*
- * The layer with LoRA dropout whose mask is drawn from a counter and never stored.  The
+ * The layer with LoRA dropout whose mask is drawn from a counter and not stored between calls (a
+ * backward may keep its bits, one to an element, in the workspace while it runs).  The
  * results are those of the calls above with the mask
  *   M[i, k] = w >= round(65536 p),  w the 16-bit half k % 8 (low halves first) of the four words
  *   Philox 4x32-10 (Salmon et al., SC 2011) gives for the counter {k / 8, i, offset low, offset

@@ -209,3 +209,22 @@ def test_two_graphs_and_two_streams(M, N, K, cd):
     torch.cuda.synchronize()
     assert all(torch.equal(u, v) for u, v in zip(here, gated(x0)))
     assert all(torch.equal(u, v) for u, v in zip(there, drop(x0)))
+
+
+@pytest.mark.parametrize("M,N,K,cd", [(50, 96, 80, "bf16"), (700, 2112, 2048, "bf16")])
+def test_a_saved_product_of_one_projection_only(M, N, K, cd):
+    """The C call with T0 of the gate alone: both are formed again."""
+    say("layouts: one T0", M, N, K, cd)
+    L, o, q = layer(M, N, K, 8, cd, 32, 256, 11)
+    x, dy, a, b = L.x.cuda(), L.dY.cuda(), [L.A.cuda()] * 2, [L.B.cuda()] * 2
+    h, pre, ts = qn.linear_fwd_gated((q, q), x, a, b, [8.0, 8.0], save=True)
+    want = qn.linear_bwd_gated((q, q), x, dy, a, b, [8.0, 8.0], pre)
+    ga = qn._GatedArgs((q, q), [8, 8], a, b, [8.0, 8.0])
+    new = lambda *shape: torch.empty(*shape, dtype=torch.float32).cuda()
+    dx, da, db = torch.empty_like(x), [new(8, K), new(8, K)], [new(N, 8), new(N, 8)]
+    ws = torch.empty(qn.gated_workspace_bytes(qn._lib.QLORA_OP_BWD, (q, q), M, (8, 8), x.dtype), dtype=torch.uint8).cuda()
+    for t in ((ts[0].data_ptr(), None), (None, ts[1].data_ptr())):
+        qn._launch(x.device, qn._lib.lib().qlora_linear_bwd_gated, ga.w, x.data_ptr(), dy.data_ptr(), pre.data_ptr(), M, ga.a, ga.b,
+                   ga.r, ga.alpha, 0, 0, qn.dtype_code(x.dtype), qn._Two(*t), 0, dx.data_ptr(), qn._two(da), qn._two(db),
+                   ws.data_ptr(), ws.numel())
+        assert torch.equal(dx, want[0]) and all(torch.equal(u, v) for u, v in zip(da + db, want[1] + want[2]))
