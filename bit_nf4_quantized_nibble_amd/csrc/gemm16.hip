@@ -62,7 +62,7 @@ constexpr int copying() { return T::TM == 256 && T::NS == 2 ? 4 : T::NW; }
 // logical chunk that lies there.  begin() sets up what a stage's copies read.
 template <class T, int MODE>
 struct Copies16 {
-  static constexpr int NW = copying<T>(), PER_A = T::TM / 8 / NW, PER = (T::TM + T::TN) / 8 / NW;
+  static constexpr int NW = copying<T>(), PER_A = T::TM / 8 / NW, PER = (T::TM + T::TN) / 8 / NW, WAVES = NW, EARLY = PER;
   const G16& p;
   Place pl;
   int KM, KT, wave, lane, chunk;

@@ -123,7 +123,7 @@ struct Tile {
   static constexpr int WMB = WMB_, WNB = WNB_, NWM = NWM_, NWN = NWN_, NS = NS_;
   static constexpr int NW = NWM * NWN, TM = 32 * WMB * NWM, TN = 32 * WNB * NWN;
   static constexpr int STAGE = (TM + TN) * 128;  // LDS bytes of a stage
-  static constexpr int PER_A = TM / 8 / NW;      // copies (8 rows each) of A rows per wave and stage
+  static constexpr int PER_A = TM / 8 / NW;      // copies (8 rows each) of A rows per wave and stage (all waves copying)
   static constexpr int PER = (TM + TN) / 8 / NW;
   static_assert((TM / 8) % NW == 0 && (TN / 8) % NW == 0 && NW % 2 == 0, "copies split evenly");
   static constexpr int LDS = NS * STAGE;
@@ -148,9 +148,13 @@ __device__ __forceinline__ void zero(Acc<T>& acc) {
 // stage before is done (what scales() has read becomes the scales in use: no product waits for the
 // read).  On entry stage 0 lies in LDS for every wave and the copies of stages 1 .. NS - 1 are requested;
 // on return the LDS is free.
-template <class T, class KIND, class C>
-__device__ __forceinline__ void contract(Acc<T>& acc, char* lds, C& cp, int wave, int lane) {
-  constexpr int WMB = T::WMB, WNB = T::WNB, NMF = WMB * WNB, SUB = KIND::SUB, SETS = KIND::SETS;
+// Where fewer waves copy than multiply (C::WAVES), C::EARLY of a stage's copies are requested in the last sub-step
+// of the stage before the last (on entry: of stage 1) and the rest beside the next stage's first products:
+// the waves that share their SIMD keep the matrix pipe busy while they go out.
+template <class T, class KIND, bool COPY, class C>
+__device__ __forceinline__ void stages(Acc<T>& acc, char* lds, C& cp, int wave, int lane) {
+  constexpr int WMB = T::WMB, WNB = T::WNB, NMF = WMB * WNB, SUB = KIND::SUB, SETS = KIND::SETS, LATE = C::PER - C::EARLY;
+  static_assert(LATE == 0 || (T::NS == 2 && SUB > 1), "late copies land in the stage they are requested in");
   // where in the last sub-step the barrier stands: before the first read of the next stage
   constexpr int BAR = SETS == 2 || NMF < 4 ? 0 : NMF < 8 ? 1 : 2;
   static_assert(BAR < WMB, "the first fragment is replaced after the barrier");
@@ -173,7 +177,7 @@ __device__ __forceinline__ void contract(Acc<T>& acc, char* lds, C& cp, int wave
   for (int u = 0; u < cp.KT; ++u) {
     char* st = lds + buf * T::STAGE;
     const int nbuf = buf + 1 == T::NS ? 0 : buf + 1;
-    const char* nx = lds + nbuf * T::STAGE;
+    char* nx = lds + nbuf * T::STAGE;
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int ks = 0; ks < SUB; ++ks) {
@@ -185,9 +189,9 @@ __device__ __forceinline__ void contract(Acc<T>& acc, char* lds, C& cp, int wave
       for (int t = 0; t < NMF; ++t) {
         if (last && t == BAR) {
           wait_lgkm0();
-          wait_vmcnt<(T::NS - 2) * T::PER>();  // this wave's copies of stage u + 1
+          wait_vmcnt<(T::NS - 2) * C::PER>();  // this wave's copies of stage u + 1
           barrier_only();
-          cp.begin(u + T::NS);
+          if (COPY) cp.begin(u + T::NS);
         }
         const int i = t % WMB, j = t / WMB;
         KIND::mma(acc[i][j], fb[set][j], fa[set][i], sb[0], sa[0][i]);
@@ -199,17 +203,31 @@ __device__ __forceinline__ void contract(Acc<T>& acc, char* lds, C& cp, int wave
           if (i == WMB - 1) frag(0, from, nks, j);
           if (j == WNB - 1) frag(0, from, nks, WNB + i);
         }
-        if (last && t >= BAR) {
-          if (t == BAR) cp.scales(u + 1, sa[1], sb[1]);
+        if (last && t == BAR) cp.scales(u + 1, sa[1], sb[1]);
+        if (COPY && last && t >= BAR) {
 #pragma unroll
-          for (int q = 0; q < T::PER; ++q)
-            if (BAR + q * (NMF - BAR) / T::PER == t) cp.one(st, u + T::NS, q);
+          for (int q = 0; q < C::EARLY; ++q)
+            if (BAR + q * (NMF - BAR) / C::EARLY == t) cp.one(st, u + T::NS, q);
+        }
+        if (COPY && LATE > 0 && ks == 0) {
+#pragma unroll
+          for (int q = 0; q < LATE; ++q)
+            if (q * NMF / (LATE > 0 ? LATE : 1) == t) cp.one(nx, u + 1, C::EARLY + q);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
     }
     cp.shift(u + 1, sa, sb);
     buf = nbuf;
+  }
+}
+template <class T, class KIND, class C>
+__device__ __forceinline__ void contract(Acc<T>& acc, char* lds, C& cp, int wave, int lane) {
+  if constexpr (C::WAVES < T::NW) {
+    if (wave < C::WAVES) stages<T, KIND, true>(acc, lds, cp, wave, lane);
+    else stages<T, KIND, false>(acc, lds, cp, wave, lane);
+  } else {
+    stages<T, KIND, true>(acc, lds, cp, wave, lane);
   }
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();  // every copy has ended and every wave is past its reads
