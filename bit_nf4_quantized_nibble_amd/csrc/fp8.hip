@@ -177,7 +177,6 @@ template <class T>
 struct Copies8 {
   // of the eight waves of the 256-column tiles with two buffers, the first four (one to a SIMD) copy
   static constexpr int WAVES = T::NW == 8 && T::NS == 2 ? 4 : T::NW, PER_A = T::TM / 8 / WAVES, PER = (T::TM + T::TN) / 8 / WAVES;
-  static constexpr int EARLY = WAVES < T::NW ? PER * 5 / 8 : PER;
   const uint8_t *a, *b;
   const uint32_t* sa;
   int64_t abytes, bbytes, stride, left;
@@ -223,12 +222,11 @@ struct Copies8 {
     const rsrc_t r = a_side ? make_rsrc(a, in ? abytes : 0) : make_rsrc(b, in ? bbytes : 0);
     copy16(r, stage_lds + (wave + WAVES * i) * 1024, off + (a_side ? i : i - PER_A) * step, stage * 128);
   }
-  __device__ __forceinline__ void all(char* stage_lds, int stage, int n = PER) const {
+  __device__ __forceinline__ void all(char* stage_lds, int stage) const {
     if (WAVES < T::NW && wave >= WAVES) return;
     begin(stage);
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (i < n) one(stage_lds, stage, i);
+    for (int i = 0; i < PER; ++i) one(stage_lds, stage, i);
   }
   __device__ __forceinline__ void scales(int stage, int (&s)[T::WMB], int& sb) const {
     const char* w = ring + ((stage >> 2) & 1) * 1024 + row * 4;
@@ -488,7 +486,7 @@ __global__ __launch_bounds__(512, 1) void k_fp8_full(F8 p) {
       int ln = lane;
       asm volatile("" : "+v"(ln));
       Copies8<T> cp(p, cur, ring, coef, wave, ln);
-      cp.all(lds + T::STAGE, 1, Copies8<T>::EARLY);
+      cp.all(lds + T::STAGE, 1);
       Acc<T> acc;
       zero<T>(acc);
       contract<T, Float8<CD == CD_F32>>(acc, lds, cp, wave, ln);

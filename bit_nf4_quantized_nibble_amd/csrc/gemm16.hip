@@ -53,7 +53,7 @@ struct Place {
 template <class T, int MODE>
 constexpr int cols_of() { return MODE == GATED ? T::TN / 2 : T::TN; }
 
-// Waves that copy: four of the largest tile's eight (contract_two), else all.
+// Waves that copy: four of the largest tile's eight, else all.
 template <class T>
 constexpr int copying() { return T::TM == 256 && T::NS == 2 ? 4 : T::NW; }
 
@@ -62,7 +62,7 @@ constexpr int copying() { return T::TM == 256 && T::NS == 2 ? 4 : T::NW; }
 // logical chunk that lies there.  begin() sets up what a stage's copies read.
 template <class T, int MODE>
 struct Copies16 {
-  static constexpr int NW = copying<T>(), PER_A = T::TM / 8 / NW, PER = (T::TM + T::TN) / 8 / NW, WAVES = NW, EARLY = PER;
+  static constexpr int NW = copying<T>(), PER_A = T::TM / 8 / NW, PER = (T::TM + T::TN) / 8 / NW, WAVES = NW;
   const G16& p;
   Place pl;
   int KM, KT, wave, lane, chunk;
@@ -339,18 +339,12 @@ __global__ __launch_bounds__(64 * T::NW, WGS) void k_gemm16(G16 p, int act) {
       Copies16<U, MODE> cp(p, cur, wave, ln);
       Acc<U> acc;
       zero<U>(acc);
-      if constexpr (copying<U>() < U::NW) {
-        wait_lgkm0();
-        barrier_only();  // the coefficients are there, the staging of the tile before is free
-        contract_two<U, Half16<CD>>(acc, lds, cp, wave, ln);
-      } else {
-        wait_vmcnt<0>();
-        wait_lgkm0();
-        barrier_only();  // and stage 0
+      wait_vmcnt<0>();
+      wait_lgkm0();
+      barrier_only();  // stage 0 and the coefficients are there, the staging of the tile before is free
 #pragma unroll
-        for (int s = 1; s < U::NS; ++s) cp.all(lds + s * U::STAGE, s);
-        contract<U, Half16<CD>>(acc, lds, cp, wave, ln);
-      }
+      for (int s = 1; s < U::NS; ++s) cp.all(lds + s * U::STAGE, s);
+      contract<U, Half16<CD>>(acc, lds, cp, wave, ln);
       asm volatile("" : "+v"(ln));
       if constexpr (MODE == MASKED) {
         add_masked<CD, U>(acc, p, cur, lds + cp.KM % U::NS * U::STAGE, wave, ln);

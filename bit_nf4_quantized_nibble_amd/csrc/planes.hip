@@ -349,7 +349,7 @@ struct Prods {
 
 template <class T>
 struct CopiesP {
-  static constexpr int NW = T::NW, WAVES = NW, PER = T::PER, EARLY = PER;
+  static constexpr int NW = T::NW, WAVES = NW, PER = T::PER;
   const Prod& p;
   int KT, left, g, k, q, lane;
   int64_t m0, n0, rows, cols;

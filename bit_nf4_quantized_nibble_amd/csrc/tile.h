@@ -148,16 +148,15 @@ __device__ __forceinline__ void zero(Acc<T>& acc) {
 // stage before is done (what scales() has read becomes the scales in use: no product waits for the
 // read).  On entry stage 0 lies in LDS for every wave and the copies of stages 1 .. NS - 1 are requested;
 // on return the LDS is free.
-// Where fewer waves copy than multiply (C::WAVES), C::EARLY of a stage's copies are requested in the last sub-step
-// of the stage before the last (on entry: of stage 1) and the rest beside the next stage's first products:
-// the waves that share their SIMD keep the matrix pipe busy while they go out.
+// Where fewer waves copy than multiply (C::WAVES: the largest tiles, one wave of each SIMD's two), the others keep the
+// matrix pipe busy while the copies go out (all waves copying: the 8-bit product of 4096 x 14336 x 4096 222 us in
+// place of 208; copies spread into the next stage's first products 211: they arrive later).
 template <class T, class KIND, bool COPY, class C>
 __device__ __forceinline__ void stages(Acc<T>& acc, char* lds, C& cp, int wave, int lane) {
-  constexpr int WMB = T::WMB, WNB = T::WNB, NMF = WMB * WNB, SUB = KIND::SUB, SETS = KIND::SETS, LATE = C::PER - C::EARLY;
-  static_assert(LATE == 0 || (T::NS == 2 && SUB > 1), "late copies land in the stage they are requested in");
+  constexpr int WMB = T::WMB, WNB = T::WNB, NMF = WMB * WNB, SUB = KIND::SUB, SETS = KIND::SETS;
   // where in the last sub-step the barrier stands: before the first read of the next stage
-  constexpr int BAR = SETS == 2 || NMF < 4 ? 0 : NMF < 8 ? 1 : 2;
-  static_assert(BAR < WMB, "the first fragment is replaced after the barrier");
+  constexpr int BAR = SETS == 2 ? (C::WAVES < T::NW ? 2 : 0) : NMF < 4 ? 0 : NMF < 8 ? 1 : 2;
+  static_assert(SETS == 2 || BAR < WMB, "the first fragment is replaced after the barrier");
   const int h = lane >> 5, r32 = lane & 31;
   const int wm = (wave / T::NWN) * 32 * WMB, wn = (wave % T::NWN) * 32 * WNB;
   const int xr = swz(r32);
@@ -198,7 +197,7 @@ __device__ __forceinline__ void stages(Acc<T>& acc, char* lds, C& cp, int wave, 
         if constexpr (SETS == 2) {
 #pragma unroll
           for (int q = 0; q < WMB + WNB; ++q)
-            if (q * NMF / (WMB + WNB) == t) frag(next, from, nks, q);
+            if ((last ? BAR + q * (NMF - BAR) / (WMB + WNB) : q * NMF / (WMB + WNB)) == t) frag(next, from, nks, q);
         } else {
           if (i == WMB - 1) frag(0, from, nks, j);
           if (j == WNB - 1) frag(0, from, nks, WNB + i);
@@ -206,13 +205,8 @@ __device__ __forceinline__ void stages(Acc<T>& acc, char* lds, C& cp, int wave, 
         if (last && t == BAR) cp.scales(u + 1, sa[1], sb[1]);
         if (COPY && last && t >= BAR) {
 #pragma unroll
-          for (int q = 0; q < C::EARLY; ++q)
-            if (BAR + q * (NMF - BAR) / C::EARLY == t) cp.one(st, u + T::NS, q);
-        }
-        if (COPY && LATE > 0 && ks == 0) {
-#pragma unroll
-          for (int q = 0; q < LATE; ++q)
-            if (q * NMF / (LATE > 0 ? LATE : 1) == t) cp.one(nx, u + 1, C::EARLY + q);
+          for (int q = 0; q < C::PER; ++q)
+            if (BAR + q * (NMF - BAR) / C::PER == t) cp.one(st, u + T::NS, q);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
@@ -231,80 +225,6 @@ __device__ __forceinline__ void contract(Acc<T>& acc, char* lds, C& cp, int wave
   }
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();  // every copy has ended and every wave is past its reads
-}
-
-// The same for the largest 16-bit tile, two buffers, eight waves of which the first four (one to a
-// SIMD) copy, one copy to a product.  One barrier per stage, in its last sub-step: there the next stage
-// has landed and every wave holds its last fragments of this one, so that the first fragments of the next
-// stage are read beside the last products, and this buffer takes the copies of the stage after it, from
-// there into the second sub-step of the next stage.  cp counts copies by four waves.
-template <class T, class KIND>
-struct Frags {
-  typename KIND::frag_t a[2][T::WMB], b[2][T::WNB];
-  int arow, brow, xr, h;
-  // fragment t in the order of first use: b0 a0, the other b's, the other a's
-  __device__ __forceinline__ void read(int set, const char* st, int ks, int t) {
-    const int i = t == 0 ? 0 : t >= 2 && t <= T::WNB ? t - 1 : -1, j = t == 1 ? 0 : t - T::WNB;
-    if (i >= 0) b[set][i] = KIND::read(st + brow + i * 32 * 128, ks, h, xr);
-    else a[set][j] = KIND::read(st + arow + j * 32 * 128, ks, h, xr);
-  }
-};
-constexpr int kBarrierAt = 2;  // products of the last sub-step before the barrier
-template <class T, class KIND, bool COPY, class C>
-__device__ __forceinline__ void stage_two(Acc<T>& acc, char* lds, int u, C& cp, Frags<T, KIND>& f) {
-  constexpr int WMB = T::WMB, WNB = T::WNB, NMF = WMB * WNB, EARLY = NMF - kBarrierAt;
-  static_assert(T::NS == 2 && T::TM == 256 && T::TN == 256 && NMF == 8 && KIND::SUB == 4, "the largest tile");
-  char *st = lds + (u & 1) * T::STAGE, *nx = lds + ((u & 1) ^ 1) * T::STAGE;
-  __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-  for (int ks = 0; ks < 4; ++ks) {
-    const int set = ks & 1;
-#pragma unroll
-    for (int t = 0; t < NMF; ++t) {
-      const int i = t / WNB, j = t % WNB;
-      if (ks == 3 && t == kBarrierAt) {
-        __builtin_amdgcn_s_waitcnt(0);  // this wave's copies of stage u + 1 and its reads of this one
-        barrier_only();
-        if (COPY) cp.begin(u + 2);
-      }
-      KIND::mma(acc[i][j], f.b[set][j], f.a[set][i], 0, 0);
-#pragma unroll
-      for (int q = 0; q < WMB + WNB; ++q) {
-        if (ks < 3 && q * NMF / (WMB + WNB) == t) f.read(set ^ 1, st, ks + 1, q);
-        if (ks == 3 && kBarrierAt + q * EARLY / (WMB + WNB) == t) f.read(0, nx, 0, q);
-      }
-      if (COPY && ks == 3 && t >= kBarrierAt) cp.one(st, u + 2, t - kBarrierAt);
-      if (COPY && 8 * ks + t < 16 - EARLY) cp.one(nx, u + 1, EARLY + 8 * ks + t);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  }
-}
-template <class T, class KIND, bool COPY, class C>
-__device__ __forceinline__ void stages_two(Acc<T>& acc, char* lds, C& cp, Frags<T, KIND>& f) {
-  __builtin_amdgcn_s_waitcnt(0);  // this wave's copies of stage 0
-  barrier_only();
-  if (COPY) {
-    cp.begin(1);
-#pragma unroll
-    for (int i = 0; i < T::WMB * T::WNB - kBarrierAt; ++i) cp.one(lds + T::STAGE, 1, i);
-  }
-#pragma unroll
-  for (int t = 0; t < T::WMB + T::WNB; ++t) f.read(0, lds, 0, t);
-  for (int u = 0; u < cp.KT; ++u) stage_two<T, KIND, COPY>(acc, lds, u, cp, f);
-}
-// On entry the copying waves have requested stage 0; on return the LDS is free.
-template <class T, class KIND, class C>
-__device__ __forceinline__ void contract_two(Acc<T>& acc, char* lds, C& cp, int wave, int lane) {
-  const int r32 = lane & 31;
-  Frags<T, KIND> f;
-  f.h = lane >> 5;
-  f.xr = swz(r32);
-  f.arow = ((wave / T::NWN) * 32 * T::WMB + r32) * 128;
-  f.brow = (T::TM + (wave % T::NWN) * 32 * T::WNB + r32) * 128;
-  if (wave < 4) stages_two<T, KIND, true>(acc, lds, cp, f);
-  else stages_two<T, KIND, false>(acc, lds, cp, f);
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
 }
 
 // Position of workgroup b among n when each XCD (workgroups b, b + 8, ...) takes a
