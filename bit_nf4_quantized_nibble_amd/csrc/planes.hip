@@ -1204,17 +1204,22 @@ int backward(const PlanesBwd& q, char* ws, int64_t* need) {
   const bool whole = direct && !q.sd;  // dX leaves from one product
   const bool saved = q.t_saved != nullptr;
 
-  Planes d[2], dt_[2], wt[2], at[2], bt[2], t0t[2], dtr[2], dtt[2], a[2], xm;
+  Planes d[2], dr[2], dt_[2], wt[2], at[2], bt[2], t0t[2], dtr[2], dtt[2], a[2], xm;
   for (int i = 0; i < q.g; ++i) {
     const LayerCall& c = q.c[i];
     if (gated) {
       Pack& j = run.pack(i ? SRC_UP : SRC_GATE, q.pre, m, n);
       j.dh = q.dy;
-      d[i] = run.rowwise(j);
+      // d B takes what the rounding of d to 16 bits leaves as a second plane: dA is the product of a small sum, whose
+      // terms cancel
+      dr[i] = run.rowwise(j, Run<CD>::kRankPlanes);
+      d[i] = dr[i];
+      d[i].n = Run<CD>::kPlanes;
       dt_[i] = run.across(j);
     } else {
       Pack& j = run.pack(SRC_CD, q.dy, m, n);
       d[i] = Run<CD>::kPlanes == 1 && n % 64 == 0 ? run.as_is(q.dy, n) : run.rowwise(j);
+      dr[i] = d[i];
       dt_[i] = run.across(j);
     }
     bt[i] = run.across(run.pack(SRC_CD, c.lora_b, n, c.r));
@@ -1248,7 +1253,7 @@ int backward(const PlanesBwd& q, char* ws, int64_t* need) {
   };
   for (int i = 0; i < q.g; ++i) {
     Prod& p = run.product(m, q.c[i].r);
-    run.add(p, run.seg(d[i], bt[i], n));
+    run.add(p, run.seg(dr[i], bt[i], n));
     run.parts(p, run.slices(m, p.n, p.steps));
     rank[i] = p;
     if (saved) {
