@@ -259,6 +259,7 @@ __global__ __launch_bounds__(kThreads) void k_pad_rows(PadRows a, PadRows b, int
 bool tuned_bwd(const GroupCall& gc) {
   const LayerCall &c0 = gc.c[0], &c1 = gc.c[1];
   if (c0.m <= 128 || c0.m * c0.w.rows * c0.w.cols <= 1LL << 32) return false;
+  if (!skinny_reaches(c0.m, 2 * c0.w.rows) || !skinny_reaches(c0.m, c0.w.cols)) return false;
   return c0.cd != CD_F32 && c0.w.rows % 64 == 0 && fast_layout(c0.w) && fast_layout(c1.w) && skinny_ok(c0.cd, c0.r) &&
          skinny_ok(c1.cd, c1.r) && gemm16_ok(c0.cd, c0.m, c0.w.cols, 2 * c0.w.rows) && dense256_ok(c0, true) &&
          dense256_ok(c1, true);

@@ -1009,7 +1009,8 @@ bool planes_seeded(int op, const LayerCall& c) {
   const bool small = op == QLORA_OP_FWD
                          ? c.m <= 64 || (c.m <= 128 && n <= 2 * K) || (n * K <= 1 << 22 && c.m * n * K <= 1LL << 33)
                          : c.m <= 128 || c.m * n * K <= 1LL << 31;
-  const bool tuned = !small && c.cd != CD_F32 && fast_layout(c.w) && (op == QLORA_OP_FWD || c.w.rows % 64 == 0) && skinny_ok(c.cd, c.r);
+  const bool reach = skinny_reaches(c.m, K) && (op == QLORA_OP_FWD || skinny_reaches(c.m, n));
+  const bool tuned = !small && reach && c.cd != CD_F32 && fast_layout(c.w) && (op == QLORA_OP_FWD || c.w.rows % 64 == 0) && skinny_ok(c.cd, c.r);
   return !tuned && !(c.flags & (QLORA_FLAG_FUSED | QLORA_FLAG_DEQUANT_GEMM));
 }
 // What it may need: a query does not know the block size.

@@ -32,6 +32,8 @@ inline void gradient_jobs(SkRed& ra, SkRed& rb, float scale, void* d_a, void* d_
 }
 // out = x M
 int apply_seeded(int cd, const void* x, const Seeded& sd, int64_t rows, int64_t cols, void* out, hipStream_t s);
+// Whether the rank-product kernels reach all of a 16-bit matrix: their offsets lie below 2^31 bytes.
+inline bool skinny_reaches(int64_t rows, int64_t ld) { return round_up(rows, 64) * ld * 2 < (1LL << 31); }
 // lora.hip: one rank product (and, TN, a second without a mask) whose Aop, x [rows][cols], counts under the
 // drawn mask.  NT: x A^T; TN: bits not null: the mask's bits are left there, rows of ldbits words.
 int skinny_drawn(int cd, bool tn, const SkSpec& a, float* part, int* S_out, const SkSpec* b2, float* part2, int* S2,

@@ -228,3 +228,51 @@ def test_a_saved_product_of_one_projection_only(M, N, K, cd):
                    ga.r, ga.alpha, 0, 0, qn.dtype_code(x.dtype), qn._Two(*t), 0, dx.data_ptr(), qn._two(da), qn._two(db),
                    ws.data_ptr(), ws.numel())
         assert torch.equal(dx, want[0]) and all(torch.equal(u, v) for u, v in zip(da + db, want[1] + want[2]))
+
+
+def close(got, want, what):
+    """Two results of different kernels, each within 5e-3 of the exact one, on the GPU in row blocks."""
+    num = den = 0.0
+    for u, v in zip(got.split(1 << 14), want.split(1 << 14)):
+        num += (u.double() - v.double()).square().sum().item()
+        den += v.double().square().sum().item()
+    assert num ** 0.5 <= 1e-2 * den ** 0.5, (what, (num / den) ** 0.5)
+
+
+def test_activations_past_two_gibibytes():
+    """Offsets past 2^31 bytes in pre, dg and du (gated) and in x (dropout): the call against its two halves."""
+    M, N, K = 270336, 2048, 128
+    say("layouts: large", M, N, K)
+    L, o, q = layer(8, N, K, 8, "bf16", 64, 256, 13)
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    draw = lambda *shape: torch.randn(*shape, generator=gen, device="cuda", dtype=torch.bfloat16)
+    x, dh, a, b = draw(M, K), draw(M, N), [L.A.cuda()] * 2, [L.B.cuda()] * 2
+    f = lambda x: qn.linear_fwd_gated((q, q), x, a, b, [16.0, 16.0], save=True)
+    g = lambda x, dh, pre, ts: qn.linear_bwd_gated((q, q), x, dh, a, b, [16.0, 16.0], pre, t_saved=ts)
+    half = M // 2
+    h, pre, ts = f(x)
+    dx, da, db = g(x, dh, pre, ts)
+    sums = [0, 0]
+    for i in (slice(0, half), slice(half, M)):
+        h2, pre2, ts2 = f(x[i])
+        dx2, da2, db2 = g(x[i], dh[i], pre2, ts2)
+        close(h[i], h2, "h"), close(pre[i], pre2, "pre"), close(dx[i], dx2, "dX")
+        sums = [sums[0] + da2[0], sums[1] + db2[1]]
+    close(da[0], sums[0], "dA"), close(db[1], sums[1], "dB")
+    del h, pre, ts, dx, h2, pre2, ts2, dx2, dh
+
+    M, N, K = 266240, 64, 4096  # the mask counts rows, so the second half has another one: rows are compared
+    L, o, q = layer(8, N, K, 8, "bf16", 64, 256, 14)
+    x, dy, sd = draw(M, K), draw(M, N), torch.tensor([1, 2], dtype=torch.int64).cuda()
+    args = (L.A.cuda(), L.B.cuda(), 16.0, 0.25, sd)
+    y, t0 = qn.linear_fwd_dropout(q, x, *args, save_t=True)
+    dx, da, db = qn.linear_bwd_dropout(q, x, dy, *args, t_saved=t0)
+    x[half:] = 0
+    dy[half:] = 0
+    y2, t2 = qn.linear_fwd_dropout(q, x[:half], *args, save_t=True)
+    dx2, da2, db2 = qn.linear_bwd_dropout(q, x[:half], dy[:half], *args, t_saved=t2)
+    close(y[:half], y2, "y"), close(t0[:half], t2, "T0"), close(dx[:half], dx2, "dX")
+    y, t0 = qn.linear_fwd_dropout(q, x, *args, save_t=True)
+    dx, da, db = qn.linear_bwd_dropout(q, x, dy, *args, t_saved=t0)
+    close(da, da2, "dA"), close(db, db2, "dB")
+    assert not y[half:].any() and not dx[half:].any()
