@@ -1,5 +1,5 @@
-// tile.h -- the tiled contraction that the 8-bit floating-point product (fp8.hip) and the gated
-// block's GEMMs (gated.hip) share, on gfx950.
+// tile.h -- the tiled contraction that the 8-bit floating-point product (fp8.hip), the 16-bit GEMMs
+// (gemm16.hip) and the products of planes (planes.hip) share, on gfx950.
 //
 // A workgroup forms a TM x TN tile: NWM x NWN waves, each with WMB x WNB blocks of a 32 x 32 matrix
 // instruction.  The contraction advances 128 bytes per stage (128 codes of 8 bits, 64 16-bit
