@@ -399,8 +399,6 @@ int fwd_impl(const qlora_nf4_t* w, const void* x, int64_t m, const void* lora_a,
   if ((rc = check_aligned(who, "y, bias, t_save and the dropout mask", {y, bias, t_save, mask}))) return rc;
   if (m == 0) return QLORA_OK;
   if (mask || sd) flags |= QLORA_FLAG_DROPOUT;
-  if ((rc = check_ws(ws, ws_bytes, fwd_workspace_bytes(m, w->rows, w->cols, r, cd, flags), who))) return rc;
-  if ((rc = check_tables(who))) return rc;
   LayerCall c;
   c.w = make_w(w);
   c.cd = cd;
@@ -416,6 +414,8 @@ int fwd_impl(const qlora_nf4_t* w, const void* x, int64_t m, const void* lora_a,
   c.ws = ws;
   c.ws_bytes = ws_bytes;
   c.stream = (hipStream_t)stream;
+  const size_t need = sd ? seeded_workspace_bytes(QLORA_OP_FWD, c) : fwd_workspace_bytes(m, w->rows, w->cols, r, cd, flags);
+  if ((rc = check_ws(ws, ws_bytes, need, who)) || (rc = check_tables(who))) return rc;
   return sd ? launch_forward_seeded(c, *sd, y, t_save) : launch_forward(c, y, t_save);
 }
 
@@ -430,8 +430,6 @@ int bwd_impl(const qlora_nf4_t* w, const void* x, const void* dy, int64_t m, con
     return rc;
   if (m == 0) return set_error(QLORA_ERR_SHAPE, "%s: m must be >= 1 (dA, dB would be all zero)", who);
   if (mask || sd) flags |= QLORA_FLAG_DROPOUT;
-  if ((rc = check_ws(ws, ws_bytes, bwd_workspace_bytes(m, w->rows, w->cols, r, cd, flags), who))) return rc;
-  if ((rc = check_tables(who))) return rc;
   LayerCall c;
   c.w = make_w(w);
   c.cd = cd;
@@ -447,6 +445,8 @@ int bwd_impl(const qlora_nf4_t* w, const void* x, const void* dy, int64_t m, con
   c.ws = ws;
   c.ws_bytes = ws_bytes;
   c.stream = (hipStream_t)stream;
+  const size_t need = sd ? seeded_workspace_bytes(QLORA_OP_BWD, c) : bwd_workspace_bytes(m, w->rows, w->cols, r, cd, flags);
+  if ((rc = check_ws(ws, ws_bytes, need, who)) || (rc = check_tables(who))) return rc;
   return launch_backward_as(c, sd, dy, t_saved, dx, d_a, d_b, gd);
 }
 

@@ -1013,9 +1013,16 @@ bool planes_seeded(int op, const LayerCall& c) {
   const bool tuned = !small && reach && c.cd != CD_F32 && fast_layout(c.w) && (op == QLORA_OP_FWD || c.w.rows % 64 == 0) && skinny_ok(c.cd, c.r);
   return !tuned && !(c.flags & (QLORA_FLAG_FUSED | QLORA_FLAG_DEQUANT_GEMM));
 }
-// What it may need: a query does not know the block size.
-int64_t planes_seeded_bytes(int op, int64_t m, int64_t rows, int64_t cols, int32_t r, int cd, int32_t flags) {
-  if (!(flags & QLORA_FLAG_DROPOUT)) return 0;
+
+size_t seeded_workspace_bytes(int op, const LayerCall& c) {
+  if (planes_seeded(op, c)) return (size_t)planes_workspace(op, &c, 1, true);
+  if (op == QLORA_OP_BWD) return (size_t)plan_bwd(c.m, c.w.rows, c.w.cols, c.r, c.cd, c.flags).total;
+  return (size_t)plan_fwd(c.m, c.w.rows, c.w.cols, c.r, c.cd, c.flags | (seeded_g16(c) ? QLORA_FLAG_DEQUANT_GEMM : 0)).total;
+}
+// The most that a seeded call needs in any layout: a query does not know the block size.  Its plan depends on the layout in two
+// things, whether the tuned kernels take it and whether a product may decode the weight (which saves the copy of W~ but
+// takes more slices, so neither plan is always the larger): blocks across rows, and blocks of 32 where the rows hold whole ones.
+size_t seeded_layouts_bytes(int op, int64_t m, int64_t rows, int64_t cols, int32_t r, int cd, int32_t flags) {
   LayerCall c = {};
   c.m = m;
   c.w.rows = rows;
@@ -1023,8 +1030,15 @@ int64_t planes_seeded_bytes(int op, int64_t m, int64_t rows, int64_t cols, int32
   c.r = r;
   c.cd = cd;
   c.flags = flags;
-  c.w.bs = 2;  // not the tuned kernels'
-  return planes_seeded(op, c) ? planes_workspace(op, &c, 1, true) : 0;
+  c.w.bs = 2;
+  c.w.bs_shift = 1;
+  size_t most = seeded_workspace_bytes(op, c);
+  if (cols % 64 == 0) {
+    c.w.bs = 32;
+    c.w.bs_shift = 5;
+    most = std::max(most, seeded_workspace_bytes(op, c));
+  }
+  return most;
 }
 
 size_t fwd_workspace_bytes(int64_t m, int64_t rows, int64_t cols, int32_t r, int cd, int32_t flags) {
@@ -1032,17 +1046,16 @@ size_t fwd_workspace_bytes(int64_t m, int64_t rows, int64_t cols, int32_t r, int
   // the query does not see the block size): room for both.  At most 16 tokens the
   // GEMM path is the generic engine, which needs only T and the rank-product partial
   // sums (the start of its plan).
-  FwdPlan P = plan_fwd(m, rows, cols, r, cd, flags);
-  if (flags & QLORA_FLAG_DROPOUT && !(flags & QLORA_FLAG_FUSED))  // the seeded call's
-    P.total = std::max(P.total, plan_fwd(m, rows, cols, r, cd, flags | QLORA_FLAG_DEQUANT_GEMM).total);
-  if (!gemv_candidate(m, flags))
-    return (size_t)std::max(P.total, planes_seeded_bytes(QLORA_OP_FWD, m, rows, cols, r, cd, flags));
+  const FwdPlan P = plan_fwd(m, rows, cols, r, cd, flags);
+  if (flags & QLORA_FLAG_DROPOUT)
+    return std::max((size_t)P.total, seeded_layouts_bytes(QLORA_OP_FWD, m, rows, cols, r, cd, flags));
+  if (!gemv_candidate(m, flags)) return (size_t)P.total;
   return std::max(gemv_workspace_bytes(m, rows, cols, r, cd), (size_t)(m <= kGemvMaxM ? P.off_wd : P.total));
 }
 
 size_t bwd_workspace_bytes(int64_t m, int64_t rows, int64_t cols, int32_t r, int cd, int32_t flags) {
-  return (size_t)std::max(plan_bwd(m, rows, cols, r, cd, flags).total,
-                          planes_seeded_bytes(QLORA_OP_BWD, m, rows, cols, r, cd, flags));
+  const size_t total = (size_t)plan_bwd(m, rows, cols, r, cd, flags).total;
+  return flags & QLORA_FLAG_DROPOUT ? std::max(total, seeded_layouts_bytes(QLORA_OP_BWD, m, rows, cols, r, cd, flags)) : total;
 }
 
 bool gemv_route(const LayerCall& c) {

@@ -30,6 +30,8 @@ inline void gradient_jobs(SkRed& ra, SkRed& rb, float scale, void* d_a, void* d_
     rb.ldcd = rb.R;
   }
 }
+// What such a call needs in its weight's layout (c.flags holds QLORA_FLAG_DROPOUT).
+size_t seeded_workspace_bytes(int op, const LayerCall& c);
 // out = x M
 int apply_seeded(int cd, const void* x, const Seeded& sd, int64_t rows, int64_t cols, void* out, hipStream_t s);
 // Whether the rank-product kernels reach all of a 16-bit matrix: their offsets lie below 2^31 bytes.
@@ -82,7 +84,7 @@ struct PlanesBwd {
 // need not null: only the workspace's size is wanted (pointers are not read).
 int planes_forward(const PlanesFwd& q, void* ws, int64_t* need);
 int planes_backward(const PlanesBwd& q, void* ws, int64_t* need);
-// The most that such a call needs, whatever its block size and whichever of its outputs are wanted.
+// The most that such a call needs in its weights' layout, whichever of its outputs are wanted (0: none that fits).
 int64_t planes_workspace(int op, const LayerCall* c, int g, bool seeded);
 // gated.hip: h [m][n] from pre
 int gate(int cd, int act, const void* pre, int64_t m, int64_t n, void* h, hipStream_t s);

@@ -1350,19 +1350,25 @@ int backward(const PlanesBwd& q, char* ws, int64_t* need) {
 
 }  // namespace
 
-// A call is sized before its first launch, so that one that does not fit is refused whole.
-int planes_forward(const PlanesFwd& q, void* ws, int64_t* need) {
+// A call is sized before its first launch, so that one that does not fit, a launch or the workspace, is refused whole.
+template <class Q>
+int check_size(const Q& q, int (*plan)(const Q&, void*, int64_t*)) {
   int64_t n;
+  if (const int rc = plan(q, nullptr, &n)) return rc;
+  if ((uint64_t)n > q.c->ws_bytes)
+    return set_error(QLORA_ERR_WORKSPACE, "layer: workspace %zu bytes < %lld required", q.c->ws_bytes, (long long)n);
+  return QLORA_OK;
+}
+int planes_forward(const PlanesFwd& q, void* ws, int64_t* need) {
   if (!need)
-    if (const int rc = planes_forward(q, nullptr, &n)) return rc;
+    if (const int rc = check_size(q, planes_forward)) return rc;
   if (q.c[0].cd == CD_BF16) return forward<CD_BF16>(q, (char*)ws, need);
   if (q.c[0].cd == CD_F16) return forward<CD_F16>(q, (char*)ws, need);
   return forward<CD_F32>(q, (char*)ws, need);
 }
 int planes_backward(const PlanesBwd& q, void* ws, int64_t* need) {
-  int64_t n;
   if (!need)
-    if (const int rc = planes_backward(q, nullptr, &n)) return rc;
+    if (const int rc = check_size(q, planes_backward)) return rc;
   if (q.c[0].cd == CD_BF16) return backward<CD_BF16>(q, (char*)ws, need);
   if (q.c[0].cd == CD_F16) return backward<CD_F16>(q, (char*)ws, need);
   return backward<CD_F32>(q, (char*)ws, need);
