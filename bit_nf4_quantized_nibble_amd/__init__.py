@@ -250,7 +250,7 @@ def linear_fwd(q: NF4Weight, x, lora_a, lora_b, alpha: float, bias=None, save_t:
         raise ValueError("t_out must hold %d x %d fp32 elements" % (m, r))
     flags = _flags(rslora, path)
     mk, p = _dropout_args(dropout_mask, dropout_p, x2)
-    qflags = flags | (_lib.QLORA_FLAG_DROPOUT if mk is not None else 0)
+    qflags = flags | (_lib.QLORA_FLAG_DROPOUT | _lib.QLORA_FLAG_STORED_MASK if mk is not None else 0)
     ws = _workspace(workspace_bytes(_lib.QLORA_OP_FWD, m, q.rows, q.cols, r, dt, qflags), x.device, workspace)
     d = q.descriptor()
     if mk is None:
@@ -452,7 +452,7 @@ def linear_bwd(q: NF4Weight, x, dy, lora_a, lora_b, alpha: float, t_saved=None, 
         raise ValueError("t_saved must hold %d x %d fp32 elements" % (m, r))
     flags = _flags(rslora, path)
     mk, p = _dropout_args(dropout_mask, dropout_p, x2)
-    qflags = flags | (_lib.QLORA_FLAG_DROPOUT if mk is not None else 0)
+    qflags = flags | (_lib.QLORA_FLAG_DROPOUT | _lib.QLORA_FLAG_STORED_MASK if mk is not None else 0)
     ws = _workspace(workspace_bytes(_lib.QLORA_OP_BWD, m, q.rows, q.cols, r, dt, qflags), x.device, workspace)
     d = q.descriptor()
     if mk is None:

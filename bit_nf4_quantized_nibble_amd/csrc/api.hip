@@ -379,7 +379,9 @@ size_t qlora_workspace_bytes(int32_t op, int64_t m, int64_t rows, int64_t cols, 
   if (m < 0 || rows < 0 || cols < 0 || r < 1 || !valid_cd(cd)) return 0;
   const int32_t flags = op >> QLORA_OP_FLAGS_SHIFT;
   op &= (1 << QLORA_OP_FLAGS_SHIFT) - 1;
-  if (flags & ~(QLORA_FLAG_RSLORA | QLORA_FLAG_FUSED | QLORA_FLAG_DEQUANT_GEMM | QLORA_FLAG_DROPOUT)) return 0;
+  if (flags & ~(QLORA_FLAG_RSLORA | QLORA_FLAG_FUSED | QLORA_FLAG_DEQUANT_GEMM | QLORA_FLAG_DROPOUT | QLORA_FLAG_STORED_MASK))
+    return 0;
+  if ((flags & QLORA_FLAG_STORED_MASK) && !(flags & QLORA_FLAG_DROPOUT)) return 0;
   if (op == QLORA_OP_FWD) return fwd_workspace_bytes(m, rows, cols, r, cd, flags);
   if (op == QLORA_OP_FWD_CACHED) {
     if (flags & ~QLORA_FLAG_RSLORA || (cd != CD_BF16 && cd != CD_F16)) return 0;
@@ -398,7 +400,7 @@ int fwd_impl(const qlora_nf4_t* w, const void* x, int64_t m, const void* lora_a,
   if (!y) return set_error(QLORA_ERR_INVALID_ARG, "%s: null y", who);
   if ((rc = check_aligned(who, "y, bias, t_save and the dropout mask", {y, bias, t_save, mask}))) return rc;
   if (m == 0) return QLORA_OK;
-  if (mask || sd) flags |= QLORA_FLAG_DROPOUT;
+  if (mask || sd) flags |= QLORA_FLAG_DROPOUT | (mask ? QLORA_FLAG_STORED_MASK : 0);
   LayerCall c;
   c.w = make_w(w);
   c.cd = cd;
@@ -429,7 +431,7 @@ int bwd_impl(const qlora_nf4_t* w, const void* x, const void* dy, int64_t m, con
   if ((rc = check_aligned(who, "dy, dx, d_a, d_b, t_saved and the dropout mask", {dy, dx, d_a, d_b, t_saved, mask})))
     return rc;
   if (m == 0) return set_error(QLORA_ERR_SHAPE, "%s: m must be >= 1 (dA, dB would be all zero)", who);
-  if (mask || sd) flags |= QLORA_FLAG_DROPOUT;
+  if (mask || sd) flags |= QLORA_FLAG_DROPOUT | (mask ? QLORA_FLAG_STORED_MASK : 0);
   LayerCall c;
   c.w = make_w(w);
   c.cd = cd;

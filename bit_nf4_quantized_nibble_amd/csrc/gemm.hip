@@ -533,8 +533,9 @@ BwdPlan plan_bwd(int64_t m, int64_t rows, int64_t cols, int32_t r, int cd, int32
   P.off_xm = P.off_wdt + (P.dense ? al(rows * cols * es) : 0);
   const bool drop = (flags & QLORA_FLAG_DROPOUT) != 0;
   P.off_zero = P.off_xm + (drop ? al(m * cols * es) : 0);
-  // (or the mask's bits)
-  P.off_split = P.off_zero + (drop ? al(m * std::max<int64_t>(P.r_pad * es, ceil_div(cols, 8))) : 0);
+  // (or a drawn mask's bits)
+  const int64_t bits = flags & QLORA_FLAG_STORED_MASK ? 0 : ceil_div(cols, 8);
+  P.off_split = P.off_zero + (drop ? al(m * std::max<int64_t>(P.r_pad * es, bits)) : 0);
   P.dsp = dense_split(m, cols, rows, !P.dense);
   // A^T [cols][r_pad] in cd: the W-side rows of the dense dX GEMM's low-rank tail
   P.off_at = P.off_split + (big_tiles(cd) ? al(dense_split_bytes(P.dsp)) : 0);
@@ -1047,7 +1048,7 @@ size_t fwd_workspace_bytes(int64_t m, int64_t rows, int64_t cols, int32_t r, int
   // GEMM path is the generic engine, which needs only T and the rank-product partial
   // sums (the start of its plan).
   const FwdPlan P = plan_fwd(m, rows, cols, r, cd, flags);
-  if (flags & QLORA_FLAG_DROPOUT)
+  if ((flags & QLORA_FLAG_DROPOUT) && !(flags & QLORA_FLAG_STORED_MASK))
     return std::max((size_t)P.total, seeded_layouts_bytes(QLORA_OP_FWD, m, rows, cols, r, cd, flags));
   if (!gemv_candidate(m, flags)) return (size_t)P.total;
   return std::max(gemv_workspace_bytes(m, rows, cols, r, cd), (size_t)(m <= kGemvMaxM ? P.off_wd : P.total));
@@ -1055,7 +1056,8 @@ size_t fwd_workspace_bytes(int64_t m, int64_t rows, int64_t cols, int32_t r, int
 
 size_t bwd_workspace_bytes(int64_t m, int64_t rows, int64_t cols, int32_t r, int cd, int32_t flags) {
   const size_t total = (size_t)plan_bwd(m, rows, cols, r, cd, flags).total;
-  return flags & QLORA_FLAG_DROPOUT ? std::max(total, seeded_layouts_bytes(QLORA_OP_BWD, m, rows, cols, r, cd, flags)) : total;
+  if (!(flags & QLORA_FLAG_DROPOUT) || (flags & QLORA_FLAG_STORED_MASK)) return total;
+  return std::max(total, seeded_layouts_bytes(QLORA_OP_BWD, m, rows, cols, r, cd, flags));
 }
 
 bool gemv_route(const LayerCall& c) {

@@ -77,7 +77,8 @@ enum {
   QLORA_FLAG_RSLORA = 1,       /* scale = alpha / sqrt(r) instead of alpha / r */
   QLORA_FLAG_FUSED = 2,
   QLORA_FLAG_DEQUANT_GEMM = 4,
-  QLORA_FLAG_DROPOUT = 8       /* workspace queries only: size for the *_dropout calls */
+  QLORA_FLAG_DROPOUT = 8,      /* workspace queries only: size for every *_dropout call */
+  QLORA_FLAG_STORED_MASK = 16  /* with QLORA_FLAG_DROPOUT: for those with a stored mask alone, which need less */
 };
 
 /* Workspace queries: op is QLORA_OP_FWD, QLORA_OP_BWD or QLORA_OP_FWD_CACHED, OR'ed with the call's
@@ -394,8 +395,8 @@ size_t qlora_stack_workspace_bytes(const qlora_stack_layer_t* layers, int32_t n_
  * with dT = s dY B.  mask: device u8 [m, cols], nonzero = kept (the caller draws it,
  * e.g. Bernoulli(1 - p), and passes the same mask to both calls); 0 <= p < 1.
  * t_save / t_saved hold x_d A^T (1 - p), i.e. (x M) A^T.  The arguments are otherwise
- * those of qlora_linear_fwd / qlora_linear_bwd; the workspace is
- * qlora_workspace_bytes(op | (flags | QLORA_FLAG_DROPOUT) << QLORA_OP_FLAGS_SHIFT, ...)
+ * those of qlora_linear_fwd / qlora_linear_bwd; the workspace is qlora_workspace_bytes(op |
+ * (flags | QLORA_FLAG_DROPOUT | QLORA_FLAG_STORED_MASK) << QLORA_OP_FLAGS_SHIFT, ...)
  * (x M is staged there; calls with m <= 16 take the GEMM path, not the decode GEMV).
  * Errors: those of qlora_linear_fwd / _bwd, plus QLORA_ERR_INVALID_ARG for a null
  * mask or p outside [0, 1).
@@ -420,7 +421,8 @@ int qlora_linear_bwd_dropout(const qlora_nf4_t* w, const void* x, const void* dy
  * aligned, read on the device when the kernels run: the backward takes the values the forward had, a
  * captured call draws another mask at each replay that finds other values there, and calls with
  * other offsets under one seed draw independent masks.  m and cols below 2^32.
- * gd: type of the adapters' gradients, QLORA_F32 or cd.  Workspaces as for the calls above.
+ * gd: type of the adapters' gradients, QLORA_F32 or cd.  Workspaces: qlora_workspace_bytes(op |
+ * (flags | QLORA_FLAG_DROPOUT) << QLORA_OP_FLAGS_SHIFT, ...), which covers a weight of any block size.
  * Errors: those of the calls above, QLORA_ERR_INVALID_ARG for a null or unaligned seed, and
  * QLORA_ERR_DTYPE for another gd.
  */

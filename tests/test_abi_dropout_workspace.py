@@ -75,3 +75,38 @@ def test_seeded_query_covers_every_layout(lib):
         flags = rng.choice((0, 0, 0, 2, 4))
         need = refused(lib, op, w, m, r, cd, flags)
         assert 0 < need <= query(lib, op, w, m, r, cd, flags | _lib.QLORA_FLAG_DROPOUT), (op, m, rows, cols, r, cd, block, flags)
+
+
+def stored(lib, op, w, m, r, cd, flags=0):
+    """The bytes that the call with a stored mask asks for when it is refused for its workspace."""
+    d = ctypes.byref(w)
+    if op == 0:
+        status = lib.qlora_linear_fwd_dropout(d, FAKE, m, FAKE, FAKE, r, 16.0, flags, None, cd, FAKE, 0.1, FAKE, None, FAKE, 0,
+                                              None)
+    else:
+        status = lib.qlora_linear_bwd_dropout(d, FAKE, FAKE, m, FAKE, FAKE, r, 16.0, flags, cd, FAKE, 0.1, None, FAKE, FAKE,
+                                              FAKE, FAKE, 0, None)
+    assert status == -5
+    return int(re.search(r"(\d+) required", lib.qlora_last_error().decode()).group(1))
+
+
+@pytest.mark.parametrize("flags", [0, 2, 4])
+def test_a_stored_mask_needs_what_its_own_pass_stages(lib, flags):
+    """The layer's plan without dropout, x M and (backward) the zeros in dT's place; nothing of the seeded call's."""
+    up = lambda v: (v + 255) // 256 * 256
+    for m, rows, cols, r, cd in ((100, 4096, 4096, 16, 0), (70, 14336, 4096, 64, 1), (4096, 4096, 4096, 64, 0),
+                                 (4096, 4096, 14336, 64, 1), (300, 1000, 704, 12, 2), (65, 77, 130, 5, 1)):
+        w, es = weight(rows, cols, 2), 2 if cd else 4
+        both = _lib.QLORA_FLAG_DROPOUT | _lib.QLORA_FLAG_STORED_MASK | flags
+        assert stored(lib, 0, w, m, r, cd, flags) == query(lib, 0, w, m, r, cd, both) \
+            == query(lib, 0, w, m, r, cd, flags) + up(m * cols * es)
+        assert stored(lib, 1, w, m, r, cd, flags) == query(lib, 1, w, m, r, cd, both) \
+            == query(lib, 1, w, m, r, cd, flags) + up(m * cols * es) + up(m * ((r + 7) // 8 * 8) * es)
+        for op in OPS:
+            assert query(lib, op, w, m, r, cd, both) <= query(lib, op, w, m, r, cd, flags | _lib.QLORA_FLAG_DROPOUT)
+
+
+def test_the_stored_mask_s_flag_stands_beside_dropout_s(lib):
+    for op in OPS:
+        assert query(lib, op, weight(64, 64, 64), 100, 8, 1, _lib.QLORA_FLAG_STORED_MASK) == 0
+    assert query(lib, 2, weight(64, 64, 64), 100, 8, 1, 24) == 0

@@ -61,3 +61,21 @@ def test_guards(M, N, K, r, cd, block, group):
     h, pre, ts = guarded(lambda ws: qn.linear_fwd_gated(*args, save=True, workspace=ws), fwd)
     for kw in (dict(), dict(t_saved=ts), dict(need_dx=False), dict(t_saved=ts, need_dx=False, grad_dtype=dt)):
         guarded(lambda ws: qn.linear_bwd_gated(args[0], x, dy, *args[2:], pre, workspace=ws, **kw), bwd)
+
+
+@pytest.mark.parametrize("M,N,K,r,cd,block,group", [(64, 4096, 512, 16, "f32", 64, 0), (1, 1408, 512, 8, "bf16", 64, 256),
+                                                    (300, 1088, 1024, 64, "bf16", 64, 256), (129, 320, 77, 9, "f16", 4, 0)])
+def test_guards_with_a_stored_mask(M, N, K, r, cd, block, group):
+    say("workspace guards, stored mask", M, N, K, r, cd, block, group)
+    L = inputs.random_layer(M, N, K, r, seed=M + N, cd=cd, with_dy=True, block_size=block, double_quant=group > 0,
+                            dq_group=group or 256)
+    q = qn.quantize(L.W.cuda(), block, group > 0, group or 256)
+    flags = qn._lib.QLORA_FLAG_DROPOUT | qn._lib.QLORA_FLAG_STORED_MASK
+    fwd, bwd = (qn.workspace_bytes(op, M, N, K, r, TORCH_DT[cd], flags) for op in (0, 1))
+    args = (L.A.cuda(), L.B.cuda(), L.alpha)
+    x, dy = L.x.cuda(), L.dY.cuda()
+    mask = (torch.rand(M, K, generator=torch.Generator().manual_seed(1)) < 0.75).to(torch.uint8).cuda()
+    drop = dict(dropout_mask=mask, dropout_p=0.25)
+    y, t0 = guarded(lambda ws: qn.linear_fwd(q, x, *args, save_t=True, workspace=ws, **drop), fwd)
+    for kw in (dict(), dict(t_saved=t0), dict(need_dx=False)):
+        guarded(lambda ws: qn.linear_bwd(q, x, dy, *args, workspace=ws, **drop, **kw), bwd)
