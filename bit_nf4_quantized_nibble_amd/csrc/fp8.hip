@@ -736,12 +736,12 @@ int quantize_cd(const void* w, int64_t ldw, const qlora_fp8_t* q, hipStream_t s)
   return check_launch("k_fp8_weight");
 }
 
-// Weight rows per workgroup: the tokens are read once for each workgroup, so more rows spare that
+// Weight rows per workgroup, in 16s: the tokens are read once for each workgroup, so more rows spare that
 // traffic, as long as there are workgroups enough.
+int few_row_blocks(int64_t n) { return ceil_div(n, 16) < 2 * cu_count() ? 1 : 2; }
 template <int CD, bool FUSE>
 int few_rows(const F8& p, const Raw& raw, hipStream_t s) {
-  const int64_t blocks = ceil_div(p.n, 16), cus = cu_count();
-  const int rb = blocks < 2 * cus ? 1 : 2;
+  const int rb = few_row_blocks(p.n);
   const dim3 g((unsigned)ceil_div(p.n, 16 * rb));
   if (rb == 1 && p.ld >= 8192) k_fp8_few<CD, 1, 8, FUSE><<<g, dim3(512), 0, s>>>(p, raw);
   else if (rb == 1) k_fp8_few<CD, 1, 4, FUSE><<<g, dim3(256), 0, s>>>(p, raw);
@@ -795,7 +795,8 @@ int linear_cd(const F8& p, const void* x, int64_t ldx, int64_t cols, Form cut, h
   const Form f = form_of(p.m, p.n, p.ld, CD);
   // before anything is launched: the kernels count tiles in 31 bits, and the tiles of all forms but the
   // largest (whose workgroups go through theirs) are one launch, of fewer than 2^32 threads
-  const int64_t tiles = f == FEW ? 0 : tiles_of(f, p.m, p.n), threads = f == FULL ? 1 : f == WIDE ? 512 : 256;
+  const int64_t tiles = f == FEW ? ceil_div(p.n, 16 * few_row_blocks(p.n)) : tiles_of(f, p.m, p.n);
+  const int64_t threads = f == FULL ? 1 : f == WIDE ? 512 : 256;
   if (tiles >= (1LL << 31) || tiles * threads >= (1LL << 32))
     return set_error(QLORA_ERR_UNSUPPORTED, "fp8: %lld tiles in one call", (long long)tiles);
   {

@@ -605,7 +605,8 @@ int qlora_fp8_quantize(const void* w, int64_t ldw, int32_t wd, qlora_fp8_t* q, v
  * a no-op.  ws: qlora_fp8_workspace_bytes(w, m, cd) bytes, 256-byte aligned.
  * Errors: QLORA_ERR_INVALID_ARG (null or unaligned pointers, y over x), QLORA_ERR_SHAPE (m < 0,
  * empty weight, ldx < cols), QLORA_ERR_DTYPE, QLORA_ERR_WORKSPACE, QLORA_ERR_UNSUPPORTED (cols >
- * QLORA_FP8_MAX_COLS, rows or m of 2^31 or more, more tiles of y than one launch takes).
+ * QLORA_FP8_MAX_COLS, rows or m of 2^31 or more, more tiles of y, or for up to 16 tokens more rows,
+ * than one launch takes).
  */
 int qlora_fp8_linear(const qlora_fp8_t* w, const void* x, int64_t m, int64_t ldx, const void* bias, int32_t cd,
                      void* y, void* ws, size_t ws_bytes, void* stream);
