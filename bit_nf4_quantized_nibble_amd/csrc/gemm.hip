@@ -1010,9 +1010,11 @@ bool planes_seeded(int op, const LayerCall& c) {
   const bool small = op == QLORA_OP_FWD
                          ? c.m <= 64 || (c.m <= 128 && n <= 2 * K) || (n * K <= 1 << 22 && c.m * n * K <= 1LL << 33)
                          : c.m <= 128 || c.m * n * K <= 1LL << 31;
+  const bool skinny = c.cd != CD_F32 && fast_layout(c.w) && skinny_ok(c.cd, c.r);
   const bool reach = skinny_reaches(c.m, K) && (op == QLORA_OP_FWD || skinny_reaches(c.m, n));
-  const bool tuned = !small && reach && c.cd != CD_F32 && fast_layout(c.w) && (op == QLORA_OP_FWD || c.w.rows % 64 == 0) && skinny_ok(c.cd, c.r);
-  return !tuned && !(c.flags & (QLORA_FLAG_FUSED | QLORA_FLAG_DEQUANT_GEMM));
+  const bool tuned = !small && reach && skinny && (op == QLORA_OP_FWD || n % 64 == 0);
+  // a path flag keeps the layer's own kernels, where their rank products reach all of x and dY
+  return c.flags & (QLORA_FLAG_FUSED | QLORA_FLAG_DEQUANT_GEMM) ? skinny && !reach : !tuned;
 }
 
 size_t seeded_workspace_bytes(int op, const LayerCall& c) {
