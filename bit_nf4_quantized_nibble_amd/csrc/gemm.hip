@@ -625,7 +625,7 @@ int forward_gemm(const LayerCall& c, const Seeded* sd, void* y, float* t_save) {
   const bool fast = fast_layout(c.w);
   // input of the low-rank branch: x, or x M with LoRA dropout
   const void* lx = c.x;
-  const bool draws = sd && fast && skinny_ok(CD, c.r);  // the rank product masks x itself
+  const bool sk = fast && skinny_ok(CD, c.r) && skinny_addresses(M, K), draws = sd && sk;  // the rank product masks x itself
   if (c.drop_mask || (sd && !draws)) {
     rc = sd ? apply_seeded(CD, c.x, *sd, M, K, ws + P.off_xm, c.stream)
             : apply_mask(CD, c.x, c.drop_mask, M * K, ws + P.off_xm, c.stream);
@@ -638,7 +638,7 @@ int forward_gemm(const LayerCall& c, const Seeded* sd, void* y, float* t_save) {
   const bool dense = fast && P.dense && dense256_ok(c, false);
   SkRed red;
   bool red_pending = false;
-  if (fast && skinny_ok(CD, c.r)) {
+  if (sk) {
     int S;
     if ((rc = draws ? skinny_drawn(CD, false, down_spec(c), part, &S, nullptr, nullptr, nullptr, *sd, nullptr, 0, c.stream,
                                    QLORA_K_LORA_DOWN)
@@ -691,6 +691,7 @@ int backward_gemm(const LayerCall& c, const Seeded* sd, const void* dy, const fl
   BwdPlan P = plan_bwd(M, N, K, c.r, CD, c.flags);
   const bool fast = fast_layout(c.w);
   if (!fast) P.sk = P.sk_n = P.dense = false;  // the generic engine for every product (see fast_layout)
+  if (!skinny_addresses(M, K) || !skinny_addresses(M, N)) P.sk = P.sk_n = false;  // or for the rank products
   char* ws = (char*)c.ws;
   float* t0 = (float*)(ws + P.off_t0);
   float* dt = (float*)(ws + P.off_dt);

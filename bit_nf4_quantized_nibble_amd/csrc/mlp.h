@@ -34,7 +34,10 @@ inline void gradient_jobs(SkRed& ra, SkRed& rb, float scale, void* d_a, void* d_
 size_t seeded_workspace_bytes(int op, const LayerCall& c);
 // out = x M
 int apply_seeded(int cd, const void* x, const Seeded& sd, int64_t rows, int64_t cols, void* out, hipStream_t s);
-// Whether the rank-product kernels reach all of a 16-bit matrix: their offsets lie below 2^31 bytes.
+// Whether the offsets of the rank-product kernels, 32 bits, hold all of a 16-bit matrix (past 2^31 bytes a row that is not there
+// still lies behind the buffer's end).
+inline bool skinny_addresses(int64_t rows, int64_t ld) { return round_up(rows, 128) * ld * 2 < (1LL << 32); }
+// Whether they lie below 2^31 bytes, where the masked forms are used.
 inline bool skinny_reaches(int64_t rows, int64_t ld) { return round_up(rows, 64) * ld * 2 < (1LL << 31); }
 // lora.hip: one rank product (and, TN, a second without a mask) whose Aop, x [rows][cols], counts under the
 // drawn mask.  NT: x A^T; TN: bits not null: the mask's bits are left there, rows of ldbits words.
