@@ -666,11 +666,15 @@ bool few_tokens(int64_t m) { return m <= 16; }
 // 4096 x 14336 11.8 and 14.9; 4 tokens of 8192 x 4096 10.8 and 12.2, of 14336 x 4096 16.5 and 15.4, of
 // 4096 x 14336 18.2 and 15.4; 8 tokens of 4096 x 4096 11.7 and 10.5 without the launch's cost on the host).
 bool fused_rows(int64_t m, int64_t n, int64_t ld) { return m <= 4 && m * n * ld <= 1LL << 27; }
-// Few tokens on tiles all the same: rows so long that the few-token kernel's waves, a row of W each, are too few; and
-// in 16 bits so many rows that the smallest tiles fill the card (16 tokens of 14336 x 4096: 14.7 us against
-// 17.0; but of 8192 x 4096 14.1 against 12.7, of 4096 x 14336 31 against 18, in fp32 24 against 18).
-bool few_on_tiles(int64_t n, int64_t ld, int cd) {
-  return (ld > 8192 && n <= 2048) || (cd != CD_F32 && ceil_div(n, 64) >= 192 && ld <= 4096);
+// Few tokens on tiles all the same.  Rows so long that the few-token kernel's waves, a row of W each, are too few (us on the
+// device, tiles and that kernel, 5 to 16 tokens: bf16 256 x 14336 12.3 and 14 to 17, 2048 x 14336 15.5 and 16 to 19,
+// 1024 x 28672 18.4 and 26 to 33; fp32 1024 x 28672 25.5 and 28 to 35, but 2048 x 14336 19.8 and 17.8 to 20.5; bf16
+// 4096 x 14336 19.9 and 18 to 21, 1024 x 8192 10.8 and 10 to 12).  And in 16 bits, from 12 tokens on, so many rows that the
+// smallest tiles fill the card (12288 x 4096, 5, 8, 12, 16 tokens: 17.3 against 16.7, 17.2, 17.9, 18.8; 14336 x 4096 18.3 against 17.2,
+// 17.4, 18.3, 18.9; 28672 x 2048 17.0 against 16.6, 16.9, 17.7, 18.4; but 28672 x 1024 11.5 against 10.6 to 11.6, 8192 x 4096 16.2
+// against 13.2 to 13.7, 14336 x 8192 32 against 28 to 32).
+bool few_on_tiles(int64_t m, int64_t n, int64_t ld, int cd) {
+  return (ld > 8192 && n <= 2048) || (cd != CD_F32 && m >= 12 && ceil_div(n, 64) >= 192 && ld > 1024 && ld <= 4096);
 }
 
 // us by form, bf16, m x n x k: 512 x 2048 x 2048 SMALL 10.9, LOW 12.0, MID 15.0; 1024 x 2048 x 2048 14.0, 13.2, 15.9;
@@ -678,7 +682,7 @@ bool few_on_tiles(int64_t n, int64_t ld, int cd) {
 // 4096 x 4096 x 4096 123, 97, 90, 74, 69.9: the smallest tiles that take one round.
 Form form_of(int64_t m, int64_t n, int64_t ld, int cd) {
   const int64_t cus = cu_count();
-  if (few_tokens(m)) return few_on_tiles(n, ld, cd) && !fused_rows(m, n, ld) ? SMALL : FEW;
+  if (few_tokens(m)) return few_on_tiles(m, n, ld, cd) && !fused_rows(m, n, ld) ? SMALL : FEW;
   auto one_round = [&](int64_t tm, int64_t tn) { return ceil_div(m, tm) * ceil_div(n, tn) <= cus; };
   if (one_round(64, 64)) return SMALL;
   if (one_round(64, 128)) return LOW;
@@ -699,7 +703,7 @@ Plan plan_fp8(const qlora_fp8_t* w, int64_t m, int cd) {
   P.stride = round_up(m, 64);
   P.off_scale = al((size_t)(m * ld));
   P.off_part = P.total = P.off_scale + al((size_t)(ceil_div(ld, 512) * P.stride * 4));
-  if (m == 0 || w->rows == 0 || (few_tokens(m) && (fused_rows(m, w->rows, ld) || !few_on_tiles(w->rows, ld, cd)))) return P;
+  if (m == 0 || w->rows == 0 || (few_tokens(m) && (fused_rows(m, w->rows, ld) || !few_on_tiles(m, w->rows, ld, cd)))) return P;
   int64_t tiles = ceil_div(m, Small::TM) * ceil_div(w->rows, Small::TN), tile = Small::TM * Small::TN;
   P.split = slices(tiles, ld);
   const int64_t mid = ceil_div(m, Mid::TM) * ceil_div(w->rows, Mid::TN);

@@ -28,6 +28,17 @@ def test_a_block_that_is_no_number_stays_alone(m, cd, bad):
     assert torch.isfinite(want).all()
 
 
+@pytest.mark.parametrize("m,n,k,cd", [(m, n, k, "bf16") for n, k in ((12225, 1153), (12224, 2048), (12290, 1024), (12300, 4100))
+                                      for m in (4, 5, 11, 12, 16)]
+                         + [(m, n, k, cd) for m in (5, 16, 17) for n, k, cd in ((2048, 8200, "f32"), (2049, 8200, "f16"))])
+def test_each_side_of_the_few_token_rules(m, n, k, cd):
+    say("fp8: few tokens", m, n, k, cd)
+    x, w, b = tensors(m, n, k, cd, m + n, True)
+    y = qn.linear_fp8(qn.quantize_fp8(w.cuda()), x.cuda(), bias=b.cuda())
+    ref, mag = of.product(to_np(x), to_np(w), to_np(b))
+    check(y, ref, mag, cd, k)
+
+
 @pytest.mark.parametrize("m,n,k,cd", [((1 << 31) // 4096 + 300, 64, 4096, "bf16"), ((1 << 31) // 14400 + 300, 14400, 128, "bf16"),
                                       ((1 << 31) // 4096 + 300, 64, 4096, "f32"), ((1 << 31) // 14400 + 300, 14400, 128, "f32")])
 def test_more_than_two_to_the_31st_elements(m, n, k, cd):
