@@ -107,7 +107,8 @@ __global__ __launch_bounds__(kThreads) void k_fp8_rows(const void* __restrict__ 
   if (lane == 0) scale[quad * stride + row] = word;
 }
 
-// The weight: a workgroup to a block of 128 x 128, two threads to a row.
+// The weight: a workgroup to a block of 128 x 128, two threads to a row.  Run once for a weight: 14336 x 4096 bf16 takes 107 to
+// 124 us, 34 at a copy's rate; a wave's loads touch 32 rows 16 bytes at a time, and it waits for those (vector pipes busy 7%).
 template <int CD>
 __global__ __launch_bounds__(kThreads) void k_fp8_weight(const void* __restrict__ w, int64_t ldw, int64_t rows, int cols,
                                                          int ld, int lds, uint8_t* __restrict__ codes,

@@ -280,8 +280,9 @@ struct HalfOf<Tile<WMB, WNB, NWM, NWN, 2>> {
   using type = Tile<WMB / 2, WNB, NWM, NWN, 2>;
 };
 
-// Bound by the matrix pipes at the card's power limit: gated, 4096 x 14336 x 4096, 733 us (1.33 PFLOP/s, pipes busy
-// 76% of the cycles at 1.61 GHz); plain, 4096 x 4096 x 28672, 715 us; masked, 4096 x 14336 x 4096, 392 us.
+// Bound by the matrix pipes at the card's power limit (us, a trace's fastest and median call): gated, 4096 x 14336 x 4096, 749
+// and 850 (1.30 and 1.15 PFLOP/s; pipes busy 76% of the cycles at 1.63 GHz); plain, 4096 x 4096 x 28672, 735 and 792 (73%);
+// masked, 4096 x 14336 x 4096, 394 and 440 (67%).
 // A workgroup goes through its tiles.  After a tile's last stage the copies of the next tile's first
 // stage are requested, so that they land while this one's outputs are formed and stored; those pass
 // through LDS behind that stage.  A last round of at most half the workgroups runs as tiles of half

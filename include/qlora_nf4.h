@@ -238,8 +238,9 @@ int qlora_linear_bwd_group(int32_t g, const qlora_nf4_t* const* w, const void* x
  * projection, equal rows and cols):
  *   g = x Wg~^T + s_g (x Ag^T) Bg^T (+ bias[0 .. rows)),  u likewise (+ bias[rows .. 2 rows)),
  *   h [m, rows] = act(g) u.
- * h is rounded once, from fp32 (many tokens with a rank above 64 in a 16-bit cd: g and u are
- * rounded into cd first.  pre (nullable) [m, 2 rows] receives [g | u] in cd, t_save (nullable
+ * h is rounded once, from fp32, but for one kind of call: in a 16-bit cd with a rank above 64, where
+ * 2 ceil(m / 64) ceil(rows / 128) >= 160 and W~ is not decoded by the product (m > 256, or a layout that it does not
+ * decode), g and u are rounded into cd first.  pre (nullable) [m, 2 rows] receives [g | u] in cd, t_save (nullable
  * array of nullable pointers) T0_i = x A_i^T fp32 [m, r_i]: what the backward takes.
  * act: QLORA_ACT_SILU z / (1 + exp(-z)); QLORA_ACT_GELU z Phi(z); QLORA_ACT_GELU_TANH
  * z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2.
